@@ -10,7 +10,8 @@ mask, and the product with V. MHA and GQA (Nq a multiple of Nk), fp32, fp16 and
 bf16. Queries may be fewer than keys (seq_offsets_k: the queries are the last tokens of
 their sequences), and the keys may start with a history held in a paged KV cache
 (kv_cache, page_offsets, page_ids, last_page_len). The work runs in libhstu_fwd.so (tcgen05/TMA kernels for fp16/bf16, CUDA-core
-FFMA for fp32); this module marshals torch tensors to its C ABI and uses torch
+FFMA for fp32); hstu_kv_append, hstu_kv_read and hstu_softmax_fwd (kv_cache.py) write that
+cache, read it back and attend over it with a softmax. This module marshals torch tensors to its C ABI and uses torch
 only for device memory and the current stream.
 """
 from __future__ import annotations
@@ -21,9 +22,11 @@ import torch
 
 from . import _abi
 from ._abi import HstuError
+from .kv_cache import hstu_kv_append, hstu_kv_read, hstu_softmax_fwd
 
 __all__ = ["hstu_fwd", "hstu_fwd_noalloc", "HstuFwdPlan", "HstuError", "count_pairs",
-           "count_pairs_kv", "useful_flops"]
+           "count_pairs_kv", "useful_flops", "hstu_kv_append", "hstu_kv_read",
+           "hstu_softmax_fwd"]
 
 _DTYPES = {torch.float32: _abi.HSTU_F32, torch.float16: _abi.HSTU_F16,
            torch.bfloat16: _abi.HSTU_BF16, torch.float8_e4m3fn: _abi.HSTU_FP8_E4M3}

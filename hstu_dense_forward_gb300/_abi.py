@@ -13,6 +13,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("HSTU_FWD_LIB") or os.path.join(
     PKG, "libhstu_fwd_trace.so" if os.environ.get("HSTU_FWD_TRACE") == "1" else "libhstu_fwd.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_fwd.h")
+KV_HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_kv.h")
 
 HSTU_OK, HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED, HSTU_ERR_CUDA, HSTU_ERR_TIMEOUT, \
     HSTU_ERR_DEVICE_CHECK = range(6)
@@ -79,6 +80,42 @@ class Args(ctypes.Structure):
     ]
 
 
+class KVCache(ctypes.Structure):
+    """hstu_kv_cache: a paged KV cache with its page table (include/hstu_kv.h)."""
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("num_heads_kv", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("index_is_int64", ctypes.c_int), ("descale", ctypes.c_int), ("reserved", ctypes.c_int),
+        ("kv_cache", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_longlong), ("page_offsets", ctypes.c_void_p),
+        ("page_ids", ctypes.c_void_p), ("last_page_len", ctypes.c_void_p),
+        ("num_page_ids", ctypes.c_longlong), ("k_descale", ctypes.c_void_p),
+        ("v_descale", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class KVRows(ctypes.Structure):
+    """hstu_kv_rows: rows of k and v written to or read from the cache."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_longlong),
+        ("v_stride", ctypes.c_longlong), ("seq_offsets", ctypes.c_void_p),
+        ("total_tokens", ctypes.c_longlong), ("dtype", ctypes.c_int),
+        ("reserved", ctypes.c_int),
+    ]
+
+
+class SoftmaxArgs(ctypes.Structure):
+    """hstu_softmax_args: the queries and outputs of one hstu_softmax_fwd."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong),
+        ("seq_offsets", ctypes.c_void_p), ("total_tokens", ctypes.c_longlong),
+        ("dtype", ctypes.c_int), ("num_heads_q", ctypes.c_int), ("max_seqlen", ctypes.c_int),
+        ("max_seqlen_k", ctypes.c_int), ("causal", ctypes.c_int), ("alpha", ctypes.c_float),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_longlong), ("reserved", ctypes.c_int),
+    ]
+
+
 class HstuError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -89,9 +126,9 @@ _lock = threading.Lock()
 _lib = None
 
 
-def declared_symbols() -> list[str]:
-    """Entry points declared in include/hstu_fwd.h (the HSTU_API functions)."""
-    text = open(HEADER).read()
+def declared_symbols(header: str = HEADER) -> list[str]:
+    """Entry points declared in a header (include/hstu_fwd.h): its HSTU_API functions."""
+    text = open(header).read()
     return re.findall(r"HSTU_API\s+[\w\s\*]+?\b(\w+)\s*\(", text)
 
 
@@ -140,6 +177,13 @@ def lib():
         L.hstu_fwd_trace_read.argtypes = [vp, vp, ll]
         L.hstu_status_string.restype = ctypes.c_char_p
         L.hstu_status_string.argtypes = [ctypes.c_int]
+        # the cache operators (HSTU_FWD_LIB may name an older build without them)
+        for name, args in (("hstu_kv_append", [vp, vp, vp]), ("hstu_kv_read", [vp, vp, vp]),
+                           ("hstu_softmax_fwd", [vp, vp, vp]),
+                           ("hstu_softmax_workspace", [vp, vp, vp])):
+            if hasattr(L, name):
+                getattr(L, name).restype = ctypes.c_int
+                getattr(L, name).argtypes = args
         _lib = L
         return _lib
 

@@ -1,0 +1,210 @@
+// C ABI of the paged KV cache operators: argument checks, the choice of kernel and of the
+// number of key ranges, and launches. See include/hstu_kv.h for the contracts.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "../../include/hstu_kv.h"
+#include "kv_cache.cuh"
+#include "kv_kernels.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int elem_bytes(int dtype) { return dtype == HSTU_F32 ? 4 : dtype == HSTU_FP8_E4M3 ? 1 : 2; }
+
+// Sizes of a cache descriptor; pointers are checked by cache_pointers_ok.
+hstu_status check_cache(const hstu_kv_cache* c) {
+  if (!c || c->reserved) return HSTU_ERR_INVALID_ARG;
+  if (c->dtype < HSTU_F32 || c->dtype > HSTU_FP8_E4M3) return HSTU_ERR_INVALID_ARG;
+  if (c->batch < 0 || c->batch > (1 << 20)) return HSTU_ERR_INVALID_ARG;
+  if (c->num_heads_kv < 1 || c->num_heads_kv > 65536) return HSTU_ERR_INVALID_ARG;
+  if (c->head_dim < 1) return HSTU_ERR_INVALID_ARG;
+  if (c->head_dim % 16 != 0 || c->head_dim > 256) return HSTU_ERR_UNSUPPORTED;
+  if (c->page_size != 32 && c->page_size != 128 && c->page_size != 256)
+    return HSTU_ERR_INVALID_ARG;
+  if (c->index_is_int64 != 0 && c->index_is_int64 != 1) return HSTU_ERR_INVALID_ARG;
+  if (c->descale < HSTU_DESCALE_CAST || c->descale > HSTU_DESCALE_BLOCK)
+    return HSTU_ERR_INVALID_ARG;
+  if (c->descale == HSTU_DESCALE_BLOCK) return HSTU_ERR_UNSUPPORTED;
+  const bool fp8 = c->dtype == HSTU_FP8_E4M3;
+  if (!fp8 && (c->descale != HSTU_DESCALE_CAST || c->kv_scale)) return HSTU_ERR_INVALID_ARG;
+  if (c->descale != HSTU_DESCALE_CAST && c->kv_scale) return HSTU_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->num_pages > (1ll << 30) || c->num_page_ids < 0)
+    return HSTU_ERR_INVALID_ARG;
+  return HSTU_OK;
+}
+
+bool cache_pointers_ok(const hstu_kv_cache* c) {
+  if (!c->kv_cache || !aligned(c->kv_cache, 16) || !c->page_offsets || !c->last_page_len ||
+      (!c->page_ids && c->num_page_ids > 0))
+    return false;
+  const uintptr_t ib = c->index_is_int64 ? 8 : 4;
+  if (!aligned(c->page_offsets, ib) || !aligned(c->last_page_len, ib) ||
+      !aligned(c->page_ids, ib) || !aligned(c->status, 4))
+    return false;
+  const bool factors = c->descale != HSTU_DESCALE_CAST;
+  if (factors != (c->k_descale != nullptr) || factors != (c->v_descale != nullptr)) return false;
+  return aligned(c->k_descale, 4) && aligned(c->v_descale, 4);
+}
+
+hstu::CacheView cache_view(const hstu_kv_cache* c, const void* seq_offsets, long long T) {
+  hstu::CacheView v = {};
+  v.cache = c->kv_cache;
+  v.scale = static_cast<uint8_t*>(c->kv_scale);
+  v.page_offsets = c->page_offsets;
+  v.page_ids = c->page_ids;
+  v.last_page_len = c->last_page_len;
+  v.seq_offsets = seq_offsets;
+  v.k_ds = c->k_descale;
+  v.v_ds = c->v_descale;
+  v.status = c->status;
+  v.num_pages = c->num_pages;
+  v.num_page_ids = c->num_page_ids;
+  v.T = T;
+  v.index64 = c->index_is_int64;
+  v.B = c->batch;
+  v.Nk = c->num_heads_kv;
+  v.D = c->head_dim;
+  v.page_shift = c->page_size == 32 ? 5 : c->page_size == 128 ? 7 : 8;
+  v.ds_b = c->descale == HSTU_DESCALE_BATCH ? 1
+           : c->descale == HSTU_DESCALE_HEAD ? c->num_heads_kv : 0;
+  v.ds_h = c->descale == HSTU_DESCALE_HEAD ? 1 : 0;
+  return v;
+}
+
+// Row dtype against the cache's: the same, or any 32- or 16-bit type with an E4M3 cache.
+bool row_dtype_ok(const hstu_kv_cache* c, int dtype) {
+  if (dtype < HSTU_F32 || dtype > HSTU_BF16) return false;
+  return c->dtype == HSTU_FP8_E4M3 || c->dtype == dtype;
+}
+
+hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append, void* stream) {
+  const hstu_status st = check_cache(c);
+  if (st != HSTU_OK) return st;
+  if (!r || r->reserved || !row_dtype_ok(c, r->dtype)) return HSTU_ERR_INVALID_ARG;
+  if (r->total_tokens < 0 || r->total_tokens > 0x7fffffffll) return HSTU_ERR_INVALID_ARG;
+  if (c->batch == 0 || r->total_tokens == 0) return HSTU_OK;
+  const long long width = (long long)c->num_heads_kv * c->head_dim;
+  const int eb = elem_bytes(r->dtype);
+  if (!r->k || !r->v || !aligned(r->k, 16) || !aligned(r->v, 16) || !r->seq_offsets ||
+      !aligned(r->seq_offsets, c->index_is_int64 ? 8 : 4) || r->k_stride < width ||
+      r->v_stride < width || r->k_stride * eb % 16 != 0 || r->v_stride * eb % 16 != 0 ||
+      r->k_stride > (1ll << 40) || r->v_stride > (1ll << 40) || !cache_pointers_ok(c))
+    return HSTU_ERR_INVALID_ARG;
+  if (hstu::kv_copy_blocks(r->total_tokens, c->num_heads_kv, c->head_dim) > 0x7fffffffll)
+    return HSTU_ERR_UNSUPPORTED;
+  const hstu::CacheView v = cache_view(c, r->seq_offsets, r->total_tokens);
+  return hstu::launch_kv_copy(v, r->k, r->v, r->k_stride, r->v_stride, r->dtype,
+                              c->dtype == HSTU_FP8_E4M3, append,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? HSTU_OK
+             : HSTU_ERR_CUDA;
+}
+
+// How a call runs: query rows of one CTA, key ranges, grid and workspace.
+struct AttnPlan {
+  int splits, min_range;
+  long long tiles, blocks, workspace;
+};
+
+hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, AttnPlan* pl) {
+  const hstu_status st = check_cache(c);
+  if (st != HSTU_OK) return st;
+  if (!a || a->reserved || !row_dtype_ok(c, a->dtype)) return HSTU_ERR_INVALID_ARG;
+  if (a->total_tokens < 0 || a->total_tokens > 0x7fffffffll || a->num_heads_q < 0 ||
+      a->num_heads_q % c->num_heads_kv != 0)
+    return HSTU_ERR_INVALID_ARG;
+  if (a->max_seqlen < 1 || a->max_seqlen > (1 << 24) || a->max_seqlen_k < 1 ||
+      a->max_seqlen_k > (1 << 30) || (a->causal != 0 && a->causal != 1) ||
+      !std::isfinite(a->alpha) || !(a->alpha > 0.0f))
+    return HSTU_ERR_INVALID_ARG;
+  const long long G = a->num_heads_q / c->num_heads_kv;
+  if (G > 128) return HSTU_ERR_UNSUPPORTED;
+  *pl = AttnPlan{1, 128, 0, 0, 0};
+  if (c->batch == 0 || a->total_tokens == 0 || G == 0) return HSTU_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return HSTU_ERR_CUDA;
+  const long long bm = hstu::softmax_simt_rows();
+  const long long most = a->max_seqlen < a->total_tokens ? a->max_seqlen : a->total_tokens;
+  pl->tiles = (most * G + bm - 1) / bm;
+  pl->blocks = c->batch * pl->tiles * c->num_heads_kv;
+  if (pl->blocks > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
+  // row tiles that hold rows: at most one partly filled tile a sequence
+  long long items = a->total_tokens * G / bm + c->batch;
+  if (items > c->batch * pl->tiles) items = c->batch * pl->tiles;
+  items *= c->num_heads_kv;
+  pl->min_range = 256;
+  const long long want = (4ll * sms + items - 1) / items;
+  const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
+  pl->splits = (int)(want < can ? want : can);
+  if (pl->splits > 1)
+    pl->workspace = (long long)pl->splits * a->total_tokens * a->num_heads_q *
+                    (c->head_dim + 1) * 4;
+  return HSTU_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+hstu_status hstu_kv_append(const hstu_kv_cache* cache, const hstu_kv_rows* rows, void* stream) {
+  return copy_rows(cache, rows, true, stream);
+}
+
+hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows* rows, void* stream) {
+  return copy_rows(cache, rows, false, stream);
+}
+
+hstu_status hstu_softmax_workspace(const hstu_kv_cache* cache, const hstu_softmax_args* args,
+                                   long long* bytes) {
+  if (!bytes) return HSTU_ERR_INVALID_ARG;
+  *bytes = 0;
+  AttnPlan pl;
+  const hstu_status st = plan_attention(cache, args, &pl);
+  if (st == HSTU_OK) *bytes = pl.workspace;
+  return st;
+}
+
+hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a, void* stream) {
+  AttnPlan pl;
+  const hstu_status st = plan_attention(c, a, &pl);
+  if (st != HSTU_OK) return st;
+  if (pl.blocks == 0) return HSTU_OK;  // empty input
+  if (!a->q || !a->out || !a->seq_offsets || !aligned(a->q, 16) || !aligned(a->out, 16) ||
+      !aligned(a->lse, 4) || !aligned(a->seq_offsets, c->index_is_int64 ? 8 : 4) ||
+      a->q_stride < (long long)a->num_heads_q * c->head_dim || a->q_stride > (1ll << 36) ||
+      a->q_stride * elem_bytes(a->dtype) % 16 != 0 || !cache_pointers_ok(c))
+    return HSTU_ERR_INVALID_ARG;
+  if (pl.workspace > 0 &&
+      (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < pl.workspace))
+    return HSTU_ERR_INVALID_ARG;
+  hstu::SoftmaxParams p = {};
+  p.c = cache_view(c, a->seq_offsets, a->total_tokens);
+  p.q = a->q;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.q_stride = a->q_stride;
+  p.Nq = a->num_heads_q;
+  p.G = a->num_heads_q / c->num_heads_kv;
+  p.max_q = a->max_seqlen;
+  p.max_k = a->max_seqlen_k;
+  p.causal = a->causal;
+  p.scale_log2 = (float)((double)a->alpha * 1.4426950408889634);
+  p.splits = pl.splits;
+  p.min_range = pl.min_range;
+  p.timeout_ns = 1000000000ll;
+  p.part_o = static_cast<float*>(a->workspace);
+  p.part_lse = p.part_o + (long long)pl.splits * a->total_tokens * a->num_heads_q * c->head_dim;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fp8 = c->dtype == HSTU_FP8_E4M3;
+  cudaError_t e = hstu::launch_softmax_simt(p, a->dtype, fp8, pl.tiles, pl.blocks, s);
+  if (e == cudaSuccess && pl.splits > 1) e = hstu::launch_softmax_combine(p, a->dtype, s);
+  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+}  // extern "C"

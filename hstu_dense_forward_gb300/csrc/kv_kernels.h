@@ -1,0 +1,25 @@
+// Launch interface between the entry points of the KV cache operators (kv_api.cu) and their
+// kernels.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace hstu {
+
+struct CacheView;
+struct SoftmaxParams;
+
+// Append (append = true) or read back; dtype of k and v, e4m3: the cache holds E4M3.
+long long kv_copy_blocks(long long T, int Nk, int D);
+cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_stride,
+                           long long v_stride, int dtype, bool e4m3, bool append,
+                           cudaStream_t stream);
+
+// CUDA-core attention.
+int softmax_simt_rows();  // query rows (token, head) of one CTA
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, int dtype, bool e4m3, long long tiles,
+                                long long blocks, cudaStream_t stream);
+
+// Joins the key ranges of sequences that have more than one.
+cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream);
+
+}  // namespace hstu

@@ -1,0 +1,315 @@
+// Softmax attention over the paged KV cache on CUDA cores (FFMA, fp32 throughout), and the
+// kernel that joins the key ranges of sequences worked on in parts.
+//
+// One CTA (256 threads) takes BM packed query rows of one kv head (packed row r of a sequence
+// is query token r / G, head hk * G + r % G, so that the G heads that share a kv head share
+// its loads) and one range of the keys, in steps of 64 keys, with the running maximum m and
+// sum l of the softmax in base 2:
+//   x = scale_log2 * Q K^T, m' = max(m, x), P = 2^(x - m'), l = 2^(m - m') l + sum P,
+//   O = 2^(m - m') O + P V,                        out = O / l, log2 of the sum = m + log2 l.
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv_cache.cuh"
+#include "kv_kernels.h"
+#include "ptx.cuh"
+
+namespace hstu {
+
+namespace {
+
+constexpr int BM = 64;  // packed query rows per CTA
+constexpr int BN = 64;  // keys per step
+constexpr int kThreads = 256;
+constexpr int kMaxD = 256;
+constexpr int kMaxU = kMaxD / 16;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxParams p, int tiles) {
+  extern __shared__ float sm[];
+  const int D = p.c.D;
+  const int ldk = D + 1;  // padded rows: threads of one warp read different K rows
+  float* Qs = sm;             // [BM][D]
+  float* Ks = Qs + BM * D;    // [BN][D + 1]
+  float* Vs = Ks + BN * ldk;  // [BN][D]
+  float* Ps = Vs + BN * D;    // [BM][BN + 1]
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+
+  // block: sequence b, row tile (later tiles first: with the causal mask they see more
+  // keys), kv head; blockIdx.y: key range
+  const long long blk = blockIdx.x;
+  const int hk = (int)(blk % p.c.Nk);
+  const int tile = tiles - 1 - (int)(blk / p.c.Nk % tiles);
+  const int b = (int)(blk / p.c.Nk / tiles);
+  const int split = blockIdx.y;
+  const PagedSeq s = paged_seq(p.c, b);
+  if (!attn_seq_ok(p, s)) {
+    if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+    return;
+  }
+  const long long rows = s.n * p.G, m0 = (long long)tile * BM;
+  const KeyRanges kr = key_ranges(p, s.Lk);
+  const int nsplit = kr.count;
+  if (m0 >= rows || split >= nsplit) return;
+  // keys any row of the tile may see, within the range
+  const long long last = (min(m0 + BM, rows) - 1) / p.G;  // last query token of the tile
+  long long kend = s.Lk;
+  if (p.causal) kend = min(kend, s.Lk - s.n + last + 1);
+  const long long k0 = split * kr.keys;
+  kend = min(kend, k0 + kr.keys);
+
+  const T* q = static_cast<const T*>(p.q);
+  for (int x = threadIdx.x; x < BM * D; x += kThreads) {
+    const int r = x / D, d = x - r * D;
+    const long long pr = m0 + r;
+    Qs[x] = pr < rows ? to_float(q[(s.t0 + pr / p.G) * p.q_stride +
+                                   (hk * p.G + pr % p.G) * (long long)D + d])
+                      : 0.f;
+  }
+  float fk = p.scale_log2, fv = 1.f;  // static factors fold into the scale and the output
+  if (p.c.k_ds) {
+    fk *= p.c.k_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
+    fv = p.c.v_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
+  }
+  float acc[4][kMaxU], m[4], l[4];
+  long long lim[4];  // keys that each row sees: [0, lim)
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    m[a] = -CUDART_INF_F;
+    l[a] = 0.f;
+    const long long pr = m0 + ty + 16 * a;
+    lim[a] = pr >= rows ? 0 : p.causal ? s.Lk - s.n + pr / p.G + 1 : s.Lk;
+    lim[a] = min(lim[a], kend);
+#pragma unroll
+    for (int u = 0; u < kMaxU; ++u) acc[a][u] = 0.f;
+  }
+
+  for (long long n0 = k0; n0 < kend; n0 += BN) {
+    __syncthreads();  // previous step finished with Ks/Vs/Ps
+    for (int x = threadIdx.x; x < BN * (D / 16); x += kThreads) {
+      const int r = x / (D / 16), d0 = (x - r * (D / 16)) * 16;
+      float kx[16], vx[16];
+      const long long page = n0 + r < kend ? page_at(p.c, s, n0 + r) : -1;
+      if (page >= 0) {
+        const long long row = (n0 + r) & (page_size(p.c) - 1);
+        const long long ka = cache_row(p.c, page, 0, row, hk) + d0;
+        const long long va = cache_row(p.c, page, 1, row, hk) + d0;
+        if constexpr (E4M3) {
+          load16(static_cast<const uint8_t*>(p.c.cache) + ka, kx);
+          load16(static_cast<const uint8_t*>(p.c.cache) + va, vx);
+          if (p.c.scale) {
+            const float ek = scale_value(p.c.scale[scale_row(p.c, page, 0, row, hk)]);
+            const float ev = scale_value(p.c.scale[scale_row(p.c, page, 1, row, hk)]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              kx[i] *= ek;
+              vx[i] *= ev;
+            }
+          }
+        } else {
+          load16(static_cast<const T*>(p.c.cache) + ka, kx);
+          load16(static_cast<const T*>(p.c.cache) + va, vx);
+        }
+      } else {
+        if (n0 + r < kend) report(p.c, HSTU_DEVERR_OFFSETS);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) kx[i] = vx[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        Ks[r * ldk + d0 + i] = kx[i];
+        Vs[r * D + d0 + i] = vx[i];
+      }
+    }
+    __syncthreads();
+    // scores of rows ty + 16a, keys tx + 16c
+    float sc[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sc[a][c] = 0.f;
+    for (int d = 0; d < D; ++d) {
+      float qa[4], kb[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) qa[a] = Qs[(ty + 16 * a) * D + d];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) kb[c] = Ks[(tx + 16 * c) * ldk + d];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[a][c] = fmaf(qa[a], kb[c], sc[a][c]);
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        sc[a][c] = n0 + tx + 16 * c < lim[a] ? sc[a][c] * fk : -CUDART_INF_F;
+        top = fmaxf(top, sc[a][c]);
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float mn = fmaxf(m[a], top);
+      const float base = mn == -CUDART_INF_F ? 0.f : mn;  // no key yet: weights 2^-inf = 0
+      const float corr = exp2f(m[a] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float w = exp2f(sc[a][c] - base);
+        sum += w;
+        Ps[(ty + 16 * a) * (BN + 1) + tx + 16 * c] = w;
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      l[a] = l[a] * corr + sum;
+      m[a] = mn;
+#pragma unroll
+      for (int u = 0; u < kMaxU; ++u) acc[a][u] *= corr;
+    }
+    __syncthreads();
+    for (int j = 0; j < BN; ++j) {
+      float pa[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) pa[a] = Ps[(ty + 16 * a) * (BN + 1) + j];
+#pragma unroll
+      for (int u = 0; u < kMaxU; ++u) {
+        const int d = tx + 16 * u;
+        if (d < D) {
+          const float vv = Vs[j * D + d];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) acc[a][u] = fmaf(pa[a], vv, acc[a][u]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const long long pr = m0 + ty + 16 * a;
+    if (pr >= rows) continue;
+    const long long row = (s.t0 + pr / p.G) * p.Nq + hk * p.G + pr % p.G;  // of out and lse
+    const float inv = l[a] > 0.f ? fv / l[a] : l[a];  // (a NaN sum stays one)
+    const float log2sum = l[a] == 0.f ? -CUDART_INF_F : m[a] + log2f(l[a]);
+#pragma unroll
+    for (int u = 0; u < kMaxU; ++u) {
+      const int d = tx + 16 * u;
+      if (d >= D) continue;
+      if (nsplit > 1)
+        p.part_o[((long long)split * p.c.T * p.Nq + row) * D + d] = acc[a][u] * inv;
+      else
+        static_cast<T*>(p.out)[row * D + d] = from_float<T>(acc[a][u] * inv);
+    }
+    if (tx == 0) {
+      if (nsplit > 1)
+        p.part_lse[(long long)split * p.c.T * p.Nq + row] = log2sum;
+      else if (p.lse)
+        p.lse[row] = log2sum * kLn2;
+    }
+  }
+}
+
+// out = sum_s 2^(e_s - max e) O_s / sum_s 2^(e_s - max e) over the key ranges s of a row, e_s
+// the base-2 logarithm of range s's sum. One group of D / 4 lanes (rounded up to a power of
+// two, one warp at most) per (row, head), four consecutive elements a lane and step.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) softmax_combine_kernel(const SoftmaxParams p,
+                                                                   int lane_shift) {
+  const long long lane = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long row = lane >> lane_shift, t = row / p.Nq;
+  if (t >= p.c.T) return;
+  const int b = seq_of_row(p.c, t);
+  const PagedSeq s = paged_seq(p.c, b);
+  if (!attn_seq_ok(p, s) || t < s.t0 || t >= s.t0 + s.n) return;
+  const int nsplit = key_ranges(p, s.Lk).count;
+  if (nsplit < 2) return;  // written by the attention kernel
+  const long long all = p.c.T * p.Nq;
+  float top = -CUDART_INF_F;
+  for (int i = 0; i < nsplit; ++i) top = fmaxf(top, p.part_lse[i * all + row]);
+  const float base = top == -CUDART_INF_F ? 0.f : top;
+  float sum = 0.f;
+  for (int i = 0; i < nsplit; ++i) sum += exp2f(p.part_lse[i * all + row] - base);
+  const int D = p.c.D, step = 4 << lane_shift;
+  const int first = (int)(lane & ((1 << lane_shift) - 1)) * 4;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int d = first; d < D; d += step) {
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < nsplit; ++i) {
+      const float w = exp2f(p.part_lse[i * all + row] - base) * inv;
+      if (w == 0.f) continue;  // a range without keys for this row holds nothing
+      const float4 f = *reinterpret_cast<const float4*>(p.part_o + (i * all + row) * D + d);
+      o[0] = fmaf(w, f.x, o[0]);
+      o[1] = fmaf(w, f.y, o[1]);
+      o[2] = fmaf(w, f.z, o[2]);
+      o[3] = fmaf(w, f.w, o[3]);
+    }
+    T* dst = static_cast<T*>(p.out) + row * D + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dst[e] = from_float<T>(o[e]);
+  }
+  if (p.lse && first == 0) p.lse[row] = (top + log2f(sum)) * kLn2;
+}
+
+template <typename T, bool E4M3>
+cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
+                   cudaStream_t stream) {
+  const size_t smem = sizeof(float) * ((size_t)BM * p.c.D + (size_t)BN * (p.c.D + 1) +
+                                       (size_t)BN * p.c.D + (size_t)BM * (BN + 1));
+  cudaError_t e = cudaFuncSetAttribute(softmax_simt_kernel<T, E4M3>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  softmax_simt_kernel<T, E4M3>
+      <<<dim3((unsigned)blocks, p.splits), kThreads, smem, stream>>>(p, (int)tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int softmax_simt_rows() { return BM; }
+
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, int dtype, bool e4m3, long long tiles,
+                                long long blocks, cudaStream_t stream) {
+  if (dtype == HSTU_F32)
+    return e4m3 ? launch<float, true>(p, tiles, blocks, stream) : launch<float, false>(p, tiles, blocks, stream);
+  if (dtype == HSTU_BF16)
+    return e4m3 ? launch<__nv_bfloat16, true>(p, tiles, blocks, stream)
+                : launch<__nv_bfloat16, false>(p, tiles, blocks, stream);
+  return e4m3 ? launch<__half, true>(p, tiles, blocks, stream) : launch<__half, false>(p, tiles, blocks, stream);
+}
+
+cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream) {
+  int shift = 0;
+  while (shift < 5 && (4 << shift) < p.c.D) ++shift;
+  const long long lanes = p.c.T * p.Nq << shift;
+  const unsigned grid = (unsigned)((lanes + kThreads - 1) / kThreads);
+  if (dtype == HSTU_F32)
+    softmax_combine_kernel<float><<<grid, kThreads, 0, stream>>>(p, shift);
+  else if (dtype == HSTU_BF16)
+    softmax_combine_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p, shift);
+  else
+    softmax_combine_kernel<__half><<<grid, kThreads, 0, stream>>>(p, shift);
+  return cudaGetLastError();
+}
+
+}  // namespace hstu

@@ -106,6 +106,8 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
 
 // How a call runs: query rows of one CTA, key ranges, grid and workspace.
 struct AttnPlan {
+  bool tensor_cores;   // bf16 / fp16 (else the fp32 CUDA-core kernel)
+  int qtiles;          // query tiles of one CTA (tensor cores)
   int splits, min_range;
   long long tiles, blocks, workspace;
 };
@@ -123,14 +125,22 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     return HSTU_ERR_INVALID_ARG;
   const long long G = a->num_heads_q / c->num_heads_kv;
   if (G > 128) return HSTU_ERR_UNSUPPORTED;
-  *pl = AttnPlan{1, 128, 0, 0, 0};
+  *pl = AttnPlan{};
+  pl->splits = 1;
+  pl->min_range = 128;
   if (c->batch == 0 || a->total_tokens == 0 || G == 0) return HSTU_OK;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return HSTU_ERR_CUDA;
-  const long long bm = hstu::softmax_simt_rows();
   const long long most = a->max_seqlen < a->total_tokens ? a->max_seqlen : a->total_tokens;
+  pl->tensor_cores = a->dtype != HSTU_F32;
+  // query rows (token, head) of one CTA
+  long long bm = hstu::softmax_simt_rows();
+  if (pl->tensor_cores) {
+    pl->qtiles = most > 128 / G && c->head_dim <= 128 ? 2 : 1;
+    bm = pl->qtiles * (128 / G) * G;
+  }
   pl->tiles = (most * G + bm - 1) / bm;
   pl->blocks = c->batch * pl->tiles * c->num_heads_kv;
   if (pl->blocks > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
@@ -139,7 +149,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   if (items > c->batch * pl->tiles) items = c->batch * pl->tiles;
   items *= c->num_heads_kv;
   pl->min_range = 256;
-  const long long want = (4ll * sms + items - 1) / items;
+  const long long want = ((pl->tensor_cores ? 2ll : 4ll) * sms + items - 1) / items;
   const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
   pl->splits = (int)(want < can ? want : can);
   if (pl->splits > 1)
@@ -202,7 +212,10 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   p.part_lse = p.part_o + (long long)pl.splits * a->total_tokens * a->num_heads_q * c->head_dim;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = c->dtype == HSTU_FP8_E4M3;
-  cudaError_t e = hstu::launch_softmax_simt(p, a->dtype, fp8, pl.tiles, pl.blocks, s);
+  cudaError_t e =
+      pl.tensor_cores
+          ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.tiles, pl.blocks, s)
+          : hstu::launch_softmax_simt(p, fp8, pl.tiles, pl.blocks, s);
   if (e == cudaSuccess && pl.splits > 1) e = hstu::launch_softmax_combine(p, a->dtype, s);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }

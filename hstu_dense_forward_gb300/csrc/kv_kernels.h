@@ -14,10 +14,16 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
                            long long v_stride, int dtype, bool e4m3, bool append,
                            cudaStream_t stream);
 
-// CUDA-core attention.
+// fp32 attention on CUDA cores.
 int softmax_simt_rows();  // query rows (token, head) of one CTA
-cudaError_t launch_softmax_simt(const SoftmaxParams& p, int dtype, bool e4m3, long long tiles,
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, long long tiles,
                                 long long blocks, cudaStream_t stream);
+
+// Tensor-core attention (bf16, fp16). A CTA takes qtiles tiles of 128 / G tokens; two where
+// D <= 128 only.
+int softmax_tc_key_tile(int D);  // keys of one tile
+cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles,
+                              long long tiles, long long blocks, cudaStream_t stream);
 
 // Joins the key ranges of sequences that have more than one.
 cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream);

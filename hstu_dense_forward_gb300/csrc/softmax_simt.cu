@@ -1,4 +1,4 @@
-// Softmax attention over the paged KV cache on CUDA cores (FFMA, fp32 throughout), and the
+// fp32 softmax attention over the paged KV cache on CUDA cores (FFMA), and the
 // kernel that joins the key ranges of sequences worked on in parts.
 //
 // One CTA (256 threads) takes BM packed query rows of one kv head (packed row r of a sequence
@@ -27,16 +27,6 @@ constexpr int kMaxU = kMaxD / 16;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) {
-  return __bfloat162float(x);
-}
-template <typename T>
 __device__ __forceinline__ T from_float(float x);
 template <>
 __device__ __forceinline__ float from_float<float>(float x) { return x; }
@@ -47,7 +37,7 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-template <typename T, bool E4M3>
+template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxParams p, int tiles) {
   extern __shared__ float sm[];
   const int D = p.c.D;
@@ -81,12 +71,12 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
   const long long k0 = split * kr.keys;
   kend = min(kend, k0 + kr.keys);
 
-  const T* q = static_cast<const T*>(p.q);
+  const float* q = static_cast<const float*>(p.q);
   for (int x = threadIdx.x; x < BM * D; x += kThreads) {
     const int r = x / D, d = x - r * D;
     const long long pr = m0 + r;
-    Qs[x] = pr < rows ? to_float(q[(s.t0 + pr / p.G) * p.q_stride +
-                                   (hk * p.G + pr % p.G) * (long long)D + d])
+    Qs[x] = pr < rows ? q[(s.t0 + pr / p.G) * p.q_stride +
+                          (hk * p.G + pr % p.G) * (long long)D + d]
                       : 0.f;
   }
   float fk = p.scale_log2, fv = 1.f;  // static factors fold into the scale and the output
@@ -130,8 +120,8 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
             }
           }
         } else {
-          load16(static_cast<const T*>(p.c.cache) + ka, kx);
-          load16(static_cast<const T*>(p.c.cache) + va, vx);
+          load16(static_cast<const float*>(p.c.cache) + ka, kx);
+          load16(static_cast<const float*>(p.c.cache) + va, vx);
         }
       } else {
         if (n0 + r < kend) report(p.c, HSTU_DEVERR_OFFSETS);
@@ -219,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
       if (nsplit > 1)
         p.part_o[((long long)split * p.c.T * p.Nq + row) * D + d] = acc[a][u] * inv;
       else
-        static_cast<T*>(p.out)[row * D + d] = from_float<T>(acc[a][u] * inv);
+        static_cast<float*>(p.out)[row * D + d] = acc[a][u] * inv;
     }
     if (tx == 0) {
       if (nsplit > 1)
@@ -271,15 +261,15 @@ __global__ void __launch_bounds__(kThreads) softmax_combine_kernel(const Softmax
   if (p.lse && first == 0) p.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
-template <typename T, bool E4M3>
+template <bool E4M3>
 cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
                    cudaStream_t stream) {
   const size_t smem = sizeof(float) * ((size_t)BM * p.c.D + (size_t)BN * (p.c.D + 1) +
                                        (size_t)BN * p.c.D + (size_t)BM * (BN + 1));
-  cudaError_t e = cudaFuncSetAttribute(softmax_simt_kernel<T, E4M3>,
+  cudaError_t e = cudaFuncSetAttribute(softmax_simt_kernel<E4M3>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  softmax_simt_kernel<T, E4M3>
+  softmax_simt_kernel<E4M3>
       <<<dim3((unsigned)blocks, p.splits), kThreads, smem, stream>>>(p, (int)tiles);
   return cudaGetLastError();
 }
@@ -288,14 +278,9 @@ cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
 
 int softmax_simt_rows() { return BM; }
 
-cudaError_t launch_softmax_simt(const SoftmaxParams& p, int dtype, bool e4m3, long long tiles,
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, long long tiles,
                                 long long blocks, cudaStream_t stream) {
-  if (dtype == HSTU_F32)
-    return e4m3 ? launch<float, true>(p, tiles, blocks, stream) : launch<float, false>(p, tiles, blocks, stream);
-  if (dtype == HSTU_BF16)
-    return e4m3 ? launch<__nv_bfloat16, true>(p, tiles, blocks, stream)
-                : launch<__nv_bfloat16, false>(p, tiles, blocks, stream);
-  return e4m3 ? launch<__half, true>(p, tiles, blocks, stream) : launch<__half, false>(p, tiles, blocks, stream);
+  return e4m3 ? launch<true>(p, tiles, blocks, stream) : launch<false>(p, tiles, blocks, stream);
 }
 
 cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream) {

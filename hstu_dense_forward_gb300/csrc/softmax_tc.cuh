@@ -1,0 +1,693 @@
+// bf16 / fp16 softmax attention over the paged KV cache on the 5th-generation tensor cores.
+//
+// Per query row and tile of KT keys, in base 2 with the running reference m and sum l:
+//   S = Q K^T (fp32, TMEM), x = scale_log2 * S, P = 2^(x - m) (16-bit, TMEM, over S),
+//   l += sum P, O += P V (fp32, TMEM);  out = O / l.
+// m is raised to the row's running maximum only when that lies more than kLazy above it: P then
+// stays at or below 2^kLazy, which 16-bit weights and fp32 sums hold with the same relative
+// precision, and O (in TMEM) has to be rescaled a few times per row instead of once per tile.
+//
+// One CTA takes one item: a kv head, NQT tiles of up to 128 packed query rows (row r of a tile
+// is token r / G and query head hk * G + r % G, so that the G heads that share keys share their
+// loads) and one range of the keys. Warp roles:
+//   warps 0 .. 4 NQT - 1   softmax, one warpgroup per query tile, one thread per row;
+//   next warp              issues every tcgen05.mma; owns TMEM;
+//   next warp              TMA loads: Q, then K and V tiles through one ring, in the order
+//                          in which the products need them;
+//   E4M3: four more warps  turn E4M3 tiles (staged by TMA) into 16-bit ones in the ring,
+//                          times their row scales (exact in bf16: a scale is a power of two).
+// With two query tiles, one tile's products run while the softmax of the other does. With one
+// (few rows, or D = 256, whose O takes half of TMEM) the scores have two buffers instead.
+//
+// Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
+// leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
+#pragma once
+#include <cuda.h>
+
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv_cache.cuh"
+#include "kv_kernels.h"
+#include "ptx.cuh"
+
+namespace hstu {
+namespace sm {
+
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLazy = 8.0f;  // log2 of the largest weight
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D_, int NQT_, bool E4M3_>
+struct Cfg {
+  static constexpr int D = D_, NQT = NQT_;
+  static constexpr bool E4M3 = E4M3_;
+  static_assert(D == 64 || D == 128 || D == 256, "head dim of the kernel");
+  static_assert(NQT == 1 || (NQT == 2 && D <= 128), "query tiles");
+  static constexpr int KT = D == 256 ? 64 : 128;  // keys of one tile
+  static constexpr int NSB = NQT == 1 ? 2 : 1;    // score buffers of one query tile
+  static constexpr int SWB = 128, EPC = 64;       // swizzled row bytes and elements of a block
+  static constexpr int NCB = D / EPC;             // column blocks of a row
+  static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
+  static constexpr int KV_CB = KT * SWB, KV_TILE = NCB * KV_CB;
+  static constexpr int ST_TILE = KT * D;          // staged E4M3 tile
+  // ring depths: what 227 KB of shared memory holds next to Q
+  static constexpr int NSLOT = !E4M3 ? (D == 64 ? 6 : (NQT == 1 && D == 128 ? 6 : 4))
+                                     : (D == 64 ? 4 : (NQT == 1 && D == 128 ? 4 : 3));
+  static constexpr int NST = E4M3 ? (D == 64 ? 4 : (NQT == 1 && D == 128 ? 3 : 3)) : 0;
+  static constexpr int SM_WARPS = 4 * NQT;
+  static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1;
+  static constexpr int CONV_WARP = SM_WARPS + 4;  // (a warpgroup of its own)
+  static constexpr int THREADS = (SM_WARPS + 4 + (E4M3 ? 4 : 0)) * 32;
+  // TMEM: score buffers of KT columns (P over them), then O
+  static constexpr uint32_t O_COL = NQT * NSB * KT;
+  static_assert(O_COL + NQT * D <= kTmemCols, "TMEM");
+  static constexpr int OFF_Q = 0, OFF_KV = NQT * Q_TILE, OFF_ST = OFF_KV + NSLOT * KV_TILE;
+  static constexpr int OFF_BAR = OFF_ST + NST * ST_TILE;
+  static constexpr int USED = OFF_BAR + 2048 + 1024;  // (1024: alignment of the base)
+  // one CTA per SM: it takes all of TMEM
+  static constexpr int SMEM = USED < 120 * 1024 ? 120 * 1024 : USED;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+struct Bars {
+  uint64_t q_full, kv_full[6], kv_empty[6], st_full[4], st_empty[4];
+  uint64_t s_full[2], p_full[2], pv_done[2], drain;
+  uint32_t tmem_base;
+  volatile int abort;
+};
+static_assert(sizeof(Bars) <= 2048, "barrier block");
+
+// One CTA's work, computed by every thread.
+struct Item {
+  PagedSeq s;
+  int b, hk, split, nsplit;
+  int nq;                 // query tiles that hold rows
+  long long tok0;         // first token of tile 0
+  long long k0, kend;     // key range: of the item, and of each tile with the mask
+  long long tile_end[2];
+  int n[2];               // key tiles of each query tile (n[0] <= n[1] when both hold rows)
+  int nmax;
+};
+
+template <class C>
+__device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, Item& it) {
+  const long long blk = blockIdx.x;
+  const int tpt = 128 / p.G;  // tokens of one query tile
+  it.hk = (int)(blk % p.c.Nk);
+  const int tile = tiles - 1 - (int)(blk / p.c.Nk % tiles);  // later tiles see more keys: first
+  it.b = (int)(blk / p.c.Nk / tiles);
+  it.split = blockIdx.y;
+  it.s = paged_seq(p.c, it.b);
+  if (!attn_seq_ok(p, it.s)) {
+    if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+    return false;
+  }
+  const KeyRanges kr = key_ranges(p, it.s.Lk);
+  it.nsplit = kr.count;
+  it.tok0 = (long long)tile * C::NQT * tpt;
+  if (it.tok0 >= it.s.n || it.split >= kr.count) return false;
+  it.k0 = it.split * kr.keys;
+  it.kend = min(it.s.Lk, it.k0 + kr.keys);
+  it.nq = 0;
+  it.nmax = 0;
+#pragma unroll
+  for (int q = 0; q < C::NQT; ++q) {
+    it.n[q] = 0;
+    it.tile_end[q] = it.k0;
+    const long long first = it.tok0 + (long long)q * tpt;
+    if (first >= it.s.n) continue;
+    it.nq = q + 1;
+    long long e = it.kend;
+    if (p.causal) e = min(e, it.s.Lk - it.s.n + min(first + tpt, it.s.n));
+    it.tile_end[q] = e;
+    it.n[q] = e > it.k0 ? (int)((e - it.k0 + C::KT - 1) / C::KT) : 0;
+    it.nmax = it.n[q];
+  }
+  return true;
+}
+
+// Place of K and V tiles in the ring's order: the order in which the MMA warp needs them.
+// One query tile: K0 K1 V0 K2 V1 ... (the scores run a tile ahead); two: K0 V0 K1 V1 ...
+template <class C>
+__device__ __forceinline__ int k_index(int t) {
+  return C::NQT == 1 ? (t == 0 ? 0 : 2 * t - 1) : 2 * t;
+}
+template <class C>
+__device__ __forceinline__ int v_index(int t, int n) {
+  return C::NQT == 1 ? (t + 1 < n ? 2 * t + 2 : 2 * t + 1) : 2 * t + 1;
+}
+// The tile behind place i: its number, and whether it is a V tile.
+template <class C>
+__device__ __forceinline__ bool ring_tile(int i, int n, int& t) {
+  if (C::NQT == 2) {
+    t = i >> 1;
+    return i & 1;
+  }
+  if (i == 0 || (i & 1)) {
+    t = (i + 1) >> 1;
+    if (t < n) return false;  // K
+    t = n - 1;                // the last place
+    return true;
+  }
+  t = (i - 2) >> 1;
+  return true;
+}
+
+__device__ __forceinline__ bool wait_bar(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
+                                         uint32_t parity) {
+  const uint32_t a = ptx::smem_u32(bar);
+  if (ptx::mbar_try_wait(a, parity)) return true;
+  const uint64_t start = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(a, parity)) return true;
+    if ((i & 15u) == 0) {
+      if (bars->abort) return false;
+      if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
+        bars->abort = 1;
+        report(p.c, HSTU_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// The same by every lane of a warp, with a warp-uniform result (the tcgen05 loads and stores
+// that follow are executed by whole warps).
+__device__ __forceinline__ bool warp_wait(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
+                                          uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_bar(p, bars, bar, parity));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// ------------------------------------------------------------------ loads
+template <class C>
+__device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const Item& it,
+                          const CUtensorMap* tq, const CUtensorMap* tc) {
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const int tpt = 128 / p.G;
+  const uint32_t q_bytes = (uint32_t)(tpt * p.G) * C::SWB * C::NCB;
+  ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars->q_full), it.nq * q_bytes);
+  for (int q = 0; q < it.nq; ++q)
+#pragma unroll
+    for (int cb = 0; cb < C::NCB; ++cb)
+      ptx::tma_load_3d(sbase + C::OFF_Q + q * C::Q_TILE + cb * C::Q_CB, tq,
+                       ptx::smem_u32(&bars->q_full), cb * C::EPC, it.hk * p.G,
+                       (int)(it.s.t0 + it.tok0 + q * tpt));
+  const int ps = 1 << p.c.page_shift;
+  constexpr int DEPTH = C::E4M3 ? C::NST : C::NSLOT;
+  uint64_t* full = C::E4M3 ? bars->st_full : bars->kv_full;
+  uint64_t* empty = C::E4M3 ? bars->st_empty : bars->kv_empty;
+  const int boxes = ps >= C::KT ? 1 : C::KT / 32;
+  for (int i = 0; i < 2 * it.nmax; ++i) {
+    int t;
+    const bool v = ring_tile<C>(i, it.nmax, t);
+    const long long n0 = it.k0 + (long long)t * C::KT;
+    // page ids first: their latency passes while the slot is waited for. Places past the
+    // sequence's last page repeat that page (their rows are masked).
+    long long page[C::KT / 32];
+#pragma unroll
+    for (int m = 0; m < C::KT / 32; ++m) {
+      if (m >= boxes) break;
+      page[m] = page_at(p.c, it.s, min(n0 + 32 * m, it.s.Lk - 1));
+      if (page[m] < 0) {  // unspecified outputs, but a valid access
+        report(p.c, HSTU_DEVERR_OFFSETS);
+        page[m] = 0;
+      }
+    }
+    const int slot = i % DEPTH;
+    if (!wait_bar(p, bars, &empty[slot], ((i / DEPTH) & 1) ^ 1)) return;
+    const uint32_t bar = ptx::smem_u32(&full[slot]);
+    ptx::mbar_arrive_expect_tx(bar, C::E4M3 ? C::ST_TILE : C::KV_TILE);
+    const int row0 = ps >= C::KT ? (int)(n0 & (ps - 1)) : 0;
+#pragma unroll
+    for (int m = 0; m < C::KT / 32; ++m) {
+      if (m >= boxes) break;
+      const int plane = (int)(2 * page[m]) + (v ? 1 : 0);
+      if constexpr (C::E4M3) {
+        ptx::tma_load_4d(sbase + C::OFF_ST + slot * C::ST_TILE + m * 32 * C::D, tc, bar, 0, it.hk,
+                         row0, plane);
+      } else {
+#pragma unroll
+        for (int cb = 0; cb < C::NCB; ++cb)
+          ptx::tma_load_4d(sbase + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB + m * 32 * C::SWB,
+                           tc, bar, cb * C::EPC, it.hk, row0, plane);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ E4M3 -> 16 bits
+// A thread converts sixteen codes of a row at a time. Rows beyond the sequence become zeros
+// (what an unused row of a page holds, NaN included, does not reach the products).
+template <class C, bool BF16>
+__device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const Item& it,
+                             int warp, int lane) {
+  constexpr int CPR = C::D / 16;         // chunks of a row
+  constexpr int RPW = 32 / CPR;          // rows of one pass of a warp; four warps: STEP rows
+  constexpr int STEP = 4 * RPW, PASSES = C::KT / STEP;
+  static_assert(RPW * PASSES <= 32, "one row scale a lane");
+  const int chunk = lane % CPR, r0 = warp * RPW + lane / CPR;
+  const int cb = chunk / 4, c16 = (chunk % 4) * 2;  // column block, first 16-byte piece in it
+  const int my_row = warp * RPW + lane % RPW + STEP * (lane / RPW);  // whose scale it loads
+  for (int i = 0; i < 2 * it.nmax; ++i) {
+    int t;
+    const bool v = ring_tile<C>(i, it.nmax, t);
+    const long long n0 = it.k0 + (long long)t * C::KT;
+    const int have = (int)min((long long)C::KT, it.s.Lk - n0);
+    float my_scale = 1.0f;  // loaded before the waits, which hide its latency
+    if (p.c.scale && my_row < have) {
+      const long long page = page_at(p.c, it.s, n0 + my_row);
+      if (page >= 0)
+        my_scale = scale_value(p.c.scale[scale_row(p.c, page, v ? 1 : 0,
+                                                   (n0 + my_row) & (page_size(p.c) - 1), it.hk)]);
+    }
+    const int st = i % C::NST, slot = i % C::NSLOT;
+    if (!warp_wait(p, bars, &bars->st_full[st], (i / C::NST) & 1)) return;
+    if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
+    const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
+    uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
+#pragma unroll 4
+    for (int k = 0; k < PASSES; ++k) {
+      const int r = r0 + STEP * k;
+      const float f = __shfl_sync(0xffffffffu, my_scale, lane / CPR + RPW * k);
+      uint32_t w[8];
+      if (r < have) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + r * C::D);
+        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t h = e4m3x2_to_f16x2(in[e >> 1] >> (16 * (e & 1)));
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          w[e] = pack2<BF16>(x.x * f, x.y * f);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 0u;
+      }
+      uint8_t* row = dst + r * C::SWB;
+      *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (r & 7)) * 16)) =
+          make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    ptx::fence_proxy_async_smem();
+    ptx::mbar_arrive(ptx::smem_u32(&bars->kv_full[slot]));
+    ptx::mbar_arrive(ptx::smem_u32(&bars->st_empty[st]));
+  }
+}
+
+// ------------------------------------------------------------------ products
+template <class C, bool BF16>
+struct Issuer {
+  const SoftmaxParams& p;
+  Bars* bars;
+  uint32_t sbase, tmem;
+  static constexpr uint32_t IDESC_S = ptx::idesc_f16(BF16 ? 1u : 0u, 128, C::KT, 0);
+  static constexpr uint32_t IDESC_O = ptx::idesc_f16(BF16 ? 1u : 0u, 128, C::D, 1);
+
+  __device__ bool kv_ready(int i) {
+    if (!wait_bar(p, bars, &bars->kv_full[i % C::NSLOT], (i / C::NSLOT) & 1)) return false;
+    ptx::tc_fence_after();
+    return true;
+  }
+  __device__ void kv_release(int i) {
+    ptx::mma_commit(ptx::smem_u32(&bars->kv_empty[i % C::NSLOT]));
+  }
+  // scores of query tile q into buffer sb, K at ring place i
+  __device__ void scores(int q, int sb, int i) {
+    const uint64_t ad0 = ptx::smem_desc(sbase + C::OFF_Q + q * C::Q_TILE, 16, 8 * C::SWB, 2);
+    const uint64_t bd0 =
+        ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, 16, 8 * C::SWB, 2);
+#pragma unroll
+    for (int kk = 0; kk < C::D / 16; ++kk) {
+      const uint32_t in = (kk % 4) * 32;
+      ptx::mma_ss(tmem + sb * C::KT, ptx::desc_add(ad0, (kk / 4) * C::Q_CB + in),
+                  ptx::desc_add(bd0, (kk / 4) * C::KV_CB + in), IDESC_S, kk > 0 ? 1u : 0u);
+    }
+    ptx::mma_commit(ptx::smem_u32(&bars->s_full[sb]));
+  }
+  // O of query tile q += P (over score buffer sb) V at ring place i
+  __device__ void accumulate(int q, int sb, int i, bool first) {
+    const uint64_t bd0 =
+        ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, C::KV_CB, 8 * C::SWB, 2);
+#pragma unroll
+    for (int kk = 0; kk < C::KT / 16; ++kk)
+      ptx::mma_ts(tmem + C::O_COL + q * C::D, tmem + sb * C::KT + kk * 8,
+                  ptx::desc_add(bd0, kk * 16 * C::SWB), IDESC_O, (!first || kk > 0) ? 1u : 0u);
+    ptx::mma_commit(ptx::smem_u32(&bars->pv_done[q]));
+  }
+};
+
+template <class C, bool BF16>
+__device__ bool mma_loop(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars, const Item& it) {
+  if (!wait_bar(p, bars, &bars->q_full, 0)) return false;
+  const int n = it.nmax;
+  if constexpr (C::NQT == 1) {
+    for (int t = 0; t < 2 && t < n; ++t) {
+      if (!is.kv_ready(k_index<C>(t))) return false;
+      is.scores(0, t, k_index<C>(t));
+      is.kv_release(k_index<C>(t));
+    }
+    for (int t = 0; t < n; ++t) {
+      const int vi = v_index<C>(t, n);
+      if (!wait_bar(p, bars, &bars->p_full[t & 1], (t >> 1) & 1) || !is.kv_ready(vi)) return false;
+      is.accumulate(0, t & 1, vi, t == 0);
+      is.kv_release(vi);
+      if (t + 2 < n) {  // over P(t), which its product must have read
+        const int ki = k_index<C>(t + 2);
+        if (!wait_bar(p, bars, &bars->pv_done[0], t & 1) || !is.kv_ready(ki)) return false;
+        is.scores(0, t & 1, ki);
+        is.kv_release(ki);
+      }
+    }
+  } else {
+    if (!is.kv_ready(0)) return false;
+    for (int q = 0; q < it.nq; ++q)
+      if (it.n[q] > 0) is.scores(q, q, 0);
+    is.kv_release(0);
+    for (int t = 0; t < n; ++t) {
+      const int vi = v_index<C>(t, n), ki = k_index<C>(t + 1);
+      bool have_k = false;
+      if (!is.kv_ready(vi)) return false;
+      for (int q = 0; q < it.nq; ++q) {
+        if (t >= it.n[q]) continue;
+        if (!wait_bar(p, bars, &bars->p_full[q], t & 1)) return false;
+        ptx::tc_fence_after();
+        is.accumulate(q, q, vi, t == 0);
+        if (t + 1 < it.n[q]) {  // over P(t), which its product must have read
+          if (!have_k && !is.kv_ready(ki)) return false;
+          have_k = true;
+          if (!wait_bar(p, bars, &bars->pv_done[q], t & 1)) return false;
+          is.scores(q, q, ki);
+        }
+      }
+      is.kv_release(vi);
+      if (t + 1 < n) is.kv_release(ki);
+    }
+  }
+  return true;
+}
+
+// Waits for the MMAs issued so far, whatever ended the loop: TMEM is freed after this.
+__device__ __forceinline__ void mma_drain(const SoftmaxParams& p, Bars* bars) {
+  ptx::mma_commit(ptx::smem_u32(&bars->drain));
+  const uint64_t start = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait(ptx::smem_u32(&bars->drain), 0)) {
+    if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
+      bars->abort = 1;
+      report(p.c, HSTU_DEVERR_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+template <class C, bool BF16>
+__device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, uint32_t tmem,
+                             const Item& it, int q, int warp, int lane) {
+  constexpr int KT = C::KT;
+  const int r = (warp & 3) * 32 + lane;  // row of the tile, TMEM lane
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const int tpt = 128 / p.G;
+  const long long tok = it.tok0 + (long long)q * tpt + r / p.G;
+  const bool valid = r < tpt * p.G && tok < it.s.n;
+  const bool any = __any_sync(0xffffffffu, valid);
+  // keys that the row sees: positions [k0, k0 + lim); rows without a token follow the widest
+  long long see = it.kend;
+  if (p.causal && valid) see = min(see, it.s.Lk - it.s.n + tok + 1);
+  const int lim = (int)max(see - it.k0, 0ll);
+  const int n = it.n[q];
+  float fk = p.scale_log2, fv = 1.0f;  // static factors fold into the scale and the output
+  if (C::E4M3 && p.c.k_ds) {
+    fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
+    fv = p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
+  }
+  float m = -CUDART_INF_F, l = 0.0f;
+  const uint32_t o_col = tmem + lane_off + C::O_COL + q * C::D;
+  for (int t = 0; t < n; ++t) {
+    const int sb = C::NQT == 1 ? (t & 1) : q;
+    const uint32_t par = C::NQT == 1 ? (t >> 1) & 1 : t & 1;
+    if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
+    ptx::tc_fence_after();
+    const uint32_t s_col = tmem + lane_off + sb * KT;
+    if (any) {
+      uint32_t sv[KT / 32][32];
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c) ptx::tmem_ld32_issue(s_col + c * 32, sv[c]);
+      ptx::tmem_ld_wait(sv[0]);
+#pragma unroll
+      for (int c = 1; c < KT / 32; ++c) ptx::reg_fence(sv[c]);
+      const int left = lim - t * KT;  // keys of the tile that the row sees
+      if (!__all_sync(0xffffffffu, left >= KT)) {
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= left) sv[c][e] = 0xff800000u;  // -inf
+      }
+      float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      if (fk >= 0.0f) {
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(sv[c][e]));
+      } else {  // a negative static factor: the scores change sign (and masked ones keep theirs)
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (c * 32 + e >= left) sv[c][e] = 0x7f800000u;
+            top[e & 3] = fmaxf(top[e & 3], -__uint_as_float(sv[c][e]));
+          }
+      }
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(fk);
+      // raise the reference: at the first visible key, and when weights would pass 2^kLazy
+      const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
+      if (__any_sync(0xffffffffu, raise)) {
+        const float corr = raise ? ex2(m - mx) : 1.0f;  // (0 at the first visible key)
+        if (raise) {
+          m = mx;
+          l *= corr;
+        }
+        if (t > 0) {  // (S(t) was issued after PV(t - 2) was done: this phase is the next one)
+          if (!warp_wait(p, bars, &bars->pv_done[q], (t - 1) & 1)) return;
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < C::D; c += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(o_col + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            ptx::tmem_st16(o_col + c, o);
+          }
+        }
+      }
+      const float neg = m == -CUDART_INF_F ? 0.0f : -m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float x0, x1;
+          ptx::fma_f32x2(x0, x1, __uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1]),
+                         fk, fk, neg, neg);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          sum[(2 * e) & 3] += p0;
+          sum[(2 * e + 1) & 3] += p1;
+          pk[e] = pack2<BF16>(p0, p1);
+        }
+        ptx::tmem_st16(s_col + c * 16, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      ptx::tmem_st_wait();
+    }
+    if constexpr (!C::E4M3) {
+      // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
+      const long long n0 = it.k0 + (long long)t * KT;
+      const int have = (int)min((long long)KT, it.s.Lk - n0);
+      if (have < KT) {
+        const int vi = v_index<C>(t, it.nmax);
+        if (!warp_wait(p, bars, &bars->kv_full[vi % C::NSLOT], (vi / C::NSLOT) & 1)) return;
+        uint8_t* v = smem + C::OFF_KV + (vi % C::NSLOT) * C::KV_TILE;
+        const int pieces = (KT - have) * (C::SWB / 16);  // of one column block
+        for (int x = r; x < C::NCB * pieces; x += 128)
+          *reinterpret_cast<uint4*>(v + (x / pieces) * C::KV_CB + have * C::SWB +
+                                    (x % pieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();
+      }
+    }
+    // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
+    // below needs PV(n - 2) to be done; S(n - 1) was issued after PV(n - 1 - NSB) only, and
+    // once P(n - 1) is handed over both may complete at any time.
+    if (C::NSB > 1 && t > 0 && t == n - 1 &&
+        !warp_wait(p, bars, &bars->pv_done[q], (t - 1) & 1))
+      return;
+    ptx::tc_fence_before();
+    ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
+  }
+  if (n > 0) {
+    if (!warp_wait(p, bars, &bars->pv_done[q], (n - 1) & 1)) return;
+    ptx::tc_fence_after();
+  }
+  if (!any) return;
+  const long long row = (it.s.t0 + tok) * p.Nq + it.hk * p.G + r % p.G;  // of out and lse
+  const float inv = l > 0.0f ? fv / l : l;  // (a NaN sum stays one)
+  const int D = p.c.D;
+#pragma unroll 1
+  for (int c = 0; c < C::D; c += 16) {
+    if (c >= D) break;
+    uint32_t o[16];
+    if (n > 0) {
+      ptx::tmem_ld16(o_col + c, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = 0u;
+    }
+    if (!valid) continue;
+    float f[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+    if (it.nsplit > 1) {
+      store16(p.part_o + ((long long)it.split * p.c.T * p.Nq + row) * D + c, f);
+    } else if constexpr (BF16) {
+      store16(static_cast<__nv_bfloat16*>(p.out) + row * D + c, f);
+    } else {
+      store16(static_cast<__half*>(p.out) + row * D + c, f);
+    }
+  }
+  if (valid) {
+    const float log2sum = l == 0.0f ? -CUDART_INF_F : m + log2f(l);
+    if (it.nsplit > 1)
+      p.part_lse[(long long)it.split * p.c.T * p.Nq + row] = log2sum;
+    else if (p.lse)
+      p.lse[row] = log2sum * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D, int NQT, bool BF16, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
+    softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_c, const SoftmaxParams p,
+                      int tiles) {
+  using C = Cfg<D, NQT, E4M3>;
+  extern __shared__ uint8_t smem_raw[];
+  Item it;
+  if (!make_item<C>(p, tiles, it)) return;  // (the whole CTA)
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == C::LOAD_WARP && lane == 0) {
+    ptx::mbar_init(ptx::smem_u32(&bars->q_full), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
+    for (int s = 0; s < 6; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), C::E4M3 ? 128 : 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->st_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->st_empty[s]), 128);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->s_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->p_full[s]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bars->pv_done[s]), 1);
+    }
+    bars->abort = 0;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == C::MMA_WARP) {
+    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // 512 threads launch with 128 registers each (65,536): the softmax keeps a row of scores in
+  // registers and takes 176, the conversion 96 and the control warps 64, 65,536 again.
+  constexpr bool SPLIT = C::THREADS == 512;
+  if constexpr (SPLIT) {
+    if (warp < C::SM_WARPS)
+      ptx::regs_inc<176>();
+    else if (warp < C::CONV_WARP)
+      ptx::regs_dec<64>();
+    else
+      ptx::regs_dec<96>();
+  }
+  if (warp < C::SM_WARPS) {
+    if (warp / 4 < it.nq) softmax_role<C, BF16>(p, bars, smem, tmem, it, warp / 4, warp, lane);
+  } else if (warp == C::MMA_WARP) {
+    if (lane == 0 && it.nmax > 0) {
+      Issuer<C, BF16> is{p, bars, ptx::smem_u32(smem), tmem};
+      mma_loop<C, BF16>(p, is, bars, it);
+      mma_drain(p, bars);
+    }
+  } else if (warp == C::LOAD_WARP) {
+    if (lane == 0 && it.nmax > 0) load_role<C>(p, bars, smem, it, &tm_q, &tm_c);
+  } else if (C::E4M3 && warp >= C::CONV_WARP) {
+    convert_role<C, BF16>(p, bars, smem, it, warp - C::CONV_WARP, lane);
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (bars->abort) {
+    // copies that were issued but never consumed land before the CTA exits
+    const uint64_t start = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - start < 200000ull) {
+    }
+  }
+  ptx::tc_fence_after();
+  if (warp == C::MMA_WARP) {
+    __syncwarp();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, int NQT, bool BF16, bool E4M3>
+cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
+                           long long tiles, long long blocks, cudaStream_t stream) {
+  using C = Cfg<D, NQT, E4M3>;
+  auto* kernel = softmax_tc_kernel<D, NQT, BF16, E4M3>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  kernel<<<dim3((unsigned)blocks, p.splits), C::THREADS, C::SMEM, stream>>>(tq, tc, p, (int)tiles);
+  return cudaGetLastError();
+}
+
+// Kernel for the head dim and number of query tiles.
+template <bool BF16, bool E4M3>
+cudaError_t launch_tc(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
+                      int qtiles, long long tiles, long long blocks, cudaStream_t s) {
+  if (p.c.D > 128) return launch_variant<256, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+  if (p.c.D > 64)
+    return qtiles == 2 ? launch_variant<128, 2, BF16, E4M3>(p, tq, tc, tiles, blocks, s)
+                       : launch_variant<128, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+  return qtiles == 2 ? launch_variant<64, 2, BF16, E4M3>(p, tq, tc, tiles, blocks, s)
+                     : launch_variant<64, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+}
+
+}  // namespace sm
+}  // namespace hstu

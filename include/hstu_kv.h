@@ -110,8 +110,9 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * page beyond the sequence's end may hold anything. Rows of out and lse that belong to no
  * sequence are left alone.
  *
- * Statistics and sums are fp32. fp16 and bf16: the weights are rounded to the type of q (to
- * fp16 over an E4M3 cache) for the product with V.
+ * Statistics and sums are fp32. fp16 and bf16: the weights are rounded to the type of q for the
+ * product with V, and the keys and values of an E4M3 cache are taken as hstu_kv_read gives them
+ * in that type (static factors are applied in fp32 to the scores and the output instead).
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */

@@ -43,7 +43,7 @@ bool cache_pointers_ok(const hstu_kv_cache* c) {
     return false;
   const uintptr_t ib = c->index_is_int64 ? 8 : 4;
   if (!aligned(c->page_offsets, ib) || !aligned(c->last_page_len, ib) ||
-      !aligned(c->page_ids, ib) || !aligned(c->status, 4))
+      !aligned(c->page_ids, ib) || !aligned(c->status, 4) || !aligned(c->kv_scale, 16))
     return false;
   const bool factors = c->descale != HSTU_DESCALE_CAST;
   if (factors != (c->k_descale != nullptr) || factors != (c->v_descale != nullptr)) return false;
@@ -106,8 +106,9 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
 
 // How a call runs: query rows of one CTA, key ranges, grid and workspace.
 struct AttnPlan {
-  bool tensor_cores;   // bf16 / fp16 (else the fp32 CUDA-core kernel)
-  int qtiles;          // query tiles of one CTA (tensor cores)
+  enum { SIMT, TC, ROWS } kernel;
+  int qtiles;          // query tiles of one CTA (TC)
+  int cluster;         // CTAs that divide the keys of one item (ROWS)
   int splits, min_range;
   long long tiles, blocks, workspace;
 };
@@ -134,24 +135,40 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return HSTU_ERR_CUDA;
   const long long most = a->max_seqlen < a->total_tokens ? a->max_seqlen : a->total_tokens;
-  pl->tensor_cores = a->dtype != HSTU_F32;
-  // query rows (token, head) of one CTA
+  // query rows (token, head) of one item: a CTA's, or a cluster's
   long long bm = hstu::softmax_simt_rows();
-  if (pl->tensor_cores) {
+  if (a->dtype == HSTU_F32) {
+    pl->kernel = AttnPlan::SIMT;
+  } else if (most * G <= 16) {
+    pl->kernel = AttnPlan::ROWS;
+    bm = 16;
+  } else {
+    pl->kernel = AttnPlan::TC;
     pl->qtiles = most > 128 / G && c->head_dim <= 128 ? 2 : 1;
     bm = pl->qtiles * (128 / G) * G;
   }
   pl->tiles = (most * G + bm - 1) / bm;
   pl->blocks = c->batch * pl->tiles * c->num_heads_kv;
-  if (pl->blocks > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
+  if (pl->blocks * 8 > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
   // row tiles that hold rows: at most one partly filled tile a sequence
   long long items = a->total_tokens * G / bm + c->batch;
   if (items > c->batch * pl->tiles) items = c->batch * pl->tiles;
   items *= c->num_heads_kv;
-  pl->min_range = 256;
-  const long long want = ((pl->tensor_cores ? 2ll : 4ll) * sms + items - 1) / items;
-  const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
-  pl->splits = (int)(want < can ? want : can);
+  pl->cluster = 1;
+  if (pl->kernel == AttnPlan::ROWS) {
+    const long long slots = (c->head_dim > 128 ? 1ll : 2ll) * sms;  // CTAs resident at a time
+    long long want = (2 * slots + items - 1) / items;
+    const long long can = (a->max_seqlen_k + 127) / 128;  // two tiles of 64 keys each
+    if (want > can) want = can;
+    while (pl->cluster < 8 && pl->cluster * 2 <= want) pl->cluster *= 2;
+    pl->splits = (int)(want / pl->cluster);
+    pl->min_range = 128 * pl->cluster;
+  } else {
+    pl->min_range = 256;
+    const long long want = ((pl->kernel == AttnPlan::TC ? 2ll : 4ll) * sms + items - 1) / items;
+    const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
+    pl->splits = (int)(want < can ? want : can);
+  }
   if (pl->splits > 1)
     pl->workspace = (long long)pl->splits * a->total_tokens * a->num_heads_q *
                     (c->head_dim + 1) * 4;
@@ -213,7 +230,9 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = c->dtype == HSTU_FP8_E4M3;
   cudaError_t e =
-      pl.tensor_cores
+      pl.kernel == AttnPlan::ROWS
+          ? hstu::launch_softmax_rows(p, a->dtype, fp8, pl.tiles, pl.blocks, pl.cluster, s)
+      : pl.kernel == AttnPlan::TC
           ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.tiles, pl.blocks, s)
           : hstu::launch_softmax_simt(p, fp8, pl.tiles, pl.blocks, s);
   if (e == cudaSuccess && pl.splits > 1) e = hstu::launch_softmax_combine(p, a->dtype, s);

@@ -16,7 +16,7 @@
  *   static factors  k_descale / v_descale of hstu_fwd_descale's TENSOR, BATCH or HEAD
  *                   granularity: value = factor * E4M3 value (the form hstu_fwd reads);
  *   row scales      kv_scale [num_pages, 2, Nk, page_size], one unsigned byte s per page,
- *                   plane, head and row: value = 2^(s - 127) * E4M3 value.
+ *                   plane, head and row, 1 <= s <= 253: value = 2^(s - 127) * E4M3 value.
  *
  * Ownership: the caller owns every tensor, workspaces included; no entry point allocates,
  * synchronises or keeps anything between calls, so calls on different streams, and captured
@@ -56,7 +56,7 @@ typedef struct {
                             (none), TENSOR, BATCH or HEAD; CAST with kv_scale */
   int reserved;          /* must be 0 */
   void* kv_cache;        /* 16-byte aligned */
-  void* kv_scale;        /* E4M3 with row scales, or NULL */
+  void* kv_scale;        /* E4M3 with row scales, 16-byte aligned, or NULL */
   long long num_pages;   /* in [1, 2^30] */
   const void* page_offsets;   /* [B + 1] */
   const void* page_ids;       /* [num_page_ids], each in [0, num_pages) */

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "../../include/hstu_kv.h"
@@ -104,6 +105,16 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
              : HSTU_ERR_CUDA;
 }
 
+// Streaming multiprocessors of a device, asked for once.
+bool device_sms(int dev, int* sms) {
+  static std::atomic<int> known[64];
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+  if (keep) known[dev].store(*sms, std::memory_order_relaxed);
+  return true;
+}
+
 // How a call runs: query rows of one CTA, key ranges, grid and workspace.
 struct AttnPlan {
   enum { SIMT, TC, ROWS } kernel;
@@ -131,9 +142,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   pl->min_range = 128;
   if (c->batch == 0 || a->total_tokens == 0 || G == 0) return HSTU_OK;
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return HSTU_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   const long long most = a->max_seqlen < a->total_tokens ? a->max_seqlen : a->total_tokens;
   // query rows (token, head) of one item: a CTA's, or a cluster's
   long long bm = hstu::softmax_simt_rows();

@@ -3,7 +3,21 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace hstu {
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device (`done`: one bit each).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit & done.load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 struct CacheView;
 struct SoftmaxParams;

@@ -607,8 +607,8 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tc, long l
                            long long blocks, int cluster, cudaStream_t stream) {
   using C = Cfg<D, BF16, E4M3>;
   auto* kernel = softmax_rows_kernel<D, BF16, E4M3>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::USED);
+  static std::atomic<unsigned long long> done;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::USED, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks * cluster), p.splits);

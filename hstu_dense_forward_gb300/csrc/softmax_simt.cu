@@ -266,8 +266,10 @@ cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
                    cudaStream_t stream) {
   const size_t smem = sizeof(float) * ((size_t)BM * p.c.D + (size_t)BN * (p.c.D + 1) +
                                        (size_t)BN * p.c.D + (size_t)BM * (BN + 1));
-  cudaError_t e = cudaFuncSetAttribute(softmax_simt_kernel<E4M3>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int kMost = sizeof(float) * (BM * kMaxD + BN * (kMaxD + 1) + BN * kMaxD + BM * (BN + 1));
+  static std::atomic<unsigned long long> done;
+  const cudaError_t e =
+      allow_smem(reinterpret_cast<const void*>(softmax_simt_kernel<E4M3>), kMost, done);
   if (e != cudaSuccess) return e;
   softmax_simt_kernel<E4M3>
       <<<dim3((unsigned)blocks, p.splits), kThreads, smem, stream>>>(p, (int)tiles);

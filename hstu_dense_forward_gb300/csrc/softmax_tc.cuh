@@ -670,8 +670,8 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const 
                            long long tiles, long long blocks, cudaStream_t stream) {
   using C = Cfg<D, NQT, E4M3>;
   auto* kernel = softmax_tc_kernel<D, NQT, BF16, E4M3>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<unsigned long long> done;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
   kernel<<<dim3((unsigned)blocks, p.splits), C::THREADS, C::SMEM, stream>>>(tq, tc, p, (int)tiles);
   return cudaGetLastError();

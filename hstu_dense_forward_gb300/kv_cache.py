@@ -14,6 +14,8 @@ the current stream. Nothing is kept between calls: workspaces come from torch's 
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 
 import torch
 
@@ -24,6 +26,13 @@ __all__ = ["hstu_kv_append", "hstu_kv_read", "hstu_softmax_fwd"]
 _ROWS = {torch.float32: _abi.HSTU_F32, torch.float16: _abi.HSTU_F16, torch.bfloat16: _abi.HSTU_BF16}
 _CACHE = {**_ROWS, torch.float8_e4m3fn: _abi.HSTU_FP8_E4M3}
 _INDEX = (torch.int32, torch.int64)
+_FP8 = torch.float8_e4m3fn
+
+# The C structs as bytes (their layouts are those of the ctypes mirrors in _abi): one pack is
+# a fraction of the cost of setting their fields.
+_PACK_CACHE = struct.Struct("@8iPPqPPPqPPP").pack
+_PACK_ROWS = struct.Struct("@PPqqPqii").pack
+_PACK_ATTN = struct.Struct("@PqPqiiiiifPPPqi4x").pack
 
 
 def _tensor(t, name, dev, dtype, shape):
@@ -42,22 +51,26 @@ def _tensor(t, name, dev, dtype, shape):
 
 
 def _rows(t, name, dev, dtype, heads, head_dim):
-    """Elements between the rows of t [T, heads, head_dim], whose rows are contiguous."""
+    """Elements between the rows of t [T, heads, head_dim], whose rows are contiguous (heads
+    None: any number)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [T, {'N' if heads is None else heads}, {head_dim}], "
-                         f"got {list(t.shape)}")
+                         f"got {list(shape)}")
+    width = shape[1] * head_dim
+    if t.is_contiguous():
+        return width
     row, head, last = t.stride()
-    width = t.shape[1] * head_dim
-    if last != 1 or (head != head_dim and t.shape[1] > 1) or (row < width and t.shape[0] > 1):
+    if last != 1 or (head != head_dim and shape[1] > 1) or (row < width and shape[0] > 1):
         raise ValueError(f"the rows of {name} must be contiguous and may not overlap, "
                          f"got strides {list(t.stride())}")
-    return row if t.shape[0] > 1 else width
+    return row if shape[0] > 1 else width
 
 
 def _factors(k_descale, v_descale, dev, B, Nk):
@@ -84,9 +97,8 @@ def _factors(k_descale, v_descale, dev, B, Nk):
                      f"got {list(shape)}")
 
 
-def _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
-           v_descale, status):
-    """The checked hstu_kv_cache, and the tensors made for it (kept until the launch)."""
+def _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale):
+    """Raises for what is wrong with these tensors."""
     if not isinstance(kv_cache, torch.Tensor):
         raise TypeError("kv_cache must be a torch.Tensor")
     dev = kv_cache.device
@@ -99,7 +111,7 @@ def _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scal
                          f"{list(kv_cache.shape)}")
     if not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous")
-    pages, _, page_size, Nk, D = kv_cache.shape
+    pages, _, page_size, Nk, _ = kv_cache.shape
     if not isinstance(seq_offsets, torch.Tensor):
         raise TypeError("seq_offsets must be a torch.Tensor")
     index = seq_offsets.dtype
@@ -109,55 +121,107 @@ def _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scal
         raise ValueError("seq_offsets must be [B + 1]")
     B = seq_offsets.shape[0] - 1
     _tensor(seq_offsets, "seq_offsets", dev, index, seq_offsets.shape)
-    c = _abi.KVCache()
-    c.page_offsets = _tensor(page_offsets, "page_offsets", dev, index, (B + 1,))
-    c.last_page_len = _tensor(last_page_len, "last_page_len", dev, index, (B,))
+    _tensor(page_offsets, "page_offsets", dev, index, (B + 1,))
+    _tensor(last_page_len, "last_page_len", dev, index, (B,))
     if not isinstance(page_ids, torch.Tensor) or page_ids.dim() != 1:
         raise ValueError("page_ids must be a one-dimensional torch.Tensor")
-    c.page_ids = _tensor(page_ids, "page_ids", dev, index, page_ids.shape) or None
-    c.num_page_ids = page_ids.shape[0]
-    fp8 = kv_cache.dtype == torch.float8_e4m3fn
-    keep = None
-    if not fp8 and not (kv_scale is None and k_descale is None and v_descale is None):
-        raise ValueError("kv_scale, k_descale and v_descale go with FP8 E4M3 caches")
+    _tensor(page_ids, "page_ids", dev, index, page_ids.shape)
     if kv_scale is not None:
-        if k_descale is not None or v_descale is not None:
+        _tensor(kv_scale, "kv_scale", dev, torch.uint8, (pages, 2, Nk, page_size))
+
+
+class _Cache:
+    """The checked hstu_kv_cache (packed) and what the entry points need of it."""
+    __slots__ = ("packed", "device", "index", "dtype", "B", "Nk", "D", "sizes", "keep")
+
+
+def _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
+           v_descale, status):
+    c = _Cache()
+    try:  # one pass over what is usually right; _explain_cache says what is not
+        dev = c.device = kv_cache.get_device()
+        pages, two, page_size, Nk, D = kv_cache.shape
+        index = seq_offsets.dtype
+        B1, = seq_offsets.shape
+        num_ids, = page_ids.shape
+        ok = (dev >= 0 and two == 2 and kv_cache.dtype in _CACHE and index in _INDEX and B1 > 0 and
+              kv_cache.is_contiguous() and page_offsets.shape == (B1,) and
+              last_page_len.shape == (B1 - 1,) and
+              (kv_scale is None or
+               (kv_scale.dtype is torch.uint8 and kv_scale.get_device() == dev and
+                kv_scale.shape == (pages, 2, Nk, page_size) and kv_scale.is_contiguous())))
+        for t in (seq_offsets, page_offsets, page_ids, last_page_len):
+            ok = ok and t.dtype is index and t.get_device() == dev and t.is_contiguous()
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale)
+        raise ValueError("kv_cache and its page table do not fit together")
+    c.dtype, c.index, c.B, c.Nk, c.D, c.keep = kv_cache.dtype, index, B1 - 1, Nk, D, None
+    fp8 = c.dtype is _FP8
+    descale, kd, vd = _abi.HSTU_DESCALE_CAST, 0, 0
+    if kv_scale is not None or k_descale is not None or v_descale is not None:
+        if not fp8:
+            raise ValueError("kv_scale, k_descale and v_descale go with FP8 E4M3 caches")
+        if kv_scale is None:
+            descale, *c.keep = _factors(k_descale, v_descale, kv_cache.device, c.B, Nk)
+            kd, vd = c.keep[0].data_ptr(), c.keep[1].data_ptr()
+        elif k_descale is not None or v_descale is not None:
             raise ValueError("a cache has row scales (kv_scale) or static factors, not both")
-        c.kv_scale = _tensor(kv_scale, "kv_scale", dev, torch.uint8, (pages, 2, Nk, page_size))
-    elif fp8:
-        c.descale, kd, vd = _factors(k_descale, v_descale, dev, B, Nk)
-        if kd is not None:
-            keep = (kd, vd)
-            c.k_descale, c.v_descale = kd.data_ptr(), vd.data_ptr()
-    if status is not None:
-        c.status = _tensor(status, "status", dev, torch.int32, (1,))
-    c.dtype = _CACHE[kv_cache.dtype]
-    c.batch, c.num_heads_kv, c.head_dim, c.page_size = B, Nk, D, page_size
-    c.index_is_int64 = index == torch.int64
-    c.kv_cache = kv_cache.data_ptr()
-    c.num_pages = pages
-    return c, keep
+    status_ptr = 0 if status is None else _tensor(status, "status", kv_cache.device, torch.int32,
+                                                  (1,))
+    c.sizes = (_CACHE[c.dtype], c.B, Nk, D, page_size, index is torch.int64, descale)
+    c.packed = _PACK_CACHE(*c.sizes, 0, kv_cache.data_ptr(),
+                           0 if kv_scale is None else kv_scale.data_ptr(), pages,
+                           page_offsets.data_ptr(), page_ids.data_ptr(), last_page_len.data_ptr(),
+                           num_ids, kd, vd, status_ptr)
+    return c
 
 
-def _row_dtype(kv_cache, dtype):
-    if dtype not in _ROWS:
+def _row_dtype(c, dtype):
+    code = _ROWS.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    if kv_cache.dtype not in (dtype, torch.float8_e4m3fn):
+    if c.dtype is not dtype and c.dtype is not _FP8:
         raise TypeError(f"{dtype} rows need a kv_cache of their type or of FP8 E4M3, got "
-                        f"{kv_cache.dtype}")
-    return _ROWS[dtype]
+                        f"{c.dtype}")
+    return code
 
 
-def _call(name, dev, *args):
-    """One entry point on dev's current stream."""
+def _call(name, c, *args):
+    """One entry point on the cache's device and that device's current stream."""
     fn = getattr(_abi.lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if torch._C._cuda_getDevice() == c.device:
+        status = fn(c.packed, *args, torch._C._cuda_getCurrentRawStream(c.device))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(c.device):
+            status = fn(c.packed, *args, torch._C._cuda_getCurrentRawStream(c.device))
     if status:
         _abi.check(status, name)
+
+
+def _copy(name, c, k, v, seq_offsets):
+    """hstu_kv_append / hstu_kv_read of the rows k and v."""
+    dtype = _row_dtype(c, k.dtype)
+    k_stride = _rows(k, "k", c.device, k.dtype, c.Nk, c.D)
+    v_stride = _rows(v, "v", c.device, k.dtype, c.Nk, c.D)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have one shape")
+    _call(name, c, _PACK_ROWS(k.data_ptr(), v.data_ptr(), k_stride, v_stride,
+                              seq_offsets.data_ptr(), T, dtype, 0))
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(device, cache_sizes, attn_sizes):
+    """hstu_softmax_workspace for these sizes (it reads no pointer) on this device."""
+    need = ctypes.c_longlong(0)
+    with torch.cuda.device(device):
+        _abi.check(_abi.lib().hstu_softmax_workspace(
+            _PACK_CACHE(*cache_sizes, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0),
+            _PACK_ATTN(0, 0, 0, *attn_sizes, 0, 0, 0, 0, 0), ctypes.byref(need)),
+            "hstu_softmax_workspace")
+    return need.value
 
 
 def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_page_len,
@@ -179,20 +243,11 @@ def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_
 
     status: an int32 tensor of one element that is set to 1 where offsets, lengths or page ids
     are found invalid on the device (nothing of such a sequence is written)."""
-    c, keep = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
-                     k_descale, v_descale, status)
-    dev = kv_cache.device
-    r = _abi.KVRows()
+    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
+               v_descale, status)
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
-    r.dtype = _row_dtype(kv_cache, k.dtype)
-    r.k_stride = _rows(k, "k", dev, k.dtype, c.num_heads_kv, c.head_dim)
-    r.v_stride = _rows(v, "v", dev, k.dtype, c.num_heads_kv, c.head_dim)
-    if k.shape != v.shape:
-        raise ValueError("k and v must have one shape")
-    r.k, r.v, r.seq_offsets = k.data_ptr(), v.data_ptr(), seq_offsets.data_ptr()
-    r.total_tokens = k.shape[0]
-    _call("hstu_kv_append", dev, ctypes.byref(c), ctypes.byref(r))
+    _copy("hstu_kv_append", c, k, v, seq_offsets)
     return kv_cache
 
 
@@ -206,33 +261,24 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
     dequantised by kv_scale or k_descale / v_descale, bf16). k and v may be given instead (rows
     as for hstu_kv_append); rows of no sequence are left as they were. Other arguments as for
     hstu_kv_append."""
-    c, keep = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
-                     k_descale, v_descale, status)
-    dev = kv_cache.device
+    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
+               v_descale, status)
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
     if k is None:
         if total_tokens is None:
             raise ValueError("hstu_kv_read needs total_tokens, or k and v")
         if dtype is None:
-            dtype = torch.bfloat16 if kv_cache.dtype == torch.float8_e4m3fn else kv_cache.dtype
-        _row_dtype(kv_cache, dtype)
-        shape = (int(total_tokens), c.num_heads_kv, c.head_dim)
-        k = torch.empty(shape, dtype=dtype, device=dev)
-        v = torch.empty(shape, dtype=dtype, device=dev)
+            dtype = torch.bfloat16 if c.dtype is _FP8 else c.dtype
+        _row_dtype(c, dtype)
+        shape = (int(total_tokens), c.Nk, c.D)
+        k = kv_cache.new_empty(shape, dtype=dtype)
+        v = kv_cache.new_empty(shape, dtype=dtype)
     elif not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
     elif dtype not in (None, k.dtype) or total_tokens not in (None, k.shape[0]):
         raise ValueError("dtype and total_tokens must be those of k")
-    r = _abi.KVRows()
-    r.dtype = _row_dtype(kv_cache, k.dtype)
-    r.k_stride = _rows(k, "k", dev, k.dtype, c.num_heads_kv, c.head_dim)
-    r.v_stride = _rows(v, "v", dev, k.dtype, c.num_heads_kv, c.head_dim)
-    if k.shape != v.shape:
-        raise ValueError("k and v must have one shape")
-    r.k, r.v, r.seq_offsets = k.data_ptr(), v.data_ptr(), seq_offsets.data_ptr()
-    r.total_tokens = k.shape[0]
-    _call("hstu_kv_read", dev, ctypes.byref(c), ctypes.byref(r))
+    _copy("hstu_kv_read", c, k, v, seq_offsets)
     return k, v
 
 
@@ -252,36 +298,26 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
     out = softmax(alpha q k^T) v with q's shape and type; with return_lse also ln sum exp(alpha
     q k) [T, Nq] fp32. A row that sees no key gets 0 (lse -inf); rows of no sequence are left
     as allocated. Other arguments as for hstu_kv_append."""
-    c, keep = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
-                     k_descale, v_descale, status)
-    dev = kv_cache.device
+    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
+               v_descale, status)
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    a = _abi.SoftmaxArgs()
-    a.dtype = _row_dtype(kv_cache, q.dtype)
-    a.q_stride = _rows(q, "q", dev, q.dtype, None, c.head_dim)
-    T, Nq, D = q.shape
-    if Nq % c.num_heads_kv:
-        raise ValueError(f"q's heads ({Nq}) must be a multiple of the cache's ({c.num_heads_kv})")
+    dtype = _row_dtype(c, q.dtype)
+    q_stride = _rows(q, "q", c.device, q.dtype, None, c.D)
+    T, Nq, D = shape = q.shape
+    if Nq % c.Nk:
+        raise ValueError(f"q's heads ({Nq}) must be a multiple of the cache's ({c.Nk})")
     if out is None:
-        out = torch.empty((T, Nq, D), dtype=q.dtype, device=dev)
-        a.out = out.data_ptr()
+        out = q.new_empty(shape)
+        out_ptr = out.data_ptr()
     else:
-        a.out = _tensor(out, "out", dev, q.dtype, q.shape)
-    a.q, a.seq_offsets, a.total_tokens, a.num_heads_q = q.data_ptr(), seq_offsets.data_ptr(), T, Nq
-    a.max_seqlen, a.max_seqlen_k = max_seqlen, max_seqlen_k
-    a.causal, a.alpha = bool(causal), alpha
-    lse = None
-    if return_lse:
-        lse = torch.empty((T, Nq), dtype=torch.float32, device=dev)
-        a.lse = lse.data_ptr()
-    need = ctypes.c_longlong(0)
-    with torch.cuda.device(dev):
-        _abi.check(_abi.lib().hstu_softmax_workspace(ctypes.byref(c), ctypes.byref(a),
-                                                     ctypes.byref(need)),
-                   "hstu_softmax_workspace")
-    if need.value:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), need.value
-    _call("hstu_softmax_fwd", dev, ctypes.byref(c), ctypes.byref(a))
+        out_ptr = _tensor(out, "out", kv_cache.device, q.dtype, shape)
+    lse = q.new_empty((T, Nq), dtype=torch.float32) if return_lse else None
+    sizes = (T, dtype, Nq, int(max_seqlen), int(max_seqlen_k), bool(causal), float(alpha))
+    need = _workspace_bytes(c.device, c.sizes, sizes)
+    workspace = kv_cache.new_empty((need,), dtype=torch.uint8) if need else None
+    _call("hstu_softmax_fwd", c,
+          _PACK_ATTN(q.data_ptr(), q_stride, seq_offsets.data_ptr(), *sizes, out_ptr,
+                     0 if lse is None else lse.data_ptr(),
+                     0 if workspace is None else workspace.data_ptr(), need, 0))
     return (out, lse) if return_lse else out

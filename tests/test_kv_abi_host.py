@@ -44,6 +44,19 @@ def test_ctypes_mirror_matches_header(tmp_path, struct, cls):
         assert c[f] == getattr(cls, f).offset, f
 
 
+def test_packed_structs_have_the_mirrors_layout():
+    """The packs of kv_cache.py against the ctypes mirrors, field by field."""
+    from hstu_dense_forward_gb300 import kv_cache as K
+    for pack, cls in ((K._PACK_CACHE, _abi.KVCache), (K._PACK_ROWS, _abi.KVRows),
+                      (K._PACK_ATTN, _abi.SoftmaxArgs)):
+        names = [f for f, _ in cls._fields_]
+        given = [0.5 if f == "alpha" else i + 1 for i, f in enumerate(names)]
+        raw = pack(*given)
+        assert len(raw) == ctypes.sizeof(cls)
+        s = cls.from_buffer_copy(raw)
+        assert [getattr(s, f) for f in names] == given
+
+
 FAKE = 1 << 20  # never dereferenced: the calls fail validation first
 
 

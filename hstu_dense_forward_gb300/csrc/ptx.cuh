@@ -472,6 +472,19 @@ __device__ __forceinline__ void fma_f32x2(float& d0, float& d1, float a0, float 
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
+__device__ __forceinline__ void add_f32x2(float& d0, float& d1, float a0, float a1) {
+  asm("{.reg .b64 ra, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rd, {%0, %1};\n\t"
+      "add.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+// Largest of three (NaN operands are passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Two fp32 values rounded to E4M3 (saturating to +-448): lo in the low byte.
 __device__ __forceinline__ uint32_t cvt_e4m3x2_f32(float lo, float hi) {
   uint16_t r;

@@ -73,7 +73,7 @@ struct Cfg {
 
 struct Bars {
   uint64_t q_full, kv_full[6], kv_empty[6], st_full[4], st_empty[4];
-  uint64_t s_full[2], p_full[2], pv_done[2], drain;
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;
   uint32_t tmem_base;
   volatile int abort;
 };
@@ -343,15 +343,28 @@ struct Issuer {
     }
     ptx::mma_commit(ptx::smem_u32(&bars->s_full[sb]));
   }
-  // O of query tile q += P (over score buffer sb) V at ring place i
-  __device__ void accumulate(int q, int sb, int i, bool first) {
+  // O of query tile q += P (over score buffer sb) V at ring place i, for one half of the keys:
+  // the first half's product runs while the second half's weights are computed
+  __device__ void accumulate(int q, int sb, int i, int half, bool first) {
     const uint64_t bd0 =
         ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, C::KV_CB, 8 * C::SWB, 2);
 #pragma unroll
-    for (int kk = 0; kk < C::KT / 16; ++kk)
+    for (int x = 0; x < C::KT / 32; ++x) {
+      const int kk = half * (C::KT / 32) + x;
       ptx::mma_ts(tmem + C::O_COL + q * C::D, tmem + sb * C::KT + kk * 8,
                   ptx::desc_add(bd0, kk * 16 * C::SWB), IDESC_O, (!first || kk > 0) ? 1u : 0u);
+    }
+  }
+  // The same for both halves as P (phase `par` of its barriers) and V arrive.
+  __device__ bool weighted_sum(int q, int sb, uint32_t par, int i, bool first) {
+    if (!kv_ready(i) || !wait_bar(p, bars, &bars->p_half[sb], par)) return false;
+    ptx::tc_fence_after();
+    accumulate(q, sb, i, 0, first);
+    if (!wait_bar(p, bars, &bars->p_full[sb], par)) return false;
+    ptx::tc_fence_after();
+    accumulate(q, sb, i, 1, false);
     ptx::mma_commit(ptx::smem_u32(&bars->pv_done[q]));
+    return true;
   }
 };
 
@@ -359,48 +372,29 @@ template <class C, bool BF16>
 __device__ bool mma_loop(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars, const Item& it) {
   if (!wait_bar(p, bars, &bars->q_full, 0)) return false;
   const int n = it.nmax;
-  if constexpr (C::NQT == 1) {
-    for (int t = 0; t < 2 && t < n; ++t) {
-      if (!is.kv_ready(k_index<C>(t))) return false;
-      is.scores(0, t, k_index<C>(t));
-      is.kv_release(k_index<C>(t));
-    }
-    for (int t = 0; t < n; ++t) {
-      const int vi = v_index<C>(t, n);
-      if (!wait_bar(p, bars, &bars->p_full[t & 1], (t >> 1) & 1) || !is.kv_ready(vi)) return false;
-      is.accumulate(0, t & 1, vi, t == 0);
-      is.kv_release(vi);
-      if (t + 2 < n) {  // over P(t), which its product must have read
-        const int ki = k_index<C>(t + 2);
-        if (!wait_bar(p, bars, &bars->pv_done[0], t & 1) || !is.kv_ready(ki)) return false;
-        is.scores(0, t & 1, ki);
-        is.kv_release(ki);
-      }
-    }
-  } else {
-    if (!is.kv_ready(0)) return false;
+  // scores of the first NSB tiles
+  for (int t = 0; t < C::NSB && t < n; ++t) {
+    if (!is.kv_ready(k_index<C>(t))) return false;
     for (int q = 0; q < it.nq; ++q)
-      if (it.n[q] > 0) is.scores(q, q, 0);
-    is.kv_release(0);
-    for (int t = 0; t < n; ++t) {
-      const int vi = v_index<C>(t, n), ki = k_index<C>(t + 1);
-      bool have_k = false;
-      if (!is.kv_ready(vi)) return false;
-      for (int q = 0; q < it.nq; ++q) {
-        if (t >= it.n[q]) continue;
-        if (!wait_bar(p, bars, &bars->p_full[q], t & 1)) return false;
-        ptx::tc_fence_after();
-        is.accumulate(q, q, vi, t == 0);
-        if (t + 1 < it.n[q]) {  // over P(t), which its product must have read
-          if (!have_k && !is.kv_ready(ki)) return false;
-          have_k = true;
-          if (!wait_bar(p, bars, &bars->pv_done[q], t & 1)) return false;
-          is.scores(q, q, ki);
-        }
+      if (t < it.n[q]) is.scores(q, C::NQT == 1 ? t : q, k_index<C>(t));
+    is.kv_release(k_index<C>(t));
+  }
+  // Then per tile and query tile: O += P(t) V, and the scores of tile t + NSB over P(t), which
+  // that product must have read. With two query tiles the softmax of one runs meanwhile.
+  for (int t = 0; t < n; ++t) {
+    const int vi = v_index<C>(t, n), ki = k_index<C>(t + C::NSB);
+#pragma unroll
+    for (int q = 0; q < C::NQT; ++q) {
+      if (t >= it.n[q]) continue;
+      const int sb = C::NQT == 1 ? t & 1 : q;
+      if (!is.weighted_sum(q, sb, C::NQT == 1 ? (t >> 1) & 1 : t & 1, vi, t == 0)) return false;
+      if (t + C::NSB < it.n[q]) {
+        if (!is.kv_ready(ki) || !wait_bar(p, bars, &bars->pv_done[q], t & 1)) return false;
+        is.scores(q, sb, ki);
       }
-      is.kv_release(vi);
-      if (t + 1 < n) is.kv_release(ki);
     }
+    is.kv_release(vi);
+    if (t + C::NSB < n) is.kv_release(ki);
   }
   return true;
 }
@@ -447,8 +441,9 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
     ptx::tc_fence_after();
     const uint32_t s_col = tmem + lane_off + sb * KT;
+    uint32_t sv[KT / 32][32];
+    float neg = 0.0f;
     if (any) {
-      uint32_t sv[KT / 32][32];
 #pragma unroll
       for (int c = 0; c < KT / 32; ++c) ptx::tmem_ld32_issue(s_col + c * 32, sv[c]);
       ptx::tmem_ld_wait(sv[0]);
@@ -463,20 +458,21 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             if (c * 32 + e >= left) sv[c][e] = 0xff800000u;  // -inf
       }
       float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-      if (fk >= 0.0f) {
-#pragma unroll
-        for (int c = 0; c < KT / 32; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(sv[c][e]));
-      } else {  // a negative static factor: the scores change sign (and masked ones keep theirs)
+      if (fk < 0.0f) {  // a negative static factor: the largest score has the smallest product
 #pragma unroll
         for (int c = 0; c < KT / 32; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            if (c * 32 + e >= left) sv[c][e] = 0x7f800000u;
-            top[e & 3] = fmaxf(top[e & 3], -__uint_as_float(sv[c][e]));
+            if (c * 32 + e >= left) sv[c][e] = 0x7f800000u;  // (masked scores stay -inf)
+            sv[c][e] ^= 0x80000000u;
           }
       }
+#pragma unroll
+      for (int c = 0; c < KT / 32; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          top[(e >> 1) & 3] = ptx::max3(top[(e >> 1) & 3], __uint_as_float(sv[c][e]),
+                                        __uint_as_float(sv[c][e + 1]));
       const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(fk);
       // raise the reference: at the first visible key, and when weights would pass 2^kLazy
       const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
@@ -499,25 +495,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
           }
         }
       }
-      const float neg = m == -CUDART_INF_F ? 0.0f : -m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < KT / 32; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float x0, x1;
-          ptx::fma_f32x2(x0, x1, __uint_as_float(sv[c][2 * e]), __uint_as_float(sv[c][2 * e + 1]),
-                         fk, fk, neg, neg);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          sum[(2 * e) & 3] += p0;
-          sum[(2 * e + 1) & 3] += p1;
-          pk[e] = pack2<BF16>(p0, p1);
-        }
-        ptx::tmem_st16(s_col + c * 16, pk);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      ptx::tmem_st_wait();
+      neg = m == -CUDART_INF_F ? 0.0f : -m;
     }
     if constexpr (!C::E4M3) {
       // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
@@ -534,6 +512,34 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         ptx::fence_proxy_async_smem();
       }
     }
+    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const float fa = fabsf(fk);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (any) {
+#pragma unroll
+        for (int x = 0; x < KT / 64; ++x) {
+          const int c = half * (KT / 64) + x;
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            ptx::fma_f32x2(x0, x1, __uint_as_float(sv[c][2 * e]),
+                           __uint_as_float(sv[c][2 * e + 1]), fa, fa, neg, neg);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            ptx::add_f32x2(sum[e & 1][0], sum[e & 1][1], p0, p1);
+            pk[e] = pack2<BF16>(p0, p1);
+          }
+          ptx::tmem_st16(s_col + c * 16, pk);
+        }
+        ptx::tmem_st_wait();
+      }
+      if (half == 0) {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
+      }
+    }
+    l += (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
     // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
     // below needs PV(n - 2) to be done; S(n - 1) was issued after PV(n - 1 - NSB) only, and
     // once P(n - 1) is handed over both may complete at any time.
@@ -609,6 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->s_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->p_half[s]), 128);
       ptx::mbar_init(ptx::smem_u32(&bars->p_full[s]), 128);
       ptx::mbar_init(ptx::smem_u32(&bars->pv_done[s]), 1);
     }
@@ -625,16 +632,22 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // 512 threads launch with 128 registers each (65,536): the softmax keeps a row of scores in
-  // registers and takes 176, the conversion 96 and the control warps 64, 65,536 again.
-  constexpr bool SPLIT = C::THREADS == 512;
-  if constexpr (SPLIT) {
+  // The softmax keeps a row of scores in registers: with two warpgroups of it the launch's
+  // registers are dealt out anew. 512 threads launch with 128 each (65,536): 176 for the
+  // softmax, 96 for the conversion and 64 for the control warps are 65,536 again; 384 launch
+  // with 168 (64,512): 208 and 72 are 62,464.
+  if constexpr (C::THREADS == 512) {
     if (warp < C::SM_WARPS)
       ptx::regs_inc<176>();
     else if (warp < C::CONV_WARP)
       ptx::regs_dec<64>();
     else
       ptx::regs_dec<96>();
+  } else if constexpr (C::NQT == 2) {
+    if (warp < C::SM_WARPS)
+      ptx::regs_inc<208>();
+    else
+      ptx::regs_dec<72>();
   }
   if (warp < C::SM_WARPS) {
     if (warp / 4 < it.nq) softmax_role<C, BF16>(p, bars, smem, tmem, it, warp / 4, warp, lane);

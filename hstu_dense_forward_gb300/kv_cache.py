@@ -272,8 +272,8 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
             dtype = torch.bfloat16 if c.dtype is _FP8 else c.dtype
         _row_dtype(c, dtype)
         shape = (int(total_tokens), c.Nk, c.D)
-        k = kv_cache.new_empty(shape, dtype=dtype)
-        v = kv_cache.new_empty(shape, dtype=dtype)
+        k = torch.empty(shape, dtype=dtype, device=kv_cache.device)
+        v = torch.empty(shape, dtype=dtype, device=kv_cache.device)
     elif not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
     elif dtype not in (None, k.dtype) or total_tokens not in (None, k.shape[0]):
@@ -308,14 +308,14 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
     if Nq % c.Nk:
         raise ValueError(f"q's heads ({Nq}) must be a multiple of the cache's ({c.Nk})")
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
         out_ptr = out.data_ptr()
     else:
         out_ptr = _tensor(out, "out", kv_cache.device, q.dtype, shape)
-    lse = q.new_empty((T, Nq), dtype=torch.float32) if return_lse else None
+    lse = torch.empty((T, Nq), dtype=torch.float32, device=q.device) if return_lse else None
     sizes = (T, dtype, Nq, int(max_seqlen), int(max_seqlen_k), bool(causal), float(alpha))
     need = _workspace_bytes(c.device, c.sizes, sizes)
-    workspace = kv_cache.new_empty((need,), dtype=torch.uint8) if need else None
+    workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
     _call("hstu_softmax_fwd", c,
           _PACK_ATTN(q.data_ptr(), q_stride, seq_offsets.data_ptr(), *sizes, out_ptr,
                      0 if lse is None else lse.data_ptr(),

@@ -51,7 +51,7 @@ struct Cfg {
   static constexpr int NCB = D / EPC;             // column blocks of a row
   static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
   static constexpr int KV_CB = KT * SWB, KV_TILE = NCB * KV_CB;
-  static constexpr int ST_TILE = KT * D;          // staged E4M3 tile
+  static constexpr int ST_TILE = KT * D;          // staged E4M3 tile; its row scales (KT bytes)
   // ring depths: what 227 KB of shared memory holds next to Q
   static constexpr int NSLOT = !E4M3 ? (D == 64 ? 6 : (NQT == 1 && D == 128 ? 6 : 4))
                                      : (D == 64 ? 4 : (NQT == 1 && D == 128 ? 4 : 3));
@@ -64,7 +64,8 @@ struct Cfg {
   static constexpr uint32_t O_COL = NQT * NSB * KT;
   static_assert(O_COL + NQT * D <= kTmemCols, "TMEM");
   static constexpr int OFF_Q = 0, OFF_KV = NQT * Q_TILE, OFF_ST = OFF_KV + NSLOT * KV_TILE;
-  static constexpr int OFF_BAR = OFF_ST + NST * ST_TILE;
+  static constexpr int OFF_SC = OFF_ST + NST * ST_TILE;  // row scales of the staged tiles
+  static constexpr int OFF_BAR = OFF_SC + NST * 128;
   static constexpr int USED = OFF_BAR + 2048 + 1024;  // (1024: alignment of the base)
   // one CTA per SM: it takes all of TMEM
   static constexpr int SMEM = USED < 120 * 1024 ? 120 * 1024 : USED;
@@ -235,7 +236,8 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
     const int slot = i % DEPTH;
     if (!wait_bar(p, bars, &empty[slot], ((i / DEPTH) & 1) ^ 1)) return;
     const uint32_t bar = ptx::smem_u32(&full[slot]);
-    ptx::mbar_arrive_expect_tx(bar, C::E4M3 ? C::ST_TILE : C::KV_TILE);
+    const bool scales = C::E4M3 && p.c.scale;
+    ptx::mbar_arrive_expect_tx(bar, C::E4M3 ? C::ST_TILE + (scales ? C::KT : 0) : C::KV_TILE);
     const int row0 = ps >= C::KT ? (int)(n0 & (ps - 1)) : 0;
 #pragma unroll
     for (int m = 0; m < C::KT / 32; ++m) {
@@ -244,6 +246,10 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
       if constexpr (C::E4M3) {
         ptx::tma_load_4d(sbase + C::OFF_ST + slot * C::ST_TILE + m * 32 * C::D, tc, bar, 0, it.hk,
                          row0, plane);
+        if (scales)
+          ptx::bulk_load(sbase + C::OFF_SC + slot * 128 + m * 32,
+                         p.c.scale + scale_row(p.c, page[m], v ? 1 : 0, row0, it.hk),
+                         boxes == 1 ? C::KT : 32, bar);
       } else {
 #pragma unroll
         for (int cb = 0; cb < C::NCB; ++cb)
@@ -260,34 +266,24 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
 template <class C, bool BF16>
 __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const Item& it,
                              int warp, int lane) {
-  constexpr int CPR = C::D / 16;         // chunks of a row
-  constexpr int RPW = 32 / CPR;          // rows of one pass of a warp; four warps: STEP rows
-  constexpr int STEP = 4 * RPW, PASSES = C::KT / STEP;
-  static_assert(RPW * PASSES <= 32, "one row scale a lane");
-  const int chunk = lane % CPR, r0 = warp * RPW + lane / CPR;
+  constexpr int CPR = C::D / 16;  // chunks of a row
+  constexpr int STEP = 128 / CPR, PASSES = C::KT / STEP;  // rows of one pass of the four warps
+  const int chunk = lane % CPR, r0 = warp * (32 / CPR) + lane / CPR;
   const int cb = chunk / 4, c16 = (chunk % 4) * 2;  // column block, first 16-byte piece in it
-  const int my_row = warp * RPW + lane % RPW + STEP * (lane / RPW);  // whose scale it loads
   for (int i = 0; i < 2 * it.nmax; ++i) {
     int t;
-    const bool v = ring_tile<C>(i, it.nmax, t);
-    const long long n0 = it.k0 + (long long)t * C::KT;
-    const int have = (int)min((long long)C::KT, it.s.Lk - n0);
-    float my_scale = 1.0f;  // loaded before the waits, which hide its latency
-    if (p.c.scale && my_row < have) {
-      const long long page = page_at(p.c, it.s, n0 + my_row);
-      if (page >= 0)
-        my_scale = scale_value(p.c.scale[scale_row(p.c, page, v ? 1 : 0,
-                                                   (n0 + my_row) & (page_size(p.c) - 1), it.hk)]);
-    }
+    ring_tile<C>(i, it.nmax, t);
+    const int have = (int)min((long long)C::KT, it.s.Lk - it.k0 - (long long)t * C::KT);
     const int st = i % C::NST, slot = i % C::NSLOT;
     if (!warp_wait(p, bars, &bars->st_full[st], (i / C::NST) & 1)) return;
     if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
+    const uint8_t* scale = smem + C::OFF_SC + st * 128;
     const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
     uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
 #pragma unroll 4
     for (int k = 0; k < PASSES; ++k) {
       const int r = r0 + STEP * k;
-      const float f = __shfl_sync(0xffffffffu, my_scale, lane / CPR + RPW * k);
+      const float f = p.c.scale ? scale_value(scale[r]) : 1.0f;
       uint32_t w[8];
       if (r < have) {
         const uint4 u = *reinterpret_cast<const uint4*>(src + r * C::D);

@@ -39,9 +39,12 @@ int softmax_tc_key_tile(int D);  // keys of one tile
 cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles,
                               long long tiles, long long blocks, cudaStream_t stream);
 
-// Attention of few rows (bf16, fp16): 16 packed rows of one kv head per cluster of CTAs.
-cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, long long tiles,
-                                long long blocks, int cluster, cudaStream_t stream);
+// Attention of few rows (bf16, fp16): `rows` (8 or 16) packed rows of one kv head per cluster
+// of CTAs; CTAs of it that an SM holds.
+int softmax_rows_ctas(int D, bool e4m3, int rows);
+cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, int rows,
+                                long long tiles, long long blocks, int cluster,
+                                cudaStream_t stream);
 
 // Joins the key ranges of sequences that have more than one.
 cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream);

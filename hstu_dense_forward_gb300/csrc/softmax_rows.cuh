@@ -1,17 +1,19 @@
 // bf16 / fp16 softmax attention of few query rows (single tokens) over the paged KV cache:
 // bound by reading the cache once.
 //
-// One CTA takes up to sixteen packed query rows (row r of a sequence is query token r / G and
-// head hk * G + r % G) of one kv head and a stretch of its keys, in tiles of 64 keys that one
-// warp loads by TMA into a ring; each of the other warps takes sixteen keys of every tile and
-// keeps its own running maximum m, sum l and output O (registers) over them:
-//   S = Q K^T, O += P V   with mma.sync m16n8k16: the sixteen rows are the M side, so that a
-// single token of a GQA group fills it; tcgen05's smallest M of 64 would waste the products of
-// 48 rows and more, and its operands' way through TMEM costs latency that so few rows cannot
-// hide. K and V go from shared memory to the fragments without ldmatrix: both products are
-// sums over, or independent in, the head dim, so the head dim may be permuted as long as Q and
-// O follow. A lane reads whole 16-byte pieces of a key's row for the scores, and the same piece
-// of four keys for the output, which byte permutes turn into pairs of keys.
+// One CTA takes 8 or 16 packed query rows (row r of a sequence is query token r / G and head
+// hk * G + r % G) of one kv head and a stretch of its keys, in tiles of 64 keys that one warp
+// loads by TMA into a ring; each of the other warps takes sixteen keys of every tile and keeps
+// its own running maximum m, sum l and output O (registers) over them. Both products are
+// transposed, so that keys and head dim are the M side and the few query rows the N side, of
+// which mma.sync m16n8k16 has as few as eight:
+//   S^T = K Q^T,   O^T += V^T P^T.
+// tcgen05's smallest M of 64 (rows) would waste most of its products, and its operands' way
+// through TMEM costs latency that so few rows cannot hide. K and V go from shared memory to the
+// fragments without ldmatrix: the scores are sums over the head dim, and the output's columns
+// are independent of each other, so the head dim may be permuted as long as Q and O follow. A
+// lane reads whole 16-byte pieces of a key's row for the scores, and the same piece of four
+// keys for the output, which byte permutes turn into pairs of keys.
 //
 // E4M3 caches: codes become fp16 by one conversion (exact) and the products run in fp16. A
 // row scale 2^e of K multiplies the score. One of V would leave fp16's range if it multiplied a
@@ -41,37 +43,36 @@ namespace hstu {
 namespace rows {
 
 constexpr int KT = 64;     // keys of one tile
-constexpr int RT = 16;     // packed query rows of one CTA
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int D_, bool BF16_, bool E4M3_>
+template <int D_, int NT_, bool BF16_, bool E4M3_>
 struct Cfg {
-  static constexpr int D = D_;
+  static constexpr int D = D_, NT = NT_, RT = 8 * NT;      // packed query rows of one CTA
   static constexpr bool BF16 = BF16_, E4M3 = E4M3_;
   static constexpr bool MMA_BF16 = BF16 && !E4M3;
   static constexpr int EB = E4M3 ? 1 : 2;
   static constexpr int SWB = D * EB < 128 ? D * EB : 128;  // bytes of one swizzled row block
   static constexpr int NCB = D * EB / SWB;                 // blocks of a key's row
+  static constexpr int BE = SWB / EB;                      // elements of a block
   static constexpr int CB = KT * SWB;                      // one block of a tile
-  static constexpr int CPB = SWB / 16;                     // 16-byte pieces of a block's row
-  static constexpr int LPC = CPB / 4;                      // pieces per lane (scores)
-  static constexpr int NV = SWB / EB / 8;                  // output columns per lane and block
-  // D = 256: two warps share sixteen keys and take half of the output columns each
-  static constexpr int HALVES = D == 256 ? 2 : 1;
-  static constexpr int OB = NCB / HALVES;                  // output blocks of one warp
-  static constexpr int KW = KT / 16;                       // groups of sixteen keys
-  static constexpr int CW = KW * HALVES, THREADS = (CW + 1) * 32;
+  static constexpr int EPP = 16 / EB;                      // elements of a 16-byte piece
+  static constexpr int LPC = SWB / 64;                     // pieces per lane and block (scores)
+  static constexpr int KS = D / 16;                        // k-steps of the scores
+  static constexpr int NV = BE / 8;                        // output columns per lane and block
+  static constexpr int CW = KT / 16, THREADS = (CW + 1) * 32;
   static constexpr int PLANE = KT * D * EB, STAGE = 2 * PLANE;
-  static constexpr int MIN_CTAS = D == 256 ? 1 : 2;  // CTAs per SM
-  // ring depth: 96 KB a CTA, two CTAs per SM (D = 256: 192 KB, one)
-  static constexpr int NST = (MIN_CTAS == 1 ? 196608 : 98304) / STAGE;
+  // CTAs per SM: what their registers (O and Q) and a ring of at least three stages leave. E4M3
+  // spends more instructions per byte and needs the warps of a third CTA.
+  static constexpr int CTAS = D == 256 ? (E4M3 && NT == 1 ? 2 : 1) : (E4M3 && NT == 1 ? 3 : 2);
+  static constexpr int NST = (CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : 65536) / STAGE;
   static constexpr int OFF_SC = NST * STAGE;               // row scales: 2 KT bytes a stage
   static constexpr int OFF_ML = OFF_SC + (E4M3 ? NST * 2 * KT : 0);
-  static constexpr int OFF_BAR = OFF_ML + (2 * KW + 2) * RT * 4;
+  static constexpr int OFF_BAR = OFF_ML + (2 * CW + 2) * RT * 4;
   static constexpr int USED = OFF_BAR + 256 + 1024;
-  static_assert(KW * RT * D * 4 <= NST * STAGE, "the joined outputs reuse the ring");
-  static_assert(USED <= 232448 / MIN_CTAS - 1024, "shared memory");
+  static_assert(NST >= 3 && NST <= 12, "ring");
+  static_assert(CW * RT * D * 4 <= NST * STAGE, "the joined outputs reuse the ring");
+  static_assert(USED <= 232448 / CTAS - 1024, "shared memory");
 };
 
 struct Bars {
@@ -117,20 +118,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // d += a b, m16n8k16.
 template <bool BF16>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements, two of a row per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Byte offset of 16-byte piece `piece` of row r inside a block with SWB-byte swizzled rows.
@@ -147,6 +155,7 @@ struct Item {
   long long k0, kend;   // keys of this CTA
 };
 
+template <int RT>
 __device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, int cluster,
                                           Item& it) {
   const long long blk = blockIdx.x / cluster;
@@ -223,16 +232,17 @@ __device__ __forceinline__ float part_weight(float m, float top) {
   return m == -CUDART_INF_F ? 0.0f : ex2(m - top);
 }
 
-template <int D, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3>::MIN_CTAS)
+template <int D, int NT, bool BF16, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF16, E4M3>::CTAS)
     softmax_rows_kernel(const __grid_constant__ CUtensorMap tm_c, const SoftmaxParams p, int tiles,
                         int cluster) {
-  using C = Cfg<D, BF16, E4M3>;
+  using C = Cfg<D, NT, BF16, E4M3>;
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   namespace cg = cooperative_groups;
+  constexpr int RT = C::RT;
   extern __shared__ uint8_t smem_raw[];
   Item it;
-  if (!make_item(p, tiles, cluster, it)) return;  // (the whole cluster)
+  if (!make_item<RT>(p, tiles, cluster, it)) return;  // (the whole cluster)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
@@ -249,31 +259,36 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
   }
   __syncthreads();
 
+  // Lane (g, c) of a warp holds, of S^T, keys g and g + 8 against rows 2c and 2c + 1 of each
+  // row tile; of O^T, columns NV g .. NV g + NV - 1 of every block against the same rows.
   const int g = lane >> 2, c = lane & 3;
-  const int kg = warp % C::KW, half = warp / C::KW;  // keys and output half of a warp
-  float o[C::OB * C::NV][4];
-  float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+  float o[NT][C::KS][4];  // [..][x]: columns 2x (elements 0, 1) and 2x + 1 of the lane's
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    m[i][0] = m[i][1] = -CUDART_INF_F;
+    l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+    for (int x = 0; x < C::KS; ++x) o[i][x][0] = o[i][x][1] = o[i][x][2] = o[i][x][3] = 0.f;
+  }
   if (warp == C::CW) {
     if (lane == 0) load_role<C>(p, bars, smem, it, n, &tm_c);
   } else {
-    // Q fragments in the scores' order of the head dim: piece j of block cb holds, for lane
-    // c, elements e0 .. of which each k-step takes four (two registers per row)
-    constexpr int EPP = 16 / C::EB;  // elements of one piece
-    uint32_t qa[C::NCB * C::LPC * EPP / 4][4];
-    float fr[2];        // score factor of rows g and g + 8
-    long long lim[2];   // keys that they see, counted from this CTA's first
     float fk = p.scale_log2;
     if (E4M3 && p.c.k_ds)
       fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
-    long long see = it.kend - it.k0;  // fewest of them
+    const int keys = (int)(it.kend - it.k0);
+    // Q fragments in the scores' order of the head dim: of piece j of block cb, lane c's
+    // elements in fours, two registers each (rows g)
+    uint32_t qb[NT][C::KS][2];
+    float fr[NT][2];  // score factor of rows 2c and 2c + 1
+    int lim[NT][2];   // keys that they see, counted from this CTA's first (maybe < 0)
+    int see = keys;   // fewest of them
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const long long pr = it.m0 + g + 8 * h;
+    for (int i = 0; i < NT; ++i) {
+      const long long pr = it.m0 + 8 * i + g;
       const bool real = pr < it.rows;
       const long long tok = real ? pr / p.G : 0;
-      lim[h] = it.kend - it.k0;
-      if (p.causal && real) lim[h] = min(lim[h], it.s.Lk - it.s.n + tok + 1 - it.k0);
-      see = min(see, lim[h]);
       const T16* q = static_cast<const T16*>(p.q) + (it.s.t0 + tok) * p.q_stride +
                      (it.hk * p.G + (real ? pr % p.G : 0)) * (long long)p.c.D;
       uint32_t top = 0;  // largest magnitude of the row, as 16-bit patterns
@@ -281,16 +296,16 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
       for (int cb = 0; cb < C::NCB; ++cb)
 #pragma unroll
         for (int j = 0; j < C::LPC; ++j) {
-          const int e0 = cb * (C::SWB / C::EB) + (c * C::LPC + j) * EPP;
+          const int e0 = cb * C::BE + (c * C::LPC + j) * C::EPP;
 #pragma unroll
-          for (int x = 0; x < EPP / 8; ++x) {
+          for (int x = 0; x < C::EPP / 8; ++x) {
             uint4 u = make_uint4(0u, 0u, 0u, 0u);
             if (real && e0 + 8 * x < p.c.D) u = *reinterpret_cast<const uint4*>(q + e0 + 8 * x);
-            const int k = ((cb * C::LPC + j) * EPP + 8 * x) / 4;
-            qa[k][h] = u.x;
-            qa[k][2 + h] = u.y;
-            qa[k + 1][h] = u.z;
-            qa[k + 1][2 + h] = u.w;
+            const int k = ((cb * C::LPC + j) * C::EPP + 8 * x) / 4;
+            qb[i][k][0] = u.x;
+            qb[i][k][1] = u.y;
+            qb[i][k + 1][0] = u.z;
+            qb[i][k + 1][1] = u.w;
             if constexpr (E4M3 && BF16) {
               const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -299,144 +314,161 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
             }
           }
         }
-      fr[h] = fk;
+      float f = fk;
       if constexpr (E4M3 && BF16) {  // the row as fp16, times 2^(14 - exponent of its largest)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int sh = min(14 - ((int)(top >> 7) - 127), 126);
         const float mul = __uint_as_float((uint32_t)(sh + 127) << 23);
-        fr[h] = fk * __uint_as_float((uint32_t)(127 - sh) << 23);
+        f = fk * __uint_as_float((uint32_t)(127 - sh) << 23);
 #pragma unroll
-        for (int k = 0; k < C::NCB * C::LPC * EPP / 4; ++k)
+        for (int k = 0; k < C::KS; ++k)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t w = qa[k][2 * x + h];
-            qa[k][2 * x + h] = pack2<false>(__uint_as_float(w << 16) * mul,
-                                            __uint_as_float(w & 0xffff0000u) * mul);
+            const uint32_t w = qb[i][k][x];
+            qb[i][k][x] = pack2<false>(__uint_as_float(w << 16) * mul,
+                                       __uint_as_float(w & 0xffff0000u) * mul);
           }
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        fr[i][y] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + y));
+        const long long row = it.m0 + 8 * i + 2 * c + y;
+        lim[i][y] = keys;
+        if (p.causal && row < it.rows)
+          lim[i][y] = (int)min((long long)keys, it.s.Lk - it.s.n + row / p.G + 1 - it.k0);
+        see = min(see, lim[i][y]);
       }
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) see = min(see, __shfl_xor_sync(0xffffffffu, see, d));
-#pragma unroll
-    for (int i = 0; i < C::OB * C::NV; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
     for (int t = 0; t < n; ++t) {
       const int st = t % C::NST;
       if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], (t / C::NST) & 1))) break;
-      const long long at = (long long)t * KT + kg * 16;  // first of the warp's keys
-      const long long left = it.kend - it.k0 - at;       // of them, keys of this CTA
+      const int at = t * KT + warp * 16;  // first of the warp's keys
+      const int left = keys - at;         // of them, keys of this CTA
       if (left > 0) {
         const uint8_t* kt = smem + st * C::STAGE;
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        // two sums per score, of alternate k-steps: a product's latency is some 35 cycles, and
+        // each waits for the one before it in its sum
+        float sc[NT][4], sd[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[i][e] = sd[i][e] = 0.f;
 #pragma unroll
         for (int cb = 0; cb < C::NCB; ++cb)
 #pragma unroll
           for (int j = 0; j < C::LPC; ++j) {
+            const uint4 u0 = *reinterpret_cast<const uint4*>(
+                kt + cb * C::CB + piece_at<C::SWB>(warp * 16 + g, c * C::LPC + j));
+            const uint4 u1 = *reinterpret_cast<const uint4*>(
+                kt + cb * C::CB + piece_at<C::SWB>(warp * 16 + 8 + g, c * C::LPC + j));
+            const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+            const int k = (cb * C::LPC + j) * C::EPP / 4;
+            if constexpr (E4M3) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // keys g and g + 8
-              const uint4 u = *reinterpret_cast<const uint4*>(
-                  kt + cb * C::CB + piece_at<C::SWB>(kg * 16 + 8 * x + g, c * C::LPC + j));
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-              const int k = (cb * C::LPC + j) * EPP / 4;
-              if constexpr (E4M3) {
+              for (int e = 0; e < 4; ++e) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x2(w0[e], a0, a2);
+                e4m3x4_to_f16x2(w1[e], a1, a3);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  mma<false>(sc[x], qa[k + e], e4m3x2_to_f16x2(w[e]),
-                             e4m3x2_to_f16x2(w[e] >> 16));
-              } else {
-                mma<C::MMA_BF16>(sc[x], qa[k], w[0], w[1]);
-                mma<C::MMA_BF16>(sc[x], qa[k + 1], w[2], w[3]);
+                for (int i = 0; i < NT; ++i)
+                  mma<false>(e & 1 ? sd[i] : sc[i], a0, a1, a2, a3, qb[i][k + e][0],
+                             qb[i][k + e][1]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                mma<C::MMA_BF16>(sc[i], w0[0], w1[0], w0[1], w1[1], qb[i][k][0], qb[i][k][1]);
+                mma<C::MMA_BF16>(sd[i], w0[2], w1[2], w0[3], w1[3], qb[i][k + 1][0],
+                                 qb[i][k + 1][1]);
               }
             }
           }
-        // u = x + exponent of V's row scale; key 8 x + 2 c + e of the warp's is sc[x][e]
-        // (row g) and sc[x][2 + e] (row g + 8)
-        float ve[2][2];  // 2^-e of V's row scales
-        if constexpr (E4M3) {
-          if (p.c.scale) {
-            const uint8_t* sp = smem + C::OFF_SC + st * 2 * KT + kg * 16 + 2 * c;
+        // u = x + exponent of V's row scale; sc[i][2 x + y]: key g + 8 x, row 2 c + y
+        float ve[2] = {1.0f, 1.0f};  // 2^-e of V's row scales
+        if (E4M3 && p.c.scale) {
+          const uint8_t* sp = smem + C::OFF_SC + st * 2 * KT + warp * 16 + g;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t ks = *reinterpret_cast<const uint16_t*>(sp + 8 * x);
-              const uint32_t vs = *reinterpret_cast<const uint16_t*>(sp + KT + 8 * x);
+          for (int x = 0; x < 2; ++x) {
+            const float f = scale_value(sp[8 * x]);
+            const int ev = (int)sp[KT + 8 * x] - 127;
+            ve[x] = __uint_as_float((uint32_t)(127 - ev) << 23);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float f = scale_value((ks >> (8 * e)) & 0xffu);
-                const int ev = (int)((vs >> (8 * e)) & 0xffu) - 127;
-                ve[x][e] = __uint_as_float((uint32_t)(127 - ev) << 23);
-                sc[x][e] = fmaf(sc[x][e] * f, fr[0], (float)ev);
-                sc[x][2 + e] = fmaf(sc[x][2 + e] * f, fr[1], (float)ev);
-              }
-            }
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                sc[i][2 * x + y] = fmaf((sc[i][2 * x + y] + sd[i][2 * x + y]) * f, fr[i][y],
+                                        (float)ev);
           }
-        }
-        if (!E4M3 || !p.c.scale) {
+        } else {
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              ve[x][e] = 1.0f;
-              sc[x][e] *= fr[0];
-              sc[x][2 + e] *= fr[1];
-            }
+            for (int e = 0; e < 4; ++e) sc[i][e] = (sc[i][e] + sd[i][e]) * fr[i][e & 1];
         }
         if (at + 16 > see) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 2; ++x) {
+            const int j = at + 8 * x + g;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const long long j = at + 8 * x + 2 * c + e;
-              if (j >= lim[0]) sc[x][e] = -CUDART_INF_F;
-              if (j >= lim[1]) sc[x][2 + e] = -CUDART_INF_F;
-              if (j >= it.kend - it.k0) ve[x][e] = 0.0f;  // (an unused scale may be anything)
-            }
-        }
-        float mx[2];
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+              for (int y = 0; y < 2; ++y)
+                if (j >= lim[i][y]) sc[i][2 * x + y] = -CUDART_INF_F;
+            if (j >= keys) ve[x] = 0.0f;  // (an unused scale may be anything)
+          }
         }
         // the reference follows the maximum when that lies more than kLazy above it
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
-          float corr[2];
+        bool over = false;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool up = mx[h] > m[h] + kLazy;
-            corr[h] = up ? ex2(m[h] - mx[h]) : 1.0f;  // (0 at the first visible key)
-            if (up) m[h] = mx[h];
-            l[h] *= corr[h];
-          }
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int i = 0; i < C::OB * C::NV; ++i) {
-            o[i][0] *= corr[0];
-            o[i][1] *= corr[0];
-            o[i][2] *= corr[1];
-            o[i][3] *= corr[1];
+          for (int e = 0; e < 4; ++e) over |= sc[i][e] > m[i][e & 1] + kLazy;
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            float corr[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float mx = fmaxf(sc[i][y], sc[i][2 + y]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              const bool up = mx > m[i][y] + kLazy;
+              corr[y] = up ? ex2(m[i][y] - mx) : 1.0f;  // (0 at the first visible key)
+              if (up) m[i][y] = mx;
+              l[i][y] *= corr[y];
+            }
+#pragma unroll
+            for (int x = 0; x < C::KS; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][x][e] *= corr[e & 1];
           }
         }
-        uint32_t pa[4];
+        uint32_t pb[NT][2];  // P^T fragments: keys 2c, 2c + 1 (and + 8) of row g
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int i = 0; i < NT; ++i) {
+          const float b0 = m[i][0] == -CUDART_INF_F ? 0.0f : m[i][0];
+          const float b1 = m[i][1] == -CUDART_INF_F ? 0.0f : m[i][1];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float base = m[h] == -CUDART_INF_F ? 0.0f : m[h];
-            const float p0 = ex2(sc[x][2 * h] - base), p1 = ex2(sc[x][2 * h + 1] - base);
-            l[h] = fmaf(p0, ve[x][0], l[h]);
-            l[h] = fmaf(p1, ve[x][1], l[h]);
-            pa[2 * x + h] = pack2<C::MMA_BF16>(p0, p1);
+          for (int x = 0; x < 2; ++x) {
+            const float p0 = ex2(sc[i][2 * x] - b0), p1 = ex2(sc[i][2 * x + 1] - b1);
+            l[i][0] = fmaf(p0, ve[x], l[i][0]);
+            l[i][1] = fmaf(p1, ve[x], l[i][1]);
+            pb[i][x] = transpose8(pack2<C::MMA_BF16>(p0, p1));
           }
+        }
         const uint8_t* vt = kt + C::PLANE;
 #pragma unroll
-        for (int ob = 0; ob < C::OB; ++ob) {
-          const uint8_t* blk = vt + (half * C::OB + ob) * C::CB;
+        for (int cb = 0; cb < C::NCB; ++cb) {
+          const uint8_t* blk = vt + cb * C::CB;
           constexpr int NW = C::NV * C::EB / 4;  // words of a lane's piece: 4, or 2 (64 codes a row)
           uint32_t v[4][NW];                     // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int key = 2 * c + (y & 1) + 8 * (y >> 1), r = kg * 16 + key;
+            const int key = 2 * c + (y & 1) + 8 * (y >> 1), r = warp * 16 + key;
             if constexpr (NW == 4) {
               const uint4 u = *reinterpret_cast<const uint4*>(blk + piece_at<C::SWB>(r, g));
               v[y][0] = u.x;
@@ -449,29 +481,35 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
               v[y][0] = u.x;
               v[y][1] = u.y;
             }
-            if (left < 16 && key >= left) {  // beyond the keys: a page's unused rows, maybe NaN
+          }
+          if (left < 16) {  // beyond the keys: a page's unused rows, maybe NaN
 #pragma unroll
-              for (int w = 0; w < NW; ++w) v[y][w] = 0u;
-            }
+            for (int y = 0; y < 4; ++y)
+              if (2 * c + (y & 1) + 8 * (y >> 1) >= left) {
+#pragma unroll
+                for (int w = 0; w < NW; ++w) v[y][w] = 0u;
+              }
           }
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
             if constexpr (E4M3) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t b0 = __byte_perm(v[0][w], v[1][w], e ? 0x7362 : 0x5140);
-                const uint32_t b1 = __byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140);
-                float(&lo)[4] = o[ob * C::NV + 4 * w + 2 * e];
-                float(&hi)[4] = o[ob * C::NV + 4 * w + 2 * e + 1];
-                mma<false>(lo, pa, e4m3x2_to_f16x2(b0), e4m3x2_to_f16x2(b1));
-                mma<false>(hi, pa, e4m3x2_to_f16x2(b0 >> 16), e4m3x2_to_f16x2(b1 >> 16));
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x2(__byte_perm(v[0][w], v[1][w], e ? 0x7362 : 0x5140), a0, a1);
+                e4m3x4_to_f16x2(__byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                  mma<false>(o[i][cb * C::NV / 2 + 2 * w + e], a0, a1, a2, a3, pb[i][0], pb[i][1]);
               }
             } else {
-              mma<C::MMA_BF16>(o[ob * C::NV + 2 * w], pa, __byte_perm(v[0][w], v[1][w], 0x5410),
-                               __byte_perm(v[2][w], v[3][w], 0x5410));
-              mma<C::MMA_BF16>(o[ob * C::NV + 2 * w + 1], pa,
-                               __byte_perm(v[0][w], v[1][w], 0x7632),
-                               __byte_perm(v[2][w], v[3][w], 0x7632));
+              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+              const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+              const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
+              const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+                mma<C::MMA_BF16>(o[i][cb * C::NV / 2 + w], a0, a1, a2, a3, pb[i][0], pb[i][1]);
             }
           }
         }
@@ -481,22 +519,24 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
     }
   }
 
-  // ---- join the warps: m and l of every (key group, row), then O relative to the largest m
-  float* wm = reinterpret_cast<float*>(smem + C::OFF_ML);  // [KW][RT]
-  float* wl = wm + C::KW * RT;                             // [KW][RT]
-  float* cm = wl + C::KW * RT;                             // [RT]
+  // ---- join the warps: m and l of every (warp, row), then O relative to the largest m
+  float* wm = reinterpret_cast<float*>(smem + C::OFF_ML);  // [CW][RT]
+  float* wl = wm + C::CW * RT;                             // [CW][RT]
+  float* cm = wl + C::CW * RT;                             // [RT]
   float* cl = cm + RT;                                     // [RT]
-  float* part = reinterpret_cast<float*>(smem);            // [KW][RT][D] over the ring
+  float* part = reinterpret_cast<float*>(smem);            // [CW][RT][D] over the ring
   if (warp < C::CW) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (c == 0 && half == 0) {
-        wm[kg * RT + g + 8 * h] = m[h];
-        wl[kg * RT + g + 8 * h] = l[h];
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[i][y] += __shfl_xor_sync(0xffffffffu, l[i][y], d);
+        if (g == 0) {
+          wm[warp * RT + 8 * i + 2 * c + y] = m[i][y];
+          wl[warp * RT + 8 * i + 2 * c + y] = l[i][y];
+        }
       }
-    }
   }
   __syncthreads();  // every warp is done with the ring, too
   if (bars->abort) {
@@ -508,32 +548,32 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
   }
   if (warp < C::CW) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = g + 8 * h;
-      if (it.m0 + r >= it.rows) continue;
-      float top = -CUDART_INF_F;
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int w = 0; w < C::KW; ++w) top = fmaxf(top, wm[w * RT + r]);
-      const float f = part_weight(m[h], top);
+      for (int y = 0; y < 2; ++y) {
+        const int r = 8 * i + 2 * c + y;
+        if (it.m0 + r >= it.rows) continue;
+        float top = -CUDART_INF_F;
 #pragma unroll
-      for (int ob = 0; ob < C::OB; ++ob)
+        for (int w = 0; w < C::CW; ++w) top = fmaxf(top, wm[w * RT + r]);
+        const float f = part_weight(m[i][y], top);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {  // columns NV * (2 c + x) + i of the block
-          float* dst = part + (kg * RT + r) * D + (half * C::OB + ob) * (C::SWB / C::EB) +
-                       C::NV * (2 * c + x);
+        for (int cb = 0; cb < C::NCB; ++cb) {
+          float* dst = part + (warp * RT + r) * D + cb * C::BE + C::NV * g;
+          const int x = cb * C::NV / 2;
 #pragma unroll
-          for (int i = 0; i < C::NV; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(
-                o[ob * C::NV + i][2 * h + x] * f, o[ob * C::NV + i + 1][2 * h + x] * f,
-                o[ob * C::NV + i + 2][2 * h + x] * f, o[ob * C::NV + i + 3][2 * h + x] * f);
+          for (int e = 0; e < C::NV / 2; e += 2)
+            *reinterpret_cast<float4*>(dst + 2 * e) =
+                make_float4(o[i][x + e][y] * f, o[i][x + e][2 + y] * f, o[i][x + e + 1][y] * f,
+                            o[i][x + e + 1][2 + y] * f);
         }
-    }
+      }
   }
   if (threadIdx.x < RT) {
     const int r = threadIdx.x;
     float top = -CUDART_INF_F, sum = 0.f;
-    for (int w = 0; w < C::KW; ++w) top = fmaxf(top, wm[w * RT + r]);
-    for (int w = 0; w < C::KW; ++w) sum = fmaf(part_weight(wm[w * RT + r], top), wl[w * RT + r], sum);
+    for (int w = 0; w < C::CW; ++w) top = fmaxf(top, wm[w * RT + r]);
+    for (int w = 0; w < C::CW; ++w) sum = fmaf(part_weight(wm[w * RT + r], top), wl[w * RT + r], sum);
     cm[r] = top;
     cl[r] = sum;
   }
@@ -547,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
       const int r = x / pieces, d = x % pieces * 4;
       float4 a = *reinterpret_cast<const float4*>(part + r * D + d);
 #pragma unroll
-      for (int w = 1; w < C::KW; ++w) {
+      for (int w = 1; w < C::CW; ++w) {
         const float4 b = *reinterpret_cast<const float4*>(part + (w * RT + r) * D + d);
         a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
       }
@@ -556,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
     cg::this_cluster().sync();
   }
   const int rank = blockIdx.x % cluster;
-  const int parts = cluster > 1 ? cluster : C::KW;
+  const int parts = cluster > 1 ? cluster : C::CW;
   const float fv = E4M3 && p.c.v_ds
                        ? p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h]
                        : 1.0f;
@@ -602,11 +642,11 @@ __global__ void __launch_bounds__(Cfg<D, BF16, E4M3>::THREADS, Cfg<D, BF16, E4M3
   if (cluster > 1) cg::this_cluster().sync();  // the others have read this CTA's shared memory
 }
 
-template <int D, bool BF16, bool E4M3>
+template <int D, int NT, bool BF16, bool E4M3>
 cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
                            long long blocks, int cluster, cudaStream_t stream) {
-  using C = Cfg<D, BF16, E4M3>;
-  auto* kernel = softmax_rows_kernel<D, BF16, E4M3>;
+  using C = Cfg<D, NT, BF16, E4M3>;
+  auto* kernel = softmax_rows_kernel<D, NT, BF16, E4M3>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::USED, done);
   if (e != cudaSuccess) return e;
@@ -623,12 +663,20 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tc, long l
   return cudaLaunchKernelEx(&cfg, kernel, tc, p, (int)tiles, cluster);
 }
 
+template <bool BF16, bool E4M3, int NT>
+cudaError_t launch_dim(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
+                       long long blocks, int cluster, cudaStream_t s) {
+  if (p.c.D > 128) return launch_variant<256, NT, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
+  if (p.c.D > 64) return launch_variant<128, NT, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
+  return launch_variant<64, NT, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
+}
+
+// rows: packed query rows of one item, 8 or 16.
 template <bool BF16, bool E4M3>
-cudaError_t launch_rows(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
+cudaError_t launch_rows(const SoftmaxParams& p, const CUtensorMap& tc, int rows, long long tiles,
                         long long blocks, int cluster, cudaStream_t s) {
-  if (p.c.D > 128) return launch_variant<256, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
-  if (p.c.D > 64) return launch_variant<128, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
-  return launch_variant<64, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
+  return rows == 8 ? launch_dim<BF16, E4M3, 1>(p, tc, tiles, blocks, cluster, s)
+                   : launch_dim<BF16, E4M3, 2>(p, tc, tiles, blocks, cluster, s);
 }
 
 }  // namespace rows

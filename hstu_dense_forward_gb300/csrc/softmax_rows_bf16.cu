@@ -4,10 +4,10 @@
 namespace hstu {
 
 cudaError_t launch_softmax_rows_bf16(const SoftmaxParams& p, bool e4m3, const CUtensorMap& tc,
-                                    long long tiles, long long blocks, int cluster,
+                                    int rows, long long tiles, long long blocks, int cluster,
                                     cudaStream_t stream) {
-  return e4m3 ? rows::launch_rows<true, true>(p, tc, tiles, blocks, cluster, stream)
-              : rows::launch_rows<true, false>(p, tc, tiles, blocks, cluster, stream);
+  return e4m3 ? rows::launch_rows<true, true>(p, tc, rows, tiles, blocks, cluster, stream)
+              : rows::launch_rows<true, false>(p, tc, rows, tiles, blocks, cluster, stream);
 }
 
 }  // namespace hstu

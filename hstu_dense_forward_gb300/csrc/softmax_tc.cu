@@ -20,7 +20,7 @@ HSTU_TC_UNIT(fp16_e4m3);
 #undef HSTU_TC_UNIT
 #define HSTU_ROWS_UNIT(n)                                                                     \
   cudaError_t launch_softmax_rows_##n(const SoftmaxParams& p, bool e4m3,                      \
-                                      const CUtensorMap& tc, long long tiles,                 \
+                                      const CUtensorMap& tc, int rows, long long tiles,       \
                                       long long blocks, int cluster, cudaStream_t stream)
 HSTU_ROWS_UNIT(bf16);
 HSTU_ROWS_UNIT(fp16);
@@ -59,15 +59,21 @@ bool cache_map(CUtensorMap* m, const SoftmaxParams& p, int dtype, bool e4m3, int
 
 }  // namespace
 
-cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, long long tiles,
-                                long long blocks, int cluster, cudaStream_t stream) {
+int softmax_rows_ctas(int D, bool e4m3, int rows) {
+  const bool more = e4m3 && rows == 8;
+  return kernel_dim(D) == 256 ? (more ? 2 : 1) : (more ? 3 : 2);
+}
+
+cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, int rows,
+                                long long tiles, long long blocks, int cluster,
+                                cudaStream_t stream) {
   CUtensorMap tc;
   const int row_bytes = kernel_dim(p.c.D) * (e4m3 ? 1 : 2);
   const int swz = row_bytes < 128 ? row_bytes : 128;
   if (!cache_map(&tc, p, dtype, e4m3, swz / (e4m3 ? 1 : 2), 64, swz)) return cudaErrorInvalidValue;
   return dtype == HSTU_BF16
-             ? launch_softmax_rows_bf16(p, e4m3, tc, tiles, blocks, cluster, stream)
-             : launch_softmax_rows_fp16(p, e4m3, tc, tiles, blocks, cluster, stream);
+             ? launch_softmax_rows_bf16(p, e4m3, tc, rows, tiles, blocks, cluster, stream)
+             : launch_softmax_rows_fp16(p, e4m3, tc, rows, tiles, blocks, cluster, stream);
 }
 
 int softmax_tc_key_tile(int D) { return kernel_dim(D) == 256 ? 64 : 128; }

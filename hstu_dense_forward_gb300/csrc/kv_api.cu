@@ -82,6 +82,16 @@ bool row_dtype_ok(const hstu_kv_cache* c, int dtype) {
   return c->dtype == HSTU_FP8_E4M3 || c->dtype == dtype;
 }
 
+// Streaming multiprocessors of a device, asked for once.
+bool device_sms(int dev, int* sms) {
+  static std::atomic<int> known[64];
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+  if (keep) known[dev].store(*sms, std::memory_order_relaxed);
+  return true;
+}
+
 hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append, void* stream) {
   const hstu_status st = check_cache(c);
   if (st != HSTU_OK) return st;
@@ -95,24 +105,14 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
       r->v_stride < width || r->k_stride * eb % 16 != 0 || r->v_stride * eb % 16 != 0 ||
       r->k_stride > (1ll << 40) || r->v_stride > (1ll << 40) || !cache_pointers_ok(c))
     return HSTU_ERR_INVALID_ARG;
-  if (hstu::kv_copy_blocks(r->total_tokens, c->num_heads_kv, c->head_dim) > 0x7fffffffll)
-    return HSTU_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   const hstu::CacheView v = cache_view(c, r->seq_offsets, r->total_tokens);
   return hstu::launch_kv_copy(v, r->k, r->v, r->k_stride, r->v_stride, r->dtype,
-                              c->dtype == HSTU_FP8_E4M3, append,
+                              c->dtype == HSTU_FP8_E4M3, append, sms,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? HSTU_OK
              : HSTU_ERR_CUDA;
-}
-
-// Streaming multiprocessors of a device, asked for once.
-bool device_sms(int dev, int* sms) {
-  static std::atomic<int> known[64];
-  const bool keep = dev >= 0 && dev < 64;
-  if (keep && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
-  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
-  if (keep) known[dev].store(*sms, std::memory_order_relaxed);
-  return true;
 }
 
 // How a call runs: query rows of one CTA, key ranges, grid and workspace.

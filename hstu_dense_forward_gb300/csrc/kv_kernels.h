@@ -23,9 +23,8 @@ struct CacheView;
 struct SoftmaxParams;
 
 // Append (append = true) or read back; dtype of k and v, e4m3: the cache holds E4M3.
-long long kv_copy_blocks(long long T, int Nk, int D);
 cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_stride,
-                           long long v_stride, int dtype, bool e4m3, bool append,
+                           long long v_stride, int dtype, bool e4m3, bool append, int sms,
                            cudaStream_t stream);
 
 // fp32 attention on CUDA cores.

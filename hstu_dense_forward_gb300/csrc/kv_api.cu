@@ -119,7 +119,7 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
 struct AttnPlan {
   enum { SIMT, TC, ROWS } kernel;
   int qtiles;          // query tiles of one CTA (TC)
-  int rows;            // query rows of one item (ROWS)
+  int rows;            // query rows of one item (SIMT, ROWS)
   int cluster;         // CTAs that divide the keys of one item (ROWS)
   int splits, min_range;
   long long tiles, blocks, workspace;
@@ -146,12 +146,15 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   const long long most = a->max_seqlen < a->total_tokens ? a->max_seqlen : a->total_tokens;
   // query rows (token, head) of one item: a CTA's, or a cluster's
-  long long bm = hstu::softmax_simt_rows();
+  long long bm;
   if (a->dtype == HSTU_F32) {
     pl->kernel = AttnPlan::SIMT;
+    pl->rows = most * G <= 16 ? 16 : 64;
+    bm = pl->rows;
   } else if (most * G <= 16) {
     pl->kernel = AttnPlan::ROWS;
-    pl->rows = bm = most * G <= 8 ? 8 : 16;
+    pl->rows = most * G <= 8 ? 8 : 16;
+    bm = pl->rows;
   } else {
     pl->kernel = AttnPlan::TC;
     pl->qtiles = most > 128 / G && c->head_dim <= 128 ? 2 : 1;
@@ -177,7 +180,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     pl->splits = (int)(want / pl->cluster);
     pl->min_range = 128 * pl->cluster;
   } else {
-    pl->min_range = 256;
+    pl->min_range = pl->kernel == AttnPlan::TC ? 256 : 128;
     const long long want = ((pl->kernel == AttnPlan::TC ? 2ll : 4ll) * sms + items - 1) / items;
     const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
     pl->splits = (int)(want < can ? want : can);
@@ -248,7 +251,7 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
                                       pl.cluster, s)
       : pl.kernel == AttnPlan::TC
           ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.tiles, pl.blocks, s)
-          : hstu::launch_softmax_simt(p, fp8, pl.tiles, pl.blocks, s);
+          : hstu::launch_softmax_simt(p, fp8, pl.rows, pl.tiles, pl.blocks, s);
   if (e == cudaSuccess && pl.splits > 1) e = hstu::launch_softmax_combine(p, a->dtype, s);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }

@@ -27,9 +27,8 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
                            long long v_stride, int dtype, bool e4m3, bool append, int sms,
                            cudaStream_t stream);
 
-// fp32 attention on CUDA cores.
-int softmax_simt_rows();  // query rows (token, head) of one CTA
-cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, long long tiles,
+// fp32 attention on CUDA cores: `rows` (16 or 64) packed query rows of one kv head per CTA.
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream);
 
 // Tensor-core attention (bf16, fp16). A CTA takes qtiles tiles of 128 / G tokens; two where

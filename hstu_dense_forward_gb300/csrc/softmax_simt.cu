@@ -1,12 +1,16 @@
 // fp32 softmax attention over the paged KV cache on CUDA cores (FFMA), and the
 // kernel that joins the key ranges of sequences worked on in parts.
 //
-// One CTA (256 threads) takes BM packed query rows of one kv head (packed row r of a sequence
-// is query token r / G, head hk * G + r % G, so that the G heads that share a kv head share
-// its loads) and one range of the keys, in steps of 64 keys, with the running maximum m and
-// sum l of the softmax in base 2:
+// One CTA (256 threads, 16 x 16) takes BM packed query rows of one kv head (packed row r of a
+// sequence is query token r / G, head hk * G + r % G, so that the G heads that share a kv head
+// share its loads) and one range of the keys, in steps of BN keys, with the running maximum m
+// and sum l of the softmax in base 2:
 //   x = scale_log2 * Q K^T, m' = max(m, x), P = 2^(x - m'), l = 2^(m - m') l + sum P,
 //   O = 2^(m - m') O + P V,                        out = O / l, log2 of the sum = m + log2 l.
+// A thread owns rows ty + 16 a, of the scores keys tx + 16 c and of the output columns
+// 4 tx + 64 u .. + 3; every operand comes from shared memory in float4 (four elements of the
+// head dim, or four keys), so that a step spends four times as many FMAs as loads. BM = 16
+// serves few rows, where reading the cache is what counts.
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -19,11 +23,7 @@ namespace hstu {
 
 namespace {
 
-constexpr int BM = 64;  // packed query rows per CTA
-constexpr int BN = 64;  // keys per step
 constexpr int kThreads = 256;
-constexpr int kMaxD = 256;
-constexpr int kMaxU = kMaxD / 16;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <typename T>
@@ -37,15 +37,47 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+template <int D_, int BM_, bool E4M3>
+struct Cfg {
+  static constexpr int D = D_, BM = BM_;
+  static constexpr int BN = D == 64 ? 64 : 32;  // (at D = 256 what shared memory holds)
+  static constexpr int RA = BM / 16, CK = BN / 16, U = D / 64;
+  static constexpr int LD = D + 4, LDP = BN + 4;  // padded rows: conflict-free float4 reads
+  static constexpr int OFF_K = BM * LD, OFF_V = OFF_K + BN * LD, OFF_P = OFF_V + BN * D;
+  static constexpr int SMEM = 4 * (OFF_P + BM * LDP);
+};
+
+// Sixteen consecutive elements of the cache as fp32 values.
 template <bool E4M3>
+__device__ __forceinline__ void load_cache(const CacheView& c, long long page, int plane,
+                                           long long row, int hk, int d0, float (&x)[16]) {
+  const long long at = cache_row(c, page, plane, row, hk) + d0;
+  if constexpr (E4M3) {
+    load16(static_cast<const uint8_t*>(c.cache) + at, x);
+    if (c.scale) {
+      const float e = scale_value(c.scale[scale_row(c, page, plane, row, hk)]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= e;
+    }
+  } else {
+    load16(static_cast<const float*>(c.cache) + at, x);
+  }
+}
+
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float s) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
+}
+
+template <int D_, int BM, bool E4M3>
 __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxParams p, int tiles) {
+  using C = Cfg<D_, BM, E4M3>;
+  constexpr int BN = C::BN;
   extern __shared__ float sm[];
   const int D = p.c.D;
-  const int ldk = D + 1;  // padded rows: threads of one warp read different K rows
-  float* Qs = sm;             // [BM][D]
-  float* Ks = Qs + BM * D;    // [BN][D + 1]
-  float* Vs = Ks + BN * ldk;  // [BN][D]
-  float* Ps = Vs + BN * D;    // [BM][BN + 1]
+  float* Qs = sm;             // [BM][LD]
+  float* Ks = sm + C::OFF_K;  // [BN][LD]
+  float* Vs = sm + C::OFF_V;  // [BN][D_]
+  float* Ps = sm + C::OFF_P;  // [BM][LDP]
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 
   // block: sequence b, row tile (later tiles first: with the causal mask they see more
@@ -71,92 +103,80 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
   const long long k0 = split * kr.keys;
   kend = min(kend, k0 + kr.keys);
 
+  // rows of zeros and columns of zeros where there are none
   const float* q = static_cast<const float*>(p.q);
-  for (int x = threadIdx.x; x < BM * D; x += kThreads) {
-    const int r = x / D, d = x - r * D;
+  for (int x = threadIdx.x; x < BM * (D_ / 4); x += kThreads) {
+    const int r = x / (D_ / 4), d = x % (D_ / 4) * 4;
     const long long pr = m0 + r;
-    Qs[x] = pr < rows ? q[(s.t0 + pr / p.G) * p.q_stride +
-                          (hk * p.G + pr % p.G) * (long long)D + d]
-                      : 0.f;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pr < rows && d < D)
+      f = *reinterpret_cast<const float4*>(q + (s.t0 + pr / p.G) * p.q_stride +
+                                           (hk * p.G + pr % p.G) * (long long)D + d);
+    *reinterpret_cast<float4*>(Qs + r * C::LD + d) = f;
   }
   float fk = p.scale_log2, fv = 1.f;  // static factors fold into the scale and the output
   if (p.c.k_ds) {
     fk *= p.c.k_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
     fv = p.c.v_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
   }
-  float acc[4][kMaxU], m[4], l[4];
-  long long lim[4];  // keys that each row sees: [0, lim)
+  float4 acc[C::RA][C::U];
+  float m[C::RA], l[C::RA];
+  long long lim[C::RA];  // keys that each row sees: [0, lim)
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
+  for (int a = 0; a < C::RA; ++a) {
     m[a] = -CUDART_INF_F;
     l[a] = 0.f;
     const long long pr = m0 + ty + 16 * a;
     lim[a] = pr >= rows ? 0 : p.causal ? s.Lk - s.n + pr / p.G + 1 : s.Lk;
     lim[a] = min(lim[a], kend);
 #pragma unroll
-    for (int u = 0; u < kMaxU; ++u) acc[a][u] = 0.f;
+    for (int u = 0; u < C::U; ++u) acc[a][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 
   for (long long n0 = k0; n0 < kend; n0 += BN) {
     __syncthreads();  // previous step finished with Ks/Vs/Ps
-    for (int x = threadIdx.x; x < BN * (D / 16); x += kThreads) {
-      const int r = x / (D / 16), d0 = (x - r * (D / 16)) * 16;
+    for (int x = threadIdx.x; x < BN * (D_ / 16); x += kThreads) {
+      const int r = x / (D_ / 16), d0 = x % (D_ / 16) * 16;
       float kx[16], vx[16];
       const long long page = n0 + r < kend ? page_at(p.c, s, n0 + r) : -1;
-      if (page >= 0) {
+      if (page >= 0 && d0 < D) {
         const long long row = (n0 + r) & (page_size(p.c) - 1);
-        const long long ka = cache_row(p.c, page, 0, row, hk) + d0;
-        const long long va = cache_row(p.c, page, 1, row, hk) + d0;
-        if constexpr (E4M3) {
-          load16(static_cast<const uint8_t*>(p.c.cache) + ka, kx);
-          load16(static_cast<const uint8_t*>(p.c.cache) + va, vx);
-          if (p.c.scale) {
-            const float ek = scale_value(p.c.scale[scale_row(p.c, page, 0, row, hk)]);
-            const float ev = scale_value(p.c.scale[scale_row(p.c, page, 1, row, hk)]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              kx[i] *= ek;
-              vx[i] *= ev;
-            }
-          }
-        } else {
-          load16(static_cast<const float*>(p.c.cache) + ka, kx);
-          load16(static_cast<const float*>(p.c.cache) + va, vx);
-        }
+        load_cache<E4M3>(p.c, page, 0, row, hk, d0, kx);
+        load_cache<E4M3>(p.c, page, 1, row, hk, d0, vx);
       } else {
-        if (n0 + r < kend) report(p.c, HSTU_DEVERR_OFFSETS);
+        if (page < 0 && n0 + r < kend) report(p.c, HSTU_DEVERR_OFFSETS);
 #pragma unroll
         for (int i = 0; i < 16; ++i) kx[i] = vx[i] = 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        Ks[r * ldk + d0 + i] = kx[i];
-        Vs[r * D + d0 + i] = vx[i];
-      }
+      store16(Ks + r * C::LD + d0, kx);
+      store16(Vs + r * D_ + d0, vx);
     }
     __syncthreads();
     // scores of rows ty + 16a, keys tx + 16c
-    float sc[4][4];
+    float sc[C::RA][C::CK];
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < C::RA; ++a)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) sc[a][c] = 0.f;
-    for (int d = 0; d < D; ++d) {
-      float qa[4], kb[4];
+      for (int c = 0; c < C::CK; ++c) sc[a][c] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D_; d += 4) {
+      float4 qa[C::RA], kb[C::CK];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) qa[a] = Qs[(ty + 16 * a) * D + d];
+      for (int a = 0; a < C::RA; ++a)
+        qa[a] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * a) * C::LD + d);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) kb[c] = Ks[(tx + 16 * c) * ldk + d];
+      for (int c = 0; c < C::CK; ++c)
+        kb[c] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * c) * C::LD + d);
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
+      for (int a = 0; a < C::RA; ++a)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[a][c] = fmaf(qa[a], kb[c], sc[a][c]);
+        for (int c = 0; c < C::CK; ++c) sc[a][c] = dot4(qa[a], kb[c], sc[a][c]);
     }
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < C::RA; ++a) {
       float top = -CUDART_INF_F;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < C::CK; ++c) {
         sc[a][c] = n0 + tx + 16 * c < lim[a] ? sc[a][c] * fk : -CUDART_INF_F;
         top = fmaxf(top, sc[a][c]);
       }
@@ -167,49 +187,61 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
       const float corr = exp2f(m[a] - base);
       float sum = 0.f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < C::CK; ++c) {
         const float w = exp2f(sc[a][c] - base);
         sum += w;
-        Ps[(ty + 16 * a) * (BN + 1) + tx + 16 * c] = w;
+        Ps[(ty + 16 * a) * C::LDP + tx + 16 * c] = w;
       }
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       l[a] = l[a] * corr + sum;
       m[a] = mn;
 #pragma unroll
-      for (int u = 0; u < kMaxU; ++u) acc[a][u] *= corr;
+      for (int u = 0; u < C::U; ++u) {
+        acc[a][u].x *= corr;
+        acc[a][u].y *= corr;
+        acc[a][u].z *= corr;
+        acc[a][u].w *= corr;
+      }
     }
     __syncthreads();
-    for (int j = 0; j < BN; ++j) {
-      float pa[4];
+#pragma unroll 2
+    for (int j = 0; j < BN; j += 4) {
+      float4 pa[C::RA];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) pa[a] = Ps[(ty + 16 * a) * (BN + 1) + j];
+      for (int a = 0; a < C::RA; ++a)
+        pa[a] = *reinterpret_cast<const float4*>(Ps + (ty + 16 * a) * C::LDP + j);
 #pragma unroll
-      for (int u = 0; u < kMaxU; ++u) {
-        const int d = tx + 16 * u;
-        if (d < D) {
-          const float vv = Vs[j * D + d];
+      for (int u = 0; u < C::U; ++u)
 #pragma unroll
-          for (int a = 0; a < 4; ++a) acc[a][u] = fmaf(pa[a], vv, acc[a][u]);
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(Vs + (j + i) * D_ + tx * 4 + 64 * u);
+#pragma unroll
+          for (int a = 0; a < C::RA; ++a) {
+            const float w = i == 0 ? pa[a].x : i == 1 ? pa[a].y : i == 2 ? pa[a].z : pa[a].w;
+            acc[a][u].x = fmaf(w, v.x, acc[a][u].x);
+            acc[a][u].y = fmaf(w, v.y, acc[a][u].y);
+            acc[a][u].z = fmaf(w, v.z, acc[a][u].z);
+            acc[a][u].w = fmaf(w, v.w, acc[a][u].w);
+          }
         }
-      }
     }
   }
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
+  for (int a = 0; a < C::RA; ++a) {
     const long long pr = m0 + ty + 16 * a;
     if (pr >= rows) continue;
     const long long row = (s.t0 + pr / p.G) * p.Nq + hk * p.G + pr % p.G;  // of out and lse
     const float inv = l[a] > 0.f ? fv / l[a] : l[a];  // (a NaN sum stays one)
     const float log2sum = l[a] == 0.f ? -CUDART_INF_F : m[a] + log2f(l[a]);
+    float* dst = nsplit > 1 ? p.part_o + ((long long)split * p.c.T * p.Nq + row) * D
+                            : static_cast<float*>(p.out) + row * D;
 #pragma unroll
-    for (int u = 0; u < kMaxU; ++u) {
-      const int d = tx + 16 * u;
-      if (d >= D) continue;
-      if (nsplit > 1)
-        p.part_o[((long long)split * p.c.T * p.Nq + row) * D + d] = acc[a][u] * inv;
-      else
-        static_cast<float*>(p.out)[row * D + d] = acc[a][u] * inv;
+    for (int u = 0; u < C::U; ++u) {
+      const int d = tx * 4 + 64 * u;
+      if (d < D)
+        *reinterpret_cast<float4*>(dst + d) = make_float4(acc[a][u].x * inv, acc[a][u].y * inv,
+                                                          acc[a][u].z * inv, acc[a][u].w * inv);
     }
     if (tx == 0) {
       if (nsplit > 1)
@@ -261,28 +293,35 @@ __global__ void __launch_bounds__(kThreads) softmax_combine_kernel(const Softmax
   if (p.lse && first == 0) p.lse[row] = (top + log2f(sum)) * kLn2;
 }
 
-template <bool E4M3>
+template <int D, int BM, bool E4M3>
 cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
                    cudaStream_t stream) {
-  const size_t smem = sizeof(float) * ((size_t)BM * p.c.D + (size_t)BN * (p.c.D + 1) +
-                                       (size_t)BN * p.c.D + (size_t)BM * (BN + 1));
-  constexpr int kMost = sizeof(float) * (BM * kMaxD + BN * (kMaxD + 1) + BN * kMaxD + BM * (BN + 1));
+  using C = Cfg<D, BM, E4M3>;
+  auto* kernel = softmax_simt_kernel<D, BM, E4M3>;
   static std::atomic<unsigned long long> done;
-  const cudaError_t e =
-      allow_smem(reinterpret_cast<const void*>(softmax_simt_kernel<E4M3>), kMost, done);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
-  softmax_simt_kernel<E4M3>
-      <<<dim3((unsigned)blocks, p.splits), kThreads, smem, stream>>>(p, (int)tiles);
+  kernel<<<dim3((unsigned)blocks, p.splits), kThreads, C::SMEM, stream>>>(p, (int)tiles);
   return cudaGetLastError();
+}
+
+template <int BM, bool E4M3>
+cudaError_t launch_dim(const SoftmaxParams& p, long long tiles, long long blocks,
+                       cudaStream_t stream) {
+  if (p.c.D > 128) return launch<256, BM, E4M3>(p, tiles, blocks, stream);
+  if (p.c.D > 64) return launch<128, BM, E4M3>(p, tiles, blocks, stream);
+  return launch<64, BM, E4M3>(p, tiles, blocks, stream);
 }
 
 }  // namespace
 
-int softmax_simt_rows() { return BM; }
-
-cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, long long tiles,
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream) {
-  return e4m3 ? launch<true>(p, tiles, blocks, stream) : launch<false>(p, tiles, blocks, stream);
+  if (rows == 16)
+    return e4m3 ? launch_dim<16, true>(p, tiles, blocks, stream)
+                : launch_dim<16, false>(p, tiles, blocks, stream);
+  return e4m3 ? launch_dim<64, true>(p, tiles, blocks, stream)
+              : launch_dim<64, false>(p, tiles, blocks, stream);
 }
 
 cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream) {

@@ -14,10 +14,21 @@
 //   next warp              issues every tcgen05.mma; owns TMEM;
 //   next warp              TMA loads: Q, then K and V tiles through one ring, in the order
 //                          in which the products need them;
-//   E4M3: four more warps  turn E4M3 tiles (staged by TMA) into 16-bit ones in the ring,
-//                          times their row scales (exact in bf16: a scale is a power of two).
+//   E4M3: eight more warps turn E4M3 tiles (staged by TMA) into fp16 ones in the ring, four
+//                          the keys and four the values (one warpgroup for both took 2750
+//                          cycles a tile, longer than the products).
 // With two query tiles, one tile's products run while the softmax of the other does. With one
 // (few rows, or D = 256, whose O takes half of TMEM) the scores have two buffers instead.
+//
+// E4M3 caches: both products run in fp16, which holds every code exactly. A tile's rows are taken
+// relative to the largest of its row scales, 2^EK (K) or 2^EV (V): a code becomes fp16 by one
+// conversion and one product with 2^(e - EK), exact unless it drops below 2^-24, that is 2^-32
+// of what the tile's largest elements are. 2^EK multiplies the scores. 2^EV would leave fp16's
+// range as a factor of the weights, so it enters their exponent: with u = x + EV,
+//   P = 2^(u - m), m following max u, l += 2^-EV sum P,
+// and O / l is the output (2^m cancels). bf16 queries become fp16 in place, times a power of two
+// of their row, chosen so that the row's largest lies in [2^14, 2^15). (Dequantising to q's type
+// instead took twice the instructions: 1056 us instead of 768 for 4096 tokens over 4096.)
 //
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
@@ -58,8 +69,11 @@ struct Cfg {
   static constexpr int NST = E4M3 ? (D == 64 ? 4 : (NQT == 1 && D == 128 ? 3 : 3)) : 0;
   static constexpr int SM_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1;
-  static constexpr int CONV_WARP = SM_WARPS + 4;  // (a warpgroup of its own)
-  static constexpr int THREADS = (SM_WARPS + 4 + (E4M3 ? 4 : 0)) * 32;
+  static constexpr int CONV_WARP = SM_WARPS + 4;  // (a warpgroup each for K and V)
+  static constexpr int THREADS = (SM_WARPS + 4 + (E4M3 ? 8 : 0)) * 32;
+  // columns of S that a softmax thread holds at a time: a whole row, or (E4M3, whose conversion
+  // needs the registers) half of one, which is then loaded twice
+  static constexpr int SC = E4M3 ? KT / 2 : KT;
   // TMEM: score buffers of KT columns (P over them), then O
   static constexpr uint32_t O_COL = NQT * NSB * KT;
   static_assert(O_COL + NQT * D <= kTmemCols, "TMEM");
@@ -72,7 +86,11 @@ struct Cfg {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
+constexpr int kExpDepth = 8;  // tiles whose exponents are kept (the conversion is fewer ahead)
+
 struct Bars {
+  uint64_t q_ready, exp_full[kExpDepth];
+  float tile_exp[kExpDepth][2];  // EK, EV
   uint64_t q_full, kv_full[6], kv_empty[6], st_full[4], st_empty[4];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;
   uint32_t tmem_base;
@@ -181,6 +199,19 @@ __device__ __forceinline__ bool warp_wait(const SoftmaxParams& p, Bars* bars, ui
   return __all_sync(0xffffffffu, wait_bar(p, bars, bar, parity));
 }
 
+// 2^-d as an fp16 pattern (0 below the smallest value).
+__device__ __forceinline__ uint32_t half_power(int d) {
+  return d < 15 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float power2(int e) {  // e in [-126, 127]
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -260,43 +291,64 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
   }
 }
 
-// ------------------------------------------------------------------ E4M3 -> 16 bits
+// ------------------------------------------------------------------ E4M3 -> fp16
 // A thread converts sixteen codes of a row at a time. Rows beyond the sequence become zeros
 // (what an unused row of a page holds, NaN included, does not reach the products).
-template <class C, bool BF16>
+template <class C>
 __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const Item& it,
-                             int warp, int lane) {
+                             bool values, int warp, int lane) {
   constexpr int CPR = C::D / 16;  // chunks of a row
   constexpr int STEP = 128 / CPR, PASSES = C::KT / STEP;  // rows of one pass of the four warps
-  const int chunk = lane % CPR, r0 = warp * (32 / CPR) + lane / CPR;
+  constexpr int RPW = 32 / CPR;  // rows of one pass of a warp
+  const int chunk = lane % CPR, r0 = warp * RPW + lane / CPR;
+  // the row whose factor this lane holds for its warp (PASSES of RPW rows, 32 at most)
+  const int my_row = warp * RPW + lane % RPW + STEP * (lane / RPW % PASSES);
   const int cb = chunk / 4, c16 = (chunk % 4) * 2;  // column block, first 16-byte piece in it
   for (int i = 0; i < 2 * it.nmax; ++i) {
     int t;
-    ring_tile<C>(i, it.nmax, t);
+    if (ring_tile<C>(i, it.nmax, t) != values) continue;
     const int have = (int)min((long long)C::KT, it.s.Lk - it.k0 - (long long)t * C::KT);
     const int st = i % C::NST, slot = i % C::NSLOT;
     if (!warp_wait(p, bars, &bars->st_full[st], (i / C::NST) & 1)) return;
-    if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
     const uint8_t* scale = smem + C::OFF_SC + st * 128;
+    int top = 127;  // the largest scale of the tile's rows
+    if (p.c.scale) {
+      uint32_t s4 = 0;
+      if (lane * 4 < C::KT) s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
+      top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (lane * 4 + e < have) top = max(top, (int)((s4 >> (8 * e)) & 0xffu));
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    if (warp == 0 && lane == 0) {
+      bars->tile_exp[t % kExpDepth][values ? 1 : 0] = (float)(top - 127);
+      ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[t % kExpDepth]));
+    }
     const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
     uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
-#pragma unroll 4
+    uint32_t mine = 0x3c003c00u;  // factor of row my_row, twice (0 beyond the sequence)
+    if (p.c.scale) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
+    if (my_row >= have) mine = 0u;
+    uint4 u[PASSES];
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      u[k] = *reinterpret_cast<const uint4*>(src + (r0 + STEP * k) * C::D);
+      if (r0 + STEP * k >= have) u[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
+#pragma unroll
     for (int k = 0; k < PASSES; ++k) {
       const int r = r0 + STEP * k;
-      const float f = p.c.scale ? scale_value(scale[r]) : 1.0f;
+      const uint32_t in[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      const uint32_t f = __shfl_sync(0xffffffffu, mine, lane / CPR + RPW * k);
       uint32_t w[8];
-      if (r < have) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src + r * C::D);
-        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t h = e4m3x2_to_f16x2(in[e >> 1] >> (16 * (e & 1)));
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          w[e] = pack2<BF16>(x.x * f, x.y * f);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 0u;
+      for (int e = 0; e < 4; ++e) {
+        e4m3x4_to_f16x2(in[e], w[2 * e], w[2 * e + 1]);
+        w[2 * e] = mul_f16x2(w[2 * e], f);
+        w[2 * e + 1] = mul_f16x2(w[2 * e + 1], f);
       }
       uint8_t* row = dst + r * C::SWB;
       *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -309,14 +361,44 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
   }
 }
 
+// Row r of a bf16 query tile (swizzled shared memory) becomes fp16 times 2^sh; returns 2^-sh.
+template <class C>
+__device__ float query_to_half(uint8_t* tile, int r) {
+  uint32_t top = 0;  // largest magnitude, as bf16 patterns
+#pragma unroll 4
+  for (int x = 0; x < C::NCB * 8; ++x) {
+    const uint4 u = *reinterpret_cast<const uint4*>(tile + (x >> 3) * C::Q_CB + r * C::SWB +
+                                                    ((x & 7) ^ (r & 7)) * 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+  }
+  const int sh = min(14 - ((int)(top >> 7) - 127), 126);
+  const float mul = power2(sh);
+#pragma unroll 4
+  for (int x = 0; x < C::NCB * 8; ++x) {
+    uint4* at = reinterpret_cast<uint4*>(tile + (x >> 3) * C::Q_CB + r * C::SWB +
+                                         ((x & 7) ^ (r & 7)) * 16);
+    const uint4 u = *at;
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack2<false>(__uint_as_float(w[e] << 16) * mul,
+                          __uint_as_float(w[e] & 0xffff0000u) * mul);
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return power2(-sh);
+}
+
 // ------------------------------------------------------------------ products
 template <class C, bool BF16>
 struct Issuer {
   const SoftmaxParams& p;
   Bars* bars;
   uint32_t sbase, tmem;
-  static constexpr uint32_t IDESC_S = ptx::idesc_f16(BF16 ? 1u : 0u, 128, C::KT, 0);
-  static constexpr uint32_t IDESC_O = ptx::idesc_f16(BF16 ? 1u : 0u, 128, C::D, 1);
+  static constexpr uint32_t AB = BF16 && !C::E4M3 ? 1u : 0u;  // operands: bf16, or fp16
+  static constexpr uint32_t IDESC_S = ptx::idesc_f16(AB, 128, C::KT, 0);
+  static constexpr uint32_t IDESC_O = ptx::idesc_f16(AB, 128, C::D, 1);
 
   __device__ bool kv_ready(int i) {
     if (!wait_bar(p, bars, &bars->kv_full[i % C::NSLOT], (i / C::NSLOT) & 1)) return false;
@@ -366,7 +448,8 @@ struct Issuer {
 
 template <class C, bool BF16>
 __device__ bool mma_loop(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars, const Item& it) {
-  if (!wait_bar(p, bars, &bars->q_full, 0)) return false;
+  if (!wait_bar(p, bars, BF16 && C::E4M3 ? &bars->q_ready : &bars->q_full, 0)) return false;
+  ptx::tc_fence_after();
   const int n = it.nmax;
   // scores of the first NSB tiles
   for (int t = 0; t < C::NSB && t < n; ++t) {
@@ -429,47 +512,69 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
     fv = p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
   }
+  if constexpr (BF16 && C::E4M3) {
+    if (n > 0 || it.nmax > 0) {  // (the loads and products run for the CTA's widest tile)
+      if (!warp_wait(p, bars, &bars->q_full, 0)) return;
+      if (valid) fk *= query_to_half<C>(smem + C::OFF_Q + q * C::Q_TILE, r);
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready));
+    }
+  }
   float m = -CUDART_INF_F, l = 0.0f;
   const uint32_t o_col = tmem + lane_off + C::O_COL + q * C::D;
   for (int t = 0; t < n; ++t) {
     const int sb = C::NQT == 1 ? (t & 1) : q;
     const uint32_t par = C::NQT == 1 ? (t >> 1) & 1 : t & 1;
+    float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
+    if constexpr (C::E4M3) {
+      if (!warp_wait(p, bars, &bars->exp_full[t % kExpDepth], (t / kExpDepth) & 1)) return;
+      ek = power2((int)bars->tile_exp[t % kExpDepth][0]);
+      ev = bars->tile_exp[t % kExpDepth][1];
+    }
     if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
     ptx::tc_fence_after();
     const uint32_t s_col = tmem + lane_off + sb * KT;
-    uint32_t sv[KT / 32][32];
+    constexpr int NC = C::SC / 32;  // chunks held at a time
+    uint32_t sv[NC][32];
     float neg = 0.0f;
-    if (any) {
+    const int left = lim - t * KT;  // keys of the tile that the row sees
+    const bool masked = !__all_sync(0xffffffffu, left >= KT);
+    // columns [c0, c0 + SC) of S: masked scores are -inf; with a negative static factor all
+    // change sign (the largest score has the smallest product), and -inf stays
+    auto load_scores = [&](int c0) {
 #pragma unroll
-      for (int c = 0; c < KT / 32; ++c) ptx::tmem_ld32_issue(s_col + c * 32, sv[c]);
+      for (int c = 0; c < NC; ++c) ptx::tmem_ld32_issue(s_col + c0 + c * 32, sv[c]);
       ptx::tmem_ld_wait(sv[0]);
 #pragma unroll
-      for (int c = 1; c < KT / 32; ++c) ptx::reg_fence(sv[c]);
-      const int left = lim - t * KT;  // keys of the tile that the row sees
-      if (!__all_sync(0xffffffffu, left >= KT)) {
+      for (int c = 1; c < NC; ++c) ptx::reg_fence(sv[c]);
+      if (C::E4M3 && fk < 0.0f) {
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c)
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sv[c][e] ^= 0x80000000u;
+      }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= left) sv[c][e] = 0xff800000u;  // -inf
+            if (c0 + c * 32 + e >= left) sv[c][e] = 0xff800000u;
       }
+    };
+    if (any) {
       float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-      if (fk < 0.0f) {  // a negative static factor: the largest score has the smallest product
+#pragma unroll 1
+      for (int c0 = 0; c0 < KT; c0 += C::SC) {
+        load_scores(c0);
 #pragma unroll
-        for (int c = 0; c < KT / 32; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (c * 32 + e >= left) sv[c][e] = 0x7f800000u;  // (masked scores stay -inf)
-            sv[c][e] ^= 0x80000000u;
-          }
+          for (int e = 0; e < 32; e += 2)
+            top[(e >> 1) & 3] = ptx::max3(top[(e >> 1) & 3], __uint_as_float(sv[c][e]),
+                                          __uint_as_float(sv[c][e + 1]));
       }
-#pragma unroll
-      for (int c = 0; c < KT / 32; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          top[(e >> 1) & 3] = ptx::max3(top[(e >> 1) & 3], __uint_as_float(sv[c][e]),
-                                        __uint_as_float(sv[c][e + 1]));
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(fk);
+      const float mx =
+          fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fabsf(fk) * ek, ev);
       // raise the reference: at the first visible key, and when weights would pass 2^kLazy
       const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
       if (__any_sync(0xffffffffu, raise)) {
@@ -491,7 +596,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
           }
         }
       }
-      neg = m == -CUDART_INF_F ? 0.0f : -m;
+      neg = m == -CUDART_INF_F ? 0.0f : ev - m;
     }
     if constexpr (!C::E4M3) {
       // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
@@ -509,33 +614,50 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       }
     }
     float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    const float fa = fabsf(fk);
+    const float fa = fabsf(fk) * ek;
+    // weights of chunk `at` held in sv[i], summed and stored as columns of P
+    auto weights = [&](int i, int at) {
+      uint32_t pk[16];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (any) {
-#pragma unroll
-        for (int x = 0; x < KT / 64; ++x) {
-          const int c = half * (KT / 64) + x;
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float x0, x1;
-            ptx::fma_f32x2(x0, x1, __uint_as_float(sv[c][2 * e]),
-                           __uint_as_float(sv[c][2 * e + 1]), fa, fa, neg, neg);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            ptx::add_f32x2(sum[e & 1][0], sum[e & 1][1], p0, p1);
-            pk[e] = pack2<BF16>(p0, p1);
-          }
-          ptx::tmem_st16(s_col + c * 16, pk);
-        }
-        ptx::tmem_st_wait();
+      for (int e = 0; e < 16; ++e) {
+        float x0, x1;
+        ptx::fma_f32x2(x0, x1, __uint_as_float(sv[i][2 * e]), __uint_as_float(sv[i][2 * e + 1]),
+                       fa, fa, neg, neg);
+        const float p0 = ex2(x0), p1 = ex2(x1);
+        ptx::add_f32x2(sum[e & 1][0], sum[e & 1][1], p0, p1);
+        pk[e] = pack2<BF16 && !C::E4M3>(p0, p1);
       }
+      ptx::tmem_st16(s_col + at * 16, pk);
+    };
+    auto half_done = [&](int half) {
+      if (any) ptx::tmem_st_wait();
       if (half == 0) {
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
       }
+    };
+    if constexpr (C::SC < KT) {  // (a rolled loop: five warps' roles share the instruction cache)
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (any) {
+          load_scores(half * C::SC);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) weights(c, half * NC + c);
+        }
+        half_done(half);
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (any) {
+#pragma unroll
+          for (int c = half * (NC / 2); c < (half + 1) * (NC / 2); ++c) weights(c, c);
+        }
+        half_done(half);
+      }
     }
-    l += (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
+    const float tile_sum = (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
+    l = C::E4M3 ? fmaf(tile_sum, power2(-(int)ev), l) : l + tile_sum;
     // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
     // below needs PV(n - 2) to be done; S(n - 1) was issued after PV(n - 1 - NSB) only, and
     // once P(n - 1) is handed over both may complete at any time.
@@ -601,6 +723,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   if (warp == C::LOAD_WARP && lane == 0) {
     ptx::mbar_init(ptx::smem_u32(&bars->q_full), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->q_ready), it.nq * 128);
+    for (int s = 0; s < kExpDepth; ++s) ptx::mbar_init(ptx::smem_u32(&bars->exp_full[s]), 2);
     for (int s = 0; s < 6; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), C::E4M3 ? 128 : 1);
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
@@ -628,22 +752,14 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // The softmax keeps a row of scores in registers: with two warpgroups of it the launch's
-  // registers are dealt out anew. 512 threads launch with 128 each (65,536): 176 for the
-  // softmax, 96 for the conversion and 64 for the control warps are 65,536 again; 384 launch
-  // with 168 (64,512): 208 and 72 are 62,464.
-  if constexpr (C::THREADS == 512) {
+  // The softmax keeps scores in registers: with two warpgroups of it the launch's registers are
+  // dealt out anew. 384 threads launch with 168 each (64,512): 208 for the softmax and 72 for the
+  // control warps are 62,464. 640 (E4M3) launch with 96 (61,440): 112 and 80 are 59,392.
+  if constexpr (C::NQT == 2) {
     if (warp < C::SM_WARPS)
-      ptx::regs_inc<176>();
-    else if (warp < C::CONV_WARP)
-      ptx::regs_dec<64>();
+      ptx::regs_inc<C::E4M3 ? 112 : 208>();
     else
-      ptx::regs_dec<96>();
-  } else if constexpr (C::NQT == 2) {
-    if (warp < C::SM_WARPS)
-      ptx::regs_inc<208>();
-    else
-      ptx::regs_dec<72>();
+      ptx::regs_dec<C::E4M3 ? 80 : 72>();
   }
   if (warp < C::SM_WARPS) {
     if (warp / 4 < it.nq) softmax_role<C, BF16>(p, bars, smem, tmem, it, warp / 4, warp, lane);
@@ -656,7 +772,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   } else if (warp == C::LOAD_WARP) {
     if (lane == 0 && it.nmax > 0) load_role<C>(p, bars, smem, it, &tm_q, &tm_c);
   } else if (C::E4M3 && warp >= C::CONV_WARP) {
-    convert_role<C, BF16>(p, bars, smem, it, warp - C::CONV_WARP, lane);
+    const int w = warp - C::CONV_WARP;
+    convert_role<C>(p, bars, smem, it, w >= 4, w & 3, lane);
   }
   __syncwarp();
   ptx::tc_fence_before();

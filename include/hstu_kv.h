@@ -111,8 +111,7 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * sequence are left alone.
  *
  * Statistics and sums are fp32. fp16 and bf16: the weights are rounded to the type of q for the
- * product with V, and the keys and values of an E4M3 cache are taken as hstu_kv_read gives them
- * in that type (static factors are applied in fp32 to the scores and the output instead).
+ * product with V, or to fp16 over an E4M3 cache.
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */

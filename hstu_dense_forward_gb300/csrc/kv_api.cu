@@ -121,8 +121,9 @@ struct AttnPlan {
   int qtiles;          // query tiles of one CTA (TC)
   int rows;            // query rows of one item (SIMT, ROWS)
   int cluster;         // CTAs that divide the keys of one item (ROWS)
+  int balanced;        // CTAs share the items' key tiles (TC)
   int splits, min_range;
-  long long tiles, blocks, workspace;
+  long long tiles, blocks, workspace, parts_bytes;
 };
 
 hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, AttnPlan* pl) {
@@ -157,7 +158,11 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     bm = pl->rows;
   } else {
     pl->kernel = AttnPlan::TC;
-    pl->qtiles = most > 128 / G && c->head_dim <= 128 ? 2 : 1;
+    // Two query tiles share the loads of K and V and keep the tensor pipe busier, if there are
+    // rows for both (4096 tokens over 4096: 670 us with two, 774 with one; 24 sequences of some
+    // 500 rows over 900 keys: 67 and 48)
+    pl->qtiles = c->head_dim <= 128 && most > 128 / G &&
+                         a->total_tokens * G / c->batch >= 256 ? 2 : 1;
     bm = pl->qtiles * (128 / G) * G;
   }
   pl->tiles = (most * G + bm - 1) / bm;
@@ -179,15 +184,24 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     while (pl->cluster < 8 && pl->cluster * 2 <= want) pl->cluster *= 2;
     pl->splits = (int)(want / pl->cluster);
     pl->min_range = 128 * pl->cluster;
-  } else {
-    pl->min_range = pl->kernel == AttnPlan::TC ? 256 : 128;
-    const long long want = ((pl->kernel == AttnPlan::TC ? 2ll : 4ll) * sms + items - 1) / items;
+  } else if (pl->kernel == AttnPlan::SIMT) {
+    pl->min_range = 128;
+    const long long want = (4ll * sms + items - 1) / items;
     const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
     pl->splits = (int)(want < can ? want : can);
+  } else if (c->batch <= hstu::kMaxSeqs && sms <= hstu::kMaxCtas &&
+             a->total_tokens * G / bm + c->batch <= hstu::kMaxItems && items < 4ll * sms) {
+    // few items: one CTA per SM takes an equal share of their key tiles
+    pl->balanced = 1;
+    pl->blocks = sms;
+    pl->parts_bytes = 2ll * sms * pl->qtiles * 128 * (c->head_dim + 1) * 4;
+    pl->workspace = pl->parts_bytes + (long long)sizeof(hstu::PlanTable);
   }
-  if (pl->splits > 1)
-    pl->workspace = (long long)pl->splits * a->total_tokens * a->num_heads_q *
-                    (c->head_dim + 1) * 4;
+  if (pl->splits > 1) {
+    pl->parts_bytes = (long long)pl->splits * a->total_tokens * a->num_heads_q *
+                      (c->head_dim + 1) * 4;
+    pl->workspace = pl->parts_bytes;
+  }
   return HSTU_OK;
 }
 
@@ -241,8 +255,11 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   p.splits = pl.splits;
   p.min_range = pl.min_range;
   p.timeout_ns = 1000000000ll;
+  p.balanced = pl.balanced;
+  // workspace: outputs of the parts, their sums, the table of items
   p.part_o = static_cast<float*>(a->workspace);
-  p.part_lse = p.part_o + (long long)pl.splits * a->total_tokens * a->num_heads_q * c->head_dim;
+  p.part_lse = p.part_o + pl.parts_bytes / 4 / (c->head_dim + 1) * c->head_dim;
+  p.plan = reinterpret_cast<hstu::PlanTable*>(static_cast<char*>(a->workspace) + pl.parts_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = c->dtype == HSTU_FP8_E4M3;
   cudaError_t e =
@@ -252,7 +269,8 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
       : pl.kernel == AttnPlan::TC
           ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.tiles, pl.blocks, s)
           : hstu::launch_softmax_simt(p, fp8, pl.rows, pl.tiles, pl.blocks, s);
-  if (e == cudaSuccess && pl.splits > 1) e = hstu::launch_softmax_combine(p, a->dtype, s);
+  if (e == cudaSuccess && (pl.splits > 1 || pl.balanced))
+    e = hstu::launch_softmax_join(p, a->dtype, 128 / p.G, pl.qtiles, (int)pl.blocks, s);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/hstu_kv.h"
@@ -194,13 +195,54 @@ __device__ __forceinline__ void store16<__half>(__half* p, const float (&x)[16])
 }
 
 // ------------------------------------------------------------- softmax attention
+// Items of a balanced run of the tensor-core kernel: (sequence, tile of query tokens) pairs in
+// order, each of them once per kv head.
+constexpr int kMaxItems = 512, kMaxSeqs = 512, kMaxCtas = 512;
+struct PlanTable {
+  long long cost[kMaxItems + 1];  // running sum of the pairs' costs, in key tiles
+  int first[kMaxSeqs + 1];        // first pair of each sequence
+  uint16_t seq[kMaxItems];        // sequence of each pair
+  int items;
+  // (in the workspace's copy) the pair and kv head at which each CTA's share begins
+  int begin_item[kMaxCtas + 1], begin_head[kMaxCtas + 1];
+};
+constexpr int kPlanSharedBytes = offsetof(PlanTable, begin_item);
+
+// An item costs its key tiles and kItemCost for what it needs besides (its queries' load, the
+// first products' and the output's latency). These units, all heads' of a pair in a row, are
+// shared out equally: CTA c takes units [share(c), share(c + 1)).
+constexpr int kItemCost = 2;
+constexpr int kMinUnits = 4;  // fewest units worth a CTA
+__host__ __device__ inline long long share(long long units, int ctas, int c) {
+  return units * c / ctas;
+}
+__host__ __device__ inline int share_ctas(long long units, int grid) {
+  const long long c = units / kMinUnits;
+  return c < 1 ? 1 : c < grid ? (int)c : grid;
+}
+// Key tiles [from, to) of an item of `cost` units that its units [o1, o2) stand for. A piece
+// from 0 to the last is the whole item; others lie in workspace slot 2 c (a piece that CTA c
+// begins inside an item) or 2 c + 1 (one that it ends inside).
+struct KeyTiles {
+  int from, to;
+};
+__host__ __device__ inline KeyTiles piece_tiles(long long o1, long long o2) {
+  KeyTiles k;
+  k.from = o1 > kItemCost ? (int)(o1 - kItemCost) : 0;
+  k.to = o2 > kItemCost ? (int)(o2 - kItemCost) : 0;
+  return k;
+}
+
 struct SoftmaxParams {
   CacheView c;
   const void* q;
   void* out;
   float* lse;              // [T, Nq] or nullptr
-  float* part_o;           // [splits][T, Nq, D]: each split's normalised output
-  float* part_lse;         // [splits][T, Nq]: log2 of each split's sum (-inf: no key)
+  float* part_o;           // [splits][T, Nq, D]: each key range's normalised output, or (balanced)
+                           // [2 per CTA][rows of an item][D]: each piece's
+  float* part_lse;         // the same without D: log2 of the sums (-inf: no key)
+  PlanTable* plan;         // copy of the table of items (balanced)
+  int balanced;            // tensor-core kernel: CTAs share the items' key tiles equally
   long long q_stride;      // elements
   int Nq, G;               // query heads, query heads of one kv head
   int max_q;               // bound on n

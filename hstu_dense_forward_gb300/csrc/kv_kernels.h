@@ -44,7 +44,9 @@ cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, in
                                 long long tiles, long long blocks, int cluster,
                                 cudaStream_t stream);
 
-// Joins the key ranges of sequences that have more than one.
-cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream);
+// Joins the parts of outputs that several CTAs worked on (balanced runs of the tensor-core
+// kernel: tokens of a query tile, query tiles of an item, CTAs of the run).
+cudaError_t launch_softmax_join(const SoftmaxParams& p, int dtype, int tile_tokens,
+                                int query_tiles, int grid, cudaStream_t stream);
 
 }  // namespace hstu

@@ -26,17 +26,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
-  return __float2bfloat16_rn(x);
-}
-
 template <int D_, int BM_, bool E4M3>
 struct Cfg {
   static constexpr int D = D_, BM = BM_;
@@ -252,47 +241,6 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
   }
 }
 
-// out = sum_s 2^(e_s - max e) O_s / sum_s 2^(e_s - max e) over the key ranges s of a row, e_s
-// the base-2 logarithm of range s's sum. One group of D / 4 lanes (rounded up to a power of
-// two, one warp at most) per (row, head), four consecutive elements a lane and step.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) softmax_combine_kernel(const SoftmaxParams p,
-                                                                   int lane_shift) {
-  const long long lane = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long row = lane >> lane_shift, t = row / p.Nq;
-  if (t >= p.c.T) return;
-  const int b = seq_of_row(p.c, t);
-  const PagedSeq s = paged_seq(p.c, b);
-  if (!attn_seq_ok(p, s) || t < s.t0 || t >= s.t0 + s.n) return;
-  const int nsplit = key_ranges(p, s.Lk).count;
-  if (nsplit < 2) return;  // written by the attention kernel
-  const long long all = p.c.T * p.Nq;
-  float top = -CUDART_INF_F;
-  for (int i = 0; i < nsplit; ++i) top = fmaxf(top, p.part_lse[i * all + row]);
-  const float base = top == -CUDART_INF_F ? 0.f : top;
-  float sum = 0.f;
-  for (int i = 0; i < nsplit; ++i) sum += exp2f(p.part_lse[i * all + row] - base);
-  const int D = p.c.D, step = 4 << lane_shift;
-  const int first = (int)(lane & ((1 << lane_shift) - 1)) * 4;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int d = first; d < D; d += step) {
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < nsplit; ++i) {
-      const float w = exp2f(p.part_lse[i * all + row] - base) * inv;
-      if (w == 0.f) continue;  // a range without keys for this row holds nothing
-      const float4 f = *reinterpret_cast<const float4*>(p.part_o + (i * all + row) * D + d);
-      o[0] = fmaf(w, f.x, o[0]);
-      o[1] = fmaf(w, f.y, o[1]);
-      o[2] = fmaf(w, f.z, o[2]);
-      o[3] = fmaf(w, f.w, o[3]);
-    }
-    T* dst = static_cast<T*>(p.out) + row * D + d;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dst[e] = from_float<T>(o[e]);
-  }
-  if (p.lse && first == 0) p.lse[row] = (top + log2f(sum)) * kLn2;
-}
-
 template <int D, int BM, bool E4M3>
 cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
                    cudaStream_t stream) {
@@ -322,20 +270,6 @@ cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, lon
                 : launch_dim<16, false>(p, tiles, blocks, stream);
   return e4m3 ? launch_dim<64, true>(p, tiles, blocks, stream)
               : launch_dim<64, false>(p, tiles, blocks, stream);
-}
-
-cudaError_t launch_softmax_combine(const SoftmaxParams& p, int dtype, cudaStream_t stream) {
-  int shift = 0;
-  while (shift < 5 && (4 << shift) < p.c.D) ++shift;
-  const long long lanes = p.c.T * p.Nq << shift;
-  const unsigned grid = (unsigned)((lanes + kThreads - 1) / kThreads);
-  if (dtype == HSTU_F32)
-    softmax_combine_kernel<float><<<grid, kThreads, 0, stream>>>(p, shift);
-  else if (dtype == HSTU_BF16)
-    softmax_combine_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p, shift);
-  else
-    softmax_combine_kernel<__half><<<grid, kThreads, 0, stream>>>(p, shift);
-  return cudaGetLastError();
 }
 
 }  // namespace hstu

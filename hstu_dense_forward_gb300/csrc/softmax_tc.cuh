@@ -7,9 +7,14 @@
 // stays at or below 2^kLazy, which 16-bit weights and fp32 sums hold with the same relative
 // precision, and O (in TMEM) has to be rescaled a few times per row instead of once per tile.
 //
-// One CTA takes one item: a kv head, NQT tiles of up to 128 packed query rows (row r of a tile
-// is token r / G and query head hk * G + r % G, so that the G heads that share keys share their
-// loads) and one range of the keys. Warp roles:
+// An item is a kv head and NQT tiles of up to 128 packed query rows (row r of a tile is token
+// r / G and query head hk * G + r % G, so that the G heads that share keys share their loads),
+// with all the keys that they see. Small numbers of items do not fill the SMs evenly, so then
+// one CTA per SM takes an equal share of all items' key tiles: every CTA computes the same
+// running sum of the items' tiles (plus kItemCost for what an item costs by itself) and works on
+// one contiguous piece of it, which may begin and end inside an item. An item in several pieces
+// leaves its pieces' outputs and sums in the workspace, and a second kernel joins them. With
+// many items each CTA takes one. Warp roles:
 //   warps 0 .. 4 NQT - 1   softmax, one warpgroup per query tile, one thread per row;
 //   next warp              issues every tcgen05.mma; owns TMEM;
 //   next warp              TMA loads: Q, then K and V tiles through one ring, in the order
@@ -64,7 +69,7 @@ struct Cfg {
   static constexpr int KV_CB = KT * SWB, KV_TILE = NCB * KV_CB;
   static constexpr int ST_TILE = KT * D;          // staged E4M3 tile; its row scales (KT bytes)
   // ring depths: what 227 KB of shared memory holds next to Q
-  static constexpr int NSLOT = !E4M3 ? (D == 64 ? 6 : (NQT == 1 && D == 128 ? 6 : 4))
+  static constexpr int NSLOT = !E4M3 ? (D == 64 ? 6 : (NQT == 1 && D == 128 ? 5 : 4))
                                      : (D == 64 ? 4 : (NQT == 1 && D == 128 ? 4 : 3));
   static constexpr int NST = E4M3 ? (D == 64 ? 4 : (NQT == 1 && D == 128 ? 3 : 3)) : 0;
   static constexpr int SM_WARPS = 4 * NQT;
@@ -73,14 +78,15 @@ struct Cfg {
   static constexpr int THREADS = (SM_WARPS + 4 + (E4M3 ? 8 : 0)) * 32;
   // columns of S that a softmax thread holds at a time: a whole row, or (E4M3, whose conversion
   // needs the registers) half of one, which is then loaded twice
-  static constexpr int SC = E4M3 ? KT / 2 : KT;
+  static constexpr int SC = KT / 2;
   // TMEM: score buffers of KT columns (P over them), then O
   static constexpr uint32_t O_COL = NQT * NSB * KT;
   static_assert(O_COL + NQT * D <= kTmemCols, "TMEM");
   static constexpr int OFF_Q = 0, OFF_KV = NQT * Q_TILE, OFF_ST = OFF_KV + NSLOT * KV_TILE;
   static constexpr int OFF_SC = OFF_ST + NST * ST_TILE;  // row scales of the staged tiles
   static constexpr int OFF_BAR = OFF_SC + NST * 128;
-  static constexpr int USED = OFF_BAR + 2048 + 1024;  // (1024: alignment of the base)
+  static constexpr int OFF_PLAN = OFF_BAR + 2048;
+  static constexpr int USED = OFF_PLAN + kPlanSharedBytes + 1024;  // (alignment of the base)
   // one CTA per SM: it takes all of TMEM
   static constexpr int SMEM = USED < 120 * 1024 ? 120 * 1024 : USED;
   static_assert(SMEM <= 232448, "shared memory");
@@ -89,7 +95,7 @@ struct Cfg {
 constexpr int kExpDepth = 8;  // tiles whose exponents are kept (the conversion is fewer ahead)
 
 struct Bars {
-  uint64_t q_ready, exp_full[kExpDepth];
+  uint64_t q_ready, q_empty, o_empty[2], exp_full[kExpDepth];
   float tile_exp[kExpDepth][2];  // EK, EV
   uint64_t q_full, kv_full[6], kv_empty[6], st_full[4], st_empty[4];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;
@@ -98,53 +104,186 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 2048, "barrier block");
 
-// One CTA's work, computed by every thread.
-struct Item {
+// A piece of one item: key tiles [a, b) of it.
+struct Seg {
   PagedSeq s;
-  int b, hk, split, nsplit;
-  int nq;                 // query tiles that hold rows
-  long long tok0;         // first token of tile 0
-  long long k0, kend;     // key range: of the item, and of each tile with the mask
-  long long tile_end[2];
-  int n[2];               // key tiles of each query tile (n[0] <= n[1] when both hold rows)
+  int b, hk;
+  int nq;              // query tiles that hold rows
+  long long tok0;      // first token of tile 0
+  long long k0, kend;  // keys of the piece
+  int n[2];            // key tiles of each query tile (n[0] <= n[1], at most one apart)
   int nmax;
+  int slot;            // workspace slot, or -1: the piece is the whole item
+};
+
+// Key tiles that query tile q (tokens from first) of a sequence sees, counted from key 0.
+template <class C>
+__device__ __forceinline__ int tiles_seen(const SoftmaxParams& p, const PagedSeq& s,
+                                          long long first, int tpt) {
+  long long e = s.Lk;
+  if (p.causal) e = min(e, s.Lk - s.n + min(first + tpt, s.n));
+  return e > 0 ? (int)((e + C::KT - 1) / C::KT) : 0;
+}
+// The same for an item: its last query tile that holds rows sees the most.
+template <class C>
+__device__ __forceinline__ int item_tiles(const SoftmaxParams& p, const PagedSeq& s, int tile) {
+  const int tpt = 128 / p.G;
+  long long first = (long long)tile * C::NQT * tpt;
+  if (C::NQT == 2 && first + tpt < s.n) first += tpt;
+  return tiles_seen<C>(p, s, first, tpt);
+}
+
+template <class C>
+__device__ __forceinline__ void fill_seg(const SoftmaxParams& p, int b, int tile, int hk, int from, int to,
+                         int slot, Seg& g) {
+  const int tpt = 128 / p.G;
+  g.s = paged_seq(p.c, b);
+  g.b = b;
+  g.hk = hk;
+  g.slot = slot;
+  g.tok0 = (long long)tile * C::NQT * tpt;
+  g.k0 = (long long)from * C::KT;
+  g.kend = min(g.s.Lk, (long long)to * C::KT);
+  g.nq = 1;
+  g.n[0] = max(0, min(tiles_seen<C>(p, g.s, g.tok0, tpt), to) - from);
+  g.n[1] = 0;
+  g.nmax = g.n[0];
+  if (C::NQT == 2 && g.tok0 + tpt < g.s.n) {
+    g.nq = 2;
+    g.nmax = g.n[1] = max(0, min(tiles_seen<C>(p, g.s, g.tok0 + tpt, tpt), to) - from);
+  }
+}
+
+// The pieces that this CTA works on, in order. Every role walks them by itself.
+struct Walk {
+  long long u, end;  // units left
+  int e, hk;         // item pair (sequence, tile) and kv head at u
 };
 
 template <class C>
-__device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, Item& it) {
-  const long long blk = blockIdx.x;
-  const int tpt = 128 / p.G;  // tokens of one query tile
-  it.hk = (int)(blk % p.c.Nk);
-  const int tile = tiles - 1 - (int)(blk / p.c.Nk % tiles);  // later tiles see more keys: first
-  it.b = (int)(blk / p.c.Nk / tiles);
-  it.split = blockIdx.y;
-  it.s = paged_seq(p.c, it.b);
-  if (!attn_seq_ok(p, it.s)) {
-    if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
-    return false;
+__device__ __forceinline__ void walk_begin(const SoftmaxParams& p, const PlanTable& pl, Walk& w) {
+  w.u = 0;
+  w.end = 1;  // one item per CTA: one unit
+  w.e = w.hk = 0;
+  if (!p.balanced) return;
+  const int items = pl.items;
+  const long long units = pl.cost[items] * p.c.Nk;
+  const int ctas = share_ctas(units, gridDim.x);
+  w.end = 0;
+  if (units == 0 || (int)blockIdx.x >= ctas) return;
+  w.u = share(units, ctas, blockIdx.x);
+  w.end = share(units, ctas, blockIdx.x + 1);
+  int lo = 0, hi = items;  // the last e with cost[e] Nk <= u
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.cost[mid] * p.c.Nk <= w.u)
+      lo = mid;
+    else
+      hi = mid;
   }
-  const KeyRanges kr = key_ranges(p, it.s.Lk);
-  it.nsplit = kr.count;
-  it.tok0 = (long long)tile * C::NQT * tpt;
-  if (it.tok0 >= it.s.n || it.split >= kr.count) return false;
-  it.k0 = it.split * kr.keys;
-  it.kend = min(it.s.Lk, it.k0 + kr.keys);
-  it.nq = 0;
-  it.nmax = 0;
+  w.e = lo;
+  w.hk = (int)((w.u - pl.cost[lo] * p.c.Nk) / (pl.cost[lo + 1] - pl.cost[lo]));
+}
+
+template <class C>
+__device__ __forceinline__ bool walk_next(const SoftmaxParams& p, const PlanTable& pl, Walk& w,
+                                       int tiles, Seg& g) {
+  if (!p.balanced) {
+    if (w.u) return false;
+    w.u = 1;
+    const long long blk = blockIdx.x;
+    const int tile = tiles - 1 - (int)(blk / p.c.Nk % tiles);  // later tiles see more keys: first
+    const int b = (int)(blk / p.c.Nk / tiles);
+    const PagedSeq s = paged_seq(p.c, b);
+    if (!attn_seq_ok(p, s)) {
+      if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+      return false;
+    }
+    if ((long long)tile * C::NQT * (128 / p.G) >= s.n) return false;
+    fill_seg<C>(p, b, tile, (int)(blk % p.c.Nk), 0, item_tiles<C>(p, s, tile), -1, g);
+    return true;
+  }
+  while (w.u < w.end) {
+    const long long cost = pl.cost[w.e + 1] - pl.cost[w.e];
+    const long long base = pl.cost[w.e] * p.c.Nk + w.hk * cost;
+    const long long o1 = w.u - base, o2 = min(cost, w.end - base);
+    const int n = (int)cost - kItemCost;
+    const KeyTiles k = piece_tiles(o1, o2);
+    const int e = w.e, hk = w.hk;
+    w.u = base + o2;
+    if (o2 == cost && ++w.hk == p.c.Nk) {
+      w.hk = 0;
+      ++w.e;
+    }
+    if (k.to > k.from || (n == 0 && o1 == 0)) {
+      const int b = pl.seq[e];
+      const bool whole = k.from == 0 && k.to == n;
+      fill_seg<C>(p, b, e - pl.first[b], hk, k.from, k.to,
+                  whole ? -1 : 2 * (int)blockIdx.x + (k.from > 0 ? 0 : 1), g);
+      return true;
+    }
+  }
+  return false;
+}
+
+// Inclusive running sums of x[1 .. n] by one warp (x[0] stays).
+template <typename T>
+__device__ void warp_scan(T* x, int n, int lane) {
+  T carry = x[0];
+  for (int base = 1; base <= n; base += 32) {
+    T v = base + lane <= n ? x[base + lane] : T(0);
 #pragma unroll
-  for (int q = 0; q < C::NQT; ++q) {
-    it.n[q] = 0;
-    it.tile_end[q] = it.k0;
-    const long long first = it.tok0 + (long long)q * tpt;
-    if (first >= it.s.n) continue;
-    it.nq = q + 1;
-    long long e = it.kend;
-    if (p.causal) e = min(e, it.s.Lk - it.s.n + min(first + tpt, it.s.n));
-    it.tile_end[q] = e;
-    it.n[q] = e > it.k0 ? (int)((e - it.k0 + C::KT - 1) / C::KT) : 0;
-    it.nmax = it.n[q];
+    for (int d = 1; d < 32; d <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += y;
+    }
+    if (base + lane <= n) x[base + lane] = carry + v;
+    carry += __shfl_sync(0xffffffffu, v, 31);
   }
-  return true;
+}
+
+// The table of items (balanced runs), by the whole CTA; CTA 0 leaves a copy for the kernel that
+// joins pieces. The host has made sure that sequences and items fit.
+template <class C>
+__device__ void make_plan(const SoftmaxParams& p, PlanTable& pl) {
+  const int tid = threadIdx.x, tokens = C::NQT * (128 / p.G);
+  if (tid == 0) {
+    pl.first[0] = 0;
+    pl.cost[0] = 0;
+  }
+  for (int b = tid; b < p.c.B; b += C::THREADS) {
+    const PagedSeq s = paged_seq(p.c, b);
+    const bool ok = attn_seq_ok(p, s);
+    if (!ok) report(p.c, HSTU_DEVERR_OFFSETS);
+    pl.first[b + 1] = ok ? (int)((s.n + tokens - 1) / tokens) : 0;
+  }
+  __syncthreads();
+  if (tid < 32) warp_scan(pl.first, p.c.B, tid);
+  __syncthreads();
+  // (offsets that overlap could name more rows than there are: what does not fit is left out)
+  const int items = min(pl.first[p.c.B], kMaxItems);
+  for (int e = tid; e < items; e += C::THREADS) {
+    int lo = 0, hi = p.c.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pl.first[mid] <= e)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    pl.seq[e] = (uint16_t)lo;
+    pl.cost[e + 1] = kItemCost + item_tiles<C>(p, paged_seq(p.c, lo), e - pl.first[lo]);
+  }
+  __syncthreads();
+  if (tid < 32) warp_scan(pl.cost, items, tid);
+  if (tid == 32) pl.items = items;
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int x = tid; x <= items; x += C::THREADS) p.plan->cost[x] = pl.cost[x];
+    for (int x = tid; x < items; x += C::THREADS) p.plan->seq[x] = pl.seq[x];
+    for (int x = tid; x <= p.c.B; x += C::THREADS) p.plan->first[x] = pl.first[x];
+    if (tid == 0) p.plan->items = items;
+  }
 }
 
 // Place of K and V tiles in the ring's order: the order in which the MMA warp needs them.
@@ -230,64 +369,78 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // ------------------------------------------------------------------ loads
+// Every role takes the CTA's pieces one after the other; its ring places and barrier phases run
+// on (ring: places before the piece, tiles: key tiles before it, and so on).
 template <class C>
-__device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const Item& it,
-                          const CUtensorMap* tq, const CUtensorMap* tc) {
+__device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const PlanTable& pl,
+                          int tiles, const CUtensorMap* tq, const CUtensorMap* tc) {
   const uint32_t sbase = ptx::smem_u32(smem);
-  const int tpt = 128 / p.G;
+  const int tpt = 128 / p.G, ps = 1 << p.c.page_shift;
   const uint32_t q_bytes = (uint32_t)(tpt * p.G) * C::SWB * C::NCB;
-  ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars->q_full), it.nq * q_bytes);
-  for (int q = 0; q < it.nq; ++q)
-#pragma unroll
-    for (int cb = 0; cb < C::NCB; ++cb)
-      ptx::tma_load_3d(sbase + C::OFF_Q + q * C::Q_TILE + cb * C::Q_CB, tq,
-                       ptx::smem_u32(&bars->q_full), cb * C::EPC, it.hk * p.G,
-                       (int)(it.s.t0 + it.tok0 + q * tpt));
-  const int ps = 1 << p.c.page_shift;
   constexpr int DEPTH = C::E4M3 ? C::NST : C::NSLOT;
   uint64_t* full = C::E4M3 ? bars->st_full : bars->kv_full;
   uint64_t* empty = C::E4M3 ? bars->st_empty : bars->kv_empty;
   const int boxes = ps >= C::KT ? 1 : C::KT / 32;
-  for (int i = 0; i < 2 * it.nmax; ++i) {
-    int t;
-    const bool v = ring_tile<C>(i, it.nmax, t);
-    const long long n0 = it.k0 + (long long)t * C::KT;
-    // page ids first: their latency passes while the slot is waited for. Places past the
-    // sequence's last page repeat that page (their rows are masked).
-    long long page[C::KT / 32];
+  uint32_t ring = 0, queries = 0;
+  Walk w;
+  Seg it;
+  walk_begin<C>(p, pl, w);
+  while (walk_next<C>(p, pl, w, tiles, it)) {
+    const int nmax = it.nmax;
+    for (int i = 0; i < 2 * nmax; ++i) {
+      int t;
+      const bool v = ring_tile<C>(i, nmax, t);
+      const long long n0 = it.k0 + (long long)t * C::KT;
+      // page ids first: their latency passes while the slot is waited for. Places past the
+      // sequence's last page repeat that page (their rows are masked).
+      long long page[C::KT / 32];
 #pragma unroll
-    for (int m = 0; m < C::KT / 32; ++m) {
-      if (m >= boxes) break;
-      page[m] = page_at(p.c, it.s, min(n0 + 32 * m, it.s.Lk - 1));
-      if (page[m] < 0) {  // unspecified outputs, but a valid access
-        report(p.c, HSTU_DEVERR_OFFSETS);
-        page[m] = 0;
+      for (int m = 0; m < C::KT / 32; ++m) {
+        if (m >= boxes) break;
+        page[m] = page_at(p.c, it.s, min(n0 + 32 * m, it.s.Lk - 1));
+        if (page[m] < 0) {  // unspecified outputs, but a valid access
+          report(p.c, HSTU_DEVERR_OFFSETS);
+          page[m] = 0;
+        }
+      }
+      const int slot = (ring + i) % DEPTH;
+      if (!wait_bar(p, bars, &empty[slot], (((ring + i) / DEPTH) & 1) ^ 1)) return;
+      const uint32_t bar = ptx::smem_u32(&full[slot]);
+      const bool scales = C::E4M3 && p.c.scale;
+      ptx::mbar_arrive_expect_tx(bar, C::E4M3 ? C::ST_TILE + (scales ? C::KT : 0) : C::KV_TILE);
+      const int row0 = ps >= C::KT ? (int)(n0 & (ps - 1)) : 0;
+#pragma unroll
+      for (int m = 0; m < C::KT / 32; ++m) {
+        if (m >= boxes) break;
+        const int plane = (int)(2 * page[m]) + (v ? 1 : 0);
+        if constexpr (C::E4M3) {
+          ptx::tma_load_4d(sbase + C::OFF_ST + slot * C::ST_TILE + m * 32 * C::D, tc, bar, 0,
+                           it.hk, row0, plane);
+          if (scales)
+            ptx::bulk_load(sbase + C::OFF_SC + slot * 128 + m * 32,
+                           p.c.scale + scale_row(p.c, page[m], v ? 1 : 0, row0, it.hk),
+                           boxes == 1 ? C::KT : 32, bar);
+        } else {
+#pragma unroll
+          for (int cb = 0; cb < C::NCB; ++cb)
+            ptx::tma_load_4d(
+                sbase + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB + m * 32 * C::SWB, tc, bar,
+                cb * C::EPC, it.hk, row0, plane);
+        }
+      }
+      if (i == 0) {  // the piece's queries, once the previous piece's scores are done
+        if (!wait_bar(p, bars, &bars->q_empty, (queries & 1) ^ 1)) return;
+        ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars->q_full), it.nq * q_bytes);
+        for (int q = 0; q < it.nq; ++q)
+#pragma unroll
+          for (int cb = 0; cb < C::NCB; ++cb)
+            ptx::tma_load_3d(sbase + C::OFF_Q + q * C::Q_TILE + cb * C::Q_CB, tq,
+                             ptx::smem_u32(&bars->q_full), cb * C::EPC, it.hk * p.G,
+                             (int)(it.s.t0 + it.tok0 + q * tpt));
+        ++queries;
       }
     }
-    const int slot = i % DEPTH;
-    if (!wait_bar(p, bars, &empty[slot], ((i / DEPTH) & 1) ^ 1)) return;
-    const uint32_t bar = ptx::smem_u32(&full[slot]);
-    const bool scales = C::E4M3 && p.c.scale;
-    ptx::mbar_arrive_expect_tx(bar, C::E4M3 ? C::ST_TILE + (scales ? C::KT : 0) : C::KV_TILE);
-    const int row0 = ps >= C::KT ? (int)(n0 & (ps - 1)) : 0;
-#pragma unroll
-    for (int m = 0; m < C::KT / 32; ++m) {
-      if (m >= boxes) break;
-      const int plane = (int)(2 * page[m]) + (v ? 1 : 0);
-      if constexpr (C::E4M3) {
-        ptx::tma_load_4d(sbase + C::OFF_ST + slot * C::ST_TILE + m * 32 * C::D, tc, bar, 0, it.hk,
-                         row0, plane);
-        if (scales)
-          ptx::bulk_load(sbase + C::OFF_SC + slot * 128 + m * 32,
-                         p.c.scale + scale_row(p.c, page[m], v ? 1 : 0, row0, it.hk),
-                         boxes == 1 ? C::KT : 32, bar);
-      } else {
-#pragma unroll
-        for (int cb = 0; cb < C::NCB; ++cb)
-          ptx::tma_load_4d(sbase + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB + m * 32 * C::SWB,
-                           tc, bar, cb * C::EPC, it.hk, row0, plane);
-      }
-    }
+    ring += 2 * nmax;
   }
 }
 
@@ -295,8 +448,8 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
 // A thread converts sixteen codes of a row at a time. Rows beyond the sequence become zeros
 // (what an unused row of a page holds, NaN included, does not reach the products).
 template <class C>
-__device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, const Item& it,
-                             bool values, int warp, int lane) {
+__device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
+                             const PlanTable& pl, int tiles, bool values, int warp, int lane) {
   constexpr int CPR = C::D / 16;  // chunks of a row
   constexpr int STEP = 128 / CPR, PASSES = C::KT / STEP;  // rows of one pass of the four warps
   constexpr int RPW = 32 / CPR;  // rows of one pass of a warp
@@ -304,60 +457,69 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
   // the row whose factor this lane holds for its warp (PASSES of RPW rows, 32 at most)
   const int my_row = warp * RPW + lane % RPW + STEP * (lane / RPW % PASSES);
   const int cb = chunk / 4, c16 = (chunk % 4) * 2;  // column block, first 16-byte piece in it
-  for (int i = 0; i < 2 * it.nmax; ++i) {
-    int t;
-    if (ring_tile<C>(i, it.nmax, t) != values) continue;
-    const int have = (int)min((long long)C::KT, it.s.Lk - it.k0 - (long long)t * C::KT);
-    const int st = i % C::NST, slot = i % C::NSLOT;
-    if (!warp_wait(p, bars, &bars->st_full[st], (i / C::NST) & 1)) return;
-    const uint8_t* scale = smem + C::OFF_SC + st * 128;
-    int top = 127;  // the largest scale of the tile's rows
-    if (p.c.scale) {
-      uint32_t s4 = 0;
-      if (lane * 4 < C::KT) s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-      top = 0;
+  uint32_t ring = 0, done = 0;
+  Walk walk;
+  Seg it;
+  walk_begin<C>(p, pl, walk);
+  while (walk_next<C>(p, pl, walk, tiles, it)) {
+    for (int x = 0; x < 2 * it.nmax; ++x) {
+      int t;
+      if (ring_tile<C>(x, it.nmax, t) != values) continue;
+      const uint32_t i = ring + x, te = (done + t) % kExpDepth;
+      const int have = (int)min((long long)C::KT, it.s.Lk - it.k0 - (long long)t * C::KT);
+      const int st = i % C::NST, slot = i % C::NSLOT;
+      if (!warp_wait(p, bars, &bars->st_full[st], (i / C::NST) & 1)) return;
+      const uint8_t* scale = smem + C::OFF_SC + st * 128;
+      int top = 127;  // the largest scale of the tile's rows
+      if (p.c.scale) {
+        uint32_t s4 = 0;
+        if (lane * 4 < C::KT) s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
+        top = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (lane * 4 + e < have) top = max(top, (int)((s4 >> (8 * e)) & 0xffu));
+        for (int e = 0; e < 4; ++e)
+          if (lane * 4 + e < have) top = max(top, (int)((s4 >> (8 * e)) & 0xffu));
 #pragma unroll
-      for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    }
-    if (warp == 0 && lane == 0) {
-      bars->tile_exp[t % kExpDepth][values ? 1 : 0] = (float)(top - 127);
-      ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[t % kExpDepth]));
-    }
-    const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
-    uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
-    uint32_t mine = 0x3c003c00u;  // factor of row my_row, twice (0 beyond the sequence)
-    if (p.c.scale) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
-    if (my_row >= have) mine = 0u;
-    uint4 u[PASSES];
-#pragma unroll
-    for (int k = 0; k < PASSES; ++k) {
-      u[k] = *reinterpret_cast<const uint4*>(src + (r0 + STEP * k) * C::D);
-      if (r0 + STEP * k >= have) u[k] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
-#pragma unroll
-    for (int k = 0; k < PASSES; ++k) {
-      const int r = r0 + STEP * k;
-      const uint32_t in[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-      const uint32_t f = __shfl_sync(0xffffffffu, mine, lane / CPR + RPW * k);
-      uint32_t w[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        e4m3x4_to_f16x2(in[e], w[2 * e], w[2 * e + 1]);
-        w[2 * e] = mul_f16x2(w[2 * e], f);
-        w[2 * e + 1] = mul_f16x2(w[2 * e + 1], f);
+        for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
       }
-      uint8_t* row = dst + r * C::SWB;
-      *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (r & 7)) * 16)) =
-          make_uint4(w[4], w[5], w[6], w[7]);
+      if (warp == 0 && lane == 0) {
+        bars->tile_exp[te][values ? 1 : 0] = (float)(top - 127);
+        ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[te]));
+      }
+      const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
+      uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
+      uint32_t mine = 0x3c003c00u;  // factor of row my_row, twice (0 beyond the sequence)
+      if (p.c.scale) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
+      if (my_row >= have) mine = 0u;
+      uint4 u[PASSES];
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k) {
+        u[k] = *reinterpret_cast<const uint4*>(src + (r0 + STEP * k) * C::D);
+        if (r0 + STEP * k >= have) u[k] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k) {
+        const int r = r0 + STEP * k;
+        const uint32_t in[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        const uint32_t f = __shfl_sync(0xffffffffu, mine, lane / CPR + RPW * k);
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          e4m3x4_to_f16x2(in[e], w[2 * e], w[2 * e + 1]);
+          w[2 * e] = mul_f16x2(w[2 * e], f);
+          w[2 * e + 1] = mul_f16x2(w[2 * e + 1], f);
+        }
+        uint8_t* row = dst + r * C::SWB;
+        *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (r & 7)) * 16)) =
+            make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(ptx::smem_u32(&bars->kv_full[slot]));
+      ptx::mbar_arrive(ptx::smem_u32(&bars->st_empty[st]));
     }
-    ptx::fence_proxy_async_smem();
-    ptx::mbar_arrive(ptx::smem_u32(&bars->kv_full[slot]));
-    ptx::mbar_arrive(ptx::smem_u32(&bars->st_empty[st]));
+    ring += 2 * it.nmax;
+    done += it.nmax;
   }
 }
 
@@ -400,16 +562,17 @@ struct Issuer {
   static constexpr uint32_t IDESC_S = ptx::idesc_f16(AB, 128, C::KT, 0);
   static constexpr uint32_t IDESC_O = ptx::idesc_f16(AB, 128, C::D, 1);
 
-  __device__ bool kv_ready(int i) {
+  // (i: ring place, running on over the pieces)
+  __device__ bool kv_ready(uint32_t i) {
     if (!wait_bar(p, bars, &bars->kv_full[i % C::NSLOT], (i / C::NSLOT) & 1)) return false;
     ptx::tc_fence_after();
     return true;
   }
-  __device__ void kv_release(int i) {
+  __device__ void kv_release(uint32_t i) {
     ptx::mma_commit(ptx::smem_u32(&bars->kv_empty[i % C::NSLOT]));
   }
   // scores of query tile q into buffer sb, K at ring place i
-  __device__ void scores(int q, int sb, int i) {
+  __device__ void scores(int q, int sb, uint32_t i) {
     const uint64_t ad0 = ptx::smem_desc(sbase + C::OFF_Q + q * C::Q_TILE, 16, 8 * C::SWB, 2);
     const uint64_t bd0 =
         ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, 16, 8 * C::SWB, 2);
@@ -423,7 +586,7 @@ struct Issuer {
   }
   // O of query tile q += P (over score buffer sb) V at ring place i, for one half of the keys:
   // the first half's product runs while the second half's weights are computed
-  __device__ void accumulate(int q, int sb, int i, int half, bool first) {
+  __device__ void accumulate(int q, int sb, uint32_t i, int half, bool first) {
     const uint64_t bd0 =
         ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, C::KV_CB, 8 * C::SWB, 2);
 #pragma unroll
@@ -434,7 +597,7 @@ struct Issuer {
     }
   }
   // The same for both halves as P (phase `par` of its barriers) and V arrive.
-  __device__ bool weighted_sum(int q, int sb, uint32_t par, int i, bool first) {
+  __device__ bool weighted_sum(int q, int sb, uint32_t par, uint32_t i, bool first) {
     if (!kv_ready(i) || !wait_bar(p, bars, &bars->p_half[sb], par)) return false;
     ptx::tc_fence_after();
     accumulate(q, sb, i, 0, first);
@@ -447,33 +610,66 @@ struct Issuer {
 };
 
 template <class C, bool BF16>
-__device__ bool mma_loop(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars, const Item& it) {
-  if (!wait_bar(p, bars, BF16 && C::E4M3 ? &bars->q_ready : &bars->q_full, 0)) return false;
-  ptx::tc_fence_after();
-  const int n = it.nmax;
-  // scores of the first NSB tiles
-  for (int t = 0; t < C::NSB && t < n; ++t) {
-    if (!is.kv_ready(k_index<C>(t))) return false;
-    for (int q = 0; q < it.nq; ++q)
-      if (t < it.n[q]) is.scores(q, C::NQT == 1 ? t : q, k_index<C>(t));
-    is.kv_release(k_index<C>(t));
-  }
-  // Then per tile and query tile: O += P(t) V, and the scores of tile t + NSB over P(t), which
-  // that product must have read. With two query tiles the softmax of one runs meanwhile.
-  for (int t = 0; t < n; ++t) {
-    const int vi = v_index<C>(t, n), ki = k_index<C>(t + C::NSB);
+__device__ bool mma_loop(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars,
+                         const PlanTable& pl, int tiles) {
+  uint32_t ring = 0, queries = 0;
+  uint32_t g[2] = {0, 0};        // key tiles of each query tile before the piece
+  uint32_t outputs[2] = {0, 0};  // pieces of it that had any
+  Walk w;
+  Seg it;
+  walk_begin<C>(p, pl, w);
+  while (walk_next<C>(p, pl, w, tiles, it)) {
+    const int n = it.nmax;
+    if (n == 0) continue;
+    const int nq[2] = {it.n[0], C::NQT == 2 ? it.n[1] : 0};
+    if (!wait_bar(p, bars, BF16 && C::E4M3 ? &bars->q_ready : &bars->q_full, queries & 1))
+      return false;
+    ptx::tc_fence_after();
+    ++queries;
+    // Scores of the first NSB tiles, over weights of the piece before: its last product must be
+    // done. (Those before it are: the softmax hands over a piece's last weights only then, so
+    // that this wait, too, cannot take one phase for another.)
+    for (int t = 0; t < C::NSB && t < n; ++t) {
+      if (!is.kv_ready(ring + k_index<C>(t))) return false;
 #pragma unroll
-    for (int q = 0; q < C::NQT; ++q) {
-      if (t >= it.n[q]) continue;
-      const int sb = C::NQT == 1 ? t & 1 : q;
-      if (!is.weighted_sum(q, sb, C::NQT == 1 ? (t >> 1) & 1 : t & 1, vi, t == 0)) return false;
-      if (t + C::NSB < it.n[q]) {
-        if (!is.kv_ready(ki) || !wait_bar(p, bars, &bars->pv_done[q], t & 1)) return false;
-        is.scores(q, sb, ki);
+      for (int q = 0; q < C::NQT; ++q) {
+        if (t >= nq[q]) continue;
+        const uint32_t gt = g[q] + t;
+        if (t == 0 && gt > 0) {
+          if (!wait_bar(p, bars, &bars->pv_done[q], (gt - 1) & 1)) return false;
+          ptx::tc_fence_after();
+        }
+        is.scores(q, C::NQT == 1 ? gt & 1 : q, ring + k_index<C>(t));
+      }
+      is.kv_release(ring + k_index<C>(t));
+    }
+    if (n <= C::NSB) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
+    // Then per tile and query tile: O += P(t) V, and the scores of tile t + NSB over P(t), which
+    // that product must have read. With two query tiles the softmax of one runs meanwhile.
+    for (int t = 0; t < n; ++t) {
+      const uint32_t vi = ring + v_index<C>(t, n), ki = ring + k_index<C>(t + C::NSB);
+#pragma unroll
+      for (int q = 0; q < C::NQT; ++q) {
+        if (t >= nq[q]) continue;
+        const uint32_t gt = g[q] + t;
+        const int sb = C::NQT == 1 ? gt & 1 : q;
+        // the piece's first product overwrites O: the previous output has been read
+        if (t == 0 && !wait_bar(p, bars, &bars->o_empty[q], (outputs[q]++ & 1) ^ 1)) return false;
+        if (!is.weighted_sum(q, sb, C::NQT == 1 ? (gt >> 1) & 1 : gt & 1, vi, t == 0)) return false;
+        if (t + C::NSB < nq[q]) {
+          if (!is.kv_ready(ki) || !wait_bar(p, bars, &bars->pv_done[q], gt & 1)) return false;
+          is.scores(q, sb, ki);
+        }
+      }
+      is.kv_release(vi);
+      if (t + C::NSB < n) {
+        is.kv_release(ki);
+        if (t + C::NSB + 1 == n) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
       }
     }
-    is.kv_release(vi);
-    if (t + C::NSB < n) is.kv_release(ki);
+    ring += 2 * n;
+    g[0] += nq[0];
+    g[1] += nq[1];
   }
   return true;
 }
@@ -494,215 +690,212 @@ __device__ __forceinline__ void mma_drain(const SoftmaxParams& p, Bars* bars) {
 // ------------------------------------------------------------------ softmax
 template <class C, bool BF16>
 __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, uint32_t tmem,
-                             const Item& it, int q, int warp, int lane) {
+                             const PlanTable& pl, int tiles, int q, int warp, int lane) {
   constexpr int KT = C::KT;
   const int r = (warp & 3) * 32 + lane;  // row of the tile, TMEM lane
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int tpt = 128 / p.G;
-  const long long tok = it.tok0 + (long long)q * tpt + r / p.G;
-  const bool valid = r < tpt * p.G && tok < it.s.n;
-  const bool any = __any_sync(0xffffffffu, valid);
-  // keys that the row sees: positions [k0, k0 + lim); rows without a token follow the widest
-  long long see = it.kend;
-  if (p.causal && valid) see = min(see, it.s.Lk - it.s.n + tok + 1);
-  const int lim = (int)max(see - it.k0, 0ll);
-  const int n = it.n[q];
-  float fk = p.scale_log2, fv = 1.0f;  // static factors fold into the scale and the output
-  if (C::E4M3 && p.c.k_ds) {
-    fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
-    fv = p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
-  }
-  if constexpr (BF16 && C::E4M3) {
-    if (n > 0 || it.nmax > 0) {  // (the loads and products run for the CTA's widest tile)
-      if (!warp_wait(p, bars, &bars->q_full, 0)) return;
+  const uint32_t o_col = tmem + lane_off + C::O_COL + q * C::D;
+  uint32_t ring = 0, queries = 0, done = 0;  // places, pieces with keys, key tiles before this one
+  uint32_t g = 0;                            // key tiles of this query tile before this piece
+  Walk walk;
+  Seg it;
+  walk_begin<C>(p, pl, walk);
+  for (; walk_next<C>(p, pl, walk, tiles, it); ring += 2 * it.nmax, done += it.nmax) {
+    float fk = p.scale_log2, fv = 1.0f;  // static factors fold into the scale and the output
+    const long long tok = it.tok0 + (long long)q * tpt + r / p.G;
+    const bool valid = q < it.nq && r < tpt * p.G && tok < it.s.n;
+    const bool any = __any_sync(0xffffffffu, valid);
+    if (C::E4M3 && p.c.k_ds) {
+      fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
+      fv = p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
+    }
+    if (BF16 && C::E4M3 && it.nmax > 0) {  // (a warpgroup without rows of the piece arrives, too)
+      if (!warp_wait(p, bars, &bars->q_full, queries++ & 1)) return;
       if (valid) fk *= query_to_half<C>(smem + C::OFF_Q + q * C::Q_TILE, r);
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready));
     }
-  }
-  float m = -CUDART_INF_F, l = 0.0f;
-  const uint32_t o_col = tmem + lane_off + C::O_COL + q * C::D;
-  for (int t = 0; t < n; ++t) {
-    const int sb = C::NQT == 1 ? (t & 1) : q;
-    const uint32_t par = C::NQT == 1 ? (t >> 1) & 1 : t & 1;
-    float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
-    if constexpr (C::E4M3) {
-      if (!warp_wait(p, bars, &bars->exp_full[t % kExpDepth], (t / kExpDepth) & 1)) return;
-      ek = power2((int)bars->tile_exp[t % kExpDepth][0]);
-      ev = bars->tile_exp[t % kExpDepth][1];
-    }
-    if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
-    ptx::tc_fence_after();
-    const uint32_t s_col = tmem + lane_off + sb * KT;
-    constexpr int NC = C::SC / 32;  // chunks held at a time
-    uint32_t sv[NC][32];
-    float neg = 0.0f;
-    const int left = lim - t * KT;  // keys of the tile that the row sees
-    const bool masked = !__all_sync(0xffffffffu, left >= KT);
-    // columns [c0, c0 + SC) of S: masked scores are -inf; with a negative static factor all
-    // change sign (the largest score has the smallest product), and -inf stays
-    auto load_scores = [&](int c0) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) ptx::tmem_ld32_issue(s_col + c0 + c * 32, sv[c]);
-      ptx::tmem_ld_wait(sv[0]);
-#pragma unroll
-      for (int c = 1; c < NC; ++c) ptx::reg_fence(sv[c]);
-      if (C::E4M3 && fk < 0.0f) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) sv[c][e] ^= 0x80000000u;
+    if (q >= it.nq) continue;
+    // keys that the row sees: positions [k0, k0 + lim); rows without a token follow the widest
+    long long see = it.kend;
+    if (p.causal && valid) see = min(see, it.s.Lk - it.s.n + tok + 1);
+    const int lim = (int)max(see - it.k0, 0ll);
+    const int n = C::NQT == 2 && q ? it.n[1] : it.n[0];
+    const int rest = (int)min(it.s.Lk - it.k0, 0x7fffffffll);  // keys of the sequence from k0 on
+    float m = -CUDART_INF_F, l = 0.0f;
+    for (int t = 0; t < n; ++t, ++g) {
+      const int sb = C::NQT == 1 ? (g & 1) : q;
+      const uint32_t par = C::NQT == 1 ? (g >> 1) & 1 : g & 1;
+      float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
+      if constexpr (C::E4M3) {
+        const uint32_t te = done + t;
+        if (!warp_wait(p, bars, &bars->exp_full[te % kExpDepth], (te / kExpDepth) & 1)) return;
+        ek = power2((int)bars->tile_exp[te % kExpDepth][0]);
+        ev = bars->tile_exp[te % kExpDepth][1];
       }
-      if (masked) {
+      if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
+      ptx::tc_fence_after();
+      const uint32_t s_col = tmem + lane_off + sb * KT;
+      constexpr int NC = C::SC / 32;  // chunks held at a time
+      uint32_t sv[NC][32];
+      float neg = 0.0f;
+      const int left = lim - t * KT;  // keys of the tile that the row sees
+      const bool masked = !__all_sync(0xffffffffu, left >= KT);
+      // columns [c0, c0 + SC) of S: masked scores are -inf; with a negative static factor all
+      // change sign (the largest score has the smallest product), and -inf stays
+      auto load_scores = [&](int c0) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c) ptx::tmem_ld32_issue(s_col + c0 + c * 32, sv[c]);
+        ptx::tmem_ld_wait(sv[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c0 + c * 32 + e >= left) sv[c][e] = 0xff800000u;
-      }
-    };
-    if (any) {
-      float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll 1
-      for (int c0 = 0; c0 < KT; c0 += C::SC) {
-        load_scores(c0);
+        for (int c = 1; c < NC; ++c) ptx::reg_fence(sv[c]);
+        if (C::E4M3 && fk < 0.0f) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            top[(e >> 1) & 3] = ptx::max3(top[(e >> 1) & 3], __uint_as_float(sv[c][e]),
-                                          __uint_as_float(sv[c][e + 1]));
-      }
-      const float mx =
-          fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fabsf(fk) * ek, ev);
-      // raise the reference: at the first visible key, and when weights would pass 2^kLazy
-      const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
-      if (__any_sync(0xffffffffu, raise)) {
-        const float corr = raise ? ex2(m - mx) : 1.0f;  // (0 at the first visible key)
-        if (raise) {
-          m = mx;
-          l *= corr;
+            for (int e = 0; e < 32; ++e) sv[c][e] ^= 0x80000000u;
         }
-        if (t > 0) {  // (S(t) was issued after PV(t - 2) was done: this phase is the next one)
-          if (!warp_wait(p, bars, &bars->pv_done[q], (t - 1) & 1)) return;
-          ptx::tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < C::D; c += 16) {
-            uint32_t o[16];
-            ptx::tmem_ld16(o_col + c, o);
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            ptx::tmem_st16(o_col + c, o);
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + c * 32 + e >= left) sv[c][e] = 0xff800000u;
+        }
+      };
+      if (any) {
+        float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+        for (int c0 = 0; c0 < KT; c0 += C::SC) {
+          load_scores(c0);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              top[(e >> 1) & 3] = ptx::max3(top[(e >> 1) & 3], __uint_as_float(sv[c][e]),
+                                            __uint_as_float(sv[c][e + 1]));
+        }
+        const float mx =
+            fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fabsf(fk) * ek, ev);
+        // raise the reference: at the first visible key, and when weights would pass 2^kLazy
+        const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
+        if (__any_sync(0xffffffffu, raise)) {
+          const float corr = raise ? ex2(m - mx) : 1.0f;  // (0 at the first visible key)
+          if (raise) {
+            m = mx;
+            l *= corr;
+          }
+          if (t > 0) {  // (S(t) was issued after PV(t - 2) was done: this phase is the next one)
+            if (!warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1)) return;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < C::D; c += 16) {
+              uint32_t o[16];
+              ptx::tmem_ld16(o_col + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              ptx::tmem_st16(o_col + c, o);
+            }
           }
         }
+        neg = m == -CUDART_INF_F ? 0.0f : ev - m;
       }
-      neg = m == -CUDART_INF_F ? 0.0f : ev - m;
-    }
-    if constexpr (!C::E4M3) {
-      // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
-      const long long n0 = it.k0 + (long long)t * KT;
-      const int have = (int)min((long long)KT, it.s.Lk - n0);
-      if (have < KT) {
-        const int vi = v_index<C>(t, it.nmax);
-        if (!warp_wait(p, bars, &bars->kv_full[vi % C::NSLOT], (vi / C::NSLOT) & 1)) return;
-        uint8_t* v = smem + C::OFF_KV + (vi % C::NSLOT) * C::KV_TILE;
-        const int pieces = (KT - have) * (C::SWB / 16);  // of one column block
-        for (int x = r; x < C::NCB * pieces; x += 128)
-          *reinterpret_cast<uint4*>(v + (x / pieces) * C::KV_CB + have * C::SWB +
-                                    (x % pieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        ptx::fence_proxy_async_smem();
+      if constexpr (!C::E4M3) {
+        // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
+        const int have = rest - t * KT;
+        if (have < KT) {
+          const uint32_t vi = ring + v_index<C>(t, it.nmax);
+          if (!warp_wait(p, bars, &bars->kv_full[vi % C::NSLOT], (vi / C::NSLOT) & 1)) return;
+          uint8_t* v = smem + C::OFF_KV + (vi % C::NSLOT) * C::KV_TILE;
+          const int pieces = (KT - have) * (C::SWB / 16);  // of one column block
+          for (int x = r; x < C::NCB * pieces; x += 128)
+            *reinterpret_cast<uint4*>(v + (x / pieces) * C::KV_CB + have * C::SWB +
+                                      (x % pieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          ptx::fence_proxy_async_smem();
+        }
       }
-    }
-    float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    const float fa = fabsf(fk) * ek;
-    // weights of chunk `at` held in sv[i], summed and stored as columns of P
-    auto weights = [&](int i, int at) {
-      uint32_t pk[16];
+      float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      const float fa = fabsf(fk) * ek;
+      // weights of chunk `at` held in sv[i], summed and stored as columns of P
+      auto weights = [&](int i, int at) {
+        uint32_t pk[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float x0, x1;
-        ptx::fma_f32x2(x0, x1, __uint_as_float(sv[i][2 * e]), __uint_as_float(sv[i][2 * e + 1]),
-                       fa, fa, neg, neg);
-        const float p0 = ex2(x0), p1 = ex2(x1);
-        ptx::add_f32x2(sum[e & 1][0], sum[e & 1][1], p0, p1);
-        pk[e] = pack2<BF16 && !C::E4M3>(p0, p1);
-      }
-      ptx::tmem_st16(s_col + at * 16, pk);
-    };
-    auto half_done = [&](int half) {
-      if (any) ptx::tmem_st_wait();
-      if (half == 0) {
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
-      }
-    };
-    if constexpr (C::SC < KT) {  // (a rolled loop: five warps' roles share the instruction cache)
+        for (int e = 0; e < 16; ++e) {
+          float x0, x1;
+          ptx::fma_f32x2(x0, x1, __uint_as_float(sv[i][2 * e]), __uint_as_float(sv[i][2 * e + 1]),
+                         fa, fa, neg, neg);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          ptx::add_f32x2(sum[e & 1][0], sum[e & 1][1], p0, p1);
+          pk[e] = pack2<BF16 && !C::E4M3>(p0, p1);
+        }
+        ptx::tmem_st16(s_col + at * 16, pk);
+      };
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         if (any) {
           load_scores(half * C::SC);
 #pragma unroll
           for (int c = 0; c < NC; ++c) weights(c, half * NC + c);
+          ptx::tmem_st_wait();
         }
-        half_done(half);
-      }
-    } else {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (any) {
-#pragma unroll
-          for (int c = half * (NC / 2); c < (half + 1) * (NC / 2); ++c) weights(c, c);
+        if (half == 0) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
         }
-        half_done(half);
       }
+      const float tile_sum = (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
+      l = C::E4M3 ? fmaf(tile_sum, power2(-(int)ev), l) : l + tile_sum;
+      // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
+      // below needs PV(n - 2) to be done (of the piece before, it is); S(n - 1) was issued after
+      // PV(n - 1 - NSB) only, and once P(n - 1) is handed over both may complete at any time.
+      if (C::NSB > 1 && t > 0 && t == n - 1 &&
+          !warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1))
+        return;
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
     }
-    const float tile_sum = (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
-    l = C::E4M3 ? fmaf(tile_sum, power2(-(int)ev), l) : l + tile_sum;
-    // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
-    // below needs PV(n - 2) to be done; S(n - 1) was issued after PV(n - 1 - NSB) only, and
-    // once P(n - 1) is handed over both may complete at any time.
-    if (C::NSB > 1 && t > 0 && t == n - 1 &&
-        !warp_wait(p, bars, &bars->pv_done[q], (t - 1) & 1))
-      return;
-    ptx::tc_fence_before();
-    ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
-  }
-  if (n > 0) {
-    if (!warp_wait(p, bars, &bars->pv_done[q], (n - 1) & 1)) return;
-    ptx::tc_fence_after();
-  }
-  if (!any) return;
-  const long long row = (it.s.t0 + tok) * p.Nq + it.hk * p.G + r % p.G;  // of out and lse
-  const float inv = l > 0.0f ? fv / l : l;  // (a NaN sum stays one)
-  const int D = p.c.D;
-#pragma unroll 1
-  for (int c = 0; c < C::D; c += 16) {
-    if (c >= D) break;
-    uint32_t o[16];
     if (n > 0) {
-      ptx::tmem_ld16(o_col + c, o);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = 0u;
+      if (!warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1)) return;
+      ptx::tc_fence_after();
     }
-    if (!valid) continue;
-    float f[16];
+    // out and lse of the row, or its place in the workspace
+    const long long row = (it.s.t0 + tok) * p.Nq + it.hk * p.G + r % p.G;
+    const long long part = (long long)it.slot * (C::NQT * 128) + q * 128 + r;
+    const float inv = l > 0.0f ? fv / l : l;  // (a NaN sum stays one)
+    const int D = p.c.D;
+#pragma unroll 1
+    for (int c = 0; any && c < D; c += 16) {
+      uint32_t o[16];
+      if (n > 0) {
+        ptx::tmem_ld16(o_col + c, o);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
-    if (it.nsplit > 1) {
-      store16(p.part_o + ((long long)it.split * p.c.T * p.Nq + row) * D + c, f);
-    } else if constexpr (BF16) {
-      store16(static_cast<__nv_bfloat16*>(p.out) + row * D + c, f);
-    } else {
-      store16(static_cast<__half*>(p.out) + row * D + c, f);
+        for (int e = 0; e < 16; ++e) o[e] = 0u;
+      }
+      if (!valid) continue;
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+      if (it.slot >= 0) {
+        store16(p.part_o + part * D + c, f);
+      } else if constexpr (BF16) {
+        store16(static_cast<__nv_bfloat16*>(p.out) + row * D + c, f);
+      } else {
+        store16(static_cast<__half*>(p.out) + row * D + c, f);
+      }
     }
-  }
-  if (valid) {
-    const float log2sum = l == 0.0f ? -CUDART_INF_F : m + log2f(l);
-    if (it.nsplit > 1)
-      p.part_lse[(long long)it.split * p.c.T * p.Nq + row] = log2sum;
-    else if (p.lse)
-      p.lse[row] = log2sum * kLn2;
+    if (valid) {
+      const float log2sum = l == 0.0f ? -CUDART_INF_F : m + log2f(l);
+      if (it.slot >= 0)
+        p.part_lse[part] = log2sum;
+      else if (p.lse)
+        p.lse[row] = log2sum * kLn2;
+    }
+    if (n > 0) {  // O has been read: the next piece's products may overwrite it
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(ptx::smem_u32(&bars->o_empty[q]));
+    }
   }
 }
 
@@ -714,16 +907,16 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
                       int tiles) {
   using C = Cfg<D, NQT, E4M3>;
   extern __shared__ uint8_t smem_raw[];
-  Item it;
-  if (!make_item<C>(p, tiles, it)) return;  // (the whole CTA)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  PlanTable& pl = *reinterpret_cast<PlanTable*>(smem + C::OFF_PLAN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == C::LOAD_WARP && lane == 0) {
     ptx::mbar_init(ptx::smem_u32(&bars->q_full), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->q_empty), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
-    ptx::mbar_init(ptx::smem_u32(&bars->q_ready), it.nq * 128);
+    ptx::mbar_init(ptx::smem_u32(&bars->q_ready), C::NQT * 128);
     for (int s = 0; s < kExpDepth; ++s) ptx::mbar_init(ptx::smem_u32(&bars->exp_full[s]), 2);
     for (int s = 0; s < 6; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), C::E4M3 ? 128 : 1);
@@ -738,6 +931,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
       ptx::mbar_init(ptx::smem_u32(&bars->p_half[s]), 128);
       ptx::mbar_init(ptx::smem_u32(&bars->p_full[s]), 128);
       ptx::mbar_init(ptx::smem_u32(&bars->pv_done[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->o_empty[s]), 128);
     }
     bars->abort = 0;
     ptx::fence_barrier_init();
@@ -747,33 +941,42 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), kTmemCols);
     ptx::tmem_relinquish();
   }
+  if (p.balanced) {
+    make_plan<C>(p, pl);
+    if (threadIdx.x == 0) {  // for the kernel that joins pieces
+      Walk w;
+      walk_begin<C>(p, pl, w);
+      p.plan->begin_item[blockIdx.x] = w.e;
+      p.plan->begin_head[blockIdx.x] = w.hk;
+    }
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // The softmax keeps scores in registers: with two warpgroups of it the launch's registers are
-  // dealt out anew. 384 threads launch with 168 each (64,512): 208 for the softmax and 72 for the
-  // control warps are 62,464. 640 (E4M3) launch with 96 (61,440): 112 and 80 are 59,392.
-  if constexpr (C::NQT == 2) {
+  // With E4M3's conversion warps the launch leaves the softmax too few registers. 512 threads
+  // launch with 128 each (65,536): 208 for its warps and 96 for the others are 63,488. 640 launch
+  // with 96 (61,440): 136 and 64 are 59,392.
+  if constexpr (C::E4M3) {
     if (warp < C::SM_WARPS)
-      ptx::regs_inc<C::E4M3 ? 112 : 208>();
+      ptx::regs_inc<C::NQT == 2 ? 120 : 208>();
     else
-      ptx::regs_dec<C::E4M3 ? 80 : 72>();
+      ptx::regs_dec<C::NQT == 2 ? 80 : 96>();
   }
   if (warp < C::SM_WARPS) {
-    if (warp / 4 < it.nq) softmax_role<C, BF16>(p, bars, smem, tmem, it, warp / 4, warp, lane);
+    softmax_role<C, BF16>(p, bars, smem, tmem, pl, tiles, warp / 4, warp, lane);
   } else if (warp == C::MMA_WARP) {
-    if (lane == 0 && it.nmax > 0) {
+    if (lane == 0) {
       Issuer<C, BF16> is{p, bars, ptx::smem_u32(smem), tmem};
-      mma_loop<C, BF16>(p, is, bars, it);
+      mma_loop<C, BF16>(p, is, bars, pl, tiles);
       mma_drain(p, bars);
     }
   } else if (warp == C::LOAD_WARP) {
-    if (lane == 0 && it.nmax > 0) load_role<C>(p, bars, smem, it, &tm_q, &tm_c);
+    if (lane == 0) load_role<C>(p, bars, smem, pl, tiles, &tm_q, &tm_c);
   } else if (C::E4M3 && warp >= C::CONV_WARP) {
     const int w = warp - C::CONV_WARP;
-    convert_role<C>(p, bars, smem, it, w >= 4, w & 3, lane);
+    convert_role<C>(p, bars, smem, pl, tiles, w >= 4, w & 3, lane);
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -799,7 +1002,7 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const 
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3((unsigned)blocks, p.splits), C::THREADS, C::SMEM, stream>>>(tq, tc, p, (int)tiles);
+  kernel<<<dim3((unsigned)blocks), C::THREADS, C::SMEM, stream>>>(tq, tc, p, (int)tiles);
   return cudaGetLastError();
 }
 

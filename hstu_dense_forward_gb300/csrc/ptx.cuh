@@ -83,6 +83,46 @@ __device__ __forceinline__ uint32_t mbar_test2(uint32_t bar_a, uint32_t par_a, u
   return ra | (rb << 1);
 }
 
+// Non-blocking tests of several barriers (bit i: barrier i), issued together: one after the other
+// each would wait for its predecessor's answer.
+__device__ __forceinline__ uint32_t mbar_tests(uint32_t b0, uint32_t p0, uint32_t b1,
+                                               uint32_t p1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 x;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 x, 2, 0, q;\n\t"
+      "or.b32 %0, %0, x;\n\t}"
+      : "=&r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ uint32_t mbar_tests(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1,
+                                               uint32_t b2, uint32_t p2, uint32_t b3,
+                                               uint32_t p3) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q, r, s;\n\t.reg .b32 x, y, z;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 s, [%7], %8;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 x, 2, 0, q;\n\t"
+      "selp.u32 y, 4, 0, r;\n\t"
+      "selp.u32 z, 8, 0, s;\n\t"
+      "or.b32 %0, %0, x;\n\t"
+      "or.b32 y, y, z;\n\t"
+      "or.b32 %0, %0, y;\n\t}"
+      : "=&r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2), "r"(b3), "r"(p3)
+      : "memory");
+  return ok;
+}
+
 // Blocking form: the thread is suspended until the phase completes or `ns`
 // nanoseconds pass, instead of spinning on the shared-memory pipe.
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t ns) {
@@ -304,6 +344,17 @@ __device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// True for one lane of a converged warp, the same one in every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t leader;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(leader));
+  return leader != 0;
 }
 
 // Arrive once on `bar` when every tcgen05 async op issued so far by this thread is done.

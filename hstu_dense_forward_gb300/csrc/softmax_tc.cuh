@@ -33,7 +33,7 @@
 //   P = 2^(u - m), m following max u, l += 2^-EV sum P,
 // and O / l is the output (2^m cancels). bf16 queries become fp16 in place, times a power of two
 // of their row, chosen so that the row's largest lies in [2^14, 2^15). (Dequantising to q's type
-// instead took twice the instructions: 1056 us instead of 768 for 4096 tokens over 4096.)
+// instead took twice the instructions: 1028 us where this took 837, 4096 tokens over 4096.)
 //
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
@@ -562,121 +562,166 @@ struct Issuer {
   static constexpr uint32_t IDESC_S = ptx::idesc_f16(AB, 128, C::KT, 0);
   static constexpr uint32_t IDESC_O = ptx::idesc_f16(AB, 128, C::D, 1);
 
-  // (i: ring place, running on over the pieces)
-  __device__ bool kv_ready(uint32_t i) {
-    if (!wait_bar(p, bars, &bars->kv_full[i % C::NSLOT], (i / C::NSLOT) & 1)) return false;
-    ptx::tc_fence_after();
-    return true;
+  __device__ __forceinline__ bool kv_ready(int slot, uint32_t phase) {
+    return warp_wait(p, bars, &bars->kv_full[slot], phase);
   }
-  __device__ void kv_release(uint32_t i) {
-    ptx::mma_commit(ptx::smem_u32(&bars->kv_empty[i % C::NSLOT]));
-  }
-  // scores of query tile q into buffer sb, K at ring place i
-  __device__ void scores(int q, int sb, uint32_t i) {
+  // scores of query tile q into buffer sb; `last`: the K tile is free after them
+  __device__ __forceinline__ void scores(int q, int sb, int slot, bool last) {
     const uint64_t ad0 = ptx::smem_desc(sbase + C::OFF_Q + q * C::Q_TILE, 16, 8 * C::SWB, 2);
-    const uint64_t bd0 =
-        ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, 16, 8 * C::SWB, 2);
+    const uint64_t bd0 = ptx::smem_desc(sbase + C::OFF_KV + slot * C::KV_TILE, 16, 8 * C::SWB, 2);
+    const uint32_t full = ptx::smem_u32(&bars->s_full[sb]);
+    const uint32_t empty = ptx::smem_u32(&bars->kv_empty[slot]);
+    if (ptx::elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < C::D / 16; ++kk) {
-      const uint32_t in = (kk % 4) * 32;
-      ptx::mma_ss(tmem + sb * C::KT, ptx::desc_add(ad0, (kk / 4) * C::Q_CB + in),
-                  ptx::desc_add(bd0, (kk / 4) * C::KV_CB + in), IDESC_S, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < C::D / 16; ++kk) {
+        const uint32_t in = (kk % 4) * 32;
+        ptx::mma_ss(tmem + sb * C::KT, ptx::desc_add(ad0, (kk / 4) * C::Q_CB + in),
+                    ptx::desc_add(bd0, (kk / 4) * C::KV_CB + in), IDESC_S, kk > 0 ? 1u : 0u);
+      }
+      ptx::mma_commit(full);
+      if (last) ptx::mma_commit(empty);
     }
-    ptx::mma_commit(ptx::smem_u32(&bars->s_full[sb]));
+    __syncwarp();
   }
-  // O of query tile q += P (over score buffer sb) V at ring place i, for one half of the keys:
-  // the first half's product runs while the second half's weights are computed
-  __device__ void accumulate(int q, int sb, uint32_t i, int half, bool first) {
+  // O of query tile q += P (over score buffer sb) V, for one half of the keys: the first half's
+  // product runs while the second half's weights are computed. `last`: the V tile is free after
+  // the second one
+  __device__ __forceinline__ void accumulate(int q, int sb, int slot, int half, bool first,
+                                             bool last) {
     const uint64_t bd0 =
-        ptx::smem_desc(sbase + C::OFF_KV + (i % C::NSLOT) * C::KV_TILE, C::KV_CB, 8 * C::SWB, 2);
+        ptx::smem_desc(sbase + C::OFF_KV + slot * C::KV_TILE, C::KV_CB, 8 * C::SWB, 2);
+    const uint32_t done = ptx::smem_u32(&bars->pv_done[q]);
+    const uint32_t empty = ptx::smem_u32(&bars->kv_empty[slot]);
+    if (ptx::elect_one()) {
 #pragma unroll
-    for (int x = 0; x < C::KT / 32; ++x) {
-      const int kk = half * (C::KT / 32) + x;
-      ptx::mma_ts(tmem + C::O_COL + q * C::D, tmem + sb * C::KT + kk * 8,
-                  ptx::desc_add(bd0, kk * 16 * C::SWB), IDESC_O, (!first || kk > 0) ? 1u : 0u);
+      for (int x = 0; x < C::KT / 32; ++x) {
+        const int kk = half * (C::KT / 32) + x;
+        ptx::mma_ts(tmem + C::O_COL + q * C::D, tmem + sb * C::KT + kk * 8,
+                    ptx::desc_add(bd0, kk * 16 * C::SWB), IDESC_O, (!first || kk > 0) ? 1u : 0u);
+      }
+      if (half) {
+        ptx::mma_commit(done);
+        if (last) ptx::mma_commit(empty);
+      }
     }
-  }
-  // The same for both halves as P (phase `par` of its barriers) and V arrive.
-  __device__ bool weighted_sum(int q, int sb, uint32_t par, uint32_t i, bool first) {
-    if (!kv_ready(i) || !wait_bar(p, bars, &bars->p_half[sb], par)) return false;
-    ptx::tc_fence_after();
-    accumulate(q, sb, i, 0, first);
-    if (!wait_bar(p, bars, &bars->p_full[sb], par)) return false;
-    ptx::tc_fence_after();
-    accumulate(q, sb, i, 1, false);
-    ptx::mma_commit(ptx::smem_u32(&bars->pv_done[q]));
-    return true;
+    __syncwarp();
   }
 };
 
+// The ring's places in their order.
+template <class C>
+struct Place {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ void next() {
+    if (++slot == C::NSLOT) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// By a whole warp, of which one lane issues: its values are uniform, what the products'
+// instructions want (in one lane's own branch each value went to the uniform registers by itself:
+// 4096 tokens over 4096 took 724 us instead of 660, with a head dim of 256 940 instead of 773).
 template <class C, bool BF16>
-__device__ bool mma_loop(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars,
+__device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars,
                          const PlanTable& pl, int tiles) {
-  uint32_t ring = 0, queries = 0;
+  Place<C> at{0, 0u};
+  uint32_t queries = 0;
   uint32_t g[2] = {0, 0};        // key tiles of each query tile before the piece
   uint32_t outputs[2] = {0, 0};  // pieces of it that had any
   Walk w;
   Seg it;
   walk_begin<C>(p, pl, w);
   while (walk_next<C>(p, pl, w, tiles, it)) {
-    const int n = it.nmax;
+    const int n = __shfl_sync(0xffffffffu, it.nmax, 0);
     if (n == 0) continue;
-    const int nq[2] = {it.n[0], C::NQT == 2 ? it.n[1] : 0};
-    if (!wait_bar(p, bars, BF16 && C::E4M3 ? &bars->q_ready : &bars->q_full, queries & 1))
-      return false;
-    ptx::tc_fence_after();
+    const int nq[2] = {__shfl_sync(0xffffffffu, it.n[0], 0),
+                       C::NQT == 2 ? __shfl_sync(0xffffffffu, it.n[1], 0) : 0};
+    if (!warp_wait(p, bars, BF16 && C::E4M3 ? &bars->q_ready : &bars->q_full, queries & 1)) return;
     ++queries;
     // Scores of the first NSB tiles, over weights of the piece before: its last product must be
     // done. (Those before it are: the softmax hands over a piece's last weights only then, so
     // that this wait, too, cannot take one phase for another.)
     for (int t = 0; t < C::NSB && t < n; ++t) {
-      if (!is.kv_ready(ring + k_index<C>(t))) return false;
+      if (!is.kv_ready(at.slot, at.phase)) return;
 #pragma unroll
       for (int q = 0; q < C::NQT; ++q) {
         if (t >= nq[q]) continue;
         const uint32_t gt = g[q] + t;
-        if (t == 0 && gt > 0) {
-          if (!wait_bar(p, bars, &bars->pv_done[q], (gt - 1) & 1)) return false;
-          ptx::tc_fence_after();
-        }
-        is.scores(q, C::NQT == 1 ? gt & 1 : q, ring + k_index<C>(t));
+        if (t == 0 && gt > 0 && !warp_wait(p, bars, &bars->pv_done[q], (gt - 1) & 1)) return;
+        ptx::tc_fence_after();
+        is.scores(q, C::NQT == 1 ? gt & 1 : q, at.slot, q == 1 || t >= nq[1]);
       }
-      is.kv_release(ring + k_index<C>(t));
+      at.next();
     }
-    if (n <= C::NSB) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
+    if (n <= C::NSB) {
+      if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
+      __syncwarp();
+    }
+    // the piece's first products overwrite O: the previous output has been read
+#pragma unroll
+    for (int q = 0; q < C::NQT; ++q)
+      if (nq[q] > 0 && !warp_wait(p, bars, &bars->o_empty[q], (outputs[q]++ & 1) ^ 1)) return;
     // Then per tile and query tile: O += P(t) V, and the scores of tile t + NSB over P(t), which
-    // that product must have read. With two query tiles the softmax of one runs meanwhile.
+    // that product must have read. With two query tiles the softmax of one runs meanwhile. One
+    // look at all barriers first: a test takes some 100 cycles, in which the tensor pipe may run
+    // empty.
     for (int t = 0; t < n; ++t) {
-      const uint32_t vi = ring + v_index<C>(t, n), ki = ring + k_index<C>(t + C::NSB);
+      const Place<C> v = at;
+      at.next();
+      const Place<C> k = at;
+      uint32_t kv = 0u;  // 4, 8: V(t), K(t + NSB) are known to be there
 #pragma unroll
       for (int q = 0; q < C::NQT; ++q) {
         if (t >= nq[q]) continue;
         const uint32_t gt = g[q] + t;
         const int sb = C::NQT == 1 ? gt & 1 : q;
-        // the piece's first product overwrites O: the previous output has been read
-        if (t == 0 && !wait_bar(p, bars, &bars->o_empty[q], (outputs[q]++ & 1) ^ 1)) return false;
-        if (!is.weighted_sum(q, sb, C::NQT == 1 ? (gt >> 1) & 1 : gt & 1, vi, t == 0)) return false;
+        const uint32_t par = C::NQT == 1 ? (gt >> 1) & 1 : gt & 1;
+        uint32_t ready = q == 0
+            ? ptx::mbar_tests(ptx::smem_u32(&bars->p_half[sb]), par,
+                              ptx::smem_u32(&bars->p_full[sb]), par,
+                              ptx::smem_u32(&bars->kv_full[v.slot]), v.phase,
+                              ptx::smem_u32(&bars->kv_full[k.slot]), k.phase)
+            : ptx::mbar_tests(ptx::smem_u32(&bars->p_half[sb]), par,
+                              ptx::smem_u32(&bars->p_full[sb]), par);
+        ready = __reduce_and_sync(0xffffffffu, ready);
+        if (q == 0) kv = ready;
+        if (!(kv & 4u) && !is.kv_ready(v.slot, v.phase)) return;
+        kv |= 4u;
+        if (!(ready & 1u) && !warp_wait(p, bars, &bars->p_half[sb], par)) return;
+        ptx::tc_fence_after();
+        is.accumulate(q, sb, v.slot, 0, t == 0, false);
+        if (!(ready & 2u) && !warp_wait(p, bars, &bars->p_full[sb], par)) return;
+        ptx::tc_fence_after();
+        is.accumulate(q, sb, v.slot, 1, false, q == 1 || t >= nq[1]);
         if (t + C::NSB < nq[q]) {
-          if (!is.kv_ready(ki) || !wait_bar(p, bars, &bars->pv_done[q], gt & 1)) return false;
-          is.scores(q, sb, ki);
+          if (!(kv & 8u) && !is.kv_ready(k.slot, k.phase)) return;
+          kv |= 8u;
+          if (!warp_wait(p, bars, &bars->pv_done[q], gt & 1)) return;
+          ptx::tc_fence_after();
+          is.scores(q, sb, k.slot, q == 1 || t + C::NSB >= nq[1]);
         }
       }
-      is.kv_release(vi);
       if (t + C::NSB < n) {
-        is.kv_release(ki);
-        if (t + C::NSB + 1 == n) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
+        at.next();
+        if (t + C::NSB + 1 == n) {
+          if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
+          __syncwarp();
+        }
       }
     }
-    ring += 2 * n;
     g[0] += nq[0];
     g[1] += nq[1];
   }
-  return true;
 }
 
-// Waits for the MMAs issued so far, whatever ended the loop: TMEM is freed after this.
+// Waits for the MMAs issued so far, whatever ended the role: TMEM is freed after this.
 __device__ __forceinline__ void mma_drain(const SoftmaxParams& p, Bars* bars) {
-  ptx::mma_commit(ptx::smem_u32(&bars->drain));
+  __syncwarp();
+  if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&bars->drain));
+  __syncwarp();
   const uint64_t start = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait(ptx::smem_u32(&bars->drain), 0)) {
     if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
@@ -967,11 +1012,9 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   if (warp < C::SM_WARPS) {
     softmax_role<C, BF16>(p, bars, smem, tmem, pl, tiles, warp / 4, warp, lane);
   } else if (warp == C::MMA_WARP) {
-    if (lane == 0) {
-      Issuer<C, BF16> is{p, bars, ptx::smem_u32(smem), tmem};
-      mma_loop<C, BF16>(p, is, bars, pl, tiles);
-      mma_drain(p, bars);
-    }
+    Issuer<C, BF16> is{p, bars, ptx::smem_u32(smem), __shfl_sync(0xffffffffu, tmem, 0)};
+    mma_role<C, BF16>(p, is, bars, pl, tiles);
+    mma_drain(p, bars);
   } else if (warp == C::LOAD_WARP) {
     if (lane == 0) load_role<C>(p, bars, smem, pl, tiles, &tm_q, &tm_c);
   } else if (C::E4M3 && warp >= C::CONV_WARP) {

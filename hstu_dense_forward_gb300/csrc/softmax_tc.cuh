@@ -68,10 +68,12 @@ struct Cfg {
   static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
   static constexpr int KV_CB = KT * SWB, KV_TILE = NCB * KV_CB;
   static constexpr int ST_TILE = KT * D;          // staged E4M3 tile; its row scales (KT bytes)
-  // ring depths: what 227 KB of shared memory holds next to Q
-  static constexpr int NSLOT = !E4M3 ? (D == 64 ? 6 : (NQT == 1 && D == 128 ? 5 : 4))
-                                     : (D == 64 ? 4 : (NQT == 1 && D == 128 ? 4 : 3));
-  static constexpr int NST = E4M3 ? (D == 64 ? 4 : (NQT == 1 && D == 128 ? 3 : 3)) : 0;
+  // The scores' A operand, Q, comes from TMEM where that has room: from shared memory it takes,
+  // with K, all of the latter's bandwidth, and threads wait for their barriers meanwhile.
+  static constexpr bool QT = NQT == 1 || D == 64;
+  // ring depths: what 227 KB of shared memory holds
+  static constexpr int NSLOT = D == 64 ? (E4M3 ? 4 : 8) : QT ? (E4M3 ? 4 : 6) : E4M3 ? 3 : 4;
+  static constexpr int NST = !E4M3 ? 0 : QT ? 4 : 3;
   static constexpr int SM_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1;
   static constexpr int CONV_WARP = SM_WARPS + 4;  // (a warpgroup each for K and V)
@@ -79,10 +81,11 @@ struct Cfg {
   // columns of S that a softmax thread holds at a time: a whole row, or (E4M3, whose conversion
   // needs the registers) half of one, which is then loaded twice
   static constexpr int SC = KT / 2;
-  // TMEM: score buffers of KT columns (P over them), then O
-  static constexpr uint32_t O_COL = NQT * NSB * KT;
-  static_assert(O_COL + NQT * D <= kTmemCols, "TMEM");
-  static constexpr int OFF_Q = 0, OFF_KV = NQT * Q_TILE, OFF_ST = OFF_KV + NSLOT * KV_TILE;
+  // TMEM: score buffers of KT columns (P over them), O, Q (two elements a column)
+  static constexpr uint32_t O_COL = NQT * NSB * KT, Q_COL = O_COL + NQT * D;
+  static_assert(Q_COL + (QT ? NQT * D / 2 : 0) <= kTmemCols, "TMEM");
+  static constexpr int OFF_Q = 0, OFF_KV = QT ? 0 : NQT * Q_TILE;
+  static constexpr int OFF_ST = OFF_KV + NSLOT * KV_TILE;
   static constexpr int OFF_SC = OFF_ST + NST * ST_TILE;  // row scales of the staged tiles
   static constexpr int OFF_BAR = OFF_SC + NST * 128;
   static constexpr int OFF_PLAN = OFF_BAR + 2048;
@@ -95,9 +98,9 @@ struct Cfg {
 constexpr int kExpDepth = 8;  // tiles whose exponents are kept (the conversion is fewer ahead)
 
 struct Bars {
-  uint64_t q_ready, q_empty, o_empty[2], exp_full[kExpDepth];
+  uint64_t q_ready[2], q_empty, o_empty[2], exp_full[kExpDepth];
   float tile_exp[kExpDepth][2];  // EK, EV
-  uint64_t q_full, kv_full[6], kv_empty[6], st_full[4], st_empty[4];
+  uint64_t q_full, kv_full[8], kv_empty[8], st_full[4], st_empty[4];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;
   uint32_t tmem_base;
   volatile int abort;
@@ -428,7 +431,7 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
                 cb * C::EPC, it.hk, row0, plane);
         }
       }
-      if (i == 0) {  // the piece's queries, once the previous piece's scores are done
+      if (!C::QT && i == 0) {  // the piece's queries, once the previous piece's scores are done
         if (!wait_bar(p, bars, &bars->q_empty, (queries & 1) ^ 1)) return;
         ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars->q_full), it.nq * q_bytes);
         for (int q = 0; q < it.nq; ++q)
@@ -523,31 +526,73 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
   }
 }
 
+// The power of two that takes a bf16 row with `top` (a magnitude's pattern) as its largest
+// into [2^14, 2^15).
+__device__ __forceinline__ int row_shift(uint32_t top) {
+  return min(14 - ((int)(top >> 7) - 127), 126);
+}
+__device__ __forceinline__ uint32_t larger_magnitude(uint32_t top, const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+  return top;
+}
+// Two bf16 values as fp16 ones, times `mul`.
+__device__ __forceinline__ uint32_t bf16_to_half(uint32_t w, float mul) {
+  return pack2<false>(__uint_as_float(w << 16) * mul, __uint_as_float(w & 0xffff0000u) * mul);
+}
+
+// The query row at p.q + at to a thread's TMEM lane; for E4M3 keys a bf16 row becomes fp16 times
+// 2^sh, and 2^-sh is returned. By a whole warp; rows without a query are zeros.
+template <class C, bool BF16>
+__device__ float query_to_tmem(const SoftmaxParams& p, uint32_t col, bool any, bool valid,
+                               long long at) {
+  if (!any) return 1.0f;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
+  int sh = 0;
+  if (BF16 && C::E4M3 && valid) {
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int x = 0; x < p.c.D / 8; ++x) top = larger_magnitude(top, q[x]);
+    sh = row_shift(top);
+  }
+  const float mul = power2(sh);
+#pragma unroll 2
+  for (int x = 0; x < C::D / 8; x += 2) {
+    uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (valid && x < p.c.D / 8) {
+      u[0] = q[x];
+      u[1] = q[x + 1];
+    }
+    uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+    if constexpr (BF16 && C::E4M3) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = bf16_to_half(w[e], mul);
+    }
+    ptx::tmem_st8(col + x * 4, w);
+  }
+  ptx::tmem_st_wait();
+  return power2(-sh);
+}
+
 // Row r of a bf16 query tile (swizzled shared memory) becomes fp16 times 2^sh; returns 2^-sh.
 template <class C>
 __device__ float query_to_half(uint8_t* tile, int r) {
-  uint32_t top = 0;  // largest magnitude, as bf16 patterns
+  uint32_t top = 0;
 #pragma unroll 4
-  for (int x = 0; x < C::NCB * 8; ++x) {
-    const uint4 u = *reinterpret_cast<const uint4*>(tile + (x >> 3) * C::Q_CB + r * C::SWB +
-                                                    ((x & 7) ^ (r & 7)) * 16);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-  }
-  const int sh = min(14 - ((int)(top >> 7) - 127), 126);
+  for (int x = 0; x < C::NCB * 8; ++x)
+    top = larger_magnitude(top, *reinterpret_cast<const uint4*>(
+                                    tile + (x >> 3) * C::Q_CB + r * C::SWB +
+                                    ((x & 7) ^ (r & 7)) * 16));
+  const int sh = row_shift(top);
   const float mul = power2(sh);
 #pragma unroll 4
   for (int x = 0; x < C::NCB * 8; ++x) {
     uint4* at = reinterpret_cast<uint4*>(tile + (x >> 3) * C::Q_CB + r * C::SWB +
                                          ((x & 7) ^ (r & 7)) * 16);
     const uint4 u = *at;
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack2<false>(__uint_as_float(w[e] << 16) * mul,
-                          __uint_as_float(w[e] & 0xffff0000u) * mul);
-    *at = make_uint4(w[0], w[1], w[2], w[3]);
+    *at = make_uint4(bf16_to_half(u.x, mul), bf16_to_half(u.y, mul), bf16_to_half(u.z, mul),
+                     bf16_to_half(u.w, mul));
   }
   return power2(-sh);
 }
@@ -575,8 +620,13 @@ struct Issuer {
 #pragma unroll
       for (int kk = 0; kk < C::D / 16; ++kk) {
         const uint32_t in = (kk % 4) * 32;
-        ptx::mma_ss(tmem + sb * C::KT, ptx::desc_add(ad0, (kk / 4) * C::Q_CB + in),
-                    ptx::desc_add(bd0, (kk / 4) * C::KV_CB + in), IDESC_S, kk > 0 ? 1u : 0u);
+        const uint64_t bd = ptx::desc_add(bd0, (kk / 4) * C::KV_CB + in);
+        if constexpr (C::QT)
+          ptx::mma_ts(tmem + sb * C::KT, tmem + C::Q_COL + q * (C::D / 2) + kk * 8, bd, IDESC_S,
+                      kk > 0 ? 1u : 0u);
+        else
+          ptx::mma_ss(tmem + sb * C::KT, ptx::desc_add(ad0, (kk / 4) * C::Q_CB + in), bd, IDESC_S,
+                      kk > 0 ? 1u : 0u);
       }
       ptx::mma_commit(full);
       if (last) ptx::mma_commit(empty);
@@ -639,7 +689,15 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
     if (n == 0) continue;
     const int nq[2] = {__shfl_sync(0xffffffffu, it.n[0], 0),
                        C::NQT == 2 ? __shfl_sync(0xffffffffu, it.n[1], 0) : 0};
-    if (!warp_wait(p, bars, BF16 && C::E4M3 ? &bars->q_ready : &bars->q_full, queries & 1)) return;
+    // Queries that the warpgroups write: those with tiles of the piece arrive (another could run
+    // any number of pieces ahead). Queries that they convert: all arrive, and none can fall
+    // behind the loads.
+#pragma unroll
+    for (int q = 0; q < C::NQT; ++q) {
+      if (C::QT ? nq[q] > 0 : BF16 && C::E4M3)
+        if (!warp_wait(p, bars, &bars->q_ready[q], (C::QT ? outputs[q] : queries) & 1)) return;
+    }
+    if (!C::QT && !(BF16 && C::E4M3) && !warp_wait(p, bars, &bars->q_full, queries & 1)) return;
     ++queries;
     // Scores of the first NSB tiles, over weights of the piece before: its last product must be
     // done. (Those before it are: the softmax hands over a piece's last weights only then, so
@@ -656,7 +714,7 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
       }
       at.next();
     }
-    if (n <= C::NSB) {
+    if (!C::QT && n <= C::NSB) {
       if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
       __syncwarp();
     }
@@ -706,7 +764,7 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
       }
       if (t + C::NSB < n) {
         at.next();
-        if (t + C::NSB + 1 == n) {
+        if (!C::QT && t + C::NSB + 1 == n) {
           if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
           __syncwarp();
         }
@@ -755,32 +813,42 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
       fv = p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
     }
-    if (BF16 && C::E4M3 && it.nmax > 0) {  // (a warpgroup without rows of the piece arrives, too)
+    const int n = C::NQT == 2 && q ? it.n[1] : it.n[0];
+    if constexpr (C::QT) {
+      if (n > 0) {  // (this tile's scores of the piece before are done: its last have been seen)
+        fk *= query_to_tmem<C, BF16>(
+            p, tmem + lane_off + C::Q_COL + q * (C::D / 2), any, valid,
+            (it.s.t0 + tok) * p.q_stride + (it.hk * p.G + r % p.G) * (long long)p.c.D);
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[q]));
+      }
+    } else if (BF16 && C::E4M3 && it.nmax > 0) {
       if (!warp_wait(p, bars, &bars->q_full, queries++ & 1)) return;
       if (valid) fk *= query_to_half<C>(smem + C::OFF_Q + q * C::Q_TILE, r);
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready));
+      ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[q]));
     }
     if (q >= it.nq) continue;
     // keys that the row sees: positions [k0, k0 + lim); rows without a token follow the widest
     long long see = it.kend;
     if (p.causal && valid) see = min(see, it.s.Lk - it.s.n + tok + 1);
     const int lim = (int)max(see - it.k0, 0ll);
-    const int n = C::NQT == 2 && q ? it.n[1] : it.n[0];
     const int rest = (int)min(it.s.Lk - it.k0, 0x7fffffffll);  // keys of the sequence from k0 on
     float m = -CUDART_INF_F, l = 0.0f;
     for (int t = 0; t < n; ++t, ++g) {
       const int sb = C::NQT == 1 ? (g & 1) : q;
       const uint32_t par = C::NQT == 1 ? (g >> 1) & 1 : g & 1;
+      if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
+      ptx::tc_fence_after();
       float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
       if constexpr (C::E4M3) {
+        // (with the scores there the conversion has come to this tile; a warpgroup without tiles
+        // of the last piece could otherwise be here phases ahead of it)
         const uint32_t te = done + t;
         if (!warp_wait(p, bars, &bars->exp_full[te % kExpDepth], (te / kExpDepth) & 1)) return;
         ek = power2((int)bars->tile_exp[te % kExpDepth][0]);
         ev = bars->tile_exp[te % kExpDepth][1];
       }
-      if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
-      ptx::tc_fence_after();
       const uint32_t s_col = tmem + lane_off + sb * KT;
       constexpr int NC = C::SC / 32;  // chunks held at a time
       uint32_t sv[NC][32];
@@ -961,9 +1029,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
     ptx::mbar_init(ptx::smem_u32(&bars->q_full), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->q_empty), 1);
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
-    ptx::mbar_init(ptx::smem_u32(&bars->q_ready), C::NQT * 128);
     for (int s = 0; s < kExpDepth; ++s) ptx::mbar_init(ptx::smem_u32(&bars->exp_full[s]), 2);
-    for (int s = 0; s < 6; ++s) {
+    for (int s = 0; s < C::NSLOT; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), C::E4M3 ? 128 : 1);
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
     }
@@ -977,6 +1044,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
       ptx::mbar_init(ptx::smem_u32(&bars->p_full[s]), 128);
       ptx::mbar_init(ptx::smem_u32(&bars->pv_done[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->o_empty[s]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bars->q_ready[s]), 128);
     }
     bars->abort = 0;
     ptx::fence_barrier_init();

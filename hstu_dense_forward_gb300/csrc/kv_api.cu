@@ -159,8 +159,8 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   } else {
     pl->kernel = AttnPlan::TC;
     // Two query tiles share the loads of K and V and keep the tensor pipe busier, if there are
-    // rows for both (4096 tokens over 4096: 670 us with two, 774 with one; 24 sequences of some
-    // 500 rows over 900 keys: 67 and 48)
+    // rows for both (4096 tokens over 4096, 16 heads of 4: 660 us with two, 712 with one; 64
+    // sequences of some 200 rows over 2500 keys: 141 and 126; 24 of 500 over 900: 48 and 54)
     pl->qtiles = c->head_dim <= 128 && most > 128 / G &&
                          a->total_tokens * G / c->batch >= 256 ? 2 : 1;
     bm = pl->qtiles * (128 / G) * G;
@@ -189,13 +189,15 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     const long long want = (4ll * sms + items - 1) / items;
     const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
     pl->splits = (int)(want < can ? want : can);
-  } else if (c->batch <= hstu::kMaxSeqs && sms <= hstu::kMaxCtas &&
-             a->total_tokens * G / bm + c->batch <= hstu::kMaxItems && items < 4ll * sms) {
-    // few items: one CTA per SM takes an equal share of their key tiles
+  } else if (c->batch <= hstu::kMaxSeqs &&
+             a->total_tokens * G / bm + c->batch <= hstu::kMaxItems && items * 2 < 3ll * sms) {
+    // Few items: one CTA per SM takes an equal share of their key tiles (a CTA for each item and
+    // this: 208 items of two sequences of 8000 keys 128 and 107 us, 185 of 16 of 4500 142 and
+    // 121; but 270 of four of 3000 97 and 105, which fill the SMs well enough)
     pl->balanced = 1;
     pl->blocks = sms;
     pl->parts_bytes = 2ll * sms * pl->qtiles * 128 * (c->head_dim + 1) * 4;
-    pl->workspace = pl->parts_bytes + (long long)sizeof(hstu::PlanTable);
+    pl->workspace = pl->parts_bytes + sms * (long long)sizeof(hstu::JoinRecord);
   }
   if (pl->splits > 1) {
     pl->parts_bytes = (long long)pl->splits * a->total_tokens * a->num_heads_q *
@@ -259,7 +261,8 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   // workspace: outputs of the parts, their sums, the table of items
   p.part_o = static_cast<float*>(a->workspace);
   p.part_lse = p.part_o + pl.parts_bytes / 4 / (c->head_dim + 1) * c->head_dim;
-  p.plan = reinterpret_cast<hstu::PlanTable*>(static_cast<char*>(a->workspace) + pl.parts_bytes);
+  p.joins =
+      reinterpret_cast<hstu::JoinRecord*>(static_cast<char*>(a->workspace) + pl.parts_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = c->dtype == HSTU_FP8_E4M3;
   cudaError_t e =

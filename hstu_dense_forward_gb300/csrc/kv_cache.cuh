@@ -197,16 +197,22 @@ __device__ __forceinline__ void store16<__half>(__half* p, const float (&x)[16])
 // ------------------------------------------------------------- softmax attention
 // Items of a balanced run of the tensor-core kernel: (sequence, tile of query tokens) pairs in
 // order, each of them once per kv head.
-constexpr int kMaxItems = 512, kMaxSeqs = 512, kMaxCtas = 512;
+constexpr int kMaxItems = 512, kMaxSeqs = 512;
 struct PlanTable {
   long long cost[kMaxItems + 1];  // running sum of the pairs' costs, in key tiles
   int first[kMaxSeqs + 1];        // first pair of each sequence
   uint16_t seq[kMaxItems];        // sequence of each pair
   int items;
-  // (in the workspace's copy) the pair and kv head at which each CTA's share begins
-  int begin_item[kMaxCtas + 1], begin_head[kMaxCtas + 1];
 };
-constexpr int kPlanSharedBytes = offsetof(PlanTable, begin_item);
+constexpr int kPlanSharedBytes = sizeof(PlanTable);
+
+// What to join at the border in front of CTA c's share, written by CTA c: pieces of CTAs
+// c - 1 .. c - 2 + count make up the outputs of one item (count 0: nothing to join here).
+struct JoinRecord {
+  int count, hk;
+  int rows;      // of the item (its tokens times G)
+  long long t0;  // its first token
+};
 
 // An item costs its key tiles and kItemCost for what it needs besides (its queries' load, the
 // first products' and the output's latency). These units, all heads' of a pair in a row, are
@@ -241,7 +247,7 @@ struct SoftmaxParams {
   float* part_o;           // [splits][T, Nq, D]: each key range's normalised output, or (balanced)
                            // [2 per CTA][rows of an item][D]: each piece's
   float* part_lse;         // the same without D: log2 of the sums (-inf: no key)
-  PlanTable* plan;         // copy of the table of items (balanced)
+  JoinRecord* joins;       // [CTAs] what to join at each share's border (balanced)
   int balanced;            // tensor-core kernel: CTAs share the items' key tiles equally
   long long q_stride;      // elements
   int Nq, G;               // query heads, query heads of one kv head

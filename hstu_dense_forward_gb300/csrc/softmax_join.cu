@@ -38,35 +38,21 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, const fl
                                             *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// The parts of a row: `count` of them, part i at row number at(i) of part_o and part_lse.
-struct Ranges {
-  long long row, all;
-  int count;
-  __device__ long long at(int i) const { return i * all + row; }
-};
-// Pieces of an item: the first ends CTA c's share inside the item (slot 2 c + 1), the others
-// begin inside it (slots 2 (c + i)).
-struct Pieces {
-  int c, count, slot_rows, row;  // (rows of a slot, the row's place in it)
-  __device__ long long at(int i) const {
-    return (long long)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_rows + row;
-  }
-};
-
-template <typename T, typename Parts>
-__device__ __forceinline__ void join(const SoftmaxParams& p, const Parts& parts, long long row,
-                                     int first, int step) {
+template <typename T>
+__device__ __forceinline__ void join(const SoftmaxParams& p, int count, long long row, int first,
+                                     int step) {
+  const long long all = p.c.T * p.Nq;  // part i of the row is number i * all + row
   float top = -CUDART_INF_F;
-  for (int i = 0; i < parts.count; ++i) top = fmaxf(top, p.part_lse[parts.at(i)]);
+  for (int i = 0; i < count; ++i) top = fmaxf(top, p.part_lse[i * all + row]);
   const float base = top == -CUDART_INF_F ? 0.f : top;
   float sum = 0.f;
-  for (int i = 0; i < parts.count; ++i) sum += exp2f(p.part_lse[parts.at(i)] - base);
+  for (int i = 0; i < count; ++i) sum += exp2f(p.part_lse[i * all + row] - base);
   const int D = p.c.D;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   for (int d = first; d < D; d += step) {
     float o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < parts.count; ++i) {
-      const long long at = parts.at(i);
+    for (int i = 0; i < count; ++i) {
+      const long long at = i * all + row;
       const float w = exp2f(p.part_lse[at] - base) * inv;
       if (w == 0.f) continue;  // a part without keys for this row holds nothing
       const float4 f = *reinterpret_cast<const float4*>(p.part_o + at * D + d);
@@ -92,41 +78,75 @@ __global__ void __launch_bounds__(kThreads) join_ranges_kernel(const SoftmaxPara
   if (!attn_seq_ok(p, s) || t < s.t0 || t >= s.t0 + s.n) return;
   const int count = key_ranges(p, s.Lk).count;
   if (count < 2) return;  // written by the attention kernel
-  join<T>(p, Ranges{row, p.c.T * p.Nq, count}, row, (int)(lane & ((1 << lane_shift) - 1)) * 4,
-          4 << lane_shift);
+  join<T>(p, count, row, (int)(lane & ((1 << lane_shift) - 1)) * 4, 4 << lane_shift);
 }
 
-// Pieces of a balanced run. Block (c, y) looks at the border between the shares of CTAs c and
-// c + 1: if it is the first that parts an item's key tiles, the block joins kJoinRows of its
-// rows. tile_tokens: tokens of one query tile, query_tiles of an item.
-constexpr int kJoinRows = 32;
+// Pieces of a balanced run: block (c, y) joins kJoinRows rows of the item that CTA c + 1's record
+// names, a warp four of them (what bounds it is the latency of its few dependent loads: one row
+// after the other, found from the table of items, took 20 us a call, this 6). An item's rows are
+// packed, `tile_rows` to a query tile of 128 slot rows; its first piece lies in slot
+// 2 first + 1 of the CTAs' slots, piece i in slot 2 (first + i).
+constexpr int kWarpRows = 4, kJoinRows = kWarpRows * kThreads / 32;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) join_pieces_kernel(const SoftmaxParams p,
-                                                               int tile_tokens, int query_tiles,
-                                                               int grid) {
+                                                               int tile_rows, int query_tiles) {
   ptx::grid_dependency_wait();
-  const PlanTable& pl = *p.plan;
-  const int c = blockIdx.x, e = pl.begin_item[c + 1], hk = pl.begin_head[c + 1];
-  const long long units = pl.cost[pl.items] * p.c.Nk;
-  const int ctas = share_ctas(units, grid);
-  if (units == 0 || c + 1 >= ctas) return;
-  const long long cost = pl.cost[e + 1] - pl.cost[e], base = pl.cost[e] * p.c.Nk + hk * cost;
-  // shares end at u1 (CTA c - 1) and u2; a border in front of the item's tiles parts nothing
-  const long long u1 = share(units, ctas, c), u2 = share(units, ctas, c + 1);
-  if (u2 <= base + kItemCost || u1 > base + kItemCost) return;
-  int last = c + 1;
-  while (share(units, ctas, last + 1) < base + cost) ++last;
-  const int b = pl.seq[e];
-  const PagedSeq s = paged_seq(p.c, b);
-  const int rows = query_tiles * 128;
-  for (int x = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-       x < min(rows, (int)(blockIdx.y + 1) * kJoinRows); x += kThreads / 32) {
-    const int q = x / 128, r = x % 128;
-    const long long tok = ((long long)(e - pl.first[b]) * query_tiles + q) * tile_tokens + r / p.G;
-    if (r >= tile_tokens * p.G || tok >= s.n) continue;
-    const long long row = (s.t0 + tok) * p.Nq + hk * p.G + r % p.G;
-    join<T>(p, Pieces{c, last - c + 1, rows, x}, row, (threadIdx.x & 31) * 4, 128);
+  const JoinRecord j = p.joins[blockIdx.x + 1];
+  const int first = blockIdx.x, lane = threadIdx.x & 31;
+  const int row0 = (int)blockIdx.y * kJoinRows + (int)(threadIdx.x >> 5) * kWarpRows;
+  if (j.count == 0 || row0 >= j.rows) return;
+  auto at = [&](int i, int row) {
+    const long long slot = i == 0 ? 2 * first + 1 : 2 * (first + i);
+    return slot * (query_tiles * 128) + row / tile_rows * 128 + row % tile_rows;
+  };
+  // lane 8 r + i: part i (and 8 + i, ...) of row r
+  const int mine = min(row0 + lane / 8, j.rows - 1), part = lane % 8;
+  auto log_sum = [&](int i) { return i < j.count ? p.part_lse[at(i, mine)] : -CUDART_INF_F; };
+  const float e0 = log_sum(part);
+  float top = e0;
+  for (int i = 8; i < j.count; i += 8) top = fmaxf(top, log_sum(i + part));
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -CUDART_INF_F ? 0.f : top;
+  float sum = exp2f(e0 - base);
+  for (int i = 8; i < j.count; i += 8) sum += exp2f(log_sum(i + part) - base);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  auto out_row = [&](int row) { return (j.t0 + row / p.G) * p.Nq + j.hk * p.G + row % p.G; };
+  if (p.lse && part == 0 && row0 + lane / 8 < j.rows)
+    p.lse[out_row(mine)] = (top + log2f(sum)) * kLn2;
+  const int D = p.c.D;
+  for (int d0 = 0; d0 < D; d0 += 128) {  // (every lane stays for the shuffles)
+    const int d = d0 + lane * 4;
+    float o[kWarpRows][4] = {};
+    for (int i0 = 0; i0 < j.count; i0 += 8) {
+      const float w = exp2f((i0 ? log_sum(i0 + part) : e0) - base) * inv;
+      for (int i = i0; i < min(j.count, i0 + 8); ++i) {
+        float4 f[kWarpRows];
+        float wr[kWarpRows];
+#pragma unroll
+        for (int r = 0; r < kWarpRows; ++r) {
+          wr[r] = __shfl_sync(0xffffffffu, w, r * 8 + i - i0);
+          f[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (wr[r] != 0.f && d < D)  // a part without keys for this row holds nothing
+            f[r] = *reinterpret_cast<const float4*>(
+                p.part_o + at(i, min(row0 + r, j.rows - 1)) * D + d);
+        }
+#pragma unroll
+        for (int r = 0; r < kWarpRows; ++r) {
+          o[r][0] = fmaf(wr[r], f[r].x, o[r][0]);
+          o[r][1] = fmaf(wr[r], f[r].y, o[r][1]);
+          o[r][2] = fmaf(wr[r], f[r].z, o[r][2]);
+          o[r][3] = fmaf(wr[r], f[r].w, o[r][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r)
+      if (row0 + r < j.rows && d < D)
+        store4(static_cast<T*>(p.out) + out_row(row0 + r) * D + d, o[r]);
   }
 }
 
@@ -142,8 +162,9 @@ cudaError_t launch(const SoftmaxParams& p, int tile_tokens, int query_tiles, int
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (p.balanced) {
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(query_tiles * 128 / kJoinRows));
-    return cudaLaunchKernelEx(&cfg, join_pieces_kernel<T>, p, tile_tokens, query_tiles, grid);
+    if (grid < 2) return cudaSuccess;  // (one CTA: nothing is parted)
+    cfg.gridDim = dim3((unsigned)grid - 1, (unsigned)(query_tiles * 128 / kJoinRows));
+    return cudaLaunchKernelEx(&cfg, join_pieces_kernel<T>, p, tile_tokens * p.G, query_tiles);
   }
   int shift = 0;
   while (shift < 5 && (4 << shift) < p.c.D) ++shift;

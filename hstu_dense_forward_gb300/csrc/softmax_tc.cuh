@@ -245,8 +245,8 @@ __device__ void warp_scan(T* x, int n, int lane) {
   }
 }
 
-// The table of items (balanced runs), by the whole CTA; CTA 0 leaves a copy for the kernel that
-// joins pieces. The host has made sure that sequences and items fit.
+// The table of items (balanced runs), by the whole CTA. The host has made sure that sequences and
+// items fit.
 template <class C>
 __device__ void make_plan(const SoftmaxParams& p, PlanTable& pl) {
   const int tid = threadIdx.x, tokens = C::NQT * (128 / p.G);
@@ -281,12 +281,33 @@ __device__ void make_plan(const SoftmaxParams& p, PlanTable& pl) {
   if (tid < 32) warp_scan(pl.cost, items, tid);
   if (tid == 32) pl.items = items;
   __syncthreads();
-  if (blockIdx.x == 0) {
-    for (int x = tid; x <= items; x += C::THREADS) p.plan->cost[x] = pl.cost[x];
-    for (int x = tid; x < items; x += C::THREADS) p.plan->seq[x] = pl.seq[x];
-    for (int x = tid; x <= p.c.B; x += C::THREADS) p.plan->first[x] = pl.first[x];
-    if (tid == 0) p.plan->items = items;
-  }
+}
+
+// Whether an item is parted at the border in front of this CTA's share, and first there: what the
+// kernel that joins the pieces needs to know then.
+template <class C>
+__device__ JoinRecord join_record(const SoftmaxParams& p, const PlanTable& pl) {
+  JoinRecord j = {0, 0, 0, 0};
+  const int c = blockIdx.x;
+  const long long units = pl.cost[pl.items] * p.c.Nk;
+  const int ctas = share_ctas(units, gridDim.x);
+  if (units == 0 || c == 0 || c >= ctas) return j;
+  Walk w;
+  walk_begin<C>(p, pl, w);
+  const long long cost = pl.cost[w.e + 1] - pl.cost[w.e];
+  const long long base = pl.cost[w.e] * p.c.Nk + w.hk * cost;
+  // (a border in front of the item's tiles parts nothing)
+  if (w.u <= base + kItemCost || share(units, ctas, c - 1) > base + kItemCost) return j;
+  int last = c;
+  while (share(units, ctas, last + 1) < base + cost) ++last;
+  const int b = pl.seq[w.e], tokens = C::NQT * (128 / p.G);
+  const PagedSeq s = paged_seq(p.c, b);
+  const long long tok0 = (long long)(w.e - pl.first[b]) * tokens;
+  j.count = last - c + 2;
+  j.hk = w.hk;
+  j.rows = (int)min((long long)tokens, s.n - tok0) * p.G;
+  j.t0 = s.t0 + tok0;
+  return j;
 }
 
 // Place of K and V tiles in the ring's order: the order in which the MMA warp needs them.
@@ -1054,15 +1075,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), kTmemCols);
     ptx::tmem_relinquish();
   }
-  if (p.balanced) {
-    make_plan<C>(p, pl);
-    if (threadIdx.x == 0) {  // for the kernel that joins pieces
-      Walk w;
-      walk_begin<C>(p, pl, w);
-      p.plan->begin_item[blockIdx.x] = w.e;
-      p.plan->begin_head[blockIdx.x] = w.hk;
-    }
-  }
+  if (p.balanced) make_plan<C>(p, pl);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1085,6 +1098,8 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
     mma_drain(p, bars);
   } else if (warp == C::LOAD_WARP) {
     if (lane == 0) load_role<C>(p, bars, smem, pl, tiles, &tm_q, &tm_c);
+  } else if (warp == C::LOAD_WARP + 1) {
+    if (p.balanced && lane == 0) p.joins[blockIdx.x] = join_record<C>(p, pl);
   } else if (C::E4M3 && warp >= C::CONV_WARP) {
     const int w = warp - C::CONV_WARP;
     convert_role<C>(p, bars, smem, pl, tiles, w >= 4, w & 3, lane);

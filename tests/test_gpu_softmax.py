@@ -141,6 +141,54 @@ def test_chunks(cuda_device, dtype, mode, Nq, Nk, D, ps, causal):
     run_case(cuda_device, *CHUNK, dtype, mode, Nq, Nk, D, ps, causal=causal, seed=21)
 
 
+# prompts: 256 rows of a kv head in the mean and more, which run in pairs of row tiles; pairs whose
+# second tile is empty or partly filled, sequences of a few rows among them
+PROMPT = ([300, 129, 70, 700, 4, 0, 1000], [300, 64, 70, 331, 1, 0, 65])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,mode,Nq,Nk,D,ps", [
+    ("bf16", "same", 8, 2, 128, 128), ("fp16", "same", 6, 2, 64, 32), ("bf16", "scale", 8, 2, 128, 32),
+    ("fp16", "scale", 4, 1, 64, 128), ("bf16", "static", 5, 1, 96, 256), ("bf16", "same", 4, 1, 256, 32),
+    ("bf16", "scale", 3, 1, 32, 128), ("fp16", "cast", 7, 1, 128, 128), ("bf16", "scale", 4, 1, 256, 256),
+])
+def test_prompts(cuda_device, dtype, mode, Nq, Nk, D, ps, causal):
+    run_case(cuda_device, *PROMPT, dtype, mode, Nq, Nk, D, ps, causal=causal, seed=71)
+
+
+@pytest.mark.parametrize("dtype,mode,Nq,Nk,D,n", [
+    ("bf16", "same", 8, 2, 128, 75), ("fp16", "same", 16, 4, 64, 70), ("bf16", "scale", 8, 2, 128, 70),
+    ("fp16", "scale", 8, 2, 64, 66), ("bf16", "same", 16, 4, 256, 20), ("bf16", "same", 4, 4, 128, 30),
+    ("bf16", "scale", 4, 4, 80, 30), ("fp16", "scale", 16, 4, 256, 20),
+])
+def test_many_sequences(cuda_device, dtype, mode, Nq, Nk, D, n):
+    """More row tiles than CTAs can share out."""
+    g = torch.Generator().manual_seed(n)
+    B = 70
+    new = torch.randint(n // 2, n + n // 2, (B,), generator=g).tolist()
+    new[3], new[-1] = 0, 1
+    lengths = [m + h for m, h in zip(new, torch.randint(0, 200, (B,), generator=g).tolist())]
+    lengths[5], new[5] = 0, 0
+    run_case(cuda_device, lengths, new, dtype, mode, Nq, Nk, D, 32, seed=81)
+
+
+@pytest.mark.parametrize("n", [1, 5, 20])
+def test_more_sequences_than_a_table_holds(cuda_device, n):
+    B = 600
+    lengths = [(7 * b) % 61 + n for b in range(B)]
+    run_case(cuda_device, lengths, [n] * B, "bf16", "same", 4, 1, 64, 32, seed=91)
+
+
+@pytest.mark.parametrize("dtype,mode,n,Nq,D", [("bf16", "same", 300, 4, 128), ("bf16", "scale", 300, 4, 128),
+                                               ("fp16", "same", 270, 4, 64), ("fp16", "scale", 200, 4, 64),
+                                               ("bf16", "same", 7, 4, 128), ("fp16", "scale", 6, 4, 64),
+                                               ("bf16", "same", 30, 4, 256)])
+def test_items_over_many_ctas(cuda_device, dtype, mode, n, Nq, D):
+    """Few items with long keys: the keys of one are parted among more CTAs than a warp's eight
+    parts, beside a short sequence and an empty one."""
+    run_case(cuda_device, [7000, 3, 0, 600], [n, 3, 0, n // 3], dtype, mode, Nq, 2, D, 128, seed=101)
+
+
 @pytest.mark.parametrize("dtype,mode,G", [("bf16", "same", 1), ("fp16", "scale", 2), ("fp32", "same", 1),
                                           ("bf16", "scale", 16), ("fp16", "same", 24), ("bf16", "same", 128)])
 def test_more_queries_than_keys(cuda_device, dtype, mode, G):

@@ -126,6 +126,20 @@ struct AttnPlan {
   long long tiles, blocks, workspace, parts_bytes;
 };
 
+// Whether CTAs share few items' key tiles: one CTA per SM takes an equal share. With a CTA for each
+// item the longest takes its keys times the rounds of CTAs that the items make; shared out the
+// work takes the part of that which the SMs have in the mean (three quarters: sequences are
+// shorter than the bound), plus some 15 us for the items' table, for what borders part, and for
+// the second kernel, the time of 2000 keys (head dims above 128, whose key tiles hold half as
+// many: 3200). Measured so: two sequences of 300 tokens over 1300 keys 29 us alone, 32 shared,
+// over 2300 43 and 35, over 4400 72 and 41; 208 items of 8000 keys 128 and 107; but 270 items of
+// 3000 97 and 105: from 1.5 rounds on the SMs are filled well enough.
+bool parting_pays(long long keys, long long items, long long sms, int head_dim) {
+  const long long rounds = (items + sms - 1) / sms;
+  return items * 2 < 3 * sms &&
+         keys * (4 * rounds * sms - 3 * items) >= (head_dim > 128 ? 3200 : 2000) * 4 * sms;
+}
+
 hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, AttnPlan* pl) {
   const hstu_status st = check_cache(c);
   if (st != HSTU_OK) return st;
@@ -189,15 +203,14 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     const long long want = (4ll * sms + items - 1) / items;
     const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
     pl->splits = (int)(want < can ? want : can);
-  } else if (c->batch <= hstu::kMaxSeqs &&
-             a->total_tokens * G / bm + c->batch <= hstu::kMaxItems && items * 2 < 3ll * sms) {
-    // Few items: one CTA per SM takes an equal share of their key tiles (a CTA for each item and
-    // this: 208 items of two sequences of 8000 keys 128 and 107 us, 185 of 16 of 4500 142 and
-    // 121; but 270 of four of 3000 97 and 105, which fill the SMs well enough)
+  } else if (c->batch <= hstu::kMaxSeqs && a->total_tokens * G / bm + c->batch <= hstu::kMaxItems &&
+             parting_pays(a->max_seqlen_k, items, sms, c->head_dim)) {
     pl->balanced = 1;
     pl->blocks = sms;
     pl->parts_bytes = 2ll * sms * pl->qtiles * 128 * (c->head_dim + 1) * 4;
     pl->workspace = pl->parts_bytes + sms * (long long)sizeof(hstu::JoinRecord);
+  } else if (a->max_seqlen_k <= 0 && pl->blocks > sms) {
+    pl->blocks = sms;
   }
   if (pl->splits > 1) {
     pl->parts_bytes = (long long)pl->splits * a->total_tokens * a->num_heads_q *

@@ -159,14 +159,15 @@ __device__ __forceinline__ void fill_seg(const SoftmaxParams& p, int b, int tile
 
 // The pieces that this CTA works on, in order. Every role walks them by itself.
 struct Walk {
-  long long u, end;  // units left
-  int e, hk;         // item pair (sequence, tile) and kv head at u
+  long long u, end;  // units (of a share) or items left
+  int e, hk;         // of a share: item pair (sequence, tile) and kv head at u
 };
 
 template <class C>
-__device__ __forceinline__ void walk_begin(const SoftmaxParams& p, const PlanTable& pl, Walk& w) {
-  w.u = 0;
-  w.end = 1;  // one item per CTA: one unit
+__device__ __forceinline__ void walk_begin(const SoftmaxParams& p, const PlanTable& pl, int tiles,
+                                           Walk& w) {
+  w.u = blockIdx.x;  // items of their own: every gridDim.x-th
+  w.end = (long long)p.c.B * tiles * p.c.Nk;
   w.e = w.hk = 0;
   if (!p.balanced) return;
   const int items = pl.items;
@@ -192,19 +193,21 @@ template <class C>
 __device__ __forceinline__ bool walk_next(const SoftmaxParams& p, const PlanTable& pl, Walk& w,
                                        int tiles, Seg& g) {
   if (!p.balanced) {
-    if (w.u) return false;
-    w.u = 1;
-    const long long blk = blockIdx.x;
-    const int tile = tiles - 1 - (int)(blk / p.c.Nk % tiles);  // later tiles see more keys: first
-    const int b = (int)(blk / p.c.Nk / tiles);
-    const PagedSeq s = paged_seq(p.c, b);
-    if (!attn_seq_ok(p, s)) {
-      if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
-      return false;
+    while (w.u < w.end) {
+      const uint32_t blk = (uint32_t)w.u, pair = blk / (uint32_t)p.c.Nk;  // (fit 31 bits)
+      w.u += gridDim.x;
+      const int tile = tiles - 1 - (int)(pair % tiles);  // later tiles see more keys: first
+      const int b = (int)(pair / tiles), hk = (int)(blk - pair * p.c.Nk);
+      const PagedSeq s = paged_seq(p.c, b);
+      if (!attn_seq_ok(p, s)) {
+        if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+        continue;
+      }
+      if ((long long)tile * C::NQT * (128 / p.G) >= s.n) continue;
+      fill_seg<C>(p, b, tile, hk, 0, item_tiles<C>(p, s, tile), -1, g);
+      return true;
     }
-    if ((long long)tile * C::NQT * (128 / p.G) >= s.n) return false;
-    fill_seg<C>(p, b, tile, (int)(blk % p.c.Nk), 0, item_tiles<C>(p, s, tile), -1, g);
-    return true;
+    return false;
   }
   while (w.u < w.end) {
     const long long cost = pl.cost[w.e + 1] - pl.cost[w.e];
@@ -286,14 +289,14 @@ __device__ void make_plan(const SoftmaxParams& p, PlanTable& pl) {
 // Whether an item is parted at the border in front of this CTA's share, and first there: what the
 // kernel that joins the pieces needs to know then.
 template <class C>
-__device__ JoinRecord join_record(const SoftmaxParams& p, const PlanTable& pl) {
+__device__ JoinRecord join_record(const SoftmaxParams& p, const PlanTable& pl, int tiles) {
   JoinRecord j = {0, 0, 0, 0};
   const int c = blockIdx.x;
   const long long units = pl.cost[pl.items] * p.c.Nk;
   const int ctas = share_ctas(units, gridDim.x);
   if (units == 0 || c == 0 || c >= ctas) return j;
   Walk w;
-  walk_begin<C>(p, pl, w);
+  walk_begin<C>(p, pl, tiles, w);
   const long long cost = pl.cost[w.e + 1] - pl.cost[w.e];
   const long long base = pl.cost[w.e] * p.c.Nk + w.hk * cost;
   // (a border in front of the item's tiles parts nothing)
@@ -408,7 +411,7 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
   uint32_t ring = 0, queries = 0;
   Walk w;
   Seg it;
-  walk_begin<C>(p, pl, w);
+  walk_begin<C>(p, pl, tiles, w);
   while (walk_next<C>(p, pl, w, tiles, it)) {
     const int nmax = it.nmax;
     for (int i = 0; i < 2 * nmax; ++i) {
@@ -484,7 +487,7 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
   uint32_t ring = 0, done = 0;
   Walk walk;
   Seg it;
-  walk_begin<C>(p, pl, walk);
+  walk_begin<C>(p, pl, tiles, walk);
   while (walk_next<C>(p, pl, walk, tiles, it)) {
     for (int x = 0; x < 2 * it.nmax; ++x) {
       int t;
@@ -570,27 +573,36 @@ __device__ float query_to_tmem(const SoftmaxParams& p, uint32_t col, bool any, b
                                long long at) {
   if (!any) return 1.0f;
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
+  const int pieces = valid ? p.c.D / 8 : 0;  // of 16 bytes, eight at a time in flight
   int sh = 0;
-  if (BF16 && C::E4M3 && valid) {
+  if constexpr (BF16 && C::E4M3) {
     uint32_t top = 0;
-#pragma unroll 4
-    for (int x = 0; x < p.c.D / 8; ++x) top = larger_magnitude(top, q[x]);
+#pragma unroll 1
+    for (int x0 = 0; x0 < C::D / 8; x0 += 8) {
+      uint4 u[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) u[x] = x0 + x < pieces ? q[x0 + x] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) top = larger_magnitude(top, u[x]);
+    }
     sh = row_shift(top);
   }
   const float mul = power2(sh);
-#pragma unroll 2
-  for (int x = 0; x < C::D / 8; x += 2) {
-    uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (valid && x < p.c.D / 8) {
-      u[0] = q[x];
-      u[1] = q[x + 1];
-    }
-    uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-    if constexpr (BF16 && C::E4M3) {
+#pragma unroll 1
+  for (int x0 = 0; x0 < C::D / 8; x0 += 8) {
+    uint4 u[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = bf16_to_half(w[e], mul);
+    for (int x = 0; x < 8; ++x) u[x] = x0 + x < pieces ? q[x0 + x] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int x = 0; x < 8; x += 2) {
+      uint32_t w[8] = {u[x].x,     u[x].y,     u[x].z,     u[x].w,
+                       u[x + 1].x, u[x + 1].y, u[x + 1].z, u[x + 1].w};
+      if constexpr (BF16 && C::E4M3) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = bf16_to_half(w[e], mul);
+      }
+      ptx::tmem_st8(col + (x0 + x) * 4, w);
     }
-    ptx::tmem_st8(col + x * 4, w);
   }
   ptx::tmem_st_wait();
   return power2(-sh);
@@ -704,7 +716,7 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
   uint32_t outputs[2] = {0, 0};  // pieces of it that had any
   Walk w;
   Seg it;
-  walk_begin<C>(p, pl, w);
+  walk_begin<C>(p, pl, tiles, w);
   while (walk_next<C>(p, pl, w, tiles, it)) {
     const int n = __shfl_sync(0xffffffffu, it.nmax, 0);
     if (n == 0) continue;
@@ -824,7 +836,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
   uint32_t g = 0;                            // key tiles of this query tile before this piece
   Walk walk;
   Seg it;
-  walk_begin<C>(p, pl, walk);
+  walk_begin<C>(p, pl, tiles, walk);
   for (; walk_next<C>(p, pl, walk, tiles, it); ring += 2 * it.nmax, done += it.nmax) {
     float fk = p.scale_log2, fv = 1.0f;  // static factors fold into the scale and the output
     const long long tok = it.tok0 + (long long)q * tpt + r / p.G;
@@ -1099,7 +1111,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   } else if (warp == C::LOAD_WARP) {
     if (lane == 0) load_role<C>(p, bars, smem, pl, tiles, &tm_q, &tm_c);
   } else if (warp == C::LOAD_WARP + 1) {
-    if (p.balanced && lane == 0) p.joins[blockIdx.x] = join_record<C>(p, pl);
+    if (p.balanced && lane == 0) p.joins[blockIdx.x] = join_record<C>(p, pl, tiles);
   } else if (C::E4M3 && warp >= C::CONV_WARP) {
     const int w = warp - C::CONV_WARP;
     convert_role<C>(p, bars, smem, pl, tiles, w >= 4, w & 3, lane);

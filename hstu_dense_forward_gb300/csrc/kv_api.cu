@@ -163,8 +163,11 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   // query rows (token, head) of one item: a CTA's, or a cluster's
   long long bm;
   if (a->dtype == HSTU_F32) {
+    // up to 16 rows in CTAs of four, which read the keys' rows straight into registers (tiles of
+    // 16 rows in shared memory instead: 128 sequences of one token and eight heads 1334 us, now
+    // 303; with 16 rows a kv head 235 and 148, over E4M3 221 and 242)
     pl->kernel = AttnPlan::SIMT;
-    pl->rows = most * G <= 16 ? 16 : 64;
+    pl->rows = most * G <= 16 ? 4 : 64;
     bm = pl->rows;
   } else if (most * G <= 16) {
     pl->kernel = AttnPlan::ROWS;
@@ -200,7 +203,9 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     pl->min_range = 128 * pl->cluster;
   } else if (pl->kernel == AttnPlan::SIMT) {
     pl->min_range = 128;
-    const long long want = (4ll * sms + items - 1) / items;
+    // resident CTAs: four an SM; of four rows three, in two waves (25 sequences of some 7500 keys,
+    // five rows: 166 us with one wave, 142 with two, 146 with four)
+    const long long want = ((pl->rows == 64 ? 4ll : 6ll) * sms + items - 1) / items;
     const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
     pl->splits = (int)(want < can ? want : can);
   } else if (c->batch <= hstu::kMaxSeqs && a->total_tokens * G / bm + c->batch <= hstu::kMaxItems &&

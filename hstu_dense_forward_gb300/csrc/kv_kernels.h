@@ -27,7 +27,7 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
                            long long v_stride, int dtype, bool e4m3, bool append, int sms,
                            cudaStream_t stream);
 
-// fp32 attention on CUDA cores: `rows` (16 or 64) packed query rows of one kv head per CTA.
+// fp32 attention on CUDA cores: `rows` (4 or 64) packed query rows of one kv head per CTA.
 cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream);
 

@@ -1,16 +1,21 @@
-// fp32 softmax attention over the paged KV cache on CUDA cores (FFMA), and the
-// kernel that joins the key ranges of sequences worked on in parts.
-//
-// One CTA (256 threads, 16 x 16) takes BM packed query rows of one kv head (packed row r of a
-// sequence is query token r / G, head hk * G + r % G, so that the G heads that share a kv head
-// share its loads) and one range of the keys, in steps of BN keys, with the running maximum m
+// fp32 softmax attention over the paged KV cache on CUDA cores (FFMA), with the running maximum m
 // and sum l of the softmax in base 2:
 //   x = scale_log2 * Q K^T, m' = max(m, x), P = 2^(x - m'), l = 2^(m - m') l + sum P,
 //   O = 2^(m - m') O + P V,                        out = O / l, log2 of the sum = m + log2 l.
-// A thread owns rows ty + 16 a, of the scores keys tx + 16 c and of the output columns
-// 4 tx + 64 u .. + 3; every operand comes from shared memory in float4 (four elements of the
-// head dim, or four keys), so that a step spends four times as many FMAs as loads. BM = 16
-// serves few rows, where reading the cache is what counts.
+// A CTA takes packed query rows of one kv head (packed row r of a sequence is query token r / G,
+// head hk * G + r % G, so that the G heads that share a kv head share its loads) and one range of
+// the keys; a second kernel joins the ranges.
+//
+// softmax_simt_kernel: 64 rows, 256 threads (16 x 16), in steps of BN keys. A thread owns rows
+// ty + 16 a, of the scores keys tx + 16 c and of the output columns 4 tx + 64 u .. + 3; every
+// operand comes from shared memory in float4 (four elements of the head dim, or four keys), so
+// that a step spends four times as many FMAs as loads.
+//
+// softmax_few_kernel: 4 rows, for calls of at most 16, where reading the cache is what counts:
+// D / 16 lanes hold a key, two keys at a time, straight from the cache in registers, and every
+// group of lanes keeps a softmax of its own keys until the end. 128 sequences of one token over
+// some 1500 keys of eight heads, D = 128: 303 us, 5.2 TB/s; what keeps it from the memory's rate
+// are the instructions (E4M3 rows, a quarter of the bytes, take longer: 515 us).
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -26,9 +31,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int D_, int BM_, bool E4M3>
+template <int D_, bool E4M3>
 struct Cfg {
-  static constexpr int D = D_, BM = BM_;
+  static constexpr int D = D_, BM = 64;
   static constexpr int BN = D == 64 ? 64 : 32;  // (at D = 256 what shared memory holds)
   static constexpr int RA = BM / 16, CK = BN / 16, U = D / 64;
   static constexpr int LD = D + 4, LDP = BN + 4;  // padded rows: conflict-free float4 reads
@@ -57,10 +62,10 @@ __device__ __forceinline__ float dot4(const float4& a, const float4& b, float s)
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
 }
 
-template <int D_, int BM, bool E4M3>
+template <int D_, bool E4M3>
 __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxParams p, int tiles) {
-  using C = Cfg<D_, BM, E4M3>;
-  constexpr int BN = C::BN;
+  using C = Cfg<D_, E4M3>;
+  constexpr int BM = C::BM, BN = C::BN;
   extern __shared__ float sm[];
   const int D = p.c.D;
   float* Qs = sm;             // [BM][LD]
@@ -241,11 +246,269 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
   }
 }
 
-template <int D, int BM, bool E4M3>
-cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
+constexpr int kFewRows = 4, kFewThreads = 128;
+
+// Sixteen elements of a key that lane j of its group holds, as four float4: E4M3 elements
+// 16 j .., fp32 ones 4 (j + i D / 16) .. in piece i, so that a group's loads are contiguous.
+// E4M3 elements stay codes until they are used (with their row's scale, which multiplies a score
+// and a weight instead of every element), so that more of them are on their way at a time.
+template <bool E4M3>
+struct FewRow;
+template <>
+struct FewRow<false> {
+  float4 x[4];
+  template <int D_>
+  __device__ __forceinline__ void load(const SoftmaxParams& p, int page, int plane, int row,
+                                       int hk, int j) {
+    const float* at = static_cast<const float*>(p.c.cache) + cache_row(p.c, page, plane, row, hk);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = 4 * (j + i * (D_ / 16));
+      x[i] = page >= 0 && d < p.c.D ? *reinterpret_cast<const float4*>(at + d)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float4 (&f)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = x[i];
+  }
+  __device__ __forceinline__ float factor() const { return 1.f; }
+};
+template <>
+struct FewRow<true> {
+  uint4 x;
+  uint8_t scale;
+  template <int D_>
+  __device__ __forceinline__ void load(const SoftmaxParams& p, int page, int plane, int row,
+                                       int hk, int j) {
+    x = make_uint4(0u, 0u, 0u, 0u);
+    scale = 127;
+    if (page < 0) return;
+    if (16 * j < p.c.D)
+      x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.c.cache) +
+                                          cache_row(p.c, page, plane, row, hk) + 16 * j);
+    if (p.c.scale) scale = p.c.scale[scale_row(p.c, page, plane, row, hk)];
+  }
+  __device__ __forceinline__ void get(float4 (&f)[4]) const {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo, hi;
+      e4m3x4_to_f16x2(w[i], lo, hi);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      f[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
+  __device__ __forceinline__ float factor() const { return scale_value(scale); }
+};
+// First of the four elements in piece i of lane j.
+template <int D_, bool E4M3>
+__device__ __forceinline__ int few_dim(int i, int j) {
+  return E4M3 ? 16 * j + 4 * i : 4 * (j + i * (D_ / 16));
+}
+
+template <int D_, bool E4M3>
+__global__ void __launch_bounds__(kFewThreads, 3) softmax_few_kernel(const SoftmaxParams p,
+                                                                     int tiles) {
+  constexpr int R = kFewRows, U = E4M3 ? 4 : 2, LPK = D_ / 16, KW = 32 / LPK;
+  constexpr int WARPS = kFewThreads / 32, STEP = WARPS * U * KW;  // keys of a step
+  __shared__ float4 qs[R][4][LPK];
+  __shared__ float part_o[WARPS][R][D_], part_m[WARPS][R], part_l[WARPS][R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = lane % LPK, g = lane / LPK;
+  const uint32_t blk = blockIdx.x;
+  const int hk = (int)(blk % (uint32_t)p.c.Nk);
+  const int tile = tiles - 1 - (int)(blk / (uint32_t)p.c.Nk % (uint32_t)tiles);
+  const int b = (int)(blk / (uint32_t)p.c.Nk / (uint32_t)tiles), split = blockIdx.y;
+  const PagedSeq s = paged_seq(p.c, b);
+  if (!attn_seq_ok(p, s)) {
+    if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+    return;
+  }
+  const long long rows = s.n * p.G, m0 = (long long)tile * R;
+  const KeyRanges kr = key_ranges(p, s.Lk);
+  if (m0 >= rows || split >= kr.count) return;
+  // keys any row of the tile may see, within the range
+  long long kend = s.Lk;
+  if (p.causal) kend = min(kend, s.Lk - s.n + (min(m0 + R, rows) - 1) / p.G + 1);
+  const long long k0 = split * kr.keys;
+  kend = min(kend, k0 + kr.keys);
+
+  const float* q = static_cast<const float*>(p.q);
+  for (int x = threadIdx.x; x < R * 4 * LPK; x += kFewThreads) {
+    const int r = x / (4 * LPK), i = x / LPK % 4, d = few_dim<D_, E4M3>(i, x % LPK);
+    const long long pr = m0 + r;
+    qs[r][i][x % LPK] = pr < rows && d < p.c.D
+        ? *reinterpret_cast<const float4*>(q + (s.t0 + pr / p.G) * p.q_stride +
+                                           (hk * p.G + pr % p.G) * (long long)p.c.D + d)
+        : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float fk = p.scale_log2, fv = 1.f;  // static factors fold into the scale and the output
+  if (p.c.k_ds) {
+    fk *= p.c.k_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
+    fv = p.c.v_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
+  }
+  __syncthreads();
+  float m[R], l[R];
+  float4 acc[R][4];
+  const int keys = (int)(kend - k0);
+  int lim[R];  // keys of the range that each row sees: [0, lim)
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -CUDART_INF_F;
+    l[r] = 0.f;
+    const long long pr = m0 + r;
+    const long long see = pr >= rows ? k0 : p.causal ? s.Lk - s.n + pr / p.G + 1 : s.Lk;
+    lim[r] = (int)(min(see, kend) - k0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const int mine = warp * U * KW + g;  // this group's keys of a step: mine, mine + KW
+  auto page_of = [&](int n) { return n < keys ? (int)page_at(p.c, s, k0 + n) : -1; };
+  int next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) next[u] = page_of(mine + u * KW);
+  for (int n0 = 0; n0 < keys; n0 += STEP) {
+    FewRow<E4M3> k[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + mine + u * KW, row = (int)(k0 + n) & (int)(page_size(p.c) - 1);
+      const int page = next[u];
+      if (page < 0 && n < keys) report(p.c, HSTU_DEVERR_OFFSETS);  // (a row of zeros then)
+      k[u].template load<D_>(p, page, 0, row, hk, j);
+      v[u].template load<D_>(p, page, 1, row, hk, j);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) next[u] = page_of(n0 + STEP + mine + u * KW);
+    float x[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float4 f[4];
+      k[u].get(f);
+      const float fu = fk * k[u].factor();
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        x[u][r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[u][r] = dot4(qs[r][i][j], f[i], x[u][r]);
+#pragma unroll
+        for (int d = 1; d < LPK; d <<= 1) x[u][r] += __shfl_xor_sync(0xffffffffu, x[u][r], d);
+        x[u][r] = n0 + mine + u * KW < lim[r] ? x[u][r] * fu : -CUDART_INF_F;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = m[r];
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = fmaxf(top, x[u][r]);
+      const float base = top == -CUDART_INF_F ? 0.f : top;  // no key yet: weights 2^-inf = 0
+      if (__any_sync(0xffffffffu, top > m[r])) {
+        const float corr = exp2f(m[r] - base);
+        l[r] *= corr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[r][i].x *= corr;
+          acc[r][i].y *= corr;
+          acc[r][i].z *= corr;
+          acc[r][i].w *= corr;
+        }
+        m[r] = top;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u][r] = exp2f(x[u][r] - base);
+        l[r] += x[u][r];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float4 f[4];
+      v[u].get(f);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float w = x[u][r] * v[u].factor();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[r][i].x = fmaf(w, f[i].x, acc[r][i].x);
+          acc[r][i].y = fmaf(w, f[i].y, acc[r][i].y);
+          acc[r][i].z = fmaf(w, f[i].z, acc[r][i].z);
+          acc[r][i].w = fmaf(w, f[i].w, acc[r][i].w);
+        }
+      }
+    }
+  }
+  // the warp's groups, then the CTA's warps
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float top = m[r];
+#pragma unroll
+    for (int d = LPK; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float corr = exp2f(m[r] - (top == -CUDART_INF_F ? 0.f : top));
+    l[r] *= corr;
+#pragma unroll
+    for (int d = LPK; d < 32; d <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float e[4] = {acc[r][i].x * corr, acc[r][i].y * corr, acc[r][i].z * corr, acc[r][i].w * corr};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int d = LPK; d < 32; d <<= 1) e[c] += __shfl_xor_sync(0xffffffffu, e[c], d);
+      if (g == 0)
+        *reinterpret_cast<float4*>(&part_o[warp][r][few_dim<D_, E4M3>(i, j)]) =
+            make_float4(e[0], e[1], e[2], e[3]);
+    }
+    if (lane == 0) {
+      part_m[warp][r] = top;
+      part_l[warp][r] = l[r];
+    }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < R * (D_ / 4); x += kFewThreads) {
+    const int r = x / (D_ / 4), d = x % (D_ / 4) * 4;
+    const long long pr = m0 + r;
+    if (pr >= rows || d >= p.c.D) continue;
+    float top = part_m[0][r];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) top = fmaxf(top, part_m[w][r]);
+    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float c = exp2f(part_m[w][r] - (top == -CUDART_INF_F ? 0.f : top));
+      const float4 f = *reinterpret_cast<const float4*>(&part_o[w][r][d]);
+      sum = fmaf(part_l[w][r], c, sum);
+      o[0] = fmaf(f.x, c, o[0]);
+      o[1] = fmaf(f.y, c, o[1]);
+      o[2] = fmaf(f.z, c, o[2]);
+      o[3] = fmaf(f.w, c, o[3]);
+    }
+    const long long row = (s.t0 + pr / p.G) * p.Nq + hk * p.G + pr % p.G;  // of out and lse
+    const float inv = sum > 0.f ? fv / sum : sum;  // (a NaN sum stays one)
+    float* dst = kr.count > 1 ? p.part_o + ((long long)split * p.c.T * p.Nq + row) * p.c.D
+                              : static_cast<float*>(p.out) + row * p.c.D;
+    *reinterpret_cast<float4*>(dst + d) =
+        make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    if (d == 0) {
+      const float log2sum = sum == 0.f ? -CUDART_INF_F : top + log2f(sum);
+      if (kr.count > 1)
+        p.part_lse[(long long)split * p.c.T * p.Nq + row] = log2sum;
+      else if (p.lse)
+        p.lse[row] = log2sum * kLn2;
+    }
+  }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const SoftmaxParams& p, int rows, long long tiles, long long blocks,
                    cudaStream_t stream) {
-  using C = Cfg<D, BM, E4M3>;
-  auto* kernel = softmax_simt_kernel<D, BM, E4M3>;
+  if (rows == kFewRows) {
+    softmax_few_kernel<D, E4M3>
+        <<<dim3((unsigned)blocks, p.splits), kFewThreads, 0, stream>>>(p, (int)tiles);
+    return cudaGetLastError();
+  }
+  using C = Cfg<D, E4M3>;
+  auto* kernel = softmax_simt_kernel<D, E4M3>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
@@ -253,23 +516,20 @@ cudaError_t launch(const SoftmaxParams& p, long long tiles, long long blocks,
   return cudaGetLastError();
 }
 
-template <int BM, bool E4M3>
-cudaError_t launch_dim(const SoftmaxParams& p, long long tiles, long long blocks,
+template <bool E4M3>
+cudaError_t launch_dim(const SoftmaxParams& p, int rows, long long tiles, long long blocks,
                        cudaStream_t stream) {
-  if (p.c.D > 128) return launch<256, BM, E4M3>(p, tiles, blocks, stream);
-  if (p.c.D > 64) return launch<128, BM, E4M3>(p, tiles, blocks, stream);
-  return launch<64, BM, E4M3>(p, tiles, blocks, stream);
+  if (p.c.D > 128) return launch<256, E4M3>(p, rows, tiles, blocks, stream);
+  if (p.c.D > 64) return launch<128, E4M3>(p, rows, tiles, blocks, stream);
+  return launch<64, E4M3>(p, rows, tiles, blocks, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream) {
-  if (rows == 16)
-    return e4m3 ? launch_dim<16, true>(p, tiles, blocks, stream)
-                : launch_dim<16, false>(p, tiles, blocks, stream);
-  return e4m3 ? launch_dim<64, true>(p, tiles, blocks, stream)
-              : launch_dim<64, false>(p, tiles, blocks, stream);
+  return e4m3 ? launch_dim<true>(p, rows, tiles, blocks, stream)
+              : launch_dim<false>(p, rows, tiles, blocks, stream);
 }
 
 }  // namespace hstu

@@ -165,7 +165,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   if (a->dtype == HSTU_F32) {
     // up to 16 rows in CTAs of four, which read the keys' rows straight into registers (tiles of
     // 16 rows in shared memory instead: 128 sequences of one token and eight heads 1334 us, now
-    // 303; with 16 rows a kv head 235 and 148, over E4M3 221 and 242)
+    // 288; with 16 rows a kv head 235 and 136, over E4M3 221 and 145)
     pl->kernel = AttnPlan::SIMT;
     pl->rows = most * G <= 16 ? 4 : 64;
     bm = pl->rows;
@@ -214,7 +214,10 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     pl->blocks = sms;
     pl->parts_bytes = 2ll * sms * pl->qtiles * 128 * (c->head_dim + 1) * 4;
     pl->workspace = pl->parts_bytes + sms * (long long)sizeof(hstu::JoinRecord);
-  } else if (a->max_seqlen_k <= 0 && pl->blocks > sms) {
+  } else if (pl->qtiles == 1 && a->max_seqlen_k <= 256 && pl->blocks > sms) {
+    // short keys: a CTA takes several items, whose first loads and last stores overlap (100
+    // sequences of up to 20 rows over 120 keys, four heads: 25.8 us, with a CTA for each item
+    // 28.5; but of up to 600 keys, uneven items, 51 and 48.5 over E4M3)
     pl->blocks = sms;
   }
   if (pl->splits > 1) {

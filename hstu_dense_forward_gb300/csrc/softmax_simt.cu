@@ -14,8 +14,8 @@
 // softmax_few_kernel: 4 rows, for calls of at most 16, where reading the cache is what counts:
 // D / 16 lanes hold a key, two keys at a time, straight from the cache in registers, and every
 // group of lanes keeps a softmax of its own keys until the end. 128 sequences of one token over
-// some 1500 keys of eight heads, D = 128: 303 us, 5.2 TB/s; what keeps it from the memory's rate
-// are the instructions (E4M3 rows, a quarter of the bytes, take longer: 515 us).
+// some 1500 keys of eight heads, D = 128: 288 us, 5.6 TB/s; over E4M3 rows, a quarter of the
+// bytes, the instructions bound it: 281 us (with two keys at a time 546, its loads too few).
 #include <math_constants.h>
 
 #include "common.cuh"

@@ -447,7 +447,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
               for (int e = 0; e < 4; ++e) o[i][x][e] *= corr[e & 1];
           }
         }
-        uint32_t pb[NT][2];  // P^T fragments: keys 2c, 2c + 1 (and + 8) of row g
+        // P^T fragments: keys 2c, 2c + 1 (and + 8) of row g. bf16 weights come with what their
+        // rounding leaves, for a product of its own: rounded to 2^-8 alone they are as far off as
+        // the output's rounding, and the cache's loads leave time for twice the products (four
+        // sequences of 100k keys: 74.0 us with one, 74.1 with both; 32 of eight heads 55.6 and 57.0).
+        constexpr int PARTS = C::MMA_BF16 ? 2 : 1;
+        uint32_t pb[PARTS][NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           const float b0 = m[i][0] == -CUDART_INF_F ? 0.0f : m[i][0];
@@ -457,7 +462,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
             const float p0 = ex2(sc[i][2 * x] - b0), p1 = ex2(sc[i][2 * x + 1] - b1);
             l[i][0] = fmaf(p0, ve[x], l[i][0]);
             l[i][1] = fmaf(p1, ve[x], l[i][1]);
-            pb[i][x] = transpose8(pack2<C::MMA_BF16>(p0, p1));
+            const uint32_t w = pack2<C::MMA_BF16>(p0, p1);
+            pb[0][i][x] = transpose8(w);
+            if constexpr (C::MMA_BF16)
+              pb[1][i][x] = transpose8(pack2<true>(p0 - __uint_as_float(w << 16),
+                                                   p1 - __uint_as_float(w & 0xffff0000u)));
           }
         }
         const uint8_t* vt = kt + C::PLANE;
@@ -500,7 +509,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
                 e4m3x4_to_f16x2(__byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                  mma<false>(o[i][cb * C::NV / 2 + 2 * w + e], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+                  mma<false>(o[i][cb * C::NV / 2 + 2 * w + e], a0, a1, a2, a3, pb[0][i][0],
+                             pb[0][i][1]);
               }
             } else {
               const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
@@ -509,7 +519,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
               const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
 #pragma unroll
               for (int i = 0; i < NT; ++i)
-                mma<C::MMA_BF16>(o[i][cb * C::NV / 2 + w], a0, a1, a2, a3, pb[i][0], pb[i][1]);
+#pragma unroll
+                for (int h = 0; h < PARTS; ++h)
+                  mma<C::MMA_BF16>(o[i][cb * C::NV / 2 + w], a0, a1, a2, a3, pb[h][i][0],
+                                   pb[h][i][1]);
             }
           }
         }

@@ -4,7 +4,6 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <cmath>
 
 #include "../../include/hstu_kv.h"
 #include "kv_cache.cuh"
@@ -149,7 +148,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     return HSTU_ERR_INVALID_ARG;
   if (a->max_seqlen < 1 || a->max_seqlen > (1 << 24) || a->max_seqlen_k < 1 ||
       a->max_seqlen_k > (1 << 30) || (a->causal != 0 && a->causal != 1) ||
-      !std::isfinite(a->alpha) || !(a->alpha > 0.0f))
+      !(a->alpha > 0.0f) || !(a->alpha <= 2e38f))  // (times log2 e it stays finite)
     return HSTU_ERR_INVALID_ARG;
   const long long G = a->num_heads_q / c->num_heads_kv;
   if (G > 128) return HSTU_ERR_UNSUPPORTED;

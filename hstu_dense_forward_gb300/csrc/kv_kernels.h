@@ -33,7 +33,6 @@ cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, lon
 
 // Tensor-core attention (bf16, fp16). A CTA takes qtiles tiles of 128 / G tokens; two where
 // D <= 128 only.
-int softmax_tc_key_tile(int D);  // keys of one tile
 cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles,
                               long long tiles, long long blocks, cudaStream_t stream);
 

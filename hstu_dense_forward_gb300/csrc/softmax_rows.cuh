@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
         // P^T fragments: keys 2c, 2c + 1 (and + 8) of row g. bf16 weights come with what their
         // rounding leaves, for a product of its own: rounded to 2^-8 alone they are as far off as
         // the output's rounding, and the cache's loads leave time for twice the products (four
-        // sequences of 100k keys: 74.0 us with one, 74.1 with both; 32 of eight heads 55.6 and 57.0).
+        // sequences of 100k keys: 74.0 us with one, 74.1 with both; 32 of 2500 keys and eight
+        // heads 55.6 and 57.0).
         constexpr int PARTS = C::MMA_BF16 ? 2 : 1;
         uint32_t pb[PARTS][NT][2];
 #pragma unroll

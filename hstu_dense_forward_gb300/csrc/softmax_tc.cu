@@ -76,24 +76,25 @@ cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, in
              : launch_softmax_rows_fp16(p, e4m3, tc, rows, tiles, blocks, cluster, stream);
 }
 
-int softmax_tc_key_tile(int D) { return kernel_dim(D) == 256 ? 64 : 128; }
-
 cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles,
                               long long tiles, long long blocks, cudaStream_t stream) {
   const EncodeTiledFn encode = encode_fn();
   if (!encode) return cudaErrorNotSupported;
-  CUtensorMap tq, tc;
-  // queries: the G heads of one kv head of 128 / G tokens make one tile of packed rows
-  const cuuint64_t dims[3] = {(cuuint64_t)p.c.D, (cuuint64_t)p.Nq, (cuuint64_t)p.c.T};
-  const cuuint64_t strides[2] = {(cuuint64_t)p.c.D * 2, (cuuint64_t)p.q_stride * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
-  const cuuint32_t one[3] = {1, 1, 1};
-  if (encode(&tq, elem_type(dtype), 3, const_cast<void*>(p.q), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  CUtensorMap tq = {}, tc;
+  if (kernel_dim(p.c.D) == 128 && qtiles == 2) {  // the variant whose queries come by TMA:
+    // the G heads of one kv head of 128 / G tokens make one tile of packed rows
+    const cuuint64_t dims[3] = {(cuuint64_t)p.c.D, (cuuint64_t)p.Nq, (cuuint64_t)p.c.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.c.D * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(128 / p.G)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    if (encode(&tq, elem_type(dtype), 3, const_cast<void*>(p.q), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
   // E4M3 rows are staged whole and unswizzled
-  const int kt = softmax_tc_key_tile(p.c.D);
+  const int kt = kernel_dim(p.c.D) == 256 ? 64 : 128;
   if (!cache_map(&tc, p, dtype, e4m3, e4m3 ? kernel_dim(p.c.D) : 64, kt, e4m3 ? 0 : 128))
     return cudaErrorInvalidValue;
   if (dtype == HSTU_BF16)

@@ -14,11 +14,13 @@
 // running sum of the items' tiles (plus kItemCost for what an item costs by itself) and works on
 // one contiguous piece of it, which may begin and end inside an item. An item in several pieces
 // leaves its pieces' outputs and sums in the workspace, and a second kernel joins them. With
-// many items each CTA takes one. Warp roles:
-//   warps 0 .. 4 NQT - 1   softmax, one warpgroup per query tile, one thread per row;
+// many items each CTA takes one (over short keys several). Warp roles:
+//   warps 0 .. 4 NQT - 1   softmax, one warpgroup per query tile, one thread per row; they also
+//                          write Q to TMEM (where it does not come by TMA) and the output;
 //   next warp              issues every tcgen05.mma; owns TMEM;
-//   next warp              TMA loads: Q, then K and V tiles through one ring, in the order
-//                          in which the products need them;
+//   next warp              TMA loads: K and V tiles through one ring, in the order in which the
+//                          products need them (and Q where TMEM has no room for it);
+//   next warp              a balanced run's record for the joining kernel;
 //   E4M3: eight more warps turn E4M3 tiles (staged by TMA) into fp16 ones in the ring, four
 //                          the keys and four the values (one warpgroup for both took 2750
 //                          cycles a tile, longer than the products).
@@ -78,8 +80,8 @@ struct Cfg {
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1;
   static constexpr int CONV_WARP = SM_WARPS + 4;  // (a warpgroup each for K and V)
   static constexpr int THREADS = (SM_WARPS + 4 + (E4M3 ? 8 : 0)) * 32;
-  // columns of S that a softmax thread holds at a time: a whole row, or (E4M3, whose conversion
-  // needs the registers) half of one, which is then loaded twice
+  // columns of S that a softmax thread holds at a time, half a row (loaded twice: for the maximum
+  // and for the weights): loops over halves stay small enough for the instruction cache
   static constexpr int SC = KT / 2;
   // TMEM: score buffers of KT columns (P over them), O, Q (two elements a column)
   static constexpr uint32_t O_COL = NQT * NSB * KT, Q_COL = O_COL + NQT * D;
@@ -137,8 +139,8 @@ __device__ __forceinline__ int item_tiles(const SoftmaxParams& p, const PagedSeq
 }
 
 template <class C>
-__device__ __forceinline__ void fill_seg(const SoftmaxParams& p, int b, int tile, int hk, int from, int to,
-                         int slot, Seg& g) {
+__device__ __forceinline__ void fill_seg(const SoftmaxParams& p, int b, int tile, int hk, int from,
+                                         int to, int slot, Seg& g) {
   const int tpt = 128 / p.G;
   g.s = paged_seq(p.c, b);
   g.b = b;
@@ -191,7 +193,7 @@ __device__ __forceinline__ void walk_begin(const SoftmaxParams& p, const PlanTab
 
 template <class C>
 __device__ __forceinline__ bool walk_next(const SoftmaxParams& p, const PlanTable& pl, Walk& w,
-                                       int tiles, Seg& g) {
+                                          int tiles, Seg& g) {
   if (!p.balanced) {
     while (w.u < w.end) {
       const uint32_t blk = (uint32_t)w.u, pair = blk / (uint32_t)p.c.Nk;  // (fit 31 bits)
@@ -1095,7 +1097,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
 
   // With E4M3's conversion warps the launch leaves the softmax too few registers. 512 threads
   // launch with 128 each (65,536): 208 for its warps and 96 for the others are 63,488. 640 launch
-  // with 96 (61,440): 136 and 64 are 59,392.
+  // with 96 (61,440): 120 and 80 are as many.
   if constexpr (C::E4M3) {
     if (warp < C::SM_WARPS)
       ptx::regs_inc<C::NQT == 2 ? 120 : 208>();

@@ -111,7 +111,8 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * sequence are left alone.
  *
  * Statistics and sums are fp32. fp16 and bf16: the weights are rounded to the type of q for the
- * product with V, or to fp16 over an E4M3 cache.
+ * product with V, or to fp16 over an E4M3 cache (bf16 weights of at most 16 rows of a kv head,
+ * single tokens for instance, come in two parts, whose sum is exact to 2^-16).
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */
@@ -124,7 +125,7 @@ typedef struct {
   int max_seqlen;         /* bound on n, in [1, 2^24] */
   int max_seqlen_k;       /* bound on Lk, in [1, 2^30] */
   int causal;             /* 0 or 1 */
-  float alpha;            /* finite, > 0 */
+  float alpha;            /* in (0, 2e38] */
   void* out;              /* [T, Nq, D] contiguous, 16-byte aligned */
   float* lse;             /* [T, Nq], or NULL */
   void* workspace;        /* hstu_softmax_workspace bytes, 16-byte aligned; NULL if that is 0.

@@ -135,7 +135,7 @@ def test_attention_refuses_bad_arguments(built_lib):
            (dict(num_heads_q=-2), INVALID), (dict(num_heads_q=258), UNSUPPORTED),  # 129 heads share one
            (dict(max_seqlen=0), INVALID), (dict(max_seqlen_k=0), INVALID), (dict(causal=2), INVALID),
            (dict(alpha=0.0), INVALID), (dict(alpha=-1.0), INVALID), (dict(alpha=float("inf")), INVALID),
-           (dict(alpha=float("nan")), INVALID), (dict(total_tokens=-1), INVALID), (dict(reserved=1), INVALID)]
+           (dict(alpha=float("nan")), INVALID), (dict(alpha=3e38), INVALID), (dict(total_tokens=-1), INVALID), (dict(reserved=1), INVALID)]
     for kw, want in bad:
         assert L.hstu_softmax_fwd(by(_cache()), by(_attn(**kw)), None) == want, kw
     for kw in (dict(batch=0),):

@@ -117,7 +117,7 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
 // How a call runs: query rows of one CTA, key ranges, grid and workspace.
 struct AttnPlan {
   enum { SIMT, TC, ROWS } kernel;
-  int qtiles;          // query tiles of one CTA (TC)
+  int qtiles, ctas;    // query tiles of one CTA, CTAs of one SM (TC)
   int rows;            // query rows of one item (SIMT, ROWS)
   int cluster;         // CTAs that divide the keys of one item (ROWS)
   int balanced;        // CTAs share the items' key tiles (TC)
@@ -137,6 +137,44 @@ bool parting_pays(long long keys, long long items, long long sms, int head_dim) 
   const long long rounds = (items + sms - 1) / sms;
   return items * 2 < 3 * sms &&
          keys * (4 * rounds * sms - 3 * items) >= (head_dim > 128 ? 3200 : 2000) * 4 * sms;
+}
+
+// Row tiles and CTAs of the tensor-core kernel (times of bf16, D = 128, unless they say more).
+template <typename SetRows>
+void plan_tiles(const hstu_kv_cache* c, const hstu_softmax_args* a, long long most, long long G,
+                long long sms, const SetRows& set_rows, const long long& bm,
+                const long long& items, AttnPlan* pl) {
+  const long long tile = 128 / G * G;
+  const bool fp8 = c->dtype == HSTU_FP8_E4M3, small = c->head_dim <= 128;
+  // Two query tiles share the loads of K and V and keep the tensor pipe busier, if there are rows
+  // for both (4096 tokens over 4096, 16 heads of 4: 660 us with two, 712 with one; 64 sequences of
+  // some 200 rows over 2500 keys: 141 and 126)
+  pl->qtiles = small && most > 128 / G && a->total_tokens * G / c->batch >= 256 ? 2 : 1;
+  pl->ctas = 1;
+  set_rows(pl->qtiles * tile);
+  if (c->batch <= hstu::kMaxSeqs && a->total_tokens * G / bm + c->batch <= hstu::kMaxItems &&
+      parting_pays(a->max_seqlen_k, items, sms, c->head_dim)) {
+    pl->balanced = 1;
+    pl->blocks = sms;
+    pl->parts_bytes = 2 * pl->blocks * pl->qtiles * 128 * (c->head_dim + 1) * 4;
+    pl->workspace = pl->parts_bytes + pl->blocks * (long long)sizeof(hstu::JoinRecord);
+    return;
+  }
+  if (small && !fp8 && (pl->qtiles == 1 || a->max_seqlen_k <= 4096)) {
+    // A CTA for each item, two on an SM if there are as many: with short keys what hides an item's
+    // first and last steps is another item (24 sequences of some 500 rows over 900 keys, D = 64:
+    // 49 us with two query tiles, 46 with two CTAs; 32 of 400 over 1400 120 and 109; with longer
+    // keys they come out even: 16 of 2048 over 4600 146 and 146). With no more items than SMs one
+    // CTA with two score buffers is faster (8 sequences of 200 rows over 600 keys: 13.2 and 14.8).
+    pl->qtiles = 1;
+    set_rows(tile);
+    pl->ctas = items > sms ? 2 : 1;
+  }
+  // Short keys: a CTA takes several items, whose first loads and last stores overlap, too (155
+  // sequences of up to 21 rows over 120 keys, eight heads: 33 us, with a CTA for each item 43;
+  // but of up to 600 keys, uneven items, 60 sequences of 400 rows 59 and 54)
+  if (pl->qtiles == 1 && a->max_seqlen_k <= 256 && pl->blocks > sms * pl->ctas)
+    pl->blocks = sms * pl->ctas;
 }
 
 hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, AttnPlan* pl) {
@@ -159,35 +197,33 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   const long long most = a->max_seqlen < a->total_tokens ? a->max_seqlen : a->total_tokens;
-  // query rows (token, head) of one item: a CTA's, or a cluster's
-  long long bm;
+  // query rows (token, head) of one item (a CTA's, or a cluster's); row tiles that hold rows: at
+  // most one partly filled tile a sequence
+  long long bm = 0, items = 0;
+  auto set_rows = [&](long long rows) {
+    bm = rows;
+    pl->tiles = (most * G + bm - 1) / bm;
+    pl->blocks = c->batch * pl->tiles * c->num_heads_kv;
+    items = a->total_tokens * G / bm + c->batch;
+    if (items > c->batch * pl->tiles) items = c->batch * pl->tiles;
+    items *= c->num_heads_kv;
+  };
   if (a->dtype == HSTU_F32) {
     // up to 16 rows in CTAs of four, which read the keys' rows straight into registers (tiles of
     // 16 rows in shared memory instead: 128 sequences of one token and eight heads 1334 us, now
     // 288; with 16 rows a kv head 235 and 136, over E4M3 221 and 145)
     pl->kernel = AttnPlan::SIMT;
     pl->rows = most * G <= 16 ? 4 : 64;
-    bm = pl->rows;
+    set_rows(pl->rows);
   } else if (most * G <= 16) {
     pl->kernel = AttnPlan::ROWS;
     pl->rows = most * G <= 8 ? 8 : 16;
-    bm = pl->rows;
+    set_rows(pl->rows);
   } else {
     pl->kernel = AttnPlan::TC;
-    // Two query tiles share the loads of K and V and keep the tensor pipe busier, if there are
-    // rows for both (4096 tokens over 4096, 16 heads of 4: 660 us with two, 712 with one; 64
-    // sequences of some 200 rows over 2500 keys: 141 and 126; 24 of 500 over 900: 48 and 54)
-    pl->qtiles = c->head_dim <= 128 && most > 128 / G &&
-                         a->total_tokens * G / c->batch >= 256 ? 2 : 1;
-    bm = pl->qtiles * (128 / G) * G;
+    plan_tiles(c, a, most, G, sms, set_rows, bm, items, pl);
   }
-  pl->tiles = (most * G + bm - 1) / bm;
-  pl->blocks = c->batch * pl->tiles * c->num_heads_kv;
-  if (pl->blocks * 8 > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
-  // row tiles that hold rows: at most one partly filled tile a sequence
-  long long items = a->total_tokens * G / bm + c->batch;
-  if (items > c->batch * pl->tiles) items = c->batch * pl->tiles;
-  items *= c->num_heads_kv;
+  if (c->batch * pl->tiles * c->num_heads_kv > 0x7fffffffll / 8) return HSTU_ERR_UNSUPPORTED;
   pl->cluster = 1;
   if (pl->kernel == AttnPlan::ROWS) {
     // one wave of CTAs: more of them, of fewer keys each, measured slower (four sequences of
@@ -207,17 +243,6 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     const long long want = ((pl->rows == 64 ? 4ll : 6ll) * sms + items - 1) / items;
     const long long can = (a->max_seqlen_k + pl->min_range - 1) / pl->min_range;
     pl->splits = (int)(want < can ? want : can);
-  } else if (c->batch <= hstu::kMaxSeqs && a->total_tokens * G / bm + c->batch <= hstu::kMaxItems &&
-             parting_pays(a->max_seqlen_k, items, sms, c->head_dim)) {
-    pl->balanced = 1;
-    pl->blocks = sms;
-    pl->parts_bytes = 2ll * sms * pl->qtiles * 128 * (c->head_dim + 1) * 4;
-    pl->workspace = pl->parts_bytes + sms * (long long)sizeof(hstu::JoinRecord);
-  } else if (pl->qtiles == 1 && a->max_seqlen_k <= 256 && pl->blocks > sms) {
-    // short keys: a CTA takes several items, whose first loads and last stores overlap (100
-    // sequences of up to 20 rows over 120 keys, four heads: 25.8 us, with a CTA for each item
-    // 28.5; but of up to 600 keys, uneven items, 51 and 48.5 over E4M3)
-    pl->blocks = sms;
   }
   if (pl->splits > 1) {
     pl->parts_bytes = (long long)pl->splits * a->total_tokens * a->num_heads_q *
@@ -290,7 +315,7 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
           ? hstu::launch_softmax_rows(p, a->dtype, fp8, pl.rows, pl.tiles, pl.blocks,
                                       pl.cluster, s)
       : pl.kernel == AttnPlan::TC
-          ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.tiles, pl.blocks, s)
+          ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.ctas, pl.tiles, pl.blocks, s)
           : hstu::launch_softmax_simt(p, fp8, pl.rows, pl.tiles, pl.blocks, s);
   if (e == cudaSuccess && (pl.splits > 1 || pl.balanced))
     e = hstu::launch_softmax_join(p, a->dtype, 128 / p.G, pl.qtiles, (int)pl.blocks, s);

@@ -31,9 +31,9 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
 cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream);
 
-// Tensor-core attention (bf16, fp16). A CTA takes qtiles tiles of 128 / G tokens; two where
-// D <= 128 only.
-cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles,
+// Tensor-core attention (bf16, fp16). A CTA takes qtiles tiles of 128 / G tokens, two where
+// D <= 128 only; an SM holds `ctas` CTAs, two where D <= 128 with one tile and no E4M3.
+cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles, int ctas,
                               long long tiles, long long blocks, cudaStream_t stream);
 
 // Attention of few rows (bf16, fp16): `rows` (8 or 16) packed rows of one kv head per cluster

@@ -11,8 +11,8 @@ namespace hstu {
 
 #define HSTU_TC_UNIT(n)                                                                       \
   cudaError_t launch_softmax_tc_##n(const SoftmaxParams& p, const CUtensorMap& tq,            \
-                                    const CUtensorMap& tc, int qtiles, long long tiles,       \
-                                    long long blocks, cudaStream_t stream)
+                                    const CUtensorMap& tc, int qtiles, int ctas,              \
+                                    long long tiles, long long blocks, cudaStream_t stream)
 HSTU_TC_UNIT(bf16);
 HSTU_TC_UNIT(fp16);
 HSTU_TC_UNIT(bf16_e4m3);
@@ -76,12 +76,12 @@ cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, bool e4m3, in
              : launch_softmax_rows_fp16(p, e4m3, tc, rows, tiles, blocks, cluster, stream);
 }
 
-cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles,
+cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int qtiles, int ctas,
                               long long tiles, long long blocks, cudaStream_t stream) {
   const EncodeTiledFn encode = encode_fn();
   if (!encode) return cudaErrorNotSupported;
   CUtensorMap tq = {}, tc;
-  if (kernel_dim(p.c.D) == 128 && qtiles == 2) {  // the variant whose queries come by TMA:
+  if (kernel_dim(p.c.D) == 128 && (qtiles == 2 || ctas == 2)) {  // queries by TMA:
     // the G heads of one kv head of 128 / G tokens make one tile of packed rows
     const cuuint64_t dims[3] = {(cuuint64_t)p.c.D, (cuuint64_t)p.Nq, (cuuint64_t)p.c.T};
     const cuuint64_t strides[2] = {(cuuint64_t)p.c.D * 2, (cuuint64_t)p.q_stride * 2};
@@ -98,10 +98,10 @@ cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, bool e4m3, int 
   if (!cache_map(&tc, p, dtype, e4m3, e4m3 ? kernel_dim(p.c.D) : 64, kt, e4m3 ? 0 : 128))
     return cudaErrorInvalidValue;
   if (dtype == HSTU_BF16)
-    return e4m3 ? launch_softmax_tc_bf16_e4m3(p, tq, tc, qtiles, tiles, blocks, stream)
-                : launch_softmax_tc_bf16(p, tq, tc, qtiles, tiles, blocks, stream);
-  return e4m3 ? launch_softmax_tc_fp16_e4m3(p, tq, tc, qtiles, tiles, blocks, stream)
-              : launch_softmax_tc_fp16(p, tq, tc, qtiles, tiles, blocks, stream);
+    return e4m3 ? launch_softmax_tc_bf16_e4m3(p, tq, tc, qtiles, ctas, tiles, blocks, stream)
+                : launch_softmax_tc_bf16(p, tq, tc, qtiles, ctas, tiles, blocks, stream);
+  return e4m3 ? launch_softmax_tc_fp16_e4m3(p, tq, tc, qtiles, ctas, tiles, blocks, stream)
+              : launch_softmax_tc_fp16(p, tq, tc, qtiles, ctas, tiles, blocks, stream);
 }
 
 }  // namespace hstu

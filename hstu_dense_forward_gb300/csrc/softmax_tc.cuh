@@ -25,7 +25,8 @@
 //                          the keys and four the values (one warpgroup for both took 2750
 //                          cycles a tile, longer than the products).
 // With two query tiles, one tile's products run while the softmax of the other does. With one
-// (few rows, or D = 256, whose O takes half of TMEM) the scores have two buffers instead.
+// (few rows, or D = 256, whose O takes half of TMEM) the scores have two buffers instead, or an SM
+// holds two CTAs with one buffer each, which also hide each other's first and last steps.
 //
 // E4M3 caches: both products run in fp16, which holds every code exactly. A tile's rows are taken
 // relative to the largest of its row scales, 2^EK (K) or 2^EV (V): a code becomes fp16 by one
@@ -53,18 +54,18 @@
 namespace hstu {
 namespace sm {
 
-constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;  // log2 of the largest weight
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int D_, int NQT_, bool E4M3_>
+template <int D_, int NQT_, int CTAS_, bool E4M3_>
 struct Cfg {
-  static constexpr int D = D_, NQT = NQT_;
+  static constexpr int D = D_, NQT = NQT_, CTAS = CTAS_;  // CTAS: of an SM
   static constexpr bool E4M3 = E4M3_;
   static_assert(D == 64 || D == 128 || D == 256, "head dim of the kernel");
   static_assert(NQT == 1 || (NQT == 2 && D <= 128), "query tiles");
+  static_assert(CTAS == 1 || (CTAS == 2 && NQT == 1 && D <= 128 && !E4M3_), "CTAs per SM");
   static constexpr int KT = D == 256 ? 64 : 128;  // keys of one tile
-  static constexpr int NSB = NQT == 1 ? 2 : 1;    // score buffers of one query tile
+  static constexpr int NSB = NQT == 1 && CTAS == 1 ? 2 : 1;  // score buffers of a query tile
   static constexpr int SWB = 128, EPC = 64;       // swizzled row bytes and elements of a block
   static constexpr int NCB = D / EPC;             // column blocks of a row
   static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
@@ -72,9 +73,12 @@ struct Cfg {
   static constexpr int ST_TILE = KT * D;          // staged E4M3 tile; its row scales (KT bytes)
   // The scores' A operand, Q, comes from TMEM where that has room: from shared memory it takes,
   // with K, all of the latter's bandwidth, and threads wait for their barriers meanwhile.
-  static constexpr bool QT = NQT == 1 || D == 64;
+  static constexpr bool QT = NSB == 2 || D == 64;
   // ring depths: what 227 KB of shared memory holds
-  static constexpr int NSLOT = D == 64 ? (E4M3 ? 4 : 8) : QT ? (E4M3 ? 4 : 6) : E4M3 ? 3 : 4;
+  static constexpr int NSLOT = CTAS == 2  ? (D == 64 ? 6 : 2)
+                               : D == 64  ? (E4M3 ? 4 : 8)
+                               : QT       ? (E4M3 ? 4 : 6)
+                                          : (E4M3 ? 3 : 4);
   static constexpr int NST = !E4M3 ? 0 : QT ? 4 : 3;
   static constexpr int SM_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1;
@@ -85,16 +89,17 @@ struct Cfg {
   static constexpr int SC = KT / 2;
   // TMEM: score buffers of KT columns (P over them), O, Q (two elements a column)
   static constexpr uint32_t O_COL = NQT * NSB * KT, Q_COL = O_COL + NQT * D;
-  static_assert(Q_COL + (QT ? NQT * D / 2 : 0) <= kTmemCols, "TMEM");
+  static constexpr uint32_t TMEM_COLS = 512 / CTAS;
+  static_assert(Q_COL + (QT ? NQT * D / 2 : 0) <= TMEM_COLS, "TMEM");
   static constexpr int OFF_Q = 0, OFF_KV = QT ? 0 : NQT * Q_TILE;
   static constexpr int OFF_ST = OFF_KV + NSLOT * KV_TILE;
   static constexpr int OFF_SC = OFF_ST + NST * ST_TILE;  // row scales of the staged tiles
   static constexpr int OFF_BAR = OFF_SC + NST * 128;
   static constexpr int OFF_PLAN = OFF_BAR + 2048;
   static constexpr int USED = OFF_PLAN + kPlanSharedBytes + 1024;  // (alignment of the base)
-  // one CTA per SM: it takes all of TMEM
-  static constexpr int SMEM = USED < 120 * 1024 ? 120 * 1024 : USED;
-  static_assert(SMEM <= 232448, "shared memory");
+  // (one CTA per SM, which takes all of TMEM: no second one may come to wait for it)
+  static constexpr int SMEM = CTAS == 1 && USED < 120 * 1024 ? 120 * 1024 : USED;
+  static_assert(SMEM <= 232448 / CTAS - (CTAS - 1) * 1024, "shared memory");
 };
 
 constexpr int kExpDepth = 8;  // tiles whose exponents are kept (the conversion is fewer ahead)
@@ -319,16 +324,16 @@ __device__ JoinRecord join_record(const SoftmaxParams& p, const PlanTable& pl, i
 // One query tile: K0 K1 V0 K2 V1 ... (the scores run a tile ahead); two: K0 V0 K1 V1 ...
 template <class C>
 __device__ __forceinline__ int k_index(int t) {
-  return C::NQT == 1 ? (t == 0 ? 0 : 2 * t - 1) : 2 * t;
+  return C::NSB == 2 ? (t == 0 ? 0 : 2 * t - 1) : 2 * t;
 }
 template <class C>
 __device__ __forceinline__ int v_index(int t, int n) {
-  return C::NQT == 1 ? (t + 1 < n ? 2 * t + 2 : 2 * t + 1) : 2 * t + 1;
+  return C::NSB == 2 ? (t + 1 < n ? 2 * t + 2 : 2 * t + 1) : 2 * t + 1;
 }
 // The tile behind place i: its number, and whether it is a V tile.
 template <class C>
 __device__ __forceinline__ bool ring_tile(int i, int n, int& t) {
-  if (C::NQT == 2) {
+  if (C::NSB == 1) {
     t = i >> 1;
     return i & 1;
   }
@@ -745,7 +750,7 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
         const uint32_t gt = g[q] + t;
         if (t == 0 && gt > 0 && !warp_wait(p, bars, &bars->pv_done[q], (gt - 1) & 1)) return;
         ptx::tc_fence_after();
-        is.scores(q, C::NQT == 1 ? gt & 1 : q, at.slot, q == 1 || t >= nq[1]);
+        is.scores(q, C::NSB == 2 ? gt & 1 : q, at.slot, q == 1 || t >= nq[1]);
       }
       at.next();
     }
@@ -770,8 +775,8 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
       for (int q = 0; q < C::NQT; ++q) {
         if (t >= nq[q]) continue;
         const uint32_t gt = g[q] + t;
-        const int sb = C::NQT == 1 ? gt & 1 : q;
-        const uint32_t par = C::NQT == 1 ? (gt >> 1) & 1 : gt & 1;
+        const int sb = C::NSB == 2 ? gt & 1 : q;
+        const uint32_t par = C::NSB == 2 ? (gt >> 1) & 1 : gt & 1;
         uint32_t ready = q == 0
             ? ptx::mbar_tests(ptx::smem_u32(&bars->p_half[sb]), par,
                               ptx::smem_u32(&bars->p_full[sb]), par,
@@ -871,8 +876,8 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     const int rest = (int)min(it.s.Lk - it.k0, 0x7fffffffll);  // keys of the sequence from k0 on
     float m = -CUDART_INF_F, l = 0.0f;
     for (int t = 0; t < n; ++t, ++g) {
-      const int sb = C::NQT == 1 ? (g & 1) : q;
-      const uint32_t par = C::NQT == 1 ? (g >> 1) & 1 : g & 1;
+      const int sb = C::NSB == 2 ? (g & 1) : q;
+      const uint32_t par = C::NSB == 2 ? (g >> 1) & 1 : g & 1;
       if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
       ptx::tc_fence_after();
       float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
@@ -1048,12 +1053,12 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, int NQT, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
+template <int D, int NQT, int CTAS, bool BF16, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, NQT, CTAS, E4M3>::THREADS, CTAS)
     softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_c, const SoftmaxParams p,
                       int tiles) {
-  using C = Cfg<D, NQT, E4M3>;
+  using C = Cfg<D, NQT, CTAS, E4M3>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1086,7 +1091,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
     ptx::fence_proxy_async_smem();
   }
   if (warp == C::MMA_WARP) {
-    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), kTmemCols);
+    ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), C::TMEM_COLS);
     ptx::tmem_relinquish();
   }
   if (p.balanced) make_plan<C>(p, pl);
@@ -1130,15 +1135,15 @@ __global__ void __launch_bounds__(Cfg<D, NQT, E4M3>::THREADS, 1)
   ptx::tc_fence_after();
   if (warp == C::MMA_WARP) {
     __syncwarp();
-    ptx::tmem_dealloc(tmem, kTmemCols);
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
-template <int D, int NQT, bool BF16, bool E4M3>
+template <int D, int NQT, int CTAS, bool BF16, bool E4M3>
 cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
                            long long tiles, long long blocks, cudaStream_t stream) {
-  using C = Cfg<D, NQT, E4M3>;
-  auto* kernel = softmax_tc_kernel<D, NQT, BF16, E4M3>;
+  using C = Cfg<D, NQT, CTAS, E4M3>;
+  auto* kernel = softmax_tc_kernel<D, NQT, CTAS, BF16, E4M3>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
@@ -1146,16 +1151,22 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const 
   return cudaGetLastError();
 }
 
-// Kernel for the head dim and number of query tiles.
+// Kernel for the head dim, the number of query tiles and the CTAs of an SM.
+template <int D, bool BF16, bool E4M3>
+cudaError_t launch_dim(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
+                       int qtiles, int ctas, long long tiles, long long blocks, cudaStream_t s) {
+  if constexpr (!E4M3) {
+    if (ctas == 2) return launch_variant<D, 1, 2, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+  }
+  return qtiles == 2 ? launch_variant<D, 2, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s)
+                     : launch_variant<D, 1, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+}
 template <bool BF16, bool E4M3>
 cudaError_t launch_tc(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
-                      int qtiles, long long tiles, long long blocks, cudaStream_t s) {
-  if (p.c.D > 128) return launch_variant<256, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
-  if (p.c.D > 64)
-    return qtiles == 2 ? launch_variant<128, 2, BF16, E4M3>(p, tq, tc, tiles, blocks, s)
-                       : launch_variant<128, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
-  return qtiles == 2 ? launch_variant<64, 2, BF16, E4M3>(p, tq, tc, tiles, blocks, s)
-                     : launch_variant<64, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+                      int qtiles, int ctas, long long tiles, long long blocks, cudaStream_t s) {
+  if (p.c.D > 128) return launch_variant<256, 1, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+  if (p.c.D > 64) return launch_dim<128, BF16, E4M3>(p, tq, tc, qtiles, ctas, tiles, blocks, s);
+  return launch_dim<64, BF16, E4M3>(p, tq, tc, qtiles, ctas, tiles, blocks, s);
 }
 
 }  // namespace sm

@@ -4,9 +4,9 @@
 namespace hstu {
 
 cudaError_t launch_softmax_tc_bf16_e4m3(const SoftmaxParams& p, const CUtensorMap& tq,
-                                 const CUtensorMap& tc, int qtiles, long long tiles,
+                                 const CUtensorMap& tc, int qtiles, int ctas, long long tiles,
                                  long long blocks, cudaStream_t stream) {
-  return sm::launch_tc<true, true>(p, tq, tc, qtiles, tiles, blocks, stream);
+  return sm::launch_tc<true, true>(p, tq, tc, qtiles, ctas, tiles, blocks, stream);
 }
 
 }  // namespace hstu

@@ -156,20 +156,22 @@ def test_prompts(cuda_device, dtype, mode, Nq, Nk, D, ps, causal):
     run_case(cuda_device, *PROMPT, dtype, mode, Nq, Nk, D, ps, causal=causal, seed=71)
 
 
-@pytest.mark.parametrize("dtype,mode,Nq,Nk,D,n", [
-    ("bf16", "same", 8, 2, 128, 75), ("fp16", "same", 16, 4, 64, 70), ("bf16", "scale", 8, 2, 128, 70),
-    ("fp16", "scale", 8, 2, 64, 66), ("bf16", "same", 16, 4, 256, 20), ("bf16", "same", 4, 4, 128, 30),
-    ("bf16", "scale", 4, 4, 80, 30), ("fp16", "scale", 16, 4, 256, 20),
+@pytest.mark.parametrize("dtype,mode,Nq,Nk,D,n,bound", [
+    ("bf16", "same", 8, 2, 128, 75, 0), ("fp16", "same", 16, 4, 64, 70, 0), ("bf16", "scale", 8, 2, 128, 70, 0),
+    ("fp16", "scale", 8, 2, 64, 66, 0), ("bf16", "same", 16, 4, 256, 20, 0), ("bf16", "same", 4, 4, 128, 30, 0),
+    ("bf16", "scale", 4, 4, 80, 30, 0), ("fp16", "scale", 16, 4, 256, 20, 0), ("bf16", "same", 8, 2, 128, 75, 5000),
+    ("fp16", "same", 16, 4, 64, 70, 5000), ("fp16", "same", 8, 8, 48, 30, 0), ("bf16", "same", 12, 4, 128, 25, 600),
 ])
-def test_many_sequences(cuda_device, dtype, mode, Nq, Nk, D, n):
-    """More row tiles than CTAs can share out."""
+def test_many_sequences(cuda_device, dtype, mode, Nq, Nk, D, n, bound):
+    """More row tiles than CTAs can share out; with a loose bound on the keys, too."""
     g = torch.Generator().manual_seed(n)
     B = 70
     new = torch.randint(n // 2, n + n // 2, (B,), generator=g).tolist()
     new[3], new[-1] = 0, 1
     lengths = [m + h for m, h in zip(new, torch.randint(0, 200, (B,), generator=g).tolist())]
     lengths[5], new[5] = 0, 0
-    run_case(cuda_device, lengths, new, dtype, mode, Nq, Nk, D, 32, seed=81)
+    run_case(cuda_device, lengths, new, dtype, mode, Nq, Nk, D, 32, seed=81,
+             bounds=(max(new), bound) if bound else None)
 
 
 @pytest.mark.parametrize("n", [1, 5, 20])

@@ -226,13 +226,14 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
   if (c->batch * pl->tiles * c->num_heads_kv > 0x7fffffffll / 8) return HSTU_ERR_UNSUPPORTED;
   pl->cluster = 1;
   if (pl->kernel == AttnPlan::ROWS) {
-    // one wave of CTAs: more of them, of fewer keys each, measured slower (four sequences of
-    // 100k bf16 keys: 74.5 us with one wave, 83.8 with two, 101 with four)
+    // at most one wave of CTAs: more of them, of fewer keys each, measured slower (four sequences
+    // of 100k bf16 keys: 74.5 us with one wave, 83.8 with two, 101 with four; 400 items of up to
+    // 500 E4M3 keys on 456 places: 13.7 us alone, 20.2 in pairs)
     const long long slots =
         (long long)hstu::softmax_rows_ctas(c->head_dim, c->dtype == HSTU_FP8_E4M3, pl->rows) * sms;
-    long long want = (slots + items - 1) / items;
     const long long can = (a->max_seqlen_k + 127) / 128;  // two tiles of 64 keys each
-    if (want > can) want = can;
+    long long want = slots / items < can ? slots / items : can;
+    if (want < 1) want = 1;
     while (pl->cluster < 8 && pl->cluster * 2 <= want) pl->cluster *= 2;
     pl->splits = (int)(want / pl->cluster);
     pl->min_range = 128 * pl->cluster;

@@ -34,7 +34,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 template <int D_, bool E4M3>
 struct Cfg {
   static constexpr int D = D_, BM = 64;
-  static constexpr int BN = D == 64 ? 64 : 32;  // (at D = 256 what shared memory holds)
+  // keys of a step: 64 spend more FMAs per load of the scores' operands, 32 leave an SM a second
+  // CTA at D = 128, which E4M3 rows, whose conversion waits, need more (965 tokens over 4000,
+  // 20 heads: D = 256 1479 and 1336 us, D = 128 773 and 716, over E4M3 725 and 730)
+  static constexpr int BN = D == 128 && E4M3 ? 32 : 64;
   static constexpr int RA = BM / 16, CK = BN / 16, U = D / 64;
   static constexpr int LD = D + 4, LDP = BN + 4;  // padded rows: conflict-free float4 reads
   static constexpr int OFF_K = BM * LD, OFF_V = OFF_K + BN * LD, OFF_P = OFF_V + BN * D;

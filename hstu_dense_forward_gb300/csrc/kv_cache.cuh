@@ -4,7 +4,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <stddef.h>
 #include <stdint.h>
 
 #include "../../include/hstu_kv.h"

@@ -200,14 +200,17 @@ def _call(name, c, *args):
         _abi.check(status, name)
 
 
-def _copy(name, c, k, v, seq_offsets):
-    """hstu_kv_append / hstu_kv_read of the rows k and v."""
+def _copy(name, c, k, v, seq_offsets, new=False):
+    """hstu_kv_append / hstu_kv_read of the rows k and v (new: just allocated, nothing to check)."""
     dtype = _row_dtype(c, k.dtype)
-    k_stride = _rows(k, "k", c.device, k.dtype, c.Nk, c.D)
-    v_stride = _rows(v, "v", c.device, k.dtype, c.Nk, c.D)
     T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError("k and v must have one shape")
+    if new:
+        k_stride = v_stride = c.Nk * c.D
+    else:
+        k_stride = _rows(k, "k", c.device, k.dtype, c.Nk, c.D)
+        v_stride = _rows(v, "v", c.device, k.dtype, c.Nk, c.D)
+        if v.shape[0] != T:
+            raise ValueError("k and v must have one shape")
     _call(name, c, _PACK_ROWS(k.data_ptr(), v.data_ptr(), k_stride, v_stride,
                               seq_offsets.data_ptr(), T, dtype, 0))
 
@@ -265,7 +268,8 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
                v_descale, status)
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
-    if k is None:
+    new = k is None
+    if new:
         if total_tokens is None:
             raise ValueError("hstu_kv_read needs total_tokens, or k and v")
         if dtype is None:
@@ -278,7 +282,7 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
         raise TypeError("k must be a torch.Tensor")
     elif dtype not in (None, k.dtype) or total_tokens not in (None, k.shape[0]):
         raise ValueError("dtype and total_tokens must be those of k")
-    _copy("hstu_kv_read", c, k, v, seq_offsets)
+    _copy("hstu_kv_read", c, k, v, seq_offsets, new)
     return k, v
 
 

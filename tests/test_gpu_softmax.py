@@ -349,6 +349,34 @@ def test_other_stream_and_graph(cuda_device, n, mode):
 
 
 @pytest.mark.parametrize("mode", ["same", "scale"])
+def test_calls_at_once(cuda_device, mode):
+    """Calls of every kernel on streams of their own, enqueued in turn, equal the calls alone bit
+    for bit."""
+    dev = cuda_device
+    calls = []
+    for lengths, n, Nq, D in (([150] * 70, [40] * 70, 8, 128), ([3000, 2500], [70, 300], 4, 128),
+                              ([400] * 20, [300] * 20, 8, 64), ([900] * 40, [1] * 40, 4, 128),
+                              ([60] * 90, [30] * 90, 16, 64)):
+        t = R.Table(lengths, 32, seed=Nq)
+        cache, _, kw = _filled(t, 2, D, torch.bfloat16, mode, dev, D)
+        g = torch.Generator().manual_seed(9)
+        q = torch.randn(sum(n), Nq, D, generator=g).bfloat16().to(dev)
+        so = R.offsets(n).to(dev)
+        kw.update(t.args(dev), max_seqlen=max(n), max_seqlen_k=max(lengths), alpha=0.1)
+        calls.append((q, cache, so, kw, torch.cuda.Stream()))
+    alone = [hstu_softmax_fwd(q, cache, so, **kw) for q, cache, so, kw, _ in calls]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for i, (q, cache, so, kw, stream) in enumerate(calls):
+            with torch.cuda.stream(stream):
+                got.append((i, hstu_softmax_fwd(q, cache, so, **kw)))
+    torch.cuda.synchronize()
+    for i, x in got:
+        assert torch.equal(x, alone[i])
+
+
+@pytest.mark.parametrize("mode", ["same", "scale"])
 def test_serving_run(cuda_device, mode):
     """As a user runs them: a prompt in two chunks, then single tokens, each step appended and
     attended to, over one growing table; every step against the whole sequence so far, and the

@@ -9,7 +9,8 @@
 // softmax_simt_kernel: 64 rows, 256 threads (16 x 16), in steps of BN keys. A thread owns rows
 // ty + 16 a, of the scores keys tx + 16 c and of the output columns 4 tx + 64 u .. + 3; every
 // operand comes from shared memory in float4 (four elements of the head dim, or four keys), so
-// that a step spends four times as many FMAs as loads.
+// that a step spends four times as many FMAs as loads. What bounds it is shared memory: 965 tokens
+// over 4000, 20 heads of 4, D = 256, take 1171 us, 36 TFLOP/s, D = 128 639.
 //
 // softmax_few_kernel: 4 rows, for calls of at most 16, where reading the cache is what counts:
 // D / 16 lanes hold a key, two keys at a time, straight from the cache in registers, and every
@@ -31,35 +32,72 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// A cached row: the place of its K elements, and of their scale. V's lie a plane further on.
+struct RowAt {
+  long long elems;  // -1: no such row
+  long long scale;
+};
+
 template <int D_, bool E4M3>
 struct Cfg {
   static constexpr int D = D_, BM = 64;
-  // keys of a step: 64 spend more FMAs per load of the scores' operands, 32 leave an SM a second
-  // CTA at D = 128, which E4M3 rows, whose conversion waits, need more (965 tokens over 4000,
-  // 20 heads: D = 256 1479 and 1336 us, D = 128 773 and 716, over E4M3 725 and 730)
+  // Keys of a step: 64 spend more FMAs per load of the scores' operands, 32 leave an SM a second
+  // CTA at D = 128, which E4M3 rows, whose conversion waits, need more (965 tokens over 4000, 20
+  // heads, with the slower loads of sixteen elements a thread: D = 256 1479 us with 32 and 1336
+  // with 64, D = 128 773 and 716, over E4M3 725 and 730).
   static constexpr int BN = D == 128 && E4M3 ? 32 : 64;
   static constexpr int RA = BM / 16, CK = BN / 16, U = D / 64;
   static constexpr int LD = D + 4, LDP = BN + 4;  // padded rows: conflict-free float4 reads
   static constexpr int OFF_K = BM * LD, OFF_V = OFF_K + BN * LD, OFF_P = OFF_V + BN * D;
-  static constexpr int SMEM = 4 * (OFF_P + BM * LDP);
+  static constexpr int OFF_ROW = OFF_P + BM * LDP;  // where the step's rows lie
+  static constexpr int SMEM = 4 * OFF_ROW + BN * (int)sizeof(RowAt);
 };
 
-// Sixteen consecutive elements of the cache as fp32 values.
+// What one access of a thread takes from the cache, until it is written to shared memory: four
+// fp32 elements, or eight E4M3 codes with their row's scale.
 template <bool E4M3>
-__device__ __forceinline__ void load_cache(const CacheView& c, long long page, int plane,
-                                           long long row, int hk, int d0, float (&x)[16]) {
-  const long long at = cache_row(c, page, plane, row, hk) + d0;
-  if constexpr (E4M3) {
-    load16(static_cast<const uint8_t*>(c.cache) + at, x);
-    if (c.scale) {
-      const float e = scale_value(c.scale[scale_row(c, page, plane, row, hk)]);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] *= e;
-    }
-  } else {
-    load16(static_cast<const float*>(c.cache) + at, x);
+struct Piece;
+template <>
+struct Piece<false> {
+  static constexpr int N = 4;
+  float4 x;
+  __device__ __forceinline__ void none() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const CacheView& c, long long elems, long long) {
+    x = *reinterpret_cast<const float4*>(static_cast<const float*>(c.cache) + elems);
   }
-}
+  __device__ __forceinline__ void store(float* at) const { *reinterpret_cast<float4*>(at) = x; }
+};
+template <>
+struct Piece<true> {
+  static constexpr int N = 8;
+  uint2 x;
+  uint8_t scale;
+  __device__ __forceinline__ void none() {
+    x = make_uint2(0u, 0u);
+    scale = 127;
+  }
+  __device__ __forceinline__ void load(const CacheView& c, long long elems, long long at) {
+    x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.cache) + elems);
+    scale = c.scale ? c.scale[at] : 127;
+  }
+  // (every second four lanes write their second half first: eight lanes, one access of shared
+  // memory, then lie in different banks)
+  __device__ __forceinline__ void store(float* at) const {
+    const float e = scale_value(scale);
+    float4 f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t lo, hi;
+      e4m3x4_to_f16x2(i ? x.y : x.x, lo, hi);
+      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      f[i] = make_float4(u.x * e, u.y * e, v.x * e, v.y * e);
+    }
+    const bool turn = threadIdx.x & 4;
+    *reinterpret_cast<float4*>(at + (turn ? 4 : 0)) = turn ? f[1] : f[0];
+    *reinterpret_cast<float4*>(at + (turn ? 0 : 4)) = turn ? f[0] : f[1];
+  }
+};
 
 __device__ __forceinline__ float dot4(const float4& a, const float4& b, float s) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
@@ -75,6 +113,7 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
   float* Ks = sm + C::OFF_K;  // [BN][LD]
   float* Vs = sm + C::OFF_V;  // [BN][D_]
   float* Ps = sm + C::OFF_P;  // [BM][LDP]
+  RowAt* rows_at = reinterpret_cast<RowAt*>(sm + C::OFF_ROW);  // [BN]
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 
   // block: sequence b, row tile (later tiles first: with the causal mask they see more
@@ -130,24 +169,63 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
     for (int u = 0; u < C::U; ++u) acc[a][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
 
+  // One thread a row loads the next step's page id before this step's products and looks at it
+  // behind them.
+  const long long plane = (long long)p.c.Nk * D << p.c.page_shift;
+  const long long scale_plane = (long long)p.c.Nk << p.c.page_shift;
+  long long id64 = 0;
+  int id32 = 0;
+  auto load_id = [&](long long n) {
+    if (threadIdx.x >= BN || n >= kend) return;
+    const long long at = s.po + (n >> p.c.page_shift);
+    if (p.c.index64)
+      id64 = static_cast<const long long*>(p.c.page_ids)[at];
+    else
+      id32 = static_cast<const int*>(p.c.page_ids)[at];
+  };
+  load_id(k0 + threadIdx.x);
   for (long long n0 = k0; n0 < kend; n0 += BN) {
     __syncthreads();  // previous step finished with Ks/Vs/Ps
-    for (int x = threadIdx.x; x < BN * (D_ / 16); x += kThreads) {
-      const int r = x / (D_ / 16), d0 = x % (D_ / 16) * 16;
-      float kx[16], vx[16];
-      const long long page = n0 + r < kend ? page_at(p.c, s, n0 + r) : -1;
-      if (page >= 0 && d0 < D) {
-        const long long row = (n0 + r) & (page_size(p.c) - 1);
-        load_cache<E4M3>(p.c, page, 0, row, hk, d0, kx);
-        load_cache<E4M3>(p.c, page, 1, row, hk, d0, vx);
-      } else {
-        if (page < 0 && n0 + r < kend) report(p.c, HSTU_DEVERR_OFFSETS);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) kx[i] = vx[i] = 0.f;
+    if (threadIdx.x < BN) {
+      const long long n = n0 + threadIdx.x, page = p.c.index64 ? id64 : id32;
+      RowAt w = {-1, 0};
+      if (n < kend) {
+        if (page >= 0 && page < p.c.num_pages) {
+          w.elems = cache_row(p.c, page, 0, n & (page_size(p.c) - 1), hk);
+          w.scale = scale_row(p.c, page, 0, n & (page_size(p.c) - 1), hk);
+        } else {
+          report(p.c, HSTU_DEVERR_OFFSETS);  // (a row of zeros then)
+        }
       }
-      store16(Ks + r * C::LD + d0, kx);
-      store16(Vs + r * D_ + d0, vx);
+      rows_at[threadIdx.x] = w;
     }
+    __syncthreads();
+    // A warp's accesses to the cache and to shared memory are contiguous (with sixteen elements a
+    // thread a fifth of all cycles of shared memory were bank conflicts: D = 256 1336 us instead
+    // of 1171), and up to sixteen of a thread are on their way at a time.
+    constexpr int NE = Piece<E4M3>::N, NX = BN * (D_ / NE) / kThreads, NB = NX < 8 ? NX : 8;
+#pragma unroll 1
+    for (int x0 = 0; x0 < NX; x0 += NB) {
+      Piece<E4M3> kx[NB], vx[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int x = (x0 + i) * kThreads + threadIdx.x, r = x / (D_ / NE), d = x % (D_ / NE) * NE;
+        const RowAt w = rows_at[r];
+        kx[i].none();
+        vx[i].none();
+        if (w.elems >= 0 && d < D) {
+          kx[i].load(p.c, w.elems + d, w.scale);
+          vx[i].load(p.c, w.elems + plane + d, w.scale + scale_plane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int x = (x0 + i) * kThreads + threadIdx.x, r = x / (D_ / NE), d = x % (D_ / NE) * NE;
+        kx[i].store(Ks + r * C::LD + d);
+        vx[i].store(Vs + r * D_ + d);
+      }
+    }
+    load_id(n0 + BN + threadIdx.x);
     __syncthreads();
     // scores of rows ty + 16a, keys tx + 16c
     float sc[C::RA][C::CK];

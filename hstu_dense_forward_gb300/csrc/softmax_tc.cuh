@@ -56,6 +56,7 @@ namespace sm {
 
 constexpr float kLazy = 8.0f;  // log2 of the largest weight
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 template <int D_, int NQT_, int CTAS_, bool E4M3_>
 struct Cfg {
@@ -889,6 +890,11 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         ek = power2((int)bars->tile_exp[te % kExpDepth][0]);
         ev = bars->tile_exp[te % kExpDepth][1];
       }
+      // Factor of the scores. For a query of zeros (or nearly) over small keys it would be 0, and
+      // a masked score, -inf, NaN by it: the smallest normal value instead leaves scores below
+      // 2^-90 (a NaN stays one).
+      float fa = fabsf(fk) * ek;
+      if (C::E4M3 && fa < kTiny) fa = kTiny;
       const uint32_t s_col = tmem + lane_off + sb * KT;
       constexpr int NC = C::SC / 32;  // chunks held at a time
       uint32_t sv[NC][32];
@@ -930,7 +936,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
                                             __uint_as_float(sv[c][e + 1]));
         }
         const float mx =
-            fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fabsf(fk) * ek, ev);
+            fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fa, ev);
         // raise the reference: at the first visible key, and when weights would pass 2^kLazy
         const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
         if (__any_sync(0xffffffffu, raise)) {
@@ -969,7 +975,6 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         }
       }
       float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-      const float fa = fabsf(fk) * ek;
       // weights of chunk `at` held in sv[i], summed and stored as columns of P
       auto weights = [&](int i, int at) {
         uint32_t pk[16];

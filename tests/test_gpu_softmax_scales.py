@@ -1,0 +1,117 @@
+"""hstu_softmax_fwd over E4M3 caches with row scales of very unlike sizes: rows far above the others
+(with and without weight, seen and hidden by the causal mask), rows of zeros (the smallest scale)
+beside large ones, queries of zeros, keys and queries at opposite ends of the range.
+
+Tolerance, from the roundings of the path. Codes times powers of two are exact, so keys and values
+are; a bf16 query becomes fp16 times a power of two of its row, exact but for elements below 2^-38 of
+the row's largest. A score of D products in fp32 is off by ex_j = (D + 8) 2^-24 alpha |q| |k_j|, which
+moves weight j by as much relatively (p_j: the normalised weights, A = sum_j p_j |v_j|). Weights are
+rounded to fp16: by half a step, 2^-11, relatively, and by 2^-25 absolutely in the unit of the
+references. That unit times the largest code is at most twice (references are whole powers of two)
+the largest p_j 448 2^(e_j), e_j the row scale's exponent, and 448 2^(e_j) at most twice the largest
+magnitude in row j: the absolute part is at most Lk 2^-25 * 2 * 2 B = Lk 2^-23 B, B the largest
+p_j max|v_j|. The output is rounded to its type, relatively by u, and absolutely by half of the
+smallest value (fp16: 2^-25).
+  |error| <= u |out| + (2^-11 + 2^-20 + Lk 2^-24) A + sum_j p_j ex_j |v_j| + (sum_j p_j ex_j) A
+             + Lk 2^-23 B
+fp32 queries: the same without the weights' roundings."""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+from hstu_dense_forward_gb300 import hstu_softmax_fwd
+
+pytestmark = pytest.mark.gpu
+
+
+def quantised(k, v, ps, dev, seed=0):
+    """k, v [L, Nk, D] (64 bits) as one sequence of an E4M3 cache with row scales: arguments of a
+    call and the values that the cache stands for."""
+    L, Nk, D = k.shape
+    t = R.Table([L], ps, seed=seed)
+    page, row = t.rows(0)
+    cache = np.full((t.num_pages, 2, ps, Nk, D), np.nan)
+    scale = np.full((t.num_pages, 2, Nk, ps), 255, dtype=np.uint8)
+    vals = []
+    for plane, x in ((0, k), (1, v)):
+        e = R.row_exponent(x)
+        codes = R.e4m3_round(np.ldexp(x, -e[..., None]))
+        cache[page, plane, row] = codes
+        scale[page, plane, :, row] = e + 127
+        vals.append(np.ldexp(codes, e[..., None]))
+    kw = dict(t.args(dev), kv_scale=torch.tensor(scale).to(dev))
+    return torch.tensor(cache).float().to(R.FP8).to(dev), kw, vals[0], vals[1]
+
+
+def check(q, K, V, got, lse, causal, alpha, sharp=False):
+    """Output and lse of the last n positions against 64 bits, with the tolerance above. sharp: every
+    key scores exactly the most or far less than that, so that its errors move no weight."""
+    dt, q = got.dtype, R.values(q.cpu())
+    n, Nq, D = q.shape
+    Lk, G = K.shape[0], Nq // K.shape[1]
+    up = 0.0 if dt == torch.float32 else 2.0 ** -11
+    u = R.HALF_STEP[dt]
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    seen = np.arange(Lk)[None, :] <= ((Lk - n + np.arange(n))[:, None] if causal else Lk)
+    for h in range(Nq):
+        k, v = K[:, h // G], V[:, h // G]
+        x = np.where(seen, alpha * (q[:, h] @ k.T), -np.inf)
+        top = x.max(1, keepdims=True)
+        assert np.isfinite(top).all()
+        p = np.exp(x - top)
+        total = p.sum(1, keepdims=True)
+        p /= total
+        out, A = p @ v, p @ np.abs(v)
+        ex = (D + 8) * 2.0 ** -24 * alpha * np.linalg.norm(q[:, h], axis=1)[:, None] * \
+            np.linalg.norm(k, axis=1)[None, :]
+        e1, e0 = (p * ex) @ np.abs(v), (p * ex).sum(1)
+        if sharp:
+            assert ((x == top) | (x < top - 4 * ex - 60.0)).all()
+            e1, e0 = 0.0 * e1, 0.0 * e0
+        B = (p * np.abs(v).max(1)).max(1)
+        tol = u * np.abs(out) + (up + 2.0 ** -20 + Lk * 2.0 ** -24 + e0[:, None]) * A * 1.01 + \
+            e1 * 1.01 + (Lk * 2.0 ** -23 * B[:, None] if up else 0.0) + \
+            (2.0 ** -25 if dt == torch.float16 else 0.0)
+        bad = ~(np.abs(got[:, h] - out) <= tol + 1e-37)
+        assert not bad.any(), (h, int(bad.sum()), np.argwhere(bad)[:4], got[:, h][bad][:4], out[bad][:4],
+                               tol[bad][:4])
+        ls = top[:, 0] + np.log(total[:, 0])
+        tol = 1.01 * (p * ex).sum(1) + 2.0 ** -20 + (Lk + 8) * 2.0 ** -24 + np.abs(ls) * 2.0 ** -22
+        bad = ~(np.abs(lse[:, h] - ls) <= tol)
+        assert not bad.any(), (h, np.argwhere(bad)[:4], lse[:, h][bad][:4], ls[bad][:4], tol[bad][:4])
+
+
+def run(dev, q, k, v, causal, alpha, ps=32, seed=0, sharp=False):
+    """q [n, Nq, D] (its type), k, v [L, Nk, D] (numpy)."""
+    cache, kw, K, V = quantised(k, v, ps, dev, seed)
+    n, q = q.shape[0], q.to(dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    got, lse = hstu_softmax_fwd(q, cache, R.offsets([n]).to(dev), max_seqlen=n, max_seqlen_k=k.shape[0],
+                                causal=causal, alpha=alpha, return_lse=True, status=status, **kw)
+    assert status.item() == 0
+    check(q, K, V, got, lse, causal, alpha, sharp)
+
+
+def directed(n, Nq, D, dtype, seed, size=3.0, noise=0.3):
+    """Queries near size * d, and the unit vector d: a key c * d scores about alpha * size * c."""
+    g = torch.Generator().manual_seed(seed)
+    d = torch.randn(D, generator=g)
+    d /= d.norm()
+    q = size * d + noise * torch.randn(n, Nq, D, generator=g)
+    return q.to(dtype), d.double().numpy()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("keys", [0.0, 2.0 ** -20, 2.0 ** -60, 1.0])
+@pytest.mark.parametrize("queries", [0.0, 2.0 ** -40, 2.0 ** -110])
+@pytest.mark.parametrize("dtype,D,n,L", [("bf16", 128, 40, 333), ("bf16", 64, 300, 300), ("fp16", 128, 40, 333),
+                                         ("bf16", 256, 40, 70), ("bf16", 128, 300, 333), ("bf16", 128, 1, 70)])
+def test_zero_and_tiny_queries(cuda_device, dtype, D, n, L, queries, keys, causal):
+    """Rows of padding: the mean of the values that they see."""
+    q, _ = directed(n, 2, D, R.DTYPES["fp32"], 13)
+    q = (q * queries).to(R.DTYPES[dtype])
+    q[n // 2] = 0
+    g = np.random.default_rng(14)
+    k, v = keys * g.standard_normal((L, 1, D)), g.standard_normal((L, 1, D))
+    run(cuda_device, q, k, v, causal, D ** -0.5)

@@ -17,11 +17,14 @@
 //
 // E4M3 caches: codes become fp16 by one conversion (exact) and the products run in fp16. A
 // row scale 2^e of K multiplies the score. One of V would leave fp16's range if it multiplied a
-// weight, so it enters the exponent instead: with u_j = x_j + e_j (base 2) and m = max u,
-//   P_j = 2^(u_j - m) is at most 1 (times 2^kLazy), O = sum P_j code_j, l = sum P_j 2^-e_j,
-// and O / l is the output (2^m cancels). bf16 queries become fp16 times a power of two of their
-// row, chosen so that the row's largest lies in [2^14, 2^15): what drops below fp16's smallest
-// value is 2^-38 of that.
+// weight, so it enters the exponent instead, relative to a reference of its own: with m = max x
+// and m + d = max (x_j + e_j) (base 2),
+//   P_j = 2^(x_j + e_j - m - d) is at most 1 (times 2^kLazy), O = sum P_j code_j,
+//   l = sum 2^(x_j - m),
+// and 2^d O / l is the output. (With one reference for both, weights would vanish from l beside
+// values 2^126 larger than theirs: a row of zeros has e = -100.) bf16 queries become fp16 times a
+// power of two of their row, chosen so that the row's largest lies in [2^14, 2^15): what drops
+// below fp16's smallest value is 2^-38 of that.
 //
 // The warps of a CTA join their (m, l, O) in shared memory, the CTAs of a cluster, which share
 // the item and divide its keys, through distributed shared memory; ranges beyond a cluster's
@@ -45,6 +48,7 @@ namespace rows {
 constexpr int KT = 64;     // keys of one tile
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNoKey = -1e38f;  // E4M3: reference of a row that has seen no key
 
 template <int D_, int NT_, bool BF16_, bool E4M3_>
 struct Cfg {
@@ -68,7 +72,7 @@ struct Cfg {
   static constexpr int NST = (CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : 65536) / STAGE;
   static constexpr int OFF_SC = NST * STAGE;               // row scales: 2 KT bytes a stage
   static constexpr int OFF_ML = OFF_SC + (E4M3 ? NST * 2 * KT : 0);
-  static constexpr int OFF_BAR = OFF_ML + (2 * CW + 2) * RT * 4;
+  static constexpr int OFF_BAR = OFF_ML + (E4M3 ? 3 : 2) * (CW + 1) * RT * 4;
   static constexpr int USED = OFF_BAR + 256 + 1024;
   static_assert(NST >= 3 && NST <= 12, "ring");
   static_assert(CW * RT * D * 4 <= NST * STAGE, "the joined outputs reuse the ring");
@@ -228,6 +232,8 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
 }
 
 // Joins results of a row: reference, sum and weights of n parts.
+// The unit of a part's output (E4M3), from that of the parts' joint sum.
+__device__ __forceinline__ float part_unit(float m, float d, float top) { return (m - top) + d; }
 __device__ __forceinline__ float part_weight(float m, float top) {
   return m == -CUDART_INF_F ? 0.0f : ex2(m - top);
 }
@@ -264,10 +270,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
   const int g = lane >> 2, c = lane & 3;
   float o[NT][C::KS][4];  // [..][x]: columns 2x (elements 0, 1) and 2x + 1 of the lane's
   float m[NT][2], l[NT][2];
+  float dv[NT][2];  // E4M3: O's unit is 2^(m + dv)
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    m[i][0] = m[i][1] = -CUDART_INF_F;
-    l[i][0] = l[i][1] = 0.f;
+    m[i][0] = m[i][1] = E4M3 ? kNoKey : -CUDART_INF_F;
+    l[i][0] = l[i][1] = dv[i][0] = dv[i][1] = 0.f;
 #pragma unroll
     for (int x = 0; x < C::KS; ++x) o[i][x][0] = o[i][x][1] = o[i][x][2] = o[i][x][3] = 0.f;
   }
@@ -387,21 +394,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
               }
             }
           }
-        // u = x + exponent of V's row scale; sc[i][2 x + y]: key g + 8 x, row 2 c + y
-        float ve[2] = {1.0f, 1.0f};  // 2^-e of V's row scales
+        // scores in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y
+        float ev[2] = {0.f, 0.f};  // exponents of V's row scales (of a key beyond the last, any)
         if (E4M3 && p.c.scale) {
           const uint8_t* sp = smem + C::OFF_SC + st * 2 * KT + warp * 16 + g;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float f = scale_value(sp[8 * x]);
-            const int ev = (int)sp[KT + 8 * x] - 127;
-            ve[x] = __uint_as_float((uint32_t)(127 - ev) << 23);
+            ev[x] = (float)((int)sp[KT + 8 * x] - 127);
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                sc[i][2 * x + y] = fmaf((sc[i][2 * x + y] + sd[i][2 * x + y]) * f, fr[i][y],
-                                        (float)ev);
+                sc[i][2 * x + y] = (sc[i][2 * x + y] + sd[i][2 * x + y]) * f * fr[i][y];
           }
         } else {
 #pragma unroll
@@ -418,15 +423,31 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
 #pragma unroll
               for (int y = 0; y < 2; ++y)
                 if (j >= lim[i][y]) sc[i][2 * x + y] = -CUDART_INF_F;
-            if (j >= keys) ve[x] = 0.0f;  // (an unused scale may be anything)
           }
         }
-        // the reference follows the maximum when that lies more than kLazy above it
+        // the references follow their maxima when those lie more than kLazy above them (E4M3: whole
+        // numbers, so that their differences are exact)
         bool over = false;
+        float xs[NT][4], xw[NT][4];  // E4M3: logarithms of what the sum takes, and of the weights
+        auto relative = [&] {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              xs[i][2 * x] = sc[i][2 * x];
+              xs[i][2 * x + 1] = sc[i][2 * x + 1];
+              ptx::add_f32x2(xs[i][2 * x], xs[i][2 * x + 1], -m[i][0], -m[i][1]);
+              xw[i][2 * x] = xw[i][2 * x + 1] = ev[x];
+              ptx::add_f32x2(xw[i][2 * x], xw[i][2 * x + 1], -dv[i][0], -dv[i][1]);
+              ptx::add_f32x2(xw[i][2 * x], xw[i][2 * x + 1], xs[i][2 * x], xs[i][2 * x + 1]);
+            }
+        };
+        if constexpr (E4M3) relative();
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) over |= sc[i][e] > m[i][e & 1] + kLazy;
+          for (int e = 0; e < 4; ++e)
+            over |= E4M3 ? fmaxf(xs[i][e], xw[i][e]) > kLazy : sc[i][e] > m[i][e & 1] + kLazy;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
@@ -437,15 +458,28 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               const bool up = mx > m[i][y] + kLazy;
-              corr[y] = up ? ex2(m[i][y] - mx) : 1.0f;  // (0 at the first visible key)
-              if (up) m[i][y] = mx;
+              const float to = E4M3 ? ceilf(mx) : mx;
+              corr[y] = up ? ex2(m[i][y] - to) : 1.0f;  // (0 at the first visible key)
               l[i][y] *= corr[y];
+              if constexpr (E4M3) {
+                if (up) dv[i][y] += m[i][y] - to;
+                if (up) m[i][y] = to;
+                float u = fmaxf((sc[i][y] - m[i][y]) + ev[0], (sc[i][2 + y] - m[i][y]) + ev[1]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+                const bool wide = u > dv[i][y] + kLazy;
+                corr[y] = wide ? ex2(dv[i][y] - ceilf(u)) : 1.0f;
+                if (wide) dv[i][y] = ceilf(u);
+              } else if (up) {
+                m[i][y] = to;
+              }
             }
 #pragma unroll
             for (int x = 0; x < C::KS; ++x)
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[i][x][e] *= corr[e & 1];
           }
+          if constexpr (E4M3) relative();
         }
         // P^T fragments: keys 2c, 2c + 1 (and + 8) of row g. bf16 weights come with what their
         // rounding leaves, for a product of its own: rounded to 2^-8 alone they are as far off as
@@ -460,9 +494,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
           const float b1 = m[i][1] == -CUDART_INF_F ? 0.0f : m[i][1];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float p0 = ex2(sc[i][2 * x] - b0), p1 = ex2(sc[i][2 * x + 1] - b1);
-            l[i][0] = fmaf(p0, ve[x], l[i][0]);
-            l[i][1] = fmaf(p1, ve[x], l[i][1]);
+            float p0 = ex2(E4M3 ? xs[i][2 * x] : sc[i][2 * x] - b0);
+            float p1 = ex2(E4M3 ? xs[i][2 * x + 1] : sc[i][2 * x + 1] - b1);
+            l[i][0] += p0;
+            l[i][1] += p1;
+            if constexpr (E4M3) {
+              p0 = ex2(xw[i][2 * x]);
+              p1 = ex2(xw[i][2 * x + 1]);
+            }
             const uint32_t w = pack2<C::MMA_BF16>(p0, p1);
             pb[0][i][x] = transpose8(w);
             if constexpr (C::MMA_BF16)
@@ -538,6 +577,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
   float* wl = wm + C::CW * RT;                             // [CW][RT]
   float* cm = wl + C::CW * RT;                             // [RT]
   float* cl = cm + RT;                                     // [RT]
+  float* wd = cl + RT;                                     // [CW][RT], E4M3: units of O
+  float* cd = wd + C::CW * RT;                             // [RT]
   float* part = reinterpret_cast<float*>(smem);            // [CW][RT][D] over the ring
   if (warp < C::CW) {
 #pragma unroll
@@ -549,6 +590,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
         if (g == 0) {
           wm[warp * RT + 8 * i + 2 * c + y] = m[i][y];
           wl[warp * RT + 8 * i + 2 * c + y] = l[i][y];
+          if constexpr (E4M3) wd[warp * RT + 8 * i + 2 * c + y] = dv[i][y];
         }
       }
   }
@@ -570,7 +612,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int w = 0; w < C::CW; ++w) top = fmaxf(top, wm[w * RT + r]);
-        const float f = part_weight(m[i][y], top);
+        float f;
+        if constexpr (E4M3) {
+          float unit = -CUDART_INF_F;
+#pragma unroll
+          for (int w = 0; w < C::CW; ++w)
+            unit = fmaxf(unit, part_unit(wm[w * RT + r], wd[w * RT + r], top));
+          f = part_weight(part_unit(m[i][y], dv[i][y], top), unit);
+        } else {
+          f = part_weight(m[i][y], top);
+        }
 #pragma unroll
         for (int cb = 0; cb < C::NCB; ++cb) {
           float* dst = part + (warp * RT + r) * D + cb * C::BE + C::NV * g;
@@ -590,6 +641,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
     for (int w = 0; w < C::CW; ++w) sum = fmaf(part_weight(wm[w * RT + r], top), wl[w * RT + r], sum);
     cm[r] = top;
     cl[r] = sum;
+    if constexpr (E4M3) {
+      float unit = -CUDART_INF_F;
+      for (int w = 0; w < C::CW; ++w)
+        unit = fmaxf(unit, part_unit(wm[w * RT + r], wd[w * RT + r], top));
+      cd[r] = unit;
+    }
   }
   __syncthreads();
 
@@ -617,18 +674,27 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
   for (int x = rank * C::THREADS + threadIdx.x; x < nrows * pieces; x += cluster * C::THREADS) {
     const int r = x / pieces, d = x % pieces * 4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float top = cm[r], sum = cl[r];
+    float top = cm[r], sum = cl[r], unit = E4M3 ? cd[r] : 0.f;
     if (cluster > 1) {
       top = -CUDART_INF_F;
       sum = 0.f;
       for (int w = 0; w < parts; ++w) top = fmaxf(top, cg::this_cluster().map_shared_rank(cm, w)[r]);
+      if constexpr (E4M3) {
+        unit = -CUDART_INF_F;
+        for (int w = 0; w < parts; ++w)
+          unit = fmaxf(unit, part_unit(cg::this_cluster().map_shared_rank(cm, w)[r],
+                                       cg::this_cluster().map_shared_rank(cd, w)[r], top));
+      }
     }
     for (int w = 0; w < parts; ++w) {
       float f = 1.0f;
       const float* src = part + (w * RT + r) * D + d;
       if (cluster > 1) {
-        f = part_weight(cg::this_cluster().map_shared_rank(cm, w)[r], top);
+        const float mw = cg::this_cluster().map_shared_rank(cm, w)[r];
+        f = part_weight(mw, top);
         sum = fmaf(f, cg::this_cluster().map_shared_rank(cl, w)[r], sum);
+        if constexpr (E4M3)
+          f = part_weight(part_unit(mw, cg::this_cluster().map_shared_rank(cd, w)[r], top), unit);
         src = cg::this_cluster().map_shared_rank(part, w) + r * D + d;
       }
       const float4 b = *reinterpret_cast<const float4*>(src);
@@ -636,7 +702,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
     }
     const long long pr = it.m0 + r;
     const long long row = (it.s.t0 + pr / p.G) * p.Nq + it.hk * p.G + pr % p.G;  // of out and lse
-    const float inv = sum == 0.0f ? 0.0f : fv / sum;
+    float inv = sum == 0.0f ? 0.0f : fv / sum;
+    if constexpr (E4M3) {  // 2^unit in two factors: it may pass fp32's range
+      const float half = truncf(unit * 0.5f), rest = ex2(unit - half);
+      inv *= ex2(half);
+      a = make_float4(a.x * rest, a.y * rest, a.z * rest, a.w * rest);
+    }
     a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     if (it.nsplit > 1) {
       *reinterpret_cast<float4*>(

@@ -32,10 +32,13 @@
 // relative to the largest of its row scales, 2^EK (K) or 2^EV (V): a code becomes fp16 by one
 // conversion and one product with 2^(e - EK), exact unless it drops below 2^-24, that is 2^-32
 // of what the tile's largest elements are. 2^EK multiplies the scores. 2^EV would leave fp16's
-// range as a factor of the weights, so it enters their exponent: with u = x + EV,
-//   P = 2^(u - m), m following max u, l += 2^-EV sum P,
-// and O / l is the output (2^m cancels). bf16 queries become fp16 in place, times a power of two
-// of their row, chosen so that the row's largest lies in [2^14, 2^15). (Dequantising to q's type
+// range as a factor of the weights, so it enters their exponent, and O has a unit of its own: with
+// m following max x, as ever, and m + d following max (x + EV),
+//   P = 2^(x + EV - m - d), O += P V in units of 2^(m + d), l += 2^(d - EV) sum P in units of 2^m,
+// and 2^d O / l is the output. (With one reference for both, weights would vanish from l beside
+// values 2^126 larger than theirs; a tile of zeros has EV = -100.) The references are whole
+// numbers, so that 2^d and EV - d - m are exact. bf16 queries become fp16 in place, times a power of two of
+// their row, chosen so that the row's largest lies in [2^14, 2^15). (Dequantising to q's type
 // instead took twice the instructions: 1028 us where this took 837, 4096 tokens over 4096.)
 //
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
@@ -57,6 +60,9 @@ namespace sm {
 constexpr float kLazy = 8.0f;  // log2 of the largest weight
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
+constexpr float kNoKey = -1e38f;          // E4M3: reference of a row that has seen no key
+constexpr float kApart = 96.0f;           // E4M3: d - EV of tiles whose sums are computed apart
+constexpr float kLargeScore = 4194304.0f; // E4M3: beyond 2^22, EV - d - m is not exact
 
 template <int D_, int NQT_, int CTAS_, bool E4M3_>
 struct Cfg {
@@ -107,7 +113,7 @@ constexpr int kExpDepth = 8;  // tiles whose exponents are kept (the conversion 
 
 struct Bars {
   uint64_t q_ready[2], q_empty, o_empty[2], exp_full[kExpDepth];
-  float tile_exp[kExpDepth][2];  // EK, EV
+  float tile_exp[kExpDepth][2];  // 2^EK, EV
   uint64_t q_full, kv_full[8], kv_empty[8], st_full[4], st_empty[4];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;
   uint32_t tmem_base;
@@ -386,6 +392,11 @@ __device__ __forceinline__ float power2(int e) {  // e in [-126, 127]
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -497,6 +508,10 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
   Seg it;
   walk_begin<C>(p, pl, tiles, walk);
   while (walk_next<C>(p, pl, walk, tiles, it)) {
+    uint32_t one = 0x3c003c00u;  // 1.0 twice; keys change sign if their static factor is negative
+    if (!values && p.c.k_ds &&
+        p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h] < 0.0f)
+      one ^= 0x80008000u;
     for (int x = 0; x < 2 * it.nmax; ++x) {
       int t;
       if (ring_tile<C>(x, it.nmax, t) != values) continue;
@@ -517,12 +532,12 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
         for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
       }
       if (warp == 0 && lane == 0) {
-        bars->tile_exp[te][values ? 1 : 0] = (float)(top - 127);
+        bars->tile_exp[te][values ? 1 : 0] = values ? (float)(top - 127) : power2(top - 127);
         ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[te]));
       }
       const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
       uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
-      uint32_t mine = 0x3c003c00u;  // factor of row my_row, twice (0 beyond the sequence)
+      uint32_t mine = one;  // factor of row my_row, twice (0 beyond the sequence)
       if (p.c.scale) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
       if (my_row >= have) mine = 0u;
       uint4 u[PASSES];
@@ -875,7 +890,9 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     if (p.causal && valid) see = min(see, it.s.Lk - it.s.n + tok + 1);
     const int lim = (int)max(see - it.k0, 0ll);
     const int rest = (int)min(it.s.Lk - it.k0, 0x7fffffffll);  // keys of the sequence from k0 on
-    float m = -CUDART_INF_F, l = 0.0f;
+    float m = C::E4M3 ? kNoKey : -CUDART_INF_F, l = 0.0f;
+    float d = 0.0f, o_ref = m;        // E4M3: O's unit is 2^(m + d)
+    float lowest = -CUDART_INF_F;     // EV below which a tile's sum is computed apart
     for (int t = 0; t < n; ++t, ++g) {
       const int sb = C::NSB == 2 ? (g & 1) : q;
       const uint32_t par = C::NSB == 2 ? (g >> 1) & 1 : g & 1;
@@ -887,34 +904,33 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         // of the last piece could otherwise be here phases ahead of it)
         const uint32_t te = done + t;
         if (!warp_wait(p, bars, &bars->exp_full[te % kExpDepth], (te / kExpDepth) & 1)) return;
-        ek = power2((int)bars->tile_exp[te % kExpDepth][0]);
+        ek = bars->tile_exp[te % kExpDepth][0];
         ev = bars->tile_exp[te % kExpDepth][1];
       }
       // Factor of the scores. For a query of zeros (or nearly) over small keys it would be 0, and
       // a masked score, -inf, NaN by it: the smallest normal value instead leaves scores below
       // 2^-90 (a NaN stays one).
-      float fa = fabsf(fk) * ek;
-      if (C::E4M3 && fa < kTiny) fa = kTiny;
+      const float fa = C::E4M3 ? max_nan(fabsf(fk) * ek, kTiny) : fk;
       const uint32_t s_col = tmem + lane_off + sb * KT;
       constexpr int NC = C::SC / 32;  // chunks held at a time
       uint32_t sv[NC][32];
       float neg = 0.0f;
+      bool apart = false;
+      float high = m + kLazy;  // a score above it raises a reference
+      if constexpr (C::E4M3) {
+        neg = ev - o_ref;
+        high = fminf(m, -neg) + kLazy;
+      }
       const int left = lim - t * KT;  // keys of the tile that the row sees
       const bool masked = !__all_sync(0xffffffffu, left >= KT);
-      // columns [c0, c0 + SC) of S: masked scores are -inf; with a negative static factor all
-      // change sign (the largest score has the smallest product), and -inf stays
+      // columns [c0, c0 + SC) of S: masked scores are -inf (fa is positive: a negative static
+      // factor has changed the keys' signs)
       auto load_scores = [&](int c0) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) ptx::tmem_ld32_issue(s_col + c0 + c * 32, sv[c]);
         ptx::tmem_ld_wait(sv[0]);
 #pragma unroll
         for (int c = 1; c < NC; ++c) ptx::reg_fence(sv[c]);
-        if (C::E4M3 && fk < 0.0f) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sv[c][e] ^= 0x80000000u;
-        }
         if (masked) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
@@ -935,13 +951,32 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
               top[(e >> 1) & 3] = ptx::max3(top[(e >> 1) & 3], __uint_as_float(sv[c][e]),
                                             __uint_as_float(sv[c][e + 1]));
         }
-        const float mx =
-            fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fa, ev);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fa;
         // raise the reference: at the first visible key, and when weights would pass 2^kLazy
-        const bool raise = valid && mx > m + kLazy;  // (any key is above -inf)
+        // (any key is above -inf)
+        const bool raise = valid && (mx > high || (C::E4M3 && ev < lowest));
         if (__any_sync(0xffffffffu, raise)) {
-          const float corr = raise ? ex2(m - mx) : 1.0f;  // (0 at the first visible key)
-          if (raise) {
+          float corr = 1.0f;  // (0 at the first visible key)
+          if constexpr (C::E4M3) {
+            if (valid && mx > m + kLazy) {
+              const float to = ceilf(mx);
+              l *= ex2(m - to);
+              d += m - to;
+              m = to;
+            }
+            const float u = (mx - m) + ev;
+            if (valid && u > d + kLazy) {
+              corr = ex2(d - ceilf(u));
+              d = ceilf(u);
+            }
+            // The sum cannot take this tile's weights: 2^-30 of its unit is below 2^-126 of O's, or
+            // neg loses bits.
+            if (raise) lowest = fabsf(m) > kLargeScore ? CUDART_INF_F : d - kApart;
+            apart = __any_sync(0xffffffffu, raise && ev < lowest);
+            o_ref = m + d;
+            neg = ev - o_ref;
+          } else if (raise) {
+            corr = ex2(m - mx);
             m = mx;
             l *= corr;
           }
@@ -957,8 +992,43 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
               ptx::tmem_st16(o_col + c, o);
             }
           }
+          // The tile in two steps then, each score relative to m first: what the sum takes, and the
+          // weight. (Few calls come here, and 16 columns at a time, in this branch that few tiles
+          // take, cost the others nothing; beside the loop below this took 4-8 % of prompts.)
+          if (C::E4M3 && apart) {
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 16) {
+              uint32_t s[16], pk[8];
+              ptx::tmem_ld16(s_col + c, s);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float x = __uint_as_float(s[e + i]);
+                  const float y = c + e + i < left ? fmaf(x, fa, -m) : -CUDART_INF_F;
+                  l += ex2(y);
+                  w[i] = ex2(y + (ev - d));
+                }
+                pk[e / 2] = pack2<false>(w[0], w[1]);
+              }
+              ptx::tmem_st8(s_col + c / 2, pk);
+              if (c == KT / 2 - 16) {
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
+              }
+            }
+            ptx::tmem_st_wait();
+            if (C::NSB > 1 && t > 0 && t == n - 1 &&
+                !warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1))
+              return;
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
+            continue;
+          }
         }
-        neg = m == -CUDART_INF_F ? 0.0f : ev - m;
+        if constexpr (!C::E4M3) neg = m == -CUDART_INF_F ? 0.0f : -m;
       }
       if constexpr (!C::E4M3) {
         // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
@@ -1003,7 +1073,8 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         }
       }
       const float tile_sum = (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
-      l = C::E4M3 ? fmaf(tile_sum, power2(-(int)ev), l) : l + tile_sum;
+      // (the sum's unit is 2^m, the weights' 2^(m + d - ev))
+      l = C::E4M3 ? fmaf(tile_sum, ex2(-neg - m), l) : l + tile_sum;
       // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
       // below needs PV(n - 2) to be done (of the piece before, it is); S(n - 1) was issued after
       // PV(n - 1 - NSB) only, and once P(n - 1) is handed over both may complete at any time.
@@ -1020,7 +1091,13 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     // out and lse of the row, or its place in the workspace
     const long long row = (it.s.t0 + tok) * p.Nq + it.hk * p.G + r % p.G;
     const long long part = (long long)it.slot * (C::NQT * 128) + q * 128 + r;
-    const float inv = l > 0.0f ? fv / l : l;  // (a NaN sum stays one)
+    float inv = l > 0.0f ? fv / l : l;  // (a NaN sum stays one)
+    float unit = 1.0f;  // 2^d in two factors: it may pass fp32's range where the output does not
+    if constexpr (C::E4M3) {
+      const int e = (int)d;
+      inv *= power2(e / 2);
+      unit = power2(e - e / 2);
+    }
     const int D = p.c.D;
 #pragma unroll 1
     for (int c = 0; any && c < D; c += 16) {
@@ -1034,7 +1111,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       if (!valid) continue;
       float f[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+      for (int e = 0; e < 16; ++e) f[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv * unit;
       if (it.slot >= 0) {
         store16(p.part_o + part * D + c, f);
       } else if constexpr (BF16) {

@@ -102,6 +102,38 @@ def directed(n, Nq, D, dtype, seed, size=3.0, noise=0.3):
     return q.to(dtype), d.double().numpy()
 
 
+ROWS = [1, 16, 17, 300]  # query rows of a kv head: both sides of the kernels' borders
+
+
+@pytest.mark.parametrize("order", ["zeros first", "zeros last", "mixed"])
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("dtype,up", [("bf16", 38), ("bf16", 90), ("fp32", 38), ("fp16", 0)])
+def test_zero_values_beside_large_ones(cuda_device, dtype, up, n, order):
+    """Value rows of zeros (scale 2^-100) that hold most of the weight beside rows of some 2^up: the
+    former count in the sum all the same."""
+    L, D = 400, 64
+    q, d = directed(n, 1, D, R.DTYPES[dtype], 9, noise=0.05)
+    g = np.random.default_rng(10)
+    v = np.ldexp(g.standard_normal((L, 1, D)), up)
+    at = np.arange(200) if order == "zeros first" else np.arange(200, 400) if order == "zeros last" else \
+        g.permutation(L)[:200]
+    v[at] = 0.0
+    k = 0.1 * g.standard_normal((L, 1, D))
+    k[at] += 3.0 / (3.0 * D ** -0.5) * d  # scores of 3 for rows of zeros, of 0 for the others
+    run(cuda_device, q, k, v, False, D ** -0.5)
+
+
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_only_zero_values(cuda_device, dtype, n):
+    """9000 value rows of zeros, with scores that lie 5 above the first tile's: out 0, lse finite."""
+    L, D = 9000, 64
+    q, d = directed(n, 1, D, R.DTYPES[dtype], 11, noise=0.01)
+    k = 0.01 * np.random.default_rng(12).standard_normal((L, 1, D))
+    k[128:] += 5.0 / (3.0 * D ** -0.5) * d
+    run(cuda_device, q, k, np.zeros((L, 1, D)), False, D ** -0.5, ps=128)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("keys", [0.0, 2.0 ** -20, 2.0 ** -60, 1.0])
 @pytest.mark.parametrize("queries", [0.0, 2.0 ** -40, 2.0 ** -110])
@@ -115,3 +147,40 @@ def test_zero_and_tiny_queries(cuda_device, dtype, D, n, L, queries, keys, causa
     g = np.random.default_rng(14)
     k, v = keys * g.standard_normal((L, 1, D)), g.standard_normal((L, 1, D))
     run(cuda_device, q, k, v, causal, D ** -0.5)
+
+
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_scores_of_hundreds_of_millions(cuda_device, dtype, n):
+    """Three equal keys, far from each other, take all the weight, with scores that 24 bits hold to a
+    few units only; their values are of unlike sizes."""
+    L, D = 300, 64
+    q, d = directed(n, 1, D, R.DTYPES[dtype], 17, size=2e4, noise=0.0)
+    g = np.random.default_rng(18)
+    c = g.uniform(-1.0, 0.5, L)
+    c[[20, 170, 290]] = 1.0
+    v = np.ldexp(g.standard_normal((L, 1, D)), g.integers(-2, 3, (L, 1, 1)))
+    v[128:256] *= 2.0 ** -8
+    run(cuda_device, q, (1e4 * c)[:, None, None] * d, v, False, 1.0, sharp=True)
+
+
+@pytest.mark.parametrize("kf,vf", [(-0.02, 0.03), (0.02, -0.03), (-0.02, -0.03)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D,n", [("bf16", 128, 300), ("fp16", 128, 300), ("fp16", 64, 40), ("bf16", 256, 40),
+                                       ("bf16", 64, 300), ("bf16", 128, 1), ("fp32", 64, 40), ("fp32", 64, 1)])
+def test_negative_static_factors(cuda_device, dtype, D, n, causal, kf, vf):
+    """Static factors of either sign, per head."""
+    dev, L, ps = cuda_device, 400, 32
+    q, _ = directed(n, 2, D, R.DTYPES[dtype], 19, noise=1.0)
+    g = np.random.default_rng(20)
+    t = R.Table([L], ps)
+    page, row = t.rows(0)
+    cache, vals = np.full((t.num_pages, 2, ps, 1, D), np.nan), []
+    for plane, f in ((0, kf), (1, vf)):
+        cache[page, plane, row] = R.e4m3_round(60.0 * g.standard_normal((L, 1, D)))
+        vals.append(cache[page, plane, row] * float(np.float32(f)))
+    got, lse = hstu_softmax_fwd(q.to(dev), torch.tensor(cache).float().to(R.FP8).to(dev), R.offsets([n]).to(dev),
+                                max_seqlen=n, max_seqlen_k=L, causal=causal, alpha=D ** -0.5, return_lse=True,
+                                k_descale=torch.full((1, 1), kf, device=dev),
+                                v_descale=torch.full((1, 1), vf, device=dev), **t.args(dev))
+    check(q, *vals, got, lse, causal, D ** -0.5)

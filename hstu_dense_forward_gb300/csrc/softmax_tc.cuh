@@ -30,16 +30,27 @@
 //
 // E4M3 caches: both products run in fp16, which holds every code exactly. A tile's rows are taken
 // relative to the largest of its row scales, 2^EK (K) or 2^EV (V): a code becomes fp16 by one
-// conversion and one product with 2^(e - EK), exact unless it drops below 2^-24, that is 2^-32
-// of what the tile's largest elements are. 2^EK multiplies the scores. 2^EV would leave fp16's
+// conversion and one product with 2^(e - EK). 2^EK multiplies the scores. 2^EV would leave fp16's
 // range as a factor of the weights, so it enters their exponent, and O has a unit of its own: with
 // m following max x, as ever, and m + d following max (x + EV),
 //   P = 2^(x + EV - m - d), O += P V in units of 2^(m + d), l += 2^(d - EV) sum P in units of 2^m,
 // and 2^d O / l is the output. (With one reference for both, weights would vanish from l beside
 // values 2^126 larger than theirs; a tile of zeros has EV = -100.) The references are whole
-// numbers, so that 2^d and EV - d - m are exact. bf16 queries become fp16 in place, times a power of two of
-// their row, chosen so that the row's largest lies in [2^14, 2^15). (Dequantising to q's type
-// instead took twice the instructions: 1028 us where this took 837, 4096 tokens over 4096.)
+// numbers, so that 2^d and EV - d - m are exact. bf16 queries become fp16 in place, times a power
+// of two of their row, chosen so that the row's largest lies in [2^14, 2^15): what drops below
+// fp16's smallest value is 2^-38 of that. (Dequantising to q's type instead took twice the
+// instructions: 1028 us where this took 837, 4096 tokens over 4096.)
+//
+// That is exact for keys within 2^14 of each other (a code's last bit is 2^-9, fp16's 2^-24), and
+// for values it keeps the weights' bits within 2^7: max (x + EV) is at most 2^7 above the largest
+// of weight times scale, and O's unit lies 2^7 below that, so that weights keep 2^-31 of it. Tiles
+// whose rows lie farther apart (outliers) keep their codes, and every column its row's exponents:
+//   x_j = 2^ek_j (q . code_j), P_j = 2^(x_j + ev_j - m - d).
+// So a row's weight and value keep their bits whatever other rows of its tile hold, seen or not.
+// Rows of the smallest scale that is written, 2^-100, do not count here: they are zeros, or count
+// as such beside rows of 2^-85. (Prompts of which every tile has such an outlier take longer: 2048
+// tokens over 2048, four of 16 heads, D = 64 708 instead of 218 us, D = 128 741 and 266, D = 256 843
+// and 480.)
 //
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
@@ -47,6 +58,7 @@
 #include <cuda.h>
 
 #include <math_constants.h>
+#include <stddef.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -59,10 +71,14 @@ namespace sm {
 
 constexpr float kLazy = 8.0f;  // log2 of the largest weight
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kTiny = 1.17549435e-38f;  // 2^-126
-constexpr float kNoKey = -1e38f;          // E4M3: reference of a row that has seen no key
-constexpr float kApart = 96.0f;           // E4M3: d - EV of tiles whose sums are computed apart
-constexpr float kLargeScore = 4194304.0f; // E4M3: beyond 2^22, EV - d - m is not exact
+// E4M3:
+constexpr float kTiny = 1.17549435e-38f;    // 2^-126
+constexpr float kNoKey = -1e38f;            // reference of a row that has seen no key
+constexpr float kHead = 7.0f;               // log2 of the largest weight when O's unit is set
+constexpr int kSpreadK = 14, kSpreadV = 7;  // spread of exponents that are taken relative to one
+constexpr uint32_t kLeast = 27;             // smallest row scale that is written
+constexpr float kApart = 96.0f;             // d - EV of tiles whose sums are computed apart
+constexpr float kLargeScore = 4194304.0f;   // from 2^22 on, EV - d - m may not be exact
 
 template <int D_, int NQT_, int CTAS_, bool E4M3_>
 struct Cfg {
@@ -102,7 +118,7 @@ struct Cfg {
   static constexpr int OFF_ST = OFF_KV + NSLOT * KV_TILE;
   static constexpr int OFF_SC = OFF_ST + NST * ST_TILE;  // row scales of the staged tiles
   static constexpr int OFF_BAR = OFF_SC + NST * 128;
-  static constexpr int OFF_PLAN = OFF_BAR + 2048;
+  static constexpr int OFF_PLAN = OFF_BAR + (E4M3 ? 4096 : 2048);
   static constexpr int USED = OFF_PLAN + kPlanSharedBytes + 1024;  // (alignment of the base)
   // (one CTA per SM, which takes all of TMEM: no second one may come to wait for it)
   static constexpr int SMEM = CTAS == 1 && USED < 120 * 1024 ? 120 * 1024 : USED;
@@ -113,13 +129,16 @@ constexpr int kExpDepth = 8;  // tiles whose exponents are kept (the conversion 
 
 struct Bars {
   uint64_t q_ready[2], q_empty, o_empty[2], exp_full[kExpDepth];
-  float tile_exp[kExpDepth][2];  // 2^EK, EV
   uint64_t q_full, kv_full[8], kv_empty[8], st_full[4], st_empty[4];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], drain;
   uint32_t tmem_base;
   volatile int abort;
+  // E4M3: 2^EK, EV, and whether the rows of K, of V have exponents of their own; then what the
+  // softmax takes for every row's, biased by 127
+  alignas(16) float tile_exp[kExpDepth][4];
+  uint8_t row_exp[kExpDepth][2][128];
 };
-static_assert(sizeof(Bars) <= 2048, "barrier block");
+static_assert(offsetof(Bars, tile_exp) <= 2048 && sizeof(Bars) <= 4096, "barrier block");
 
 // A piece of one item: key tiles [a, b) of it.
 struct Seg {
@@ -379,9 +398,9 @@ __device__ __forceinline__ bool warp_wait(const SoftmaxParams& p, Bars* bars, ui
   return __all_sync(0xffffffffu, wait_bar(p, bars, bar, parity));
 }
 
-// 2^-d as an fp16 pattern (0 below the smallest value).
+// 2^-d as an fp16 pattern, d in [0, 14]; beyond, 0 (rows of the smallest scale).
 __device__ __forceinline__ uint32_t half_power(int d) {
-  return d < 15 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
+  return d < 15 ? (uint32_t)(15 - d) << 10 : 0u;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -521,24 +540,38 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
       if (!warp_wait(p, bars, &bars->st_full[st], (i / C::NST) & 1)) return;
       const uint8_t* scale = smem + C::OFF_SC + st * 128;
       int top = 127;  // the largest scale of the tile's rows
+      uint32_t exps = 0x7f7f7f7fu;
+      bool own = false;  // the rows keep exponents of their own
       if (p.c.scale) {
-        uint32_t s4 = 0;
-        if (lane * 4 < C::KT) s4 = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
-        top = 0;
+        if (lane * 4 < C::KT) exps = *reinterpret_cast<const uint32_t*>(scale + lane * 4);
+        uint32_t b[4], high = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (lane * 4 + e < have) top = max(top, (int)((s4 >> (8 * e)) & 0xffu));
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        for (int e = 0; e < 4; ++e) {
+          b[e] = lane * 4 + e < have ? (exps >> (8 * e)) & 0xffu : kLeast;
+          high = max(high, b[e]);
+        }
+        top = (int)__reduce_max_sync(0xffffffffu, high);
+        // scales in (kLeast, top - spread) lie apart
+        const int spread = values ? kSpreadV : kSpreadK;
+        const uint32_t least = kLeast + 1, range = (uint32_t)max(top - spread - (int)least, 0);
+        own = __any_sync(0xffffffffu, b[0] - least < range || b[1] - least < range ||
+                                          b[2] - least < range || b[3] - least < range);
+        if (!own) exps = (uint32_t)top * 0x01010101u;
       }
-      if (warp == 0 && lane == 0) {
-        bars->tile_exp[te][values ? 1 : 0] = values ? (float)(top - 127) : power2(top - 127);
-        ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[te]));
+      if (warp == 0) {
+        if (lane * 4 < C::KT)
+          *reinterpret_cast<uint32_t*>(&bars->row_exp[te][values ? 1 : 0][lane * 4]) = exps;
+        __syncwarp();
+        if (lane == 0) {
+          bars->tile_exp[te][values ? 1 : 0] = values ? (float)(top - 127) : power2(top - 127);
+          bars->tile_exp[te][values ? 3 : 2] = own ? 1.0f : 0.0f;
+          ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[te]));
+        }
       }
       const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
       uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
       uint32_t mine = one;  // factor of row my_row, twice (0 beyond the sequence)
-      if (p.c.scale) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
+      if (p.c.scale && !own) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
       if (my_row >= have) mine = 0u;
       uint4 u[PASSES];
 #pragma unroll
@@ -899,13 +932,16 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       if (!warp_wait(p, bars, &bars->s_full[sb], par)) return;
       ptx::tc_fence_after();
       float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
+      bool own = false;            // its rows have exponents of their own
       if constexpr (C::E4M3) {
         // (with the scores there the conversion has come to this tile; a warpgroup without tiles
         // of the last piece could otherwise be here phases ahead of it)
         const uint32_t te = done + t;
         if (!warp_wait(p, bars, &bars->exp_full[te % kExpDepth], (te / kExpDepth) & 1)) return;
-        ek = bars->tile_exp[te % kExpDepth][0];
-        ev = bars->tile_exp[te % kExpDepth][1];
+        const float4 x = *reinterpret_cast<const float4*>(bars->tile_exp[te % kExpDepth]);
+        ek = x.x;
+        ev = x.y;
+        own = x.z + x.w > 0.0f;
       }
       // Factor of the scores. For a query of zeros (or nearly) over small keys it would be 0, and
       // a masked score, -inf, NaN by it: the smallest normal value instead leaves scores below
@@ -915,11 +951,10 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       constexpr int NC = C::SC / 32;  // chunks held at a time
       uint32_t sv[NC][32];
       float neg = 0.0f;
-      bool apart = false;
       float high = m + kLazy;  // a score above it raises a reference
       if constexpr (C::E4M3) {
         neg = ev - o_ref;
-        high = fminf(m, -neg) + kLazy;
+        high = fminf(m, kHead - neg) + kLazy;
       }
       const int left = lim - t * KT;  // keys of the tile that the row sees
       const bool masked = !__all_sync(0xffffffffu, left >= KT);
@@ -939,6 +974,20 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
               if (c0 + c * 32 + e >= left) sv[c][e] = 0xff800000u;
         }
       };
+      auto rescale = [&](float corr) {  // O, by a factor
+        // (S(t) was issued after PV(t - 2) was done: this phase is the next one)
+        if (!warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1)) return false;
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < C::D; c += 16) {
+          uint32_t o[16];
+          ptx::tmem_ld16(o_col + c, o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          ptx::tmem_st16(o_col + c, o);
+        }
+        return true;
+      };
       if (any) {
         float top[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll 1
@@ -955,78 +1004,94 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         // raise the reference: at the first visible key, and when weights would pass 2^kLazy
         // (any key is above -inf)
         const bool raise = valid && (mx > high || (C::E4M3 && ev < lowest));
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, raise || own)) {
           float corr = 1.0f;  // (0 at the first visible key)
           if constexpr (C::E4M3) {
-            if (valid && mx > m + kLazy) {
-              const float to = ceilf(mx);
+            // f(score relative to `ref`, exponent of the value row) of 16 keys from c on
+            const uint8_t* rows = bars->row_exp[(done + t) % kExpDepth][0];
+            auto columns = [&](int c, float ref, auto f) {
+              uint32_t s[16];
+              ptx::tmem_ld16(s_col + c, s);
+              const uint4 ku = *reinterpret_cast<const uint4*>(rows + c);
+              const uint4 vu = *reinterpret_cast<const uint4*>(rows + 128 + c);
+              const uint32_t kw[4] = {ku.x, ku.y, ku.z, ku.w}, vw[4] = {vu.x, vu.y, vu.z, vu.w};
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t kb = (kw[e >> 2] >> (8 * (e & 3))) & 0xffu;
+                const int vb = (int)((vw[e >> 2] >> (8 * (e & 3))) & 0xffu) - 127;
+                // (rounded like `top`: an exact product would be far from a large one's rounding)
+                const float y = __fmul_rn(__uint_as_float(s[e]), fabsf(fk) * scale_value(kb)) - ref;
+                f(e, c + e < left ? y : -CUDART_INF_F, (float)vb);
+              }
+            };
+            float top = mx;
+            if (own) {  // (mx took codes for keys)
+              top = -CUDART_INF_F;
+#pragma unroll 1
+              for (int c = 0; c < KT; c += 16)
+                columns(c, 0.0f, [&](int, float y, float) { top = fmaxf(top, y); });
+            }
+            if (valid && top > m + kLazy) {
+              const float to = ceilf(top);
               l *= ex2(m - to);
               d += m - to;
               m = to;
             }
-            const float u = (mx - m) + ev;
-            if (valid && u > d + kLazy) {
-              corr = ex2(d - ceilf(u));
-              d = ceilf(u);
+            float u = (top - m) + ev;
+            if (own) {
+              u = -CUDART_INF_F;
+#pragma unroll 1
+              for (int c = 0; c < KT; c += 16)
+                columns(c, m, [&](int, float y, float e) { u = fmaxf(u, y + e); });
+            }
+            if (valid && u > d + (kHead + kLazy)) {
+              const float to = ceilf(u) - kHead;
+              corr = ex2(d - to);
+              d = to;
             }
             // The sum cannot take this tile's weights: 2^-30 of its unit is below 2^-126 of O's, or
             // neg loses bits.
-            if (raise) lowest = fabsf(m) > kLargeScore ? CUDART_INF_F : d - kApart;
-            apart = __any_sync(0xffffffffu, raise && ev < lowest);
+            if (valid && m != kNoKey) lowest = fabsf(m) > kLargeScore ? CUDART_INF_F : d - kApart;
+            const bool apart = __any_sync(0xffffffffu, ev < lowest) || own;
             o_ref = m + d;
             neg = ev - o_ref;
+            // Tiles of either kind in two steps: each score relative to m first, which is what the
+            // sum takes, then the weight. (Few calls come here. 16 columns at a time, in this
+            // branch that few tiles take, cost the others nothing; beside the loop below this took
+            // 4-8 % of prompts.)
+            if (apart) {
+              if (t > 0 && __any_sync(0xffffffffu, corr != 1.0f) && !rescale(corr)) return;
+#pragma unroll 1
+              for (int c = 0; c < KT; c += 16) {
+                uint32_t pk[8];
+                float w[16];
+                columns(c, m, [&](int i, float y, float e) {
+                  l += ex2(y);
+                  w[i] = ex2(y + (e - d));
+                });
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pk[e] = pack2<false>(w[2 * e], w[2 * e + 1]);
+                ptx::tmem_st8(s_col + c / 2, pk);
+                if (c == KT / 2 - 16) {
+                  ptx::tmem_st_wait();
+                  ptx::tc_fence_before();
+                  ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
+                }
+              }
+              ptx::tmem_st_wait();
+              if (C::NSB > 1 && t > 0 && t == n - 1 &&
+                  !warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1))
+                return;
+              ptx::tc_fence_before();
+              ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
+              continue;
+            }
           } else if (raise) {
             corr = ex2(m - mx);
             m = mx;
             l *= corr;
           }
-          if (t > 0) {  // (S(t) was issued after PV(t - 2) was done: this phase is the next one)
-            if (!warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1)) return;
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < C::D; c += 16) {
-              uint32_t o[16];
-              ptx::tmem_ld16(o_col + c, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              ptx::tmem_st16(o_col + c, o);
-            }
-          }
-          // The tile in two steps then, each score relative to m first: what the sum takes, and the
-          // weight. (Few calls come here, and 16 columns at a time, in this branch that few tiles
-          // take, cost the others nothing; beside the loop below this took 4-8 % of prompts.)
-          if (C::E4M3 && apart) {
-#pragma unroll 1
-            for (int c = 0; c < KT; c += 16) {
-              uint32_t s[16], pk[8];
-              ptx::tmem_ld16(s_col + c, s);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float w[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float x = __uint_as_float(s[e + i]);
-                  const float y = c + e + i < left ? fmaf(x, fa, -m) : -CUDART_INF_F;
-                  l += ex2(y);
-                  w[i] = ex2(y + (ev - d));
-                }
-                pk[e / 2] = pack2<false>(w[0], w[1]);
-              }
-              ptx::tmem_st8(s_col + c / 2, pk);
-              if (c == KT / 2 - 16) {
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
-              }
-            }
-            ptx::tmem_st_wait();
-            if (C::NSB > 1 && t > 0 && t == n - 1 &&
-                !warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1))
-              return;
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
-            continue;
-          }
+          if (t > 0 && !rescale(corr)) return;
         }
         if constexpr (!C::E4M3) neg = m == -CUDART_INF_F ? 0.0f : -m;
       }

@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
             for (int i = 0; i < NT; ++i)
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                sc[i][2 * x + y] = (sc[i][2 * x + y] + sd[i][2 * x + y]) * f * fr[i][y];
+                // (the factors first: their product is in range where the score is)
+                sc[i][2 * x + y] = (sc[i][2 * x + y] + sd[i][2 * x + y]) * (f * fr[i][y]);
           }
         } else {
 #pragma unroll

@@ -205,6 +205,17 @@ def test_zero_and_tiny_queries(cuda_device, dtype, D, n, L, queries, keys, causa
 
 
 @pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_large_keys_and_small_queries(cuda_device, dtype, n):
+    """Queries of some 2^-115 over keys of some 2^115: scores of ordinary size."""
+    q, _ = directed(n, 2, 128, R.DTYPES["fp32"], 15, noise=1.0)
+    q = (q * 2.0 ** -115).to(R.DTYPES[dtype])
+    g = np.random.default_rng(16)
+    k, v = np.ldexp(g.standard_normal((300, 1, 128)), 115), g.standard_normal((300, 1, 128))
+    run(cuda_device, q, k, v, True, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("n", ROWS)
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_scores_of_hundreds_of_millions(cuda_device, dtype, n):
     """Three equal keys, far from each other, take all the weight, with scores that 24 bits hold to a

@@ -71,6 +71,9 @@ namespace sm {
 
 constexpr float kLazy = 8.0f;  // log2 of the largest weight
 constexpr float kLn2 = 0.69314718055994530942f;
+// References beyond 2^22 are rounded by 1/4 and more, and what is relative to them is computed so
+// that the largest score is 0 all the same.
+constexpr float kLargeScore = 4194304.0f;
 // E4M3:
 constexpr float kTiny = 1.17549435e-38f;    // 2^-126
 constexpr float kNoKey = -1e38f;            // reference of a row that has seen no key
@@ -78,7 +81,6 @@ constexpr float kHead = 7.0f;               // log2 of the largest weight when O
 constexpr int kSpreadK = 14, kSpreadV = 7;  // spread of exponents that are taken relative to one
 constexpr uint32_t kLeast = 27;             // smallest row scale that is written
 constexpr float kApart = 96.0f;             // d - EV of tiles whose sums are computed apart
-constexpr float kLargeScore = 4194304.0f;   // from 2^22 on, EV - d - m may not be exact
 
 template <int D_, int NQT_, int CTAS_, bool E4M3_>
 struct Cfg {
@@ -926,6 +928,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     float m = C::E4M3 ? kNoKey : -CUDART_INF_F, l = 0.0f;
     float d = 0.0f, o_ref = m;        // E4M3: O's unit is 2^(m + d)
     float lowest = -CUDART_INF_F;     // EV below which a tile's sum is computed apart
+    float high = -CUDART_INF_F;       // a score above it raises a reference
     for (int t = 0; t < n; ++t, ++g) {
       const int sb = C::NSB == 2 ? (g & 1) : q;
       const uint32_t par = C::NSB == 2 ? (g >> 1) & 1 : g & 1;
@@ -951,7 +954,6 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       constexpr int NC = C::SC / 32;  // chunks held at a time
       uint32_t sv[NC][32];
       float neg = 0.0f;
-      float high = m + kLazy;  // a score above it raises a reference
       if constexpr (C::E4M3) {
         neg = ev - o_ref;
         high = fminf(m, kHead - neg) + kLazy;
@@ -973,6 +975,21 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             for (int e = 0; e < 32; ++e)
               if (c0 + c * 32 + e >= left) sv[c][e] = 0xff800000u;
         }
+      };
+      // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN. (E4M3: the
+      // conversion has done that.)
+      auto clear_values = [&] {
+        const int have = rest - t * KT;
+        if (C::E4M3 || have >= KT) return true;
+        const uint32_t vi = ring + v_index<C>(t, it.nmax);
+        if (!warp_wait(p, bars, &bars->kv_full[vi % C::NSLOT], (vi / C::NSLOT) & 1)) return false;
+        uint8_t* v = smem + C::OFF_KV + (vi % C::NSLOT) * C::KV_TILE;
+        const int pieces = (KT - have) * (C::SWB / 16);  // of one column block
+        for (int x = r; x < C::NCB * pieces; x += 128)
+          *reinterpret_cast<uint4*>(v + (x / pieces) * C::KV_CB + have * C::SWB +
+                                    (x % pieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();
+        return true;
       };
       auto rescale = [&](float corr) {  // O, by a factor
         // (S(t) was issued after PV(t - 2) was done: this phase is the next one)
@@ -1006,24 +1023,29 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         const bool raise = valid && (mx > high || (C::E4M3 && ev < lowest));
         if (__any_sync(0xffffffffu, raise || own)) {
           float corr = 1.0f;  // (0 at the first visible key)
-          if constexpr (C::E4M3) {
-            // f(score relative to `ref`, exponent of the value row) of 16 keys from c on
-            const uint8_t* rows = bars->row_exp[(done + t) % kExpDepth][0];
-            auto columns = [&](int c, float ref, auto f) {
-              uint32_t s[16];
-              ptx::tmem_ld16(s_col + c, s);
-              const uint4 ku = *reinterpret_cast<const uint4*>(rows + c);
-              const uint4 vu = *reinterpret_cast<const uint4*>(rows + 128 + c);
-              const uint32_t kw[4] = {ku.x, ku.y, ku.z, ku.w}, vw[4] = {vu.x, vu.y, vu.z, vu.w};
+          bool apart;
+          // f(score relative to `ref`, exponent of the value row) of 16 keys from c on
+          auto columns = [&](int c, float ref, auto f) {
+            uint32_t s[16];
+            ptx::tmem_ld16(s_col + c, s);
+            uint4 ku, vu;
+            if constexpr (C::E4M3) {
+              const uint8_t* rows = bars->row_exp[(done + t) % kExpDepth][0];
+              ku = *reinterpret_cast<const uint4*>(rows + c);
+              vu = *reinterpret_cast<const uint4*>(rows + 128 + c);
+            }
+            const uint32_t kw[4] = {ku.x, ku.y, ku.z, ku.w}, vw[4] = {vu.x, vu.y, vu.z, vu.w};
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const uint32_t kb = (kw[e >> 2] >> (8 * (e & 3))) & 0xffu;
-                const int vb = (int)((vw[e >> 2] >> (8 * (e & 3))) & 0xffu) - 127;
-                // (rounded like `top`: an exact product would be far from a large one's rounding)
-                const float y = __fmul_rn(__uint_as_float(s[e]), fabsf(fk) * scale_value(kb)) - ref;
-                f(e, c + e < left ? y : -CUDART_INF_F, (float)vb);
-              }
-            };
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t kb = (kw[e >> 2] >> (8 * (e & 3))) & 0xffu;
+              const int vb = (int)((vw[e >> 2] >> (8 * (e & 3))) & 0xffu) - 127;
+              const float k = C::E4M3 ? fabsf(fk) * scale_value(kb) : fa;
+              // (rounded like m: an exact product may be far from a large one's rounding)
+              const float y = __fmul_rn(__uint_as_float(s[e]), k) - ref;
+              f(e, c + e < left ? y : -CUDART_INF_F, C::E4M3 ? (float)vb : 0.0f);
+            }
+          };
+          if constexpr (C::E4M3) {
             float top = mx;
             if (own) {  // (mx took codes for keys)
               top = -CUDART_INF_F;
@@ -1052,63 +1074,56 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             // The sum cannot take this tile's weights: 2^-30 of its unit is below 2^-126 of O's, or
             // neg loses bits.
             if (valid && m != kNoKey) lowest = fabsf(m) > kLargeScore ? CUDART_INF_F : d - kApart;
-            const bool apart = __any_sync(0xffffffffu, ev < lowest) || own;
+            apart = __any_sync(0xffffffffu, ev < lowest) || own;
             o_ref = m + d;
             neg = ev - o_ref;
-            // Tiles of either kind in two steps: each score relative to m first, which is what the
-            // sum takes, then the weight. (Few calls come here. 16 columns at a time, in this
-            // branch that few tiles take, cost the others nothing; beside the loop below this took
-            // 4-8 % of prompts.)
-            if (apart) {
-              if (t > 0 && __any_sync(0xffffffffu, corr != 1.0f) && !rescale(corr)) return;
-#pragma unroll 1
-              for (int c = 0; c < KT; c += 16) {
-                uint32_t pk[8];
-                float w[16];
-                columns(c, m, [&](int i, float y, float e) {
-                  l += ex2(y);
-                  w[i] = ex2(y + (e - d));
-                });
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pk[e] = pack2<false>(w[2 * e], w[2 * e + 1]);
-                ptx::tmem_st8(s_col + c / 2, pk);
-                if (c == KT / 2 - 16) {
-                  ptx::tmem_st_wait();
-                  ptx::tc_fence_before();
-                  ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
-                }
-              }
-              ptx::tmem_st_wait();
-              if (C::NSB > 1 && t > 0 && t == n - 1 &&
-                  !warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1))
-                return;
-              ptx::tc_fence_before();
-              ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
-              continue;
+          } else {
+            if (valid && mx > m + kLazy) {
+              corr = ex2(m - mx);
+              m = mx;
+              l *= corr;
+              high = fabsf(m) > kLargeScore ? -CUDART_INF_F : m + kLazy;
             }
-          } else if (raise) {
-            corr = ex2(m - mx);
-            m = mx;
-            l *= corr;
+            apart = __any_sync(0xffffffffu, high < m);
+          }
+          // Such tiles in two steps: each score relative to m first, which is what the sum takes,
+          // then the weight. (Few calls come here. 16 columns at a time, in this branch that few
+          // tiles take, cost the others nothing; beside the loop below this took 4-8 % of prompts.)
+          if (apart) {
+            if (t > 0 && __any_sync(0xffffffffu, corr != 1.0f) && !rescale(corr)) return;
+            if (!clear_values()) return;
+#pragma unroll 1
+            for (int c = 0; c < KT; c += 16) {
+              uint32_t pk[8];
+              float w[16];
+              columns(c, m == -CUDART_INF_F ? 0.0f : m, [&](int i, float y, float e) {
+                const float x = ex2(y);
+                l += x;
+                w[i] = C::E4M3 ? ex2(y + (e - d)) : x;
+              });
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                pk[e] = pack2<BF16 && !C::E4M3>(w[2 * e], w[2 * e + 1]);
+              ptx::tmem_st8(s_col + c / 2, pk);
+              if (c == KT / 2 - 16) {
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[sb]));
+              }
+            }
+            ptx::tmem_st_wait();
+            if (C::NSB > 1 && t > 0 && t == n - 1 &&
+                !warp_wait(p, bars, &bars->pv_done[q], (g - 1) & 1))
+              return;
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[sb]));
+            continue;
           }
           if (t > 0 && !rescale(corr)) return;
         }
         if constexpr (!C::E4M3) neg = m == -CUDART_INF_F ? 0.0f : -m;
       }
-      if constexpr (!C::E4M3) {
-        // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN
-        const int have = rest - t * KT;
-        if (have < KT) {
-          const uint32_t vi = ring + v_index<C>(t, it.nmax);
-          if (!warp_wait(p, bars, &bars->kv_full[vi % C::NSLOT], (vi / C::NSLOT) & 1)) return;
-          uint8_t* v = smem + C::OFF_KV + (vi % C::NSLOT) * C::KV_TILE;
-          const int pieces = (KT - have) * (C::SWB / 16);  // of one column block
-          for (int x = r; x < C::NCB * pieces; x += 128)
-            *reinterpret_cast<uint4*>(v + (x / pieces) * C::KV_CB + have * C::SWB +
-                                      (x % pieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          ptx::fence_proxy_async_smem();
-        }
-      }
+      if (!clear_values()) return;
       float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
       // weights of chunk `at` held in sv[i], summed and stored as columns of P
       auto weights = [&](int i, int at) {

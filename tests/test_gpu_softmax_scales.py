@@ -44,13 +44,14 @@ def quantised(k, v, ps, dev, seed=0):
     return torch.tensor(cache).float().to(R.FP8).to(dev), kw, vals[0], vals[1]
 
 
-def check(q, K, V, got, lse, causal, alpha, sharp=False):
+def check(q, K, V, got, lse, causal, alpha, sharp=False, weight_bits=11):
     """Output and lse of the last n positions against 64 bits, with the tolerance above. sharp: every
-    key scores exactly the most or far less than that, so that its errors move no weight."""
+    key scores exactly the most or far less than that, so that its errors move no weight. The weights
+    are rounded to weight_bits bits."""
     dt, q = got.dtype, R.values(q.cpu())
     n, Nq, D = q.shape
     Lk, G = K.shape[0], Nq // K.shape[1]
-    up = 0.0 if dt == torch.float32 else 2.0 ** -11
+    up = 0.0 if dt == torch.float32 else 2.0 ** -weight_bits
     u = R.HALF_STEP[dt]
     got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
     seen = np.arange(Lk)[None, :] <= ((Lk - n + np.arange(n))[:, None] if causal else Lk)
@@ -250,3 +251,32 @@ def test_negative_static_factors(cuda_device, dtype, D, n, causal, kf, vf):
                                 k_descale=torch.full((1, 1), kf, device=dev),
                                 v_descale=torch.full((1, 1), vf, device=dev), **t.args(dev))
     check(q, *vals, got, lse, causal, D ** -0.5)
+
+
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e9])
+@pytest.mark.parametrize("dtype,cache,D,n,L", [
+    ("bf16", "same", 128, 300, 900), ("bf16", "same", 128, 17, 900), ("bf16", "same", 64, 300, 900),
+    ("bf16", "same", 256, 40, 900), ("bf16", "same", 128, 1, 900), ("fp16", "same", 128, 300, 900),
+    ("fp16", "same", 64, 20, 900), ("fp32", "same", 64, 40, 900), ("bf16", "e4m3", 128, 300, 900),
+    ("fp16", "e4m3", 64, 20, 900), ("bf16", "e4m3", 256, 40, 900), ("bf16", "e4m3", 128, 1, 900)])
+def test_scores_beyond_24_bits(cuda_device, dtype, cache, D, n, L, size):
+    """Scores of up to some `size`^2 / 10: one key takes all the weight, whatever a product's rounding."""
+    dev, dt, ps = cuda_device, R.DTYPES[dtype], 32
+    if dt == torch.float16:
+        size = min(size, 4e4)
+    q, d = directed(n, 1, D, dt, 21, size=size, noise=0.0)
+    g = np.random.default_rng(22)
+    c = g.uniform(-1.0, 0.5, L)
+    c[[20, 170, 700]] = 1.0
+    k, v = (size * c)[:, None, None] * d, g.standard_normal((L, 1, D))
+    if cache == "e4m3":
+        run(dev, q, k, v, False, 0.5, sharp=True)
+        return
+    t = R.Table([L], ps)
+    page, row = t.rows(0)
+    rows = torch.full((t.num_pages, 2, ps, 1, D), torch.nan, dtype=dt)
+    rows[page, 0, row], rows[page, 1, row] = torch.tensor(k).to(dt), torch.tensor(v).to(dt)
+    got, lse = hstu_softmax_fwd(q.to(dev), rows.to(dev), R.offsets([n]).to(dev), max_seqlen=n, max_seqlen_k=L,
+                                causal=False, alpha=0.5, return_lse=True, **t.args(dev))
+    K, V = (R.values(rows[page, plane, row]) for plane in (0, 1))
+    check(q, K, V, got, lse, False, 0.5, sharp=True, weight_bits=8 if dt == torch.bfloat16 else 11)

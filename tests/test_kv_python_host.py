@@ -10,9 +10,9 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _documented_calls():
-    """Calls of the package's functions in the indented blocks of README.md."""
+    """Calls of the package's functions in the indented paragraphs of README.md."""
     text = open(os.path.join(ROOT, "README.md")).read()
-    for block in re.findall(r"(?:^    .*\n|^\n(?=    ))+", text, flags=re.M):
+    for block in re.findall(r"(?:^    .*\n)+", text, flags=re.M):
         code = "\n".join(line[4:] for line in block.split("\n"))
         try:
             tree = ast.parse(code)

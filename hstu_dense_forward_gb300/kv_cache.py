@@ -318,7 +318,10 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
         out_ptr = _tensor(out, "out", kv_cache.device, q.dtype, shape)
     lse = torch.empty((T, Nq), dtype=torch.float32, device=q.device) if return_lse else None
     sizes = (T, dtype, Nq, int(max_seqlen), int(max_seqlen_k), bool(causal), float(alpha))
-    need = _workspace_bytes(c.device, c.sizes, sizes)
+    try:
+        need = _workspace_bytes(c.device, c.sizes, sizes)
+    except (struct.error, OverflowError):  # max_seqlen, max_seqlen_k or alpha that no C type holds
+        raise _abi.HstuError(_abi.HSTU_ERR_INVALID_ARG, "hstu_softmax_fwd") from None
     workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
     _call("hstu_softmax_fwd", c,
           _PACK_ATTN(q.data_ptr(), q_stride, seq_offsets.data_ptr(), *sizes, out_ptr,

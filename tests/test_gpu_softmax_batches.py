@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kv_reference as R
-from hstu_dense_forward_gb300 import hstu_softmax_fwd
+from hstu_dense_forward_gb300 import HstuError, hstu_softmax_fwd
 from test_gpu_softmax import _filled, check, run_case
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +77,15 @@ def test_one_prompt_among_single_tokens(cuda_device, dtype, mode, Nq, Nk, D, bou
 def test_single_tokens_under_loose_bounds(cuda_device, dtype, mode):
     lengths = [(37 * b) % 400 + 1 for b in range(40)]
     run_case(cuda_device, lengths, [1] * 40, dtype, mode, 8, 2, 128, 32, bounds=(1 << 24, 1 << 30), seed=121)
+
+
+@pytest.mark.parametrize("bad", [dict(max_seqlen=1 << 31), dict(max_seqlen_k=1 << 31), dict(max_seqlen=-(1 << 40)),
+                                 dict(alpha=1e39), dict(alpha=-1e300), dict(alpha=float("inf"))])
+def test_sizes_beyond_the_abi_are_refused(cuda_device, bad):
+    dev = cuda_device
+    t = R.Table([5], 32)
+    cache, _, _ = _filled(t, 2, 64, torch.bfloat16, "same", dev, 1)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device=dev)
+    kw = dict(max_seqlen=1, max_seqlen_k=5, **t.args(dev))
+    with pytest.raises(HstuError):
+        hstu_softmax_fwd(q, cache, R.offsets([1]).to(dev), **{**kw, **bad})

@@ -102,7 +102,8 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
   if (!r->k || !r->v || !aligned(r->k, 16) || !aligned(r->v, 16) || !r->seq_offsets ||
       !aligned(r->seq_offsets, c->index_is_int64 ? 8 : 4) || r->k_stride < width ||
       r->v_stride < width || r->k_stride * eb % 16 != 0 || r->v_stride * eb % 16 != 0 ||
-      r->k_stride > (1ll << 40) || r->v_stride > (1ll << 40) || !cache_pointers_ok(c))
+      r->k_stride > (1ll << 40) || r->v_stride > (1ll << 40) || !cache_pointers_ok(c) ||
+      (!append && r->k == r->v))  // (one place for both planes)
     return HSTU_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;

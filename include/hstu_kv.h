@@ -95,7 +95,7 @@ HSTU_API hstu_status hstu_kv_append(const hstu_kv_cache* cache, const hstu_kv_ro
 
 /* Read rows of the cache into k and v, dequantised and rounded to rows->dtype: the last n
  * positions of every sequence, n = its seq_offsets difference (its whole length Lk for the
- * whole sequence). */
+ * whole sequence). k and v must not overlap. */
 HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows* rows,
                                   void* stream);
 

@@ -36,3 +36,17 @@ def test_documented_calls_pass_what_the_parameters_are_called():
         names = set(inspect.signature(f).parameters)
         assert {k.arg for k in call.keywords if k.arg} <= names, call.func.id
     assert {"hstu_fwd", "hstu_kv_append", "hstu_softmax_fwd"} <= seen
+
+
+def test_read_refuses_one_place_for_keys_and_values(built_lib):
+    """The library's check (no device call before it): k and v of a read are written."""
+    import ctypes
+    from hstu_dense_forward_gb300 import _abi
+    at = 1 << 20  # never dereferenced
+    cache = _abi.KVCache(dtype=_abi.HSTU_BF16, batch=2, num_heads_kv=2, head_dim=64, page_size=32,
+                         index_is_int64=1, kv_cache=at, num_pages=8, page_offsets=at, page_ids=at,
+                         last_page_len=at, num_page_ids=4)
+    rows = _abi.KVRows(k=at, v=at, k_stride=128, v_stride=128, seq_offsets=at, total_tokens=4,
+                       dtype=_abi.HSTU_BF16)
+    assert _abi.lib().hstu_kv_read(ctypes.byref(cache), ctypes.byref(rows), None) == \
+        _abi.HSTU_ERR_INVALID_ARG

@@ -1096,10 +1096,9 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             for (int c = 0; c < KT; c += 16) {
               uint32_t pk[8];
               float w[16];
-              columns(c, m == -CUDART_INF_F ? 0.0f : m, [&](int i, float y, float e) {
-                const float x = ex2(y);
-                l += x;
-                w[i] = C::E4M3 ? ex2(y + (e - d)) : x;
+              columns(c, !C::E4M3 && m == -CUDART_INF_F ? 0.0f : m, [&](int i, float y, float e) {
+                l += ex2(y);
+                w[i] = ex2(C::E4M3 ? y + (e - d) : y);
               });
 #pragma unroll
               for (int e = 0; e < 8; ++e)

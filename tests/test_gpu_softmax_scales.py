@@ -280,3 +280,33 @@ def test_scores_beyond_24_bits(cuda_device, dtype, cache, D, n, L, size):
                                 causal=False, alpha=0.5, return_lse=True, **t.args(dev))
     K, V = (R.values(rows[page, plane, row]) for plane in (0, 1))
     check(q, K, V, got, lse, False, 0.5, sharp=True, weight_bits=8 if dt == torch.bfloat16 else 11)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D,Nq,Nk,n", [
+    ("bf16", 128, 4, 2, 300), ("fp16", 64, 4, 2, 300), ("bf16", 256, 2, 2, 40), ("bf16", 64, 4, 1, 30),
+    ("fp16", 128, 2, 2, 20), ("bf16", 128, 4, 2, 1), ("fp16", 64, 8, 1, 2), ("fp32", 64, 4, 2, 40),
+    ("fp32", 64, 4, 2, 1)])
+def test_unlike_sizes_over_many_ctas(cuda_device, dtype, D, Nq, Nk, n, causal):
+    """A long sequence whose keys are parted among CTAs: stretches of ordinary rows, of outliers, of zeros
+    and of rows of every size, in every order."""
+    L = 6100
+    q, d = directed(n, Nq, D, R.DTYPES[dtype], 23, noise=1.0)
+    g = np.random.default_rng(24)
+    k, v = g.standard_normal((L, Nk, D)), g.standard_normal((L, Nk, D))
+    at = 0
+    while at < L:
+        end, kind = at + int(g.integers(1, 400)), g.integers(0, 6)
+        if kind == 1:
+            v[at:end] = 0.0
+        elif kind == 2:
+            v[at:end] = np.ldexp(v[at:end], g.integers(-24, 9, v[at:end].shape[:2])[..., None])
+        elif kind == 3:
+            k[at:end] = np.ldexp(k[at:end], g.integers(-40, 2, k[at:end].shape[:2])[..., None])
+        elif kind == 4:
+            v[at] = np.ldexp(v[at], 12)
+            k[at, 0] = -30.0 / (3.0 * D ** -0.5) * d
+        elif kind == 5:
+            k[at:end] = v[at:end] = 0.0
+        at = end
+    run(cuda_device, q, k, v, causal, D ** -0.5, ps=128)

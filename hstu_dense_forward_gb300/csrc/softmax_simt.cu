@@ -9,8 +9,8 @@
 // softmax_simt_kernel: 64 rows, 256 threads (16 x 16), in steps of BN keys. A thread owns rows
 // ty + 16 a, of the scores keys tx + 16 c and of the output columns 4 tx + 64 u .. + 3; every
 // operand comes from shared memory in float4 (four elements of the head dim, or four keys), so
-// that a step spends four times as many FMAs as loads. What bounds it is shared memory: 965 tokens
-// over 4000, 20 heads of 4, D = 256, take 1171 us, 36 TFLOP/s, D = 128 639.
+// that a step spends four times as many FMAs as loads. What bounds it is shared memory: 773 tokens
+// over 2275 cached ones, 20 heads of 4, D = 256, take 1171 us, 36 TFLOP/s, D = 128 639.
 //
 // softmax_few_kernel: 4 rows, for calls of at most 16, where reading the cache is what counts:
 // D / 16 lanes hold a key, two keys at a time, straight from the cache in registers, and every
@@ -42,7 +42,7 @@ template <int D_, bool E4M3>
 struct Cfg {
   static constexpr int D = D_, BM = 64;
   // Keys of a step: 64 spend more FMAs per load of the scores' operands, 32 leave an SM a second
-  // CTA at D = 128, which E4M3 rows, whose conversion waits, need more (965 tokens over 4000, 20
+  // CTA at D = 128, which E4M3 rows, whose conversion waits, need more (773 tokens over 2275, 20
   // heads, with the slower loads of sixteen elements a thread: D = 256 1479 us with 32 and 1336
   // with 64, D = 128 773 and 716, over E4M3 725 and 730).
   static constexpr int BN = D == 128 && E4M3 ? 32 : 64;

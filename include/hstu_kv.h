@@ -32,7 +32,8 @@
  * invalid is left unwritten (append, read); a sequence with such an id among its pages gets
  * unspecified attention outputs. Each sets *status (if given) to HSTU_DEVERR_OFFSETS, and a
  * pipeline wait of hstu_softmax_fwd that ran past its limit sets it to HSTU_DEVERR_TIMEOUT
- * (outputs incomplete); *status is left alone otherwise (the caller zeroes it).
+ * (outputs incomplete); *status is left alone otherwise (the caller zeroes it). A call without
+ * sequences or without rows (total_tokens = 0) has nothing to do and looks at nothing.
  */
 #ifndef HSTU_KV_H_
 #define HSTU_KV_H_
@@ -95,7 +96,9 @@ HSTU_API hstu_status hstu_kv_append(const hstu_kv_cache* cache, const hstu_kv_ro
 
 /* Read rows of the cache into k and v, dequantised and rounded to rows->dtype: the last n
  * positions of every sequence, n = its seq_offsets difference (its whole length Lk for the
- * whole sequence). k and v must not overlap. */
+ * whole sequence). k and v must not overlap. A value beyond the type's range becomes infinite:
+ * quantisation may have rounded a row's largest up to 2^16 (fp16, from 63488 on) or 2^128 (bf16
+ * and fp32, from 248 * 2^120 on). */
 HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows* rows,
                                   void* stream);
 
@@ -115,7 +118,7 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * a bf16 cache, single tokens for instance, come in two parts, whose sum is exact to 2^-16).
  * fp16 holds what is 2^-24 of the largest of the weights, or, over an E4M3 cache, of the weights
  * times their rows' scales. Rows of an E4M3 cache keep their bits whatever the scales of others,
- * but those of scale 2^-100 may count as zeros. bf16 queries over an E4M3 cache are products of
+ * but those of scale 2^-100 or less may count as zeros. bf16 queries over an E4M3 cache are products of
  * fp16 with a power of two of their row: elements below 2^-38 of its largest vanish.
  */
 typedef struct {

@@ -1028,7 +1028,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
           auto columns = [&](int c, float ref, auto f) {
             uint32_t s[16];
             ptx::tmem_ld16(s_col + c, s);
-            uint4 ku, vu;
+            uint4 ku = {}, vu = {};
             if constexpr (C::E4M3) {
               const uint8_t* rows = bars->row_exp[(done + t) % kExpDepth][0];
               ku = *reinterpret_cast<const uint4*>(rows + c);

@@ -242,7 +242,8 @@ def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_
     two per row and head, 2^(kv_scale - 127), the smallest that brings the row's largest
     magnitude to 448 or less; k_descale / v_descale (floats or one-element fp32 tensors, [B] or
     [B, Nk]: hstu_fwd's factors) divide the rows; neither is a plain cast. Rounding is to
-    nearest even, saturating at +-448.
+    nearest even, saturating at +-448. (hstu_fwd reads the last two forms; a cache with row
+    scales goes to hstu_softmax_fwd, or to hstu_fwd by way of hstu_kv_read.)
 
     status: an int32 tensor of one element that is set to 1 where offsets, lengths or page ids
     are found invalid on the device (nothing of such a sequence is written)."""

@@ -47,10 +47,12 @@
 // whose rows lie farther apart (outliers) keep their codes, and every column its row's exponents:
 //   x_j = 2^ek_j (q . code_j), P_j = 2^(x_j + ev_j - m - d).
 // So a row's weight and value keep their bits whatever other rows of its tile hold, seen or not.
-// Rows of the smallest scale that is written, 2^-100, do not count here: they are zeros, or count
-// as such beside rows of 2^-85. (Prompts of which every tile has such an outlier take longer: 2048
-// tokens over 2048, four of 16 heads, D = 64 708 instead of 218 us, D = 128 741 and 266, D = 256 843
-// and 480.)
+// (Prompts of which every tile has an outlier take longer: 2048 tokens over 2048, four of 16 heads,
+// D = 64 708 instead of 218 us, D = 128 741 and 266, D = 256 843 and 480.) Rows of the smallest
+// scale that is written, 2^-100, are left out of this: they are zeros, or count as such beside rows
+// of 2^-85. Their scores do raise O's unit, like those of a row of the tile's largest scale, and
+// weights keep 2^-31 of theirs. (Telling such rows apart where the unit is raised took 20-30 % of
+// prompts with a row of zeros in every tile.)
 //
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
@@ -976,8 +978,8 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
               if (c0 + c * 32 + e >= left) sv[c][e] = 0xff800000u;
         }
       };
-      // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN. (E4M3: the
-      // conversion has done that.)
+      // V rows beyond the sequence (their pages may hold anything) become zeros: 0 * NaN. (E4M3:
+      // the conversion has done that.)
       auto clear_values = [&] {
         const int have = rest - t * KT;
         if (C::E4M3 || have >= KT) return true;

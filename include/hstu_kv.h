@@ -118,8 +118,9 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * a bf16 cache, single tokens for instance, come in two parts, whose sum is exact to 2^-16).
  * fp16 holds what is 2^-24 of the largest of the weights, or, over an E4M3 cache, of the weights
  * times their rows' scales. Rows of an E4M3 cache keep their bits whatever the scales of others,
- * but those of scale 2^-100 or less may count as zeros. bf16 queries over an E4M3 cache are
- * products of fp16 with a power of two of their row: elements below 2^-38 of its largest vanish.
+ * but those of scale 2^-100 or less (rows of zeros) may count as zeros, and their weights with the
+ * largest scale of the 127 rows around them. bf16 queries over an E4M3 cache are products of fp16
+ * with a power of two of their row: elements below 2^-38 of its largest vanish.
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */

@@ -10,7 +10,9 @@ rounded to fp16: by half a step, 2^-11, relatively, and by 2^-25 absolutely in t
 references. That unit times the largest code is at most twice (references are whole powers of two)
 the largest p_j 448 2^(e_j), e_j the row scale's exponent, and 448 2^(e_j) at most twice the largest
 magnitude in row j: the absolute part is at most Lk 2^-25 * 2 * 2 B = Lk 2^-23 B, B the largest
-p_j max|v_j|. The output is rounded to its type, relatively by u, and absolutely by half of the
+p_j max|v_j|. A row of zeros is no reason to treat its key tile (128 keys at most) row by row, so its
+score enters the reference with the largest scale of the tile: in B it counts like the largest row
+less than 128 rows away. The output is rounded to its type, relatively by u, and absolutely by half of the
 smallest value (fp16: 2^-25).
   |error| <= u |out| + (2^-11 + 2^-20 + Lk 2^-24) A + sum_j p_j ex_j |v_j| + (sum_j p_j ex_j) A
              + Lk 2^-23 B
@@ -70,7 +72,9 @@ def check(q, K, V, got, lse, causal, alpha, sharp=False, weight_bits=11):
         if sharp:
             assert ((x == top) | (x < top - 4 * ex - 60.0)).all()
             e1, e0 = 0.0 * e1, 0.0 * e0
-        B = (p * np.abs(v).max(1)).max(1)
+        size = np.abs(v).max(1)
+        near = np.array([size[max(0, j - 127):j + 128].max() for j in range(Lk)])
+        B = (p * np.where(size == 0.0, near, size)).max(1)
         tol = u * np.abs(out) + (up + 2.0 ** -20 + Lk * 2.0 ** -24 + e0[:, None]) * A * 1.01 + \
             e1 * 1.01 + (Lk * 2.0 ** -23 * B[:, None] if up else 0.0) + \
             (2.0 ** -25 if dt == torch.float16 else 0.0)
@@ -310,3 +314,19 @@ def test_unlike_sizes_over_many_ctas(cuda_device, dtype, D, Nq, Nk, n, causal):
             k[at:end] = v[at:end] = 0.0
         at = end
     run(cuda_device, q, k, v, causal, D ** -0.5, ps=128)
+
+
+@pytest.mark.parametrize("ahead", [5.0, 15.0, 40.0])
+@pytest.mark.parametrize("zeros", ["one", "many", "tile"])
+@pytest.mark.parametrize("n", ROWS)
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 256), ("fp32", 64)])
+def test_zero_values_with_nearly_all_the_weight(cuda_device, dtype, D, n, zeros, ahead):
+    """Value rows of zeros whose scores lie far above the others': what the others give keeps its bits."""
+    L = 500
+    q, d = directed(n, 1, D, R.DTYPES[dtype], 25, noise=0.05)
+    g = np.random.default_rng(26)
+    k, v = 0.3 * g.standard_normal((L, 1, D)), g.standard_normal((L, 1, D))
+    at = {"one": [200], "many": g.permutation(L)[:150], "tile": np.arange(128, 256)}[zeros]
+    v[at] = 0.0
+    k[at] += ahead / (3.0 * D ** -0.5) * d
+    run(cuda_device, q, k, v, False, D ** -0.5, ps=128)

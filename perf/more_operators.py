@@ -177,7 +177,7 @@ def _quantise4(x):
     code = (m > 0.25).to(torch.uint8)
     for middle in (m >= 0.75, m > 1.25, m >= 1.75, m > 2.5, m >= 3.5, m > 5):
         code += middle
-    code = (code + 8 * (x < 0)).flatten(-2)
+    code = (code + 8 * (x < 0).to(torch.uint8)).flatten(-2)
     return code[..., 0::2] | code[..., 1::2] << 4, group, (e + 127).to(torch.uint8)
 
 

@@ -18,6 +18,7 @@ KV_HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_kv.h")
 HSTU_OK, HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED, HSTU_ERR_CUDA, HSTU_ERR_TIMEOUT, \
     HSTU_ERR_DEVICE_CHECK = range(6)
 HSTU_F32, HSTU_F16, HSTU_BF16, HSTU_FP8_E4M3 = 0, 1, 2, 3
+HSTU_FP4_E2M1 = 5  # of a paged KV cache (include/hstu_kv.h)
 HSTU_MASK_CAUSAL, HSTU_MASK_UPPER, HSTU_MASK_NONE, HSTU_MASK_CUSTOM = 0, 1, 2, 3
 HSTU_DEVERR_NONE, HSTU_DEVERR_OFFSETS, HSTU_DEVERR_TIMEOUT = 0, 1, 2
 HSTU_LAYOUT_JAGGED, HSTU_LAYOUT_NORMAL = 0, 1
@@ -91,6 +92,7 @@ class KVCache(ctypes.Structure):
         ("page_ids", ctypes.c_void_p), ("last_page_len", ctypes.c_void_p),
         ("num_page_ids", ctypes.c_longlong), ("k_descale", ctypes.c_void_p),
         ("v_descale", ctypes.c_void_p), ("status", ctypes.c_void_p),
+        ("kv_group_scale", ctypes.c_void_p),
     ]
 
 

@@ -13,24 +13,31 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-int elem_bytes(int dtype) { return dtype == HSTU_F32 ? 4 : dtype == HSTU_FP8_E4M3 ? 1 : 2; }
+int elem_bytes(int dtype) { return dtype == HSTU_F32 ? 4 : 2; }
+
+int cache_format(int dtype) {
+  return dtype == HSTU_FP8_E4M3   ? hstu::kE4m3
+         : dtype == HSTU_FP4_E2M1 ? hstu::kE2m1
+                                  : hstu::kSame;
+}
 
 // Sizes of a cache descriptor; pointers are checked by cache_pointers_ok.
 hstu_status check_cache(const hstu_kv_cache* c) {
   if (!c || c->reserved) return HSTU_ERR_INVALID_ARG;
-  if (c->dtype < HSTU_F32 || c->dtype > HSTU_FP8_E4M3) return HSTU_ERR_INVALID_ARG;
+  const bool fp8 = c->dtype == HSTU_FP8_E4M3, fp4 = c->dtype == HSTU_FP4_E2M1;
+  if (!fp4 && (c->dtype < HSTU_F32 || c->dtype > HSTU_FP8_E4M3)) return HSTU_ERR_INVALID_ARG;
   if (c->batch < 0 || c->batch > (1 << 20)) return HSTU_ERR_INVALID_ARG;
   if (c->num_heads_kv < 1 || c->num_heads_kv > 65536) return HSTU_ERR_INVALID_ARG;
   if (c->head_dim < 1) return HSTU_ERR_INVALID_ARG;
-  if (c->head_dim % 16 != 0 || c->head_dim > 256) return HSTU_ERR_UNSUPPORTED;
+  if (c->head_dim % (fp4 ? 32 : 16) != 0 || c->head_dim > 256) return HSTU_ERR_UNSUPPORTED;
   if (c->page_size != 32 && c->page_size != 128 && c->page_size != 256)
     return HSTU_ERR_INVALID_ARG;
   if (c->index_is_int64 != 0 && c->index_is_int64 != 1) return HSTU_ERR_INVALID_ARG;
   if (c->descale < HSTU_DESCALE_CAST || c->descale > HSTU_DESCALE_BLOCK)
     return HSTU_ERR_INVALID_ARG;
   if (c->descale == HSTU_DESCALE_BLOCK) return HSTU_ERR_UNSUPPORTED;
-  const bool fp8 = c->dtype == HSTU_FP8_E4M3;
-  if (!fp8 && (c->descale != HSTU_DESCALE_CAST || c->kv_scale)) return HSTU_ERR_INVALID_ARG;
+  if (!fp8 && (c->descale != HSTU_DESCALE_CAST || (c->kv_scale && !fp4)))
+    return HSTU_ERR_INVALID_ARG;
   if (c->descale != HSTU_DESCALE_CAST && c->kv_scale) return HSTU_ERR_INVALID_ARG;
   if (c->num_pages < 1 || c->num_pages > (1ll << 30) || c->num_page_ids < 0)
     return HSTU_ERR_INVALID_ARG;
@@ -45,6 +52,9 @@ bool cache_pointers_ok(const hstu_kv_cache* c) {
   if (!aligned(c->page_offsets, ib) || !aligned(c->last_page_len, ib) ||
       !aligned(c->page_ids, ib) || !aligned(c->status, 4) || !aligned(c->kv_scale, 16))
     return false;
+  if (c->dtype == HSTU_FP4_E2M1 &&
+      (!c->kv_scale || !c->kv_group_scale || !aligned(c->kv_group_scale, 16)))
+    return false;
   const bool factors = c->descale != HSTU_DESCALE_CAST;
   if (factors != (c->k_descale != nullptr) || factors != (c->v_descale != nullptr)) return false;
   return aligned(c->k_descale, 4) && aligned(c->v_descale, 4);
@@ -54,6 +64,8 @@ hstu::CacheView cache_view(const hstu_kv_cache* c, const void* seq_offsets, long
   hstu::CacheView v = {};
   v.cache = c->kv_cache;
   v.scale = static_cast<uint8_t*>(c->kv_scale);
+  // (a field that callers of the other forms may not have)
+  v.group = c->dtype == HSTU_FP4_E2M1 ? static_cast<uint8_t*>(c->kv_group_scale) : nullptr;
   v.page_offsets = c->page_offsets;
   v.page_ids = c->page_ids;
   v.last_page_len = c->last_page_len;
@@ -75,10 +87,10 @@ hstu::CacheView cache_view(const hstu_kv_cache* c, const void* seq_offsets, long
   return v;
 }
 
-// Row dtype against the cache's: the same, or any 32- or 16-bit type with an E4M3 cache.
+// Row dtype against the cache's: the same, or any 32- or 16-bit type with a cache of codes.
 bool row_dtype_ok(const hstu_kv_cache* c, int dtype) {
   if (dtype < HSTU_F32 || dtype > HSTU_BF16) return false;
-  return c->dtype == HSTU_FP8_E4M3 || c->dtype == dtype;
+  return cache_format(c->dtype) != hstu::kSame || c->dtype == dtype;
 }
 
 // Streaming multiprocessors of a device, asked for once.
@@ -109,7 +121,7 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   const hstu::CacheView v = cache_view(c, r->seq_offsets, r->total_tokens);
   return hstu::launch_kv_copy(v, r->k, r->v, r->k_stride, r->v_stride, r->dtype,
-                              c->dtype == HSTU_FP8_E4M3, append, sms,
+                              cache_format(c->dtype), append, sms,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? HSTU_OK
              : HSTU_ERR_CUDA;
@@ -146,7 +158,7 @@ void plan_tiles(const hstu_kv_cache* c, const hstu_softmax_args* a, long long mo
                 long long sms, const SetRows& set_rows, const long long& bm,
                 const long long& items, AttnPlan* pl) {
   const long long tile = 128 / G * G;
-  const bool fp8 = c->dtype == HSTU_FP8_E4M3, small = c->head_dim <= 128;
+  const bool codes = cache_format(c->dtype) != hstu::kSame, small = c->head_dim <= 128;
   // Two query tiles share the loads of K and V and keep the tensor pipe busier, if there are rows
   // for both (4096 tokens over 4096, 16 heads of 4: 660 us with two, 712 with one; 64 sequences of
   // some 200 rows over 2500 keys: 141 and 126)
@@ -161,7 +173,7 @@ void plan_tiles(const hstu_kv_cache* c, const hstu_softmax_args* a, long long mo
     pl->workspace = pl->parts_bytes + pl->blocks * (long long)sizeof(hstu::JoinRecord);
     return;
   }
-  if (small && !fp8 && (pl->qtiles == 1 || a->max_seqlen_k <= 4096)) {
+  if (small && !codes && (pl->qtiles == 1 || a->max_seqlen_k <= 4096)) {
     // A CTA for each item, two on an SM if there are as many: with short keys what hides an item's
     // first and last steps is another item (24 sequences of some 500 rows over 900 keys, D = 64:
     // 49 us with two query tiles, 46 with two CTAs; 32 of 400 over 1400 120 and 109; with longer
@@ -231,7 +243,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     // of 100k bf16 keys: 74.5 us with one wave, 83.8 with two, 101 with four; 400 items of up to
     // 500 E4M3 keys on 456 places: 13.7 us alone, 20.2 in pairs)
     const long long slots =
-        (long long)hstu::softmax_rows_ctas(c->head_dim, c->dtype == HSTU_FP8_E4M3, pl->rows) * sms;
+        (long long)hstu::softmax_rows_ctas(c->head_dim, cache_format(c->dtype), pl->rows) * sms;
     const long long can = (a->max_seqlen_k + 127) / 128;  // two tiles of 64 keys each
     long long want = slots / items < can ? slots / items : can;
     if (want < 1) want = 1;
@@ -311,14 +323,14 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   p.joins =
       reinterpret_cast<hstu::JoinRecord*>(static_cast<char*>(a->workspace) + pl.parts_bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool fp8 = c->dtype == HSTU_FP8_E4M3;
+  const int fmt = cache_format(c->dtype);
   cudaError_t e =
       pl.kernel == AttnPlan::ROWS
-          ? hstu::launch_softmax_rows(p, a->dtype, fp8, pl.rows, pl.tiles, pl.blocks,
+          ? hstu::launch_softmax_rows(p, a->dtype, fmt, pl.rows, pl.tiles, pl.blocks,
                                       pl.cluster, s)
       : pl.kernel == AttnPlan::TC
-          ? hstu::launch_softmax_tc(p, a->dtype, fp8, pl.qtiles, pl.ctas, pl.tiles, pl.blocks, s)
-          : hstu::launch_softmax_simt(p, fp8, pl.rows, pl.tiles, pl.blocks, s);
+          ? hstu::launch_softmax_tc(p, a->dtype, fmt, pl.qtiles, pl.ctas, pl.tiles, pl.blocks, s)
+          : hstu::launch_softmax_simt(p, fmt, pl.rows, pl.tiles, pl.blocks, s);
   if (e == cudaSuccess && (pl.splits > 1 || pl.balanced))
     e = hstu::launch_softmax_join(p, a->dtype, 128 / p.G, pl.qtiles, (int)pl.blocks, s);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;

@@ -1,5 +1,5 @@
 // Paged KV cache as the cache operators' kernels see it: the page table, a sequence's
-// geometry with the checks of it, and conversions of E4M3 elements.
+// geometry with the checks of it, and conversions of E4M3 and E2M1 elements.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -11,10 +11,14 @@
 
 namespace hstu {
 
+// What the cache holds: elements of the rows' type, E4M3 codes, or E2M1 codes.
+enum : int { kSame = 0, kE4m3 = 1, kE2m1 = 2 };
+
 // Device view of hstu_kv_cache (see include/hstu_kv.h).
 struct CacheView {
-  void* cache;              // [num_pages, 2, page_size, Nk, D]
+  void* cache;              // [num_pages, 2, page_size, Nk, D]; E2M1 [num_pages, 2, Nk, page_size, D / 2]
   uint8_t* scale;           // [num_pages, 2, Nk, page_size] or nullptr
+  uint8_t* group;           // E2M1: E4M3 factors [num_pages, 2, Nk, page_size, D / 16]
   const void* page_offsets;
   const void* page_ids;
   const void* last_page_len;
@@ -63,7 +67,8 @@ __device__ __forceinline__ long long page_at(const CacheView& c, const PagedSeq&
   return id >= 0 && id < c.num_pages ? id : -1;
 }
 
-// First element of (page, plane, row of the page, kv head) in the cache.
+// First element of (page, plane, row of the page, kv head) in the cache. (An E2M1 cache has its
+// heads before the rows, as the scales do: row scale_row of D / 2 bytes and of D / 16 factors.)
 __device__ __forceinline__ long long cache_row(const CacheView& c, long long page, int plane,
                                                long long row, int hk) {
   return ((((page * 2 + plane) << c.page_shift) + row) * c.Nk + hk) * c.D;
@@ -104,6 +109,49 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t x, uint32_t& lo, uint32
       "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
+}
+
+// Eight E2M1 codes (element i in bits 4 i ..) as four pairs of fp16 values (exact).
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t x, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(x));
+}
+
+// Eight fp32 values rounded to E2M1 (nearest, ties to even, 6 at most), packed likewise.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float* x) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// An E4M3 code's value.
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const uint32_t h = e4m3x2_to_f16x2(code & 0xffu);
+  return __low2float(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Sixteen E2M1 elements as codes' values (without their factor).
+__device__ __forceinline__ void load16_e2m1(const uint8_t* p, float (&x)[16]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    uint32_t h[4];
+    e2m1x8_to_f16x2(w ? u.y : u.x, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      x[8 * w + 2 * i] = f.x;
+      x[8 * w + 2 * i + 1] = f.y;
+    }
+  }
 }
 
 // Sixteen consecutive elements as fp32 values (exact).

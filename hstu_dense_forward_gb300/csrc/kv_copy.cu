@@ -10,6 +10,10 @@
 // and the scale is a power of two, so that scaling is exact and the rounding to E4M3 is the
 // only one (an arbitrary factor would add one, and E4M3 is a floating-point format: it gains
 // nothing by it).
+// E2M1 has one bit behind the leading one and six powers of two less, so there each group of
+// sixteen elements, which is what a lane holds, has a factor besides, rounded to E4M3. Codes are
+// roundings of exact quotients: a quotient in fp32 falls on the middle of two codes only if the
+// exact one does, since element, factor (4 bits) and middle (3 bits) all are fp32 values.
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "kv_kernels.h"
@@ -31,7 +35,7 @@ struct CopyParams {
   int row_shift;                 // log2(rows of a block)
 };
 
-enum : int { kCopy = 0, kCast = 1, kStatic = 2, kScale = 3 };
+enum : int { kCopy = 0, kCast = 1, kStatic = 2, kScale = 3, kGroup = 4 };
 
 constexpr int kMaxRows = 32;  // rows of a block
 
@@ -80,6 +84,31 @@ __device__ __forceinline__ float factor(const CacheView& c, const float* f, int 
 __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   return e < kMinExp ? kMinExp : e;
+}
+
+// The same for E2M1 rows: 2688 = 1.3125 * 2^11 (448 times 6).
+__device__ __forceinline__ int group_exponent(uint32_t bits) {
+  const int e = (int)(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u ? 1 : 0);
+  return e < kMinExp ? kMinExp : e;
+}
+
+// Sixteen elements times 2^-e as E2M1 codes and their factor's E4M3 code. A NaN makes the factor one.
+__device__ __forceinline__ uint2 group_codes(const float (&x)[16], int e, uint32_t& factor) {
+  const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
+  float y[16], top = 0.0f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    nan |= x[i] != x[i];
+    y[i] = fminf(fmaxf(x[i] * mul, -2688.0f), 2688.0f);  // (infinities)
+    top = fmaxf(top, fabsf(y[i]));
+  }
+  factor = ptx::cvt_e4m3x2_f32(top / 6.0f, 0.0f) & 0xffu;
+  const float f = e4m3_value(factor);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = factor ? __fdiv_rn(y[i], f) : 0.0f;
+  if (nan) factor = 0x7fu;
+  return make_uint2(f32x8_to_e2m1(y), f32x8_to_e2m1(y + 8));
 }
 
 __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[16], float mul) {
@@ -151,8 +180,19 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const CopyParams p)
 #pragma unroll
     for (int plane = 0; plane < 2; ++plane) {
       uint32_t top = 0;
-      if constexpr (MODE == kScale) top = row_max(x[plane], ok, 1 << p.lane_shift);
+      if constexpr (MODE == kScale || MODE == kGroup)
+        top = row_max(x[plane], ok, 1 << p.lane_shift);
       if (!ok) continue;
+      if constexpr (MODE == kGroup) {
+        const int e = group_exponent(top);
+        const long long r = scale_row(p.c, w.page, plane, w.row, u.hk);
+        uint32_t factor;
+        const uint2 codes = group_codes(x[plane], e, factor);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.c.cache) + (r * p.c.D + d0) / 2) = codes;
+        p.c.group[(r * p.c.D + d0) / 16] = (uint8_t)factor;
+        if (d0 == 0) p.c.scale[r] = (uint8_t)(e + 127);
+        continue;
+      }
       const long long at = cache_row(p.c, w.page, plane, w.row, u.hk) + d0;
       if constexpr (MODE == kCopy) {
         store16(static_cast<T*>(p.c.cache) + at, x[plane]);
@@ -191,6 +231,12 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CopyParams p) {
     float x[2][16], f[2] = {1.0f, 1.0f};
 #pragma unroll
     for (int plane = 0; plane < 2; ++plane) {
+      if constexpr (MODE == kGroup) {
+        const long long r = scale_row(p.c, w.page, plane, w.row, u.hk);
+        f[plane] = scale_value(p.c.scale[r]) * e4m3_value(p.c.group[(r * p.c.D + d0) / 16]);
+        load16_e2m1(static_cast<const uint8_t*>(p.c.cache) + (r * p.c.D + d0) / 2, x[plane]);
+        continue;
+      }
       const long long at = cache_row(p.c, w.page, plane, w.row, u.hk) + d0;
       if constexpr (MODE == kScale)
         f[plane] = scale_value(p.c.scale[scale_row(p.c, w.page, plane, w.row, u.hk)]);
@@ -203,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const CopyParams p) {
     }
 #pragma unroll
     for (int plane = 0; plane < 2; ++plane) {
-      if constexpr (MODE == kScale || MODE == kStatic) {
+      if constexpr (MODE == kScale || MODE == kStatic || MODE == kGroup) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[plane][e] *= f[plane];
       }
@@ -226,6 +272,7 @@ cudaError_t launch(const CopyParams& p, bool append, int mode, unsigned grid, cu
     case kCopy: HSTU_COPY(kCopy);
     case kCast: HSTU_COPY(kCast);
     case kStatic: HSTU_COPY(kStatic);
+    case kGroup: HSTU_COPY(kGroup);
     default: HSTU_COPY(kScale);
   }
 #undef HSTU_COPY
@@ -235,7 +282,7 @@ cudaError_t launch(const CopyParams& p, bool append, int mode, unsigned grid, cu
 }  // namespace
 
 cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_stride,
-                           long long v_stride, int dtype, bool e4m3, bool append, int sms,
+                           long long v_stride, int dtype, int fmt, bool append, int sms,
                            cudaStream_t stream) {
   CopyParams p = {};
   p.c = c;
@@ -251,7 +298,11 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
     ++p.row_shift;
   const long long blocks = (c.T + (1 << p.row_shift) - 1) >> p.row_shift;
   const unsigned grid = (unsigned)blocks;
-  const int mode = !e4m3 ? kCopy : c.scale ? kScale : c.k_ds ? kStatic : kCast;
+  const int mode = fmt == kSame    ? kCopy
+                   : fmt == kE2m1 ? kGroup
+                   : c.scale      ? kScale
+                   : c.k_ds       ? kStatic
+                                  : kCast;
   if (dtype == HSTU_F32) return launch<float>(p, append, mode, grid, stream);
   if (dtype == HSTU_BF16) return launch<__nv_bfloat16>(p, append, mode, grid, stream);
   return launch<__half>(p, append, mode, grid, stream);

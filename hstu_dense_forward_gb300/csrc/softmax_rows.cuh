@@ -15,6 +15,10 @@
 // lane reads whole 16-byte pieces of a key's row for the scores, and the same piece of four
 // keys for the output, which byte permutes turn into pairs of keys.
 //
+// E2M1 caches: a lane's sixteen consecutive elements of a key are a group, whose factor multiplies
+// them in fp16; factor times code has seven bits, 2^-10 .. 2688, and is exact. What follows holds for
+// them as for E4M3 codes.
+//
 // E4M3 caches: codes become fp16 by one conversion (exact) and the products run in fp16. A
 // row scale 2^e of K multiplies the score. One of V would leave fp16's range if it multiplied a
 // weight, so it enters the exponent instead, relative to a reference of its own: with m = max x
@@ -50,29 +54,34 @@ constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNoKey = -1e38f;  // E4M3: reference of a row that has seen no key
 
-template <int D_, int NT_, bool BF16_, bool E4M3_>
+template <int D_, int NT_, bool BF16_, int FMT_>
 struct Cfg {
   static constexpr int D = D_, NT = NT_, RT = 8 * NT;      // packed query rows of one CTA
-  static constexpr bool BF16 = BF16_, E4M3 = E4M3_;
-  static constexpr bool MMA_BF16 = BF16 && !E4M3;
-  static constexpr int EB = E4M3 ? 1 : 2;
-  static constexpr int SWB = D * EB < 128 ? D * EB : 128;  // bytes of one swizzled row block
-  static constexpr int NCB = D * EB / SWB;                 // blocks of a key's row
-  static constexpr int BE = SWB / EB;                      // elements of a block
+  static constexpr int FMT = FMT_;
+  static constexpr bool BF16 = BF16_, CODES = FMT != kSame, FP4 = FMT == kE2m1;
+  static constexpr bool MMA_BF16 = BF16 && !CODES;
+  static constexpr int RB = FP4 ? D / 2 : CODES ? D : 2 * D;  // bytes of a key's row
+  static constexpr int SWB = RB < 128 ? RB : 128;          // bytes of one swizzled row block
+  static constexpr int NCB = RB / SWB;                     // blocks of a key's row
+  static constexpr int BE = D / NCB;                       // elements of a block
   static constexpr int CB = KT * SWB;                      // one block of a tile
-  static constexpr int EPP = 16 / EB;                      // elements of a 16-byte piece
+  static constexpr int EPP = 16 * D / RB;                  // elements of a 16-byte piece
   static constexpr int LPC = SWB / 64;                     // pieces per lane and block (scores)
+  static constexpr int LE = BE / 4;                        // elements per lane and block (scores)
   static constexpr int KS = D / 16;                        // k-steps of the scores
   static constexpr int NV = BE / 8;                        // output columns per lane and block
   static constexpr int CW = KT / 16, THREADS = (CW + 1) * 32;
-  static constexpr int PLANE = KT * D * EB, STAGE = 2 * PLANE;
+  static constexpr int PLANE = KT * RB, STAGE = 2 * PLANE;
   // CTAs per SM: what their registers (O and Q) and a ring of at least three stages leave. E4M3
   // spends more instructions per byte and needs the warps of a third CTA.
-  static constexpr int CTAS = D == 256 ? (E4M3 && NT == 1 ? 2 : 1) : (E4M3 && NT == 1 ? 3 : 2);
-  static constexpr int NST = (CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : 65536) / STAGE;
+  static constexpr int CTAS = D == 256 ? (CODES && NT == 1 ? 2 : 1) : (CODES && NT == 1 ? 3 : 2);
+  static constexpr int RING = CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : FP4 ? 57344 : 65536;
+  static constexpr int NST = RING / STAGE < 12 ? RING / STAGE : 12;
   static constexpr int OFF_SC = NST * STAGE;               // row scales: 2 KT bytes a stage
-  static constexpr int OFF_ML = OFF_SC + (E4M3 ? NST * 2 * KT : 0);
-  static constexpr int OFF_BAR = OFF_ML + (E4M3 ? 3 : 2) * (CW + 1) * RT * 4;
+  static constexpr int GPLANE = KT * (D / 16);             // E2M1: factors of a plane's tile
+  static constexpr int OFF_GR = OFF_SC + (CODES ? NST * 2 * KT : 0);
+  static constexpr int OFF_ML = OFF_GR + (FP4 ? NST * 2 * GPLANE : 0);
+  static constexpr int OFF_BAR = OFF_ML + (CODES ? 3 : 2) * (CW + 1) * RT * 4;
   static constexpr int USED = OFF_BAR + 256 + 1024;
   static_assert(NST >= 3 && NST <= 12, "ring");
   static_assert(CW * RT * D * 4 <= NST * STAGE, "the joined outputs reuse the ring");
@@ -136,6 +145,16 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Two factors of E2M1 groups as fp16.
+__device__ __forceinline__ uint32_t group_pair(uint32_t lo, uint32_t hi) {
+  return e4m3x2_to_f16x2(lo | hi << 8);
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit elements, two of a row per lane.
@@ -210,8 +229,9 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
     const int st = t % C::NST;
     if (!wait_bar(p, bars, &bars->empty[st], ((t / C::NST) & 1) ^ 1)) return;
     const uint32_t bar = ptx::smem_u32(&bars->full[st]);
-    const bool scales = C::E4M3 && p.c.scale;
-    ptx::mbar_arrive_expect_tx(bar, C::STAGE + (scales ? 2 * KT : 0));
+    const bool scales = C::CODES && p.c.scale;
+    const int gb = p.c.D / 16;  // E2M1: factors of a row
+    ptx::mbar_arrive_expect_tx(bar, C::STAGE + (scales ? 2 * KT : 0) + (C::FP4 ? 2 * KT * gb : 0));
     const int row0 = ps >= KT ? (int)(n0 & (ps - 1)) : 0;
 #pragma unroll
     for (int m = 0; m < KT / 32; ++m) {
@@ -219,10 +239,18 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
 #pragma unroll
       for (int plane = 0; plane < 2; ++plane) {
 #pragma unroll
-        for (int cb = 0; cb < C::NCB; ++cb)
-          ptx::tma_load_4d(sbase + st * C::STAGE + plane * C::PLANE + cb * C::CB + m * 32 * C::SWB,
-                           tc, bar, cb * (C::SWB / C::EB), it.hk, row0,
-                           (int)(2 * page[m]) + plane);
+        for (int cb = 0; cb < C::NCB; ++cb) {
+          const uint32_t dst =
+              sbase + st * C::STAGE + plane * C::PLANE + cb * C::CB + m * 32 * C::SWB;
+          if constexpr (C::FP4)
+            ptx::tma_load_4d(dst, tc, bar, 0, row0, it.hk, (int)(2 * page[m]) + plane);
+          else
+            ptx::tma_load_4d(dst, tc, bar, cb * C::BE, it.hk, row0, (int)(2 * page[m]) + plane);
+        }
+        if constexpr (C::FP4)
+          ptx::bulk_load(sbase + C::OFF_GR + (2 * st + plane) * C::GPLANE + m * 32 * gb,
+                         p.c.group + scale_row(p.c, page[m], plane, row0, it.hk) * gb, brows * gb,
+                         bar);
         if (scales)
           ptx::bulk_load(sbase + C::OFF_SC + st * 2 * KT + plane * KT + m * 32,
                          p.c.scale + scale_row(p.c, page[m], plane, row0, it.hk), brows, bar);
@@ -238,12 +266,13 @@ __device__ __forceinline__ float part_weight(float m, float top) {
   return m == -CUDART_INF_F ? 0.0f : ex2(m - top);
 }
 
-template <int D, int NT, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF16, E4M3>::CTAS)
+template <int D, int NT, bool BF16, int FMT>
+__global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF16, FMT>::CTAS)
     softmax_rows_kernel(const __grid_constant__ CUtensorMap tm_c, const SoftmaxParams p, int tiles,
                         int cluster) {
-  using C = Cfg<D, NT, BF16, E4M3>;
+  using C = Cfg<D, NT, BF16, FMT>;
   using T16 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  constexpr bool CODES = C::CODES;
   namespace cg = cooperative_groups;
   constexpr int RT = C::RT;
   extern __shared__ uint8_t smem_raw[];
@@ -273,7 +302,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
   float dv[NT][2];  // E4M3: O's unit is 2^(m + dv)
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    m[i][0] = m[i][1] = E4M3 ? kNoKey : -CUDART_INF_F;
+    m[i][0] = m[i][1] = CODES ? kNoKey : -CUDART_INF_F;
     l[i][0] = l[i][1] = dv[i][0] = dv[i][1] = 0.f;
 #pragma unroll
     for (int x = 0; x < C::KS; ++x) o[i][x][0] = o[i][x][1] = o[i][x][2] = o[i][x][3] = 0.f;
@@ -282,7 +311,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
     if (lane == 0) load_role<C>(p, bars, smem, it, n, &tm_c);
   } else {
     float fk = p.scale_log2;
-    if (E4M3 && p.c.k_ds)
+    if (CODES && p.c.k_ds)
       fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
     const int keys = (int)(it.kend - it.k0);
     // Q fragments in the scores' order of the head dim: of piece j of block cb, lane c's
@@ -302,27 +331,24 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
 #pragma unroll
       for (int cb = 0; cb < C::NCB; ++cb)
 #pragma unroll
-        for (int j = 0; j < C::LPC; ++j) {
-          const int e0 = cb * C::BE + (c * C::LPC + j) * C::EPP;
+        for (int x = 0; x < C::LE / 8; ++x) {
+          const int e0 = cb * C::BE + c * C::LE + 8 * x;
+          uint4 u = make_uint4(0u, 0u, 0u, 0u);
+          if (real && e0 < p.c.D) u = *reinterpret_cast<const uint4*>(q + e0);
+          const int k = (cb * C::LE + 8 * x) / 4;
+          qb[i][k][0] = u.x;
+          qb[i][k][1] = u.y;
+          qb[i][k + 1][0] = u.z;
+          qb[i][k + 1][1] = u.w;
+          if constexpr (CODES && BF16) {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int x = 0; x < C::EPP / 8; ++x) {
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (real && e0 + 8 * x < p.c.D) u = *reinterpret_cast<const uint4*>(q + e0 + 8 * x);
-            const int k = ((cb * C::LPC + j) * C::EPP + 8 * x) / 4;
-            qb[i][k][0] = u.x;
-            qb[i][k][1] = u.y;
-            qb[i][k + 1][0] = u.z;
-            qb[i][k + 1][1] = u.w;
-            if constexpr (E4M3 && BF16) {
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-            }
+            for (int e = 0; e < 4; ++e)
+              top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
           }
         }
       float f = fk;
-      if constexpr (E4M3 && BF16) {  // the row as fp16, times 2^(14 - exponent of its largest)
+      if constexpr (CODES && BF16) {  // the row as fp16, times 2^(14 - exponent of its largest)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int sh = min(14 - ((int)(top >> 7) - 127), 126);
@@ -364,8 +390,57 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[i][e] = sd[i][e] = 0.f;
+        if constexpr (C::FP4) {
+          const int gb = p.c.D / 16, r0 = warp * 16 + g;
+          const uint8_t* gp = smem + C::OFF_GR + 2 * st * C::GPLANE + r0 * gb;
+          constexpr int LU = C::LE / 16;  // groups of sixteen elements that the lane holds
+          uint32_t w[2][2 * LU];
 #pragma unroll
-        for (int cb = 0; cb < C::NCB; ++cb)
+          for (int y = 0; y < 2; ++y) {
+            if constexpr (LU == 1) {
+              const uint2 u = *reinterpret_cast<const uint2*>(kt + (r0 + 8 * y) * C::SWB + c * 8);
+              w[y][0] = u.x;
+              w[y][1] = u.y;
+            } else {
+#pragma unroll
+              for (int j = 0; j < LU / 2; ++j) {
+                const uint4 u = *reinterpret_cast<const uint4*>(
+                    kt + piece_at<C::SWB>(r0 + 8 * y, c * (LU / 2) + j));
+                w[y][4 * j] = u.x;
+                w[y][4 * j + 1] = u.y;
+                w[y][4 * j + 2] = u.z;
+                w[y][4 * j + 3] = u.w;
+              }
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < LU; ++u) {
+            uint32_t f[2] = {0u, 0u};  // (behind the head dim another row's, or nothing)
+            if (c * LU + u < gb) {
+              f[0] = group_pair(gp[c * LU + u], gp[c * LU + u]);
+              f[1] = group_pair(gp[8 * gb + c * LU + u], gp[8 * gb + c * LU + u]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t h[2][4];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                e2m1x8_to_f16x2(w[y][2 * u + x], h[y]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[y][e] = mul_f16x2(h[y][e], f[y]);
+              }
+              const int k = 4 * u + 2 * x;
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                mma<false>(sc[i], h[0][0], h[1][0], h[0][1], h[1][1], qb[i][k][0], qb[i][k][1]);
+                mma<false>(sd[i], h[0][2], h[1][2], h[0][3], h[1][3], qb[i][k + 1][0],
+                           qb[i][k + 1][1]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int cb = 0; cb < (C::FP4 ? 0 : C::NCB); ++cb)
 #pragma unroll
           for (int j = 0; j < C::LPC; ++j) {
             const uint4 u0 = *reinterpret_cast<const uint4*>(
@@ -374,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
                 kt + cb * C::CB + piece_at<C::SWB>(warp * 16 + 8 + g, c * C::LPC + j));
             const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
             const int k = (cb * C::LPC + j) * C::EPP / 4;
-            if constexpr (E4M3) {
+            if constexpr (CODES) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t a0, a1, a2, a3;
@@ -396,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
           }
         // scores in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y
         float ev[2] = {0.f, 0.f};  // exponents of V's row scales (of a key beyond the last, any)
-        if (E4M3 && p.c.scale) {
+        if (CODES && p.c.scale) {
           const uint8_t* sp = smem + C::OFF_SC + st * 2 * KT + warp * 16 + g;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -443,12 +518,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
               ptx::add_f32x2(xw[i][2 * x], xw[i][2 * x + 1], xs[i][2 * x], xs[i][2 * x + 1]);
             }
         };
-        if constexpr (E4M3) relative();
+        if constexpr (CODES) relative();
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            over |= E4M3 ? fmaxf(xs[i][e], xw[i][e]) > kLazy : sc[i][e] > m[i][e & 1] + kLazy;
+            over |= CODES ? fmaxf(xs[i][e], xw[i][e]) > kLazy : sc[i][e] > m[i][e & 1] + kLazy;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
@@ -459,10 +534,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               const bool up = mx > m[i][y] + kLazy;
-              const float to = E4M3 ? ceilf(mx) : mx;
+              const float to = CODES ? ceilf(mx) : mx;
               corr[y] = up ? ex2(m[i][y] - to) : 1.0f;  // (0 at the first visible key)
               l[i][y] *= corr[y];
-              if constexpr (E4M3) {
+              if constexpr (CODES) {
                 if (up) dv[i][y] += m[i][y] - to;
                 if (up) m[i][y] = to;
                 float u = fmaxf((sc[i][y] - m[i][y]) + ev[0], (sc[i][2 + y] - m[i][y]) + ev[1]);
@@ -480,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[i][x][e] *= corr[e & 1];
           }
-          if constexpr (E4M3) relative();
+          if constexpr (CODES) relative();
         }
         // P^T fragments: keys 2c, 2c + 1 (and + 8) of row g. bf16 weights come with what their
         // rounding leaves, for a product of its own: rounded to 2^-8 alone they are as far off as
@@ -495,11 +570,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
           const float b1 = m[i][1] == -CUDART_INF_F ? 0.0f : m[i][1];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float p0 = ex2(E4M3 ? xs[i][2 * x] : sc[i][2 * x] - b0);
-            float p1 = ex2(E4M3 ? xs[i][2 * x + 1] : sc[i][2 * x + 1] - b1);
+            float p0 = ex2(CODES ? xs[i][2 * x] : sc[i][2 * x] - b0);
+            float p1 = ex2(CODES ? xs[i][2 * x + 1] : sc[i][2 * x + 1] - b1);
             l[i][0] += p0;
             l[i][1] += p1;
-            if constexpr (E4M3) {
+            if constexpr (CODES) {
               p0 = ex2(xw[i][2 * x]);
               p1 = ex2(xw[i][2 * x + 1]);
             }
@@ -511,10 +586,64 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
           }
         }
         const uint8_t* vt = kt + C::PLANE;
+        if constexpr (C::FP4) {
+          constexpr int NW = C::NV / 8;  // words of the lane's columns of a key
+          const int gb = p.c.D / 16;
+          const uint8_t* gp = smem + C::OFF_GR + (2 * st + 1) * C::GPLANE + warp * 16 * gb;
+          uint32_t v[4][NW];  // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-        for (int cb = 0; cb < C::NCB; ++cb) {
+          for (int y = 0; y < 4; ++y) {
+            const int key = 2 * c + (y & 1) + 8 * (y >> 1), r = warp * 16 + key;
+            if constexpr (NW == 1) {
+              v[y][0] = *reinterpret_cast<const uint32_t*>(vt + r * C::SWB + g * 4);
+            } else if constexpr (NW == 2) {
+              const uint2 u = *reinterpret_cast<const uint2*>(vt + piece_at<C::SWB>(r, g >> 1) +
+                                                              (g & 1) * 8);
+              v[y][0] = u.x;
+              v[y][1] = u.y;
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(vt + piece_at<C::SWB>(r, g));
+              v[y][0] = u.x;
+              v[y][1] = u.y;
+              v[y][2] = u.z;
+              v[y][3] = u.w;
+            }
+          }
+          constexpr int GW = NW > 2 ? 2 : 1;  // groups of the lane's columns
+#pragma unroll
+          for (int u = 0; u < GW; ++u) {
+            const int gr = g * C::NV / 16 + u;
+            uint32_t b[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // (beyond the keys: a page's unused rows, maybe NaN)
+              const int key = 2 * c + (y & 1) + 8 * (y >> 1);
+              b[y] = gr < gb && key < left ? gp[key * gb + gr] : 0u;
+            }
+            const uint32_t f01 = group_pair(b[0], b[1]), f23 = group_pair(b[2], b[3]);
+#pragma unroll
+            for (int w = u * (NW / GW); w < (u + 1) * (NW / GW); ++w) {
+              // byte t of e (o): the codes of both keys in column 2 t (2 t + 1) of the word's eight
+              constexpr uint32_t M = 0x0f0f0f0fu;
+              uint32_t e0[4], o0[4], e1[4], o1[4];
+              e2m1x8_to_f16x2((v[0][w] & M) | ((v[1][w] << 4) & ~M), e0);
+              e2m1x8_to_f16x2(((v[0][w] >> 4) & M) | (v[1][w] & ~M), o0);
+              e2m1x8_to_f16x2((v[2][w] & M) | ((v[3][w] << 4) & ~M), e1);
+              e2m1x8_to_f16x2(((v[2][w] >> 4) & M) | (v[3][w] & ~M), o1);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const uint32_t a0 = mul_f16x2(e0[t], f01), a1 = mul_f16x2(o0[t], f01);
+                const uint32_t a2 = mul_f16x2(e1[t], f23), a3 = mul_f16x2(o1[t], f23);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                  mma<false>(o[i][4 * w + t], a0, a1, a2, a3, pb[0][i][0], pb[0][i][1]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int cb = 0; cb < (C::FP4 ? 0 : C::NCB); ++cb) {
           const uint8_t* blk = vt + cb * C::CB;
-          constexpr int NW = C::NV * C::EB / 4;  // words of a lane's piece: 4, or 2 (64 codes a row)
+          constexpr int NW = C::FP4 ? 2 : C::NV * (C::CODES ? 1 : 2) / 4;  // words of a lane's piece: 4, or 2 (64 codes a row)
           uint32_t v[4][NW];                     // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -542,7 +671,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
           }
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
-            if constexpr (E4M3) {
+            if constexpr (CODES) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 uint32_t a0, a1, a2, a3;
@@ -591,7 +720,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
         if (g == 0) {
           wm[warp * RT + 8 * i + 2 * c + y] = m[i][y];
           wl[warp * RT + 8 * i + 2 * c + y] = l[i][y];
-          if constexpr (E4M3) wd[warp * RT + 8 * i + 2 * c + y] = dv[i][y];
+          if constexpr (CODES) wd[warp * RT + 8 * i + 2 * c + y] = dv[i][y];
         }
       }
   }
@@ -614,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
 #pragma unroll
         for (int w = 0; w < C::CW; ++w) top = fmaxf(top, wm[w * RT + r]);
         float f;
-        if constexpr (E4M3) {
+        if constexpr (CODES) {
           float unit = -CUDART_INF_F;
 #pragma unroll
           for (int w = 0; w < C::CW; ++w)
@@ -642,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
     for (int w = 0; w < C::CW; ++w) sum = fmaf(part_weight(wm[w * RT + r], top), wl[w * RT + r], sum);
     cm[r] = top;
     cl[r] = sum;
-    if constexpr (E4M3) {
+    if constexpr (CODES) {
       float unit = -CUDART_INF_F;
       for (int w = 0; w < C::CW; ++w)
         unit = fmaxf(unit, part_unit(wm[w * RT + r], wd[w * RT + r], top));
@@ -669,18 +798,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
   }
   const int rank = blockIdx.x % cluster;
   const int parts = cluster > 1 ? cluster : C::CW;
-  const float fv = E4M3 && p.c.v_ds
+  const float fv = CODES && p.c.v_ds
                        ? p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h]
                        : 1.0f;
   for (int x = rank * C::THREADS + threadIdx.x; x < nrows * pieces; x += cluster * C::THREADS) {
     const int r = x / pieces, d = x % pieces * 4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float top = cm[r], sum = cl[r], unit = E4M3 ? cd[r] : 0.f;
+    float top = cm[r], sum = cl[r], unit = CODES ? cd[r] : 0.f;
     if (cluster > 1) {
       top = -CUDART_INF_F;
       sum = 0.f;
       for (int w = 0; w < parts; ++w) top = fmaxf(top, cg::this_cluster().map_shared_rank(cm, w)[r]);
-      if constexpr (E4M3) {
+      if constexpr (CODES) {
         unit = -CUDART_INF_F;
         for (int w = 0; w < parts; ++w)
           unit = fmaxf(unit, part_unit(cg::this_cluster().map_shared_rank(cm, w)[r],
@@ -694,7 +823,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
         const float mw = cg::this_cluster().map_shared_rank(cm, w)[r];
         f = part_weight(mw, top);
         sum = fmaf(f, cg::this_cluster().map_shared_rank(cl, w)[r], sum);
-        if constexpr (E4M3)
+        if constexpr (CODES)
           f = part_weight(part_unit(mw, cg::this_cluster().map_shared_rank(cd, w)[r], top), unit);
         src = cg::this_cluster().map_shared_rank(part, w) + r * D + d;
       }
@@ -704,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
     const long long pr = it.m0 + r;
     const long long row = (it.s.t0 + pr / p.G) * p.Nq + it.hk * p.G + pr % p.G;  // of out and lse
     float inv = sum == 0.0f ? 0.0f : fv / sum;
-    if constexpr (E4M3) {  // 2^unit in two factors: it may pass fp32's range
+    if constexpr (CODES) {  // 2^unit in two factors: it may pass fp32's range
       const float half = truncf(unit * 0.5f), rest = ex2(unit - half);
       inv *= ex2(half);
       a = make_float4(a.x * rest, a.y * rest, a.z * rest, a.w * rest);
@@ -728,11 +857,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, E4M3>::THREADS, Cfg<D, NT, BF
   if (cluster > 1) cg::this_cluster().sync();  // the others have read this CTA's shared memory
 }
 
-template <int D, int NT, bool BF16, bool E4M3>
+template <int D, int NT, bool BF16, int FMT>
 cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
                            long long blocks, int cluster, cudaStream_t stream) {
-  using C = Cfg<D, NT, BF16, E4M3>;
-  auto* kernel = softmax_rows_kernel<D, NT, BF16, E4M3>;
+  using C = Cfg<D, NT, BF16, FMT>;
+  auto* kernel = softmax_rows_kernel<D, NT, BF16, FMT>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::USED, done);
   if (e != cudaSuccess) return e;
@@ -749,20 +878,20 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tc, long l
   return cudaLaunchKernelEx(&cfg, kernel, tc, p, (int)tiles, cluster);
 }
 
-template <bool BF16, bool E4M3, int NT>
+template <bool BF16, int FMT, int NT>
 cudaError_t launch_dim(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
                        long long blocks, int cluster, cudaStream_t s) {
-  if (p.c.D > 128) return launch_variant<256, NT, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
-  if (p.c.D > 64) return launch_variant<128, NT, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
-  return launch_variant<64, NT, BF16, E4M3>(p, tc, tiles, blocks, cluster, s);
+  if (p.c.D > 128) return launch_variant<256, NT, BF16, FMT>(p, tc, tiles, blocks, cluster, s);
+  if (p.c.D > 64) return launch_variant<128, NT, BF16, FMT>(p, tc, tiles, blocks, cluster, s);
+  return launch_variant<64, NT, BF16, FMT>(p, tc, tiles, blocks, cluster, s);
 }
 
 // rows: packed query rows of one item, 8 or 16.
-template <bool BF16, bool E4M3>
+template <bool BF16, int FMT>
 cudaError_t launch_rows(const SoftmaxParams& p, const CUtensorMap& tc, int rows, long long tiles,
                         long long blocks, int cluster, cudaStream_t s) {
-  return rows == 8 ? launch_dim<BF16, E4M3, 1>(p, tc, tiles, blocks, cluster, s)
-                   : launch_dim<BF16, E4M3, 2>(p, tc, tiles, blocks, cluster, s);
+  return rows == 8 ? launch_dim<BF16, FMT, 1>(p, tc, tiles, blocks, cluster, s)
+                   : launch_dim<BF16, FMT, 2>(p, tc, tiles, blocks, cluster, s);
 }
 
 }  // namespace rows

@@ -38,14 +38,14 @@ struct RowAt {
   long long scale;
 };
 
-template <int D_, bool E4M3>
+template <int D_, int FMT>
 struct Cfg {
   static constexpr int D = D_, BM = 64;
   // Keys of a step: 64 spend more FMAs per load of the scores' operands, 32 leave an SM a second
   // CTA at D = 128, which E4M3 rows, whose conversion waits, need more (773 tokens over 2275, 20
   // heads, with the slower loads of sixteen elements a thread: D = 256 1479 us with 32 and 1336
   // with 64, D = 128 773 and 716, over E4M3 725 and 730).
-  static constexpr int BN = D == 128 && E4M3 ? 32 : 64;
+  static constexpr int BN = D == 128 && FMT != kSame ? 32 : 64;
   static constexpr int RA = BM / 16, CK = BN / 16, U = D / 64;
   static constexpr int LD = D + 4, LDP = BN + 4;  // padded rows: conflict-free float4 reads
   static constexpr int OFF_K = BM * LD, OFF_V = OFF_K + BN * LD, OFF_P = OFF_V + BN * D;
@@ -54,11 +54,11 @@ struct Cfg {
 };
 
 // What one access of a thread takes from the cache, until it is written to shared memory: four
-// fp32 elements, or eight E4M3 codes with their row's scale.
-template <bool E4M3>
+// fp32 elements, or eight codes with their row's scale (and their group's factor).
+template <int FMT>
 struct Piece;
 template <>
-struct Piece<false> {
+struct Piece<kSame> {
   static constexpr int N = 4;
   float4 x;
   __device__ __forceinline__ void none() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
@@ -68,7 +68,7 @@ struct Piece<false> {
   __device__ __forceinline__ void store(float* at) const { *reinterpret_cast<float4*>(at) = x; }
 };
 template <>
-struct Piece<true> {
+struct Piece<kE4m3> {
   static constexpr int N = 8;
   uint2 x;
   uint8_t scale;
@@ -99,13 +99,46 @@ struct Piece<true> {
   }
 };
 
+template <>
+struct Piece<kE2m1> {
+  static constexpr int N = 8;
+  uint32_t x;
+  uint8_t scale, group;
+  __device__ __forceinline__ void none() {
+    x = 0u;
+    scale = 127;
+    group = 0;
+  }
+  // (elems: the row's first element, plus d, in a layout of heads before rows)
+  __device__ __forceinline__ void load(const CacheView& c, long long elems, long long at) {
+    x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c.cache) + elems / 2);
+    group = c.group[elems / 16];
+    scale = c.scale[at];
+  }
+  __device__ __forceinline__ void store(float* at) const {
+    const float e = scale_value(scale) * e4m3_value(group);
+    uint32_t h[4];
+    e2m1x8_to_f16x2(x, h);
+    float4 f[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
+      f[i] = make_float4(u.x * e, u.y * e, v.x * e, v.y * e);
+    }
+    const bool turn = threadIdx.x & 4;
+    *reinterpret_cast<float4*>(at + (turn ? 4 : 0)) = turn ? f[1] : f[0];
+    *reinterpret_cast<float4*>(at + (turn ? 0 : 4)) = turn ? f[0] : f[1];
+  }
+};
+
 __device__ __forceinline__ float dot4(const float4& a, const float4& b, float s) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
 }
 
-template <int D_, bool E4M3>
+template <int D_, int FMT>
 __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxParams p, int tiles) {
-  using C = Cfg<D_, E4M3>;
+  using C = Cfg<D_, FMT>;
   constexpr int BM = C::BM, BN = C::BN;
   extern __shared__ float sm[];
   const int D = p.c.D;
@@ -191,8 +224,9 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
       RowAt w = {-1, 0};
       if (n < kend) {
         if (page >= 0 && page < p.c.num_pages) {
-          w.elems = cache_row(p.c, page, 0, n & (page_size(p.c) - 1), hk);
           w.scale = scale_row(p.c, page, 0, n & (page_size(p.c) - 1), hk);
+          w.elems = FMT == kE2m1 ? w.scale * D
+                                 : cache_row(p.c, page, 0, n & (page_size(p.c) - 1), hk);
         } else {
           report(p.c, HSTU_DEVERR_OFFSETS);  // (a row of zeros then)
         }
@@ -203,10 +237,10 @@ __global__ void __launch_bounds__(kThreads) softmax_simt_kernel(const SoftmaxPar
     // A warp's accesses to the cache and to shared memory are contiguous (with sixteen elements a
     // thread a fifth of all cycles of shared memory were bank conflicts: D = 256 1336 us instead
     // of 1171), and up to sixteen of a thread are on their way at a time.
-    constexpr int NE = Piece<E4M3>::N, NX = BN * (D_ / NE) / kThreads, NB = NX < 8 ? NX : 8;
+    constexpr int NE = Piece<FMT>::N, NX = BN * (D_ / NE) / kThreads, NB = NX < 8 ? NX : 8;
 #pragma unroll 1
     for (int x0 = 0; x0 < NX; x0 += NB) {
-      Piece<E4M3> kx[NB], vx[NB];
+      Piece<FMT> kx[NB], vx[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         const int x = (x0 + i) * kThreads + threadIdx.x, r = x / (D_ / NE), d = x % (D_ / NE) * NE;
@@ -333,10 +367,10 @@ constexpr int kFewRows = 4, kFewThreads = 128;
 // 16 j .., fp32 ones 4 (j + i D / 16) .. in piece i, so that a group's loads are contiguous.
 // E4M3 elements stay codes until they are used (with their row's scale, which multiplies a score
 // and a weight instead of every element), so that more of them are on their way at a time.
-template <bool E4M3>
+template <int FMT>
 struct FewRow;
 template <>
-struct FewRow<false> {
+struct FewRow<kSame> {
   float4 x[4];
   template <int D_>
   __device__ __forceinline__ void load(const SoftmaxParams& p, int page, int plane, int row,
@@ -356,7 +390,7 @@ struct FewRow<false> {
   __device__ __forceinline__ float factor() const { return 1.f; }
 };
 template <>
-struct FewRow<true> {
+struct FewRow<kE4m3> {
   uint4 x;
   uint8_t scale;
   template <int D_>
@@ -383,16 +417,51 @@ struct FewRow<true> {
   }
   __device__ __forceinline__ float factor() const { return scale_value(scale); }
 };
+template <>
+struct FewRow<kE2m1> {
+  uint2 x;
+  uint8_t scale, group;
+  template <int D_>
+  __device__ __forceinline__ void load(const SoftmaxParams& p, int page, int plane, int row,
+                                       int hk, int j) {
+    x = make_uint2(0u, 0u);
+    scale = 127;
+    group = 0;
+    if (page < 0) return;
+    const long long r = scale_row(p.c, page, plane, row, hk);
+    if (16 * j < p.c.D) {
+      x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.c.cache) +
+                                          r * (p.c.D / 2) + 8 * j);
+      group = p.c.group[r * (p.c.D / 16) + j];
+    }
+    scale = p.c.scale[r];
+  }
+  __device__ __forceinline__ void get(float4 (&f)[4]) const {
+    const float g = e4m3_value(group);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t h[4];
+      e2m1x8_to_f16x2(w ? x.y : x.x, h);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
+        f[2 * w + i] = make_float4(a.x * g, a.y * g, b.x * g, b.y * g);
+      }
+    }
+  }
+  __device__ __forceinline__ float factor() const { return scale_value(scale); }
+};
 // First of the four elements in piece i of lane j.
-template <int D_, bool E4M3>
+template <int D_, int FMT>
 __device__ __forceinline__ int few_dim(int i, int j) {
-  return E4M3 ? 16 * j + 4 * i : 4 * (j + i * (D_ / 16));
+  return FMT != kSame ? 16 * j + 4 * i : 4 * (j + i * (D_ / 16));
 }
 
-template <int D_, bool E4M3>
+template <int D_, int FMT>
 __global__ void __launch_bounds__(kFewThreads, 3) softmax_few_kernel(const SoftmaxParams p,
                                                                      int tiles) {
-  constexpr int R = kFewRows, U = E4M3 ? 4 : 2, LPK = D_ / 16, KW = 32 / LPK;
+  constexpr int R = kFewRows, U = FMT != kSame ? 4 : 2, LPK = D_ / 16, KW = 32 / LPK;
   constexpr int WARPS = kFewThreads / 32, STEP = WARPS * U * KW;  // keys of a step
   __shared__ float4 qs[R][4][LPK];
   __shared__ float part_o[WARPS][R][D_], part_m[WARPS][R], part_l[WARPS][R];
@@ -418,7 +487,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) softmax_few_kernel(const Softm
 
   const float* q = static_cast<const float*>(p.q);
   for (int x = threadIdx.x; x < R * 4 * LPK; x += kFewThreads) {
-    const int r = x / (4 * LPK), i = x / LPK % 4, d = few_dim<D_, E4M3>(i, x % LPK);
+    const int r = x / (4 * LPK), i = x / LPK % 4, d = few_dim<D_, FMT>(i, x % LPK);
     const long long pr = m0 + r;
     qs[r][i][x % LPK] = pr < rows && d < p.c.D
         ? *reinterpret_cast<const float4*>(q + (s.t0 + pr / p.G) * p.q_stride +
@@ -451,7 +520,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) softmax_few_kernel(const Softm
 #pragma unroll
   for (int u = 0; u < U; ++u) next[u] = page_of(mine + u * KW);
   for (int n0 = 0; n0 < keys; n0 += STEP) {
-    FewRow<E4M3> k[U], v[U];
+    FewRow<FMT> k[U], v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int n = n0 + mine + u * KW, row = (int)(k0 + n) & (int)(page_size(p.c) - 1);
@@ -537,7 +606,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) softmax_few_kernel(const Softm
 #pragma unroll
         for (int d = LPK; d < 32; d <<= 1) e[c] += __shfl_xor_sync(0xffffffffu, e[c], d);
       if (g == 0)
-        *reinterpret_cast<float4*>(&part_o[warp][r][few_dim<D_, E4M3>(i, j)]) =
+        *reinterpret_cast<float4*>(&part_o[warp][r][few_dim<D_, FMT>(i, j)]) =
             make_float4(e[0], e[1], e[2], e[3]);
     }
     if (lane == 0) {
@@ -580,16 +649,16 @@ __global__ void __launch_bounds__(kFewThreads, 3) softmax_few_kernel(const Softm
   }
 }
 
-template <int D, bool E4M3>
+template <int D, int FMT>
 cudaError_t launch(const SoftmaxParams& p, int rows, long long tiles, long long blocks,
                    cudaStream_t stream) {
   if (rows == kFewRows) {
-    softmax_few_kernel<D, E4M3>
+    softmax_few_kernel<D, FMT>
         <<<dim3((unsigned)blocks, p.splits), kFewThreads, 0, stream>>>(p, (int)tiles);
     return cudaGetLastError();
   }
-  using C = Cfg<D, E4M3>;
-  auto* kernel = softmax_simt_kernel<D, E4M3>;
+  using C = Cfg<D, FMT>;
+  auto* kernel = softmax_simt_kernel<D, FMT>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
@@ -597,20 +666,21 @@ cudaError_t launch(const SoftmaxParams& p, int rows, long long tiles, long long 
   return cudaGetLastError();
 }
 
-template <bool E4M3>
+template <int FMT>
 cudaError_t launch_dim(const SoftmaxParams& p, int rows, long long tiles, long long blocks,
                        cudaStream_t stream) {
-  if (p.c.D > 128) return launch<256, E4M3>(p, rows, tiles, blocks, stream);
-  if (p.c.D > 64) return launch<128, E4M3>(p, rows, tiles, blocks, stream);
-  return launch<64, E4M3>(p, rows, tiles, blocks, stream);
+  if (p.c.D > 128) return launch<256, FMT>(p, rows, tiles, blocks, stream);
+  if (p.c.D > 64) return launch<128, FMT>(p, rows, tiles, blocks, stream);
+  return launch<64, FMT>(p, rows, tiles, blocks, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_softmax_simt(const SoftmaxParams& p, bool e4m3, int rows, long long tiles,
+cudaError_t launch_softmax_simt(const SoftmaxParams& p, int fmt, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream) {
-  return e4m3 ? launch_dim<true>(p, rows, tiles, blocks, stream)
-              : launch_dim<false>(p, rows, tiles, blocks, stream);
+  return fmt == kE4m3   ? launch_dim<kE4m3>(p, rows, tiles, blocks, stream)
+         : fmt == kE2m1 ? launch_dim<kE2m1>(p, rows, tiles, blocks, stream)
+                        : launch_dim<kSame>(p, rows, tiles, blocks, stream);
 }
 
 }  // namespace hstu

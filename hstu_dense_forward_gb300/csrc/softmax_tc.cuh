@@ -54,6 +54,9 @@
 // weights keep 2^-31 of theirs. (Telling such rows apart where the unit is raised took 20-30 % of
 // prompts with a row of zeros in every tile.)
 //
+// E2M1 caches: a code becomes fp16 times its group's factor (and 2^(e - EK)); factor times code has
+// seven bits, 2^-10 .. 2688. All the rest is as for E4M3, with 2688 in the place of 448.
+//
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
 #pragma once
@@ -84,33 +87,34 @@ constexpr int kSpreadK = 14, kSpreadV = 7;  // spread of exponents that are take
 constexpr uint32_t kLeast = 27;             // smallest row scale that is written
 constexpr float kApart = 96.0f;             // d - EV of tiles whose sums are computed apart
 
-template <int D_, int NQT_, int CTAS_, bool E4M3_>
+template <int D_, int NQT_, int CTAS_, int FMT_>
 struct Cfg {
   static constexpr int D = D_, NQT = NQT_, CTAS = CTAS_;  // CTAS: of an SM
-  static constexpr bool E4M3 = E4M3_;
+  static constexpr bool CODES = FMT_ != kSame, FP4 = FMT_ == kE2m1;
   static_assert(D == 64 || D == 128 || D == 256, "head dim of the kernel");
   static_assert(NQT == 1 || (NQT == 2 && D <= 128), "query tiles");
-  static_assert(CTAS == 1 || (CTAS == 2 && NQT == 1 && D <= 128 && !E4M3_), "CTAs per SM");
+  static_assert(CTAS == 1 || (CTAS == 2 && NQT == 1 && D <= 128 && FMT_ == kSame), "CTAs per SM");
   static constexpr int KT = D == 256 ? 64 : 128;  // keys of one tile
   static constexpr int NSB = NQT == 1 && CTAS == 1 ? 2 : 1;  // score buffers of a query tile
   static constexpr int SWB = 128, EPC = 64;       // swizzled row bytes and elements of a block
   static constexpr int NCB = D / EPC;             // column blocks of a row
   static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
   static constexpr int KV_CB = KT * SWB, KV_TILE = NCB * KV_CB;
-  static constexpr int ST_TILE = KT * D;          // staged E4M3 tile; its row scales (KT bytes)
+  static constexpr int ST_ROW = FP4 ? D / 2 : D, ST_TILE = KT * ST_ROW;  // staged tile of codes
+  static constexpr int GR_TILE = FP4 ? KT * (D / 16) : 0;  // E2M1: its factors
   // The scores' A operand, Q, comes from TMEM where that has room: from shared memory it takes,
   // with K, all of the latter's bandwidth, and threads wait for their barriers meanwhile.
   static constexpr bool QT = NSB == 2 || D == 64;
   // ring depths: what 227 KB of shared memory holds
   static constexpr int NSLOT = CTAS == 2  ? (D == 64 ? 6 : 2)
-                               : D == 64  ? (E4M3 ? 4 : 8)
-                               : QT       ? (E4M3 ? 4 : 6)
-                                          : (E4M3 ? 3 : 4);
-  static constexpr int NST = !E4M3 ? 0 : QT ? 4 : 3;
+                               : D == 64  ? (CODES ? 4 : 8)
+                               : QT       ? (CODES ? 4 : 6)
+                                          : (CODES ? 3 : 4);
+  static constexpr int NST = !CODES ? 0 : QT ? 4 : 3;
   static constexpr int SM_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SM_WARPS, LOAD_WARP = SM_WARPS + 1;
   static constexpr int CONV_WARP = SM_WARPS + 4;  // (a warpgroup each for K and V)
-  static constexpr int THREADS = (SM_WARPS + 4 + (E4M3 ? 8 : 0)) * 32;
+  static constexpr int THREADS = (SM_WARPS + 4 + (CODES ? 8 : 0)) * 32;
   // columns of S that a softmax thread holds at a time, half a row (loaded twice: for the maximum
   // and for the weights): loops over halves stay small enough for the instruction cache
   static constexpr int SC = KT / 2;
@@ -121,8 +125,9 @@ struct Cfg {
   static constexpr int OFF_Q = 0, OFF_KV = QT ? 0 : NQT * Q_TILE;
   static constexpr int OFF_ST = OFF_KV + NSLOT * KV_TILE;
   static constexpr int OFF_SC = OFF_ST + NST * ST_TILE;  // row scales of the staged tiles
-  static constexpr int OFF_BAR = OFF_SC + NST * 128;
-  static constexpr int OFF_PLAN = OFF_BAR + (E4M3 ? 4096 : 2048);
+  static constexpr int OFF_GR = OFF_SC + NST * 128;
+  static constexpr int OFF_BAR = OFF_GR + NST * GR_TILE;
+  static constexpr int OFF_PLAN = OFF_BAR + (CODES ? 4096 : 2048);
   static constexpr int USED = OFF_PLAN + kPlanSharedBytes + 1024;  // (alignment of the base)
   // (one CTA per SM, which takes all of TMEM: no second one may come to wait for it)
   static constexpr int SMEM = CTAS == 1 && USED < 120 * 1024 ? 120 * 1024 : USED;
@@ -446,9 +451,9 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
   const uint32_t sbase = ptx::smem_u32(smem);
   const int tpt = 128 / p.G, ps = 1 << p.c.page_shift;
   const uint32_t q_bytes = (uint32_t)(tpt * p.G) * C::SWB * C::NCB;
-  constexpr int DEPTH = C::E4M3 ? C::NST : C::NSLOT;
-  uint64_t* full = C::E4M3 ? bars->st_full : bars->kv_full;
-  uint64_t* empty = C::E4M3 ? bars->st_empty : bars->kv_empty;
+  constexpr int DEPTH = C::CODES ? C::NST : C::NSLOT;
+  uint64_t* full = C::CODES ? bars->st_full : bars->kv_full;
+  uint64_t* empty = C::CODES ? bars->st_empty : bars->kv_empty;
   const int boxes = ps >= C::KT ? 1 : C::KT / 32;
   uint32_t ring = 0, queries = 0;
   Walk w;
@@ -475,16 +480,26 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
       const int slot = (ring + i) % DEPTH;
       if (!wait_bar(p, bars, &empty[slot], (((ring + i) / DEPTH) & 1) ^ 1)) return;
       const uint32_t bar = ptx::smem_u32(&full[slot]);
-      const bool scales = C::E4M3 && p.c.scale;
-      ptx::mbar_arrive_expect_tx(bar, C::E4M3 ? C::ST_TILE + (scales ? C::KT : 0) : C::KV_TILE);
+      const bool scales = C::CODES && p.c.scale;
+      const int gb = p.c.D / 16;  // E2M1: factors of a row
+      ptx::mbar_arrive_expect_tx(bar, C::CODES ? C::ST_TILE + (scales ? C::KT : 0) +
+                                                     (C::FP4 ? C::KT * gb : 0)
+                                               : C::KV_TILE);
       const int row0 = ps >= C::KT ? (int)(n0 & (ps - 1)) : 0;
 #pragma unroll
       for (int m = 0; m < C::KT / 32; ++m) {
         if (m >= boxes) break;
         const int plane = (int)(2 * page[m]) + (v ? 1 : 0);
-        if constexpr (C::E4M3) {
-          ptx::tma_load_4d(sbase + C::OFF_ST + slot * C::ST_TILE + m * 32 * C::D, tc, bar, 0,
-                           it.hk, row0, plane);
+        if constexpr (C::CODES) {
+          const uint32_t dst = sbase + C::OFF_ST + slot * C::ST_TILE + m * 32 * C::ST_ROW;
+          if constexpr (C::FP4) {
+            ptx::tma_load_4d(dst, tc, bar, 0, row0, it.hk, plane);
+            ptx::bulk_load(sbase + C::OFF_GR + slot * C::GR_TILE + m * 32 * gb,
+                           p.c.group + scale_row(p.c, page[m], v ? 1 : 0, row0, it.hk) * gb,
+                           (boxes == 1 ? C::KT : 32) * gb, bar);
+          } else {
+            ptx::tma_load_4d(dst, tc, bar, 0, it.hk, row0, plane);
+          }
           if (scales)
             ptx::bulk_load(sbase + C::OFF_SC + slot * 128 + m * 32,
                            p.c.scale + scale_row(p.c, page[m], v ? 1 : 0, row0, it.hk),
@@ -513,8 +528,8 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
   }
 }
 
-// ------------------------------------------------------------------ E4M3 -> fp16
-// A thread converts sixteen codes of a row at a time. Rows beyond the sequence become zeros
+// ------------------------------------------------------------------ codes -> fp16
+// A thread converts sixteen codes of a row at a time (of E2M1 a group). Rows beyond the sequence become zeros
 // (what an unused row of a page holds, NaN included, does not reach the products).
 template <class C>
 __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
@@ -572,7 +587,7 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
           ptx::mbar_arrive(ptx::smem_u32(&bars->exp_full[te]));
         }
       }
-      const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * 16;
+      const uint8_t* src = smem + C::OFF_ST + st * C::ST_TILE + chunk * (C::FP4 ? 8 : 16);
       uint8_t* dst = smem + C::OFF_KV + slot * C::KV_TILE + cb * C::KV_CB;
       uint32_t mine = one;  // factor of row my_row, twice (0 beyond the sequence)
       if (p.c.scale && !own) mine = half_power(top - (int)scale[my_row]) * 0x10001u;
@@ -580,7 +595,14 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
       uint4 u[PASSES];
 #pragma unroll
       for (int k = 0; k < PASSES; ++k) {
-        u[k] = *reinterpret_cast<const uint4*>(src + (r0 + STEP * k) * C::D);
+        if constexpr (C::FP4) {  // (and the group's factor)
+          const uint2 x = *reinterpret_cast<const uint2*>(src + (r0 + STEP * k) * C::ST_ROW);
+          u[k] = make_uint4(x.x, x.y, 0u, 0u);
+          if (chunk < p.c.D / 16)
+            u[k].z = smem[C::OFF_GR + st * C::GR_TILE + (r0 + STEP * k) * (p.c.D / 16) + chunk];
+        } else {
+          u[k] = *reinterpret_cast<const uint4*>(src + (r0 + STEP * k) * C::ST_ROW);
+        }
         if (r0 + STEP * k >= have) u[k] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (!warp_wait(p, bars, &bars->kv_empty[slot], ((i / C::NSLOT) & 1) ^ 1)) return;
@@ -590,11 +612,23 @@ __device__ void convert_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem,
         const uint32_t in[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
         const uint32_t f = __shfl_sync(0xffffffffu, mine, lane / CPR + RPW * k);
         uint32_t w[8];
+        if constexpr (C::FP4) {
+          // (factor 2^-9 .. 448 times 2^-14 .. 1 and code: multiples of 2^-24, at most 2688)
+          const uint32_t fg = mul_f16x2(f, e4m3x2_to_f16x2(in[2] * 0x101u));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          e4m3x4_to_f16x2(in[e], w[2 * e], w[2 * e + 1]);
-          w[2 * e] = mul_f16x2(w[2 * e], f);
-          w[2 * e + 1] = mul_f16x2(w[2 * e + 1], f);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[4];
+            e2m1x8_to_f16x2(in[h], x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[4 * h + e] = mul_f16x2(x[e], fg);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            e4m3x4_to_f16x2(in[e], w[2 * e], w[2 * e + 1]);
+            w[2 * e] = mul_f16x2(w[2 * e], f);
+            w[2 * e + 1] = mul_f16x2(w[2 * e + 1], f);
+          }
         }
         uint8_t* row = dst + r * C::SWB;
         *reinterpret_cast<uint4*>(row + ((c16 ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -635,7 +669,7 @@ __device__ float query_to_tmem(const SoftmaxParams& p, uint32_t col, bool any, b
   const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at);
   const int pieces = valid ? p.c.D / 8 : 0;  // of 16 bytes, eight at a time in flight
   int sh = 0;
-  if constexpr (BF16 && C::E4M3) {
+  if constexpr (BF16 && C::CODES) {
     uint32_t top = 0;
 #pragma unroll 1
     for (int x0 = 0; x0 < C::D / 8; x0 += 8) {
@@ -657,7 +691,7 @@ __device__ float query_to_tmem(const SoftmaxParams& p, uint32_t col, bool any, b
     for (int x = 0; x < 8; x += 2) {
       uint32_t w[8] = {u[x].x,     u[x].y,     u[x].z,     u[x].w,
                        u[x + 1].x, u[x + 1].y, u[x + 1].z, u[x + 1].w};
-      if constexpr (BF16 && C::E4M3) {
+      if constexpr (BF16 && C::CODES) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = bf16_to_half(w[e], mul);
       }
@@ -696,7 +730,7 @@ struct Issuer {
   const SoftmaxParams& p;
   Bars* bars;
   uint32_t sbase, tmem;
-  static constexpr uint32_t AB = BF16 && !C::E4M3 ? 1u : 0u;  // operands: bf16, or fp16
+  static constexpr uint32_t AB = BF16 && !C::CODES ? 1u : 0u;  // operands: bf16, or fp16
   static constexpr uint32_t IDESC_S = ptx::idesc_f16(AB, 128, C::KT, 0);
   static constexpr uint32_t IDESC_O = ptx::idesc_f16(AB, 128, C::D, 1);
 
@@ -787,10 +821,10 @@ __device__ void mma_role(const SoftmaxParams& p, Issuer<C, BF16>& is, Bars* bars
     // behind the loads.
 #pragma unroll
     for (int q = 0; q < C::NQT; ++q) {
-      if (C::QT ? nq[q] > 0 : BF16 && C::E4M3)
+      if (C::QT ? nq[q] > 0 : BF16 && C::CODES)
         if (!warp_wait(p, bars, &bars->q_ready[q], (C::QT ? outputs[q] : queries) & 1)) return;
     }
-    if (!C::QT && !(BF16 && C::E4M3) && !warp_wait(p, bars, &bars->q_full, queries & 1)) return;
+    if (!C::QT && !(BF16 && C::CODES) && !warp_wait(p, bars, &bars->q_full, queries & 1)) return;
     ++queries;
     // Scores of the first NSB tiles, over weights of the piece before: its last product must be
     // done. (Those before it are: the softmax hands over a piece's last weights only then, so
@@ -902,7 +936,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     const long long tok = it.tok0 + (long long)q * tpt + r / p.G;
     const bool valid = q < it.nq && r < tpt * p.G && tok < it.s.n;
     const bool any = __any_sync(0xffffffffu, valid);
-    if (C::E4M3 && p.c.k_ds) {
+    if (C::CODES && p.c.k_ds) {
       fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
       fv = p.c.v_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
     }
@@ -915,7 +949,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bars->q_ready[q]));
       }
-    } else if (BF16 && C::E4M3 && it.nmax > 0) {
+    } else if (BF16 && C::CODES && it.nmax > 0) {
       if (!warp_wait(p, bars, &bars->q_full, queries++ & 1)) return;
       if (valid) fk *= query_to_half<C>(smem + C::OFF_Q + q * C::Q_TILE, r);
       ptx::fence_proxy_async_smem();
@@ -927,7 +961,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     if (p.causal && valid) see = min(see, it.s.Lk - it.s.n + tok + 1);
     const int lim = (int)max(see - it.k0, 0ll);
     const int rest = (int)min(it.s.Lk - it.k0, 0x7fffffffll);  // keys of the sequence from k0 on
-    float m = C::E4M3 ? kNoKey : -CUDART_INF_F, l = 0.0f;
+    float m = C::CODES ? kNoKey : -CUDART_INF_F, l = 0.0f;
     float d = 0.0f, o_ref = m;        // E4M3: O's unit is 2^(m + d)
     float lowest = -CUDART_INF_F;     // EV below which a tile's sum is computed apart
     float high = -CUDART_INF_F;       // a score above it raises a reference
@@ -938,7 +972,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       ptx::tc_fence_after();
       float ek = 1.0f, ev = 0.0f;  // the tile's 2^EK and EV
       bool own = false;            // its rows have exponents of their own
-      if constexpr (C::E4M3) {
+      if constexpr (C::CODES) {
         // (with the scores there the conversion has come to this tile; a warpgroup without tiles
         // of the last piece could otherwise be here phases ahead of it)
         const uint32_t te = done + t;
@@ -951,12 +985,12 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       // Factor of the scores. For a query of zeros (or nearly) over small keys it would be 0, and
       // a masked score, -inf, NaN by it: the smallest normal value instead leaves scores below
       // 2^-90 (a NaN stays one).
-      const float fa = C::E4M3 ? max_nan(fabsf(fk) * ek, kTiny) : fk;
+      const float fa = C::CODES ? max_nan(fabsf(fk) * ek, kTiny) : fk;
       const uint32_t s_col = tmem + lane_off + sb * KT;
       constexpr int NC = C::SC / 32;  // chunks held at a time
       uint32_t sv[NC][32];
       float neg = 0.0f;
-      if constexpr (C::E4M3) {
+      if constexpr (C::CODES) {
         neg = ev - o_ref;
         high = fminf(m, kHead - neg) + kLazy;
       }
@@ -982,7 +1016,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       // the conversion has done that.)
       auto clear_values = [&] {
         const int have = rest - t * KT;
-        if (C::E4M3 || have >= KT) return true;
+        if (C::CODES || have >= KT) return true;
         const uint32_t vi = ring + v_index<C>(t, it.nmax);
         if (!warp_wait(p, bars, &bars->kv_full[vi % C::NSLOT], (vi / C::NSLOT) & 1)) return false;
         uint8_t* v = smem + C::OFF_KV + (vi % C::NSLOT) * C::KV_TILE;
@@ -1022,7 +1056,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
         const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fa;
         // raise the reference: at the first visible key, and when weights would pass 2^kLazy
         // (any key is above -inf)
-        const bool raise = valid && (mx > high || (C::E4M3 && ev < lowest));
+        const bool raise = valid && (mx > high || (C::CODES && ev < lowest));
         if (__any_sync(0xffffffffu, raise || own)) {
           float corr = 1.0f;  // (0 at the first visible key)
           bool apart;
@@ -1031,7 +1065,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             uint32_t s[16];
             ptx::tmem_ld16(s_col + c, s);
             uint4 ku = {}, vu = {};
-            if constexpr (C::E4M3) {
+            if constexpr (C::CODES) {
               const uint8_t* rows = bars->row_exp[(done + t) % kExpDepth][0];
               ku = *reinterpret_cast<const uint4*>(rows + c);
               vu = *reinterpret_cast<const uint4*>(rows + 128 + c);
@@ -1041,13 +1075,13 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             for (int e = 0; e < 16; ++e) {
               const uint32_t kb = (kw[e >> 2] >> (8 * (e & 3))) & 0xffu;
               const int vb = (int)((vw[e >> 2] >> (8 * (e & 3))) & 0xffu) - 127;
-              const float k = C::E4M3 ? fabsf(fk) * scale_value(kb) : fa;
+              const float k = C::CODES ? fabsf(fk) * scale_value(kb) : fa;
               // (rounded like m: an exact product may be far from a large one's rounding)
               const float y = __fmul_rn(__uint_as_float(s[e]), k) - ref;
-              f(e, c + e < left ? y : -CUDART_INF_F, C::E4M3 ? (float)vb : 0.0f);
+              f(e, c + e < left ? y : -CUDART_INF_F, C::CODES ? (float)vb : 0.0f);
             }
           };
-          if constexpr (C::E4M3) {
+          if constexpr (C::CODES) {
             float top = mx;
             if (own) {  // (mx took codes for keys)
               top = -CUDART_INF_F;
@@ -1098,13 +1132,13 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
             for (int c = 0; c < KT; c += 16) {
               uint32_t pk[8];
               float w[16];
-              columns(c, !C::E4M3 && m == -CUDART_INF_F ? 0.0f : m, [&](int i, float y, float e) {
+              columns(c, !C::CODES && m == -CUDART_INF_F ? 0.0f : m, [&](int i, float y, float e) {
                 l += ex2(y);
-                w[i] = ex2(C::E4M3 ? y + (e - d) : y);
+                w[i] = ex2(C::CODES ? y + (e - d) : y);
               });
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                pk[e] = pack2<BF16 && !C::E4M3>(w[2 * e], w[2 * e + 1]);
+                pk[e] = pack2<BF16 && !C::CODES>(w[2 * e], w[2 * e + 1]);
               ptx::tmem_st8(s_col + c / 2, pk);
               if (c == KT / 2 - 16) {
                 ptx::tmem_st_wait();
@@ -1122,7 +1156,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
           }
           if (t > 0 && !rescale(corr)) return;
         }
-        if constexpr (!C::E4M3) neg = m == -CUDART_INF_F ? 0.0f : -m;
+        if constexpr (!C::CODES) neg = m == -CUDART_INF_F ? 0.0f : -m;
       }
       if (!clear_values()) return;
       float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -1136,7 +1170,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
                          fa, fa, neg, neg);
           const float p0 = ex2(x0), p1 = ex2(x1);
           ptx::add_f32x2(sum[e & 1][0], sum[e & 1][1], p0, p1);
-          pk[e] = pack2<BF16 && !C::E4M3>(p0, p1);
+          pk[e] = pack2<BF16 && !C::CODES>(p0, p1);
         }
         ptx::tmem_st16(s_col + at * 16, pk);
       };
@@ -1155,7 +1189,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
       }
       const float tile_sum = (sum[0][0] + sum[0][1]) + (sum[1][0] + sum[1][1]);
       // (the sum's unit is 2^m, the weights' 2^(m + d - ev))
-      l = C::E4M3 ? fmaf(tile_sum, ex2(-neg - m), l) : l + tile_sum;
+      l = C::CODES ? fmaf(tile_sum, ex2(-neg - m), l) : l + tile_sum;
       // A parity wait cannot tell a phase from the one two before it. The wait for PV(n - 1)
       // below needs PV(n - 2) to be done (of the piece before, it is); S(n - 1) was issued after
       // PV(n - 1 - NSB) only, and once P(n - 1) is handed over both may complete at any time.
@@ -1174,7 +1208,7 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
     const long long part = (long long)it.slot * (C::NQT * 128) + q * 128 + r;
     float inv = l > 0.0f ? fv / l : l;  // (a NaN sum stays one)
     float unit = 1.0f;  // 2^d in two factors: it may pass fp32's range where the output does not
-    if constexpr (C::E4M3) {
+    if constexpr (C::CODES) {
       const int e = (int)d;
       inv *= power2(e / 2);
       unit = power2(e - e / 2);
@@ -1216,12 +1250,12 @@ __device__ void softmax_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, 
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, int NQT, int CTAS, bool BF16, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NQT, CTAS, E4M3>::THREADS, CTAS)
+template <int D, int NQT, int CTAS, bool BF16, int FMT>
+__global__ void __launch_bounds__(Cfg<D, NQT, CTAS, FMT>::THREADS, CTAS)
     softmax_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_c, const SoftmaxParams p,
                       int tiles) {
-  using C = Cfg<D, NQT, CTAS, E4M3>;
+  using C = Cfg<D, NQT, CTAS, FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1234,7 +1268,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, CTAS, E4M3>::THREADS, CTAS)
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
     for (int s = 0; s < kExpDepth; ++s) ptx::mbar_init(ptx::smem_u32(&bars->exp_full[s]), 2);
     for (int s = 0; s < C::NSLOT; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), C::E4M3 ? 128 : 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->kv_full[s]), C::CODES ? 128 : 1);
       ptx::mbar_init(ptx::smem_u32(&bars->kv_empty[s]), 1);
     }
     for (int s = 0; s < 4; ++s) {
@@ -1266,7 +1300,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, CTAS, E4M3>::THREADS, CTAS)
   // With E4M3's conversion warps the launch leaves the softmax too few registers. 512 threads
   // launch with 128 each (65,536): 208 for its warps and 96 for the others are 63,488. 640 launch
   // with 96 (61,440): 120 and 80 are as many.
-  if constexpr (C::E4M3) {
+  if constexpr (C::CODES) {
     if (warp < C::SM_WARPS)
       ptx::regs_inc<C::NQT == 2 ? 120 : 208>();
     else
@@ -1282,7 +1316,7 @@ __global__ void __launch_bounds__(Cfg<D, NQT, CTAS, E4M3>::THREADS, CTAS)
     if (lane == 0) load_role<C>(p, bars, smem, pl, tiles, &tm_q, &tm_c);
   } else if (warp == C::LOAD_WARP + 1) {
     if (p.balanced && lane == 0) p.joins[blockIdx.x] = join_record<C>(p, pl, tiles);
-  } else if (C::E4M3 && warp >= C::CONV_WARP) {
+  } else if (C::CODES && warp >= C::CONV_WARP) {
     const int w = warp - C::CONV_WARP;
     convert_role<C>(p, bars, smem, pl, tiles, w >= 4, w & 3, lane);
   }
@@ -1302,11 +1336,11 @@ __global__ void __launch_bounds__(Cfg<D, NQT, CTAS, E4M3>::THREADS, CTAS)
   }
 }
 
-template <int D, int NQT, int CTAS, bool BF16, bool E4M3>
+template <int D, int NQT, int CTAS, bool BF16, int FMT>
 cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
                            long long tiles, long long blocks, cudaStream_t stream) {
-  using C = Cfg<D, NQT, CTAS, E4M3>;
-  auto* kernel = softmax_tc_kernel<D, NQT, CTAS, BF16, E4M3>;
+  using C = Cfg<D, NQT, CTAS, FMT>;
+  auto* kernel = softmax_tc_kernel<D, NQT, CTAS, BF16, FMT>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
@@ -1315,21 +1349,21 @@ cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tq, const 
 }
 
 // Kernel for the head dim, the number of query tiles and the CTAs of an SM.
-template <int D, bool BF16, bool E4M3>
+template <int D, bool BF16, int FMT>
 cudaError_t launch_dim(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
                        int qtiles, int ctas, long long tiles, long long blocks, cudaStream_t s) {
-  if constexpr (!E4M3) {
-    if (ctas == 2) return launch_variant<D, 1, 2, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+  if constexpr (FMT == kSame) {
+    if (ctas == 2) return launch_variant<D, 1, 2, BF16, FMT>(p, tq, tc, tiles, blocks, s);
   }
-  return qtiles == 2 ? launch_variant<D, 2, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s)
-                     : launch_variant<D, 1, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
+  return qtiles == 2 ? launch_variant<D, 2, 1, BF16, FMT>(p, tq, tc, tiles, blocks, s)
+                     : launch_variant<D, 1, 1, BF16, FMT>(p, tq, tc, tiles, blocks, s);
 }
-template <bool BF16, bool E4M3>
+template <bool BF16, int FMT>
 cudaError_t launch_tc(const SoftmaxParams& p, const CUtensorMap& tq, const CUtensorMap& tc,
                       int qtiles, int ctas, long long tiles, long long blocks, cudaStream_t s) {
-  if (p.c.D > 128) return launch_variant<256, 1, 1, BF16, E4M3>(p, tq, tc, tiles, blocks, s);
-  if (p.c.D > 64) return launch_dim<128, BF16, E4M3>(p, tq, tc, qtiles, ctas, tiles, blocks, s);
-  return launch_dim<64, BF16, E4M3>(p, tq, tc, qtiles, ctas, tiles, blocks, s);
+  if (p.c.D > 128) return launch_variant<256, 1, 1, BF16, FMT>(p, tq, tc, tiles, blocks, s);
+  if (p.c.D > 64) return launch_dim<128, BF16, FMT>(p, tq, tc, qtiles, ctas, tiles, blocks, s);
+  return launch_dim<64, BF16, FMT>(p, tq, tc, qtiles, ctas, tiles, blocks, s);
 }
 
 }  // namespace sm

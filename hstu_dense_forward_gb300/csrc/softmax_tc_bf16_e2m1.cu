@@ -1,0 +1,12 @@
+// Tensor-core softmax attention: bf16 queries over a 4-bit (E2M1) cache.
+#include "softmax_tc.cuh"
+
+namespace hstu {
+
+cudaError_t launch_softmax_tc_bf16_e2m1(const SoftmaxParams& p, const CUtensorMap& tq,
+                                 const CUtensorMap& tc, int qtiles, int ctas, long long tiles,
+                                 long long blocks, cudaStream_t stream) {
+  return sm::launch_tc<true, kE2m1>(p, tq, tc, qtiles, ctas, tiles, blocks, stream);
+}
+
+}  // namespace hstu

@@ -24,13 +24,16 @@ from . import _abi
 __all__ = ["hstu_kv_append", "hstu_kv_read", "hstu_softmax_fwd"]
 
 _ROWS = {torch.float32: _abi.HSTU_F32, torch.float16: _abi.HSTU_F16, torch.bfloat16: _abi.HSTU_BF16}
-_CACHE = {**_ROWS, torch.float8_e4m3fn: _abi.HSTU_FP8_E4M3}
+_CACHE = {**_ROWS, torch.float8_e4m3fn: _abi.HSTU_FP8_E4M3, torch.uint8: _abi.HSTU_FP4_E2M1}
+if hasattr(torch, "float4_e2m1fn_x2"):
+    _CACHE[torch.float4_e2m1fn_x2] = _abi.HSTU_FP4_E2M1
 _INDEX = (torch.int32, torch.int64)
 _FP8 = torch.float8_e4m3fn
+_FP4 = _abi.HSTU_FP4_E2M1
 
 # The C structs as bytes (their layouts are those of the ctypes mirrors in _abi): one pack is
 # a fraction of the cost of setting their fields.
-_PACK_CACHE = struct.Struct("@8iPPqPPPqPPP").pack
+_PACK_CACHE = struct.Struct("@8iPPqPPPqPPPP").pack
 _PACK_ROWS = struct.Struct("@PPqqPqii").pack
 _PACK_ATTN = struct.Struct("@PqPqiiiiifPPPqi4x").pack
 
@@ -97,7 +100,8 @@ def _factors(k_descale, v_descale, dev, B, Nk):
                      f"got {list(shape)}")
 
 
-def _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale):
+def _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
+                   kv_group_scale):
     """Raises for what is wrong with these tensors."""
     if not isinstance(kv_cache, torch.Tensor):
         raise TypeError("kv_cache must be a torch.Tensor")
@@ -106,12 +110,17 @@ def _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len,
         raise ValueError("the KV cache operators run on CUDA tensors only")
     if kv_cache.dtype not in _CACHE:
         raise TypeError(f"unsupported kv_cache dtype {kv_cache.dtype}")
+    fp4 = _CACHE[kv_cache.dtype] == _FP4
     if kv_cache.dim() != 5 or kv_cache.shape[1] != 2:
-        raise ValueError("kv_cache must be [num_pages, 2, page_size, Nk, D], got "
-                         f"{list(kv_cache.shape)}")
+        raise ValueError("kv_cache must be [num_pages, 2, page_size, Nk, D] (4-bit codes: "
+                         f"[num_pages, 2, Nk, page_size, D / 2]), got {list(kv_cache.shape)}")
     if not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be contiguous")
-    pages, _, page_size, Nk, _ = kv_cache.shape
+    pages, _, page_size, Nk, D = kv_cache.shape
+    if fp4:
+        page_size, Nk, D = Nk, page_size, 2 * D
+        if D % 32:
+            raise ValueError(f"a 4-bit kv_cache needs a head dim that is a multiple of 32, got {D}")
     if not isinstance(seq_offsets, torch.Tensor):
         raise TypeError("seq_offsets must be a torch.Tensor")
     index = seq_offsets.dtype
@@ -128,53 +137,68 @@ def _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len,
     _tensor(page_ids, "page_ids", dev, index, page_ids.shape)
     if kv_scale is not None:
         _tensor(kv_scale, "kv_scale", dev, torch.uint8, (pages, 2, Nk, page_size))
+    if fp4 != (kv_group_scale is not None) or (fp4 and kv_scale is None):
+        raise ValueError("a 4-bit kv_cache has kv_scale and kv_group_scale, no other has the latter")
+    if fp4:
+        _tensor(kv_group_scale, "kv_group_scale", dev, _FP8, (pages, 2, Nk, page_size, D // 16))
 
 
 class _Cache:
     """The checked hstu_kv_cache (packed) and what the entry points need of it."""
-    __slots__ = ("packed", "device", "index", "dtype", "B", "Nk", "D", "sizes", "keep")
+    __slots__ = ("packed", "device", "index", "dtype", "codes", "B", "Nk", "D", "sizes", "keep")
 
 
-def _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
-           v_descale, status):
+def _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, kv_group_scale,
+           k_descale, v_descale, status):
     c = _Cache()
     try:  # one pass over what is usually right; _explain_cache says what is not
         dev = c.device = kv_cache.get_device()
         pages, two, page_size, Nk, D = kv_cache.shape
+        code = _CACHE.get(kv_cache.dtype)
+        if code == _FP4:
+            page_size, Nk, D = Nk, page_size, 2 * D
         index = seq_offsets.dtype
         B1, = seq_offsets.shape
         num_ids, = page_ids.shape
-        ok = (dev >= 0 and two == 2 and kv_cache.dtype in _CACHE and index in _INDEX and B1 > 0 and
+        ok = (dev >= 0 and two == 2 and code is not None and index in _INDEX and B1 > 0 and
               kv_cache.is_contiguous() and page_offsets.shape == (B1,) and
               last_page_len.shape == (B1 - 1,) and
               (kv_scale is None or
                (kv_scale.dtype is torch.uint8 and kv_scale.get_device() == dev and
-                kv_scale.shape == (pages, 2, Nk, page_size) and kv_scale.is_contiguous())))
+                kv_scale.shape == (pages, 2, Nk, page_size) and kv_scale.is_contiguous())) and
+              (code == _FP4) is (kv_group_scale is not None))
+        if code == _FP4:
+            ok = (ok and D % 32 == 0 and kv_scale is not None and kv_group_scale.dtype is _FP8 and
+                  kv_group_scale.get_device() == dev and kv_group_scale.is_contiguous() and
+                  kv_group_scale.shape == (pages, 2, Nk, page_size, D // 16))
         for t in (seq_offsets, page_offsets, page_ids, last_page_len):
             ok = ok and t.dtype is index and t.get_device() == dev and t.is_contiguous()
     except (AttributeError, ValueError, TypeError):
         ok = False
     if not ok:
-        _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale)
+        _explain_cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
+                       kv_group_scale)
         raise ValueError("kv_cache and its page table do not fit together")
     c.dtype, c.index, c.B, c.Nk, c.D, c.keep = kv_cache.dtype, index, B1 - 1, Nk, D, None
-    fp8 = c.dtype is _FP8
     descale, kd, vd = _abi.HSTU_DESCALE_CAST, 0, 0
     if kv_scale is not None or k_descale is not None or v_descale is not None:
-        if not fp8:
-            raise ValueError("kv_scale, k_descale and v_descale go with FP8 E4M3 caches")
+        if c.dtype is not _FP8 and code != _FP4:
+            raise ValueError("kv_scale, k_descale and v_descale go with FP8 E4M3 caches, kv_scale "
+                             "also with 4-bit ones")
         if kv_scale is None:
             descale, *c.keep = _factors(k_descale, v_descale, kv_cache.device, c.B, Nk)
             kd, vd = c.keep[0].data_ptr(), c.keep[1].data_ptr()
         elif k_descale is not None or v_descale is not None:
             raise ValueError("a cache has row scales (kv_scale) or static factors, not both")
+    c.codes = code == _FP4 or c.dtype is _FP8
     status_ptr = 0 if status is None else _tensor(status, "status", kv_cache.device, torch.int32,
                                                   (1,))
-    c.sizes = (_CACHE[c.dtype], c.B, Nk, D, page_size, index is torch.int64, descale)
+    c.sizes = (code, c.B, Nk, D, page_size, index is torch.int64, descale)
     c.packed = _PACK_CACHE(*c.sizes, 0, kv_cache.data_ptr(),
                            0 if kv_scale is None else kv_scale.data_ptr(), pages,
                            page_offsets.data_ptr(), page_ids.data_ptr(), last_page_len.data_ptr(),
-                           num_ids, kd, vd, status_ptr)
+                           num_ids, kd, vd, status_ptr,
+                           0 if kv_group_scale is None else kv_group_scale.data_ptr())
     return c
 
 
@@ -182,9 +206,9 @@ def _row_dtype(c, dtype):
     code = _ROWS.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}")
-    if c.dtype is not dtype and c.dtype is not _FP8:
-        raise TypeError(f"{dtype} rows need a kv_cache of their type or of FP8 E4M3, got "
-                        f"{c.dtype}")
+    if c.dtype is not dtype and not c.codes:
+        raise TypeError(f"{dtype} rows need a kv_cache of their type, of FP8 E4M3 or of 4-bit "
+                        f"codes, got {c.dtype}")
     return code
 
 
@@ -221,14 +245,14 @@ def _workspace_bytes(device, cache_sizes, attn_sizes):
     need = ctypes.c_longlong(0)
     with torch.cuda.device(device):
         _abi.check(_abi.lib().hstu_softmax_workspace(
-            _PACK_CACHE(*cache_sizes, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0),
+            _PACK_CACHE(*cache_sizes, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0),
             _PACK_ATTN(0, 0, 0, *attn_sizes, 0, 0, 0, 0, 0), ctypes.byref(need)),
             "hstu_softmax_workspace")
     return need.value
 
 
 def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_page_len,
-                   kv_scale=None, k_descale=None, v_descale=None, status=None):
+                   kv_scale=None, kv_group_scale=None, k_descale=None, v_descale=None, status=None):
     """Write new rows into the paged cache; returns kv_cache.
 
     k, v [T, Nk, D] fp32, fp16 or bf16; rows of D * Nk contiguous elements, which may be
@@ -245,10 +269,18 @@ def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_
     nearest even, saturating at +-448. (hstu_fwd reads the last two forms; a cache with row
     scales goes to hstu_softmax_fwd, or to hstu_fwd by way of hstu_kv_read.)
 
+    4-bit caches: kv_cache [num_pages, 2, Nk, page_size, D / 2] (uint8, or float4_e2m1fn_x2; D a
+    multiple of 32) takes E2M1 codes, element 2 i in the low half of byte i, kv_group_scale
+    [num_pages, 2, Nk, page_size, D / 16] float8_e4m3fn a factor per sixteen elements, and kv_scale
+    a power of two per row and head; the value is 2^(kv_scale - 127) * factor * code. The power is
+    the smallest that brings the row's largest magnitude to 2688 (448 * 6) or less, the factor a
+    sixth of the sixteen's largest over it. What lies beyond saturates; a NaN makes its sixteen
+    values NaN.
+
     status: an int32 tensor of one element that is set to 1 where offsets, lengths or page ids
     are found invalid on the device (nothing of such a sequence is written)."""
-    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
-               v_descale, status)
+    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
+               kv_group_scale, k_descale, v_descale, status)
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
     _copy("hstu_kv_append", c, k, v, seq_offsets)
@@ -256,17 +288,17 @@ def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_
 
 
 def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len,
-                 total_tokens=None, dtype=None, kv_scale=None, k_descale=None, v_descale=None,
-                 k=None, v=None, status=None):
+                 total_tokens=None, dtype=None, kv_scale=None, kv_group_scale=None, k_descale=None,
+                 v_descale=None, k=None, v=None, status=None):
     """Read rows of the paged cache back as contiguous k, v [T, Nk, D] (what hstu_fwd takes
     with seq_offsets_k = seq_offsets): the last seq_offsets[b+1] - seq_offsets[b] rows of each
     sequence, which is all of it when that is its length. total_tokens = T, at least
-    seq_offsets[B]. dtype: fp32, fp16 or bf16 (default: the cache's; for an E4M3 cache, which is
-    dequantised by kv_scale or k_descale / v_descale, bf16). k and v may be given instead (rows
+    seq_offsets[B]. dtype: fp32, fp16 or bf16 (default: the cache's; for an E4M3 or 4-bit cache,
+    which is dequantised by its scales, bf16). k and v may be given instead (rows
     as for hstu_kv_append); rows of no sequence are left as they were. Other arguments as for
     hstu_kv_append."""
-    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
-               v_descale, status)
+    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
+               kv_group_scale, k_descale, v_descale, status)
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
     new = k is None
@@ -274,7 +306,7 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
         if total_tokens is None:
             raise ValueError("hstu_kv_read needs total_tokens, or k and v")
         if dtype is None:
-            dtype = torch.bfloat16 if c.dtype is _FP8 else c.dtype
+            dtype = torch.bfloat16 if c.codes else c.dtype
         _row_dtype(c, dtype)
         shape = (int(total_tokens), c.Nk, c.D)
         k = torch.empty(shape, dtype=dtype, device=kv_cache.device)
@@ -289,13 +321,14 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
 
 def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page_offsets,
                      page_ids, last_page_len, causal=True, alpha=1.0, kv_scale=None,
-                     k_descale=None, v_descale=None, out=None, return_lse=False, status=None):
+                     kv_group_scale=None, k_descale=None, v_descale=None, out=None,
+                     return_lse=False, status=None):
     """Softmax attention of the newest tokens of each sequence over its paged cache, which
     holds their keys too (hstu_kv_append first).
 
     q [T, Nq, D] fp32, fp16 or bf16 (rows may be slices of a wider tensor), Nq a multiple of
-    the cache's Nk; the cache of q's type or float8_e4m3fn (kv_scale or k_descale / v_descale as
-    hstu_kv_append wrote it). The n = seq_offsets[b+1] - seq_offsets[b] queries of a sequence
+    the cache's Nk; the cache of q's type, float8_e4m3fn (kv_scale or k_descale / v_descale as
+    hstu_kv_append wrote it) or 4-bit (kv_scale and kv_group_scale). The n = seq_offsets[b+1] - seq_offsets[b] queries of a sequence
     are its last n positions; with causal=True each sees the keys up to its own position, with
     causal=False all of them (n may then exceed the keys: cross attention). max_seqlen bounds n,
     max_seqlen_k the cached keys of a sequence.
@@ -303,8 +336,8 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
     out = softmax(alpha q k^T) v with q's shape and type; with return_lse also ln sum exp(alpha
     q k) [T, Nq] fp32. A row that sees no key gets 0 (lse -inf); rows of no sequence are left
     as allocated. Other arguments as for hstu_kv_append."""
-    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale, k_descale,
-               v_descale, status)
+    c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
+               kv_group_scale, k_descale, v_descale, status)
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dtype = _row_dtype(c, q.dtype)

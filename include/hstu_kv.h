@@ -11,12 +11,21 @@
  * For these operators the table describes the sequences with their new rows: the n rows
  * seq_offsets gives a sequence are its last n positions, Lk - n .. Lk - 1.
  *
- * Element types of the cache: fp32, fp16, bf16, or FP8 E4M3 in one of three forms,
+ * Element types of the cache: fp32, fp16, bf16, FP4 E2M1 (below), or FP8 E4M3 in one of three
+ * forms,
  *   plain cast      the value of an element is its E4M3 value;
  *   static factors  k_descale / v_descale of hstu_fwd_descale's TENSOR, BATCH or HEAD
  *                   granularity: value = factor * E4M3 value (the form hstu_fwd reads);
  *   row scales      kv_scale [num_pages, 2, Nk, page_size], one unsigned byte s per page,
  *                   plane, head and row, 1 <= s <= 253: value = 2^(s - 127) * E4M3 value.
+ *
+ * 4-bit caches (HSTU_FP4_E2M1) have their heads before the rows, so that the rows of a head lie
+ * next to each other:
+ *   kv_cache [num_pages, 2, Nk, page_size, D / 2]   E2M1 codes, element 2 i in the low four bits
+ *                                                   of byte i (D a multiple of 32)
+ *   kv_group_scale [num_pages, 2, Nk, page_size, D / 16]   one E4M3 factor >= 0 per 16 elements
+ *   kv_scale                                        row scales as above
+ * and value = 2^(s - 127) * factor * code: 4.5 bits an element and a byte a row.
  *
  * Ownership: the caller owns every tensor, workspaces included; no entry point allocates,
  * synchronises or keeps anything between calls, so calls on different streams, and captured
@@ -44,20 +53,23 @@
 extern "C" {
 #endif
 
+/* Type of kv_cache besides hstu_dtype's (of no rows): 4-bit codes. */
+enum { HSTU_FP4_E2M1 = 5 };
+
 /* A cache with its page table. Index arrays are int32 or int64 (index_is_int64), and so are
  * the seq_offsets that come with it. */
 typedef struct {
-  int dtype;             /* hstu_dtype of kv_cache */
+  int dtype;             /* hstu_dtype of kv_cache, or HSTU_FP4_E2M1 */
   int batch;             /* B in [0, 2^20]; 0 = nothing to do */
   int num_heads_kv;      /* Nk in [1, 65536] */
-  int head_dim;          /* D: a multiple of 16 in [16, 256] */
+  int head_dim;          /* D: a multiple of 16 in [16, 256]; E2M1: of 32 */
   int page_size;         /* 32, 128 or 256 */
   int index_is_int64;    /* 0 or 1 */
   int descale;           /* E4M3: hstu_descale_granularity of k_descale and v_descale: CAST
                             (none), TENSOR, BATCH or HEAD; CAST with kv_scale */
   int reserved;          /* must be 0 */
   void* kv_cache;        /* 16-byte aligned */
-  void* kv_scale;        /* E4M3 with row scales, 16-byte aligned, or NULL */
+  void* kv_scale;        /* E2M1, and E4M3 with row scales: 16-byte aligned; or NULL */
   long long num_pages;   /* in [1, 2^30] */
   const void* page_offsets;   /* [B + 1] */
   const void* page_ids;       /* [num_page_ids], each in [0, num_pages) */
@@ -66,6 +78,7 @@ typedef struct {
   const float* k_descale;     /* fp32, 4-byte aligned, non-zero; [1], [B] or [B, Nk] */
   const float* v_descale;
   int* status;                /* device word for what the device finds, or NULL */
+  void* kv_group_scale;       /* E2M1: 16-byte aligned; not looked at for other types */
 } hstu_kv_cache;
 
 /* Rows of k and v: row t of k starts at k + t * k_stride elements and holds [Nk, D]
@@ -78,7 +91,8 @@ typedef struct {
   long long v_stride;
   const void* seq_offsets;
   long long total_tokens; /* rows of k and v; rows of no sequence are left alone */
-  int dtype;              /* HSTU_F32, HSTU_F16 or HSTU_BF16; the cache's, unless that is E4M3 */
+  int dtype;              /* HSTU_F32, HSTU_F16 or HSTU_BF16; the cache's, unless that is E4M3
+                             or E2M1 */
   int reserved;           /* must be 0 */
 } hstu_kv_rows;
 
@@ -88,7 +102,12 @@ typedef struct {
  * finite magnitude of the row's D values is at most 448 * 2^e (-100 for a row of zeros), and
  * the code is x * 2^-e rounded to E4M3; with static factors it is x / factor rounded, and with
  * a plain cast x rounded. Rounding is to nearest even; what lies beyond +-448 (infinities
- * included) becomes +-448, a NaN stays a NaN. No page may belong to two sequences that
+ * included) becomes +-448, a NaN stays a NaN.
+ * Rows of an E2M1 cache: s - 127 is the smallest e >= -100 for which the largest finite magnitude
+ * of the row is at most 2688 * 2^e (-100 for a row of zeros). With y = x * 2^-e, beyond +-2688
+ * (infinities) +-2688, a group's factor is max |y| / 6 rounded to E4M3, and a code y / factor
+ * rounded to E2M1 (both to nearest even; 6 at most; 0 where the factor is 0). A NaN makes its
+ * group's factor a NaN, and so the group's values. No page may belong to two sequences that
  * append to it in one call (the order of their writes is not defined).
  */
 HSTU_API hstu_status hstu_kv_append(const hstu_kv_cache* cache, const hstu_kv_rows* rows,
@@ -98,7 +117,8 @@ HSTU_API hstu_status hstu_kv_append(const hstu_kv_cache* cache, const hstu_kv_ro
  * positions of every sequence, n = its seq_offsets difference (its whole length Lk for the
  * whole sequence). k and v must not overlap. A value beyond the type's range becomes infinite:
  * quantisation may have rounded a row's largest up to 2^16 (fp16, from 63488 on) or 2^128 (bf16
- * and fp32, from 248 * 2^120 on). */
+ * and fp32, from 248 * 2^120 on); that of an E2M1 cache by up to a sixteenth (from 61440, and from
+ * 240 * 2^120 on). */
 HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows* rows,
                                   void* stream);
 
@@ -114,12 +134,12 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * sequence are left alone.
  *
  * Statistics and sums are fp32. fp16 and bf16: the weights are rounded to the type of q for the
- * product with V, or to fp16 over an E4M3 cache (bf16 weights of at most 16 rows of a kv head over
+ * product with V, or to fp16 over an E4M3 or E2M1 cache (bf16 weights of at most 16 rows of a kv head over
  * a bf16 cache, single tokens for instance, come in two parts, whose sum is exact to 2^-16).
- * fp16 holds what is 2^-24 of the largest of the weights, or, over an E4M3 cache, of the weights
- * times their rows' scales. Rows of an E4M3 cache keep their bits whatever the scales of others,
+ * fp16 holds what is 2^-24 of the largest of the weights, or, over such a cache, of the weights
+ * times their rows' scales. Rows of such a cache keep their bits whatever the scales of others,
  * but those of scale 2^-100 or less (rows of zeros) may count as zeros, and their weights with the
- * largest scale of the 127 rows around them. bf16 queries over an E4M3 cache are products of fp16
+ * largest scale of the 127 rows around them. bf16 queries over it are products of fp16
  * with a power of two of their row: elements below 2^-38 of its largest vanish.
  */
 typedef struct {
@@ -128,7 +148,7 @@ typedef struct {
   const void* seq_offsets;/* [B + 1] */
   long long total_tokens; /* T */
   int dtype;              /* of q and out: HSTU_F32, HSTU_F16 or HSTU_BF16; the cache's, or the
-                             cache is E4M3 */
+                             cache is E4M3 or E2M1 */
   int num_heads_q;        /* Nq >= 0, a multiple of Nk, Nq / Nk <= 128 */
   int max_seqlen;         /* bound on n, in [1, 2^24] */
   int max_seqlen_k;       /* bound on Lk, in [1, 2^30] */

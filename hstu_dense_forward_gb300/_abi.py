@@ -14,6 +14,7 @@ LIB_PATH = os.environ.get("HSTU_FWD_LIB") or os.path.join(
     PKG, "libhstu_fwd_trace.so" if os.environ.get("HSTU_FWD_TRACE") == "1" else "libhstu_fwd.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_fwd.h")
 KV_HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_kv.h")
+EVICT_HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_evict.h")
 
 HSTU_OK, HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED, HSTU_ERR_CUDA, HSTU_ERR_TIMEOUT, \
     HSTU_ERR_DEVICE_CHECK = range(6)
@@ -118,6 +119,41 @@ class SoftmaxArgs(ctypes.Structure):
     ]
 
 
+class WeightsArgs(ctypes.Structure):
+    """hstu_weights_args: the queries of one hstu_kv_weights (include/hstu_evict.h)."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong),
+        ("seq_offsets", ctypes.c_void_p), ("total_tokens", ctypes.c_longlong),
+        ("dtype", ctypes.c_int), ("num_heads_q", ctypes.c_int), ("max_seqlen", ctypes.c_int),
+        ("max_seqlen_k", ctypes.c_int), ("causal", ctypes.c_int), ("alpha", ctypes.c_float),
+        ("lse", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("accumulate", ctypes.c_int),
+        ("reserved", ctypes.c_int),
+    ]
+
+
+class SelectArgs(ctypes.Structure):
+    """hstu_select_args: a table with the weights of its rows, and what hstu_kv_select writes."""
+    _fields_ = [
+        ("batch", ctypes.c_int), ("num_heads_kv", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("index_is_int64", ctypes.c_int), ("num_pages", ctypes.c_longlong),
+        ("page_offsets", ctypes.c_void_p), ("page_ids", ctypes.c_void_p),
+        ("last_page_len", ctypes.c_void_p), ("num_page_ids", ctypes.c_longlong),
+        ("weights", ctypes.c_void_p), ("budget", ctypes.c_int), ("recent", ctypes.c_int),
+        ("max_seqlen_k", ctypes.c_int), ("reserved", ctypes.c_int), ("kept", ctypes.c_void_p),
+        ("new_page_offsets", ctypes.c_void_p), ("new_page_ids", ctypes.c_void_p),
+        ("new_last_page_len", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class CompactArgs(ctypes.Structure):
+    """hstu_compact_args: which rows one hstu_kv_compact moves."""
+    _fields_ = [
+        ("kept", ctypes.c_void_p), ("budget", ctypes.c_int), ("max_seqlen_k", ctypes.c_int),
+        ("weights", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_longlong), ("reserved", ctypes.c_int),
+    ]
+
+
 class HstuError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -182,7 +218,10 @@ def lib():
         # the cache operators (HSTU_FWD_LIB may name an older build without them)
         for name, args in (("hstu_kv_append", [vp, vp, vp]), ("hstu_kv_read", [vp, vp, vp]),
                            ("hstu_softmax_fwd", [vp, vp, vp]),
-                           ("hstu_softmax_workspace", [vp, vp, vp])):
+                           ("hstu_softmax_workspace", [vp, vp, vp]),
+                           ("hstu_kv_weights", [vp, vp, vp]), ("hstu_kv_select", [vp, vp]),
+                           ("hstu_compact_workspace", [vp, vp, vp]),
+                           ("hstu_kv_compact", [vp, vp, vp])):
             if hasattr(L, name):
                 getattr(L, name).restype = ctypes.c_int
                 getattr(L, name).argtypes = args

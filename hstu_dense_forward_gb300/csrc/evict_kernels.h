@@ -1,0 +1,54 @@
+// Launch interface between the entry points of eviction (evict_api.cu) and their kernels.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "kv_cache.cuh"
+
+namespace hstu {
+
+// Attention weights of the cached keys: a.q .. a.causal as in the attention.
+struct WeightsParams {
+  SoftmaxParams a;
+  const float* lse;  // [T, Nq]
+  float* weights;    // [num_pages, Nk, page_size]
+  int accumulate;
+};
+
+// Few rows (16-bit; at most `rows`, 8 or 16, of a kv head and sequence); CTAs that an SM holds.
+int weights_rows_ctas(int D, int fmt);
+cudaError_t launch_weights_rows(const WeightsParams& w, int dtype, int fmt, int rows,
+                                cudaStream_t stream);
+
+// More rows, on the tensor cores; `slots` CTAs take turns at the key steps of a sequence and kv head.
+int weights_tc_keys(int D);  // keys of a step
+cudaError_t launch_weights_tc(const WeightsParams& w, int dtype, int fmt, int slots,
+                              cudaStream_t stream);
+
+// fp32 rows, on CUDA cores.
+cudaError_t launch_weights_simt(const WeightsParams& w, int fmt, int slots, cudaStream_t stream);
+constexpr int kWeightsSimtKeys = 64;  // keys of a step
+
+struct SelectParams {
+  CacheView c;  // the table and Nk alone
+  const float* weights;
+  int budget, recent;
+  long long max_k;
+  int* kept;
+  void* new_page_offsets;
+  void* new_page_ids;
+  void* new_last_page_len;
+};
+cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
+
+struct CompactParams {
+  CacheView c;
+  const int* kept;
+  int budget;
+  long long max_k;
+  float* weights;  // or nullptr
+  int row_bytes;   // of a head's row in one plane of the cache
+  int by_head;     // the cache has its heads before the rows (E2M1)
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+}  // namespace hstu

@@ -59,6 +59,20 @@ __device__ __forceinline__ PagedSeq paged_seq(const CacheView& c, long long b) {
   return s;
 }
 
+// The same of a table alone: no rows of the call.
+__device__ __forceinline__ PagedSeq paged_table(const CacheView& c, long long b) {
+  PagedSeq s;
+  s.t0 = s.n = 0;
+  s.po = load_index(c.page_offsets, b, c.index64);
+  const long long pe = load_index(c.page_offsets, b + 1, c.index64);
+  const long long last = load_index(c.last_page_len, b, c.index64);
+  s.pages = pe - s.po;
+  s.ok = s.po >= 0 && s.pages >= 0 && pe <= c.num_page_ids &&
+         (s.pages == 0 || (last >= 1 && last <= page_size(c)));
+  s.Lk = s.ok && s.pages > 0 ? ((s.pages - 1) << c.page_shift) + last : 0;
+  return s;
+}
+
 // Page that holds position pos of a valid sequence (pos < Lk), or -1 if its id is outside
 // the cache.
 __device__ __forceinline__ long long page_at(const CacheView& c, const PagedSeq& s,

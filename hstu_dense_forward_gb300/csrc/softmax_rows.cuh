@@ -54,10 +54,11 @@ constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNoKey = -1e38f;  // E4M3: reference of a row that has seen no key
 
-template <int D_, int NT_, bool BF16_, int FMT_>
+// PLANES: of the cache that the kernel reads (both, or the keys alone).
+template <int D_, int NT_, bool BF16_, int FMT_, int PLANES_ = 2>
 struct Cfg {
   static constexpr int D = D_, NT = NT_, RT = 8 * NT;      // packed query rows of one CTA
-  static constexpr int FMT = FMT_;
+  static constexpr int FMT = FMT_, PLANES = PLANES_;
   static constexpr bool BF16 = BF16_, CODES = FMT != kSame, FP4 = FMT == kE2m1;
   static constexpr bool MMA_BF16 = BF16 && !CODES;
   static constexpr int RB = FP4 ? D / 2 : CODES ? D : 2 * D;  // bytes of a key's row
@@ -71,20 +72,27 @@ struct Cfg {
   static constexpr int KS = D / 16;                        // k-steps of the scores
   static constexpr int NV = BE / 8;                        // output columns per lane and block
   static constexpr int CW = KT / 16, THREADS = (CW + 1) * 32;
-  static constexpr int PLANE = KT * RB, STAGE = 2 * PLANE;
+  static constexpr int PLANE = KT * RB, STAGE = PLANES * PLANE;
   // CTAs per SM: what their registers (O and Q) and a ring of at least three stages leave. E4M3
   // spends more instructions per byte and needs the warps of a third CTA.
-  static constexpr int CTAS = D == 256 ? (CODES && NT == 1 ? 2 : 1) : (CODES && NT == 1 ? 3 : 2);
-  static constexpr int RING = CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : FP4 ? 57344 : 65536;
+  static constexpr int CTAS = PLANES == 1 ? (RB == 512 ? 2 : D == 256 ? 3 : 4)
+                              : D == 256  ? (CODES && NT == 1 ? 2 : 1)
+                                          : (CODES && NT == 1 ? 3 : 2);
+  static constexpr int RING = CTAS == 1   ? 196608
+                              : CTAS == 2 ? 98304
+                              : CTAS == 4 ? (FP4 ? 45056 : 49152)
+                              : FP4       ? 57344
+                                          : 65536;
   static constexpr int NST = RING / STAGE < 12 ? RING / STAGE : 12;
-  static constexpr int OFF_SC = NST * STAGE;               // row scales: 2 KT bytes a stage
+  static constexpr int OFF_SC = NST * STAGE;               // row scales: KT bytes a plane and stage
   static constexpr int GPLANE = KT * (D / 16);             // E2M1: factors of a plane's tile
-  static constexpr int OFF_GR = OFF_SC + (CODES ? NST * 2 * KT : 0);
-  static constexpr int OFF_ML = OFF_GR + (FP4 ? NST * 2 * GPLANE : 0);
-  static constexpr int OFF_BAR = OFF_ML + (CODES ? 3 : 2) * (CW + 1) * RT * 4;
+  static constexpr int OFF_GR = OFF_SC + (CODES ? NST * PLANES * KT : 0);
+  static constexpr int OFF_ML = OFF_GR + (FP4 ? NST * PLANES * GPLANE : 0);
+  static constexpr int OFF_BAR =
+      OFF_ML + (PLANES == 1 ? 0 : (CODES ? 3 : 2) * (CW + 1) * RT * 4);
   static constexpr int USED = OFF_BAR + 256 + 1024;
   static_assert(NST >= 3 && NST <= 12, "ring");
-  static_assert(CW * RT * D * 4 <= NST * STAGE, "the joined outputs reuse the ring");
+  static_assert(PLANES == 1 || CW * RT * D * 4 <= NST * STAGE, "the joined outputs reuse the ring");
   static_assert(USED <= 232448 / CTAS - 1024, "shared memory");
 };
 
@@ -231,13 +239,14 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
     const uint32_t bar = ptx::smem_u32(&bars->full[st]);
     const bool scales = C::CODES && p.c.scale;
     const int gb = p.c.D / 16;  // E2M1: factors of a row
-    ptx::mbar_arrive_expect_tx(bar, C::STAGE + (scales ? 2 * KT : 0) + (C::FP4 ? 2 * KT * gb : 0));
+    ptx::mbar_arrive_expect_tx(
+        bar, C::STAGE + (scales ? C::PLANES * KT : 0) + (C::FP4 ? C::PLANES * KT * gb : 0));
     const int row0 = ps >= KT ? (int)(n0 & (ps - 1)) : 0;
 #pragma unroll
     for (int m = 0; m < KT / 32; ++m) {
       if (m >= boxes) break;
 #pragma unroll
-      for (int plane = 0; plane < 2; ++plane) {
+      for (int plane = 0; plane < C::PLANES; ++plane) {
 #pragma unroll
         for (int cb = 0; cb < C::NCB; ++cb) {
           const uint32_t dst =
@@ -248,14 +257,207 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
             ptx::tma_load_4d(dst, tc, bar, cb * C::BE, it.hk, row0, (int)(2 * page[m]) + plane);
         }
         if constexpr (C::FP4)
-          ptx::bulk_load(sbase + C::OFF_GR + (2 * st + plane) * C::GPLANE + m * 32 * gb,
+          ptx::bulk_load(sbase + C::OFF_GR + (C::PLANES * st + plane) * C::GPLANE + m * 32 * gb,
                          p.c.group + scale_row(p.c, page[m], plane, row0, it.hk) * gb, brows * gb,
                          bar);
         if (scales)
-          ptx::bulk_load(sbase + C::OFF_SC + st * 2 * KT + plane * KT + m * 32,
+          ptx::bulk_load(sbase + C::OFF_SC + (C::PLANES * st + plane) * KT + m * 32,
                          p.c.scale + scale_row(p.c, page[m], plane, row0, it.hk), brows, bar);
       }
     }
+  }
+}
+
+// What a warp holds of the item's query rows. Lane (g, c): the products' fragments of rows g of
+// each row tile, in the scores' order of the head dim (of block cb, lane c's elements in fours, two
+// registers each), and of rows 2c and 2c + 1
+template <class C>
+struct Queries {
+  uint32_t qb[C::NT][C::KS][2];
+  float fr[C::NT][2];  // the score's factor
+  int lim[C::NT][2];   // keys that they see, counted from this CTA's first (maybe < 0)
+  int see;             // fewest of them
+};
+
+template <class C>
+__device__ __forceinline__ void load_queries(const SoftmaxParams& p, const Item& it, int keys,
+                                             int g, int c, Queries<C>& qs) {
+  using T16 = typename std::conditional<C::BF16, __nv_bfloat16, __half>::type;
+  float fk = p.scale_log2;
+  if (C::CODES && p.c.k_ds)
+    fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
+  auto& qb = qs.qb;
+  qs.see = keys;
+#pragma unroll
+  for (int i = 0; i < C::NT; ++i) {
+    const long long pr = it.m0 + 8 * i + g;
+    const bool real = pr < it.rows;
+    const long long tok = real ? pr / p.G : 0;
+    const T16* q = static_cast<const T16*>(p.q) + (it.s.t0 + tok) * p.q_stride +
+                   (it.hk * p.G + (real ? pr % p.G : 0)) * (long long)p.c.D;
+    uint32_t top = 0;  // largest magnitude of the row, as 16-bit patterns
+#pragma unroll
+    for (int cb = 0; cb < C::NCB; ++cb)
+#pragma unroll
+      for (int x = 0; x < C::LE / 8; ++x) {
+        const int e0 = cb * C::BE + c * C::LE + 8 * x;
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (real && e0 < p.c.D) u = *reinterpret_cast<const uint4*>(q + e0);
+        const int k = (cb * C::LE + 8 * x) / 4;
+        qb[i][k][0] = u.x;
+        qb[i][k][1] = u.y;
+        qb[i][k + 1][0] = u.z;
+        qb[i][k + 1][1] = u.w;
+        if constexpr (C::CODES && C::BF16) {
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+      }
+    float f = fk;
+    if constexpr (C::CODES && C::BF16) {  // the row as fp16, times 2^(14 - exponent of its largest)
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int sh = min(14 - ((int)(top >> 7) - 127), 126);
+      const float mul = __uint_as_float((uint32_t)(sh + 127) << 23);
+      f = fk * __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+      for (int k = 0; k < C::KS; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t w = qb[i][k][x];
+          qb[i][k][x] = pack2<false>(__uint_as_float(w << 16) * mul,
+                                     __uint_as_float(w & 0xffff0000u) * mul);
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      qs.fr[i][y] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + y));
+      const long long row = it.m0 + 8 * i + 2 * c + y;
+      qs.lim[i][y] = keys;
+      if (p.causal && row < it.rows)
+        qs.lim[i][y] = (int)min((long long)keys, it.s.Lk - it.s.n + row / p.G + 1 - it.k0);
+      qs.see = min(qs.see, qs.lim[i][y]);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) qs.see = min(qs.see, __shfl_xor_sync(0xffffffffu, qs.see, d));
+}
+
+// Scores of a tile's keys r16 .. r16 + 15 in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y. ev:
+// exponents of V's row scales (unless they are 0).
+template <class C>
+__device__ __forceinline__ void tile_scores(const SoftmaxParams& p, const uint8_t* smem, int st,
+                                            int r16, int g, int c, const Queries<C>& qs,
+                                            float (&sc)[C::NT][4], float (&ev)[2]) {
+  constexpr int NT = C::NT;
+  const uint8_t* kt = smem + st * C::STAGE;
+  // two sums per score, of alternate k-steps: a product's latency is some 35 cycles, and
+  // each waits for the one before it in its sum
+  float sd[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sc[i][e] = sd[i][e] = 0.f;
+  if constexpr (C::FP4) {
+    const int gb = p.c.D / 16, r0 = r16 + g;
+    const uint8_t* gp = smem + C::OFF_GR + C::PLANES * st * C::GPLANE + r0 * gb;
+    constexpr int LU = C::LE / 16;  // groups of sixteen elements that the lane holds
+    uint32_t w[2][2 * LU];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      if constexpr (LU == 1) {
+        const uint2 u = *reinterpret_cast<const uint2*>(kt + (r0 + 8 * y) * C::SWB + c * 8);
+        w[y][0] = u.x;
+        w[y][1] = u.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < LU / 2; ++j) {
+          const uint4 u = *reinterpret_cast<const uint4*>(
+              kt + piece_at<C::SWB>(r0 + 8 * y, c * (LU / 2) + j));
+          w[y][4 * j] = u.x;
+          w[y][4 * j + 1] = u.y;
+          w[y][4 * j + 2] = u.z;
+          w[y][4 * j + 3] = u.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < LU; ++u) {
+      uint32_t f[2] = {0u, 0u};  // (behind the head dim another row's, or nothing)
+      if (c * LU + u < gb) {
+        f[0] = group_pair(gp[c * LU + u], gp[c * LU + u]);
+        f[1] = group_pair(gp[8 * gb + c * LU + u], gp[8 * gb + c * LU + u]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t h[2][4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          e2m1x8_to_f16x2(w[y][2 * u + x], h[y]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[y][e] = mul_f16x2(h[y][e], f[y]);
+        }
+        const int k = 4 * u + 2 * x;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          mma<false>(sc[i], h[0][0], h[1][0], h[0][1], h[1][1], qs.qb[i][k][0], qs.qb[i][k][1]);
+          mma<false>(sd[i], h[0][2], h[1][2], h[0][3], h[1][3], qs.qb[i][k + 1][0],
+                     qs.qb[i][k + 1][1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int cb = 0; cb < (C::FP4 ? 0 : C::NCB); ++cb)
+#pragma unroll
+    for (int j = 0; j < C::LPC; ++j) {
+      const uint4 u0 = *reinterpret_cast<const uint4*>(
+          kt + cb * C::CB + piece_at<C::SWB>(r16 + g, c * C::LPC + j));
+      const uint4 u1 = *reinterpret_cast<const uint4*>(
+          kt + cb * C::CB + piece_at<C::SWB>(r16 + 8 + g, c * C::LPC + j));
+      const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+      const int k = (cb * C::LPC + j) * C::EPP / 4;
+      if constexpr (C::CODES) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2(w0[e], a0, a2);
+          e4m3x4_to_f16x2(w1[e], a1, a3);
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+            mma<false>(e & 1 ? sd[i] : sc[i], a0, a1, a2, a3, qs.qb[i][k + e][0],
+                       qs.qb[i][k + e][1]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          mma<C::MMA_BF16>(sc[i], w0[0], w1[0], w0[1], w1[1], qs.qb[i][k][0], qs.qb[i][k][1]);
+          mma<C::MMA_BF16>(sd[i], w0[2], w1[2], w0[3], w1[3], qs.qb[i][k + 1][0],
+                           qs.qb[i][k + 1][1]);
+        }
+      }
+    }
+  // scores in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y
+  if (C::CODES && p.c.scale) {
+    const uint8_t* sp = smem + C::OFF_SC + st * C::PLANES * KT + r16 + g;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float f = scale_value(sp[8 * x]);
+      if (C::PLANES == 2) ev[x] = (float)((int)sp[KT + 8 * x] - 127);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          // (the factors first: their product is in range where the score is)
+          sc[i][2 * x + y] = (sc[i][2 * x + y] + sd[i][2 * x + y]) * (f * qs.fr[i][y]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[i][e] = (sc[i][e] + sd[i][e]) * qs.fr[i][e & 1];
   }
 }
 
@@ -310,71 +512,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
   if (warp == C::CW) {
     if (lane == 0) load_role<C>(p, bars, smem, it, n, &tm_c);
   } else {
-    float fk = p.scale_log2;
-    if (CODES && p.c.k_ds)
-      fk *= p.c.k_ds[(long long)it.b * p.c.ds_b + (long long)it.hk * p.c.ds_h];
     const int keys = (int)(it.kend - it.k0);
-    // Q fragments in the scores' order of the head dim: of piece j of block cb, lane c's
-    // elements in fours, two registers each (rows g)
-    uint32_t qb[NT][C::KS][2];
-    float fr[NT][2];  // score factor of rows 2c and 2c + 1
-    int lim[NT][2];   // keys that they see, counted from this CTA's first (maybe < 0)
-    int see = keys;   // fewest of them
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const long long pr = it.m0 + 8 * i + g;
-      const bool real = pr < it.rows;
-      const long long tok = real ? pr / p.G : 0;
-      const T16* q = static_cast<const T16*>(p.q) + (it.s.t0 + tok) * p.q_stride +
-                     (it.hk * p.G + (real ? pr % p.G : 0)) * (long long)p.c.D;
-      uint32_t top = 0;  // largest magnitude of the row, as 16-bit patterns
-#pragma unroll
-      for (int cb = 0; cb < C::NCB; ++cb)
-#pragma unroll
-        for (int x = 0; x < C::LE / 8; ++x) {
-          const int e0 = cb * C::BE + c * C::LE + 8 * x;
-          uint4 u = make_uint4(0u, 0u, 0u, 0u);
-          if (real && e0 < p.c.D) u = *reinterpret_cast<const uint4*>(q + e0);
-          const int k = (cb * C::LE + 8 * x) / 4;
-          qb[i][k][0] = u.x;
-          qb[i][k][1] = u.y;
-          qb[i][k + 1][0] = u.z;
-          qb[i][k + 1][1] = u.w;
-          if constexpr (CODES && BF16) {
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-          }
-        }
-      float f = fk;
-      if constexpr (CODES && BF16) {  // the row as fp16, times 2^(14 - exponent of its largest)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int sh = min(14 - ((int)(top >> 7) - 127), 126);
-        const float mul = __uint_as_float((uint32_t)(sh + 127) << 23);
-        f = fk * __uint_as_float((uint32_t)(127 - sh) << 23);
-#pragma unroll
-        for (int k = 0; k < C::KS; ++k)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t w = qb[i][k][x];
-            qb[i][k][x] = pack2<false>(__uint_as_float(w << 16) * mul,
-                                       __uint_as_float(w & 0xffff0000u) * mul);
-          }
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        fr[i][y] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + y));
-        const long long row = it.m0 + 8 * i + 2 * c + y;
-        lim[i][y] = keys;
-        if (p.causal && row < it.rows)
-          lim[i][y] = (int)min((long long)keys, it.s.Lk - it.s.n + row / p.G + 1 - it.k0);
-        see = min(see, lim[i][y]);
-      }
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) see = min(see, __shfl_xor_sync(0xffffffffu, see, d));
+    Queries<C> qs;
+    load_queries<C>(p, it, keys, g, c, qs);
+    auto& lim = qs.lim;
+    const int see = qs.see;
 
     for (int t = 0; t < n; ++t) {
       const int st = t % C::NST;
@@ -383,113 +525,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
       const int left = keys - at;         // of them, keys of this CTA
       if (left > 0) {
         const uint8_t* kt = smem + st * C::STAGE;
-        // two sums per score, of alternate k-steps: a product's latency is some 35 cycles, and
-        // each waits for the one before it in its sum
-        float sc[NT][4], sd[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[i][e] = sd[i][e] = 0.f;
-        if constexpr (C::FP4) {
-          const int gb = p.c.D / 16, r0 = warp * 16 + g;
-          const uint8_t* gp = smem + C::OFF_GR + 2 * st * C::GPLANE + r0 * gb;
-          constexpr int LU = C::LE / 16;  // groups of sixteen elements that the lane holds
-          uint32_t w[2][2 * LU];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if constexpr (LU == 1) {
-              const uint2 u = *reinterpret_cast<const uint2*>(kt + (r0 + 8 * y) * C::SWB + c * 8);
-              w[y][0] = u.x;
-              w[y][1] = u.y;
-            } else {
-#pragma unroll
-              for (int j = 0; j < LU / 2; ++j) {
-                const uint4 u = *reinterpret_cast<const uint4*>(
-                    kt + piece_at<C::SWB>(r0 + 8 * y, c * (LU / 2) + j));
-                w[y][4 * j] = u.x;
-                w[y][4 * j + 1] = u.y;
-                w[y][4 * j + 2] = u.z;
-                w[y][4 * j + 3] = u.w;
-              }
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < LU; ++u) {
-            uint32_t f[2] = {0u, 0u};  // (behind the head dim another row's, or nothing)
-            if (c * LU + u < gb) {
-              f[0] = group_pair(gp[c * LU + u], gp[c * LU + u]);
-              f[1] = group_pair(gp[8 * gb + c * LU + u], gp[8 * gb + c * LU + u]);
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t h[2][4];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                e2m1x8_to_f16x2(w[y][2 * u + x], h[y]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[y][e] = mul_f16x2(h[y][e], f[y]);
-              }
-              const int k = 4 * u + 2 * x;
-#pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                mma<false>(sc[i], h[0][0], h[1][0], h[0][1], h[1][1], qb[i][k][0], qb[i][k][1]);
-                mma<false>(sd[i], h[0][2], h[1][2], h[0][3], h[1][3], qb[i][k + 1][0],
-                           qb[i][k + 1][1]);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int cb = 0; cb < (C::FP4 ? 0 : C::NCB); ++cb)
-#pragma unroll
-          for (int j = 0; j < C::LPC; ++j) {
-            const uint4 u0 = *reinterpret_cast<const uint4*>(
-                kt + cb * C::CB + piece_at<C::SWB>(warp * 16 + g, c * C::LPC + j));
-            const uint4 u1 = *reinterpret_cast<const uint4*>(
-                kt + cb * C::CB + piece_at<C::SWB>(warp * 16 + 8 + g, c * C::LPC + j));
-            const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-            const int k = (cb * C::LPC + j) * C::EPP / 4;
-            if constexpr (CODES) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16x2(w0[e], a0, a2);
-                e4m3x4_to_f16x2(w1[e], a1, a3);
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                  mma<false>(e & 1 ? sd[i] : sc[i], a0, a1, a2, a3, qb[i][k + e][0],
-                             qb[i][k + e][1]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                mma<C::MMA_BF16>(sc[i], w0[0], w1[0], w0[1], w1[1], qb[i][k][0], qb[i][k][1]);
-                mma<C::MMA_BF16>(sd[i], w0[2], w1[2], w0[3], w1[3], qb[i][k + 1][0],
-                                 qb[i][k + 1][1]);
-              }
-            }
-          }
-        // scores in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y
-        float ev[2] = {0.f, 0.f};  // exponents of V's row scales (of a key beyond the last, any)
-        if (CODES && p.c.scale) {
-          const uint8_t* sp = smem + C::OFF_SC + st * 2 * KT + warp * 16 + g;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float f = scale_value(sp[8 * x]);
-            ev[x] = (float)((int)sp[KT + 8 * x] - 127);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int y = 0; y < 2; ++y)
-                // (the factors first: their product is in range where the score is)
-                sc[i][2 * x + y] = (sc[i][2 * x + y] + sd[i][2 * x + y]) * (f * fr[i][y]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[i][e] = (sc[i][e] + sd[i][e]) * fr[i][e & 1];
-        }
+        float sc[NT][4], ev[2] = {0.f, 0.f};  // exponents of V's row scales (of a key beyond the last, any)
+        tile_scores<C>(p, smem, st, warp * 16, g, c, qs, sc, ev);
         if (at + 16 > see) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {

@@ -1,0 +1,13 @@
+// Attention weights of the cached keys from few bf16 query rows.
+#include "weights_rows.cuh"
+
+namespace hstu {
+
+cudaError_t launch_weights_rows_bf16(const WeightsParams& w, int fmt, const CUtensorMap& tc, int rows,
+                                   cudaStream_t s) {
+  return fmt == kE4m3   ? rows::launch_weights_fmt<true, kE4m3>(w, tc, rows, s)
+         : fmt == kE2m1 ? rows::launch_weights_fmt<true, kE2m1>(w, tc, rows, s)
+                        : rows::launch_weights_fmt<true, kSame>(w, tc, rows, s);
+}
+
+}  // namespace hstu

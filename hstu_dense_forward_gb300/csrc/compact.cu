@@ -1,115 +1,170 @@
 // Moving the kept rows of a paged cache together, in place (hstu_kv_compact).
 //
-// Positions increase in the list of kept rows, so that rank r never lies behind its source: a CTA per
-// (sequence, kv head) takes the ranks in order, some at a time, whose rows it holds in registers
-// between its loads and its stores.
+// Rank r of a (sequence, kv head) takes the row at position kept[r] >= r. Ranks are moved in chunks,
+// each by a CTA that holds the chunk's rows in registers between its loads and its stores. Positions
+// increase with the ranks, so that what a chunk overwrites can be a source of that chunk and of those
+// in front of it only: it stores once those have loaded. Chunks are handed out by a counter, in order
+// for every (sequence, kv head), and load without waiting for anything, so that a chunk waits for
+// loads alone that are under way. (One CTA for all of a (sequence, kv head), chunk after chunk: 128
+// of 4096 ranks of 256-byte rows took 312 us, one of 50,000 3355.) Bound by memory: a kept row is read
+// once and written once.
 #include "common.cuh"
 #include "evict_kernels.h"
 #include "kernels.h"
 #include "kv_cache.cuh"
+#include "ptx.cuh"
 
 namespace hstu {
 
 namespace {
 
 constexpr int kThreads = 256, kPieces = 8;  // 16-byte pieces that a thread holds
-constexpr int kMaxRows = 256;               // ranks of a round
+constexpr int kCtas = 4;                    // of an SM
 
-// Rows of one head in plane 0 (the other lies `plane` rows further on).
+// A row of one head in plane 0: its first 16-byte piece in the cache, and the row among those of what
+// has its heads before the rows (the other plane lies a plane further on).
 struct Move {
-  long long from, to;        // rows of the cache, -1: nothing to move
-  long long sfrom, sto;      // of the scales
+  long long from, to;  // -1: nothing to move
+  long long sfrom, sto;
 };
 
-__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p, int rows) {
-  __shared__ Move moves[kMaxRows];
-  __shared__ int s_any;
-  const int hk = (int)(blockIdx.x % (unsigned)p.c.Nk), b = (int)(blockIdx.x / (unsigned)p.c.Nk);
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int x;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+__device__ __forceinline__ void store_release(int* p, int x) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, kCtas)
+    compact_kernel(const CompactParams p, int rows, int chunks, int lanes_shift) {
+  __shared__ Move moves[kCompactRows];
+  __shared__ int s_ticket, s_any, s_wait, s_late, s_before[4];
   const int tid = threadIdx.x;
-  const PagedSeq s = paged_table(p.c, b);
-  if (!s.ok || s.Lk > p.max_k) {
-    if (tid == 0) report(p.c, HSTU_DEVERR_OFFSETS);
-    return;
-  }
-  const int* kept = p.kept + ((long long)b * p.c.Nk + hk) * p.budget;
-  const int most = (int)min(s.Lk, (long long)p.budget);
-  const int pieces = p.row_bytes / 16, gb = p.c.D / 16;
+  const int pieces = p.row_bytes / 16;
   const long long plane = (long long)p.c.Nk << p.c.page_shift;  // rows of a plane
-  auto row_of = [&](long long page, long long pos, bool by_head) {
-    const long long row = pos & (page_size(p.c) - 1);
-    return by_head ? scale_row(p.c, page, 0, row, hk)
-                   : (((page * 2) << p.c.page_shift) + row) * p.c.Nk + hk;
+  const unsigned pairs = (unsigned)p.c.B * p.c.Nk;
+  const long long tickets = (long long)pairs * chunks;
+  uint4* cache = static_cast<uint4*>(p.c.cache);
+  // (a row among those with heads before rows, without the planes: the weights' place)
+  auto weight_at = [&](long long srow) {
+    const long long page = srow / (2 * plane);
+    return srow - page * plane;
   };
-  for (int r0 = 0; r0 < most; r0 += rows) {
-    const int n = min(rows, most - r0);
-    __syncthreads();  // the stores of the round before are done with `moves`
-    if (tid == 0) s_any = 0;
-    __syncthreads();
-    if (tid < n) {
-      const int r = r0 + tid, src = kept[r];
-      Move m = {-1, -1, -1, -1};
-      if (src > r && src < s.Lk) {
-        const long long a = page_at(p.c, s, src), d = page_at(p.c, s, r);
-        if (a >= 0 && d >= 0) {
-          m.from = row_of(a, src, p.by_head);
-          m.to = row_of(d, r, p.by_head);
-          m.sfrom = row_of(a, src, true);
-          m.sto = row_of(d, r, true);
-          s_any = 1;
-        } else {
-          report(p.c, HSTU_DEVERR_OFFSETS);
-        }
-      } else if (src >= 0 && src != r) {
-        report(p.c, HSTU_DEVERR_OFFSETS);
-      }
-      moves[tid] = m;
+  // 2^lanes_shift lanes take the pieces of a row, of plane 0 and then of plane 1: of each round's
+  // rows, this thread one piece. An E2M1 row has as many 16-bit pieces of factors.
+  const int y = tid & ((1 << lanes_shift) - 1), step = kThreads >> lanes_shift;
+  const int row0 = y < 2 * pieces ? tid >> lanes_shift : kCompactRows;  // (a lane too many: no row)
+  const long long off = y >= pieces ? plane * pieces + y - pieces : y;
+  uint16_t* factors = reinterpret_cast<uint16_t*>(p.c.group);
+  // (one chunk each: they are not handed out, and none waits)
+  if (tid == 0) s_ticket = chunks > 1 ? atomicAdd(p.counter, 1) : (int)blockIdx.x;
+  __syncthreads();
+  for (;;) {
+    const unsigned ticket = (unsigned)s_ticket;
+    if ((long long)ticket >= tickets) return;
+    const int chunk = (int)(ticket / pairs), pair = (int)(ticket % pairs);
+    const int hk = pair % p.c.Nk, b = pair / p.c.Nk;
+    const PagedSeq s = paged_table(p.c, b);
+    const bool ok = s.ok && s.Lk <= p.max_k;
+    const int* kept = p.kept + ((long long)b * p.c.Nk + hk) * p.budget;
+    const int most = ok ? (int)min(s.Lk, (long long)p.budget) : 0;
+    const int r0 = chunk * rows, n = max(0, min(rows, most - r0));
+    int* loaded = p.loaded + (long long)pair * chunks;  // chunks that have loaded
+    if (!ok && chunk == 0 && hk == 0 && tid == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+    __syncthreads();  // everyone has the ticket, and the chunk before is done with `moves`
+    if (tid == 0) {
+      // (its latency passes meanwhile)
+      s_ticket = chunks > 1 ? atomicAdd(p.counter, 1) : (int)(ticket + gridDim.x);
+      s_any = s_wait = s_late = 0;
     }
     __syncthreads();
-    if (!s_any) continue;
-    const int all = n * 2 * pieces;  // at most kThreads * kPieces
-    uint4* cache = static_cast<uint4*>(p.c.cache);
+    if (n > 0) {
+      for (int x = tid; x < n; x += kThreads) {
+        const int r = r0 + x, src = kept[r];
+        Move m = {-1, -1, -1, -1};
+        if (src > r && src < s.Lk) {
+          const long long a = page_at(p.c, s, src), d = page_at(p.c, s, r);
+          if (a >= 0 && d >= 0) {
+            const long long mask = page_size(p.c) - 1;
+            m.sfrom = scale_row(p.c, a, 0, src & mask, hk);
+            m.sto = scale_row(p.c, d, 0, r & mask, hk);
+            m.from = p.by_head ? m.sfrom
+                               : (((a * 2) << p.c.page_shift) + (src & mask)) * p.c.Nk + hk;
+            m.to = p.by_head ? m.sto : (((d * 2) << p.c.page_shift) + (r & mask)) * p.c.Nk + hk;
+            m.from *= pieces;
+            m.to *= pieces;
+            s_any = 1;
+          } else {
+            report(p.c, HSTU_DEVERR_OFFSETS);
+          }
+        } else if (src >= 0 && src != r) {
+          report(p.c, HSTU_DEVERR_OFFSETS);
+        }
+        moves[x] = m;
+      }
+      // chunks in front with sources among positions [r0, r0 + n): two at most
+      for (int c = tid; c < chunk; c += kThreads) {
+        const int first = kept[c * rows], last = kept[c * rows + rows - 1];
+        if (first >= 0 && first < r0 + n && (last >= r0 || last < 0)) {
+          const int i = atomicAdd(&s_wait, 1);
+          if (i < 4) s_before[i] = c;
+        }
+      }
+      __syncthreads();
+    }
     uint4 u[kPieces];
     uint16_t group[kPieces];
     uint8_t scale[2];
     float weight = 0.f;
+    const bool mine = tid < n && moves[tid].from >= 0;
+    const bool any = n > 0 && s_any;
+    if (any) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int x = i * kThreads + tid, r = x / (2 * pieces), y = x % (2 * pieces);
-      if (x < all && moves[r].from >= 0)
-        u[i] = cache[(moves[r].from + (y >= pieces ? plane : 0)) * pieces + y % pieces];
-      if (p.c.group) {
-        const int gr = x / gb, gy = x % gb;  // pairs of factors, of both planes
-        if (gr < n && moves[gr].from >= 0)
-          group[i] = reinterpret_cast<const uint16_t*>(
-              p.c.group)[(moves[gr].sfrom + (gy >= gb / 2 ? plane : 0)) * (gb / 2) + gy % (gb / 2)];
+      for (int i = 0; i < kPieces; ++i) {
+        const int r = row0 + i * step;
+        if (r < n && moves[r].from >= 0) {
+          u[i] = cache[moves[r].from + off];
+          if (factors) group[i] = factors[moves[r].from + off];
+        }
+      }
+      if (mine) {
+        if (p.c.scale) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) scale[i] = p.c.scale[moves[tid].sfrom + i * plane];
+        }
+        if (p.weights) weight = p.weights[weight_at(moves[tid].sfrom)];
       }
     }
-    if (p.c.scale) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (tid < n && moves[tid].from >= 0) scale[i] = p.c.scale[moves[tid].sfrom + i * plane];
-    }
-    // (a scale row of plane 0 lies in page 2 * page: half of it is the weights' place)
-    auto weight_at = [&](long long srow) {
-      const long long page = srow / (2 * plane);
-      return page * plane + (srow - page * 2 * plane);
-    };
-    if (p.weights && tid < n && moves[tid].from >= 0) weight = p.weights[weight_at(moves[tid].sfrom)];
-    __syncthreads();  // every row of the round is in registers
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int x = i * kThreads + tid, r = x / (2 * pieces), y = x % (2 * pieces);
-      if (x < all && moves[r].from >= 0)
-        cache[(moves[r].to + (y >= pieces ? plane : 0)) * pieces + y % pieces] = u[i];
-      if (p.c.group) {
-        const int gr = x / gb, gy = x % gb;
-        if (gr < n && moves[gr].from >= 0)
-          reinterpret_cast<uint16_t*>(
-              p.c.group)[(moves[gr].sto + (gy >= gb / 2 ? plane : 0)) * (gb / 2) + gy % (gb / 2)] =
-              group[i];
+    __syncthreads();  // every row of the chunk is in registers
+    if (n > 0 && tid == 0 && chunks > 1) store_release(loaded + chunk, 1);
+    if (!any) continue;
+    // (a list that does not increase may name more chunks; it is not waited for)
+    if (tid < min(s_wait, 4)) {
+      const int* flag = loaded + s_before[tid];
+      if (!load_acquire(flag)) {
+        const uint64_t start = ptx::globaltimer_ns();
+        while (!load_acquire(flag)) {
+          if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
+            s_late = 1;
+            report(p.c, HSTU_DEVERR_TIMEOUT);
+            break;
+          }
+        }
       }
     }
-    if (tid < n && moves[tid].from >= 0) {
+    __syncthreads();
+    if (s_late) continue;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = row0 + i * step;
+      if (r < n && moves[r].from >= 0) {
+        cache[moves[r].to + off] = u[i];
+        if (factors) factors[moves[r].to + off] = group[i];
+      }
+    }
+    if (mine) {
       if (p.c.scale) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) p.c.scale[moves[tid].sto + i * plane] = scale[i];
@@ -121,12 +176,29 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
 
 }  // namespace
 
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  // as many rows as the registers hold, of both planes (the factors of an E2M1 row are an eighth
-  // of it, a 16-bit piece of them for each of its own)
-  int rows = kThreads * kPieces / (2 * (p.row_bytes / 16));
-  if (rows > kMaxRows) rows = kMaxRows;
-  compact_kernel<<<(unsigned)((long long)p.c.B * p.c.Nk), kThreads, 0, stream>>>(p, rows);
+namespace {
+int lanes_shift(int row_bytes) {
+  int s = 0;
+  while ((1 << s) < 2 * (row_bytes / 16)) ++s;
+  return s;
+}
+}  // namespace
+
+int compact_rows(int row_bytes) {
+  // as many rows of both planes as the registers hold
+  const int rows = kThreads * kPieces >> lanes_shift(row_bytes);
+  return rows < kCompactRows ? rows : kCompactRows;
+}
+
+cudaError_t launch_compact(const CompactParams& p, int chunks, int sms, cudaStream_t stream) {
+  const long long tickets = (long long)p.c.B * p.c.Nk * chunks;
+  if (chunks > 1) {
+    const cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(int) * (4 + tickets), stream);
+    if (e != cudaSuccess) return e;
+  }
+  const long long most = (long long)kCtas * sms;
+  compact_kernel<<<(unsigned)(tickets < most ? tickets : most), kThreads, 0, stream>>>(
+      p, compact_rows(p.row_bytes), chunks, lanes_shift(p.row_bytes));
   return cudaGetLastError();
 }
 

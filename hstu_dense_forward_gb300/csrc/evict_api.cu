@@ -13,6 +13,20 @@ namespace {
 
 bool bad_bound(int x) { return x < 1 || x > (1 << 30); }
 
+int row_bytes(const hstu_kv_cache* c) {
+  const int fmt = cache_format(c->dtype);
+  return fmt == kE2m1   ? c->head_dim / 2
+         : fmt == kE4m3 ? c->head_dim
+                        : c->head_dim * elem_bytes(c->dtype);
+}
+
+// Chunks of the ranks of a sequence and kv head.
+long long compact_chunks(const hstu_kv_cache* c, const hstu_compact_args* a) {
+  const long long ranks = a->budget < a->max_seqlen_k ? a->budget : a->max_seqlen_k;
+  const int rows = compact_rows(row_bytes(c));
+  return (ranks + rows - 1) / rows;
+}
+
 }  // namespace
 
 extern "C" {
@@ -127,8 +141,10 @@ hstu_status hstu_kv_select(const hstu_select_args* a, void* stream) {
   p.new_page_offsets = a->new_page_offsets;
   p.new_page_ids = a->new_page_ids;
   p.new_last_page_len = a->new_last_page_len;
-  return launch_select(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HSTU_OK
-                                                                            : HSTU_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
+  return launch_select(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HSTU_OK
+                                                                                 : HSTU_ERR_CUDA;
 }
 
 hstu_status hstu_compact_workspace(const hstu_kv_cache* c, const hstu_compact_args* a,
@@ -139,7 +155,9 @@ hstu_status hstu_compact_workspace(const hstu_kv_cache* c, const hstu_compact_ar
   if (st != HSTU_OK) return st;
   if (!a || a->reserved || bad_bound(a->budget) || bad_bound(a->max_seqlen_k))
     return HSTU_ERR_INVALID_ARG;
-  if ((long long)c->batch * c->num_heads_kv > 0x7fffffffll) return HSTU_ERR_UNSUPPORTED;
+  const long long tickets = (long long)c->batch * c->num_heads_kv * compact_chunks(c, a);
+  if (tickets > 0x70000000ll) return HSTU_ERR_UNSUPPORTED;  // (they are counted in 32 bits)
+  *bytes = tickets ? (4 + tickets) * (long long)sizeof(int) : 0;
   return HSTU_OK;
 }
 
@@ -158,13 +176,17 @@ hstu_status hstu_kv_compact(const hstu_kv_cache* c, const hstu_compact_args* a, 
   p.budget = a->budget;
   p.max_k = a->max_seqlen_k;
   p.weights = a->weights;
-  const int fmt = cache_format(c->dtype);
-  p.row_bytes = fmt == kE2m1   ? c->head_dim / 2
-                : fmt == kE4m3 ? c->head_dim
-                               : c->head_dim * elem_bytes(c->dtype);
-  p.by_head = fmt == kE2m1;
-  return launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? HSTU_OK
-                                                                             : HSTU_ERR_CUDA;
+  p.row_bytes = row_bytes(c);
+  p.by_head = cache_format(c->dtype) == kE2m1;
+  p.counter = static_cast<int*>(a->workspace);
+  p.loaded = p.counter + 4;
+  p.timeout_ns = 1000000000ll;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
+  return launch_compact(p, (int)compact_chunks(c, a), sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? HSTU_OK
+             : HSTU_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -38,7 +38,7 @@ struct SelectParams {
   void* new_page_ids;
   void* new_last_page_len;
 };
-cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
+cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream);
 
 struct CompactParams {
   CacheView c;
@@ -48,7 +48,12 @@ struct CompactParams {
   float* weights;  // or nullptr
   int row_bytes;   // of a head's row in one plane of the cache
   int by_head;     // the cache has its heads before the rows (E2M1)
+  int* counter;    // of the chunks that have been handed out
+  int* loaded;     // [B, Nk, chunks]: the chunk's rows have been read
+  long long timeout_ns;
 };
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+constexpr int kCompactRows = 256;  // most ranks of a chunk
+int compact_rows(int row_bytes);   // ranks of a chunk
+cudaError_t launch_compact(const CompactParams& p, int chunks, int sms, cudaStream_t stream);
 
 }  // namespace hstu

@@ -14,12 +14,13 @@ pointers to its C ABI on the current stream. Nothing is kept between calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
 
 from . import _abi
-from .kv_cache import (_INDEX, _call, _cache, _row_dtype, _rows, _tensor)
+from .kv_cache import _INDEX, _PACK_CACHE, _call, _cache, _row_dtype, _rows, _tensor
 
 __all__ = ["hstu_kv_weights", "hstu_kv_select", "hstu_kv_compact"]
 
@@ -69,6 +70,16 @@ def hstu_kv_weights(q, lse, kv_cache, seq_offsets, weights, *, max_seqlen, max_s
         raise _abi.HstuError(_abi.HSTU_ERR_INVALID_ARG, "hstu_kv_weights") from None
     _call("hstu_kv_weights", c, args)
     return weights
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(cache_sizes, budget, bound):
+    """hstu_compact_workspace for these sizes (it reads no pointer)."""
+    need = ctypes.c_longlong(0)
+    _abi.check(_abi.lib().hstu_compact_workspace(
+        _PACK_CACHE(*cache_sizes, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0),
+        _PACK_COMPACT(0, budget, bound, 0, 0, 0, 0), ctypes.byref(need)), "hstu_compact_workspace")
+    return need.value
 
 
 class _Table:
@@ -150,13 +161,8 @@ def hstu_kv_compact(kv_cache, kept, *, page_offsets, page_ids, last_page_len, ma
     bound = _MOST if max_seqlen_k is None else _count(max_seqlen_k, "max_seqlen_k", 1)
     if not c.B or not kept.shape[2]:
         return kv_cache
-    need = ctypes.c_longlong(0)
-    with torch.cuda.device(c.device):
-        _abi.check(_abi.lib().hstu_compact_workspace(
-            c.packed, _PACK_COMPACT(0, kept.shape[2], bound, 0, 0, 0, 0), ctypes.byref(need)),
-            "hstu_compact_workspace")
-    workspace = torch.empty((need.value,), dtype=torch.uint8, device=dev) if need.value else None
-    _call("hstu_kv_compact", c,
-          _PACK_COMPACT(kept_ptr, kept.shape[2], bound, w,
-                        0 if workspace is None else workspace.data_ptr(), need.value, 0))
+    need = _workspace_bytes(c.sizes, kept.shape[2], bound)
+    workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _call("hstu_kv_compact", c, _PACK_COMPACT(kept_ptr, kept.shape[2], bound, w,
+                                              workspace.data_ptr(), need, 0))
     return kv_cache

@@ -6,6 +6,7 @@
 #include "../../include/hstu_evict.h"
 #include "evict_kernels.h"
 #include "kv_checks.h"
+#include "kv_kernels.h"
 
 using namespace hstu;
 
@@ -93,6 +94,7 @@ hstu_status hstu_kv_weights(const hstu_kv_cache* c, const hstu_weights_args* a, 
     const long long ctas = (long long)weights_rows_ctas(c->head_dim, fmt) * sms;
     const long long can = (a->max_seqlen_k + 127) / 128, want = ctas / pairs;
     w.a.splits = (int)(want < 1 ? 1 : want < can ? want : can);
+    w.a.by_length = rows_by_length(c->batch, pairs * w.a.splits, sms);
     e = launch_weights_rows(w, a->dtype, fmt, none || most * G <= 8 ? 8 : 16, s);
   } else {
     e = launch_weights_tc(w, a->dtype, fmt, slots_for(4ll * sms, weights_tc_keys(c->head_dim)), s);

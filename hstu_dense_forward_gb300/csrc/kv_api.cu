@@ -42,6 +42,7 @@ struct AttnPlan {
   int qtiles, ctas;    // query tiles of one CTA, CTAs of one SM (TC)
   int rows;            // query rows of one item (SIMT, ROWS)
   int cluster;         // CTAs that divide the keys of one item (ROWS)
+  int by_length;       // CTAs of a round (ROWS)
   int balanced;        // CTAs share the items' key tiles (TC)
   int splits, min_range;
   long long tiles, blocks, workspace, parts_bytes;
@@ -159,6 +160,7 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     while (pl->cluster < 8 && pl->cluster * 2 <= want) pl->cluster *= 2;
     pl->splits = (int)(want / pl->cluster);
     pl->min_range = 128 * pl->cluster;
+    if (pl->cluster == 1) pl->by_length = rows_by_length(c->batch, pl->blocks * pl->splits, sms);
   } else if (pl->kernel == AttnPlan::SIMT) {
     pl->min_range = 128;
     // resident CTAs: four an SM; of four rows three, in two waves (25 sequences of some 7500 keys,
@@ -226,6 +228,7 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   p.min_range = pl.min_range;
   p.timeout_ns = 1000000000ll;
   p.balanced = pl.balanced;
+  p.by_length = pl.by_length;
   // workspace: outputs of the parts, their sums, the table of items
   p.part_o = static_cast<float*>(a->workspace);
   p.part_lse = p.part_o + pl.parts_bytes / 4 / (c->head_dim + 1) * c->head_dim;

@@ -316,6 +316,8 @@ struct SoftmaxParams {
   long long max_k;         // bound on Lk
   int causal;
   float scale_log2;        // alpha * log2(e): scores in powers of two
+  int by_length;           // few rows: CTAs take the sequences longest first, in rounds of so many
+                           // (0: in order)
   int splits;              // most key ranges of one sequence (1: outputs are written at once)
   int min_range;           // fewest keys worth a range of their own (a multiple of 128)
   long long timeout_ns;

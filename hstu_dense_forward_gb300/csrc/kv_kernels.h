@@ -36,6 +36,13 @@ cudaError_t launch_softmax_simt(const SoftmaxParams& p, int fmt, int rows, long 
 cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, int fmt, int qtiles, int ctas,
                               long long tiles, long long blocks, cudaStream_t stream);
 
+// Items of one tile each that share SMs are taken by the sequences' lengths (see softmax_rows.cuh):
+// CTAs of a round, or 0. A CTA compares every length with its own sequence's, which up to 256 of them
+// allow.
+inline int rows_by_length(long long batch, long long ctas, long long sms) {
+  return batch > 1 && batch <= 256 && ctas > sms ? (int)sms : 0;
+}
+
 // Attention of few rows (bf16, fp16): `rows` (8 or 16) packed rows of one kv head per cluster
 // of CTAs; CTAs of it that an SM holds.
 int softmax_rows_ctas(int D, int fmt, int rows);

@@ -179,6 +179,33 @@ __device__ __forceinline__ uint32_t piece_at(int r, int piece) {
   return SWB == 128 ? o ^ ((o >> 3) & 0x70u) : SWB == 64 ? o ^ ((o >> 3) & 0x30u) : o;
 }
 
+// The sequence that is number `rank` by length, the longest first and equal ones in order, by the whole
+// CTA; len: shared memory for kMaxSorted lengths.
+constexpr int kMaxSorted = 256;
+__device__ __forceinline__ int sequence_by_length(const SoftmaxParams& p, int rank, int threads,
+                                                  long long* len, int* found) {
+  for (int b = threadIdx.x; b < p.c.B; b += threads) len[b] = paged_table(p.c, b).Lk;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.c.B; b += threads) {
+    const long long mine = len[b];
+    int before = 0;
+    for (int j = 0; j < p.c.B; ++j) before += len[j] > mine || (len[j] == mine && j < b);
+    if (before == rank) *found = b;
+  }
+  __syncthreads();
+  return *found;
+}
+
+// Place of the CTA's item in the order of the lengths. A round of by_length CTAs, one an SM, goes
+// through it forwards, the next backwards, so that an SM's share of long and short sequences evens out
+// (128 sequences of 1k-4k keys and four heads on 456 places: 78 us in the sequences' order, 64 so).
+__device__ __forceinline__ long long place_by_length(const SoftmaxParams& p, long long blk,
+                                                     long long blocks) {
+  const long long round = blk / p.by_length, first = round * p.by_length;
+  if (!(round & 1) || first + p.by_length > blocks) return blk;
+  return 2 * first + p.by_length - 1 - blk;
+}
+
 struct Item {
   PagedSeq s;
   int b, hk, split, nsplit;
@@ -186,11 +213,16 @@ struct Item {
   long long k0, kend;   // keys of this CTA
 };
 
-template <int RT>
+template <int RT, int THREADS>
 __device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, int cluster,
-                                          Item& it) {
-  const long long blk = blockIdx.x / cluster;
+                                          Item& it, long long* len, int* found) {
+  long long blk = blockIdx.x / cluster;
   const int rank = blockIdx.x % cluster;
+  if (p.by_length) {  // (one tile)
+    blk = place_by_length(p, blk, gridDim.x / cluster);
+    const int b = sequence_by_length(p, (int)(blk / p.c.Nk), THREADS, len, found);
+    blk = (long long)b * p.c.Nk + blk % p.c.Nk;
+  }
   it.hk = (int)(blk % p.c.Nk);
   const int tile = (int)(blk / p.c.Nk % tiles);
   it.b = (int)(blk / p.c.Nk / tiles);
@@ -478,10 +510,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
   namespace cg = cooperative_groups;
   constexpr int RT = C::RT;
   extern __shared__ uint8_t smem_raw[];
-  Item it;
-  if (!make_item<RT>(p, tiles, cluster, it)) return;  // (the whole cluster)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ int found;
+  Item it;
+  if (!make_item<RT, C::THREADS>(p, tiles, cluster, it, reinterpret_cast<long long*>(smem), &found))
+    return;  // (the whole cluster)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = (int)((it.kend - it.k0 + KT - 1) / KT);
@@ -518,9 +552,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
     auto& lim = qs.lim;
     const int see = qs.see;
 
+    int st = 0;  // of the ring
+    uint32_t phase = 0;
     for (int t = 0; t < n; ++t) {
-      const int st = t % C::NST;
-      if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], (t / C::NST) & 1))) break;
+      if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], phase))) break;
       const int at = t * KT + warp * 16;  // first of the warp's keys
       const int left = keys - at;         // of them, keys of this CTA
       if (left > 0) {
@@ -736,6 +771,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->empty[st]));
+      if (++st == C::NST) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
   }
 

@@ -19,9 +19,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
   using C = Cfg<D, NT, BF16, FMT, 1>;
   const SoftmaxParams& p = w.a;
   extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ int found;
   Item it;
-  it.hk = (int)(blockIdx.x % (unsigned)p.c.Nk);
-  it.b = (int)(blockIdx.x / (unsigned)p.c.Nk);
+  long long blk = blockIdx.x;
+  if (p.by_length) {
+    blk = place_by_length(p, blk, gridDim.x);
+    const int b = sequence_by_length(p, (int)(blk / p.c.Nk), C::THREADS,
+                                     reinterpret_cast<long long*>(smem), &found);
+    blk = (long long)b * p.c.Nk + blk % p.c.Nk;
+  }
+  it.hk = (int)(blk % p.c.Nk);
+  it.b = (int)(blk / p.c.Nk);
   it.split = blockIdx.y;
   it.s = paged_seq(p.c, it.b);
   if (!attn_seq_ok(p, it.s) || it.s.n * p.G > C::RT) {
@@ -35,8 +45,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
   it.k0 = it.split * kr.keys;
   it.kend = min(it.s.Lk, it.k0 + kr.keys);
   if (it.k0 >= it.kend || (it.rows == 0 && w.accumulate)) return;
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int keys = (int)(it.kend - it.k0), n = (keys + KT - 1) / KT;
@@ -67,19 +75,26 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
           l2[i][y] = w.lse[(it.s.t0 + r / p.G) * p.Nq + it.hk * p.G + r % p.G] * kLog2e;
       }
     const int mine = g + 8 * (c & 1);  // of the warp's sixteen keys, the one that this lane writes
+    // the page of the lane's key in a tile, loaded a tile ahead: what its place holds is then loaded
+    // while the tile is waited for
+    auto page_of = [&](int t) {
+      const int at = t * KT + warp * 16 + mine;
+      return at < keys ? page_at(p.c, it.s, it.k0 + at) : -1ll;
+    };
+    long long next = page_of(0);
+    int st = 0;
+    uint32_t phase = 0;
     for (int t = 0; t < n; ++t) {
-      const int st = t % C::NST;
       const int at = t * KT + warp * 16;  // first of the warp's keys
-      // the place of the lane's key and what it holds, before the keys are waited for
-      const long long pos = it.k0 + at + mine;
-      const long long page = at + mine < keys ? page_at(p.c, it.s, pos) : -1;
+      const long long pos = it.k0 + at + mine, page = next;
       float* to = w.weights;
       float old = 0.f;
       if (page >= 0) {
         to += ((page * p.c.Nk + it.hk) << p.c.page_shift) + (pos & (page_size(p.c) - 1));
         if (w.accumulate && c < 2) old = *to;
       }
-      if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], (t / C::NST) & 1))) break;
+      next = page_of(t + 1);
+      if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], phase))) break;
       if (at < keys) {
         float sc[NT][4], ev[2], sum[2] = {0.f, 0.f};
         tile_scores<C>(p, smem, st, warp * 16, g, c, qs, sc, ev);
@@ -101,6 +116,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->empty[st]));
+      if (++st == C::NST) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
   }
   __syncthreads();

@@ -91,11 +91,12 @@ hstu_status hstu_kv_weights(const hstu_kv_cache* c, const hstu_weights_args* a, 
     e = launch_weights_simt(w, fmt, slots_for(4ll * sms, kWeightsSimtKeys), s);
   } else if (none || most * G <= 16) {
     // one wave of CTAs, each with a stretch of the keys
-    const long long ctas = (long long)weights_rows_ctas(c->head_dim, fmt) * sms;
+    const int rows = none || most * G <= 8 ? 8 : 16;
+    const long long ctas = (long long)weights_rows_ctas(c->head_dim, fmt, rows) * sms;
     const long long can = (a->max_seqlen_k + 127) / 128, want = ctas / pairs;
     w.a.splits = (int)(want < 1 ? 1 : want < can ? want : can);
     w.a.by_length = rows_by_length(c->batch, pairs * w.a.splits, sms);
-    e = launch_weights_rows(w, a->dtype, fmt, none || most * G <= 8 ? 8 : 16, s);
+    e = launch_weights_rows(w, a->dtype, fmt, rows, s);
   } else {
     e = launch_weights_tc(w, a->dtype, fmt, slots_for(4ll * sms, weights_tc_keys(c->head_dim)), s);
   }

@@ -15,7 +15,7 @@ struct WeightsParams {
 };
 
 // Few rows (16-bit; at most `rows`, 8 or 16, of a kv head and sequence); CTAs that an SM holds.
-int weights_rows_ctas(int D, int fmt);
+int weights_rows_ctas(int D, int fmt, int rows);
 cudaError_t launch_weights_rows(const WeightsParams& w, int dtype, int fmt, int rows,
                                 cudaStream_t stream);
 

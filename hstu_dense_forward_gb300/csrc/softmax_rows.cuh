@@ -49,7 +49,6 @@
 namespace hstu {
 namespace rows {
 
-constexpr int KT = 64;     // keys of one tile
 constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNoKey = -1e38f;  // E4M3: reference of a row that has seen no key
@@ -65,6 +64,9 @@ struct Cfg {
   static constexpr int SWB = RB < 128 ? RB : 128;          // bytes of one swizzled row block
   static constexpr int NCB = RB / SWB;                     // blocks of a key's row
   static constexpr int BE = D / NCB;                       // elements of a block
+  // Keys of a tile, sixteen a warp. A CTA's time is its longest sequence's, tile after tile; where a
+  // key's bytes are few, more warps (and fewer CTAs on an SM) shorten that.
+  static constexpr int KT = PLANES == 1 ? 128 : 64;
   static constexpr int CB = KT * SWB;                      // one block of a tile
   static constexpr int EPP = 16 * D / RB;                  // elements of a 16-byte piece
   static constexpr int LPC = SWB / 64;                     // pieces per lane and block (scores)
@@ -75,14 +77,12 @@ struct Cfg {
   static constexpr int PLANE = KT * RB, STAGE = PLANES * PLANE;
   // CTAs per SM: what their registers (O and Q) and a ring of at least three stages leave. E4M3
   // spends more instructions per byte and needs the warps of a third CTA.
-  static constexpr int CTAS = PLANES == 1 ? (RB == 512 ? 2 : D == 256 ? 3 : 4)
+  static constexpr int CTAS = PLANES == 1 ? (RB == 512 || (D == 256 && NT == 2)        ? 1
+                                             : RB > 128 || D == 256 || NT == 2 ? 2
+                                                                               : 3)
                               : D == 256  ? (CODES && NT == 1 ? 2 : 1)
                                           : (CODES && NT == 1 ? 3 : 2);
-  static constexpr int RING = CTAS == 1   ? 196608
-                              : CTAS == 2 ? 98304
-                              : CTAS == 4 ? (FP4 ? 45056 : 49152)
-                              : FP4       ? 57344
-                                          : 65536;
+  static constexpr int RING = CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : FP4 || PLANES == 1 ? 57344 : 65536;
   static constexpr int NST = RING / STAGE < 12 ? RING / STAGE : 12;
   static constexpr int OFF_SC = NST * STAGE;               // row scales: KT bytes a plane and stage
   static constexpr int GPLANE = KT * (D / 16);             // E2M1: factors of a plane's tile
@@ -213,14 +213,14 @@ struct Item {
   long long k0, kend;   // keys of this CTA
 };
 
-template <int RT, int THREADS>
+template <class C>
 __device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, int cluster,
                                           Item& it, long long* len, int* found) {
   long long blk = blockIdx.x / cluster;
   const int rank = blockIdx.x % cluster;
   if (p.by_length) {  // (one tile)
     blk = place_by_length(p, blk, gridDim.x / cluster);
-    const int b = sequence_by_length(p, (int)(blk / p.c.Nk), THREADS, len, found);
+    const int b = sequence_by_length(p, (int)(blk / p.c.Nk), C::THREADS, len, found);
     blk = (long long)b * p.c.Nk + blk % p.c.Nk;
   }
   it.hk = (int)(blk % p.c.Nk);
@@ -233,18 +233,18 @@ __device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, int
     return false;
   }
   it.rows = it.s.n * p.G;
-  it.m0 = (long long)tile * RT;
+  it.m0 = (long long)tile * C::RT;
   const KeyRanges kr = key_ranges(p, it.s.Lk);
   it.nsplit = kr.count;
   if (it.m0 >= it.rows || it.split >= kr.count) return false;
-  const long long last = (min(it.m0 + RT, it.rows) - 1) / p.G;  // last token of the tile
+  const long long last = (min(it.m0 + C::RT, it.rows) - 1) / p.G;  // last token of the tile
   long long e = min(it.s.Lk, (it.split + 1) * kr.keys);
   if (p.causal) e = min(e, it.s.Lk - it.s.n + last + 1);
   const long long k0 = it.split * kr.keys;
-  const long long nt = e > k0 ? (e - k0 + KT - 1) / KT : 0;
+  const long long nt = e > k0 ? (e - k0 + C::KT - 1) / C::KT : 0;
   const long long per = (nt + cluster - 1) / cluster;  // tiles of one CTA of the cluster
-  it.k0 = min(e, k0 + rank * per * KT);
-  it.kend = min(e, k0 + (rank + 1) * per * KT);
+  it.k0 = min(e, k0 + rank * per * C::KT);
+  it.kend = min(e, k0 + (rank + 1) * per * C::KT);
   return true;
 }
 
@@ -253,12 +253,12 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
                           int tiles, const CUtensorMap* tc) {
   const uint32_t sbase = ptx::smem_u32(smem);
   const int ps = 1 << p.c.page_shift;
-  const int boxes = ps >= KT ? 1 : KT / 32, brows = ps >= KT ? KT : 32;
+  const int boxes = ps >= C::KT ? 1 : C::KT / 32, brows = ps >= C::KT ? C::KT : 32;
   for (int t = 0; t < tiles; ++t) {
-    const long long n0 = it.k0 + (long long)t * KT;
-    long long page[KT / 32];
+    const long long n0 = it.k0 + (long long)t * C::KT;
+    long long page[C::KT / 32];
 #pragma unroll
-    for (int m = 0; m < KT / 32; ++m) {
+    for (int m = 0; m < C::KT / 32; ++m) {
       if (m >= boxes) break;
       page[m] = page_at(p.c, it.s, min(n0 + 32 * m, it.s.Lk - 1));
       if (page[m] < 0) {  // unspecified outputs, but a valid access
@@ -272,10 +272,10 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
     const bool scales = C::CODES && p.c.scale;
     const int gb = p.c.D / 16;  // E2M1: factors of a row
     ptx::mbar_arrive_expect_tx(
-        bar, C::STAGE + (scales ? C::PLANES * KT : 0) + (C::FP4 ? C::PLANES * KT * gb : 0));
-    const int row0 = ps >= KT ? (int)(n0 & (ps - 1)) : 0;
+        bar, C::STAGE + (scales ? C::PLANES * C::KT : 0) + (C::FP4 ? C::PLANES * C::KT * gb : 0));
+    const int row0 = ps >= C::KT ? (int)(n0 & (ps - 1)) : 0;
 #pragma unroll
-    for (int m = 0; m < KT / 32; ++m) {
+    for (int m = 0; m < C::KT / 32; ++m) {
       if (m >= boxes) break;
 #pragma unroll
       for (int plane = 0; plane < C::PLANES; ++plane) {
@@ -293,7 +293,7 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
                          p.c.group + scale_row(p.c, page[m], plane, row0, it.hk) * gb, brows * gb,
                          bar);
         if (scales)
-          ptx::bulk_load(sbase + C::OFF_SC + (C::PLANES * st + plane) * KT + m * 32,
+          ptx::bulk_load(sbase + C::OFF_SC + (C::PLANES * st + plane) * C::KT + m * 32,
                          p.c.scale + scale_row(p.c, page[m], plane, row0, it.hk), brows, bar);
       }
     }
@@ -473,11 +473,11 @@ __device__ __forceinline__ void tile_scores(const SoftmaxParams& p, const uint8_
     }
   // scores in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y
   if (C::CODES && p.c.scale) {
-    const uint8_t* sp = smem + C::OFF_SC + st * C::PLANES * KT + r16 + g;
+    const uint8_t* sp = smem + C::OFF_SC + st * C::PLANES * C::KT + r16 + g;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const float f = scale_value(sp[8 * x]);
-      if (C::PLANES == 2) ev[x] = (float)((int)sp[KT + 8 * x] - 127);
+      if (C::PLANES == 2) ev[x] = (float)((int)sp[C::KT + 8 * x] - 127);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -514,11 +514,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ int found;
   Item it;
-  if (!make_item<RT, C::THREADS>(p, tiles, cluster, it, reinterpret_cast<long long*>(smem), &found))
+  if (!make_item<C>(p, tiles, cluster, it, reinterpret_cast<long long*>(smem), &found))
     return;  // (the whole cluster)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = (int)((it.kend - it.k0 + KT - 1) / KT);
+  const int n = (int)((it.kend - it.k0 + C::KT - 1) / C::KT);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->full[s]), 1);
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
     uint32_t phase = 0;
     for (int t = 0; t < n; ++t) {
       if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], phase))) break;
-      const int at = t * KT + warp * 16;  // first of the warp's keys
+      const int at = t * C::KT + warp * 16;  // first of the warp's keys
       const int left = keys - at;         // of them, keys of this CTA
       if (left > 0) {
         const uint8_t* kt = smem + st * C::STAGE;

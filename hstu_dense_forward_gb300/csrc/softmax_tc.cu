@@ -29,8 +29,8 @@ HSTU_ROWS_UNIT(fp16);
 #undef HSTU_ROWS_UNIT
 
 int softmax_rows_ctas(int D, int fmt, int rows) {
-  const bool more = fmt != kSame && rows == 8;
-  return kernel_dim(D) == 256 ? (more ? 2 : 1) : (more ? 3 : 2);
+  const bool wide = kernel_dim(D) == 256, more = fmt != kSame && rows == 8;
+  return wide ? (more ? 2 : 1) : (more ? 3 : 2);
 }
 
 cudaError_t launch_softmax_rows(const SoftmaxParams& p, int dtype, int fmt, int rows,

@@ -16,9 +16,10 @@ HSTU_WEIGHTS_UNITS(bf16);
 HSTU_WEIGHTS_UNITS(fp16);
 #undef HSTU_WEIGHTS_UNITS
 
-int weights_rows_ctas(int D, int fmt) {
-  const int dim = kernel_dim(D);
-  return dim == 256 ? (fmt == kSame ? 2 : 3) : 4;
+int weights_rows_ctas(int D, int fmt, int rows) {
+  const int dim = kernel_dim(D), row = fmt == kE2m1 ? dim / 2 : fmt == kE4m3 ? dim : 2 * dim;
+  if (row == 512 || (dim == 256 && rows == 16)) return 1;
+  return row > 128 || dim == 256 || rows == 16 ? 2 : 3;
 }
 
 int weights_tc_keys(int D) { return kernel_dim(D) == 256 ? 128 : 256; }
@@ -30,8 +31,8 @@ cudaError_t launch_weights_rows(const WeightsParams& w, int dtype, int fmt, int 
   const int row_bytes =
       fmt == kE2m1 ? kernel_dim(w.a.c.D) / 2 : kernel_dim(w.a.c.D) * (e4m3 ? 1 : 2);
   const int swz = row_bytes < 128 ? row_bytes : 128;
-  if (!(fmt == kE2m1 ? code_map(&tc, w.a, swz, 64, swz)
-                     : cache_map(&tc, w.a, dtype, e4m3, swz / (e4m3 ? 1 : 2), 64, swz)))
+  if (!(fmt == kE2m1 ? code_map(&tc, w.a, swz, 128, swz)
+                     : cache_map(&tc, w.a, dtype, e4m3, swz / (e4m3 ? 1 : 2), 128, swz)))
     return cudaErrorInvalidValue;
   return dtype == HSTU_BF16 ? launch_weights_rows_bf16(w, fmt, tc, rows, stream)
                             : launch_weights_rows_fp16(w, fmt, tc, rows, stream);

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
   if (it.k0 >= it.kend || (it.rows == 0 && w.accumulate)) return;
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int keys = (int)(it.kend - it.k0), n = (keys + KT - 1) / KT;
+  const int keys = (int)(it.kend - it.k0), n = (keys + C::KT - 1) / C::KT;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->full[s]), 1);
@@ -78,14 +78,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
     // the page of the lane's key in a tile, loaded a tile ahead: what its place holds is then loaded
     // while the tile is waited for
     auto page_of = [&](int t) {
-      const int at = t * KT + warp * 16 + mine;
+      const int at = t * C::KT + warp * 16 + mine;
       return at < keys ? page_at(p.c, it.s, it.k0 + at) : -1ll;
     };
     long long next = page_of(0);
     int st = 0;
     uint32_t phase = 0;
     for (int t = 0; t < n; ++t) {
-      const int at = t * KT + warp * 16;  // first of the warp's keys
+      const int at = t * C::KT + warp * 16;  // first of the warp's keys
       const long long pos = it.k0 + at + mine, page = next;
       float* to = w.weights;
       float old = 0.f;

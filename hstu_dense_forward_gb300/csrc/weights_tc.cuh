@@ -8,13 +8,14 @@
 // A CTA keeps a step of KT keys (one or two tiles of 128) in shared memory and passes over the query
 // tiles (128 / G tokens each) that see any of them, then takes the next step of its share; the first
 // keys, which with the causal mask the most rows see, come first in the grid. Warp roles:
-//   warps 0 .. 4 NT - 1   the sums, one warpgroup per key tile, one thread per key;
+//   warps 0 .. 7          the sums, a warpgroup for each half of the columns, a thread for a key of
+//                         every tile: what belongs to a row is read once for both keys;
 //   next warp             issues every tcgen05.mma; owns TMEM;
 //   next warp             TMA loads: query tiles, and the keys of a cache of the queries' type;
+//   next warp             the rows' logarithms, into shared memory;
 //   codes: four warps     load the keys and turn them into the queries' type (E4M3 codes and
 //                         products of an E2M1 code and factor have 4 and 7 bits: exact in both).
-// Each key tile's scores have two buffers in TMEM: the next product runs while one is summed up. What
-// bounds it is one exponential per score.
+// The scores have two buffers in TMEM: the next products run while one is summed up.
 //
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
@@ -46,20 +47,21 @@ struct Cfg {
   static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
   static constexpr int NK = D == 64 ? 3 : 2, NQ = D == 256 ? 1 : D == 128 ? 2 : 4;
   static constexpr int OFF_Q = NK * K_STEP, OFF_L = OFF_Q + NQ * Q_TILE;
-  static constexpr int OFF_BAR = OFF_L + NT * 2 * 128 * 4;  // rows' logarithms, two tiles
+  static constexpr int OFF_S = OFF_L + 4 * 128 * 4;         // rows' logarithms, of four tiles
+  static constexpr int OFF_BAR = OFF_S + 2 * KT * 4;        // half the columns' sums, of two steps
   static constexpr int USED = OFF_BAR + 512 + 1024;
   // (one CTA per SM, which takes its share of TMEM: no second one may come to wait for it)
   static constexpr int SMEM = USED < 120 * 1024 ? 120 * 1024 : USED;
   static_assert(SMEM <= 232448, "shared memory");
-  static constexpr int SUM_WARPS = 4 * NT, MMA_WARP = SUM_WARPS, LOAD_WARP = SUM_WARPS + 1;
-  static constexpr int CONV_WARP = SUM_WARPS + 4;  // (a warpgroup's boundary)
-  static constexpr int THREADS = (CODES ? CONV_WARP + 4 : LOAD_WARP + 1) * 32;
+  static constexpr int SUM_WARPS = 8, MMA_WARP = 8, LOAD_WARP = 9, LOG_WARP = 10;
+  static constexpr int CONV_WARP = 12;  // (a warpgroup's boundary)
+  static constexpr int THREADS = (CODES ? CONV_WARP + 4 : LOG_WARP + 1) * 32;
   static constexpr uint32_t TMEM_COLS = NT * 2 * 128;
 };
 
 struct Bars {
   uint64_t k_full[3], k_empty[3], q_full[4], q_empty[4];
-  uint64_t s_full[2][2], s_empty[2][2], drain;
+  uint64_t s_full[2], s_empty[2], drain;
   uint32_t tmem_base;
   volatile int abort;
 };
@@ -243,24 +245,23 @@ __device__ void mma_role(const SoftmaxParams& p, Bars* bars, uint32_t sbase, uin
       const int qslot = qi % C::NQ, sb = qi & 1;
       if (!warp_wait(p, bars, &bars->q_full[qslot], (qi / C::NQ) & 1)) return;
       const uint64_t bd0 = ptx::smem_desc(sbase + C::OFF_Q + qslot * C::Q_TILE, 16, 8 * C::SWB, 2);
+      if (!warp_wait(p, bars, &bars->s_empty[sb], ((qi >> 1) & 1) ^ 1)) return;
+      ptx::tc_fence_after();
+      const uint64_t ad0 = ptx::smem_desc(sbase + kslot * C::K_STEP, 16, 8 * C::SWB, 2);
+      if (ptx::elect_one()) {
 #pragma unroll
-      for (int m = 0; m < C::NT; ++m) {
-        if (!warp_wait(p, bars, &bars->s_empty[m][sb], ((qi >> 1) & 1) ^ 1)) return;
-        ptx::tc_fence_after();
-        const uint64_t ad0 = ptx::smem_desc(sbase + kslot * C::K_STEP + m * 128 * C::SWB, 16,
-                                            8 * C::SWB, 2);
-        if (ptx::elect_one()) {
+        for (int m = 0; m < C::NT; ++m)
 #pragma unroll
           for (int kk = 0; kk < C::D / 16; ++kk) {
             const uint32_t in = (kk % 4) * 32;
-            ptx::mma_ss(tmem + (m * 2 + sb) * 128, ptx::desc_add(ad0, (kk / 4) * C::K_CB + in),
+            ptx::mma_ss(tmem + (sb * C::NT + m) * 128,
+                        ptx::desc_add(ad0, (kk / 4) * C::K_CB + m * 128 * C::SWB + in),
                         ptx::desc_add(bd0, (kk / 4) * C::Q_CB + in), IDESC, kk > 0 ? 1u : 0u);
           }
-          ptx::mma_commit(ptx::smem_u32(&bars->s_full[m][sb]));
-          if (m == C::NT - 1) ptx::mma_commit(ptx::smem_u32(&bars->q_empty[qslot]));
-        }
-        __syncwarp();
+        ptx::mma_commit(ptx::smem_u32(&bars->s_full[sb]));
+        ptx::mma_commit(ptx::smem_u32(&bars->q_empty[qslot]));
       }
+      __syncwarp();
     }
     if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&bars->k_empty[kslot]));
     __syncwarp();
@@ -282,89 +283,183 @@ __device__ __forceinline__ void mma_drain(const SoftmaxParams& p, Bars* bars) {
   }
 }
 
-// ------------------------------------------------------------------ sums
+// ------------------------------------------------------------------ logarithms
+// -lse log2 e of a query tile's columns, four a lane; columns without a row: their weights are 0. A
+// tile's scores count as there once these are. Slots are written again four tiles on: two tiles after
+// their own the warps that sum have told that they are done with the one between.
 template <class C>
-__device__ void sum_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, uint32_t tmem,
-                         const Work& w, int slots, int m, int warp, int lane) {
+__device__ void log_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, const Work& w,
+                         int slots, int lane) {
   const SoftmaxParams& p = wp.a;
-  const int r = (warp & 3) * 32 + lane;  // key of the tile, TMEM lane
-  const uint32_t s_col = tmem + ((uint32_t)((warp & 3) * 32) << 16) + m * 256;
-  float* logs = reinterpret_cast<float*>(smem + C::OFF_L) + m * 256;  // [2][128], negated
-  // the logarithm of column r of a query tile; columns without a row: their weights are 0
-  auto row_log = [&](int t) {
-    const long long tok = (long long)t * w.tpt + r / p.G;
-    if (r >= w.tpt * p.G || tok >= w.s.n) return -CUDART_INF_F;
-    return -wp.lse[(w.s.t0 + tok) * p.Nq + w.hk * p.G + r % p.G] * kLog2e;
+  float4* logs = reinterpret_cast<float4*>(smem + C::OFF_L);
+  const int columns = w.tpt * p.G;
+  int off[4];  // lse of the lane's columns, counted from the tile's first
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = min(4 * lane + i, columns - 1);
+    off[i] = c / p.G * p.Nq + c % p.G;
+  }
+  auto load = [&](int t) {
+    const float* at = wp.lse + (w.s.t0 + (long long)t * w.tpt) * p.Nq + w.hk * p.G;
+    const int rows = (int)min((long long)w.tpt, w.s.n - (long long)t * w.tpt) * p.G;
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = 4 * lane + i < rows ? at[off[i]] * -kLog2e : -CUDART_INF_F;
+    return make_float4(x[0], x[1], x[2], x[3]);
   };
   uint32_t qi = 0;
-  bool ok = true;  // no wait has run out; if one has, the warps still meet at every barrier
   for (int step = w.first; step < w.steps; step += slots) {
-    const long long k0 = (long long)step * C::KT, pos = k0 + m * 128 + r;
-    const int t0 = first_tile(p, w, k0);
-    const long long page = pos < w.s.Lk ? page_at(p.c, w.s, pos) : -1;
-    float f = p.scale_log2, old = 0.f;
-    float* to = wp.weights;
-    if (page >= 0) {
-      const long long row = pos & (page_size(p.c) - 1);
-      if (C::CODES && p.c.scale) f *= scale_value(p.c.scale[scale_row(p.c, page, 0, row, w.hk)]);
-      to += ((page * p.c.Nk + w.hk) << p.c.page_shift) + row;
-      if (wp.accumulate) old = *to;
-    }
-    if (C::CODES && p.c.k_ds)
-      f *= p.c.k_ds[(long long)w.b * p.c.ds_b + (long long)w.hk * p.c.ds_h];
-    f = fminf(fmaxf(f, -3e38f), 3e38f);  // (finite: columns without a row have scores of 0)
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    float next = t0 < w.tiles ? row_log(t0) : 0.f;
+    const int t0 = first_tile(p, w, (long long)step * C::KT);
+    float4 x = t0 < w.tiles ? load(t0) : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int t = t0; t < w.tiles; ++t, ++qi) {
-      const int sb = qi & 1;
-      float* ls = logs + sb * 128;
-      ls[r] = next;  // (the tile before the last one has been read by all: the barrier between)
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + m) : "memory");
-      if (t + 1 < w.tiles) next = row_log(t + 1);
-      ok = ok && warp_wait(p, bars, &bars->s_full[m][sb], (qi >> 1) & 1);
-      if (!ok) continue;
-      ptx::tc_fence_after();
-      // columns [lo, hi) see the key
-      const long long tok0 = (long long)t * w.tpt;
-      const int hi = (int)min((long long)w.tpt, w.s.n - tok0) * p.G;
-      int lo = 0;
-      if (p.causal) {
-        const long long tok = pos - (w.s.Lk - w.s.n) - tok0;
-        lo = tok > 0 ? (int)min(tok * p.G, 128ll) : 0;
+      if (!warp_wait(p, bars, &bars->s_empty[qi & 1], ((qi >> 1) & 1) ^ 1)) return;
+      logs[(qi & 3) * 32 + lane] = x;
+      ptx::mbar_arrive(ptx::smem_u32(&bars->s_full[qi & 1]));
+      if (t + 1 < w.tiles) x = load(t + 1);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sums
+// A thread takes its columns of its NT keys in four chunks, each of which it loads from TMEM while it
+// sums up the one before; the first chunk of a tile is loaded behind the last one of the tile before
+// if its products are done by then (their barrier is looked at a chunk earlier: an answer takes some
+// hundred cycles). So a tile's buffer is free again before its last chunk is summed up.
+template <class C>
+__device__ void sum_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, uint32_t tmem,
+                         const Work& w, int slots, int warp, int lane) {
+  constexpr int NT = C::NT, CH = 16;  // columns of a chunk
+  const SoftmaxParams& p = wp.a;
+  const int half = warp / 4, r = (warp & 3) * 32 + lane;  // key of a tile, TMEM lane
+  const uint32_t s_col = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 64;
+  const float* logs = reinterpret_cast<const float*>(smem + C::OFF_L) + half * 64;  // [4][128]
+  float* sums = reinterpret_cast<float*>(smem + C::OFF_S) + r;                      // [2][KT]
+  const int full_tiles = (int)(w.s.n / w.tpt);  // whose tokens are all there
+  uint32_t qi = 0, si = 0;
+  uint32_t s[2][NT][CH];
+  bool ok = true;  // no wait has run out; if one has, the warps still meet at every barrier
+  auto load_chunk = [&](int b, uint32_t col) {
+#pragma unroll
+    for (int m = 0; m < NT; ++m) ptx::tmem_ld16_issue(col + m * 128, s[b][m]);
+  };
+  for (int step = w.first; step < w.steps; step += slots, ++si) {
+    const long long k0 = (long long)step * C::KT;
+    const int t0 = first_tile(p, w, k0);
+    float f[NT], old[NT];
+    float* to[NT];
+    float2 sum[NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      const long long pos = k0 + m * 128 + r;
+      const long long page = pos < w.s.Lk ? page_at(p.c, w.s, pos) : -1;
+      f[m] = p.scale_log2;
+      old[m] = 0.f;
+      to[m] = nullptr;
+      sum[m] = make_float2(0.f, 0.f);
+      if (page >= 0) {
+        const long long row = pos & (page_size(p.c) - 1);
+        if (C::CODES && p.c.scale)
+          f[m] *= scale_value(p.c.scale[scale_row(p.c, page, 0, row, w.hk)]);
+        to[m] = wp.weights + ((page * p.c.Nk + w.hk) << p.c.page_shift) + row;
+        if (wp.accumulate && half == 0) old[m] = *to[m];
       }
-      const bool whole = __all_sync(0xffffffffu, lo == 0) && tok0 + w.tpt <= w.s.n;
-      const uint32_t col = s_col + sb * 128;
-      auto add = [&](auto masked) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t s[32];
-          ptx::tmem_ld32(col + c0, s);
+      if (C::CODES && p.c.k_ds)
+        f[m] *= p.c.k_ds[(long long)w.b * p.c.ds_b + (long long)w.hk * p.c.ds_h];
+      f[m] = fminf(fmaxf(f[m], -3e38f), 3e38f);  // (finite: columns without a row have scores of 0)
+    }
+    // tiles from `seen` on see every key of the step
+    int seen = 0;
+    if (p.causal) {
+      const long long tok = k0 + C::KT - 1 - (w.s.Lk - w.s.n);
+      seen = tok > 0 ? (int)min((tok + w.tpt - 1) / w.tpt, (long long)w.tiles) : 0;
+    }
+    if (t0 < w.tiles) {
+      ok = ok && warp_wait(p, bars, &bars->s_full[qi & 1], (qi >> 1) & 1);
+      ptx::tc_fence_after();
+      if (ok) load_chunk(0, s_col + (qi & 1) * NT * 128);
+    }
+    for (int t = t0; t < w.tiles && ok; ++t, ++qi) {
+      const int sb = qi & 1;
+      const uint32_t col = s_col + sb * NT * 128, next_col = s_col + (sb ^ 1) * NT * 128;
+      const uint32_t next_full = ptx::smem_u32(&bars->s_full[sb ^ 1]);
+      const uint32_t next_parity = ((qi + 1) >> 1) & 1;
+      const bool more = t + 1 < w.tiles;
+      const float* ls = logs + (qi & 3) * 128;
+      const bool whole = t >= seen && t < full_tiles;
+      int lo[NT], hi = 0;  // columns [lo, hi) of this half see the key
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(ls + c0 + e);
-            float x[4];
-            ptx::fma_f32x2(x[0], x[1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), f, f, l.x,
-                           l.y);
-            ptx::fma_f32x2(x[2], x[3], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]), f, f,
-                           l.z, l.w);
-            if constexpr (decltype(masked)::value) {
+      for (int m = 0; m < NT; ++m) lo[m] = 0;
+      if (!whole) {
+        const long long tok0 = (long long)t * w.tpt;
+        hi = (int)min((long long)w.tpt, w.s.n - tok0) * p.G - half * 64;
+        if (p.causal) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (c0 + e + i < lo || c0 + e + i >= hi) x[i] = -CUDART_INF_F;
-            }
-            ptx::add_f32x2(sum[0], sum[1], ex2(x[0]), ex2(x[1]));
-            ptx::add_f32x2(sum[2], sum[3], ex2(x[2]), ex2(x[3]));
+          for (int m = 0; m < NT; ++m) {
+            const long long tok = k0 + m * 128 + r - (w.s.Lk - w.s.n) - tok0;
+            lo[m] = tok > 0 ? (int)min(tok * p.G, 128ll) - half * 64 : 0;
           }
         }
-      };
-      if (whole)
-        add(std::false_type{});
-      else
-        add(std::true_type{});
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bars->s_empty[m][sb]));
+      }
+      bool ready = false;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t(&v)[NT][CH] = s[c & 1];
+        ptx::tmem_ld_wait(v[0]);
+        if constexpr (NT == 2) ptx::reg_fence(v[1]);
+        if (c < 3) {
+          load_chunk((c + 1) & 1, col + CH * (c + 1));
+        } else {  // the buffer is free
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(ptx::smem_u32(&bars->s_empty[sb]));
+          if (__all_sync(0xffffffffu, ready)) {
+            ptx::tc_fence_after();
+            load_chunk(0, next_col);
+          }
+        }
+        if (c == 2 && more) ready = ptx::mbar_test(next_full, next_parity);
+        auto add = [&](auto masked) {
+#pragma unroll
+          for (int e = 0; e < CH; e += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(ls + CH * c + e);
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+              float x[4];
+              ptx::fma_f32x2(x[0], x[1], __uint_as_float(v[m][e]), __uint_as_float(v[m][e + 1]),
+                             f[m], f[m], l.x, l.y);
+              ptx::fma_f32x2(x[2], x[3], __uint_as_float(v[m][e + 2]),
+                             __uint_as_float(v[m][e + 3]), f[m], f[m], l.z, l.w);
+              if constexpr (decltype(masked)::value) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (CH * c + e + i < lo[m] || CH * c + e + i >= hi) x[i] = -CUDART_INF_F;
+              }
+              ptx::add_f32x2(sum[m].x, sum[m].y, ex2(x[0]), ex2(x[1]));
+              ptx::add_f32x2(sum[m].x, sum[m].y, ex2(x[2]), ex2(x[3]));
+            }
+          }
+        };
+        if (whole)
+          add(std::false_type{});
+        else
+          add(std::true_type{});
+      }
+      if (more && !__all_sync(0xffffffffu, ready)) {
+        ok = warp_wait(p, bars, &bars->s_full[sb ^ 1], next_parity);
+        ptx::tc_fence_after();
+        if (ok) load_chunk(0, next_col);
+      }
     }
-    if (page >= 0 && ok) *to = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (half) {
+#pragma unroll
+      for (int m = 0; m < NT; ++m) sums[(si & 1) * C::KT + m * 128] = sum[m].x + sum[m].y;
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (half == 0 && ok) {
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+        if (to[m]) *to[m] = old[m] + (sum[m].x + sum[m].y + sums[(si & 1) * C::KT + m * 128]);
+    }
   }
 }
 
@@ -403,8 +498,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     for (int s = 0; s < 4; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->q_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->q_empty[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars->s_full[s >> 1][s & 1]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars->s_empty[s >> 1][s & 1]), 128);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bars->s_full[s]), 1 + 32);  // (the products, the logarithms)
+      ptx::mbar_init(ptx::smem_u32(&bars->s_empty[s]), 256);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
     bars->abort = 0;
@@ -427,12 +524,14 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   if (warp < C::SUM_WARPS) {
-    sum_role<C>(wp, bars, smem, tmem, w, slots, warp / 4, warp, lane);
+    sum_role<C>(wp, bars, smem, tmem, w, slots, warp, lane);
   } else if (warp == C::MMA_WARP) {
     mma_role<C, BF16>(p, bars, ptx::smem_u32(smem), __shfl_sync(0xffffffffu, tmem, 0), w, slots);
     mma_drain(p, bars);
   } else if (warp == C::LOAD_WARP) {
     if (lane == 0) load_role<C>(p, bars, smem, w, slots, &tm_q, &tm_c);
+  } else if (warp == C::LOG_WARP) {
+    log_role<C>(wp, bars, smem, w, slots, lane);
   } else if (C::CODES && warp >= C::CONV_WARP) {
     convert_role<C, BF16>(p, bars, smem, w, slots, threadIdx.x - C::CONV_WARP * 32);
   }

@@ -98,7 +98,14 @@ hstu_status hstu_kv_weights(const hstu_kv_cache* c, const hstu_weights_args* a, 
     w.a.by_length = rows_by_length(c->batch, pairs * w.a.splits, sms);
     e = launch_weights_rows(w, a->dtype, fmt, rows, s);
   } else {
-    e = launch_weights_tc(w, a->dtype, fmt, slots_for(4ll * sms, weights_tc_keys(c->head_dim)), s);
+    const int keys = weights_tc_keys(c->head_dim);
+    const long long steps = ((long long)a->max_seqlen_k + keys - 1) / keys;
+    const long long tiles = (most + 128 / G - 1) / (128 / G);  // of query rows
+    int slots = slots_for(2ll * sms, keys), cluster = 1;
+    if (slots == steps)
+      while (cluster < 8 && slots * pairs * cluster * 2 <= 2ll * sms && tiles >= 8 * cluster)
+        cluster *= 2;
+    e = launch_weights_tc(w, a->dtype, fmt, slots, cluster, s);
   }
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }

@@ -20,8 +20,9 @@ cudaError_t launch_weights_rows(const WeightsParams& w, int dtype, int fmt, int 
                                 cudaStream_t stream);
 
 // More rows, on the tensor cores; `slots` CTAs take turns at the key steps of a sequence and kv head.
+// Or clusters of `cluster` CTAs, which divide the query rows; they have a step each.
 int weights_tc_keys(int D);  // keys of a step
-cudaError_t launch_weights_tc(const WeightsParams& w, int dtype, int fmt, int slots,
+cudaError_t launch_weights_tc(const WeightsParams& w, int dtype, int fmt, int slots, int cluster,
                               cudaStream_t stream);
 
 // fp32 rows, on CUDA cores.

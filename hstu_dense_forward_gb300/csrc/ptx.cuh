@@ -123,6 +123,36 @@ __device__ __forceinline__ uint32_t mbar_tests(uint32_t b0, uint32_t p0, uint32_
   return ok;
 }
 
+// The same with what other CTAs of the cluster did before their arrivals visible.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A store to, and an arrival at, the place that an address of this CTA's shared memory has in
+// another CTA of the cluster.
+__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, float x) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(addr),
+      "r"(rank), "f"(x)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+
 // Blocking form: the thread is suspended until the phase completes or `ns`
 // nanoseconds pass, instead of spinning on the shared-memory pipe.
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity, uint32_t ns) {

@@ -11,7 +11,8 @@ namespace hstu {
   cudaError_t launch_weights_rows_##n(const WeightsParams& w, int fmt, const CUtensorMap& tc, \
                                       int rows, cudaStream_t s);                              \
   cudaError_t launch_weights_tc_##n(const WeightsParams& w, int fmt, const CUtensorMap& tq,   \
-                                    const CUtensorMap& tc, int slots, cudaStream_t s)
+                                    const CUtensorMap& tc, int slots, int cluster,            \
+                                    cudaStream_t s)
 HSTU_WEIGHTS_UNITS(bf16);
 HSTU_WEIGHTS_UNITS(fp16);
 #undef HSTU_WEIGHTS_UNITS
@@ -38,15 +39,15 @@ cudaError_t launch_weights_rows(const WeightsParams& w, int dtype, int fmt, int 
                             : launch_weights_rows_fp16(w, fmt, tc, rows, stream);
 }
 
-cudaError_t launch_weights_tc(const WeightsParams& w, int dtype, int fmt, int slots,
+cudaError_t launch_weights_tc(const WeightsParams& w, int dtype, int fmt, int slots, int cluster,
                               cudaStream_t stream) {
   CUtensorMap tq, tc = {};
   if (!query_map(&tq, w.a, dtype)) return cudaErrorInvalidValue;
   // (the keys of other caches are converted, from plain loads)
   if (fmt == kSame && !cache_map(&tc, w.a, dtype, false, 64, 128, 128))
     return cudaErrorInvalidValue;
-  return dtype == HSTU_BF16 ? launch_weights_tc_bf16(w, fmt, tq, tc, slots, stream)
-                            : launch_weights_tc_fp16(w, fmt, tq, tc, slots, stream);
+  return dtype == HSTU_BF16 ? launch_weights_tc_bf16(w, fmt, tq, tc, slots, cluster, stream)
+                            : launch_weights_tc_fp16(w, fmt, tq, tc, slots, cluster, stream);
 }
 
 }  // namespace hstu

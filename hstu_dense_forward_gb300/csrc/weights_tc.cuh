@@ -7,7 +7,9 @@
 //
 // A CTA keeps a step of KT keys (one or two tiles of 128) in shared memory and passes over the query
 // tiles (128 / G tokens each) that see any of them, then takes the next step of its share; the first
-// keys, which with the causal mask the most rows see, come first in the grid. Warp roles:
+// keys, which with the causal mask the most rows see, come first in the grid. Where there are few
+// steps, a cluster of CTAs divides the query tiles of one and adds its sums up in the first of them
+// (one prompt of 4096 tokens, two kv heads: 138 us alone). Warp roles:
 //   warps 0 .. 7          the sums, a warpgroup for each half of the columns, a thread for a key of
 //                         every tile: what belongs to a row is read once for both keys;
 //   next warp             issues every tcgen05.mma; owns TMEM;
@@ -20,6 +22,7 @@
 // Every wait is bounded (timeout_ns): on expiry the CTA reports HSTU_DEVERR_TIMEOUT, every role
 // leaves its loop, the MMAs in flight are waited for, TMEM is freed and the kernel returns.
 #pragma once
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -37,6 +40,8 @@ namespace wt {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
+constexpr int kMaxCluster = 8;
+
 template <int D_, int FMT_>
 struct Cfg {
   static constexpr int D = D_, FMT = FMT_;
@@ -45,10 +50,12 @@ struct Cfg {
   static constexpr int SWB = 128, EPC = 64, NCB = D / EPC;    // swizzled blocks of a row
   static constexpr int K_CB = KT * SWB, K_STEP = NCB * K_CB;
   static constexpr int Q_CB = 128 * SWB, Q_TILE = NCB * Q_CB;
-  static constexpr int NK = D == 64 ? 3 : 2, NQ = D == 256 ? 1 : D == 128 ? 2 : 4;
+  // (D = 256: with two steps of keys and one query tile four prompts of 4096 tokens took 334 us)
+  static constexpr int NK = D == 64 ? 3 : D == 128 ? 2 : 1, NQ = D == 64 ? 4 : 2;
   static constexpr int OFF_Q = NK * K_STEP, OFF_L = OFF_Q + NQ * Q_TILE;
   static constexpr int OFF_S = OFF_L + 4 * 128 * 4;         // rows' logarithms, of four tiles
-  static constexpr int OFF_BAR = OFF_S + 2 * KT * 4;        // half the columns' sums, of two steps
+  static constexpr int OFF_R = OFF_S + 2 * KT * 4;          // half the columns' sums, of two steps
+  static constexpr int OFF_BAR = OFF_R + (kMaxCluster - 1) * KT * 4;  // the other CTAs' sums
   static constexpr int USED = OFF_BAR + 512 + 1024;
   // (one CTA per SM, which takes its share of TMEM: no second one may come to wait for it)
   static constexpr int SMEM = USED < 120 * 1024 ? 120 * 1024 : USED;
@@ -61,7 +68,7 @@ struct Cfg {
 
 struct Bars {
   uint64_t k_full[3], k_empty[3], q_full[4], q_empty[4];
-  uint64_t s_full[2], s_empty[2], drain;
+  uint64_t s_full[2], s_empty[2], joined, drain;
   uint32_t tmem_base;
   volatile int abort;
 };
@@ -91,23 +98,40 @@ __device__ __forceinline__ bool warp_wait(const SoftmaxParams& p, Bars* bars, ui
   return __all_sync(0xffffffffu, wait_bar(p, bars, bar, parity));
 }
 
+// The cluster's other CTAs have stored their sums.
+__device__ __forceinline__ bool wait_joined(const SoftmaxParams& p, Bars* bars) {
+  const uint32_t a = ptx::smem_u32(&bars->joined);
+  const uint64_t start = ptx::globaltimer_ns();
+  while (!ptx::mbar_try_wait_cluster(a, 0)) {
+    if (bars->abort || (long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
+      bars->abort = 1;
+      report(p.c, HSTU_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// A CTA's work: steps first, first + slots, .. of one sequence and kv head.
+// A CTA's work: steps first, first + slots, .. of one sequence and kv head; of the query tiles, those
+// of its rank in the cluster, every cluster-th.
 struct Work {
   PagedSeq s;
   int b, hk, steps, first, tpt;
   int tiles;  // query tiles of the sequence
+  int rank, cluster;
 };
 
-// First query tile that sees a key of the step from k0 on.
+// First query tile of the CTA that sees a key of the step from k0 on.
 __device__ __forceinline__ int first_tile(const SoftmaxParams& p, const Work& w, long long k0) {
   const long long tok = p.causal ? k0 - (w.s.Lk - w.s.n) : 0;
-  return tok > 0 ? (int)min(tok / w.tpt, (long long)w.tiles) : 0;
+  const int t = tok > 0 ? (int)min(tok / w.tpt, (long long)w.tiles) : 0;
+  return t + (w.rank - t % w.cluster + w.cluster) % w.cluster;
 }
 
 // ------------------------------------------------------------------ loads
@@ -138,7 +162,7 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
                            cb * C::EPC, w.hk, (int)((k0 + r) & (ps - 1)), (int)(2 * page));
       }
     }
-    for (int t = first_tile(p, w, k0); t < w.tiles; ++t, ++qi) {
+    for (int t = first_tile(p, w, k0); t < w.tiles; t += w.cluster, ++qi) {
       const int slot = qi % C::NQ;
       if (!wait_bar(p, bars, &bars->q_empty[slot], ((qi / C::NQ) & 1) ^ 1)) return;
       const uint32_t bar = ptx::smem_u32(&bars->q_full[slot]);
@@ -241,7 +265,7 @@ __device__ void mma_role(const SoftmaxParams& p, Bars* bars, uint32_t sbase, uin
   for (int step = w.first; step < w.steps; step += slots, ++ki) {
     const int t0 = first_tile(p, w, (long long)step * C::KT), kslot = ki % C::NK;
     if (!warp_wait(p, bars, &bars->k_full[kslot], (ki / C::NK) & 1)) return;
-    for (int t = t0; t < w.tiles; ++t, ++qi) {
+    for (int t = t0; t < w.tiles; t += w.cluster, ++qi) {
       const int qslot = qi % C::NQ, sb = qi & 1;
       if (!warp_wait(p, bars, &bars->q_full[qslot], (qi / C::NQ) & 1)) return;
       const uint64_t bd0 = ptx::smem_desc(sbase + C::OFF_Q + qslot * C::Q_TILE, 16, 8 * C::SWB, 2);
@@ -312,11 +336,11 @@ __device__ void log_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, con
   for (int step = w.first; step < w.steps; step += slots) {
     const int t0 = first_tile(p, w, (long long)step * C::KT);
     float4 x = t0 < w.tiles ? load(t0) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int t = t0; t < w.tiles; ++t, ++qi) {
+    for (int t = t0; t < w.tiles; t += w.cluster, ++qi) {
       if (!warp_wait(p, bars, &bars->s_empty[qi & 1], ((qi >> 1) & 1) ^ 1)) return;
       logs[(qi & 3) * 32 + lane] = x;
       ptx::mbar_arrive(ptx::smem_u32(&bars->s_full[qi & 1]));
-      if (t + 1 < w.tiles) x = load(t + 1);
+      if (t + w.cluster < w.tiles) x = load(t + w.cluster);
     }
   }
 }
@@ -379,17 +403,18 @@ __device__ void sum_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, uin
       ptx::tc_fence_after();
       if (ok) load_chunk(0, s_col + (qi & 1) * NT * 128);
     }
-    for (int t = t0; t < w.tiles && ok; ++t, ++qi) {
+    for (int t = t0; t < w.tiles && ok; t += w.cluster, ++qi) {
       const int sb = qi & 1;
       const uint32_t col = s_col + sb * NT * 128, next_col = s_col + (sb ^ 1) * NT * 128;
       const uint32_t next_full = ptx::smem_u32(&bars->s_full[sb ^ 1]);
       const uint32_t next_parity = ((qi + 1) >> 1) & 1;
-      const bool more = t + 1 < w.tiles;
+      const bool more = t + w.cluster < w.tiles;
       const float* ls = logs + (qi & 3) * 128;
       const bool whole = t >= seen && t < full_tiles;
-      int lo[NT], hi = 0;  // columns [lo, hi) of this half see the key
+      // columns [lo, hi) of this half see the key; those of the warp's first key, and of its last
+      int lo[NT], first[NT], last[NT], hi = 64;
 #pragma unroll
-      for (int m = 0; m < NT; ++m) lo[m] = 0;
+      for (int m = 0; m < NT; ++m) lo[m] = first[m] = last[m] = 0;
       if (!whole) {
         const long long tok0 = (long long)t * w.tpt;
         hi = (int)min((long long)w.tpt, w.s.n - tok0) * p.G - half * 64;
@@ -397,53 +422,80 @@ __device__ void sum_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, uin
 #pragma unroll
           for (int m = 0; m < NT; ++m) {
             const long long tok = k0 + m * 128 + r - (w.s.Lk - w.s.n) - tok0;
-            lo[m] = tok > 0 ? (int)min(tok * p.G, 128ll) - half * 64 : 0;
+            lo[m] = (tok > 0 ? (int)min(tok * p.G, 128ll) : 0) - half * 64;
+            first[m] = __shfl_sync(0xffffffffu, lo[m], 0);
+            last[m] = __shfl_sync(0xffffffffu, lo[m], 31);
           }
         }
       }
       bool ready = false;
+      // (a loop of its own for tiles that are seen whole: branches in it cost 15 % of prompts)
+      auto sum_up = [&](auto masked) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t(&v)[NT][CH] = s[c & 1];
-        ptx::tmem_ld_wait(v[0]);
-        if constexpr (NT == 2) ptx::reg_fence(v[1]);
-        if (c < 3) {
-          load_chunk((c + 1) & 1, col + CH * (c + 1));
-        } else {  // the buffer is free
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(ptx::smem_u32(&bars->s_empty[sb]));
-          if (__all_sync(0xffffffffu, ready)) {
-            ptx::tc_fence_after();
-            load_chunk(0, next_col);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&v)[NT][CH] = s[c & 1];
+          ptx::tmem_ld_wait(v[0]);
+          if constexpr (NT == 2) ptx::reg_fence(v[1]);
+          if (c < 3) {
+            load_chunk((c + 1) & 1, col + CH * (c + 1));
+          } else {  // the buffer is free
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_u32(&bars->s_empty[sb]));
+            if (__all_sync(0xffffffffu, ready)) {
+              ptx::tc_fence_after();
+              load_chunk(0, next_col);
+            }
           }
-        }
-        if (c == 2 && more) ready = ptx::mbar_test(next_full, next_parity);
-        auto add = [&](auto masked) {
+          if (c == 2 && more) ready = ptx::mbar_test(next_full, next_parity);
+          // x of four columns of key tile m; the sum of their weights
+          auto exponents = [&](int m, int e, const float4& l, float (&x)[4]) {
+            ptx::fma_f32x2(x[0], x[1], __uint_as_float(v[m][e]), __uint_as_float(v[m][e + 1]), f[m],
+                           f[m], l.x, l.y);
+            ptx::fma_f32x2(x[2], x[3], __uint_as_float(v[m][e + 2]), __uint_as_float(v[m][e + 3]),
+                           f[m], f[m], l.z, l.w);
+          };
+          auto add = [&](int m, const float (&x)[4]) {
+            ptx::add_f32x2(sum[m].x, sum[m].y, ex2(x[0]), ex2(x[1]));
+            ptx::add_f32x2(sum[m].x, sum[m].y, ex2(x[2]), ex2(x[3]));
+          };
+          bool all = true;  // every column of the chunk sees the warp's keys
+          if constexpr (decltype(masked)::value) {
+            all = CH * (c + 1) <= hi;
 #pragma unroll
-          for (int e = 0; e < CH; e += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(ls + CH * c + e);
+            for (int m = 0; m < NT; ++m) all = all && CH * c >= last[m];
+          }
+          if (all) {
+#pragma unroll
+            for (int e = 0; e < CH; e += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(ls + CH * c + e);
+              float x[4];
+#pragma unroll
+              for (int m = 0; m < NT; ++m) {
+                exponents(m, e, l, x);
+                add(m, x);
+              }
+            }
+          } else if constexpr (decltype(masked)::value) {
 #pragma unroll
             for (int m = 0; m < NT; ++m) {
-              float x[4];
-              ptx::fma_f32x2(x[0], x[1], __uint_as_float(v[m][e]), __uint_as_float(v[m][e + 1]),
-                             f[m], f[m], l.x, l.y);
-              ptx::fma_f32x2(x[2], x[3], __uint_as_float(v[m][e + 2]),
-                             __uint_as_float(v[m][e + 3]), f[m], f[m], l.z, l.w);
-              if constexpr (decltype(masked)::value) {
+              if (CH * (c + 1) <= first[m] || CH * c >= hi) continue;  // none does
+#pragma unroll
+              for (int e = 0; e < CH; e += 4) {
+                float x[4];
+                exponents(m, e, *reinterpret_cast<const float4*>(ls + CH * c + e), x);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   if (CH * c + e + i < lo[m] || CH * c + e + i >= hi) x[i] = -CUDART_INF_F;
+                add(m, x);
               }
-              ptx::add_f32x2(sum[m].x, sum[m].y, ex2(x[0]), ex2(x[1]));
-              ptx::add_f32x2(sum[m].x, sum[m].y, ex2(x[2]), ex2(x[3]));
             }
           }
-        };
-        if (whole)
-          add(std::false_type{});
-        else
-          add(std::true_type{});
-      }
+        }
+      };
+      if (whole)
+        sum_up(std::false_type{});
+      else
+        sum_up(std::true_type{});
       if (more && !__all_sync(0xffffffffu, ready)) {
         ok = warp_wait(p, bars, &bars->s_full[sb ^ 1], next_parity);
         ptx::tc_fence_after();
@@ -456,9 +508,29 @@ __device__ void sum_role(const WeightsParams& wp, Bars* bars, uint8_t* smem, uin
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (half == 0 && ok) {
+      float total[NT];
 #pragma unroll
       for (int m = 0; m < NT; ++m)
-        if (to[m]) *to[m] = old[m] + (sum[m].x + sum[m].y + sums[(si & 1) * C::KT + m * 128]);
+        total[m] = sum[m].x + sum[m].y + sums[(si & 1) * C::KT + m * 128];
+      if (w.cluster > 1) {  // (one step: the first CTA adds the others' sums, in their order)
+        const uint32_t red = ptx::smem_u32(smem + C::OFF_R) + r * 4;
+        if (w.rank) {
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            ptx::store_remote(red + ((w.rank - 1) * C::KT + m * 128) * 4, 0, total[m]);
+          ptx::arrive_remote(ptx::smem_u32(&bars->joined), 0);
+          continue;
+        }
+        if (!wait_joined(p, bars)) continue;
+        for (int c = 1; c < w.cluster; ++c)
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            total[m] += reinterpret_cast<const float*>(
+                smem + C::OFF_R)[(c - 1) * C::KT + m * 128 + r];
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+        if (to[m]) *to[m] = old[m] + total[m];
     }
   }
 }
@@ -468,15 +540,17 @@ template <int D, bool BF16, int FMT>
 __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_c, const WeightsParams wp,
-                      int slots) {
+                      int slots, int cluster) {
   using C = Cfg<D, FMT>;
   const SoftmaxParams& p = wp.a;
   extern __shared__ uint8_t smem_raw[];
   Work w;
-  const unsigned pairs = (unsigned)p.c.B * p.c.Nk, pair = blockIdx.x % pairs;
+  const unsigned pairs = (unsigned)p.c.B * p.c.Nk, blk = blockIdx.x / cluster, pair = blk % pairs;
   w.hk = (int)(pair % p.c.Nk);
   w.b = (int)(pair / p.c.Nk);
-  w.first = (int)(blockIdx.x / pairs);
+  w.first = (int)(blk / pairs);
+  w.cluster = cluster;
+  w.rank = (int)(blockIdx.x % cluster);
   w.s = paged_seq(p.c, w.b);
   if (!attn_seq_ok(p, w.s)) {
     if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
@@ -504,6 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       ptx::mbar_init(ptx::smem_u32(&bars->s_empty[s]), 256);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->drain), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars->joined), 128 * (cluster > 1 ? cluster - 1 : 1));
     bars->abort = 0;
     ptx::fence_barrier_init();
   }
@@ -520,7 +595,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   }
   ptx::fence_proxy_async_smem();
   ptx::tc_fence_before();
-  __syncthreads();
+  if (cluster > 1)  // (the others' barriers are there)
+    cooperative_groups::this_cluster().sync();
+  else
+    __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   if (warp < C::SUM_WARPS) {
@@ -553,23 +631,32 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
 
 template <int D, bool BF16, int FMT>
 cudaError_t launch_variant(const WeightsParams& w, const CUtensorMap& tq, const CUtensorMap& tc,
-                           int slots, cudaStream_t stream) {
+                           int slots, int cluster, cudaStream_t stream) {
   using C = Cfg<D, FMT>;
   auto* kernel = weights_tc_kernel<D, BF16, FMT>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM, done);
   if (e != cudaSuccess) return e;
-  const long long blocks = (long long)w.a.c.B * w.a.c.Nk * slots;
-  kernel<<<dim3((unsigned)blocks), C::THREADS, C::SMEM, stream>>>(tq, tc, w, slots);
-  return cudaGetLastError();
+  const long long blocks = (long long)w.a.c.B * w.a.c.Nk * slots * cluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tq, tc, w, slots, cluster);
 }
 
 template <bool BF16, int FMT>
 cudaError_t launch_dim(const WeightsParams& w, const CUtensorMap& tq, const CUtensorMap& tc,
-                       int slots, cudaStream_t s) {
-  if (w.a.c.D > 128) return launch_variant<256, BF16, FMT>(w, tq, tc, slots, s);
-  if (w.a.c.D > 64) return launch_variant<128, BF16, FMT>(w, tq, tc, slots, s);
-  return launch_variant<64, BF16, FMT>(w, tq, tc, slots, s);
+                       int slots, int cluster, cudaStream_t s) {
+  if (w.a.c.D > 128) return launch_variant<256, BF16, FMT>(w, tq, tc, slots, cluster, s);
+  if (w.a.c.D > 64) return launch_variant<128, BF16, FMT>(w, tq, tc, slots, cluster, s);
+  return launch_variant<64, BF16, FMT>(w, tq, tc, slots, cluster, s);
 }
 
 }  // namespace wt

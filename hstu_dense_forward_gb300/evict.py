@@ -87,17 +87,8 @@ class _Table:
     __slots__ = ("packed", "device")
 
 
-def hstu_kv_select(weights, *, budget, max_seqlen_k, page_offsets, page_ids, last_page_len,
-                   recent=0, status=None):
-    """Choose the rows of a cache to keep, by their attention weights.
-
-    weights [num_pages, Nk, page_size] fp32 (hstu_kv_weights). Of every sequence and kv head,
-    min(length, budget) rows are kept: the last `recent` and those of the largest weights among the
-    others (of equal weights the earlier; a NaN counts as less than any). max_seqlen_k bounds the
-    lengths. Returns kept [B, Nk, budget] int32, their positions in increasing order and -1 behind
-    them, and the table of the shorter sequences, a dict of page_offsets, page_ids and last_page_len
-    as they are once hstu_kv_compact has moved the rows: each sequence keeps its first pages, and
-    entries of page_ids behind the last are -1. Pages that it no longer names are free."""
+def _explain_select(weights, page_offsets, page_ids, last_page_len):
+    """Raises for what is wrong with these tensors."""
     for t, name in ((weights, "weights"), (page_offsets, "page_offsets"), (page_ids, "page_ids"),
                     (last_page_len, "last_page_len")):
         if not isinstance(t, torch.Tensor):
@@ -111,16 +102,45 @@ def hstu_kv_select(weights, *, budget, max_seqlen_k, page_offsets, page_ids, las
         raise TypeError("index tensors must be int32 or int64")
     if page_offsets.dim() != 1 or page_offsets.shape[0] < 1 or page_ids.dim() != 1:
         raise ValueError("page_offsets must be [B + 1], page_ids one-dimensional")
-    pages, Nk, page_size = weights.shape
-    B, ids = page_offsets.shape[0] - 1, page_ids.shape[0]
-    w = _tensor(weights, "weights", dev, torch.float32, weights.shape)
-    table = (_tensor(page_offsets, "page_offsets", dev, index, (B + 1,)),
-             _tensor(page_ids, "page_ids", dev, index, (ids,)),
-             _tensor(last_page_len, "last_page_len", dev, index, (B,)))
+    B = page_offsets.shape[0] - 1
+    _tensor(weights, "weights", dev, torch.float32, weights.shape)
+    _tensor(page_offsets, "page_offsets", dev, index, (B + 1,))
+    _tensor(page_ids, "page_ids", dev, index, page_ids.shape)
+    _tensor(last_page_len, "last_page_len", dev, index, (B,))
+
+
+def hstu_kv_select(weights, *, budget, max_seqlen_k, page_offsets, page_ids, last_page_len,
+                   recent=0, status=None):
+    """Choose the rows of a cache to keep, by their attention weights.
+
+    weights [num_pages, Nk, page_size] fp32 (hstu_kv_weights). Of every sequence and kv head,
+    min(length, budget) rows are kept: the last `recent` and those of the largest weights among the
+    others (of equal weights the earlier; a NaN counts as less than any). max_seqlen_k bounds the
+    lengths. Returns kept [B, Nk, budget] int32, their positions in increasing order and -1 behind
+    them, and the table of the shorter sequences, a dict of page_offsets, page_ids and last_page_len
+    as they are once hstu_kv_compact has moved the rows: each sequence keeps its first pages, and
+    entries of page_ids behind the last are -1. Pages that it no longer names are free."""
+    try:  # one pass over what is usually right; _explain_select says what is not
+        dev = weights.get_device()
+        pages, Nk, page_size = weights.shape
+        index = page_offsets.dtype
+        B1, = page_offsets.shape
+        ids, = page_ids.shape
+        ok = (dev >= 0 and index in _INDEX and B1 > 0 and weights.dtype is torch.float32 and
+              weights.is_contiguous() and last_page_len.shape == (B1 - 1,))
+        for t in (page_offsets, page_ids, last_page_len):
+            ok = ok and t.dtype is index and t.get_device() == dev and t.is_contiguous()
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok:
+        _explain_select(weights, page_offsets, page_ids, last_page_len)
+        raise ValueError("weights and the page table do not fit together")
+    B = B1 - 1
     budget, recent = _count(budget, "budget", 1), min(_count(recent, "recent", 0, 1 << 62), _MOST)
     bound = _count(max_seqlen_k, "max_seqlen_k", 1)
-    status_ptr = 0 if status is None else _tensor(status, "status", dev, torch.int32, (1,))
-    kept = torch.empty((B, Nk, budget), dtype=torch.int32, device=dev)
+    status_ptr = 0 if status is None else _tensor(status, "status", weights.device, torch.int32,
+                                                  (1,))
+    kept = torch.empty((B, Nk, budget), dtype=torch.int32, device=weights.device)
     new = {"page_offsets": torch.empty_like(page_offsets), "page_ids": torch.empty_like(page_ids),
            "last_page_len": torch.empty_like(last_page_len)}
     if not B:  # nothing for the library to do
@@ -128,11 +148,12 @@ def hstu_kv_select(weights, *, budget, max_seqlen_k, page_offsets, page_ids, las
         new["page_ids"].fill_(-1)
         return kept, new
     t = _Table()
-    t.device = weights.get_device()
-    t.packed = _PACK_SELECT(B, Nk, page_size, index is torch.int64, pages, *table, ids, w, budget,
-                            recent, bound, 0, kept.data_ptr(), new["page_offsets"].data_ptr(),
-                            new["page_ids"].data_ptr(), new["last_page_len"].data_ptr(),
-                            status_ptr)
+    t.device = dev
+    t.packed = _PACK_SELECT(B, Nk, page_size, index is torch.int64, pages, page_offsets.data_ptr(),
+                            page_ids.data_ptr(), last_page_len.data_ptr(), ids, weights.data_ptr(),
+                            budget, recent, bound, 0, kept.data_ptr(),
+                            new["page_offsets"].data_ptr(), new["page_ids"].data_ptr(),
+                            new["last_page_len"].data_ptr(), status_ptr)
     _call("hstu_kv_select", t)
     return kept, new
 

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
   const KeyRanges kr = key_ranges(p, it.s.Lk);
   it.nsplit = kr.count;
   it.m0 = 0;
-  it.rows = it.s.n * p.G;
+  it.rows = p.Nq ? it.s.n * p.G : 0;
   it.k0 = it.split * kr.keys;
   it.kend = min(it.s.Lk, it.k0 + kr.keys);
   if (it.k0 >= it.kend || (it.rows == 0 && w.accumulate)) return;

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightsPar
     if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
     return;
   }
-  const long long rows = s.n * p.G;
+  const long long rows = p.Nq ? s.n * p.G : 0;
   if (rows == 0 && w.accumulate) return;
   float fk = p.scale_log2;
   if (p.c.k_ds) fk *= p.c.k_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];

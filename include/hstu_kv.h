@@ -134,13 +134,14 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * sequence are left alone.
  *
  * Statistics and sums are fp32. fp16 and bf16: the weights are rounded to the type of q for the
- * product with V, or to fp16 over an E4M3 or E2M1 cache (bf16 weights of at most 16 rows of a kv head over
- * a bf16 cache, single tokens for instance, come in two parts, whose sum is exact to 2^-16).
- * fp16 holds what is 2^-24 of the largest of the weights, or, over such a cache, of the weights
- * times their rows' scales. Rows of such a cache keep their bits whatever the scales of others,
- * but those of scale 2^-100 or less (rows of zeros) may count as zeros, and their weights with the
- * largest scale of the 127 rows around them. bf16 queries over it are products of fp16
- * with a power of two of their row: elements below 2^-38 of its largest vanish.
+ * product with V, or to fp16 over an E4M3 or E2M1 cache (the weights of at most 16 rows of a kv
+ * head, single tokens for instance, come in two parts: bf16 ones over a bf16 cache, whose sum is
+ * exact to 2^-16, and those of fp16 queries over an E2M1 cache). fp16 holds what is 2^-24 of the
+ * largest of the weights, or, over an E4M3 or E2M1 cache, of the weights times their rows' scales.
+ * Rows of such a cache keep their bits whatever the scales of others, but those of scale 2^-100 or
+ * less (rows of zeros) may count as zeros, and their weights with the largest scale of the 127 rows
+ * around them. bf16 queries over such a cache are products of fp16 with a power of two of their row:
+ * elements below 2^-38 of its largest vanish.
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */

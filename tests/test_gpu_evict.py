@@ -158,6 +158,32 @@ def test_weights_without_queries(cuda_device):
     assert (w[used] == 0).all() and torch.equal(w[~used], before[~used])
 
 
+def test_weights_of_queries_without_heads(cuda_device):
+    """Rows of no heads add nothing; stored, 0."""
+    dev = cuda_device
+    for dtype in (torch.bfloat16, torch.float32):
+        t = R.Table([40, 0, 7], 32)
+        cache, _, kw = _cache(t, 2, 64, dtype, "same", dev, 3)
+        w = torch.rand(t.num_pages, 2, 32, device=dev)
+        before = w.clone()
+        args = dict(max_seqlen=3, max_seqlen_k=64, **t.args(dev))
+        q, lse = torch.empty(6, 0, 64, dtype=dtype, device=dev), torch.empty(6, 0, device=dev)
+        so = R.offsets([3, 0, 3]).to(dev)
+        hstu_kv_weights(q, lse, cache, so, w, **args)
+        assert torch.equal(w, before)
+        hstu_kv_weights(q, lse, cache, so, w, accumulate=False, **args)
+        used = torch.tensor(_used(t)).to(dev)[:, None].expand(-1, 2, -1)
+        assert (w[used] == 0).all() and torch.equal(w[~used], before[~used])
+
+
+@pytest.mark.parametrize("dtype,mode,n,Nq,Nk,D", [("bf16", "same", 2100, 4, 1, 128), ("fp16", "scale", 700, 16, 1, 64),
+                                                  ("bf16", "fp4", 1500, 8, 2, 32), ("fp16", "same", 900, 8, 1, 256)])
+def test_weights_of_few_prompts(cuda_device, dtype, mode, n, Nq, Nk, D):
+    """Clusters of CTAs divide the query rows of a step of keys; a short sequence beside."""
+    for causal in (True, False):
+        run_weights(cuda_device, [n, 9], [n, 5], dtype, mode, Nq, Nk, D, 128, causal=causal, seed=111)
+
+
 # ------------------------------------------------------------------ select
 def check_select(dev, t, weights, budget, recent, bound=None):
     Nk, ps = weights.shape[1], t.page_size
@@ -224,6 +250,14 @@ def test_select_of_long_sequences(cuda_device, length, budget, recent):
     w = torch.exp(2 * torch.randn(t.num_pages, 2, 256, generator=g))
     w[torch.rand(w.shape, generator=g) < 0.4] = 0
     check_select(cuda_device, t, w.to(cuda_device), budget, recent)
+
+
+def test_select_of_one_long_sequence_among_many(cuda_device):
+    """Lists that a CTA each works on, one of more positions than its shared memory holds."""
+    t = R.Table([70000] + [40] * 330, 128, seed=12)
+    g = torch.Generator().manual_seed(10)
+    w = torch.exp(2 * torch.randn(t.num_pages, 1, 128, generator=g))
+    check_select(cuda_device, t, w.to(cuda_device), 30000, 100)
 
 
 def test_select_of_many_sequences(cuda_device):

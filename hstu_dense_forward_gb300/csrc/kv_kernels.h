@@ -27,6 +27,10 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
                            long long v_stride, int dtype, int fmt, bool append, int sms,
                            cudaStream_t stream);
 
+// The pages that the table of an E2M1 cache names, as bf16 [num_page_ids, 2, page_size, Nk, D], and
+// their ids 0, 1, .. (-1 for one outside the cache).
+cudaError_t launch_expand(const CacheView& c, void* pages, void* ids, cudaStream_t stream);
+
 // fp32 attention on CUDA cores: `rows` (4 or 64) packed query rows of one kv head per CTA.
 cudaError_t launch_softmax_simt(const SoftmaxParams& p, int fmt, int rows, long long tiles,
                                 long long blocks, cudaStream_t stream);

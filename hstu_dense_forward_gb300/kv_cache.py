@@ -240,12 +240,12 @@ def _copy(name, c, k, v, seq_offsets, new=False):
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(device, cache_sizes, attn_sizes):
+def _workspace_bytes(device, cache_sizes, attn_sizes, num_ids):
     """hstu_softmax_workspace for these sizes (it reads no pointer) on this device."""
     need = ctypes.c_longlong(0)
     with torch.cuda.device(device):
         _abi.check(_abi.lib().hstu_softmax_workspace(
-            _PACK_CACHE(*cache_sizes, 0, 0, 0, 1, 0, 0, 0, 0, 0, 0, 0, 0),
+            _PACK_CACHE(*cache_sizes, 0, 0, 0, 1, 0, 0, 0, num_ids, 0, 0, 0, 0),
             _PACK_ATTN(0, 0, 0, *attn_sizes, 0, 0, 0, 0, 0), ctypes.byref(need)),
             "hstu_softmax_workspace")
     return need.value
@@ -353,7 +353,8 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
     lse = torch.empty((T, Nq), dtype=torch.float32, device=q.device) if return_lse else None
     sizes = (T, dtype, Nq, int(max_seqlen), int(max_seqlen_k), bool(causal), float(alpha))
     try:
-        need = _workspace_bytes(c.device, c.sizes, sizes)
+        need = _workspace_bytes(c.device, c.sizes, sizes,
+                                page_ids.shape[0] if kv_group_scale is not None else 0)
     except (struct.error, OverflowError):  # max_seqlen, max_seqlen_k or alpha that no C type holds
         raise _abi.HstuError(_abi.HSTU_ERR_INVALID_ARG, "hstu_softmax_fwd") from None
     workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None

@@ -163,7 +163,8 @@ typedef struct {
   int reserved;           /* must be 0 */
 } hstu_softmax_args;
 
-/* Bytes of workspace that hstu_softmax_fwd needs for these sizes (pointers are not read). */
+/* Bytes of workspace that hstu_softmax_fwd needs for these sizes (pointers are not read; of an E2M1
+ * cache num_page_ids counts, whose pages may be held there as bf16). */
 HSTU_API hstu_status hstu_softmax_workspace(const hstu_kv_cache* cache,
                                             const hstu_softmax_args* args, long long* bytes);
 

@@ -188,6 +188,41 @@ def test_prompts(cuda_device, dtype, Nq, Nk, D, ps, causal):
     run_case(cuda_device, *S.PROMPT, dtype, Nq, Nk, D, ps, causal=causal, seed=71)
 
 
+# prompts of bf16 queries of 768 rows of a kv head in the mean and more, over pages turned into bf16
+LONG = ([300, 1000, 70, 700, 40, 0], [300, 999, 70, 331, 0, 0])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Nq,Nk,D,ps,index", [(8, 2, 128, 128, torch.int64), (6, 2, 64, 32, torch.int32), (5, 1, 32, 256, torch.int64),
+                                              (12, 3, 192, 128, torch.int32), (16, 4, 96, 32, torch.int64)])
+def test_long_prompts(cuda_device, Nq, Nk, D, ps, index, causal):
+    run_case(cuda_device, *LONG, "bf16", Nq, Nk, D, ps, causal=causal, index=index, seed=81, strided=Nk == 2)
+
+
+def test_long_prompts_over_bad_pages(cuda_device):
+    """Page ids outside the cache, in a sequence and behind the last: the others' outputs are right,
+    and only ids that a sequence has are told."""
+    dev = cuda_device
+    t = R.Table([600, 600, 600], 128)
+    n = [600, 600, 600]
+    cache, vals, kw = _filled(t, 1, 64, dev, 5)
+    q = torch.randn(1800, 4, 64, device=dev).to(torch.bfloat16)
+    args = {**t.args(dev), **kw}
+    args["page_ids"] = torch.cat([args["page_ids"], torch.tensor([-1, 1 << 40, -7], device=dev)])
+    for bad in (False, True):
+        if bad:
+            args["page_ids"][7] = t.num_pages
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        out, lse = hstu_softmax_fwd(q, cache, R.offsets(n).to(dev), max_seqlen=600, max_seqlen_k=600, alpha=0.125,
+                                    return_lse=True, status=status, **args)
+        assert status.item() == bad
+        for b in (0, 2) if bad else (0, 1, 2):
+            one = R.Table([600], 128)
+            one.page_offsets, one.page_ids = torch.tensor([0, 5]), t.page_ids[5 * b:5 * b + 5]
+            at = slice(600 * b, 600 * b + 600)
+            S.check(one, [600], q[at], vals, out[at], lse[at], True, 0.125, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype,n,D", [("bf16", 300, 128), ("fp16", 200, 64), ("bf16", 30, 256), ("fp16", 6, 64),
                                        ("bf16", 3, 128), ("fp32", 3, 128)])
 def test_items_over_many_ctas(cuda_device, dtype, n, D):

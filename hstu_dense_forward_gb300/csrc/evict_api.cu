@@ -88,7 +88,10 @@ hstu_status hstu_kv_weights(const hstu_kv_cache* c, const hstu_weights_args* a, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->dtype == HSTU_F32) {
-    e = launch_weights_simt(w, fmt, slots_for(4ll * sms, kWeightsSimtKeys), s);
+    const bool few = none || most * G <= 16;
+    const int slots = slots_for((few ? 16ll : 4ll) * sms, few ? 128 : kWeightsSimtKeys);
+    if (few) w.a.splits = slots;
+    e = launch_weights_simt(w, fmt, few ? 0 : slots, s);
   } else if (none || most * G <= 16) {
     // one wave of CTAs, each with a stretch of the keys
     const int rows = none || most * G <= 8 ? 8 : 16;

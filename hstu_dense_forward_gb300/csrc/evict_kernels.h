@@ -25,7 +25,8 @@ int weights_tc_keys(int D);  // keys of a step
 cudaError_t launch_weights_tc(const WeightsParams& w, int dtype, int fmt, int slots, int cluster,
                               cudaStream_t stream);
 
-// fp32 rows, on CUDA cores.
+// fp32 rows, on CUDA cores; slots = 0: at most 16 of a kv head and sequence, whose keys a.splits CTAs
+// divide.
 cudaError_t launch_weights_simt(const WeightsParams& w, int fmt, int slots, cudaStream_t stream);
 constexpr int kWeightsSimtKeys = 64;  // keys of a step
 

@@ -1,7 +1,14 @@
-// Attention weights of the cached keys from fp32 query rows, on CUDA cores (FFMA). A CTA holds 64 keys
-// of one kv head in shared memory and passes over the packed query rows that see any of them, 64 at a
-// time: a thread owns keys tx + 16 c and rows ty + 16 a, whose weights it adds up over the rows; the
-// sums of the sixteen ty are joined in order at the end. Then the next 64 keys of its share.
+// Attention weights of the cached keys from fp32 query rows, on CUDA cores (FFMA).
+//
+// weights_simt_kernel: a CTA holds 64 keys of one kv head in shared memory and passes over the packed
+// query rows that see any of them, 64 at a time: a thread owns keys tx + 16 c and rows ty + 16 a, whose
+// weights it adds up over the rows; the sums of the sixteen ty are joined in order at the end. Then
+// the next 64 keys of its share. Shared memory's loads of the operands bound it (the last 64 tokens of
+// two sequences of some 10,000, two kv heads of four: 105 us, 23 TFLOP/s).
+//
+// weights_few_kernel: calls of at most 16 rows, where reading the keys counts: D / 16 lanes hold a key,
+// straight from the cache in registers, and go through the rows (64 sequences of one token over some
+// 2500 keys of four heads, D = 128: 67 us, 5.1 TB/s, with the kernel above 380).
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -148,8 +155,103 @@ __global__ void __launch_bounds__(kThreads) weights_simt_kernel(const WeightsPar
   }
 }
 
+constexpr int kFewRows = 16, kFewThreads = 128;
+
+template <int D_, int FMT>
+__global__ void __launch_bounds__(kFewThreads) weights_few_kernel(const WeightsParams w) {
+  constexpr int U = FMT != kSame ? 4 : 2, LPK = D_ / 16, KW = 32 / LPK;
+  constexpr int WARPS = kFewThreads / 32, STEP = WARPS * U * KW;  // keys of a step
+  __shared__ float4 qs[kFewRows][4][LPK];
+  __shared__ float logs[kFewRows];
+  __shared__ int lims[kFewRows];  // keys of the range that each row sees: [0, lim)
+  const SoftmaxParams& p = w.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = lane % LPK, g = lane / LPK;
+  const int hk = (int)(blockIdx.x % (unsigned)p.c.Nk), b = (int)(blockIdx.x / (unsigned)p.c.Nk);
+  const PagedSeq s = paged_seq(p.c, b);
+  const long long all = p.Nq ? s.n * p.G : 0;
+  if (!attn_seq_ok(p, s) || all > kFewRows) {
+    if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+    return;
+  }
+  const KeyRanges kr = key_ranges(p, s.Lk);
+  const long long k0 = blockIdx.y * kr.keys, kend = min(s.Lk, k0 + kr.keys);
+  const int rows = (int)all, keys = (int)(kend - k0);
+  if (k0 >= kend || (rows == 0 && w.accumulate)) return;
+  const float* q = static_cast<const float*>(p.q);
+  for (int x = threadIdx.x; x < rows * 4 * LPK; x += kFewThreads) {
+    const int r = x / (4 * LPK), i = x / LPK % 4, d = few_dim<D_, FMT>(i, x % LPK);
+    qs[r][i][x % LPK] = d < p.c.D
+        ? *reinterpret_cast<const float4*>(q + (s.t0 + r / p.G) * p.q_stride +
+                                           (hk * p.G + r % p.G) * (long long)p.c.D + d)
+        : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (threadIdx.x < rows) {
+    const int r = threadIdx.x;
+    logs[r] = w.lse[(s.t0 + r / p.G) * p.Nq + hk * p.G + r % p.G] * kLog2e;
+    const long long see = p.causal ? s.Lk - s.n + r / p.G + 1 : s.Lk;
+    lims[r] = (int)(min(see, kend) - k0);
+  }
+  float fk = p.scale_log2;
+  if (p.c.k_ds) fk *= p.c.k_ds[(long long)b * p.c.ds_b + (long long)hk * p.c.ds_h];
+  __syncthreads();
+  const int mine = warp * U * KW + g;  // this group's keys of a step: mine, mine + KW ..
+  auto page_of = [&](int n) { return n < keys ? (int)page_at(p.c, s, k0 + n) : -1; };
+  int next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) next[u] = page_of(mine + u * KW);
+  for (int n0 = 0; n0 < keys; n0 += STEP) {
+    FewRow<FMT> k[U];
+    float* to[U];
+    float old[U], sum[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + mine + u * KW, row = (int)(k0 + n) & (int)(page_size(p.c) - 1);
+      const int page = next[u];
+      if (page < 0 && n < keys) report(p.c, HSTU_DEVERR_OFFSETS);
+      k[u].template load<D_>(p.c, page, 0, row, hk, j);
+      to[u] = page >= 0 && j == 0
+                  ? w.weights + (((long long)page * p.c.Nk + hk) << p.c.page_shift) + row
+                  : nullptr;
+      old[u] = w.accumulate && to[u] ? *to[u] : 0.f;
+      sum[u] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) next[u] = page_of(n0 + STEP + mine + u * KW);
+    float4 f[U][4];
+    float fu[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      k[u].get(f[u]);
+      fu[u] = fk * k[u].factor();
+    }
+    for (int r = 0; r < rows; ++r) {
+      float4 qr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qr[i] = qs[r][i][j];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x = dot4(qr[i], f[u][i], x);
+#pragma unroll
+        for (int d = 1; d < LPK; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (n0 + mine + u * KW < lims[r]) sum[u] += exp2f(fmaf(x, fu[u], -logs[r]));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (to[u]) *to[u] = old[u] + sum[u];
+  }
+}
+
 template <int D, int FMT>
 cudaError_t launch(const WeightsParams& w, int slots, cudaStream_t stream) {
+  if (slots == 0) {
+    weights_few_kernel<D, FMT>
+        <<<dim3((unsigned)(w.a.c.B * (long long)w.a.c.Nk), w.a.splits), kFewThreads, 0, stream>>>(w);
+    return cudaGetLastError();
+  }
   using C = Cfg<D>;
   auto* kernel = weights_simt_kernel<D, FMT>;
   static std::atomic<unsigned long long> done;

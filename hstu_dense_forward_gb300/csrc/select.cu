@@ -61,9 +61,12 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warps, l
   return before + v - x;
 }
 
-// Page offsets and last pages' lengths of the shorter sequences, by one CTA.
+// Page offsets and last pages' lengths of the shorter sequences, by one CTA. (Sequences whose entries
+// of page_ids overlap can have more pages than new_page_ids holds: the offsets stop behind its end,
+// where they are no valid table's.)
 __global__ void __launch_bounds__(kThreads) new_table_kernel(const SelectParams p) {
   __shared__ long long warps[kWarps];
+  const long long most = p.c.index64 ? p.c.num_page_ids + 1 : min(p.c.num_page_ids + 1, 0x7fffffffll);
   long long carry = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
@@ -79,10 +82,10 @@ __global__ void __launch_bounds__(kThreads) new_table_kernel(const SelectParams 
     }
     long long total;
     const long long before = block_scan(pages, warps, total);
-    if (b < p.c.B) store_index(p.new_page_offsets, b, p.c.index64, carry + before);
+    if (b < p.c.B) store_index(p.new_page_offsets, b, p.c.index64, min(carry + before, most));
     carry += total;
   }
-  if (threadIdx.x == 0) store_index(p.new_page_offsets, p.c.B, p.c.index64, carry);
+  if (threadIdx.x == 0) store_index(p.new_page_offsets, p.c.B, p.c.index64, min(carry, most));
 }
 
 constexpr int kMaxKeys = 49152;  // of a CTA that shared memory holds; others are read anew
@@ -113,7 +116,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
 
   if (hk == 0 && rank == 0) {  // the sequence's page ids, and -1 behind the last sequence's
     const long long first = load_index(p.new_page_offsets, b, p.c.index64);
-    const long long pages = load_index(p.new_page_offsets, b + 1, p.c.index64) - first;
+    long long pages = load_index(p.new_page_offsets, b + 1, p.c.index64) - first;
+    if (pages > p.c.num_page_ids - first) {  // (entries that overlap)
+      if (tid == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+      pages = p.c.num_page_ids - first;
+    }
     for (long long i = tid; i < pages; i += kThreads)
       store_index(p.new_page_ids, first + i, p.c.index64,
                   load_index(p.c.page_ids, s.po + i, p.c.index64));

@@ -59,7 +59,9 @@ HSTU_API hstu_status hstu_kv_weights(const hstu_kv_cache* cache, const hstu_weig
  *
  * new_page_offsets, new_last_page_len and new_page_ids describe the sequences once their kept rows
  * lie at positions 0 .. keep - 1: the first pages of each, without gaps; -1 behind the last id
- * (and in place of ids of a sequence whose table is invalid, which keeps no page).
+ * (and in place of ids of a sequence whose table is invalid, which keeps no page). Where
+ * sequences share entries of page_ids and the new table would be longer than that array, this is
+ * reported, and the new table invalid from there on.
  */
 typedef struct {
   int batch;              /* as in hstu_kv_cache */

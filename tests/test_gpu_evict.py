@@ -379,6 +379,15 @@ def test_lists_and_tables_that_the_device_rejects(cuda_device):
             status = torch.zeros(1, dtype=torch.int32, device=dev)
             call(status)
             assert status.item() == 1
+    # sequences that share entries of page_ids: more of them than there is room for
+    for index in (torch.int32, torch.int64):
+        table = dict(page_offsets=torch.tensor([0, 8, 3, 8], dtype=index, device=dev),
+                     page_ids=torch.arange(8, dtype=index, device=dev),
+                     last_page_len=torch.tensor([32, 32, 32], dtype=index, device=dev))
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        kept, new = hstu_kv_select(torch.rand(8, 1, 32, device=dev), budget=256, max_seqlen_k=256, status=status, **table)
+        assert status.item() == 1 and new["page_offsets"].tolist() == [0, 8, 8, 9]
+        assert new["page_ids"].tolist() == list(range(8))
     # a length above its bound leaves the sequence out
     status = torch.zeros(1, dtype=torch.int32, device=dev)
     kept, new = hstu_kv_select(w, budget=30, max_seqlen_k=64, status=status, **good)

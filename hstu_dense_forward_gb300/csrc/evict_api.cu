@@ -192,8 +192,8 @@ hstu_status hstu_kv_compact(const hstu_kv_cache* c, const hstu_compact_args* a, 
   p.row_bytes = row_bytes(c);
   p.by_head = cache_format(c->dtype) == kE2m1;
   p.counter = static_cast<int*>(a->workspace);
-  p.loaded = p.counter + 4;
-  p.timeout_ns = 1000000000ll;
+  p.state = p.counter + 4;
+  p.timeout_ns = 1000000000u;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   return launch_compact(p, (int)compact_chunks(c, a), sms, static_cast<cudaStream_t>(stream)) ==

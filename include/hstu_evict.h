@@ -92,7 +92,7 @@ HSTU_API hstu_status hstu_kv_select(const hstu_select_args* args, void* stream);
  * (scales and factors too, and its entry of weights, if given) that position kept[b, hk, r] holds,
  * for r = 0, 1, .. as long as kept[b, hk, r] >= 0 (at most budget). cache describes the sequences as
  * they were. Positions increase with r (hstu_kv_select's do); a list where they do not, or pass the
- * sequence's length, ends there. Other rows are left as they are.
+ * sequence's length, is reported and ends there. Other rows are left as they are.
  */
 typedef struct {
   const int* kept;        /* [B, Nk, budget], 4-byte aligned */

@@ -351,6 +351,32 @@ def test_compact_again_is_no_change(cuda_device):
     check_compact(cuda_device, t, 2, 64, "same", torch.bfloat16, _lists(t, 2, 300, 1, "first"))
 
 
+@pytest.mark.parametrize("mode,D,budget", [("same", 128, 20), ("same", 128, 3000), ("fp4", 64, 3000), ("scale", 256, 3000)])
+@pytest.mark.parametrize("at", [1, 17, 64, 128, 1000, 2999])
+@pytest.mark.parametrize("kind", ["same again", "before", "ended", "behind"])
+def test_lists_that_do_not_increase_end_there(cuda_device, mode, D, budget, at, kind):
+    """Of short lists and of those that many CTAs move, with as good as anything behind the end."""
+    if at >= budget:
+        return
+    dev, ps = cuda_device, 32
+    t = R.Table([4000, 3500], ps, torch.int32, seed=3)
+    whole = _lists(t, 1, budget, 4)
+    bad, ended = whole.copy(), whole.copy()
+    ended[1, 0, at:] = -1
+    bad[1, 0, at] = {"same again": bad[1, 0, at - 1], "before": bad[1, 0, 0] - (bad[1, 0, 0] > 0), "ended": -1, "behind": 3500}[kind]
+    if kind != "ended":
+        bad[1, 0, at + 1:at + 7] = np.array([5, 5, 1 << 30, 70, -3, 0])[:max(0, budget - at - 1)]
+    results = []
+    for lists in (bad, ended):
+        cache, _, kw = _cache(t, 1, D, torch.bfloat16, mode, dev, 5)
+        w = torch.rand(t.num_pages, 1, ps, device=dev, generator=torch.Generator(device=dev).manual_seed(1))
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        hstu_kv_compact(cache, torch.tensor(lists, device=dev), weights=w, status=status, **t.args(dev), **kw)
+        assert status.item() == (lists is bad and kind != "ended")
+        results.append([x.contiguous().view(torch.uint8) for x in (cache, w, *kw.values())])
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
 def test_lists_and_tables_that_the_device_rejects(cuda_device):
     """Positions out of range and page ids out of range: no access outside, a status, the rest done."""
     dev = cuda_device

@@ -617,7 +617,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   }
   __syncwarp();
   ptx::tc_fence_before();
-  __syncthreads();
+  if (cluster > 1)  // (the first CTA stays until the others have stored their sums there)
+    cooperative_groups::this_cluster().sync();
+  else
+    __syncthreads();
   if (bars->abort) {
     // copies that were issued but never consumed land before the CTA exits
     const uint64_t start = ptx::globaltimer_ns();

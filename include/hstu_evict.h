@@ -27,9 +27,9 @@ extern "C" {
  *   exp(alpha * sum_d q[i, h, d] * k[j, hk, d] - lse[i, h])
  * is added to weights[page, hk, row of j], or stored there. Every cached row of a valid sequence
  * takes part: where no query sees it, 0 is added or stored. Elements of weights that belong to no
- * cached row are left alone. Scores and sums are fp32, products exact (bf16 queries over an E4M3 or
- * E2M1 cache: as hstu_softmax_fwd has them, or exact). The result does not depend on the order in
- * which anything runs.
+ * cached row are left alone; a key that holds an infinity or a NaN may be given a NaN. Scores and
+ * sums are fp32, products exact (bf16 queries over an E4M3 or E2M1 cache: as hstu_softmax_fwd has
+ * them, or exact). The result does not depend on the order in which anything runs.
  */
 typedef struct {
   const void* q;          /* as in hstu_softmax_args */

@@ -3,12 +3,13 @@
 // Rank r of a (sequence, kv head) takes the row at position kept[r] >= r. Ranks are moved in chunks,
 // each by a CTA that holds the chunk's rows in registers between its loads and its stores. Positions
 // increase with the ranks, so that what a chunk overwrites can be a source of that chunk and of those
-// in front of it only: it stores once those have loaded, and found that the list goes on so far. It
-// looks back for that, up to one that has looked back itself. Chunks are handed out by a counter, in
-// order for every (sequence, kv head), and load without waiting for anything, so that a chunk waits
-// for loads alone that are under way. (One CTA for all of a (sequence, kv head), chunk after chunk: 128
-// of 4096 ranks of 256-byte rows took 312 us, one of 50,000 3355.) Bound by memory: a kept row is read
-// once and written once.
+// in front of it only: it stores once those have loaded. Chunks are handed out by a counter, in order
+// for every (sequence, kv head), and load without waiting for anything, so that a chunk waits for
+// loads alone that are under way. (One CTA for all of a (sequence, kv head), chunk after chunk: 128
+// of 4096 ranks of 256-byte rows took 312 us, one of 50,000 3355; now 103 and 28.) Lists that do not
+// increase end there: a launch of its own finds where, 4 us of the 103. (Chunks that ask all in front
+// of them wait for CTAs that are at an earlier chunk yet: eight lists that keep 40,000 of 100,000 rows
+// took 105 us in place of 79.) Bound by memory: a kept row is read once and written once.
 #include "common.cuh"
 #include "evict_kernels.h"
 #include "kernels.h"
@@ -38,20 +39,34 @@ __device__ __forceinline__ void store_release(int* p, int x) {
   asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
 }
 
-__device__ __forceinline__ uint32_t now_ns() {
-  uint32_t t;
-  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-  return t;
+// Whether rank r is none of the list's, whose positions increase.
+__device__ __forceinline__ bool ends_at(const int* kept, int r, long long Lk) {
+  const int src = kept[r];
+  return src >= Lk || src <= (r ? kept[r - 1] : -1);
 }
 
-// What is known of a chunk: nothing yet, that its rows have been read, that the list has ended, or that
-// it and all in front of it have been read and go on.
-enum { kUnread = 0, kRead = 1, kEnded = 2, kAllRead = 3 };
+// Where lists end: ends[pair] becomes kNoEnd - the first rank that is none of the list's, and stays 0
+// where all are. A warp for each chunk.
+constexpr int kNoEnd = 0x7fffffff;
+__global__ void __launch_bounds__(kThreads) lists_kernel(const CompactParams p, int rows, int chunks) {
+  const long long ticket = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (ticket >= (long long)p.c.B * p.c.Nk * chunks) return;
+  const long long pair = ticket / chunks;
+  const PagedSeq s = paged_table(p.c, pair / p.c.Nk);
+  const int* kept = p.kept + pair * p.budget;
+  const int most = s.ok && s.Lk <= p.max_k ? (int)min(s.Lk, (long long)p.budget) : 0;
+  const int r0 = (int)(ticket % chunks) * rows, last = min(r0 + rows, most);
+  for (int r = r0 + (threadIdx.x & 31); r < last; r += 32)
+    if (ends_at(kept, r, s.Lk)) {
+      atomicMax(p.ends + pair, kNoEnd - r);
+      break;
+    }
+}
 
 __global__ void __launch_bounds__(kThreads, kCtas)
     compact_kernel(const CompactParams p, int rows, int chunks, int lanes_shift) {
   __shared__ Move moves[kCompactRows];
-  __shared__ int s_ticket, s_any, s_late, s_end, s_ended;
+  __shared__ int s_ticket, s_any, s_wait, s_late, s_end, s_before[2];
   const int tid = threadIdx.x;
   const int pieces = p.row_bytes / 16;
   const long long plane = (long long)p.c.Nk << p.c.page_shift;  // rows of a plane
@@ -81,22 +96,26 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const bool ok = s.ok && s.Lk <= p.max_k;
     const int* kept = p.kept + ((long long)b * p.c.Nk + hk) * p.budget;
     const int most = ok ? (int)min(s.Lk, (long long)p.budget) : 0;
-    const int r0 = chunk * rows, can = max(0, min(rows, most - r0));
-    if (!ok && chunk == 0 && hk == 0 && tid == 0) report(p.c, HSTU_DEVERR_OFFSETS);
+    const int end = chunks > 1 ? kNoEnd - p.ends[pair] : most;  // of the list
+    const int r0 = chunk * rows;
+    int n = max(0, min(rows, min(most, end) - r0));
+    int* loaded = p.loaded + (long long)pair * chunks;  // chunks that have loaded
+    if (tid == 0 && chunk == 0 && ((!ok && hk == 0) || (end < most && kept[end] >= 0)))
+      report(p.c, HSTU_DEVERR_OFFSETS);  // (lists end at negative positions)
     __syncthreads();  // everyone has the ticket, and the chunk before is done with `moves`
     if (tid == 0) {
       // (its latency passes meanwhile)
       s_ticket = chunks > 1 ? atomicAdd(p.counter, 1) : (int)(ticket + gridDim.x);
-      s_any = s_late = s_ended = 0;
-      s_end = 2 * can;
+      s_any = s_wait = s_late = 0;
+      s_end = n;
     }
     __syncthreads();
-    if (can > 0) {
-      for (int x = tid; x < can; x += kThreads) {
+    if (n > 0) {
+      for (int x = tid; x < n; x += kThreads) {
         const int r = r0 + x, src = kept[r];
         Move m = {-1, -1, -1, -1};
-        if (src <= (r ? kept[r - 1] : -1) || src >= s.Lk) {
-          atomicMin(&s_end, 2 * x + (src >= 0));
+        if (chunks == 1 && ends_at(kept, r, s.Lk)) {
+          atomicMin(&s_end, r);
         } else if (src > r) {
           const long long a = page_at(p.c, s, src), d = page_at(p.c, s, r);
           if (a >= 0 && d >= 0) {
@@ -115,9 +134,19 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         }
         moves[x] = m;
       }
+      // chunks in front with sources among positions [r0, r0 + n): two at most
+      for (int c = tid; c < chunk; c += kThreads) {
+        if (kept[c * rows] < r0 + n && kept[c * rows + rows - 1] >= r0) {
+          const int i = atomicAdd(&s_wait, 1);
+          if (i < 2) s_before[i] = c;
+        }
+      }
       __syncthreads();
+      if (chunks == 1) {
+        n = s_end;
+        if (tid == 0 && n < most && kept[n] >= 0) report(p.c, HSTU_DEVERR_OFFSETS);
+      }
     }
-    const int n = s_end >> 1;  // ranks of the list's
     uint4 u[kPieces];
     uint16_t group[kPieces];
     uint8_t scale[2];
@@ -142,33 +171,22 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
     }
     __syncthreads();  // every row of the chunk is in registers
-    int* state = p.state + (long long)pair * chunks + chunk;
-    if (tid == 0 && chunks > 1) store_release(state, n < can ? kEnded : kRead);
-    // (a list ends at a negative position; another is reported)
-    if (!any && !(s_end & 1)) continue;
-    if (tid < 32) {
-      for (int c = 1 + tid; c - tid <= chunk; c += 32) {
-        int x = kRead;
-        if (c <= chunk) {
-          const uint32_t start = now_ns();
-          while ((x = load_acquire(state - c)) == kUnread) {
-            if (now_ns() - start > p.timeout_ns) {
-              s_late = 1;
-              report(p.c, HSTU_DEVERR_TIMEOUT);
-              break;
-            }
+    if (n > 0 && tid == 0 && chunks > 1) store_release(loaded + chunk, 1);
+    if (!any) continue;
+    if (tid < min(s_wait, 2)) {
+      const int* flag = loaded + s_before[tid];
+      if (!load_acquire(flag)) {
+        const uint64_t start = ptx::globaltimer_ns();
+        while (!load_acquire(flag)) {
+          if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
+            s_late = 1;
+            report(p.c, HSTU_DEVERR_TIMEOUT);
+            break;
           }
-          if (x == kEnded) s_ended = 1;
         }
-        if (__any_sync(0xffffffffu, x != kRead)) break;
       }
     }
     __syncthreads();
-    if (s_ended) continue;
-    if (tid == 0) {
-      if (s_end & 1) report(p.c, HSTU_DEVERR_OFFSETS);
-      if (n == can && chunks > 1 && !s_late) store_release(state, kAllRead);
-    }
     if (s_late) continue;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -206,13 +224,19 @@ int compact_rows(int row_bytes) {
 
 cudaError_t launch_compact(const CompactParams& p, int chunks, int sms, cudaStream_t stream) {
   const long long tickets = (long long)p.c.B * p.c.Nk * chunks;
+  const int rows = compact_rows(p.row_bytes);
   if (chunks > 1) {
-    const cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(int) * (4 + tickets), stream);  // (kUnread)
+    const size_t ints = 4 + (size_t)p.c.B * p.c.Nk + tickets;
+    cudaError_t e = cudaMemsetAsync(p.counter, 0, sizeof(int) * ints, stream);
+    if (e != cudaSuccess) return e;
+    const long long warps = kThreads / 32;
+    lists_kernel<<<(unsigned)((tickets + warps - 1) / warps), kThreads, 0, stream>>>(p, rows, chunks);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   const long long most = (long long)kCtas * sms;
   compact_kernel<<<(unsigned)(tickets < most ? tickets : most), kThreads, 0, stream>>>(
-      p, compact_rows(p.row_bytes), chunks, lanes_shift(p.row_bytes));
+      p, rows, chunks, lanes_shift(p.row_bytes));
   return cudaGetLastError();
 }
 

@@ -170,7 +170,7 @@ hstu_status hstu_compact_workspace(const hstu_kv_cache* c, const hstu_compact_ar
     return HSTU_ERR_INVALID_ARG;
   const long long tickets = (long long)c->batch * c->num_heads_kv * compact_chunks(c, a);
   if (tickets > 0x70000000ll) return HSTU_ERR_UNSUPPORTED;  // (they are counted in 32 bits)
-  *bytes = tickets ? (4 + tickets) * (long long)sizeof(int) : 0;
+  *bytes = tickets ? (4 + (long long)c->batch * c->num_heads_kv + tickets) * (long long)sizeof(int) : 0;
   return HSTU_OK;
 }
 
@@ -192,8 +192,9 @@ hstu_status hstu_kv_compact(const hstu_kv_cache* c, const hstu_compact_args* a, 
   p.row_bytes = row_bytes(c);
   p.by_head = cache_format(c->dtype) == kE2m1;
   p.counter = static_cast<int*>(a->workspace);
-  p.state = p.counter + 4;
-  p.timeout_ns = 1000000000u;
+  p.ends = p.counter + 4;
+  p.loaded = p.ends + (long long)c->batch * c->num_heads_kv;
+  p.timeout_ns = 1000000000ll;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   return launch_compact(p, (int)compact_chunks(c, a), sms, static_cast<cudaStream_t>(stream)) ==

@@ -51,8 +51,9 @@ struct CompactParams {
   int row_bytes;   // of a head's row in one plane of the cache
   int by_head;     // the cache has its heads before the rows (E2M1)
   int* counter;    // of the chunks that have been handed out
-  int* state;      // [B, Nk, chunks]: what is known of the chunk
-  uint32_t timeout_ns;
+  int* ends;       // [B, Nk]: where lists end
+  int* loaded;     // [B, Nk, chunks]: the chunk's rows have been read
+  long long timeout_ns;
 };
 constexpr int kCompactRows = 256;  // most ranks of a chunk
 int compact_rows(int row_bytes);   // ranks of a chunk

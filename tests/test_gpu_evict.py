@@ -542,6 +542,49 @@ def test_other_streams_and_captured_graphs(cuda_device):
         assert all(same(x.float(), y.float()) for x, y in zip((kept, ids, c, w), want[i]))
 
 
+@pytest.mark.parametrize("mode,dtype,pages", [("same", "bf16", 20000), ("fp4", "bf16", 70000), ("fp4", "fp32", 70000)])
+def test_offsets_beyond_32_bits(cuda_device, mode, dtype, pages):
+    """The last pages of a cache of more than 2^32 bytes (and 2^31 elements) do as the same pages of a
+    small one."""
+    dev, Nq, Nk, D, ps, dt = cuda_device, 8, 4, 128, 128, R.DTYPES[dtype]
+    n = [1, 3, 130]
+    t = R.Table([700, 90, 400], ps)
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(sum(n), h, D, generator=g).to(dt).to(dev) for h in (Nq, Nk, Nk))
+    so = R.offsets(n).to(dev)
+    small = K4._filled(t, Nk, D, dev, 5) if mode == "fp4" else S._filled(t, Nk, D, dt, mode, dev, 5)
+    small = [small[0], *small[2].values(), torch.rand(t.num_pages, Nk, ps, device=dev)]
+
+    def run(tensors, shift):
+        cache, w = tensors[0], tensors[-1]
+        kw = dict(zip(("kv_scale", "kv_group_scale"), tensors[1:-1]))
+        args = t.args(dev)
+        args["page_ids"] = args["page_ids"] + shift
+        bounds = dict(max_seqlen=max(n), max_seqlen_k=max(t.lengths))
+        hstu_kv_append(k, v, so, cache, **args, **kw)
+        results = list(hstu_kv_read(cache, so, total_tokens=sum(n), dtype=dt, **args, **kw))
+        out, lse = hstu_softmax_fwd(q, cache, so, alpha=0.1, return_lse=True, **bounds, **args, **kw)
+        hstu_kv_weights(q, lse, cache, so, w, alpha=0.1, **bounds, **args, **kw)
+        few = dict(max_seqlen=1, max_seqlen_k=max(t.lengths), alpha=0.1)
+        one = torch.arange(4, device=dev)
+        results += [out, lse, hstu_softmax_fwd(q[:3], cache, one, **few, **args, **kw)]
+        hstu_kv_weights(q[:3], lse[:3], cache, one, w, **few, **args, **kw)
+        kept, new = hstu_kv_select(w, budget=200, recent=9, max_seqlen_k=max(t.lengths), **args)
+        hstu_kv_compact(cache, kept, weights=w, **args, **kw)
+        used = torch.arange(t.num_pages, device=dev) + shift
+        return [*results, kept, new["page_ids"] - shift * (new["page_ids"] >= 0)] + \
+            [x[used].contiguous().view(torch.uint8) for x in tensors]
+
+    shift = pages - t.num_pages
+    large = []
+    for x in small:
+        y = torch.empty(pages, *x.shape[1:], dtype=x.dtype, device=dev)
+        y[shift:] = x
+        large.append(y)
+    for x, y in zip(run(small, 0), run(large, shift)):
+        assert torch.equal(x, y)
+
+
 def test_empty_calls(cuda_device):
     dev = cuda_device
     w = torch.rand(4, 2, 32, device=dev)

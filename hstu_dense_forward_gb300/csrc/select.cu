@@ -7,8 +7,9 @@
 // agree with what is known (eight at a time, whose first are a sign and seven of an exponent, crowd
 // few counters). Then it writes the positions in order: all of larger keys and, of that
 // key, as many as the budget leaves, from the first on. Warps own stretches of the positions, so that a
-// count before the writes gives every warp its first rank. (Keys that were read anew in each of the
-// five passes, by one CTA: 128 lists of 4k-16k positions 58 us, one of 100,000 350.)
+// count before the writes gives every warp its first rank. Two CTAs share an SM (one, with all of its
+// registers: 31 us in place of 26 for 128 lists of 4k-16k positions). (Keys that were read anew in
+// each of the five passes, by one CTA: 58 us, and one list of 100,000 350.)
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -61,25 +62,36 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warps, l
   return before + v - x;
 }
 
-// Page offsets and last pages' lengths of the shorter sequences, by one CTA. (Sequences whose entries
-// of page_ids overlap can have more pages than new_page_ids holds: the offsets stop behind its end,
-// where they are no valid table's.)
+// Pages that sequence b keeps. (store: its last page's length is written, a bad table reported.)
+__device__ __forceinline__ long long kept_pages(const SelectParams& p, int b, bool store) {
+  const PagedSeq s = paged_table(p.c, b);
+  const bool ok = table_ok(p, s);
+  const long long keep = ok ? min(s.Lk, (long long)p.budget) : 0;
+  const long long pages = (keep + page_size(p.c) - 1) >> p.c.page_shift;
+  if (store) {
+    if (!ok) report(p.c, HSTU_DEVERR_OFFSETS);
+    store_index(p.new_last_page_len, b, p.c.index64,
+                pages ? keep - ((pages - 1) << p.c.page_shift) : 1);
+  }
+  return pages;
+}
+
+// What the new page offsets stop at. (Sequences whose entries of page_ids overlap can have more pages
+// than new_page_ids holds: the offsets stop behind its end, where they are no valid table's.)
+__device__ __forceinline__ long long most_pages(const SelectParams& p) {
+  return p.c.index64 ? p.c.num_page_ids + 1 : min(p.c.num_page_ids + 1, 0x7fffffffll);
+}
+
+// Page offsets and last pages' lengths of the shorter sequences, by one CTA (of more sequences than a
+// CTA has threads; of fewer select_kernel's CTAs find their offsets by themselves, a launch less: five
+// sequences of up to 300 rows 9.0 us in place of 10.0).
 __global__ void __launch_bounds__(kThreads) new_table_kernel(const SelectParams p) {
   __shared__ long long warps[kWarps];
-  const long long most = p.c.index64 ? p.c.num_page_ids + 1 : min(p.c.num_page_ids + 1, 0x7fffffffll);
+  const long long most = most_pages(p);
   long long carry = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    long long pages = 0;
-    if (b < p.c.B) {
-      const PagedSeq s = paged_table(p.c, b);
-      const bool ok = table_ok(p, s);
-      if (!ok) report(p.c, HSTU_DEVERR_OFFSETS);
-      const long long keep = ok ? min(s.Lk, (long long)p.budget) : 0;
-      pages = (keep + page_size(p.c) - 1) >> p.c.page_shift;
-      store_index(p.new_last_page_len, b, p.c.index64,
-                  pages ? keep - ((pages - 1) << p.c.page_shift) : 1);
-    }
+    const long long pages = b < p.c.B ? kept_pages(p, b, true) : 0;
     long long total;
     const long long before = block_scan(pages, warps, total);
     if (b < p.c.B) store_index(p.new_page_offsets, b, p.c.index64, min(carry + before, most));
@@ -92,7 +104,7 @@ constexpr int kMaxKeys = 49152;  // of a CTA that shared memory holds; others ar
 constexpr int kBins = 2 * kThreads;  // of eleven bits
 constexpr int kLoads = 8;        // of a lane at a time
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, int cluster,
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectParams p, int cluster,
                                                           int capacity) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];  // [capacity]
@@ -115,8 +127,24 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
   const bool decide = take > 0 && take < others;
 
   if (hk == 0 && rank == 0) {  // the sequence's page ids, and -1 behind the last sequence's
-    const long long first = load_index(p.new_page_offsets, b, p.c.index64);
-    long long pages = load_index(p.new_page_offsets, b + 1, p.c.index64) - first;
+    long long first, end;
+    if (p.c.B <= kThreads) {
+      __shared__ long long scan[kWarps], s_first;
+      const long long x = tid < p.c.B ? kept_pages(p, tid, b == 0) : 0, most = most_pages(p);
+      const long long before = min(block_scan(x, scan, end), most);
+      end = min(end, most);
+      if (tid == b) s_first = before;
+      if (b == 0) {
+        if (tid < p.c.B) store_index(p.new_page_offsets, tid, p.c.index64, before);
+        if (tid == 0) store_index(p.new_page_offsets, p.c.B, p.c.index64, end);
+      }
+      __syncthreads();
+      first = s_first;
+    } else {
+      first = load_index(p.new_page_offsets, b, p.c.index64);
+      end = load_index(p.new_page_offsets, p.c.B, p.c.index64);
+    }
+    long long pages = ((long long)keep + page_size(p.c) - 1) >> p.c.page_shift;
     if (pages > p.c.num_page_ids - first) {  // (entries that overlap)
       if (tid == 0) report(p.c, HSTU_DEVERR_OFFSETS);
       pages = p.c.num_page_ids - first;
@@ -124,7 +152,6 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
     for (long long i = tid; i < pages; i += kThreads)
       store_index(p.new_page_ids, first + i, p.c.index64,
                   load_index(p.c.page_ids, s.po + i, p.c.index64));
-    const long long end = load_index(p.new_page_offsets, p.c.B, p.c.index64);
     for (long long i = end + (long long)b * kThreads + tid; i < p.c.num_page_ids;
          i += (long long)p.c.B * kThreads)
       store_index(p.new_page_ids, i, p.c.index64, -1);
@@ -269,9 +296,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p, 
 }  // namespace
 
 cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t stream) {
-  new_table_kernel<<<1, kThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (p.c.B > kThreads) {
+    new_table_kernel<<<1, kThreads, 0, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const long long pairs = (long long)p.c.B * p.c.Nk;
   // as many CTAs a list as the SMs have room for, of 2048 positions at least
   int cluster = 1;

@@ -36,14 +36,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
   it.b = (int)(blk / p.c.Nk);
   it.split = blockIdx.y;
   it.s = paged_seq(p.c, it.b);
-  if (!attn_seq_ok(p, it.s) || it.s.n * p.G > C::RT) {
+  it.rows = p.Nq ? it.s.n * p.G : 0;  // (of queries without heads none, however many tokens)
+  if (!attn_seq_ok(p, it.s) || it.rows > C::RT) {
     if (threadIdx.x == 0) report(p.c, HSTU_DEVERR_OFFSETS);
     return;
   }
   const KeyRanges kr = key_ranges(p, it.s.Lk);
   it.nsplit = kr.count;
   it.m0 = 0;
-  it.rows = p.Nq ? it.s.n * p.G : 0;
   it.k0 = it.split * kr.keys;
   it.kend = min(it.s.Lk, it.k0 + kr.keys);
   if (it.k0 >= it.kend || (it.rows == 0 && w.accumulate)) return;

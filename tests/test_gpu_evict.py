@@ -176,6 +176,28 @@ def test_weights_of_queries_without_heads(cuda_device):
         assert (w[used] == 0).all() and torch.equal(w[~used], before[~used])
 
 
+@pytest.mark.parametrize("dtype,mode", [("bf16", "same"), ("fp16", "scale"), ("bf16", "fp4"), ("fp32", "same")])
+@pytest.mark.parametrize("n", [8, 9, 17, 200])
+def test_weights_of_many_queries_without_heads(cuda_device, dtype, mode, n):
+    """However many tokens have no heads: nothing is reported, and 0 stored for every cached row."""
+    dev, dt = cuda_device, R.DTYPES[dtype]
+    t = R.Table([n + 40, n, 7], 32)
+    cache, _, kw = _cache(t, 2, 64, dt, mode, dev, 3)
+    lengths = [n, n, 3]
+    q, lse = torch.empty(sum(lengths), 0, 64, dtype=dt, device=dev), torch.empty(sum(lengths), 0, device=dev)
+    so = R.offsets(lengths).to(dev)
+    used = torch.tensor(_used(t)).to(dev)[:, None].expand(-1, 2, -1)
+    for accumulate in (True, False):
+        w = torch.rand(t.num_pages, 2, 32, device=dev)
+        before = w.clone()
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        hstu_kv_weights(q, lse, cache, so, w, max_seqlen=n, max_seqlen_k=n + 40, accumulate=accumulate, status=status,
+                        **t.args(dev), **kw)
+        assert status.item() == 0
+        assert torch.equal(w[~used], before[~used])
+        assert torch.equal(w[used], before[used] if accumulate else torch.zeros_like(w[used]))
+
+
 @pytest.mark.parametrize("dtype,mode,n,Nq,Nk,D", [("bf16", "same", 2100, 4, 1, 128), ("fp16", "scale", 700, 16, 1, 64),
                                                   ("bf16", "fp4", 1500, 8, 2, 32), ("fp16", "same", 900, 8, 1, 256)])
 def test_weights_of_few_prompts(cuda_device, dtype, mode, n, Nq, Nk, D):

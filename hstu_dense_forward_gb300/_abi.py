@@ -20,6 +20,7 @@ HSTU_OK, HSTU_ERR_INVALID_ARG, HSTU_ERR_UNSUPPORTED, HSTU_ERR_CUDA, HSTU_ERR_TIM
     HSTU_ERR_DEVICE_CHECK = range(6)
 HSTU_F32, HSTU_F16, HSTU_BF16, HSTU_FP8_E4M3 = 0, 1, 2, 3
 HSTU_FP4_E2M1 = 5  # of a paged KV cache (include/hstu_kv.h)
+HSTU_ROWS_WEIGHTS = 2  # hstu_kv_rows has the field weights
 HSTU_MASK_CAUSAL, HSTU_MASK_UPPER, HSTU_MASK_NONE, HSTU_MASK_CUSTOM = 0, 1, 2, 3
 HSTU_DEVERR_NONE, HSTU_DEVERR_OFFSETS, HSTU_DEVERR_TIMEOUT = 0, 1, 2
 HSTU_LAYOUT_JAGGED, HSTU_LAYOUT_NORMAL = 0, 1
@@ -103,7 +104,7 @@ class KVRows(ctypes.Structure):
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_longlong),
         ("v_stride", ctypes.c_longlong), ("seq_offsets", ctypes.c_void_p),
         ("total_tokens", ctypes.c_longlong), ("dtype", ctypes.c_int),
-        ("reserved", ctypes.c_int),
+        ("reserved", ctypes.c_int), ("weights", ctypes.c_void_p),
     ]
 
 

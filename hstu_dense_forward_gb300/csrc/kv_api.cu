@@ -15,7 +15,10 @@ namespace {
 hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append, void* stream) {
   const hstu_status st = check_cache(c);
   if (st != HSTU_OK) return st;
-  if (!r || r->reserved || !row_dtype_ok(c, r->dtype)) return HSTU_ERR_INVALID_ARG;
+  if (!r || !row_dtype_ok(c, r->dtype)) return HSTU_ERR_INVALID_ARG;
+  const bool more = append && r->reserved == HSTU_ROWS_WEIGHTS;  // (fields behind `reserved`)
+  if (r->reserved && !more) return HSTU_ERR_INVALID_ARG;
+  float* weights = more ? r->weights : nullptr;
   if (r->total_tokens < 0 || r->total_tokens > 0x7fffffffll) return HSTU_ERR_INVALID_ARG;
   if (c->batch == 0 || r->total_tokens == 0) return HSTU_OK;
   const long long width = (long long)c->num_heads_kv * c->head_dim;
@@ -24,12 +27,12 @@ hstu_status copy_rows(const hstu_kv_cache* c, const hstu_kv_rows* r, bool append
       !aligned(r->seq_offsets, c->index_is_int64 ? 8 : 4) || r->k_stride < width ||
       r->v_stride < width || r->k_stride * eb % 16 != 0 || r->v_stride * eb % 16 != 0 ||
       r->k_stride > (1ll << 40) || r->v_stride > (1ll << 40) || !cache_pointers_ok(c) ||
-      (!append && r->k == r->v))  // (one place for both planes)
+      !aligned(weights, 16) || (!append && r->k == r->v))  // (one place for both planes)
     return HSTU_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;
   const hstu::CacheView v = cache_view(c, r->seq_offsets, r->total_tokens);
-  return hstu::launch_kv_copy(v, r->k, r->v, r->k_stride, r->v_stride, r->dtype,
+  return hstu::launch_kv_copy(v, r->k, r->v, r->k_stride, r->v_stride, weights, r->dtype,
                               cache_format(c->dtype), append, sms,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? HSTU_OK

@@ -23,8 +23,9 @@ struct CacheView;
 struct SoftmaxParams;
 
 // Append (append = true) or read back; dtype of k and v, fmt: what the cache holds (kSame, ..).
+// weights: of the rows' entries, which an append sets to 0, or nullptr.
 cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_stride,
-                           long long v_stride, int dtype, int fmt, bool append, int sms,
+                           long long v_stride, float* weights, int dtype, int fmt, bool append, int sms,
                            cudaStream_t stream);
 
 // The pages that the table of an E2M1 cache names, as bf16 [num_page_ids, 2, page_size, Nk, D], and

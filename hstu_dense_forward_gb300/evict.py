@@ -1,6 +1,7 @@
 """Eviction from the paged KV cache: the attention weight that every cached key has received, the
 choice of the rows to keep by it, and moving those together (C ABI: include/hstu_evict.h).
 
+    hstu_kv_append(k, v, seq_offsets, kv_cache, weights=weights, **table)
     out, lse = hstu_softmax_fwd(q, kv_cache, seq_offsets, ..., return_lse=True, **table)
     hstu_kv_weights(q, lse, kv_cache, seq_offsets, weights, ..., **table)
     kept, shorter = hstu_kv_select(weights, budget=4096, recent=256, max_seqlen_k=Sk, **table)
@@ -48,8 +49,9 @@ def hstu_kv_weights(q, lse, kv_cache, seq_offsets, weights, *, max_seqlen, max_s
     what it holds, or with accumulate=False in its place (0 where no query sees the row). lse
     [T, Nq] fp32 is hstu_softmax_fwd's of the same call; its other arguments are the same here. To
     weigh keys by the last tokens of a prompt alone, pass those tokens' q, lse and seq_offsets.
-    Elements of weights that belong to no cached row are left as they are; no page may belong to two
-    sequences. Repeated calls give the same bits."""
+    Elements of weights that belong to no cached row are left as they are, with what earlier rows of
+    their place have received: hstu_kv_append, given weights, sets those of new rows to 0. No page may
+    belong to two sequences. Repeated calls give the same bits."""
     c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
                kv_group_scale, k_descale, v_descale, status)
     if not isinstance(q, torch.Tensor):
@@ -167,7 +169,8 @@ def hstu_kv_compact(kv_cache, kept, *, page_offsets, page_ids, last_page_len, ma
     position kept[b, hk, r], with its scales and factors, and its entry of weights if that is given
     [num_pages, Nk, page_size]. The table is the one from before, of which max_seqlen_k may bound the
     lengths; the one that hstu_kv_select returned describes the result. Rows that are not written
-    keep what they hold; a cache with static factors (k_descale) keeps those. No page may belong to
+    keep what they hold, entries of weights too (pass weights to the hstu_kv_append that fills them
+    next); a cache with static factors (k_descale) keeps those. No page may belong to
     two sequences."""
     if not isinstance(page_offsets, torch.Tensor):
         raise TypeError("page_offsets must be a torch.Tensor")

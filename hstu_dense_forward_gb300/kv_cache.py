@@ -34,7 +34,7 @@ _FP4 = _abi.HSTU_FP4_E2M1
 # The C structs as bytes (their layouts are those of the ctypes mirrors in _abi): one pack is
 # a fraction of the cost of setting their fields.
 _PACK_CACHE = struct.Struct("@8iPPqPPPqPPPP").pack
-_PACK_ROWS = struct.Struct("@PPqqPqii").pack
+_PACK_ROWS = struct.Struct("@PPqqPqiiP").pack
 _PACK_ATTN = struct.Struct("@PqPqiiiiifPPPqi4x").pack
 
 
@@ -224,8 +224,9 @@ def _call(name, c, *args):
         _abi.check(status, name)
 
 
-def _copy(name, c, k, v, seq_offsets, new=False):
-    """hstu_kv_append / hstu_kv_read of the rows k and v (new: just allocated, nothing to check)."""
+def _copy(name, c, k, v, seq_offsets, new=False, weights=0):
+    """hstu_kv_append / hstu_kv_read of the rows k and v (new: just allocated, nothing to check;
+    weights: the place of hstu_kv_append's)."""
     dtype = _row_dtype(c, k.dtype)
     T = k.shape[0]
     if new:
@@ -236,7 +237,8 @@ def _copy(name, c, k, v, seq_offsets, new=False):
         if v.shape[0] != T:
             raise ValueError("k and v must have one shape")
     _call(name, c, _PACK_ROWS(k.data_ptr(), v.data_ptr(), k_stride, v_stride,
-                              seq_offsets.data_ptr(), T, dtype, 0))
+                              seq_offsets.data_ptr(), T, dtype,
+                              _abi.HSTU_ROWS_WEIGHTS if weights else 0, weights))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -252,7 +254,8 @@ def _workspace_bytes(device, cache_sizes, attn_sizes, num_ids):
 
 
 def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_page_len,
-                   kv_scale=None, kv_group_scale=None, k_descale=None, v_descale=None, status=None):
+                   kv_scale=None, kv_group_scale=None, k_descale=None, v_descale=None, weights=None,
+                   status=None):
     """Write new rows into the paged cache; returns kv_cache.
 
     k, v [T, Nk, D] fp32, fp16 or bf16; rows of D * Nk contiguous elements, which may be
@@ -277,13 +280,18 @@ def hstu_kv_append(k, v, seq_offsets, kv_cache, *, page_offsets, page_ids, last_
     sixth of the sixteen's largest over it. What lies beyond saturates; a NaN makes its sixteen
     values NaN.
 
+    weights [num_pages, Nk, page_size] fp32 (hstu_kv_weights'): the entries of the rows that are
+    written become 0, whatever an earlier row of their place had received.
+
     status: an int32 tensor of one element that is set to 1 where offsets, lengths or page ids
     are found invalid on the device (nothing of such a sequence is written)."""
     c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
                kv_group_scale, k_descale, v_descale, status)
     if not isinstance(k, torch.Tensor):
         raise TypeError("k must be a torch.Tensor")
-    _copy("hstu_kv_append", c, k, v, seq_offsets)
+    w = 0 if weights is None else _tensor(weights, "weights", kv_cache.device, torch.float32,
+                                          (kv_cache.shape[0], c.Nk, c.sizes[4]))
+    _copy("hstu_kv_append", c, k, v, seq_offsets, weights=w)
     return kv_cache
 
 

@@ -3,9 +3,10 @@
  * that every cached key has received, the choice of the rows to keep by it, and moving those
  * together. hstu_kv.h has the cache, its page table and the attention over it.
  *
- * A step of a serving loop: hstu_kv_append, hstu_softmax_fwd (with lse), hstu_kv_weights with that
- * lse; and where a cache has to become shorter, hstu_kv_select and hstu_kv_compact, after which
- * the tables that hstu_kv_select has written describe it. Pages that they no longer name are free.
+ * A step of a serving loop: hstu_kv_append (with the weights, whose entries of the new rows become
+ * 0), hstu_softmax_fwd (with lse), hstu_kv_weights with that lse; and where a cache has to become
+ * shorter, hstu_kv_select and hstu_kv_compact, after which the tables that hstu_kv_select has written
+ * describe it. Pages that they no longer name are free.
  *
  * Ownership, streams, errors and what only the device can see are as in hstu_kv.h: nothing is
  * allocated, synchronised or kept between calls, status codes are returned, and an invalid sequence
@@ -25,7 +26,9 @@ extern "C" {
  * head hk, the sum over the queries i that see j (all, or j <= Lk - n + i if causal) and the heads h
  * of hk (h / (Nq / Nk) = hk) of
  *   exp(alpha * sum_d q[i, h, d] * k[j, hk, d] - lse[i, h])
- * is added to weights[page, hk, row of j], or stored there. Every cached row of a valid sequence
+ * is added to weights[page, hk, row of j], or stored there. (Rows behind those that hstu_kv_compact has
+ * moved together, and rows of pages that are used again, have entries of earlier rows until
+ * hstu_kv_append, with the weights, sets them to 0.) Every cached row of a valid sequence
  * takes part: where no query sees it, 0 is added or stored. Elements of weights that belong to no
  * cached row are left alone; a key that holds an infinity or a NaN may be given a NaN. Scores and
  * sums are fp32, products exact (bf16 queries over an E4M3 or E2M1 cache: as hstu_softmax_fwd has
@@ -92,7 +95,8 @@ HSTU_API hstu_status hstu_kv_select(const hstu_select_args* args, void* stream);
  * (scales and factors too, and its entry of weights, if given) that position kept[b, hk, r] holds,
  * for r = 0, 1, .. as long as kept[b, hk, r] >= 0 (at most budget). cache describes the sequences as
  * they were. Positions increase with r (hstu_kv_select's do); a list where they do not, or pass the
- * sequence's length, is reported and ends there. Other rows are left as they are.
+ * sequence's length, is reported and ends there. Other rows are left as they are, and so are their
+ * entries of weights: hstu_kv_append sets those of the rows that come next to 0.
  */
 typedef struct {
   const int* kept;        /* [B, Nk, budget], 4-byte aligned */

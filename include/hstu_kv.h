@@ -81,6 +81,9 @@ typedef struct {
   void* kv_group_scale;       /* E2M1: 16-byte aligned; not looked at for other types */
 } hstu_kv_cache;
 
+/* hstu_kv_rows.reserved of callers whose hstu_kv_rows has the field weights. */
+enum { HSTU_ROWS_WEIGHTS = 2 };
+
 /* Rows of k and v: row t of k starts at k + t * k_stride elements and holds [Nk, D]
  * contiguously (a slice of a fused projection's output, for instance). Rows start on 16-byte
  * boundaries. seq_offsets [B + 1]: increasing from >= 0, last <= total_tokens. */
@@ -93,7 +96,9 @@ typedef struct {
   long long total_tokens; /* rows of k and v; rows of no sequence are left alone */
   int dtype;              /* HSTU_F32, HSTU_F16 or HSTU_BF16; the cache's, unless that is E4M3
                              or E2M1 */
-  int reserved;           /* must be 0 */
+  int reserved;           /* 0, or HSTU_ROWS_WEIGHTS: there is a field behind this one */
+  float* weights;         /* hstu_kv_append with HSTU_ROWS_WEIGHTS: [num_pages, Nk, page_size],
+                             16-byte aligned, or NULL; not looked at otherwise */
 } hstu_kv_rows;
 
 /*
@@ -107,7 +112,9 @@ typedef struct {
  * of the row is at most 2688 * 2^e (-100 for a row of zeros). With y = x * 2^-e, beyond +-2688
  * (infinities) +-2688, a group's factor is max |y| / 6 rounded to E4M3, and a code y / factor
  * rounded to E2M1 (both to nearest even; 6 at most; 0 where the factor is 0). A NaN makes its
- * group's factor a NaN, and so the group's values. No page may belong to two sequences that
+ * group's factor a NaN, and so the group's values.
+ * With rows->weights (hstu_evict.h's), the entries of the rows that are written become 0: what an
+ * earlier row of that place had received does not count for the new one. No page may belong to two sequences that
  * append to it in one call (the order of their writes is not defined).
  */
 HSTU_API hstu_status hstu_kv_append(const hstu_kv_cache* cache, const hstu_kv_rows* rows,

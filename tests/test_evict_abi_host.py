@@ -166,6 +166,20 @@ def test_four_bit_caches_refuse_bad_arguments(built_lib):
     assert L.hstu_softmax_workspace(by(_fp4(batch=0, kv_scale=None, kv_group_scale=None)), by(attn), by(need)) == OK
 
 
+def test_append_with_weights_refuses_bad_arguments(built_lib):
+    """hstu_kv_rows.weights counts where hstu_kv_rows.reserved says that the struct has it."""
+    L, by = _abi.lib(), ctypes.byref
+
+    def rows(**kw):
+        return _set(_abi.KVRows(k=FAKE, v=2 * FAKE, k_stride=128, v_stride=128, seq_offsets=FAKE, total_tokens=4,
+                                dtype=_abi.HSTU_BF16, reserved=_abi.HSTU_ROWS_WEIGHTS, weights=FAKE), kw)
+
+    for kw in (dict(weights=FAKE + 4), dict(reserved=1), dict(reserved=3), dict(k=None)):
+        assert L.hstu_kv_append(by(_cache()), by(rows(**kw)), None) == INVALID, kw
+    assert L.hstu_kv_read(by(_cache()), by(rows()), None) == INVALID  # no call to write weights
+    assert L.hstu_kv_append(by(_cache()), by(rows(total_tokens=0)), None) == OK
+
+
 def test_references():
     m = np.array([0.25, 0.26, 0.75, 0.74, 1.25, 1.26, 1.75, 2.5, 3.5, 5.0, 5.01, 100.0, -0.3])
     assert list(R4.E2M1[R4.e2m1_code(m)]) == [0, 0.5, 1, 0.5, 1, 1.5, 2, 2, 4, 4, 6, 6, -0.5]

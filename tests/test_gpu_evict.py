@@ -520,6 +520,133 @@ def test_a_serving_loop(cuda_device, mode):
     step([1, 5, 1])
 
 
+@pytest.mark.parametrize("mode,dtype,ps", [("same", "bf16", 32), ("scale", "bf16", 128), ("fp4", "fp16", 32), ("same", "fp32", 32),
+                                           ("fp4", "bf16", 256)])
+def test_weights_through_a_serving_loop(cuda_device, mode, dtype, ps):
+    """What every key has received, from the step that appended it on, through shortened sequences and
+    pages that are used again, against sums in 64 bits; nothing is cleared but by hstu_kv_append.
+
+    Tolerance: each step's of the file's head, from the call's own lse, one 2^-24 of the sum per step."""
+    dev, Nq, Nk, D, B, dt = cuda_device, 4, 2, 64, 3, R.DTYPES[dtype]
+    g = torch.Generator().manual_seed(2)
+    pages, alpha = 24 if ps < 256 else 8, 0.3
+    if mode == "fp4":
+        cache = torch.zeros(pages, 2, Nk, ps, D // 2, dtype=torch.uint8, device=dev)
+        kw = dict(kv_scale=torch.zeros(pages, 2, Nk, ps, dtype=torch.uint8, device=dev),
+                  kv_group_scale=torch.zeros(pages, 2, Nk, ps, D // 16, device=dev).to(R.FP8))
+    else:
+        cache = torch.zeros(pages, 2, ps, Nk, D, device=dev).to(dt if mode == "same" else R.FP8)
+        kw = dict(kv_scale=torch.zeros(pages, 2, Nk, ps, dtype=torch.uint8, device=dev)) if mode == "scale" else {}
+    weights = torch.full((pages, Nk, ps), 1e6, device=dev)  # what the pages' last users left
+    free, owned, lengths = list(range(pages)), [[] for _ in range(B)], [0] * B
+    keys = [np.zeros((0, Nk, D)) for _ in range(B)]   # as the cache holds them
+    sums = [np.zeros((Nk, 0)) for _ in range(B)]
+    tols = [np.zeros((Nk, 0)) for _ in range(B)]
+
+    def table():
+        return dict(page_offsets=R.offsets([len(o) for o in owned]).to(dev),
+                    page_ids=torch.tensor([p for o in owned for p in o], device=dev),
+                    last_page_len=torch.tensor([L - (len(o) - 1) * ps if o else 1 for L, o in zip(lengths, owned)], device=dev))
+
+    def check():
+        w = weights.cpu().numpy().astype(np.float64)
+        for b in range(B):
+            at = np.arange(lengths[b])
+            got = w[np.array(owned[b], dtype=int)[at // ps], :, at % ps].T if lengths[b] else np.zeros((Nk, 0))
+            bad = ~(np.abs(got - sums[b]) <= tols[b])
+            assert not bad.any(), (b, np.argwhere(bad)[:5], got[bad][:5], sums[b][bad][:5])
+
+    def step(n):
+        for b in range(B):
+            lengths[b] += n[b]
+            while len(owned[b]) * ps < lengths[b]:
+                owned[b].append(free.pop())
+        q, k, v = (torch.randn(sum(n), h, D, generator=g).to(dt).to(dev) for h in (Nq, Nk, Nk))
+        so, tab = R.offsets(n).to(dev), table()
+        hstu_kv_append(k, v, so, cache, weights=weights, **tab, **kw)
+        kr, _ = hstu_kv_read(cache, so, total_tokens=sum(n), dtype=dt if mode == "same" else torch.float32, **tab, **kw)
+        bounds = dict(max_seqlen=max(n), max_seqlen_k=max(lengths), alpha=alpha)
+        _, lse = hstu_softmax_fwd(q, cache, so, return_lse=True, **bounds, **tab, **kw)
+        assert hstu_kv_weights(q, lse, cache, so, weights, **bounds, **tab, **kw) is weights
+        ends = np.concatenate([[0], np.cumsum(n)])
+        for b in range(B):
+            at = slice(ends[b], ends[b + 1])
+            keys[b] = np.concatenate([keys[b], R.values(kr[at].cpu())])
+            pad = np.zeros((Nk, n[b]))
+            w, size, off = E.key_weights(R.values(q[at].cpu()), lse[at].double().cpu().numpy(), keys[b], True, alpha)
+            sums[b] = np.concatenate([sums[b], pad], 1) + w
+            tols[b] = np.concatenate([tols[b], pad], 1) + 1.1 * (D + 16) * 2.0 ** -24 * size + 2.0 ** -22 * off + \
+                (2.0 ** -21 + n[b] * (Nq // Nk) * 2.0 ** -24) * w + 2.0 ** -24 * sums[b] + 1e-30
+        check()
+
+    def shorten(budget, recent):
+        kept, new = hstu_kv_select(weights, budget=budget, recent=recent, max_seqlen_k=max(lengths), **table())
+        hstu_kv_compact(cache, kept, weights=weights, **table(), **kw)
+        kept = kept.cpu().numpy()
+        for b in range(B):
+            lengths[b] = min(lengths[b], budget)
+            left = -(-lengths[b] // ps)
+            free.extend(owned[b][left:])
+            owned[b] = owned[b][:left]
+            rows = [kept[b, h, :lengths[b]] for h in range(Nk)]
+            keys[b] = np.stack([keys[b][r, h] for h, r in enumerate(rows)], 1)
+            sums[b] = np.stack([sums[b][h, r] for h, r in enumerate(rows)])
+            tols[b] = np.stack([tols[b][h, r] for h, r in enumerate(rows)])
+        assert new["page_offsets"].tolist() == table()["page_offsets"].tolist()
+        check()
+
+    step([100, 37, 1])
+    step([1, 1, 1])
+    shorten(60, 8)
+    step([1, 1, 1])
+    step([40, 2, 70])
+    shorten(20, 5)  # (not whole pages)
+    for _ in range(3):
+        step([1, 3, 1])
+    step([90, 1, 50])
+    shorten(33, 0)
+    step([1, 0, 1])
+
+
+def test_append_clears_weights_of_the_rows_it_writes(cuda_device):
+    """Those alone, of every cache form and both index types; not of sequences or pages that the device
+    rejects, nor of rows of no sequence."""
+    dev = cuda_device
+    for dtype, mode, Nk, D, ps, index in (("bf16", "same", 3, 48, 32, torch.int32), ("fp16", "scale", 1, 256, 128, torch.int64),
+                                          ("fp32", "cast", 2, 16, 256, torch.int64), ("bf16", "static", 4, 128, 32, torch.int32),
+                                          ("bf16", "fp4", 5, 32, 32, torch.int64)):
+        n = [1, 0, 40, 7, 130]
+        t = R.Table([1, 50, 40, 90, 300], ps, index, seed=2)
+        cache, _, kw = _cache(t, Nk, D, R.DTYPES[dtype], mode, dev, 3)
+        k, v = (torch.randn(sum(n) + 2, Nk, D, device=dev).to(R.DTYPES[dtype]) for _ in range(2))
+        w = torch.rand(t.num_pages, Nk, ps, device=dev) + 1
+        want = w.clone()
+        for b in range(len(n)):
+            page, row = (torch.tensor(x[len(x) - n[b]:], device=dev) for x in t.rows(b))
+            want[page, :, row] = 0
+        untouched = cache.clone()
+        hstu_kv_append(k, v, R.offsets(n, index).to(dev), untouched, **t.args(dev), **kw)
+        hstu_kv_append(k, v, R.offsets(n, index).to(dev), cache, weights=w, **t.args(dev), **kw)
+        assert torch.equal(w, want)
+        assert torch.equal(cache.view(torch.uint8), untouched.view(torch.uint8))  # the rows are as without
+        # (nothing of a sequence with a bad length, nor of a bad page)
+        args = t.args(dev)
+        args["last_page_len"][2] = 0
+        args["page_ids"][-1] = -1
+        w = torch.rand(t.num_pages, Nk, ps, device=dev) + 1
+        want = w.clone()
+        for b in (0, 3, 4):
+            page, row = (torch.tensor(x[len(x) - n[b]:], device=dev) for x in t.rows(b))
+            good = page != int(t.page_ids[-1])
+            want[page[good], :, row[good]] = 0
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        hstu_kv_append(k, v, R.offsets(n, index).to(dev), cache, weights=w, status=status, **args, **kw)
+        assert status.item() == 1 and torch.equal(w, want)
+    for bad, error in ((w.half(), TypeError), (w[:1], ValueError), (w.cpu(), ValueError), (w.transpose(0, 2), ValueError)):
+        with pytest.raises(error):
+            hstu_kv_append(k, v, R.offsets(n, index).to(dev), cache, weights=bad, **t.args(dev), **kw)
+
+
 def test_other_streams_and_captured_graphs(cuda_device):
     """The three calls on a stream of their own, two at once, and in a graph that is replayed."""
     dev = cuda_device

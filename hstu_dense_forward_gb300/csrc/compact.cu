@@ -96,12 +96,16 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const bool ok = s.ok && s.Lk <= p.max_k;
     const int* kept = p.kept + ((long long)b * p.c.Nk + hk) * p.budget;
     const int most = ok ? (int)min(s.Lk, (long long)p.budget) : 0;
-    const int end = chunks > 1 ? kNoEnd - p.ends[pair] : most;  // of the list
+    // ranks of the list (of one chunk, whose end is not known yet: that it may have)
+    const int end = chunks > 1 ? min(most, kNoEnd - p.ends[pair]) : most;
     const int r0 = chunk * rows;
-    int n = max(0, min(rows, min(most, end) - r0));
+    int n = max(0, min(rows, end - r0));
     int* loaded = p.loaded + (long long)pair * chunks;  // chunks that have loaded
-    if (tid == 0 && chunk == 0 && ((!ok && hk == 0) || (end < most && kept[end] >= 0)))
-      report(p.c, HSTU_DEVERR_OFFSETS);  // (lists end at negative positions)
+    auto goes_on = [&](int end) {  // (lists end at negative positions, or with the budget)
+      return ok ? end < p.budget && kept[end] >= 0 : hk == 0;
+    };
+    if (tid == 0 && chunk == 0 && (chunks > 1 || n == 0) && goes_on(end))
+      report(p.c, HSTU_DEVERR_OFFSETS);
     __syncthreads();  // everyone has the ticket, and the chunk before is done with `moves`
     if (tid == 0) {
       // (its latency passes meanwhile)
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       __syncthreads();
       if (chunks == 1) {
         n = s_end;
-        if (tid == 0 && n < most && kept[n] >= 0) report(p.c, HSTU_DEVERR_OFFSETS);
+        if (tid == 0 && goes_on(n)) report(p.c, HSTU_DEVERR_OFFSETS);
       }
     }
     uint4 u[kPieces];

@@ -399,6 +399,28 @@ def test_lists_that_do_not_increase_end_there(cuda_device, mode, D, budget, at, 
     assert all(torch.equal(x, y) for x, y in zip(*results))
 
 
+@pytest.mark.parametrize("budget", [10, 60, 3000])
+@pytest.mark.parametrize("length", [0, 1, 7, 40])
+def test_lists_that_go_on_behind_the_sequence(cuda_device, budget, length):
+    """Reported, also where every position before is kept; the others' lists and the rows are as
+    without what lies behind."""
+    dev, ps = cuda_device, 32
+    t = R.Table([3500, length, 50], ps, seed=3)
+    m = min(length, budget)
+    whole = _lists(t, 1, budget, 4, "first")
+    bad = whole.copy()
+    if m < budget:
+        bad[1, 0, m:m + 3] = [max(length, 5), 70, 2][:budget - m]
+    for more, good in ((bad, m == budget), (whole, True)):
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        cache, _, _ = _cache(t, 1, 64, torch.bfloat16, "same", dev, 5)
+        w = torch.rand(t.num_pages, 1, ps, device=dev)
+        before = [cache.clone().view(torch.uint8), w.clone()]
+        hstu_kv_compact(cache, torch.tensor(more, device=dev), weights=w, status=status, **t.args(dev))
+        assert status.item() == (not good)
+        assert torch.equal(cache.view(torch.uint8), before[0]) and torch.equal(w, before[1])
+
+
 def test_lists_and_tables_that_the_device_rejects(cuda_device):
     """Positions out of range and page ids out of range: no access outside, a status, the rest done."""
     dev = cuda_device

@@ -1,4 +1,4 @@
-// The pages of an E2M1 cache as bf16, in the layout of a bf16 cache, for attention of many query rows
+// The pages of an E2M1 cache that sequences with queries have as bf16, in the layout of a bf16 cache, for attention of many query rows
 // over them. Every CTA of that kernel would turn the keys and values of its items into 16 bits by
 // itself, and its softmax waits for the warps that do: with several items a kv head and sequence it is
 // faster to convert them once, a pass that is bound by memory (16 sequences of 100-512 tokens over some
@@ -15,15 +15,18 @@ namespace {
 constexpr int kThreads = 256;
 
 __global__ void __launch_bounds__(kThreads)
-    expand_kernel(const CacheView c, __nv_bfloat16* pages, void* ids) {
-  const long long slot = blockIdx.x;
-  const long long page = load_index(c.page_ids, slot, c.index64);
+    expand_kernel(const CacheView c, __nv_bfloat16* pages, void* ids, unsigned per, bool by_entry) {
+  const unsigned b = blockIdx.x / per, i = blockIdx.x % per;
+  const PagedSeq s = paged_seq(c, b);
+  if (!s.ok || s.n == 0 || i >= s.pages || s.pages > per) return;  // (nothing reads its pages)
+  const long long entry = s.po + i, slot = by_entry ? entry : blockIdx.x;
+  const long long page = load_index(c.page_ids, entry, c.index64);
   const bool ok = page >= 0 && page < c.num_pages;
   if (threadIdx.x == 0 && blockIdx.y == 0) {  // (an id outside the cache stays one)
     if (c.index64)
-      static_cast<long long*>(ids)[slot] = ok ? slot : -1;
+      static_cast<long long*>(ids)[entry] = ok ? slot : -1;
     else
-      static_cast<int*>(ids)[slot] = ok ? (int)slot : -1;
+      static_cast<int*>(ids)[entry] = ok ? (int)slot : -1;
   }
   if (!ok) return;
   const int groups = c.D / 16, ps = 1 << c.page_shift;
@@ -52,12 +55,14 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-cudaError_t launch_expand(const CacheView& c, void* pages, void* ids, cudaStream_t stream) {
+cudaError_t launch_expand(const CacheView& c, void* pages, void* ids, long long per, bool by_entry,
+                          cudaStream_t stream) {
   // four chunks a thread, if a page has as many
   const long long chunks = (2ll * c.Nk * (c.D / 16)) << c.page_shift;
   const long long parts = chunks / (4 * kThreads);
-  expand_kernel<<<dim3((unsigned)c.num_page_ids, parts < 1 ? 1 : parts < 1024 ? (unsigned)parts : 1024),
-                  kThreads, 0, stream>>>(c, static_cast<__nv_bfloat16*>(pages), ids);
+  expand_kernel<<<dim3((unsigned)(c.B * per), parts < 1 ? 1 : parts < 1024 ? (unsigned)parts : 1024),
+                  kThreads, 0, stream>>>(c, static_cast<__nv_bfloat16*>(pages), ids, (unsigned)per,
+                                         by_entry);
   return cudaGetLastError();
 }
 

@@ -189,29 +189,44 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
 // An E2M1 cache whose pages are turned into bf16 ones first (see expand.cu): for bf16 queries of 768
 // packed rows a sequence in the mean, three of the attention kernel's items (16 sequences of 256
 // tokens, four heads to a kv head: 121 us so, 147 without; of 128 tokens 88 and 86), as long as the
-// pages take a gigabyte at most.
+// pages that batch and max_seqlen_k allow take a gigabyte at most. (What page_ids holds besides has no
+// part in it: the weights are bf16 here and fp16 without.)
 struct Expanded {
   long long ids, pages;  // bytes
+  long long per;         // pages of a sequence at most
+  bool by_entry;         // a place for every entry of page_ids; or `per` for every sequence
   hstu_kv_cache cache;
 };
 bool expand_pays(const hstu_kv_cache* c, const hstu_softmax_args* a, Expanded* e) {
   if (!c || !a || c->dtype != HSTU_FP4_E2M1 || a->dtype != HSTU_BF16 || c->batch < 1 ||
       c->num_heads_kv < 1 || a->num_heads_q < 1 || c->num_page_ids < 1 ||
+      c->num_page_ids > (1ll << 40) || a->total_tokens > 0x7fffffffll || a->max_seqlen_k < 1 ||
       check_cache(c) != HSTU_OK)
     return false;
   const long long rows = a->total_tokens * (a->num_heads_q / c->num_heads_kv);
   const long long page = 4ll * c->page_size * c->num_heads_kv * c->head_dim;
-  if (rows < 768ll * c->batch || c->num_page_ids > (1ll << 30) / page) return false;
+  e->per = ((long long)a->max_seqlen_k + c->page_size - 1) / c->page_size;
+  const long long most = c->batch * e->per;
+  if (rows < 768ll * c->batch || most > (1ll << 30) / page) return false;
+  e->by_entry = c->num_page_ids <= most;
   e->ids = (c->num_page_ids * (c->index_is_int64 ? 8 : 4) + 15) / 16 * 16;
-  e->pages = c->num_page_ids * page;
   e->cache = *c;
   e->cache.dtype = HSTU_BF16;
   e->cache.kv_scale = nullptr;
-  e->cache.num_pages = c->num_page_ids;
+  e->cache.num_pages = e->by_entry ? c->num_page_ids : most;
+  e->pages = e->cache.num_pages * page;
   return true;
 }
 
 hstu_status softmax_over(const hstu_kv_cache* c, const hstu_softmax_args* a, void* stream);
+
+// The rows' tensors (not the workspace).
+bool attn_pointers_ok(const hstu_kv_cache* c, const hstu_softmax_args* a) {
+  return a->q && a->out && a->seq_offsets && aligned(a->q, 16) && aligned(a->out, 16) &&
+         aligned(a->lse, 4) && aligned(a->seq_offsets, c->index_is_int64 ? 8 : 4) &&
+         a->q_stride >= (long long)a->num_heads_q * c->head_dim && a->q_stride <= (1ll << 36) &&
+         a->q_stride * elem_bytes(a->dtype) % 16 == 0;
+}
 
 }  // namespace
 
@@ -246,8 +261,9 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   if (!expand_pays(c, a, &e)) return softmax_over(c, a, stream);
   const hstu_status st = hstu_softmax_workspace(c, a, &need);
   if (st != HSTU_OK) return st;
-  if (!cache_pointers_ok(c) || !a->workspace || !aligned(a->workspace, 16) ||
-      a->workspace_bytes < need)
+  if (a->workspace_bytes < need) return softmax_over(c, a, stream);  // (the caller's choice)
+  if (!cache_pointers_ok(c) || !attn_pointers_ok(c, a) || !a->workspace ||
+      !aligned(a->workspace, 16))
     return HSTU_ERR_INVALID_ARG;
   hstu_softmax_args b = *a;
   char* at = static_cast<char*>(a->workspace);
@@ -255,8 +271,8 @@ hstu_status hstu_softmax_fwd(const hstu_kv_cache* c, const hstu_softmax_args* a,
   e.cache.kv_cache = at + e.ids;
   b.workspace = need > e.ids + e.pages ? at + e.ids + e.pages : nullptr;
   b.workspace_bytes = a->workspace_bytes - e.ids - e.pages;
-  if (launch_expand(cache_view(c, nullptr, 0), e.cache.kv_cache, at,
-                    static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (launch_expand(cache_view(c, a->seq_offsets, a->total_tokens), e.cache.kv_cache, at, e.per,
+                    e.by_entry, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return HSTU_ERR_CUDA;
   return softmax_over(&e.cache, &b, stream);
 }
@@ -270,11 +286,7 @@ hstu_status softmax_over(const hstu_kv_cache* c, const hstu_softmax_args* a, voi
   const hstu_status st = plan_attention(c, a, &pl);
   if (st != HSTU_OK) return st;
   if (pl.blocks == 0) return HSTU_OK;  // empty input
-  if (!a->q || !a->out || !a->seq_offsets || !aligned(a->q, 16) || !aligned(a->out, 16) ||
-      !aligned(a->lse, 4) || !aligned(a->seq_offsets, c->index_is_int64 ? 8 : 4) ||
-      a->q_stride < (long long)a->num_heads_q * c->head_dim || a->q_stride > (1ll << 36) ||
-      a->q_stride * elem_bytes(a->dtype) % 16 != 0 || !cache_pointers_ok(c))
-    return HSTU_ERR_INVALID_ARG;
+  if (!attn_pointers_ok(c, a) || !cache_pointers_ok(c)) return HSTU_ERR_INVALID_ARG;
   if (pl.workspace > 0 &&
       (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < pl.workspace))
     return HSTU_ERR_INVALID_ARG;

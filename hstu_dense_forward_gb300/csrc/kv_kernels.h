@@ -28,9 +28,12 @@ cudaError_t launch_kv_copy(const CacheView& c, void* k, void* v, long long k_str
                            long long v_stride, float* weights, int dtype, int fmt, bool append, int sms,
                            cudaStream_t stream);
 
-// The pages that the table of an E2M1 cache names, as bf16 [num_page_ids, 2, page_size, Nk, D], and
-// their ids 0, 1, .. (-1 for one outside the cache).
-cudaError_t launch_expand(const CacheView& c, void* pages, void* ids, cudaStream_t stream);
+// The pages of an E2M1 cache that sequences with queries have, as bf16 [.., 2, page_size, Nk, D], and
+// the entries of a table of them for theirs (-1 for an id outside the cache). Page i of sequence b comes
+// to the place of its entry of page_ids (by_entry), or to b * per + i; sequences have `per` pages at most
+// (longer ones are left out).
+cudaError_t launch_expand(const CacheView& c, void* pages, void* ids, long long per, bool by_entry,
+                          cudaStream_t stream);
 
 // fp32 attention on CUDA cores: `rows` (4 or 64) packed query rows of one kv head per CTA.
 cudaError_t launch_softmax_simt(const SoftmaxParams& p, int fmt, int rows, long long tiles,

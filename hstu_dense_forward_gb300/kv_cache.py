@@ -330,20 +330,25 @@ def hstu_kv_read(kv_cache, seq_offsets, *, page_offsets, page_ids, last_page_len
 def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page_offsets,
                      page_ids, last_page_len, causal=True, alpha=1.0, kv_scale=None,
                      kv_group_scale=None, k_descale=None, v_descale=None, out=None,
-                     return_lse=False, status=None):
+                     return_lse=False, expand=True, status=None):
     """Softmax attention of the newest tokens of each sequence over its paged cache, which
     holds their keys too (hstu_kv_append first).
 
     q [T, Nq, D] fp32, fp16 or bf16 (rows may be slices of a wider tensor), Nq a multiple of
     the cache's Nk; the cache of q's type, float8_e4m3fn (kv_scale or k_descale / v_descale as
-    hstu_kv_append wrote it) or 4-bit (kv_scale and kv_group_scale). The n = seq_offsets[b+1] - seq_offsets[b] queries of a sequence
-    are its last n positions; with causal=True each sees the keys up to its own position, with
+    hstu_kv_append wrote it) or 4-bit (kv_scale and kv_group_scale). The n = seq_offsets[b+1] -
+    seq_offsets[b] queries of a sequence are its last n positions; with causal=True each sees the keys up to its own position, with
     causal=False all of them (n may then exceed the keys: cross attention). max_seqlen bounds n,
     max_seqlen_k the cached keys of a sequence.
 
     out = softmax(alpha q k^T) v with q's shape and type; with return_lse also ln sum exp(alpha
     q k) [T, Nq] fp32. A row that sees no key gets 0 (lse -inf); rows of no sequence are left
-    as allocated. Other arguments as for hstu_kv_append."""
+    as allocated. Other arguments as for hstu_kv_append.
+
+    expand: bf16 queries of 768 packed rows (tokens times Nq / Nk) a sequence in the mean and more
+    turn the pages of a 4-bit cache into bf16 first, if those that the batch and max_seqlen_k allow
+    are a gigabyte at most; the weights are bf16 then. With expand=False they are fp16, as for fewer
+    rows, and no workspace is taken for pages."""
     c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,
                kv_group_scale, k_descale, v_descale, status)
     if not isinstance(q, torch.Tensor):
@@ -362,7 +367,7 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
     sizes = (T, dtype, Nq, int(max_seqlen), int(max_seqlen_k), bool(causal), float(alpha))
     try:
         need = _workspace_bytes(c.device, c.sizes, sizes,
-                                page_ids.shape[0] if kv_group_scale is not None else 0)
+                                page_ids.shape[0] if expand and kv_group_scale is not None else 0)
     except (struct.error, OverflowError):  # max_seqlen, max_seqlen_k or alpha that no C type holds
         raise _abi.HstuError(_abi.HSTU_ERR_INVALID_ARG, "hstu_softmax_fwd") from None
     workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None

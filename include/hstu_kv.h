@@ -149,6 +149,12 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * less (rows of zeros) may count as zeros, and their weights with the largest scale of the 127 rows
  * around them. bf16 queries over such a cache are products of fp16 with a power of two of their row:
  * elements below 2^-38 of its largest vanish.
+ *
+ * bf16 queries over an E2M1 cache, total_tokens * Nq / Nk >= 768 * batch: the cache's pages are turned
+ * into bf16 first (exactly), in workspace, if batch * ceil(max_seqlen_k / page_size) of them are 2^30
+ * bytes at most; queries, weights and products are then those over a bf16 cache. With less workspace
+ * than hstu_softmax_workspace gives, but at least what it gives for num_page_ids = 0, that is not done,
+ * and what the paragraph above says of E2M1 caches holds.
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */
@@ -171,7 +177,8 @@ typedef struct {
 } hstu_softmax_args;
 
 /* Bytes of workspace that hstu_softmax_fwd needs for these sizes (pointers are not read; of an E2M1
- * cache num_page_ids counts, whose pages may be held there as bf16). */
+ * cache, whose pages may be held there as bf16, num_page_ids counts: a table of as many entries, and
+ * pages for as many if batch and max_seqlen_k allow more). */
 HSTU_API hstu_status hstu_softmax_workspace(const hstu_kv_cache* cache,
                                             const hstu_softmax_args* args, long long* bytes);
 

@@ -1,7 +1,8 @@
 """Paged KV caches of 4-bit codes: hstu_kv_append and hstu_kv_read against a plain 64-bit
 implementation (exactly: quantisation has one result), and hstu_softmax_fwd over such caches with
 the tolerance of test_gpu_softmax.py. Codes times factors are exact in fp16, so a 4-bit cache changes
-that tolerance no more than an E4M3 one: bf16 weights are fp16 there, whose half step is smaller."""
+that tolerance no more than an E4M3 one: weights of bf16 queries are bf16 or fp16 there (see
+include/hstu_kv.h), whose half step is smaller."""
 import numpy as np
 import pytest
 import torch
@@ -221,6 +222,71 @@ def test_long_prompts_over_bad_pages(cuda_device):
             one.page_offsets, one.page_ids = torch.tensor([0, 5]), t.page_ids[5 * b:5 * b + 5]
             at = slice(600 * b, 600 * b + 600)
             S.check(one, [600], q[at], vals, out[at], lse[at], True, 0.125, torch.bfloat16)
+
+
+def _check_weights_of(half_step, t, n, q, vals, got, alpha):
+    """The tolerance of test_gpu_softmax.py with weights of this half step (u_p). fp16 weights stand
+    beside the largest weight times its row's scale: 2^-25 of that times a row's codes, 2688 at most
+    where the row of the largest has 1344, is 2^-24 max |v| a key."""
+    so = np.concatenate([[0], np.cumsum(n)])
+    for b in range(len(n)):
+        page, row = t.rows(b)
+        K, V = vals[page, 0, row], vals[page, 1, row]
+        out, _, A, size = R.softmax_rows(R.values(q[so[b]:so[b + 1]].cpu()), K, V, True, alpha)
+        ex, Lk = (out.shape[2] + 8) * 2.0 ** -24 * size, K.shape[0]
+        tol = 2.0 ** -8 * np.abs(out) + (half_step + 2.0 ** -20 + Lk * 2.0 ** -24 + 2 * ex[..., None]) * A * 1.01
+        tol = tol + Lk * 2.0 ** -24 * np.abs(V).max(initial=0) + 1e-30
+        bad = ~(np.abs(got[so[b]:so[b + 1]].double().cpu().numpy() - out) <= tol)
+        assert not bad.any(), (b, np.argwhere(bad)[:5])
+
+
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+@pytest.mark.parametrize("lengths,n,Nq,Nk,D,ps", [([600, 0, 900, 300], [600, 0, 850, 0], 4, 1, 64, 128),
+                                                 ([1000, 30], [1000, 1], 8, 2, 96, 32)])
+def test_pages_as_bf16_or_not(cuda_device, lengths, n, Nq, Nk, D, ps, index):
+    """The choice does not look at entries of page_ids that no sequence has, of which there may be more
+    than pages that fit the workspace; and a caller that declines it gets fp16 weights."""
+    dev, alpha = cuda_device, D ** -0.5
+    t = R.Table(lengths, ps, index, seed=4)
+    cache, vals, kw = _filled(t, Nk, D, dev, 5)
+    q = torch.randn(sum(n), Nq, D, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(dev)
+    args = dict(max_seqlen=max(n), max_seqlen_k=max(lengths), alpha=alpha, return_lse=True, **kw)
+    table, so = t.args(dev), R.offsets(n, index).to(dev)
+    page = 4 * ps * Nk * D
+    more = torch.randint(-2, t.num_pages + 2, ((1 << 30) // page + 100,), device=dev).to(index)
+    results = []
+    for extra in (more[:0], more[:1], more):
+        for expand in (True, False):
+            status = torch.zeros(1, dtype=torch.int32, device=dev)
+            ids = torch.cat([table["page_ids"], extra])
+            out, lse = hstu_softmax_fwd(q, cache, so, expand=expand, status=status, **{**table, "page_ids": ids}, **args)
+            assert status.item() == 0
+            _check_weights_of(2.0 ** -8 if expand else 2.0 ** -11, t, n, q, vals, out, alpha)
+            results.append((out, lse))
+    for i in (2, 4):
+        for j in (0, 1):
+            assert all(torch.equal(x, y) for x, y in zip(results[i + j], results[j]))
+    assert not torch.equal(results[0][0], results[1][0])
+
+
+def test_pages_as_bf16_of_sequences_that_share_entries(cuda_device):
+    """Of tables with more entries than pages that sequences can have, too; an invalid sequence between."""
+    dev, D, ps = cuda_device, 64, 32
+    t = R.Table([30 * ps], ps, seed=4)
+    cache, vals, kw = _filled(t, 1, D, dev, 5)
+    q = torch.randn(1600, 8, D, device=dev).to(torch.bfloat16)
+    so = torch.tensor([0, 800, 800, 1600], device=dev)
+    for extra in (0, 200):
+        table = dict(page_offsets=torch.tensor([0, 25, 5, 30], device=dev),
+                     page_ids=torch.cat([t.page_ids, torch.zeros(extra, dtype=torch.int64)]).to(dev),
+                     last_page_len=torch.tensor([ps, ps, ps], device=dev))
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        out = hstu_softmax_fwd(q, cache, so, max_seqlen=800, max_seqlen_k=25 * ps, alpha=0.125, status=status, **table, **kw)
+        assert status.item() == 1  # (offsets decrease)
+        for first, at in ((0, 0), (5, 800)):
+            one = R.Table([800], ps)
+            one.page_offsets, one.page_ids = torch.tensor([0, 25]), t.page_ids[first:first + 25]
+            _check_weights_of(2.0 ** -8, one, [800], q[at:at + 800], vals, out[at:at + 800], 0.125)
 
 
 @pytest.mark.parametrize("dtype,n,D", [("bf16", 300, 128), ("fp16", 200, 64), ("bf16", 30, 256), ("fp16", 6, 64),

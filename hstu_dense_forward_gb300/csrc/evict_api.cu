@@ -98,7 +98,9 @@ hstu_status hstu_kv_weights(const hstu_kv_cache* c, const hstu_weights_args* a, 
     const long long ctas = (long long)weights_rows_ctas(c->head_dim, fmt, rows) * sms;
     const long long can = (a->max_seqlen_k + 127) / 128, want = ctas / pairs;
     w.a.splits = (int)(want < 1 ? 1 : want < can ? want : can);
-    w.a.by_length = rows_by_length(c->batch, pairs * w.a.splits, sms);
+    if (w.a.splits == 1)
+      w.a.by_length = rows_by_length(c->batch, pairs, sms, c->num_page_ids, c->page_size,
+                                     a->max_seqlen_k);
     e = launch_weights_rows(w, a->dtype, fmt, rows, s);
   } else {
     const int keys = weights_tc_keys(c->head_dim);

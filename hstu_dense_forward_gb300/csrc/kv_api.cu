@@ -169,7 +169,9 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     if (c->dtype == HSTU_FP4_E2M1 && pl->cluster == 8 && pl->splits > 1)
       pl->splits = (int)(want * 7 / 64);
     pl->min_range = 128 * pl->cluster;
-    if (pl->cluster == 1) pl->by_length = rows_by_length(c->batch, pl->blocks * pl->splits, sms);
+    if (pl->cluster == 1 && pl->splits == 1 && pl->rows == 8 && c->head_dim <= 128)
+      pl->by_length = rows_by_length(c->batch, pl->blocks, sms, c->num_page_ids, c->page_size,
+                                     a->max_seqlen_k);
   } else if (pl->kernel == AttnPlan::SIMT) {
     pl->min_range = 128;
     // resident CTAs: four an SM; of four rows three, in two waves (25 sequences of some 7500 keys,

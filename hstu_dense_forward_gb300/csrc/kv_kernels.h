@@ -44,11 +44,22 @@ cudaError_t launch_softmax_simt(const SoftmaxParams& p, int fmt, int rows, long 
 cudaError_t launch_softmax_tc(const SoftmaxParams& p, int dtype, int fmt, int qtiles, int ctas,
                               long long tiles, long long blocks, cudaStream_t stream);
 
-// Items of one tile each that share SMs are taken by the sequences' lengths (see softmax_rows.cuh):
-// CTAs of a round, or 0. A CTA compares every length with its own sequence's, which up to 256 of them
-// allow.
-inline int rows_by_length(long long batch, long long ctas, long long sms) {
-  return batch > 1 && batch <= 256 && ctas > sms ? (int)sms : 0;
+// Items of one tile each, `ctas` of them, are taken by the sequences' lengths (see softmax_rows.cuh)
+// where that pays: CTAs of a round, or 0. A CTA finds its sequence in some 2 us, for up to 256 of them;
+// what it saves is that an SM's items are long ones together. So there have to be two an SM at least,
+// the mean length (as far as the host sees it: of as many pages as page_ids has entries) must be 2048
+// keys and more, and the longest a quarter longer. Measured with four heads over 16-bit, E4M3 and E2M1
+// caches: 128 sequences of 1024-4096 keys 112 -> 104 us, 73 -> 62 and 79 -> 62, 80 of them 79 -> 73,
+// 50 -> 46 and 61 -> 52. Where the rule says 0: 160 of 200-500 keys 30 -> 32, 19 -> 23 and 23 -> 26, 128
+// of 4096 each 153 -> 156, 109 -> 116 and 106 -> 110, 40 of 1024-4096 (one item an SM, 16 bits) 44 -> 46,
+// 200 of 10-100 and one head 6.4 -> 8.3, 6.8 -> 9.0 and 7.3 -> 9.3.
+inline int rows_by_length(long long batch, long long ctas, long long sms, long long num_page_ids,
+                          int page_size, long long max_keys) {
+  const long long keys = (num_page_ids < (1ll << 32) ? num_page_ids : 1ll << 32) * page_size;
+  return batch > 1 && batch <= 256 && ctas >= 2 * sms && keys >= 2048 * batch &&
+                 5 * keys <= 4 * max_keys * batch
+             ? (int)sms
+             : 0;
 }
 
 // Attention of few rows (bf16, fp16): `rows` (8 or 16) packed rows of one kv head per cluster

@@ -87,6 +87,9 @@ struct Cfg {
                                           : (CODES && NT == 1 ? 3 : 2);
   static constexpr int RING = CTAS == 1 ? 196608 : CTAS == 2 ? 98304 : FP4 || PLANES == 1 ? 57344 : 65536;
   static constexpr int NST = RING / STAGE < 12 ? RING / STAGE : 12;
+  // the tile's stage is counted where registers allow it (16 rows, D = 256, E4M3: 319 us so, 298
+  // with a division)
+  static constexpr bool COUNTED = NT == 1 && D <= 128;
   static constexpr int OFF_SC = NST * STAGE;               // row scales: KT bytes a plane and stage
   static constexpr int GPLANE = KT * (D / 16);             // E2M1: factors of a plane's tile
   static constexpr int OFF_GR = OFF_SC + (CODES ? NST * PLANES * KT : 0);
@@ -182,22 +185,56 @@ __device__ __forceinline__ uint32_t piece_at(int r, int piece) {
   return SWB == 128 ? o ^ ((o >> 3) & 0x70u) : SWB == 64 ? o ^ ((o >> 3) & 0x30u) : o;
 }
 
-// The sequence that is number `rank` by length, the longest first and equal ones in order, by the whole
-// CTA; len: shared memory for kMaxSorted lengths.
+// The sequence that is number `rank` by length, the longest first, by the whole CTA. Lengths count in
+// 256ths of their bound, equal ones in order. (Ranks by comparing every length with every other took
+// 4 us of a CTA at 200 sequences, where this takes 2.)
 constexpr int kMaxSorted = 256;
+struct LengthOrder {
+  int bins[256];  // sequences of a length
+  uint8_t bin[kMaxSorted];
+  int found;
+};
 __device__ __forceinline__ int sequence_by_length(const SoftmaxParams& p, int rank, int threads,
-                                                  long long* len, int* found) {
-  for (int b = threadIdx.x; b < p.c.B; b += threads) len[b] = paged_table(p.c, b).Lk;
+                                                  LengthOrder* w) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const float per_key = 256.0f / ((float)p.max_k + 1.0f);
+  for (int i = tid; i < 256; i += threads) w->bins[i] = 0;
+  for (int b = tid; b < p.c.B; b += threads)
+    w->bin[b] = (uint8_t)min(255, (int)((float)min(paged_table(p.c, b).Lk, p.max_k) * per_key));
   __syncthreads();
-  for (int b = threadIdx.x; b < p.c.B; b += threads) {
-    const long long mine = len[b];
-    int before = 0;
-    for (int j = 0; j < p.c.B; ++j) before += len[j] > mine || (len[j] == mine && j < b);
-    if (before == rank) *found = b;
+  for (int b = tid; b < p.c.B; b += threads) atomicAdd(&w->bins[w->bin[b]], 1);
+  __syncthreads();
+  if (tid < 32) {
+    // lane l has bins 255 - 8 l .. 248 - 8 l; the one that rank falls into, and its number there
+    int count[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += count[i] = w->bins[255 - 8 * lane - i];
+    int before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += y;
+    }
+    int left = rank - (before - sum), bin = 255 - 8 * lane;
+    const uint32_t has = __ballot_sync(0xffffffffu, left >= 0 && left < sum);
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      const bool on = left >= count[i] && bin == 255 - 8 * lane - i;
+      left -= on ? count[i] : 0;
+      bin -= on ? 1 : 0;
+    }
+    const int owner = __ffs(has) - 1;
+    left = __shfl_sync(0xffffffffu, left, owner);
+    bin = __shfl_sync(0xffffffffu, bin, owner);
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+      const uint32_t in = __ballot_sync(0xffffffffu, b0 + lane < p.c.B && w->bin[b0 + lane] == bin);
+      if ((in >> lane & 1u) && __popc(in & ((1u << lane) - 1u)) == left) w->found = b0 + lane;
+      left -= __popc(in);
+    }
   }
   ptx::fence_proxy_async_smem();  // (TMA writes there next)
   __syncthreads();
-  return *found;
+  return w->found;
 }
 
 // Place of the CTA's item in the order of the lengths. A round of by_length CTAs, one an SM, goes
@@ -210,6 +247,13 @@ __device__ __forceinline__ long long place_by_length(const SoftmaxParams& p, lon
   return 2 * first + p.by_length - 1 - blk;
 }
 
+__device__ __forceinline__ long long item_by_length(const SoftmaxParams& p, long long blk,
+                                                    long long blocks, int threads, LengthOrder* w) {
+  blk = place_by_length(p, blk, blocks);
+  const int b = sequence_by_length(p, (int)(blk / p.c.Nk), threads, w);
+  return (long long)b * p.c.Nk + blk % p.c.Nk;
+}
+
 struct Item {
   PagedSeq s;
   int b, hk, split, nsplit;
@@ -217,15 +261,13 @@ struct Item {
   long long k0, kend;   // keys of this CTA
 };
 
-template <class C>
+template <class C, bool ORDER>
 __device__ __forceinline__ bool make_item(const SoftmaxParams& p, int tiles, int cluster,
-                                          Item& it, long long* len, int* found) {
+                                          Item& it, uint8_t* smem) {
   long long blk = blockIdx.x / cluster;
   const int rank = blockIdx.x % cluster;
-  if (p.by_length) {  // (one tile)
-    blk = place_by_length(p, blk, gridDim.x / cluster);
-    const int b = sequence_by_length(p, (int)(blk / p.c.Nk), C::THREADS, len, found);
-    blk = (long long)b * p.c.Nk + blk % p.c.Nk;
+  if constexpr (ORDER) {  // (one tile, no clusters)
+    blk = item_by_length(p, blk, gridDim.x, C::THREADS, reinterpret_cast<LengthOrder*>(smem));
   }
   it.hk = (int)(blk % p.c.Nk);
   const int tile = (int)(blk / p.c.Nk % tiles);
@@ -504,7 +546,9 @@ __device__ __forceinline__ float part_weight(float m, float top) {
   return m == -CUDART_INF_F ? 0.0f : ex2(m - top);
 }
 
-template <int D, int NT, bool BF16, int FMT>
+// ORDER: CTAs take the sequences by length. (A kernel of its own: as a branch in one kernel it cost
+// registers that those of 16 rows and of D = 256 have not got, and 0.2 us of every call.)
+template <int D, int NT, bool BF16, int FMT, bool ORDER>
 __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF16, FMT>::CTAS)
     softmax_rows_kernel(const __grid_constant__ CUtensorMap tm_c, const SoftmaxParams p, int tiles,
                         int cluster) {
@@ -516,10 +560,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ int found;
   Item it;
-  if (!make_item<C>(p, tiles, cluster, it, reinterpret_cast<long long*>(smem), &found))
-    return;  // (the whole cluster)
+  if (!make_item<C, ORDER>(p, tiles, cluster, it, smem)) return;  // (the whole cluster)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = (int)((it.kend - it.k0 + C::KT - 1) / C::KT);
@@ -556,10 +598,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
     auto& lim = qs.lim;
     const int see = qs.see;
 
-    int st = 0;  // of the ring
+    int stage = 0;  // of the ring
     uint32_t phase = 0;
     for (int t = 0; t < n; ++t) {
-      if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], phase))) break;
+      const int st = C::COUNTED ? stage : t % C::NST;
+      const uint32_t parity = C::COUNTED ? phase : (t / C::NST) & 1;
+      if (!__all_sync(0xffffffffu, wait_bar(p, bars, &bars->full[st], parity))) break;
       const int at = t * C::KT + warp * 16;  // first of the warp's keys
       const int left = keys - at;         // of them, keys of this CTA
       if (left > 0) {
@@ -783,8 +827,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->empty[st]));
-      if (++st == C::NST) {
-        st = 0;
+      if (C::COUNTED && ++stage == C::NST) {
+        stage = 0;
         phase ^= 1u;
       }
     }
@@ -945,11 +989,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
   if (cluster > 1) cg::this_cluster().sync();  // the others have read this CTA's shared memory
 }
 
-template <int D, int NT, bool BF16, int FMT>
+template <int D, int NT, bool BF16, int FMT, bool ORDER = false>
 cudaError_t launch_variant(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
                            long long blocks, int cluster, cudaStream_t stream) {
   using C = Cfg<D, NT, BF16, FMT>;
-  auto* kernel = softmax_rows_kernel<D, NT, BF16, FMT>;
+  auto* kernel = softmax_rows_kernel<D, NT, BF16, FMT, ORDER>;
   static std::atomic<unsigned long long> done;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::USED, done);
   if (e != cudaSuccess) return e;
@@ -970,6 +1014,11 @@ template <bool BF16, int FMT, int NT>
 cudaError_t launch_dim(const SoftmaxParams& p, const CUtensorMap& tc, long long tiles,
                        long long blocks, int cluster, cudaStream_t s) {
   if (p.c.D > 128) return launch_variant<256, NT, BF16, FMT>(p, tc, tiles, blocks, cluster, s);
+  if constexpr (NT == 1) {
+    if (p.by_length)
+      return p.c.D > 64 ? launch_variant<128, NT, BF16, FMT, true>(p, tc, tiles, blocks, 1, s)
+                        : launch_variant<64, NT, BF16, FMT, true>(p, tc, tiles, blocks, 1, s);
+  }
   if (p.c.D > 64) return launch_variant<128, NT, BF16, FMT>(p, tc, tiles, blocks, cluster, s);
   return launch_variant<64, NT, BF16, FMT>(p, tc, tiles, blocks, cluster, s);
 }

@@ -23,15 +23,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT, 1>::THREADS, Cfg<D, NT, 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ int found;
   Item it;
   long long blk = blockIdx.x;
-  if (p.by_length) {
-    blk = place_by_length(p, blk, gridDim.x);
-    const int b = sequence_by_length(p, (int)(blk / p.c.Nk), C::THREADS,
-                                     reinterpret_cast<long long*>(smem), &found);
-    blk = (long long)b * p.c.Nk + blk % p.c.Nk;
-  }
+  if (p.by_length)
+    blk = item_by_length(p, blk, gridDim.x, C::THREADS, reinterpret_cast<LengthOrder*>(smem));
   it.hk = (int)(blk % p.c.Nk);
   it.b = (int)(blk / p.c.Nk);
   it.split = blockIdx.y;

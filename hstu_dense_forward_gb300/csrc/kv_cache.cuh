@@ -14,11 +14,12 @@ namespace hstu {
 // What the cache holds: elements of the rows' type, E4M3 codes, or E2M1 codes.
 enum : int { kSame = 0, kE4m3 = 1, kE2m1 = 2 };
 
-// Device view of hstu_kv_cache (see include/hstu_kv.h).
+// Device view of hstu_kv_cache (see include/hstu_kv.h). (What few kernels read comes last, here and in
+// SoftmaxParams: with `group` and `by_length` among the others, at other offsets then, the tensor-core
+// attention over E4M3 caches was compiled 1-2 % slower: chunks 183.3 -> 187.4 us.)
 struct CacheView {
   void* cache;              // [num_pages, 2, page_size, Nk, D]; E2M1 [num_pages, 2, Nk, page_size, D / 2]
   uint8_t* scale;           // [num_pages, 2, Nk, page_size] or nullptr
-  uint8_t* group;           // E2M1: E4M3 factors [num_pages, 2, Nk, page_size, D / 16]
   const void* page_offsets;
   const void* page_ids;
   const void* last_page_len;
@@ -30,6 +31,7 @@ struct CacheView {
   int index64, B, Nk, D;
   int page_shift;           // log2(page_size)
   int ds_b, ds_h;
+  uint8_t* group;           // E2M1: E4M3 factors [num_pages, 2, Nk, page_size, D / 16]
 };
 
 __device__ __forceinline__ long long page_size(const CacheView& c) { return 1ll << c.page_shift; }
@@ -316,11 +318,11 @@ struct SoftmaxParams {
   long long max_k;         // bound on Lk
   int causal;
   float scale_log2;        // alpha * log2(e): scores in powers of two
-  int by_length;           // few rows: CTAs take the sequences longest first, in rounds of so many
-                           // (0: in order)
   int splits;              // most key ranges of one sequence (1: outputs are written at once)
   int min_range;           // fewest keys worth a range of their own (a multiple of 128)
   long long timeout_ns;
+  int by_length;           // few rows: CTAs take the sequences longest first, in rounds of so many
+                           // (0: in order)
 };
 
 // Key ranges of a sequence of Lk keys: `count` ranges of `keys` keys each (a multiple of 128;

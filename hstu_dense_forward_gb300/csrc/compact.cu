@@ -3,13 +3,16 @@
 // Rank r of a (sequence, kv head) takes the row at position kept[r] >= r. Ranks are moved in chunks,
 // each by a CTA that holds the chunk's rows in registers between its loads and its stores. Positions
 // increase with the ranks, so that what a chunk overwrites can be a source of that chunk and of those
-// in front of it only: it stores once those have loaded. Chunks are handed out by a counter, in order
-// for every (sequence, kv head), and load without waiting for anything, so that a chunk waits for
-// loads alone that are under way. (One CTA for all of a (sequence, kv head), chunk after chunk: 128
-// of 4096 ranks of 256-byte rows took 312 us, one of 50,000 3355; now 103 and 28.) Lists that do not
-// increase end there: a launch of its own finds where, 4 us of the 103. (Chunks that ask all in front
-// of them wait for CTAs that are at an earlier chunk yet: eight lists that keep 40,000 of 100,000 rows
-// took 105 us in place of 79.) Bound by memory: a kept row is read once and written once.
+// in front of it only, two of them at most: it stores once those have loaded. Chunks are handed out by a
+// counter, in order for every (sequence, kv head). A CTA takes its next chunk's number before it is done
+// with the one it has, so that the CTA that has a chunk in front may still wait itself; but waits are
+// for lower numbers only, and the lowest one that is not done has nothing to wait for. (One CTA for all
+// of a (sequence, kv head), chunk after chunk: 128 of 4096 ranks of 256-byte rows took 312 us, one of
+// 50,000 3355; now 94 and 20.) Lists that do not increase end there, and which chunks one waits for
+// follows from the list, too: a launch of its own finds both. (Chunks that asked all in front of them for
+// the list's end waited for CTAs at an earlier chunk: eight lists that keep 40,000 of 100,000 rows took
+// 105 us in place of 79, now 64.) Bound by memory: a kept row is read once and written once (rows of
+// 256 bytes 94 us for 32 sequences, 4096 of 4k-16k rows of four heads, 5.7 TB/s; E4M3 59, E2M1 51).
 #include "common.cuh"
 #include "evict_kernels.h"
 #include "kernels.h"
@@ -46,7 +49,11 @@ __device__ __forceinline__ bool ends_at(const int* kept, int r, long long Lk) {
 }
 
 // Where lists end: ends[pair] becomes kNoEnd - the first rank that is none of the list's, and stays 0
-// where all are. A warp for each chunk.
+// where all are. And which chunks in front have sources where a chunk stores, two at most, next to each
+// other: fronts[..] is four times the first, plus how many. Positions increase up to the list's end, so
+// that the lanes' looks at the ends of 32 parts of the chunks leave one part. (All of them looked at by
+// every chunk: a list of a million rows of 256 bytes took 721 us, now 181; of 100,000 fp32 rows of
+// D = 256, 6250 chunks, 120 and 77.) A warp for each chunk.
 constexpr int kNoEnd = 0x7fffffff;
 __global__ void __launch_bounds__(kThreads) lists_kernel(const CompactParams p, int rows, int chunks) {
   const long long ticket = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -55,18 +62,36 @@ __global__ void __launch_bounds__(kThreads) lists_kernel(const CompactParams p, 
   const PagedSeq s = paged_table(p.c, pair / p.c.Nk);
   const int* kept = p.kept + pair * p.budget;
   const int most = s.ok && s.Lk <= p.max_k ? (int)min(s.Lk, (long long)p.budget) : 0;
-  const int r0 = (int)(ticket % chunks) * rows, last = min(r0 + rows, most);
-  for (int r = r0 + (threadIdx.x & 31); r < last; r += 32)
-    if (ends_at(kept, r, s.Lk)) {
-      atomicMax(p.ends + pair, kNoEnd - r);
-      break;
-    }
+  const int chunk = (int)(ticket % chunks), r0 = chunk * rows, last = min(r0 + rows, most);
+  const int lane = threadIdx.x & 31;
+  if (r0 >= most) return;
+  int lo = 0, len = chunk;  // the first with a source at r0 or behind is one of [lo, lo + len]
+  while (len > 30) {
+    const int step = (len + 31) / 32;
+    const int end = lo + min((lane + 1) * step, len) - 1;  // of the lane's part
+    const int before = min(len, step * __popc(__ballot_sync(
+        0xffffffffu, lane * step < len && kept[end * rows + rows - 1] < r0)));
+    lo += before;
+    len = max(min(step, len - before) - 1, 0);  // (the part's last one is at r0 or behind)
+  }
+  const int c = lo + lane;  // (and the one behind it)
+  const bool look = lane <= len + 1 && c < chunk;
+  const int c_first = look ? kept[c * rows] : r0 + rows, c_last = look ? kept[c * rows + rows - 1] : 0;
+  int end = kNoEnd;
+#pragma unroll
+  for (int i = 0; i < kCompactRows / 32; ++i) {
+    const int r = r0 + lane + 32 * i;
+    if (r < last && ends_at(kept, r, s.Lk)) end = min(end, r);
+  }
+  if (end < kNoEnd) atomicMax(p.ends + pair, kNoEnd - end);
+  const uint32_t with = __ballot_sync(0xffffffffu, c_first < r0 + rows && c_last >= r0);
+  if (lane == 0) p.fronts[ticket] = with ? 4 * (lo + __ffs(with) - 1) + min(__popc(with), 2) : 0;
 }
 
 __global__ void __launch_bounds__(kThreads, kCtas)
     compact_kernel(const CompactParams p, int rows, int chunks, int lanes_shift) {
   __shared__ Move moves[kCompactRows];
-  __shared__ int s_ticket, s_any, s_wait, s_late, s_end, s_before[2];
+  __shared__ int s_ticket, s_any, s_late, s_end, s_front;
   const int tid = threadIdx.x;
   const int pieces = p.row_bytes / 16;
   const long long plane = (long long)p.c.Nk << p.c.page_shift;  // rows of a plane
@@ -110,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     if (tid == 0) {
       // (its latency passes meanwhile)
       s_ticket = chunks > 1 ? atomicAdd(p.counter, 1) : (int)(ticket + gridDim.x);
-      s_any = s_wait = s_late = 0;
+      s_front = chunks > 1 && n > 0 ? p.fronts[(long long)pair * chunks + chunk] : 0;
+      s_any = s_late = 0;
       s_end = n;
     }
     __syncthreads();
@@ -137,13 +163,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           }
         }
         moves[x] = m;
-      }
-      // chunks in front with sources among positions [r0, r0 + n): two at most
-      for (int c = tid; c < chunk; c += kThreads) {
-        if (kept[c * rows] < r0 + n && kept[c * rows + rows - 1] >= r0) {
-          const int i = atomicAdd(&s_wait, 1);
-          if (i < 2) s_before[i] = c;
-        }
       }
       __syncthreads();
       if (chunks == 1) {
@@ -177,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     __syncthreads();  // every row of the chunk is in registers
     if (n > 0 && tid == 0 && chunks > 1) store_release(loaded + chunk, 1);
     if (!any) continue;
-    if (tid < min(s_wait, 2)) {
-      const int* flag = loaded + s_before[tid];
+    if (tid < (s_front & 3)) {
+      const int* flag = loaded + (s_front >> 2) + tid;
       if (!load_acquire(flag)) {
         const uint64_t start = ptx::globaltimer_ns();
         while (!load_acquire(flag)) {

@@ -172,7 +172,8 @@ hstu_status hstu_compact_workspace(const hstu_kv_cache* c, const hstu_compact_ar
     return HSTU_ERR_INVALID_ARG;
   const long long tickets = (long long)c->batch * c->num_heads_kv * compact_chunks(c, a);
   if (tickets > 0x70000000ll) return HSTU_ERR_UNSUPPORTED;  // (they are counted in 32 bits)
-  *bytes = tickets ? (4 + (long long)c->batch * c->num_heads_kv + tickets) * (long long)sizeof(int) : 0;
+  const long long pairs = (long long)c->batch * c->num_heads_kv;
+  *bytes = tickets ? (4 + pairs + 2 * tickets) * (long long)sizeof(int) : 0;
   return HSTU_OK;
 }
 
@@ -196,6 +197,7 @@ hstu_status hstu_kv_compact(const hstu_kv_cache* c, const hstu_compact_args* a, 
   p.counter = static_cast<int*>(a->workspace);
   p.ends = p.counter + 4;
   p.loaded = p.ends + (long long)c->batch * c->num_heads_kv;
+  p.fronts = p.loaded + (long long)c->batch * c->num_heads_kv * compact_chunks(c, a);
   p.timeout_ns = 1000000000ll;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || !device_sms(dev, &sms)) return HSTU_ERR_CUDA;

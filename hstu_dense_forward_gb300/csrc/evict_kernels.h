@@ -53,6 +53,7 @@ struct CompactParams {
   int* counter;    // of the chunks that have been handed out
   int* ends;       // [B, Nk]: where lists end
   int* loaded;     // [B, Nk, chunks]: the chunk's rows have been read
+  int* fronts;     // [B, Nk, chunks]: the chunks in front that a chunk waits for
   long long timeout_ns;
 };
 constexpr int kCompactRows = 256;  // most ranks of a chunk

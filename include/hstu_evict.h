@@ -96,7 +96,8 @@ HSTU_API hstu_status hstu_kv_select(const hstu_select_args* args, void* stream);
  * for r = 0, 1, .. as long as kept[b, hk, r] >= 0 (at most budget). cache describes the sequences as
  * they were. Positions increase with r (hstu_kv_select's do); a list where they do not, or pass the
  * sequence's length, is reported and ends there. Other rows are left as they are, and so are their
- * entries of weights: hstu_kv_append sets those of the rows that come next to 0.
+ * entries of weights: hstu_kv_append sets those of the rows that come next to 0. Where *status becomes
+ * HSTU_DEVERR_TIMEOUT, rows are moved in part: what the sequences hold is lost.
  */
 typedef struct {
   const int* kept;        /* [B, Nk, budget], 4-byte aligned */

@@ -367,6 +367,24 @@ def test_compact_of_long_sequences(cuda_device, mode, D, kind):
     check_compact(cuda_device, t, 2, D, mode, torch.bfloat16, _lists(t, 2, 20000, 9, kind))
 
 
+@pytest.mark.parametrize("length,budget", [(200000, 100000), (30000, 29990), (1150000, 1100000)])
+def test_compact_of_lists_of_many_chunks(cuda_device, length, budget):
+    """Rows of a kilobyte, of which few make a chunk: thousands of chunks, and more than 65536, whose
+    sources are far away or next door."""
+    dev, D, ps = cuda_device, 256, 256
+    t = R.Table([length], ps, torch.int32, seed=3)
+    g = torch.Generator(device=dev).manual_seed(4)
+    cache = torch.randint(0, 1 << 30, (t.num_pages, 2, ps, 1, D), generator=g, device=dev, dtype=torch.int32).view(torch.float32)
+    kept = torch.randperm(length, generator=g, device=dev)[:budget].sort().values
+    page = t.page_ids.to(dev).long()
+    want = cache.view(torch.int32).clone()
+    to = torch.arange(budget, device=dev)
+    want[page[to // ps], :, to % ps] = want[page[kept // ps], :, kept % ps]
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    hstu_kv_compact(cache, kept.int().view(1, 1, -1), status=status, **t.args(dev))
+    assert status.item() == 0 and torch.equal(cache.view(torch.int32), want)
+
+
 def test_compact_again_is_no_change(cuda_device):
     """Lists that keep rows where they are move nothing."""
     t = R.Table([300, 64], 32)

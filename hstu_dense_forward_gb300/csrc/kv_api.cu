@@ -162,12 +162,22 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
     if (want < 1) want = 1;
     while (pl->cluster < 8 && pl->cluster * 2 <= want) pl->cluster *= 2;
     pl->splits = (int)(want / pl->cluster);
-    // A cluster's CTAs lie in one group of SMs, whose number eight CTAs do not divide: the last
-    // clusters of a full wave wait for a second one. Seven eighths of the wave fit (four sequences of
-    // 100k E2M1 keys, two kv heads: 70 us with 56 CTAs each, 52 with 48; the bf16 kernel's numbers
-    // are multiples that fit as they are)
-    if (c->dtype == HSTU_FP4_E2M1 && pl->cluster == 8 && pl->splits > 1)
-      pl->splits = (int)(want * 7 / 64);
+    // E2M1: a cluster's CTAs lie in one group of SMs, whose number eight CTAs do not divide, so that the
+    // last clusters of a full wave wait for a second one. Seven eighths of the wave fit (eight items of
+    // 100k keys: 8 x 7 CTAs each 73 us, 8 x 6 53; one 40 and 31, four 43 and 32). Of few CTAs an item that
+    // may be half of them, and those of clusters of two all fit, but their many ranges cost some 2 us to
+    // join (items of 100k keys: 12 with 8 x 4 CTAs each 72, 2 x 19 65; 16 8 x 3 91, 2 x 14 81; 25 8 x 1
+    // 186, 8 x 2 128, 2 x 9 118; 28 8 x 1 179, 8 x 2 183, 2 x 8 126; 36 8 x 1 179, 2 x 6 168. Of 40k keys:
+    // 16 36 and 35, 25 67 and 49; of 20k: 16 25.1 and 25.8, 24 29 and 30, 28 36 and 31). The bf16
+    // kernel's numbers are multiples that fit as they are.
+    if (c->dtype == HSTU_FP4_E2M1 && pl->cluster == 8) {
+      if (a->max_seqlen_k >= 32768 && want >= 12 && want < 48) {
+        pl->cluster = 2;
+        pl->splits = (int)(want / 2);
+      } else if (pl->splits > 1) {
+        pl->splits = (int)(want * 7 / 64);
+      }
+    }
     pl->min_range = 128 * pl->cluster;
     if (pl->cluster == 1 && pl->splits == 1 && pl->rows == 8 && c->head_dim <= 128)
       pl->by_length = rows_by_length(c->batch, pl->blocks, sms, c->num_page_ids, c->page_size,

@@ -289,6 +289,14 @@ def test_pages_as_bf16_of_sequences_that_share_entries(cuda_device):
             _check_weights_of(2.0 ** -8, one, [800], q[at:at + 800], vals, out[at:at + 800], 0.125)
 
 
+@pytest.mark.parametrize("dtype,B,Nk,D", [("bf16", 1, 1, 64), ("fp16", 4, 2, 32), ("bf16", 4, 4, 32), ("fp16", 25, 1, 64),
+                                          ("bf16", 7, 4, 32), ("bf16", 9, 4, 32), ("bf16", 3, 2, 256)])
+def test_single_tokens_over_long_keys(cuda_device, dtype, B, Nk, D):
+    """As many items as clusters of eight, clusters of two and single CTAs divide the keys of."""
+    lengths = [40000, 100] + [2000 + 37 * b for b in range(B)]
+    run_case(cuda_device, lengths[:B], [1] * B, dtype, 2 * Nk, Nk, D, 128, seed=61, bounds=(1, 40000))
+
+
 @pytest.mark.parametrize("dtype,n,D", [("bf16", 300, 128), ("fp16", 200, 64), ("bf16", 30, 256), ("fp16", 6, 64),
                                        ("bf16", 3, 128), ("fp32", 3, 128)])
 def test_items_over_many_ctas(cuda_device, dtype, n, D):

@@ -200,8 +200,10 @@ hstu_status plan_attention(const hstu_kv_cache* c, const hstu_softmax_args* a, A
 
 // An E2M1 cache whose pages are turned into bf16 ones first (see expand.cu): for bf16 queries of 768
 // packed rows a sequence in the mean, three of the attention kernel's items (16 sequences of 256
-// tokens, four heads to a kv head: 121 us so, 147 without; of 128 tokens 88 and 86), as long as the
-// pages that batch and max_seqlen_k allow take a gigabyte at most. (What page_ids holds besides has no
+// tokens, four heads to a kv head: 121 us so, 147 without; of 128 tokens 88 and 86; one head to a kv head,
+// of 768 tokens over 8000 keys at D = 64 116 and 150), and of 2048 rows above D = 128, whose kernel waits
+// less for the conversion (16 sequences of 768 rows over 8000 keys, D = 256: 374 us so, 266 without; four
+// of 1536 over 30,000 518 and 425, 16 over 8000 484 and 547, of 4096 980 and 1220), as long as the pages that batch and max_seqlen_k allow take a gigabyte at most. (What page_ids holds besides has no
 // part in it: the weights are bf16 here and fp16 without.)
 struct Expanded {
   long long ids, pages;  // bytes
@@ -219,7 +221,8 @@ bool expand_pays(const hstu_kv_cache* c, const hstu_softmax_args* a, Expanded* e
   const long long page = 4ll * c->page_size * c->num_heads_kv * c->head_dim;
   e->per = ((long long)a->max_seqlen_k + c->page_size - 1) / c->page_size;
   const long long most = c->batch * e->per;
-  if (rows < 768ll * c->batch || most > (1ll << 30) / page) return false;
+  if (rows < (c->head_dim > 128 ? 2048ll : 768ll) * c->batch || most > (1ll << 30) / page)
+    return false;
   e->by_entry = c->num_page_ids <= most;
   e->ids = (c->num_page_ids * (c->index_is_int64 ? 8 : 4) + 15) / 16 * 16;
   e->cache = *c;

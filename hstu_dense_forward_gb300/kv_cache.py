@@ -346,7 +346,7 @@ def hstu_softmax_fwd(q, kv_cache, seq_offsets, *, max_seqlen, max_seqlen_k, page
     as allocated. Other arguments as for hstu_kv_append.
 
     expand: bf16 queries of 768 packed rows (tokens times Nq / Nk) a sequence in the mean and more
-    turn the pages of a 4-bit cache into bf16 first, if those that the batch and max_seqlen_k allow
+    (2048 above D = 128) turn the pages of a 4-bit cache into bf16 first, if those that the batch and max_seqlen_k allow
     are a gigabyte at most; the weights are bf16 then. With expand=False they are fp16, as for fewer
     rows, and no workspace is taken for pages."""
     c = _cache(kv_cache, seq_offsets, page_offsets, page_ids, last_page_len, kv_scale,

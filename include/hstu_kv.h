@@ -150,11 +150,12 @@ HSTU_API hstu_status hstu_kv_read(const hstu_kv_cache* cache, const hstu_kv_rows
  * around them. bf16 queries over such a cache are products of fp16 with a power of two of their row:
  * elements below 2^-38 of its largest vanish.
  *
- * bf16 queries over an E2M1 cache, total_tokens * Nq / Nk >= 768 * batch: the cache's pages are turned
- * into bf16 first (exactly), in workspace, if batch * ceil(max_seqlen_k / page_size) of them are 2^30
- * bytes at most; queries, weights and products are then those over a bf16 cache. With less workspace
- * than hstu_softmax_workspace gives, but at least what it gives for num_page_ids = 0, that is not done,
- * and what the paragraph above says of E2M1 caches holds.
+ * bf16 queries over an E2M1 cache, total_tokens * Nq / Nk >= 768 * batch (2048 * batch for head dims
+ * above 128): the cache's pages are turned into bf16 first (exactly), in workspace, if
+ * batch * ceil(max_seqlen_k / page_size) of them are 2^30 bytes at most; queries, weights and products
+ * are then those over a bf16 cache. With less workspace than hstu_softmax_workspace gives, but at least
+ * what it gives for num_page_ids = 0, that is not done, and what the paragraph above says of E2M1 caches
+ * holds.
  */
 typedef struct {
   const void* q;          /* [T, Nq, D]: row t at q + t * q_stride elements, 16-byte aligned */

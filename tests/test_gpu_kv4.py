@@ -242,7 +242,7 @@ def _check_weights_of(half_step, t, n, q, vals, got, alpha):
 
 @pytest.mark.parametrize("index", [torch.int32, torch.int64])
 @pytest.mark.parametrize("lengths,n,Nq,Nk,D,ps", [([600, 0, 900, 300], [600, 0, 850, 0], 4, 1, 64, 128),
-                                                 ([1000, 30], [1000, 1], 8, 2, 96, 32)])
+                                                 ([1000, 30], [1000, 1], 8, 2, 96, 32), ([900, 700], [880, 700], 6, 1, 160, 128)])
 def test_pages_as_bf16_or_not(cuda_device, lengths, n, Nq, Nk, D, ps, index):
     """The choice does not look at entries of page_ids that no sequence has, of which there may be more
     than pages that fit the workspace; and a caller that declines it gets fp16 weights."""

@@ -45,6 +45,7 @@
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "kv_kernels.h"
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace hstu {
@@ -107,30 +108,6 @@ struct Bars {
   volatile int abort;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
-
-__device__ __forceinline__ bool wait_bar(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
-                                         uint32_t parity) {
-  const uint32_t a = ptx::smem_u32(bar);
-  if (ptx::mbar_try_wait(a, parity)) return true;
-  const uint64_t start = ptx::globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(a, parity)) return true;
-    if ((i & 15u) == 0) {
-      if (bars->abort) return false;
-      if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
-        bars->abort = 1;
-        report(p.c, HSTU_DEVERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -348,7 +325,7 @@ __device__ void load_role(const SoftmaxParams& p, Bars* bars, uint8_t* smem, con
 
 // What a warp holds of the item's query rows. Lane (g, c): the products' fragments of rows g of
 // each row tile, in the scores' order of the head dim (of block cb, lane c's elements in fours, two
-// registers each), and of rows 2c and 2c + 1
+// registers each), and what the scores of rows 2c and 2c + 1 need.
 template <class C>
 struct Queries {
   uint32_t qb[C::NT][C::KS][2];
@@ -486,37 +463,38 @@ __device__ __forceinline__ void tile_scores(const SoftmaxParams& p, const uint8_
         }
       }
     }
-  }
+  } else {
 #pragma unroll
-  for (int cb = 0; cb < (C::FP4 ? 0 : C::NCB); ++cb)
+    for (int cb = 0; cb < C::NCB; ++cb)
 #pragma unroll
-    for (int j = 0; j < C::LPC; ++j) {
-      const uint4 u0 = *reinterpret_cast<const uint4*>(
-          kt + cb * C::CB + piece_at<C::SWB>(r16 + g, c * C::LPC + j));
-      const uint4 u1 = *reinterpret_cast<const uint4*>(
-          kt + cb * C::CB + piece_at<C::SWB>(r16 + 8 + g, c * C::LPC + j));
-      const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-      const int k = (cb * C::LPC + j) * C::EPP / 4;
-      if constexpr (C::CODES) {
+      for (int j = 0; j < C::LPC; ++j) {
+        const uint4 u0 = *reinterpret_cast<const uint4*>(
+            kt + cb * C::CB + piece_at<C::SWB>(r16 + g, c * C::LPC + j));
+        const uint4 u1 = *reinterpret_cast<const uint4*>(
+            kt + cb * C::CB + piece_at<C::SWB>(r16 + 8 + g, c * C::LPC + j));
+        const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+        const int k = (cb * C::LPC + j) * C::EPP / 4;
+        if constexpr (C::CODES) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x2(w0[e], a0, a2);
-          e4m3x4_to_f16x2(w1[e], a1, a3);
+          for (int e = 0; e < 4; ++e) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x2(w0[e], a0, a2);
+            e4m3x4_to_f16x2(w1[e], a1, a3);
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            mma<false>(e & 1 ? sd[i] : sc[i], a0, a1, a2, a3, qs.qb[i][k + e][0],
-                       qs.qb[i][k + e][1]);
-        }
-      } else {
+            for (int i = 0; i < NT; ++i)
+              mma<false>(e & 1 ? sd[i] : sc[i], a0, a1, a2, a3, qs.qb[i][k + e][0],
+                         qs.qb[i][k + e][1]);
+          }
+        } else {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          mma<C::MMA_BF16>(sc[i], w0[0], w1[0], w0[1], w1[1], qs.qb[i][k][0], qs.qb[i][k][1]);
-          mma<C::MMA_BF16>(sd[i], w0[2], w1[2], w0[3], w1[3], qs.qb[i][k + 1][0],
-                           qs.qb[i][k + 1][1]);
+          for (int i = 0; i < NT; ++i) {
+            mma<C::MMA_BF16>(sc[i], w0[0], w1[0], w0[1], w1[1], qs.qb[i][k][0], qs.qb[i][k][1]);
+            mma<C::MMA_BF16>(sd[i], w0[2], w1[2], w0[3], w1[3], qs.qb[i][k + 1][0],
+                             qs.qb[i][k + 1][1]);
+          }
         }
       }
-    }
+  }
   // scores in base 2; sc[i][2 x + y]: key g + 8 x, row 2 c + y
   if (C::CODES && p.c.scale) {
     const uint8_t* sp = smem + C::OFF_SC + st * C::PLANES * C::KT + r16 + g;
@@ -539,8 +517,7 @@ __device__ __forceinline__ void tile_scores(const SoftmaxParams& p, const uint8_
   }
 }
 
-// Joins results of a row: reference, sum and weights of n parts.
-// The unit of a part's output (E4M3), from that of the parts' joint sum.
+// Parts of a row: the unit of one's output (codes), and its weight, against those of all (top).
 __device__ __forceinline__ float part_unit(float m, float d, float top) { return (m - top) + d; }
 __device__ __forceinline__ float part_weight(float m, float top) {
   return m == -CUDART_INF_F ? 0.0f : ex2(m - top);
@@ -767,60 +744,61 @@ __global__ void __launch_bounds__(Cfg<D, NT, BF16, FMT>::THREADS, Cfg<D, NT, BF1
               }
             }
           }
-        }
+        } else {
 #pragma unroll
-        for (int cb = 0; cb < (C::FP4 ? 0 : C::NCB); ++cb) {
-          const uint8_t* blk = vt + cb * C::CB;
-          constexpr int NW = C::FP4 ? 2 : C::NV * (C::CODES ? 1 : 2) / 4;  // words of a lane's piece: 4, or 2 (64 codes a row)
-          uint32_t v[4][NW];                     // keys 2c, 2c + 1, 2c + 8, 2c + 9
+          for (int cb = 0; cb < C::NCB; ++cb) {
+            const uint8_t* blk = vt + cb * C::CB;
+            constexpr int NW = C::NV * (C::CODES ? 1 : 2) / 4;  // words of a lane's piece: 4, or 2
+            uint32_t v[4][NW];                     // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int key = 2 * c + (y & 1) + 8 * (y >> 1), r = warp * 16 + key;
-            if constexpr (NW == 4) {
-              const uint4 u = *reinterpret_cast<const uint4*>(blk + piece_at<C::SWB>(r, g));
-              v[y][0] = u.x;
-              v[y][1] = u.y;
-              v[y][2] = u.z;
-              v[y][3] = u.w;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(blk + piece_at<C::SWB>(r, g >> 1) +
-                                                              (g & 1) * 8);
-              v[y][0] = u.x;
-              v[y][1] = u.y;
-            }
-          }
-          if (left < 16) {  // beyond the keys: a page's unused rows, maybe NaN
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if (2 * c + (y & 1) + 8 * (y >> 1) >= left) {
-#pragma unroll
-                for (int w = 0; w < NW; ++w) v[y][w] = 0u;
+            for (int y = 0; y < 4; ++y) {
+              const int key = 2 * c + (y & 1) + 8 * (y >> 1), r = warp * 16 + key;
+              if constexpr (NW == 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(blk + piece_at<C::SWB>(r, g));
+                v[y][0] = u.x;
+                v[y][1] = u.y;
+                v[y][2] = u.z;
+                v[y][3] = u.w;
+              } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(blk + piece_at<C::SWB>(r, g >> 1) +
+                                                                (g & 1) * 8);
+                v[y][0] = u.x;
+                v[y][1] = u.y;
               }
-          }
+            }
+            if (left < 16) {  // beyond the keys: a page's unused rows, maybe NaN
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            if constexpr (CODES) {
+              for (int y = 0; y < 4; ++y)
+                if (2 * c + (y & 1) + 8 * (y >> 1) >= left) {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16x2(__byte_perm(v[0][w], v[1][w], e ? 0x7362 : 0x5140), a0, a1);
-                e4m3x4_to_f16x2(__byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140), a2, a3);
+                  for (int w = 0; w < NW; ++w) v[y][w] = 0u;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              if constexpr (CODES) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t a0, a1, a2, a3;
+                  e4m3x4_to_f16x2(__byte_perm(v[0][w], v[1][w], e ? 0x7362 : 0x5140), a0, a1);
+                  e4m3x4_to_f16x2(__byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                  for (int i = 0; i < NT; ++i)
+                    mma<false>(o[i][cb * C::NV / 2 + 2 * w + e], a0, a1, a2, a3, pb[0][i][0],
+                               pb[0][i][1]);
+                }
+              } else {
+                const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+                const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+                const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
+                const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                  mma<false>(o[i][cb * C::NV / 2 + 2 * w + e], a0, a1, a2, a3, pb[0][i][0],
-                             pb[0][i][1]);
+#pragma unroll
+                  for (int h = 0; h < PARTS; ++h)
+                    mma<C::MMA_BF16>(o[i][cb * C::NV / 2 + w], a0, a1, a2, a3, pb[h][i][0],
+                                     pb[h][i][1]);
               }
-            } else {
-              const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
-              const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-              const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
-              const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
-#pragma unroll
-              for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int h = 0; h < PARTS; ++h)
-                  mma<C::MMA_BF16>(o[i][cb * C::NV / 2 + w], a0, a1, a2, a3, pb[h][i][0],
-                                   pb[h][i][1]);
             }
           }
         }

@@ -69,6 +69,7 @@
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "kv_kernels.h"
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace hstu {
@@ -382,31 +383,6 @@ __device__ __forceinline__ bool ring_tile(int i, int n, int& t) {
   return true;
 }
 
-__device__ __forceinline__ bool wait_bar(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
-                                         uint32_t parity) {
-  const uint32_t a = ptx::smem_u32(bar);
-  if (ptx::mbar_try_wait(a, parity)) return true;
-  const uint64_t start = ptx::globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(a, parity)) return true;
-    if ((i & 15u) == 0) {
-      if (bars->abort) return false;
-      if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
-        bars->abort = 1;
-        report(p.c, HSTU_DEVERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
-// The same by every lane of a warp, with a warp-uniform result (the tcgen05 loads and stores
-// that follow are executed by whole warps).
-__device__ __forceinline__ bool warp_wait(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
-                                          uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_bar(p, bars, bar, parity));
-}
-
 // 2^-d as an fp16 pattern, d in [0, 14]; beyond, 0 (rows of the smallest scale).
 __device__ __forceinline__ uint32_t half_power(int d) {
   return d < 15 ? (uint32_t)(15 - d) << 10 : 0u;
@@ -424,11 +400,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one is
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 template <bool BF16>

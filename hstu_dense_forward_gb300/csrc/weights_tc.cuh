@@ -36,6 +36,7 @@
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "kv_kernels.h"
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace hstu {
@@ -76,30 +77,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-__device__ __forceinline__ bool wait_bar(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
-                                         uint32_t parity) {
-  const uint32_t a = ptx::smem_u32(bar);
-  if (ptx::mbar_try_wait(a, parity)) return true;
-  const uint64_t start = ptx::globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(a, parity)) return true;
-    if ((i & 15u) == 0) {
-      if (bars->abort) return false;
-      if ((long long)(ptx::globaltimer_ns() - start) > p.timeout_ns) {
-        bars->abort = 1;
-        report(p.c, HSTU_DEVERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-
-// The same by every lane of a warp, with a warp-uniform result.
-__device__ __forceinline__ bool warp_wait(const SoftmaxParams& p, Bars* bars, uint64_t* bar,
-                                          uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_bar(p, bars, bar, parity));
-}
-
 // The cluster's other CTAs have stored their sums.
 __device__ __forceinline__ bool wait_joined(const SoftmaxParams& p, Bars* bars) {
   const uint32_t a = ptx::smem_u32(&bars->joined);
@@ -112,12 +89,6 @@ __device__ __forceinline__ bool wait_joined(const SoftmaxParams& p, Bars* bars) 
     }
   }
   return true;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // A CTA's work: steps first, first + slots, .. of one sequence and kv head; of the query tiles, those

@@ -14,7 +14,8 @@
 // sixteen elements, which is what a lane holds, has a factor besides, rounded to E4M3. Codes are
 // roundings of exact quotients: a quotient in fp32 falls on the middle of two codes only if the
 // exact one does, since element, factor (4 bits) and middle (3 bits) all are fp32 values. Writing
-// 72,000 rows of eight heads (D = 128, bf16) takes 90 us, 4.2 TB/s, reading them back 73, 5.1 TB/s.
+// 68,000 rows of eight heads (D = 128, bf16) takes 90 us, 4.0 TB/s: warps wait for loads, of which each
+// has one unit ahead, and convert meanwhile (57 % of issue slots). Reading them back takes 73.5, 4.9 TB/s.
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "kv_kernels.h"
@@ -98,7 +99,7 @@ __device__ __forceinline__ int group_exponent(uint32_t bits) {
 // bits, infinities and NaN included. A NaN makes the factor one. Quotients are products with the
 // factor's reciprocal, corrected once by the exact residual, which rounds them as a division does
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990): two
-// of them in three packed instructions (72,000 rows of eight heads 90 us, with sixteen divisions a lane
+// of them in three packed instructions (68,000 rows of eight heads 90 us, with sixteen divisions a lane
 // 154).
 __device__ __forceinline__ uint2 group_codes(const float (&x)[16], uint32_t own, int e,
                                              uint32_t& factor) {

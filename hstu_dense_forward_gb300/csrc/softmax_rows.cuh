@@ -17,8 +17,8 @@
 //
 // E2M1 caches: a lane's sixteen consecutive elements of a key are a group, whose factor multiplies
 // them in fp16; factor times code has seven bits, 2^-10 .. 2688, and is exact. What follows holds for
-// them as for E4M3 codes. Instructions bind them, some 460 a warp and sixteen keys (128 tokens over
-// 1k-4k keys of four heads, D = 128: 65 us, 3.1 TB/s of codes).
+// them as for E4M3 codes. What bounds them is a warp's chain over sixteen keys, some 460 instructions
+// (128 tokens over 1k-4k keys of four heads, D = 128: 62 us, 3.2 TB/s of codes, 59 % of issue slots).
 //
 // E4M3 caches: codes become fp16 by one conversion (exact) and the products run in fp16. A
 // row scale 2^e of K multiplies the score. One of V would leave fp16's range if it multiplied a
@@ -216,7 +216,7 @@ __device__ __forceinline__ int sequence_by_length(const SoftmaxParams& p, int ra
 
 // Place of the CTA's item in the order of the lengths. A round of by_length CTAs, one an SM, goes
 // through it forwards, the next backwards, so that an SM's share of long and short sequences evens out
-// (128 sequences of 1k-4k keys and four heads on 456 places: 78 us in the sequences' order, 65 so).
+// (128 sequences of 1k-4k keys and four heads on 456 places: 79 us in the sequences' order, 62 so).
 __device__ __forceinline__ long long place_by_length(const SoftmaxParams& p, long long blk,
                                                      long long blocks) {
   const long long round = blk / p.by_length, first = round * p.by_length;

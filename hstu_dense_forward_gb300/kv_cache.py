@@ -1,5 +1,5 @@
-"""Paged KV cache operators: writing new rows into the cache that hstu_fwd reads, reading
-rows back, and softmax attention over it (C ABI: include/hstu_kv.h).
+"""Paged KV cache operators: writing new rows into the cache (which hstu_fwd reads unless it has row
+scales), reading rows back, and softmax attention over it (C ABI: include/hstu_kv.h).
 
     hstu_kv_append(k, v, seq_offsets, kv_cache, page_offsets=po, page_ids=ids,
                    last_page_len=last, kv_scale=scale)

@@ -1,7 +1,8 @@
 /*
  * hstu_kv.h — C ABI of the paged KV cache operators (GB300, sm_103a): writing new rows
- * into the cache that hstu_fwd_run_kv reads, reading a sequence's rows back, and softmax
- * attention of new tokens over the cache.
+ * into a paged cache, reading a sequence's rows back, and softmax attention of new tokens over
+ * the cache. (hstu_fwd_run_kv reads such caches, too, but none with row scales: those of E4M3
+ * with them, and 4-bit ones, go there by way of hstu_kv_read.)
  *
  * The cache ("RecOps Running Case Documentation", Inputs and Outputs table, kv_cache /
  * page_offsets / page_ids / last_page_len rows): kv_cache [num_pages, 2, page_size, Nk, D],
@@ -24,7 +25,7 @@
  *   kv_cache [num_pages, 2, Nk, page_size, D / 2]   E2M1 codes, element 2 i in the low four bits
  *                                                   of byte i (D a multiple of 32)
  *   kv_group_scale [num_pages, 2, Nk, page_size, D / 16]   one E4M3 factor >= 0 per 16 elements
- *   kv_scale                                        row scales as above
+ *   kv_scale                                        row scales as above, 1 <= s <= 244
  * and value = 2^(s - 127) * factor * code: 4.5 bits an element and a byte a row.
  *
  * Ownership: the caller owns every tensor, workspaces included; no entry point allocates,

@@ -1,9 +1,9 @@
-// The pages of an E2M1 cache that sequences with queries have as bf16, in the layout of a bf16 cache, for attention of many query rows
-// over them. Every CTA of that kernel would turn the keys and values of its items into 16 bits by
-// itself, and its softmax waits for the warps that do: with several items a kv head and sequence it is
-// faster to convert them once, a pass that is bound by memory (16 sequences of 100-512 tokens over some
-// 4500 keys, two kv heads of four: 191 us, with this 145; four of 4096 over 4096 965 and 672). The
-// products of codes, factors and powers of two have seven bits, so that bf16 holds them.
+// The pages of an E2M1 cache that sequences with queries have as bf16, in the layout of a bf16 cache,
+// for attention of many query rows over them. Every CTA of that kernel would turn the keys and values of
+// its items into 16 bits by itself, and its softmax waits for the warps that do: with several items a kv
+// head and sequence it is faster to convert them once, a pass that is bound by memory (16 sequences of
+// 100-512 tokens over some 4500 keys, two kv heads of four: 191 us, with this 145; four of 4096 over 4096
+// 965 and 672). The products of codes, factors and powers of two have seven bits, so that bf16 holds them.
 #include "kernels.h"
 #include "kv_cache.cuh"
 #include "kv_kernels.h"
